@@ -1,6 +1,8 @@
 """GB300-native second-order Higher-order Linear Attention (HLA): masked, unmasked and
 the asymmetric variant AHLA, the backward pass of the masked forward, and masked
-third-order HLA (forward and decode).
+third-order HLA (forward and decode); beside them two more layers whose serving state
+has a constant size: a gated linear recurrence (``gated_*``) and softmax attention over a
+sliding window with first tokens that stay visible (``window_*``).
 
 Thin ctypes binding over the C ABI in ``include/hla.h`` (library
 ``_lib/libhla_gb300.so``, built for sm_103a by ``_build.build()``).  Functions named
@@ -15,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 from dataclasses import dataclass
 
 from ._build import LIB_PATH
@@ -22,6 +25,7 @@ from ._build import LIB_PATH
 HLA_OK, HLA_ERR_ARG, HLA_ERR_UNSUPPORTED, HLA_ERR_CUDA, HLA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 HLA_F32, HLA_BF16 = 0, 1
 HLA_NORMALIZE, HLA_DECAY, HLA_UNMASKED, HLA_ASYMMETRIC = 1, 2, 4, 8
+HLA_GATE_GIVEN, HLA_GATE_SIGMOID, HLA_GATE_RATE = 0, 1, 2
 
 __all__ = [
     "HLA_OK", "HLA_ERR_ARG", "HLA_ERR_UNSUPPORTED", "HLA_ERR_CUDA", "HLA_ERR_TIMEOUT",
@@ -33,6 +37,12 @@ __all__ = [
     "hla_backward_chunked_state", "hla_state3", "hla_state3_combine", "state3_combine", "hla_forward3_workspace_size", "hla_forward3_chunked", "hla_forward3_chunked_traced",
     "hla_decode3_step", "State3", "forward3", "decode3_step", "hla_selftest_expired_wait",
     "State", "new_workspace", "forward", "state_combine", "decode_step", "backward",
+    "HLA_GATE_GIVEN", "HLA_GATE_SIGMOID", "HLA_GATE_RATE", "hla_tensor", "hla_gated_params", "hla_window_params",
+    "hla_gated_workspace_size", "hla_gated_forward", "hla_gated_backward", "hla_gated_step",
+    "hla_window_forward", "hla_window_backward_workspace_size", "hla_window_backward", "hla_window_step",
+    "hla_window_cache_fill",
+    "gated_workspace", "gated_forward", "gated_backward", "gated_step", "GatedGradients",
+    "window_forward", "window_workspace", "window_backward", "window_cache", "window_cache_fill", "window_step",
 ]
 
 # Every symbol include/hla.h declares.
@@ -40,7 +50,10 @@ EXPORTS = ("hla_forward_workspace_size", "hla_forward_chunked", "hla_state_combi
            "hla_sync_status", "hla_status_string", "hla_last_error", "hla_forward_chunked_noalloc",
            "hla_backward_workspace_size", "hla_backward_chunked", "hla_backward_chunked_traced",
            "hla_forward3_workspace_size", "hla_forward3_chunked", "hla_forward3_chunked_traced", "hla_decode3_step",
-           "hla_selftest_expired_wait", "hla_forward_kernel", "hla_backward_chunked_state", "hla_state3_combine")
+           "hla_selftest_expired_wait", "hla_forward_kernel", "hla_backward_chunked_state", "hla_state3_combine",
+           "hla_gated_workspace_size", "hla_gated_forward", "hla_gated_backward", "hla_gated_step",
+           "hla_window_forward", "hla_window_backward_workspace_size", "hla_window_backward", "hla_window_step",
+           "hla_window_cache_fill")
 
 
 class HlaError(RuntimeError):
@@ -65,6 +78,22 @@ class hla_state3(ctypes.Structure):
     _fields_ = [("S", ctypes.c_void_p), ("P", ctypes.c_void_p), ("T", ctypes.c_void_p),
                 ("m", ctypes.c_void_p), ("h", ctypes.c_void_p),
                 ("SQ", ctypes.c_void_p), ("MQP", ctypes.c_void_p), ("MKQ", ctypes.c_void_p), ("mqm", ctypes.c_void_p)]
+
+
+class hla_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong), ("st", ctypes.c_longlong)]
+
+
+class hla_gated_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("n", ctypes.c_int), ("d", ctypes.c_int), ("in_dtype", ctypes.c_int),
+                ("gate", ctypes.c_int), ("rate", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
+
+
+class hla_window_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("n", ctypes.c_int),
+                ("nk", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int), ("in_dtype", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
+                ("lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -111,6 +140,21 @@ def library(path: str | None = None):
                lib.hla_backward_chunked, lib.hla_backward_chunked_traced, lib.hla_forward3_chunked,
                lib.hla_forward3_chunked_traced, lib.hla_decode3_step, lib.hla_selftest_expired_wait,
                lib.hla_state3_combine):
+        fn.restype = ctypes.c_int
+    GP, WP, T = ctypes.POINTER(hla_gated_params), ctypes.POINTER(hla_window_params), ctypes.POINTER(hla_tensor)
+    lib.hla_gated_workspace_size.argtypes = [GP]
+    lib.hla_gated_workspace_size.restype = sz
+    lib.hla_gated_forward.argtypes = [GP, T, T, T, vp, vp, vp, sz, vp]
+    lib.hla_gated_backward.argtypes = [GP, T, T, T, T, vp, vp, T, T, vp, vp, vp, sz, vp]
+    lib.hla_gated_step.argtypes = [GP, T, T, T, vp, vp, vp]
+    lib.hla_window_forward.argtypes = [WP, T, T, T, T, vp, vp]
+    lib.hla_window_backward_workspace_size.argtypes = [WP]
+    lib.hla_window_backward_workspace_size.restype = sz
+    lib.hla_window_backward.argtypes = [WP, T, T, T, T, vp, T, T, T, T, vp, sz, vp]
+    lib.hla_window_step.argtypes = [WP, T, T, T, T, T, vp, T, vp]
+    lib.hla_window_cache_fill.argtypes = [WP, T, T, T, T, vp]
+    for fn in (lib.hla_gated_forward, lib.hla_gated_backward, lib.hla_gated_step, lib.hla_window_forward,
+               lib.hla_window_backward, lib.hla_window_step, lib.hla_window_cache_fill):
         fn.restype = ctypes.c_int
     lib.hla_status_string.argtypes = [ctypes.c_int]
     lib.hla_status_string.restype = ctypes.c_char_p
@@ -282,6 +326,49 @@ def hla_selftest_expired_wait(stream=None) -> None:
 
 def hla_sync_status(stream=None) -> None:
     _check(library().hla_sync_status(_stream(stream)))
+
+
+def hla_gated_workspace_size(params: hla_gated_params) -> int:
+    return library().hla_gated_workspace_size(ctypes.byref(params))
+
+
+def hla_gated_forward(params: hla_gated_params, x, g, y, state_in=None, state_out=None, workspace=None,
+                      workspace_bytes: int = 0, stream=None) -> None:
+    _check(library().hla_gated_forward(ctypes.byref(params), x, g, y, _ptr(state_in), _ptr(state_out),
+                                       _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def hla_gated_backward(params: hla_gated_params, x, g, y, dy, state_in, d_state_out, dx, dg, d_rate, d_state_in,
+                       workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(library().hla_gated_backward(ctypes.byref(params), x, g, y, dy, _ptr(state_in), _ptr(d_state_out), dx, dg,
+                                        _ptr(d_rate), _ptr(d_state_in), _ptr(workspace), workspace_bytes,
+                                        _stream(stream)))
+
+
+def hla_gated_step(params: hla_gated_params, x, g, y, state, state_out, stream=None) -> None:
+    _check(library().hla_gated_step(ctypes.byref(params), x, g, y, _ptr(state), _ptr(state_out), _stream(stream)))
+
+
+def hla_window_forward(params: hla_window_params, q, k, v, o, lse=None, stream=None) -> None:
+    _check(library().hla_window_forward(ctypes.byref(params), q, k, v, o, _ptr(lse), _stream(stream)))
+
+
+def hla_window_backward_workspace_size(params: hla_window_params) -> int:
+    return library().hla_window_backward_workspace_size(ctypes.byref(params))
+
+
+def hla_window_backward(params: hla_window_params, q, k, v, o, lse, dout, dq, dk, dv, workspace,
+                        workspace_bytes: int, stream=None) -> None:
+    _check(library().hla_window_backward(ctypes.byref(params), q, k, v, o, _ptr(lse), dout, dq, dk, dv,
+                                         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def hla_window_step(params: hla_window_params, q, k, v, kc, vc, pos, o, stream=None) -> None:
+    _check(library().hla_window_step(ctypes.byref(params), q, k, v, kc, vc, _ptr(pos), o, _stream(stream)))
+
+
+def hla_window_cache_fill(params: hla_window_params, k, v, kc, vc, stream=None) -> None:
+    _check(library().hla_window_cache_fill(ctypes.byref(params), k, v, kc, vc, _stream(stream)))
 
 
 # ------------------------------------------------------- tensor-level helpers
@@ -478,3 +565,309 @@ def decode3_step(state: State3, q, k, v, out=None, stream=None, H: int = 1, gamm
     flags = (HLA_DECAY if gamma is not None else 0) | (HLA_NORMALIZE if normalize else 0)
     hla_decode3_step(N, H, d, dv, _dtype_code(q), flags, float(eps), gamma, state, q, k, v, o, stream)
     return o
+
+
+# ------------------------------------------------- gated recurrence, windowed attention
+_GATES = {"given": HLA_GATE_GIVEN, "sigmoid": HLA_GATE_SIGMOID, "rate": HLA_GATE_RATE}
+GatedGradients = namedtuple("GatedGradients", "dx dg d_rate d_state_in")
+
+
+def _expect(t, name, shape, dtype, device, contiguous=False):
+    """Shape, type and device of one argument; its channels have to be adjacent."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of the last dimension must be adjacent")
+
+
+def _current(t):
+    """The kernels run on the current device: refuse tensors of another one."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("CUDA tensors are needed")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _on(stream):
+    """What a call allocates belongs to the stream the call runs on."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _t2(t):
+    """[B, d] rows, or [B, n, d]."""
+    s = t.stride()
+    return ctypes.byref(hla_tensor(t.data_ptr(), s[0], 0, s[1] if len(s) == 3 else 0))
+
+
+def _t4(t):
+    """[B, H, w] rows, or [B, H, n, w]."""
+    s = t.stride()
+    return ctypes.byref(hla_tensor(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0))
+
+
+def _int32(x, name):
+    """ctypes would cut a larger number to its low bits."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _gated_params(x, g, gate, rate, lengths, device):
+    if gate not in _GATES:
+        raise ValueError(f"gate must be one of {sorted(_GATES)}")
+    import torch
+    code = _dtype_code(x)
+    B, d = x.shape[0], x.shape[-1]
+    n = x.shape[1] if x.dim() == 3 else 1
+    _expect(x, "x", x.shape, x.dtype, device)
+    _expect(g, "g", x.shape, x.dtype, device)
+    if (rate is not None) != (gate == "rate"):
+        raise ValueError("rate belongs to gate='rate', which needs it")
+    if rate is not None:
+        _expect(rate, "rate", (d,), torch.float32, device, True)
+    if lengths is not None:
+        _expect(lengths, "lengths", (B,), torch.int32, device, True)
+    return hla_gated_params(B, n, d, code, _GATES[gate], _ptr(rate), _ptr(lengths))
+
+
+def _optional(t, name, shape, dtype, device):
+    if t is not None:
+        _expect(t, name, shape, dtype, device, True)
+
+
+def _space(need, workspace, device, zeroed):
+    """(workspace, bytes) of a call that needs `need` bytes."""
+    import torch
+    if workspace is None:
+        if not need:
+            return None, 0
+        workspace = new_workspace(need, device) if zeroed else torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("the workspace must be a contiguous tensor on the same device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def gated_workspace(x, stream=None):
+    """A zeroed workspace for gated_forward and gated_backward of x [B,n,d]; each call leaves
+    it ready for the next.  Calls that may overlap in time need one each."""
+    B, n, d = x.shape
+    with _on(stream):
+        return new_workspace(hla_gated_workspace_size(hla_gated_params(B, n, d, _dtype_code(x), 0, None, None)), x.device)
+
+
+def gated_forward(x, g, gate: str = "given", rate=None, state_in=None, return_state: bool = False, lengths=None,
+                  out=None, workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + b_t over x, g [B,n,d] (bf16 or fp32, any
+    strides with adjacent channels): gate "given" a = g, b = x; "sigmoid" a = sigma(g),
+    b = (1 - a) x; "rate" a = exp(-rate sigma(g)), b = sqrt(1 - a^2) x with rate [d] fp32,
+    positive.  state_in [B,d] fp32 or None (zeros); lengths [B] int32: tokens of each
+    sequence (rows behind them: zero in a new y, left as they were in ``out``).  Returns
+    y [B,n,d] (and the final state [B,d] fp32)."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, n, d]")
+    p = _gated_params(x, g, gate, rate, lengths, dev)
+    _optional(state_in, "state_in", (p.B, p.d), torch.float32, dev)
+    with _on(stream):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        st = torch.empty((p.B, p.d), dtype=torch.float32, device=dev) if return_state else None
+        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 128 or workspace is not None else 0, workspace, dev, True)
+        hla_gated_forward(p, _t2(x), _t2(g), _t2(out), state_in, st, ws, nbytes, stream)
+    return (out, st) if return_state else out
+
+
+def gated_backward(x, g, y, dy, gate: str = "given", rate=None, state_in=None, d_state_out=None,
+                   want_dstate: bool = False, lengths=None, out=None, workspace=None, stream=None):
+    """Gradients of gated_forward from its y and the gradients dy of y and d_state_out [B,d]
+    fp32 of the final state (None: zero).  Returns GatedGradients(dx, dg, d_rate, d_state_in):
+    d_rate [d] fp32 with gate "rate" (else None), d_state_in [B,d] fp32 with want_dstate
+    (else None).  ``out`` may hold two tensors for dx and dg."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, n, d]")
+    p = _gated_params(x, g, gate, rate, lengths, dev)
+    _expect(y, "y", x.shape, x.dtype, dev)
+    _expect(dy, "dy", x.shape, x.dtype, dev)
+    _optional(state_in, "state_in", (p.B, p.d), torch.float32, dev)
+    _optional(d_state_out, "d_state_out", (p.B, p.d), torch.float32, dev)
+    with _on(stream):
+        new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+        if out is None:
+            make = torch.zeros if lengths is not None else torch.empty
+            out = (make(x.shape, dtype=x.dtype, device=dev), make(x.shape, dtype=x.dtype, device=dev))
+        dx, dg = out
+        _expect(dx, "dx", x.shape, x.dtype, dev)
+        _expect(dg, "dg", x.shape, x.dtype, dev)
+        dr = new(p.d) if gate == "rate" else None
+        ds = new(p.B, p.d) if want_dstate else None
+        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 128 or dr is not None or workspace is not None else 0,
+                            workspace, dev, True)
+        hla_gated_backward(p, _t2(x), _t2(g), _t2(y), _t2(dy), state_in, d_state_out, _t2(dx), _t2(dg), dr, ds, ws,
+                           nbytes, stream)
+    return GatedGradients(dx, dg, dr, ds)
+
+
+def gated_step(state, x, g, gate: str = "given", rate=None, lengths=None, state_out=None, out=None, stream=None):
+    """One token of every sequence: x, g [B,d], state [B,d] fp32 updated in place, or read and
+    the new one written to ``state_out``.  lengths [B] int32: 0 marks an idle sequence, whose
+    rows of y (zero in a new one) and of the state are left as they were.  Returns (y, state)."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [B, d]")
+    p = _gated_params(x, g, gate, rate, lengths, dev)
+    _expect(state, "state", x.shape, torch.float32, dev, True)
+    if state_out is None:
+        state_out = state
+    else:
+        _expect(state_out, "state_out", x.shape, torch.float32, dev, True)
+    with _on(stream):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        hla_gated_step(p, _t2(x), _t2(g), _t2(out), state, state_out, stream)
+    return out, state_out
+
+
+def _window_params(q, k, v, window, sinks, scale, lengths, device):
+    import torch
+    code = _dtype_code(q)
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, heads, tokens, width]")
+    B, H, n, d = q.shape
+    Hkv, nk, dv = k.shape[1], k.shape[2], v.shape[3]
+    _expect(q, "q", q.shape, q.dtype, device)
+    _expect(k, "k", (B, Hkv, nk, d), q.dtype, device)
+    _expect(v, "v", (B, Hkv, nk, dv), q.dtype, device)
+    if lengths is not None:
+        _expect(lengths, "lengths", (B,), torch.int32, device, True)
+    return hla_window_params(B, H, Hkv, n, nk, d, dv, code, _int32(window, "window"), _int32(sinks, "sinks"),
+                             d ** -0.5 if scale is None else scale, _ptr(lengths))
+
+
+def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = None, lengths=None,
+                   return_lse: bool = False, out=None, stream=None):
+    """Softmax attention of q [B,H,n,d] over k [B,Hkv,nk,d], v [B,Hkv,nk,dv] (bf16 or fp32,
+    widths up to 128, any strides with adjacent channels): the query at position
+    p = nk - n + i sees the keys j <= p with j > p - window or j < sinks.  scale: 1/sqrt(d)
+    unless given.  lengths [B] int32: tokens of each sequence; rows behind them are zero in a
+    new o, left as they were in ``out``.  Returns o [B,H,n,dv] (and lse [B,H,n] fp32)."""
+    import torch
+    dev = _current(q)
+    p = _window_params(q, k, v, window, sinks, scale, lengths, dev)
+    with _on(stream):
+        make = torch.zeros if lengths is not None else torch.empty
+        if out is None:
+            out = make((p.B, p.H, p.n, p.dv), dtype=q.dtype, device=dev)
+        else:
+            _expect(out, "out", (p.B, p.H, p.n, p.dv), q.dtype, dev)
+        lse = make((p.B, p.H, p.n), dtype=torch.float32, device=dev) if return_lse else None
+        hla_window_forward(p, _t4(q), _t4(k), _t4(v), _t4(out), lse, stream)
+    return (out, lse) if return_lse else out
+
+
+def window_workspace(q, k, v, window: int, sinks: int = 0, stream=None):
+    """A workspace for window_backward of these shapes."""
+    import torch
+    p = _window_params(q, k, v, window, sinks, None, None, q.device)
+    with _on(stream):
+        return torch.empty(max(hla_window_backward_workspace_size(p), 1), dtype=torch.uint8, device=q.device)
+
+
+def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None, lengths=None,
+                    out=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * o) for window_forward, from its o and lse.  ``out``
+    may hold the three result tensors; rows behind the lengths are zero in new ones, left as
+    they were in those."""
+    import torch
+    dev = _current(q)
+    p = _window_params(q, k, v, window, sinks, scale, lengths, dev)
+    _expect(o, "o", (p.B, p.H, p.n, p.dv), q.dtype, dev)
+    _expect(dout, "dout", (p.B, p.H, p.n, p.dv), q.dtype, dev)
+    _expect(lse, "lse", (p.B, p.H, p.n), torch.float32, dev, True)
+    with _on(stream):
+        if out is None:
+            make = torch.zeros if lengths is not None else torch.empty
+            out = tuple(make(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
+        dq, dk, dv = out
+        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+            _expect(t, name, like.shape, q.dtype, dev)
+        ws, nbytes = _space(hla_window_backward_workspace_size(p) if workspace is None else 0, workspace, dev, False)
+        hla_window_backward(p, _t4(q), _t4(k), _t4(v), _t4(o), lse, _t4(dout), _t4(dq), _t4(dk), _t4(dv), ws, nbytes,
+                            stream)
+    return dq, dk, dv
+
+
+def window_cache(B: int, Hkv: int, window: int, sinks: int, d: int, dv: int | None = None, dtype=None, device="cuda"):
+    """Ring cache (kc [B,Hkv,sinks+window,d], vc [B,Hkv,sinks+window,dv]) for window_step,
+    bf16 unless given; slots are written before they are read, so it is not cleared."""
+    import torch
+    new = lambda w: torch.empty((B, Hkv, sinks + window, w), dtype=dtype or torch.bfloat16, device=device)  # noqa: E731
+    return new(d), new(d if dv is None else dv)
+
+
+def _cache_params(kc, vc, q_heads, window, sinks, scale, lengths, nk, device):
+    import torch
+    if kc.dim() != 4 or vc.dim() != 4:
+        raise ValueError("kc and vc must be [B, Hkv, sinks + window, width]")
+    B, Hkv, d, dv = kc.shape[0], kc.shape[1], kc.shape[3], vc.shape[3]
+    _expect(kc, "kc", (B, Hkv, sinks + window, d), kc.dtype, device)
+    _expect(vc, "vc", (B, Hkv, sinks + window, dv), kc.dtype, device)
+    if lengths is not None:
+        _expect(lengths, "lengths", (B,), torch.int32, device, True)
+    return hla_window_params(B, q_heads, Hkv, 1, nk, d, dv, _dtype_code(kc), _int32(window, "window"),
+                             _int32(sinks, "sinks"), d ** -0.5 if scale is None else scale, _ptr(lengths))
+
+
+def window_cache_fill(kc, vc, k, v, window: int, sinks: int = 0, lengths=None, stream=None) -> None:
+    """The cache after a prompt k [B,Hkv,n,d], v [B,Hkv,n,dv]: the first ``sinks`` and the last
+    ``window`` tokens of every sequence (lengths [B] int32, None: n).  Decoding goes on at
+    pos = the lengths."""
+    dev = _current(kc)
+    p = _cache_params(kc, vc, kc.shape[1], window, sinks, None, lengths, k.shape[2], dev)
+    _expect(k, "k", (p.B, p.Hkv, p.nk, p.d), kc.dtype, dev)
+    _expect(v, "v", (p.B, p.Hkv, p.nk, p.dv), kc.dtype, dev)
+    hla_window_cache_fill(p, _t4(k), _t4(v), _t4(kc), _t4(vc), stream)
+
+
+def window_step(kc, vc, pos, q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, stream=None):
+    """One token of every sequence: writes k [B,Hkv,d], v [B,Hkv,dv] into the ring cache at the
+    token's slot and attends q [B,H,d] over the visible slots.  pos [B] int64: the tokens
+    before this one (advanced by the caller), or negative for an idle sequence, whose row of o
+    (zero in a new one) and cache are left as they were.  Returns o [B,H,dv]."""
+    import torch
+    dev = _current(q)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, d]")
+    p = _cache_params(kc, vc, q.shape[1], window, sinks, scale, None, 1, dev)
+    _expect(q, "q", (p.B, p.H, p.d), kc.dtype, dev)
+    _expect(k, "k", (p.B, p.Hkv, p.d), kc.dtype, dev)
+    _expect(v, "v", (p.B, p.Hkv, p.dv), kc.dtype, dev)
+    _expect(pos, "pos", (p.B,), torch.int64, dev, True)
+    with _on(stream):
+        if out is None:
+            out = torch.zeros((p.B, p.H, p.dv), dtype=q.dtype, device=dev)
+        else:
+            _expect(out, "out", (p.B, p.H, p.dv), q.dtype, dev)
+        hla_window_step(p, _t4(q), _t4(k), _t4(v), _t4(kc), _t4(vc), pos, _t4(out), stream)
+    return out

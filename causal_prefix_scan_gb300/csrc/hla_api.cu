@@ -113,6 +113,7 @@ namespace hla {
 // Record `msg` as this thread's last error and return `s` (used by entry points
 // defined in other translation units).
 hla_status report(hla_status s, const char *msg) { return fail(s, "%s", msg); }
+cudaError_t dev_status_ptr(unsigned **p) { return status_ptr(p); }
 }  // namespace hla
 
 extern "C" {

@@ -1,0 +1,801 @@
+// hla_gated.cu -- gated linear recurrence over [B][n][d], elementwise per channel:
+//   h_t = a_t h_{t-1} + b_t,   y_t = h_t,
+//   HLA_GATE_GIVEN:   a = g,                  b = x
+//   HLA_GATE_SIGMOID: a = sigma(g),           b = (1 - a) x
+//   HLA_GATE_RATE:    a = exp(-r sigma(g)),   b = sqrt(1 - a^2) x
+// its backward pass and its single-token step.
+//
+// A stretch of tokens is the map h -> A h + B (A the product of its a_t); stretches
+// compose by (A1,B1) then (A2,B2) = (A2 A1, A2 B1 + B2).  The backward pass is the same
+// scan in the other direction, of c_t = a_t gh_t (the gradient that token t hands to
+// token t-1): gh_t = dy_t + c_{t+1}, c_t = a_t c_{t+1} + a_t dy_t.
+//
+// Bound by HBM: every input element is read once and every output element written once
+// (x, g -> y; g, y, dy[, x] -> dx, dg), with a few fp32 operations on each.  One CTA takes
+// a tile of 8 warps x TS tokens by 32 lanes x VEC channels, holds it in registers, and
+// gets the state before its tile from the tiles before it while its own loads are the only
+// traffic: each tile publishes its map (A, B) as soon as it has it, then looks back over
+// the published maps to the nearest published state, folds forward from there, and
+// publishes its own state.  The fold always runs state -> later tiles in order with the
+// same fmaf, so a state has the same bits wherever the look-back found its start: results
+// do not depend on timing.  Reading the inputs a second time instead (maps, scan, states)
+// would move 5/3 of the forward's bytes.
+#include "hla_internal.h"
+
+namespace hla {
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int kThreads = WARPS * 32;
+constexpr int TS = 16;                // tokens of one thread
+constexpr int TILE_T = WARPS * TS;    // tokens of one tile
+constexpr int BACK = 8;               // windows of WARPS earlier tiles kept by one look-back
+
+// Published map or state of one channel of one tile, 16 bytes, read and written whole.
+// `tag` is 4 * (number of the call) + kind; anything else is left over from another call.
+struct __align__(16) Record {
+    float a, b;
+    unsigned long long tag;
+};
+enum : unsigned long long { REC_MAP = 1, REC_STATE = 2 };
+
+// Workspace: header, then one record per channel slot of every tile, then (backward with
+// HLA_GATE_RATE) one partial sum per channel slot of every tile, in records with tag 0.
+// Header word 0 counts tickets over all calls, word 1 is the count at which this call
+// began: both only grow, so no call number ever returns.
+struct Header {
+    unsigned long long tickets, base;
+};
+constexpr size_t kHeaderBytes = 256;
+
+struct Tensor {
+    const void *p;
+    long long sb, st;
+};
+
+struct Args {
+    int B, n, d, tiles, slices;
+    const float *rate;
+    const int *lengths;
+    Tensor x, g, y, dy, o1, o2;   // o1: y or dx, o2: dg
+    const float *state_in;        // [B][d]: before the first token (NULL: zeros)
+    const float *d_state_out;     // [B][d]: gradient of the state after the last (NULL: zeros)
+    float *out_state;             // state after the last token, or d_state_in (NULL: skip)
+    Header *hdr;
+    Record *rec, *part;           // part: NULL when the rates' gradient is not wanted
+    unsigned *err;
+};
+
+// ------------------------------------------------------------ element access
+// VEC adjacent channels of one token as they lie in memory.
+template <typename T, int VEC>
+struct Raw;
+template <>
+struct Raw<float, 1> { using type = float; };
+template <>
+struct Raw<float, 2> { using type = float2; };
+template <>
+struct Raw<__nv_bfloat16, 1> { using type = unsigned short; };
+template <>
+struct Raw<__nv_bfloat16, 2> { using type = unsigned; };
+template <typename T, int VEC>
+using raw_t = typename Raw<T, VEC>::type;
+
+__device__ __forceinline__ void unpack(float r, float (&v)[1]) { v[0] = r; }
+__device__ __forceinline__ void unpack(float2 r, float (&v)[2]) { v[0] = r.x; v[1] = r.y; }
+__device__ __forceinline__ void unpack(unsigned short r, float (&v)[1]) { v[0] = __uint_as_float((unsigned)r << 16); }
+__device__ __forceinline__ void unpack(unsigned r, float (&v)[2]) {
+    v[0] = __uint_as_float(r << 16);
+    v[1] = __uint_as_float(r & 0xFFFF0000u);
+}
+__device__ __forceinline__ void pack(const float (&v)[1], float &r) { r = v[0]; }
+__device__ __forceinline__ void pack(const float (&v)[2], float2 &r) { r = make_float2(v[0], v[1]); }
+__device__ __forceinline__ void pack(const float (&v)[1], unsigned short &r) {
+    r = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+}
+__device__ __forceinline__ void pack(const float (&v)[2], unsigned &r) { r = pack_bf16(v[0], v[1]); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ raw_t<T, VEC> load(const Tensor &t, size_t off) {
+    return __ldg(reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(t.p) + off));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store(const Tensor &t, size_t off, const float (&v)[VEC]) {
+    raw_t<T, VEC> r;
+    pack(v, r);
+    *reinterpret_cast<raw_t<T, VEC> *>(const_cast<T *>(static_cast<const T *>(t.p)) + off) = r;
+}
+
+// ------------------------------------------------------------ gates
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// sigma(z) and 1 - sigma(z), both with a relative error of a few units in the last place of
+// the smaller: the larger is one minus it, so that a gate near one, whose error a long
+// product of gates multiplies, is off by its rounding only.  Below -87 the exponential
+// would pass the largest float; sigma is then under the smallest normal one.
+__device__ __forceinline__ void sigmoid2(float z, float &s, float &c) {
+    const float e = __expf(z < -87.f ? 87.f : -z), r = __fdividef(1.f, 1.f + e), er = e * r;
+    s = z > 0.f ? 1.f - er : r;
+    c = z > 0.f ? er : 1.f - r;
+}
+// 1 - exp(-u) for u >= 0.  Below 1/4 the difference would cancel: Taylor's series in nested
+// form to u^7, whose next term is under 2^-28 of the sum there.
+__device__ __forceinline__ float one_minus_exp(float u) {
+    if (u < 0.25f) {
+        float p = fmaf(-u, 1.f / 7.f, 1.f);
+        p = fmaf(-u * (1.f / 6.f), p, 1.f);
+        p = fmaf(-u * (1.f / 5.f), p, 1.f);
+        p = fmaf(-u * (1.f / 4.f), p, 1.f);
+        p = fmaf(-u * (1.f / 3.f), p, 1.f);
+        p = fmaf(-u * 0.5f, p, 1.f);
+        return u * p;
+    }
+    return 1.f - __expf(-u);
+}
+
+// a_t and the factor of x_t
+template <int GATE>
+__device__ __forceinline__ void gate_fwd(float g, float r, float &a, float &f) {
+    if constexpr (GATE == HLA_GATE_GIVEN) {
+        a = g;
+        f = 1.f;
+    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
+        sigmoid2(g, a, f);
+    } else {
+        float s, c;
+        sigmoid2(g, s, c);
+        const float w = one_minus_exp(r * s), q = w * (2.f - w);  // 1 - a and 1 - a^2
+        a = 1.f - w;
+        f = q > 0.f ? q * rsqrt_approx(q) : q;  // q = 0: no input; a NaN stays one
+    }
+}
+// Gradients with respect to x, g and (HLA_GATE_RATE) the rate, from gh = dL/dh_t, x_t and
+// y = h_{t-1}; a is the gate.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f,
+// da/du = -a.  f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
+template <int GATE>
+__device__ __forceinline__ void gate_bwd(float g, float r, float x, float y, float gh, float &a, float &dx, float &dg,
+                                         float &dr) {
+    if constexpr (GATE == HLA_GATE_GIVEN) {
+        a = g;
+        dx = gh;
+        dg = gh * y;
+    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
+        float f;
+        sigmoid2(g, a, f);
+        dx = gh * f;
+        dg = gh * (y - x) * (a * f);
+    } else {
+        float s, c;
+        sigmoid2(g, s, c);
+        const float u = r * s, w = one_minus_exp(u), q = w * (2.f - w);
+        a = 1.f - w;
+        const float rf = q == 0.f ? 0.f : rsqrt_approx(q);
+        dx = gh * (q * rf);
+        const float du = gh * a * fmaf(x * a, rf, -y);
+        dg = du * u * c;
+        dr = du * s;
+    }
+}
+
+// ------------------------------------------------------------ look-back
+__device__ __forceinline__ void publish(Record *p, float a, float b, unsigned long long tag) {
+    const unsigned long long ab = (unsigned long long)__float_as_uint(a) | ((unsigned long long)__float_as_uint(b) << 32);
+    asm volatile("{\n .reg .b128 r;\n mov.b128 r, {%1, %2};\n st.relaxed.gpu.global.b128 [%0], r;\n}\n" ::"l"(p), "l"(ab),
+                 "l"(tag)
+                 : "memory");
+}
+__device__ __forceinline__ Record peek(const Record *p) {
+    unsigned long long ab, tag;
+    asm volatile("{\n .reg .b128 r;\n ld.relaxed.gpu.global.b128 r, [%2];\n mov.b128 {%0, %1}, r;\n}\n"
+                 : "=l"(ab), "=l"(tag)
+                 : "l"(p)
+                 : "memory");
+    Record x;
+    x.a = __uint_as_float((unsigned)ab);
+    x.b = __uint_as_float((unsigned)(ab >> 32));
+    x.tag = tag;
+    return x;
+}
+// Wait, bounded, until the record belongs to call `call` and is at least a map (at least
+// a state with `need_state`).  False: the limit passed and the sticky status is raised.
+__device__ __forceinline__ bool await_record(const Record *p, unsigned long long call, bool need_state, Record &x, unsigned *err) {
+    const unsigned long long state = 4 * call + REC_STATE, map = 4 * call + REC_MAP;
+    x = peek(p);
+    if (x.tag == state || (x.tag == map && !need_state)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        __nanosleep(40);
+        x = peek(p);
+        if (x.tag == state || (x.tag == map && !need_state)) return true;
+    } while (globaltimer_ns() - t0 < (uint64_t)kWaitLimitUs * 1000u);
+    atomicOr(err, DEV_TIMEOUT);
+    return false;
+}
+
+template <int VEC>
+struct Shared {
+    float2 agg[WARPS][32 * VEC];           // the warps' maps
+    float2 back[BACK * WARPS][32 * VEC];   // maps of earlier tiles, nearest first
+    int kind[WARPS][32 * VEC];             // of the newest window: REC_MAP, REC_STATE, 0 (none)
+    float carry[32 * VEC];                 // state before the tile
+    unsigned long long ticket, call;
+};
+
+// The state before tile `pos` of chain `chain` (positions count along the scan's
+// direction, `first` is the chain's first active position) into sh.carry, and this tile's
+// own state published.  `init` is the state before the chain.  Every thread of the CTA
+// calls this once sh.agg is complete; false: a wait expired.
+template <int VEC>
+__device__ __forceinline__ bool look_back(Shared<VEC> &sh, const Args &a, size_t chain, int pos, int first,
+                                          const float *init, int c0, float *out_state) {
+    constexpr int C = 32 * VEC;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Record *rec = a.rec + (chain * a.tiles) * C;
+    const unsigned long long call = sh.call;
+    float A = 1.f, Bv = 0.f;  // the tile's map, one channel per thread below C
+    if (tid < C) {
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float2 m = sh.agg[w][tid];
+            Bv = fmaf(m.x, Bv, m.y);
+            A *= m.x;
+        }
+    }
+    float h = 0.f;
+    bool ok = true;
+    if (pos == first) {
+        if (tid < C && init && c0 + tid < a.d) h = init[c0 + tid];
+    } else {
+        if (tid < C) publish(rec + (size_t)pos * C + tid, A, Bv, 4 * call + REC_MAP);
+        int found = -1;  // index in sh.back of the state this channel starts from
+        for (int r = 0;; ++r) {
+            const int slot = r < BACK ? r : BACK - 1;
+            const int prev = pos - 1 - (slot * WARPS + warp);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const int c = lane * VEC + v;
+                Record x{};
+                int kind = 0;
+                if (prev >= first) {
+                    // past the kept windows: wait for the states of the last one
+                    ok = await_record(rec + (size_t)prev * C + c, call, r >= BACK, x, a.err) && ok;
+                    kind = (int)(x.tag & 3);
+                }
+                sh.back[slot * WARPS + warp][c] = make_float2(x.a, x.b);
+                sh.kind[warp][c] = kind;
+            }
+            if (!__syncthreads_and(ok)) {  // a state all the same, so that no later tile waits as long again
+                if (tid < C) publish(rec + (size_t)pos * C + tid, 1.f, __int_as_float(0x7fc00000), 4 * call + REC_STATE);
+                return false;
+            }
+            if (tid < C && found < 0) {
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    if (found < 0 && sh.kind[w][tid] == (int)REC_STATE) found = slot * WARPS + w;
+            }
+            if (__syncthreads_and(tid >= C || found >= 0)) break;
+        }
+        if (tid < C) {
+            h = sh.back[found][tid].y;
+            for (int i = found - 1; i >= 0; --i) h = fmaf(sh.back[i][tid].x, h, sh.back[i][tid].y);
+        }
+    }
+    if (tid < C) {
+        sh.carry[tid] = h;
+        const float after = fmaf(A, h, Bv);
+        if (a.hdr) publish(rec + (size_t)pos * C + tid, A, after, 4 * call + REC_STATE);
+        if (out_state && c0 + tid < a.d) out_state[c0 + tid] = after;
+    }
+    __syncthreads();
+    return true;
+}
+
+// This CTA's place: tiles of one position across all chains come before those of the
+// next, in the order in which CTAs begin, so every tile that one waits for has begun.
+template <int VEC>
+__device__ __forceinline__ void take_place(Shared<VEC> &sh, const Args &a) {
+    if (threadIdx.x == 0) {
+        if (a.hdr) {
+            volatile unsigned long long *base = &a.hdr->base;
+            const unsigned long long b0 = *base;  // stands until the last ticket is out
+            __threadfence();
+            const unsigned long long t = atomicAdd(&a.hdr->tickets, 1ull);
+            sh.ticket = t - b0;
+            sh.call = b0 + 1;
+            if (sh.ticket == gridDim.x - 1) {  // every CTA of this call has read base
+                __threadfence();
+                *base = t + 1;
+            }
+        } else {
+            sh.ticket = blockIdx.x;
+            sh.call = 0;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int length_of(const Args &a, int b) {
+    if (!a.lengths) return a.n;
+    const int L = a.lengths[b];
+    return L < 0 ? 0 : L > a.n ? a.n : L;
+}
+
+// ------------------------------------------------------------ forward
+template <typename T, int GATE, int VEC>
+__global__ void __launch_bounds__(kThreads) gated_fwd_kernel(const Args a) {
+    constexpr int C = 32 * VEC;
+    __shared__ Shared<VEC> sh;
+    take_place(sh, a);
+    const size_t chains = (size_t)a.B * a.slices;
+    const int pos = (int)(sh.ticket / chains);
+    const size_t chain = sh.ticket % chains;
+    const int b = (int)(chain / a.slices), c0 = (int)(chain % a.slices) * C;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
+    const int len = length_of(a, b);
+    const size_t so = (size_t)b * a.d;
+    if (len == 0 && pos == 0 && a.out_state) {  // no tokens: the state passes through
+        for (int c = threadIdx.x; c < C; c += kThreads)
+            if (c0 + c < a.d) a.out_state[so + c0 + c] = a.state_in ? a.state_in[so + c0 + c] : 0.f;
+    }
+    if (pos * TILE_T >= len) return;
+    const int t0 = pos * TILE_T + warp * TS;
+    const int m = ch < a.d ? min(TS, len - t0) : 0;  // tokens of this thread (may be <= 0)
+
+    raw_t<T, VEC> xr[TS], gr[TS];
+    size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch, go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        if (i < m) {
+            xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
+            gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
+        }
+    }
+    float r[VEC];
+    if constexpr (GATE == HLA_GATE_RATE) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) r[v] = ch + v < a.d ? a.rate[ch + v] : 0.f;
+    }
+    float ea[TS][VEC], eb[TS][VEC], A[VEC], Bv[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { A[v] = 1.f; Bv[v] = 0.f; }
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        if (i < m) {
+            float x[VEC], g[VEC];
+            unpack(xr[i], x);
+            unpack(gr[i], g);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float f;
+                gate_fwd<GATE>(g[v], r[v], ea[i][v], f);
+                eb[i][v] = GATE == HLA_GATE_GIVEN ? x[v] : f * x[v];
+                Bv[v] = fmaf(ea[i][v], Bv[v], eb[i][v]);
+                A[v] *= ea[i][v];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A[v], Bv[v]);
+    __syncthreads();
+    const bool last = pos == (len - 1) / TILE_T;
+    if (!look_back<VEC>(sh, a, chain, pos, 0, a.state_in ? a.state_in + so : nullptr, c0,
+                        last && a.out_state ? a.out_state + so : nullptr))
+        return;
+    float h[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        h[v] = sh.carry[lane * VEC + v];
+        for (int w = 0; w < warp; ++w) {
+            const float2 mp = sh.agg[w][lane * VEC + v];
+            h[v] = fmaf(mp.x, h[v], mp.y);
+        }
+    }
+    const size_t yo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        if (i < m) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = fmaf(ea[i][v], h[v], eb[i][v]);
+            store<T, VEC>(a.o1, yo + (size_t)i * a.o1.st, h);
+        }
+    }
+}
+
+// ------------------------------------------------------------ backward
+template <typename T, int GATE, int VEC>
+__global__ void __launch_bounds__(kThreads) gated_bwd_kernel(const Args a) {
+    constexpr int C = 32 * VEC;
+    __shared__ Shared<VEC> sh;
+    take_place(sh, a);
+    const size_t chains = (size_t)a.B * a.slices;
+    const int pos = (int)(sh.ticket / chains);   // counts from the last tile
+    const size_t chain = sh.ticket % chains;
+    const int b = (int)(chain / a.slices), c0 = (int)(chain % a.slices) * C;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
+    const int len = length_of(a, b), tile = a.tiles - 1 - pos;
+    const size_t so = (size_t)b * a.d;
+    if (len == 0 && tile == 0 && a.out_state) {
+        for (int c = threadIdx.x; c < C; c += kThreads)
+            if (c0 + c < a.d) a.out_state[so + c0 + c] = a.d_state_out ? a.d_state_out[so + c0 + c] : 0.f;
+    }
+    if (tile * TILE_T >= len) return;
+    // warp 0 takes the tile's last tokens: the warps follow the scan's direction
+    const int t0 = tile * TILE_T + (WARPS - 1 - warp) * TS;
+    const int m = ch < a.d ? min(TS, len - t0) : 0;
+
+    raw_t<T, VEC> gr[TS], dr[TS], yr[TS], xr[TS];
+    const size_t go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch, dyo = (size_t)b * a.dy.sb + (size_t)t0 * a.dy.st + ch;
+    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch;
+    // y one token earlier: h_{t-1}; the token before the first is state_in
+    const T *yp = static_cast<const T *>(a.y.p) + (size_t)b * a.y.sb + ch;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        if (i < m) {
+            gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
+            dr[i] = load<T, VEC>(a.dy, dyo + (size_t)i * a.dy.st);
+            if (t0 + i > 0)
+                yr[i] = __ldg(reinterpret_cast<const raw_t<T, VEC> *>(yp + (size_t)(t0 + i - 1) * a.y.st));
+            if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
+        }
+    }
+    float r[VEC], h0[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        r[v] = GATE == HLA_GATE_RATE && ch + v < a.d ? a.rate[ch + v] : 0.f;
+        h0[v] = t0 == 0 && a.state_in && ch + v < a.d ? a.state_in[so + ch + v] : 0.f;
+    }
+    float A[VEC], Bv[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { A[v] = 1.f; Bv[v] = 0.f; }
+#pragma unroll
+    for (int i = TS - 1; i >= 0; --i) {
+        if (i < m) {
+            float g[VEC], dy[VEC];
+            unpack(gr[i], g);
+            unpack(dr[i], dy);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float ea, f;
+                gate_fwd<GATE>(g[v], r[v], ea, f);
+                Bv[v] = ea * (dy[v] + Bv[v]);
+                A[v] *= ea;
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A[v], Bv[v]);
+    __syncthreads();
+    const int first = a.tiles - 1 - (len - 1) / TILE_T;
+    if (!look_back<VEC>(sh, a, chain, pos, first, a.d_state_out ? a.d_state_out + so : nullptr, c0,
+                        tile == 0 && a.out_state ? a.out_state + so : nullptr))
+        return;
+    float c[VEC], sum[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        c[v] = sh.carry[lane * VEC + v];
+        sum[v] = 0.f;
+        for (int w = 0; w < warp; ++w) {
+            const float2 mp = sh.agg[w][lane * VEC + v];
+            c[v] = fmaf(mp.x, c[v], mp.y);
+        }
+    }
+    const size_t dxo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch, dgo = (size_t)b * a.o2.sb + (size_t)t0 * a.o2.st + ch;
+#pragma unroll
+    for (int i = TS - 1; i >= 0; --i) {
+        if (i < m) {
+            float g[VEC], dy[VEC], x[VEC], y[VEC], dx[VEC], dg[VEC];
+            unpack(gr[i], g);
+            unpack(dr[i], dy);
+            if (t0 + i > 0) {
+                unpack(yr[i], y);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) y[v] = h0[v];
+            }
+            if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float gh = dy[v] + c[v];
+                float ea, drv = 0.f;
+                gate_bwd<GATE>(g[v], r[v], GATE == HLA_GATE_GIVEN ? 0.f : x[v], y[v], gh, ea, dx[v], dg[v], drv);
+                sum[v] += drv;
+                c[v] = ea * gh;
+            }
+            store<T, VEC>(a.o1, dxo + (size_t)i * a.o1.st, dx);
+            store<T, VEC>(a.o2, dgo + (size_t)i * a.o2.st, dg);
+        }
+    }
+    if constexpr (GATE == HLA_GATE_RATE) {
+        if (a.part) {  // the tile's sum of every channel, warps in order
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v].x = sum[v];
+            __syncthreads();
+            if (threadIdx.x < C) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) s += sh.agg[w][threadIdx.x].x;
+                Record *p = a.part + (chain * a.tiles + tile) * C + threadIdx.x;
+                *reinterpret_cast<float4 *>(p) = make_float4(s, 0.f, 0.f, 0.f);
+            }
+        }
+    }
+}
+
+// d_rate[c] = sum of the tiles' partial sums, in an order fixed by the sizes: warp w of a
+// channel group takes tiles w, w + 8, ... of sequence 0, 1, ..., then the warps are added.
+template <int VEC>
+__global__ void __launch_bounds__(kThreads) gated_rate_kernel(const Args a, float *d_rate) {
+    constexpr int C = 32 * VEC;
+    __shared__ float red[WARPS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < a.d) {
+        for (int b = 0; b < a.B; ++b) {
+            const int used = (length_of(a, b) + TILE_T - 1) / TILE_T;
+            const Record *p = a.part + (((size_t)b * a.slices + c / C) * a.tiles) * C + c % C;
+            for (int t = warp; t < used; t += WARPS) s += __ldg(&p[(size_t)t * C].a);
+        }
+    }
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < a.d) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) t += red[w][lane];
+        d_rate[c] = t;
+    }
+}
+
+// ------------------------------------------------------------ one token
+template <typename T, int GATE, int VEC>
+__global__ void __launch_bounds__(kThreads) gated_step_kernel(const Args a) {
+    const size_t cols = (a.d + VEC - 1) / VEC, e = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= cols * a.B) return;
+    const int b = (int)(e / cols), ch = (int)(e % cols) * VEC;
+    if (a.lengths && a.lengths[b] <= 0) return;
+    float x[VEC], g[VEC], h[VEC];
+    unpack(load<T, VEC>(a.x, (size_t)b * a.x.sb + ch), x);
+    unpack(load<T, VEC>(a.g, (size_t)b * a.g.sb + ch), g);
+    const size_t so = (size_t)b * a.d + ch;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        float ea, f;
+        gate_fwd<GATE>(g[v], GATE == HLA_GATE_RATE ? a.rate[ch + v] : 0.f, ea, f);
+        h[v] = fmaf(ea, a.state_in[so + v], GATE == HLA_GATE_GIVEN ? x[v] : f * x[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) a.out_state[so + v] = h[v];
+    store<T, VEC>(a.o1, (size_t)b * a.o1.sb + ch, h);
+}
+
+// ------------------------------------------------------------ host
+template <int VEC>
+int slices_of(int d) { return (d + 32 * VEC - 1) / (32 * VEC); }
+int tiles_of(int n) { return (n + TILE_T - 1) / TILE_T; }
+
+// Two channels per lane when every row of every tensor starts on a two-channel boundary
+// and rows hold a whole number of them: a row segment is then 128 bytes (bf16) per warp
+// and load.  One channel per lane otherwise (odd widths or strides, offset pointers).
+bool pairable(const hla_tensor *t, size_t el) {
+    return !t || !t->p || ((reinterpret_cast<uintptr_t>(t->p) % (2 * el)) == 0 && t->sb % 2 == 0 && t->st % 2 == 0);
+}
+
+hla_status check(const hla_gated_params *p) {
+    if (!p) return report(HLA_ERR_ARG, "params is NULL");
+    if (p->B < 1 || p->d < 1 || p->n < 0) return report(HLA_ERR_ARG, "need B >= 1, d >= 1, n >= 0");
+    if (p->in_dtype != HLA_F32 && p->in_dtype != HLA_BF16) return report(HLA_ERR_ARG, "unknown in_dtype");
+    if (p->gate != HLA_GATE_GIVEN && p->gate != HLA_GATE_SIGMOID && p->gate != HLA_GATE_RATE)
+        return report(HLA_ERR_ARG, "unknown gate");
+    if (p->gate == HLA_GATE_RATE && !p->rate) return report(HLA_ERR_ARG, "HLA_GATE_RATE needs rate");
+    const double tiles = (double)((p->n + (long long)TILE_T - 1) / TILE_T), slices = (double)((p->d + 31LL) / 32);
+    if ((double)p->B * (tiles < 1 ? 1 : tiles) * slices > 2147483647.0 || (double)p->B * p->d > 1099511627776.0)
+        return report(HLA_ERR_ARG, "problem too large");
+    return HLA_OK;
+}
+
+// in: null when not used by this gate; n rows of d channels per sequence.
+hla_status check_in(const hla_tensor *t, const hla_gated_params *p, const char *what) {
+    if (!t || !t->p) return report(HLA_ERR_ARG, what);
+    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(t->p) % el) return report(HLA_ERR_ARG, "a tensor is not aligned to its elements");
+    if (t->sb < 0 || t->st < 0) return report(HLA_ERR_ARG, "strides must not be negative");
+    if ((double)t->sb * (p->B - 1) + (double)t->st * (p->n > 0 ? p->n - 1 : 0) + p->d > 4e18)
+        return report(HLA_ERR_ARG, "a tensor is too large");
+    return HLA_OK;
+}
+// An output's rows must not share memory.
+hla_status check_out(const hla_tensor *t, const hla_gated_params *p, const char *what) {
+    hla_status s = check_in(t, p, what);
+    if (s != HLA_OK) return s;
+    const long long n = p->n, B = p->B, d = p->d;
+    const bool tokens_inside = (n <= 1 || t->st >= d) && (B <= 1 || t->sb >= (n > 0 ? (n - 1) * t->st : 0) + d);
+    const bool seqs_inside = (B <= 1 || t->sb >= d) && (n <= 1 || t->st >= (B - 1) * t->sb + d);
+    if (!tokens_inside && !seqs_inside) return report(HLA_ERR_ARG, "rows of an output overlap");
+    return HLA_OK;
+}
+
+Tensor view(const hla_tensor *t) {
+    Tensor r{nullptr, 0, 0};
+    if (t) r = Tensor{t->p, t->sb, t->st};
+    return r;
+}
+
+// Records of a call: the channel slots of all tiles, for the wider of the two layouts.
+size_t record_count(const hla_gated_params *p) {
+    const size_t tiles = tiles_of(p->n);
+    const size_t s1 = (size_t)slices_of<1>(p->d) * 32, s2 = (size_t)slices_of<2>(p->d) * 64;
+    return (size_t)p->B * tiles * (s1 > s2 ? s1 : s2);
+}
+size_t workspace_bytes_of(const hla_gated_params *p) {
+    // one tile per sequence and no rates' gradient needs none, but one size serves every call
+    return p->n == 0 ? 0 : kHeaderBytes + 2 * record_count(p) * sizeof(Record);
+}
+
+enum Which { FWD, BWD, STEP };
+
+template <typename T, int GATE, int VEC>
+cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
+    a.slices = slices_of<VEC>(a.d);
+    a.tiles = tiles_of(a.n);
+    if (w == STEP) {
+        const size_t total = (size_t)a.B * ((a.d + VEC - 1) / VEC);
+        gated_step_kernel<T, GATE, VEC><<<(unsigned)((total + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    const unsigned grid = (unsigned)((size_t)a.B * a.slices * a.tiles);
+    if (a.tiles <= 1) a.hdr = nullptr;  // no tile waits for another
+    if (w == FWD) {
+        gated_fwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    gated_bwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.part && GATE == HLA_GATE_RATE) {
+        gated_rate_kernel<VEC><<<(a.d + 31) / 32, kThreads, 0, st>>>(a, d_rate);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+template <typename T, int VEC>
+cudaError_t by_gate(int gate, Which w, const Args &a, float *d_rate, cudaStream_t st) {
+    if (gate == HLA_GATE_GIVEN) return launch<T, HLA_GATE_GIVEN, VEC>(w, a, d_rate, st);
+    if (gate == HLA_GATE_SIGMOID) return launch<T, HLA_GATE_SIGMOID, VEC>(w, a, d_rate, st);
+    return launch<T, HLA_GATE_RATE, VEC>(w, a, d_rate, st);
+}
+hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, float *d_rate, cudaStream_t st) {
+    a.B = p->B; a.n = p->n; a.d = p->d;
+    a.rate = p->rate;
+    a.lengths = p->lengths;
+    cudaError_t e = dev_status_ptr(&a.err);
+    if (e == cudaSuccess) {
+        if (p->in_dtype == HLA_F32)
+            e = pairs ? by_gate<float, 2>(p->gate, w, a, d_rate, st) : by_gate<float, 1>(p->gate, w, a, d_rate, st);
+        else
+            e = pairs ? by_gate<__nv_bfloat16, 2>(p->gate, w, a, d_rate, st)
+                      : by_gate<__nv_bfloat16, 1>(p->gate, w, a, d_rate, st);
+    }
+    if (e != cudaSuccess) return report(HLA_ERR_CUDA, cudaGetErrorString(e));
+    return HLA_OK;
+}
+
+// Splits the caller's workspace; the header is needed from two tiles on.
+hla_status take_workspace(const hla_gated_params *p, void *ws, size_t bytes, bool partials, Args &a) {
+    const size_t need = workspace_bytes_of(p);
+    if (!ws && tiles_of(p->n) <= 1 && !partials) return HLA_OK;
+    if (!ws || bytes < need) return report(HLA_ERR_ARG, "workspace too small (hla_gated_workspace_size)");
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return report(HLA_ERR_ARG, "workspace must be 256-byte aligned");
+    a.hdr = static_cast<Header *>(ws);
+    a.rec = reinterpret_cast<Record *>(static_cast<uint8_t *>(ws) + kHeaderBytes);
+    if (partials) a.part = a.rec + record_count(p);
+    return HLA_OK;
+}
+
+bool even_state(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+}  // namespace hla
+
+using namespace hla;
+
+extern "C" {
+
+size_t hla_gated_workspace_size(const hla_gated_params *p) {
+    if (check(p) != HLA_OK) return 0;
+    return workspace_bytes_of(p);
+}
+
+hla_status hla_gated_forward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
+                             const float *state_in, float *state_out, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+    hla_status s = check(p);
+    if (s != HLA_OK) return s;
+    if (!even_state(state_in) || !even_state(state_out)) return report(HLA_ERR_ARG, "a state is not aligned to its elements");
+    if (state_in && state_in == state_out) return report(HLA_ERR_ARG, "state_out may not alias state_in");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p->n == 0) {
+        if (!state_out) return HLA_OK;
+        const size_t bytes = (size_t)p->B * p->d * 4;
+        const cudaError_t e = state_in ? cudaMemcpyAsync(state_out, state_in, bytes, cudaMemcpyDeviceToDevice, st)
+                                       : cudaMemsetAsync(state_out, 0, bytes, st);
+        return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
+    }
+    if ((s = check_in(x, p, "x must be set")) != HLA_OK || (s = check_in(g, p, "g must be set")) != HLA_OK ||
+        (s = check_out(y, p, "y must be set")) != HLA_OK)
+        return s;
+    if (y->p == x->p || y->p == g->p) return report(HLA_ERR_ARG, "y may not be x or g");
+    Args a{};
+    if ((s = take_workspace(p, workspace, workspace_bytes, false, a)) != HLA_OK) return s;
+    a.x = view(x); a.g = view(g); a.o1 = view(y);
+    a.state_in = state_in;
+    a.out_state = state_out;
+    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
+    return dispatch(p, FWD, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr, st);
+}
+
+hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
+                              const hla_tensor *dy, const float *state_in, const float *d_state_out,
+                              const hla_tensor *dx, const hla_tensor *dg, float *d_rate, float *d_state_in,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+    hla_status s = check(p);
+    if (s != HLA_OK) return s;
+    if (!even_state(state_in) || !even_state(d_state_out) || !even_state(d_state_in) || !even_state(d_rate))
+        return report(HLA_ERR_ARG, "a state is not aligned to its elements");
+    if (d_state_out && d_state_out == d_state_in) return report(HLA_ERR_ARG, "d_state_in may not alias d_state_out");
+    if (d_rate && p->gate != HLA_GATE_RATE) return report(HLA_ERR_ARG, "d_rate belongs to HLA_GATE_RATE");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p->n == 0) {
+        cudaError_t e = cudaSuccess;
+        const size_t bytes = (size_t)p->B * p->d * 4;
+        if (d_rate) e = cudaMemsetAsync(d_rate, 0, (size_t)p->d * 4, st);
+        if (e == cudaSuccess && d_state_in)
+            e = d_state_out ? cudaMemcpyAsync(d_state_in, d_state_out, bytes, cudaMemcpyDeviceToDevice, st)
+                            : cudaMemsetAsync(d_state_in, 0, bytes, st);
+        return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
+    }
+    const bool given = p->gate == HLA_GATE_GIVEN;
+    if ((!given && (s = check_in(x, p, "x must be set")) != HLA_OK) || (s = check_in(g, p, "g must be set")) != HLA_OK ||
+        (s = check_in(y, p, "y must be set")) != HLA_OK || (s = check_in(dy, p, "dy must be set")) != HLA_OK ||
+        (s = check_out(dx, p, "dx must be set")) != HLA_OK || (s = check_out(dg, p, "dg must be set")) != HLA_OK)
+        return s;
+    const hla_tensor *ins[4] = {given ? nullptr : x, g, y, dy};
+    for (const hla_tensor *i : ins)
+        if (i && (dx->p == i->p || dg->p == i->p)) return report(HLA_ERR_ARG, "dx and dg may not be inputs");
+    if (dx->p == dg->p) return report(HLA_ERR_ARG, "dx may not be dg");
+    Args a{};
+    if ((s = take_workspace(p, workspace, workspace_bytes, d_rate != nullptr, a)) != HLA_OK) return s;
+    a.x = given ? Tensor{nullptr, 0, 0} : view(x);
+    a.g = view(g); a.y = view(y); a.dy = view(dy); a.o1 = view(dx); a.o2 = view(dg);
+    a.state_in = state_in;
+    a.d_state_out = d_state_out;
+    a.out_state = d_state_in;
+    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
+    bool pairs = p->d % 2 == 0 && pairable(dx, el) && pairable(dg, el);
+    for (const hla_tensor *i : ins) pairs = pairs && pairable(i, el);
+    return dispatch(p, BWD, a, pairs, d_rate, st);
+}
+
+hla_status hla_gated_step(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
+                          const float *state, float *state_out, void *stream) {
+    hla_status s = check(p);
+    if (s != HLA_OK) return s;
+    if (p->n != 1) return report(HLA_ERR_ARG, "a step takes one token: n must be 1");
+    if (!state || !state_out) return report(HLA_ERR_ARG, "state and state_out must be set");
+    if (!even_state(state) || !even_state(state_out)) return report(HLA_ERR_ARG, "a state is not aligned to its elements");
+    if ((s = check_in(x, p, "x must be set")) != HLA_OK || (s = check_in(g, p, "g must be set")) != HLA_OK ||
+        (s = check_out(y, p, "y must be set")) != HLA_OK)
+        return s;
+    if (y->p == x->p || y->p == g->p) return report(HLA_ERR_ARG, "y may not be x or g");
+    Args a{};
+    a.x = view(x); a.g = view(g); a.o1 = view(y);
+    a.state_in = state;
+    a.out_state = state_out;
+    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
+    return dispatch(p, STEP, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr,
+                    static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -185,5 +185,7 @@ cudaError_t decode3_launch(const Decode3Args &a, cudaStream_t st);
 
 // Set this thread's last-error message and return `s`.
 hla_status report(hla_status s, const char *msg);
+// Device address of the sticky status word of the current device.
+cudaError_t dev_status_ptr(unsigned **p);
 
 }  // namespace hla

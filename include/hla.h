@@ -449,6 +449,139 @@ HLA_API hla_status hla_forward_chunked_noalloc(const hla_params *p, const void *
                                                const void *v, void *o, const hla_state *state_in,
                                                const hla_state *state_out, void *stream);
 
+/*
+ * ------------------------------------------------------------------ gated recurrence
+ * The elementwise causal scan that stands beside the matrix-valued ones above: per
+ * channel c of [B][n][d], with the state h (fp32, [B][d]) carried from token to token,
+ *   h_t = a_t h_{t-1} + b_t,   y_t = h_t (rounded to the element type),
+ *   HLA_GATE_GIVEN    a = g,                  b = x
+ *   HLA_GATE_SIGMOID  a = sigma(g),           b = (1 - a) x
+ *   HLA_GATE_RATE     a = exp(-r sigma(g)),   b = sqrt(1 - a^2) x    (r = rate[c] > 0)
+ * All arithmetic is fp32; only y (and dx, dg) are rounded to the element type.  The
+ * pages have no counterpart; stacks that use constant-state layers do.
+ *
+ * Tensors of this and the next section are strided: element (b, head, token, channel) at
+ * p + b sb + head sh + token st + channel (strides in elements, not negative; sh is not
+ * used here).  Pointers need the alignment of one element only; even strides and widths
+ * with 4-byte (bf16) or 8-byte (fp32) pointers run twice as wide.  Inputs may be
+ * broadcast (stride 0); the rows of an output must not share memory, and an output must
+ * not overlap an input.
+ */
+typedef struct {
+    void *p;
+    long long sb, sh, st;
+} hla_tensor;
+
+typedef enum { HLA_GATE_GIVEN = 0, HLA_GATE_SIGMOID = 1, HLA_GATE_RATE = 2 } hla_gate;
+
+typedef struct {
+    int B, n, d;          /* sequences, tokens per sequence (n >= 0), channels               */
+    hla_dtype in_dtype;   /* element type of x, g, y and of their gradients                  */
+    int gate;             /* an hla_gate                                                     */
+    const float *rate;    /* [d] device fp32, with HLA_GATE_RATE                              */
+    const int *lengths;   /* [B] device: tokens of each sequence (clamped to 0..n), or NULL: n.
+                             Rows from the length on are neither read nor written.           */
+} hla_gated_params;
+
+/* Bytes of device workspace hla_gated_forward and hla_gated_backward need (0 for invalid
+ * parameters and n = 0).  Set to zero before its first use; every call leaves it ready for
+ * the next one, of either direction and any sizes it is large enough for.  Calls sharing
+ * one workspace must not overlap in time, and no other entry point may use it.  Up to 128
+ * tokens the forward, and the backward without d_rate, take NULL as well. */
+HLA_API size_t hla_gated_workspace_size(const hla_gated_params *p);
+
+/*
+ * The recurrence over n tokens, one launch.
+ *   x, g       [B][n][d] (read only);  y  [B][n][d], written;
+ *   state_in   [B][d] fp32 before the first token, or NULL for zeros;
+ *   state_out  [B][d] fp32 after each sequence's last token, or NULL; not state_in.
+ * The result does not depend on timing: repeated calls give the same bits.
+ */
+HLA_API hla_status hla_gated_forward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g,
+                                     const hla_tensor *y, const float *state_in, float *state_out, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient, one launch (two with d_rate).
+ *   x, g, y    as the forward took and wrote them (y is read as h_{t-1}; x may be NULL with
+ *              HLA_GATE_GIVEN);  dy  gradient of y;
+ *   state_in   as given to the forward;  d_state_out  gradient of state_out, or NULL (zeros);
+ *   dx, dg     written;  d_rate [d] fp32, written, or NULL (HLA_GATE_RATE only);
+ *   d_state_in [B][d] fp32, written, or NULL; not d_state_out.
+ */
+HLA_API hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g,
+                                      const hla_tensor *y, const hla_tensor *dy, const float *state_in,
+                                      const float *d_state_out, const hla_tensor *dx, const hla_tensor *dg,
+                                      float *d_rate, float *d_state_in, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* One token of every sequence (p->n must be 1; st is not used): x, g, y [B][d].  state is
+ * read and state_out written ([B][d] fp32); they may be the same.  With lengths, a sequence
+ * of length 0 is idle: its row of y and state_out is left as it was. */
+HLA_API hla_status hla_gated_step(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g,
+                                  const hla_tensor *y, const float *state, float *state_out, void *stream);
+
+/*
+ * ------------------------------------------------------------------ windowed attention
+ * Softmax attention with a state of constant size: a query at position p sees the keys
+ *   j <= p with j > p - window, and those with j < sinks,
+ *   o = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j).
+ * q is [B][H][n][d], k [B][Hkv][nk][d], v [B][Hkv][nk][dv], o [B][H][n][dv] (strided, see
+ * above); query row i stands at position nk - n + i, so n < nk continues a sequence whose
+ * earlier keys are still held.  Query head h reads key/value head h / (H / Hkv).
+ * Rows of k and v below the length must be finite: a NaN or infinity there may reach
+ * queries that do not see it.  Rows from the length on may hold anything.
+ */
+typedef struct {
+    int B, H, Hkv;        /* batch, query heads, key/value heads (H % Hkv == 0)               */
+    int n, nk;            /* query rows (>= 0) and keys (>= n) per sequence                   */
+    int d, dv;            /* widths, 1..128                                                   */
+    hla_dtype in_dtype;
+    int window;           /* >= 1; nk or more is plain causal attention                       */
+    int sinks;            /* >= 0: first tokens that stay visible                             */
+    float scale;          /* finite                                                           */
+    const int *lengths;   /* [B] device: tokens of each sequence (clamped to 0..nk), or NULL:
+                             nk.  Rows at positions from the length on are neither read nor
+                             written.                                                         */
+} hla_window_params;
+
+/* o, and lse [B][H][n] fp32 contiguous (or NULL).  One launch.  bf16 with 16-byte aligned
+ * rows (pointers, strides and widths in multiples of 8 elements) runs on the tensor cores,
+ * everything else on the CUDA cores in fp32. */
+HLA_API hla_status hla_window_forward(const hla_window_params *p, const hla_tensor *q, const hla_tensor *k,
+                                      const hla_tensor *v, const hla_tensor *o, float *lse, void *stream);
+
+/* Gradients dq, dk, dv (written, not accumulated; with Hkv < H, dk and dv are the sums over
+ * each group) from o and lse as the forward wrote them and dout.  workspace: at least
+ * hla_window_backward_workspace_size(p) bytes, 256-byte aligned, no initial contents
+ * needed.  The same bits on every call. */
+HLA_API size_t hla_window_backward_workspace_size(const hla_window_params *p);
+HLA_API hla_status hla_window_backward(const hla_window_params *p, const hla_tensor *q, const hla_tensor *k,
+                                       const hla_tensor *v, const hla_tensor *o, const float *lse,
+                                       const hla_tensor *dout, const hla_tensor *dq, const hla_tensor *dk,
+                                       const hla_tensor *dv, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Decoding from a cache of sinks + window slots per sequence and key/value head, kc
+ * [B][Hkv][slots][d] and vc [B][Hkv][slots][dv] (st is the stride of a slot): token j lies
+ * in slot j while j < sinks, then in slot sinks + (j - sinks) % window.
+ * hla_window_step takes one token of every sequence (p->n must be 1; nk and lengths are not
+ * used): writes k, v [B][Hkv][d | dv] into the token's slot and attends q [B][H][d] over
+ * the visible slots into o [B][H][dv].
+ *   pos  [B] device int64: the token's position (tokens before it), or negative for an idle
+ *        sequence, whose rows of o, kc and vc are left as they were.  The call does not
+ *        change it.
+ */
+HLA_API hla_status hla_window_step(const hla_window_params *p, const hla_tensor *q, const hla_tensor *k,
+                                   const hla_tensor *v, const hla_tensor *kc, const hla_tensor *vc,
+                                   const long long *pos, const hla_tensor *o, void *stream);
+
+/* The cache after a prompt of nk tokens (n is not used; lengths as above): copies the first
+ * `sinks` and the last `window` tokens of every sequence into their slots.  Slots without a
+ * token are left as they were.  Decoding goes on with pos[b] = length of sequence b. */
+HLA_API hla_status hla_window_cache_fill(const hla_window_params *p, const hla_tensor *k, const hla_tensor *v,
+                                         const hla_tensor *kc, const hla_tensor *vc, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
