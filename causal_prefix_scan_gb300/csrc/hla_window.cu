@@ -188,7 +188,10 @@ hla_status hla_window_forward(const hla_window_params *p, const hla_tensor *q, c
     a.q = win::view(q); a.k = win::view(k); a.v = win::view(v); a.o = win::view(o);
     a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == HLA_F32 ? simt<float>(a, false, st) : simt<__nv_bfloat16>(a, false, st);
+    cudaError_t e = dev_status_ptr(&a.err);
+    if (e != cudaSuccess) return report(HLA_ERR_CUDA, cudaGetErrorString(e));
+    e = dt == HLA_BF16 && fwd_tc_takes(a) ? fwd_tc(a, st) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = dt == HLA_F32 ? simt<float>(a, false, st) : simt<__nv_bfloat16>(a, false, st);
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 

@@ -62,7 +62,8 @@ struct StepArgs {
 };
 cudaError_t step(const StepArgs &a, hla_dtype dt, cudaStream_t st);
 
-// bf16 tensor-core kernels (rows in multiples of 16 bytes)
+// bf16 tensor-core kernels (rows in multiples of 16 bytes); cudaErrorNotSupported, with
+// nothing launched, when the driver cannot describe a tensor to the TMA unit
 bool fwd_tc_takes(const Args &a);
 cudaError_t fwd_tc(const Args &a, cudaStream_t st);
 

@@ -1,0 +1,115 @@
+// hla_window_tc.cuh -- what the tensor-core kernels of windowed attention share: tensor
+// maps over strided [B][H][n][width] bf16 tensors, MMA groups on 128-row tiles, bounded
+// barrier waits with an abort flag.
+#pragma once
+#include <cstring>
+
+#include "hla_tmap.h"
+#include "hla_window.h"
+
+namespace hla {
+namespace win {
+namespace tcw {
+
+constexpr int T = 128;  // rows of a tile (queries or keys)
+
+// Rows that a tensor map can describe: 16-byte aligned, strides in multiples of 16 bytes
+// (0 for a broadcast head or sequence), tokens apart.
+inline bool mappable(const View &v) {
+    return (reinterpret_cast<uintptr_t>(v.p) & 15u) == 0 && v.sb % 8 == 0 && v.sh % 8 == 0 && v.st % 8 == 0 &&
+           v.st > 0 && v.sb < (1LL << 38) && v.sh < (1LL << 38) && v.st < (1LL << 38);
+}
+
+// Boxes of 64 columns x `rows` rows; rows past n and columns past `width` read as zeros.
+// A broadcast dimension (stride 0) is given extent 1; its coordinate is then always 0.
+inline bool encode(CUtensorMap *tm, const View &v, int width, int n, int H, int B, int rows) {
+    auto enc = tc::get_encoder();
+    if (!enc) return false;
+    const cuuint64_t st = (cuuint64_t)v.st * 2;
+    cuuint64_t dim[4] = {(cuuint64_t)width, (cuuint64_t)n, (cuuint64_t)(v.sh ? H : 1), (cuuint64_t)(v.sb ? B : 1)};
+    cuuint64_t str[3] = {st, v.sh ? (cuuint64_t)v.sh * 2 : st, v.sb ? (cuuint64_t)v.sb * 2 : st};
+    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dim, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+HLA_DEVICE void tma_load_4d(void *dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// A tile of `ROWS` rows and DP columns (DP / 64 boxes) at row r0 of (b, h).
+template <int DP, int ROWS = T>
+HLA_DEVICE void load_tile(uint8_t *dst, const CUtensorMap *m, const View &v, uint64_t *bar, int r0, int h, int b) {
+#pragma unroll
+    for (int c = 0; c < DP; c += 64) tma_load_4d(dst + (c >> 6) * ROWS * 128, m, bar, c, r0, v.sh ? h : 0, v.sb ? b : 0);
+}
+
+HLA_DEVICE void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Bounded, warp-uniform waits: a poll sleeps in hardware until the phase completes; the
+// CTA's abort flag or the time limit end it (the latter raises the device status word).
+struct Waits {
+    uint64_t *bars;
+    volatile int *abort_p;
+    unsigned *err;
+    HLA_DEVICE uint64_t *bar(int i) const { return bars + i; }
+    HLA_DEVICE bool wait(int b, uint32_t parity) const {
+        bool ok = mbar_try_wait(bars + b, parity);
+        if (!ok) ok = slow(b, parity);
+        return __all_sync(0xffffffffu, ok);
+    }
+    HLA_DEVICE bool slow(int b, uint32_t parity) const {
+        const uint64_t t0 = globaltimer_ns();
+        while (!*abort_p) {
+            if (mbar_try_wait(bars + b, parity)) return true;
+            if (globaltimer_ns() - t0 > (uint64_t)kWaitLimitUs * 1000u) {
+                atomicOr(err, DEV_TIMEOUT);
+                *abort_p = 1;
+            }
+        }
+        return false;
+    }
+};
+
+// ---- MMA groups, issued by a whole warp (one elected lane).  `steps` contraction steps of 16.
+// D [128 x N] (+)= A [128 x K] B [N x K]^T: both K-major tiles of 128 rows (B: RB rows)
+template <int RB = T>
+HLA_DEVICE void mma_kk(uint32_t d, const uint8_t *a, const uint8_t *b, uint32_t idesc, int steps, bool acc) {
+    const uint64_t da = make_sdesc(smem_u32(a), 16u, 1024u), db = make_sdesc(smem_u32(b), 16u, 1024u);
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t in = (uint32_t)(s & 3) * 2u;
+        umma_f16_warp(d, da + (uint32_t)(s >> 2) * (T * 8u) + in, db + (uint32_t)(s >> 2) * (RB * 8u) + in, idesc,
+                      acc || s > 0 ? 1u : 0u);
+    }
+}
+// D [128 x N] (+)= A [128 x K] B [K x N]: A packed bf16 in TMEM, B MN-major (its rows contract)
+HLA_DEVICE void mma_tm(uint32_t d, uint32_t a, const uint8_t *b, uint32_t idesc, int steps, bool acc) {
+    const uint64_t db = make_sdesc(smem_u32(b), T * 128u, 1024u);
+    for (int s = 0; s < steps; ++s)
+        asm volatile(
+            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+            "r"(a + (uint32_t)s * 8u), "l"(db + (uint64_t)(s * 128)), "r"(idesc), "r"((acc || s > 0) ? 1u : 0u)
+            : "memory");
+}
+
+// Zeroes rows [r0, 128) of a tile (one warp) and shows the tensor cores the result.
+template <int DP>
+HLA_DEVICE void zero_rows(uint8_t *tile, int r0, int lane) {
+#pragma unroll
+    for (int c = 0; c < DP; c += 64)
+        for (int e = (r0 << 3) + lane; e < T * 8; e += 32)
+            reinterpret_cast<uint4 *>(tile + (c >> 6) * T * 128)[e] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    __syncwarp();
+}
+
+}  // namespace tcw
+}  // namespace win
+}  // namespace hla
