@@ -689,7 +689,7 @@ def gated_forward(x, g, gate: str = "given", rate=None, state_in=None, return_st
         else:
             _expect(out, "out", x.shape, x.dtype, dev)
         st = torch.empty((p.B, p.d), dtype=torch.float32, device=dev) if return_state else None
-        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 128 or workspace is not None else 0, workspace, dev, True)
+        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 64 or workspace is not None else 0, workspace, dev, True)
         hla_gated_forward(p, _t2(x), _t2(g), _t2(out), state_in, st, ws, nbytes, stream)
     return (out, st) if return_state else out
 
@@ -719,7 +719,7 @@ def gated_backward(x, g, y, dy, gate: str = "given", rate=None, state_in=None, d
         _expect(dg, "dg", x.shape, x.dtype, dev)
         dr = new(p.d) if gate == "rate" else None
         ds = new(p.B, p.d) if want_dstate else None
-        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 128 or dr is not None or workspace is not None else 0,
+        ws, nbytes = _space(hla_gated_workspace_size(p) if p.n > 64 or dr is not None or workspace is not None else 0,
                             workspace, dev, True)
         hla_gated_backward(p, _t2(x), _t2(g), _t2(y), _t2(dy), state_in, d_state_out, _t2(dx), _t2(dg), dr, ds, ws,
                            nbytes, stream)

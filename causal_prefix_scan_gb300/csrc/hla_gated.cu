@@ -12,7 +12,7 @@
 //
 // Bound by HBM: every input element is read once and every output element written once
 // (x, g -> y; g, y, dy[, x] -> dx, dg), with a few fp32 operations on each.  One CTA takes
-// a tile of 8 warps x TS tokens by 32 lanes x VEC channels, holds it in registers, and
+// a tile of 8 warps x kTS tokens by 32 lanes x VEC channels, holds it in registers, and
 // gets the state before its tile from the tiles before it while its own loads are the only
 // traffic: each tile publishes its map (A, B) as soon as it has it, then looks back over
 // the published maps to the nearest published state, folds forward from there, and
@@ -27,8 +27,14 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int kThreads = WARPS * 32;
-constexpr int TS = 16;                // tokens of one thread
-constexpr int TILE_T = WARPS * TS;    // tokens of one tile
+// Tokens of one thread: as many as leave what it holds of them in registers at two CTAs per
+// SM (the backward's four inputs and the fp32 ones take twice the room).
+enum Dir { FWD, BWD };
+template <typename T, Dir DIR>
+constexpr int kTS = DIR == FWD && sizeof(T) == 2 ? 16 : 8;
+template <typename T, Dir DIR>
+constexpr int kTileT = WARPS * kTS<T, DIR>;  // tokens of one tile
+constexpr int kTileLeast = WARPS * 8;
 constexpr int BACK = 8;               // windows of WARPS earlier tiles kept by one look-back
 
 // Published map or state of one channel of one tile, 16 bytes, read and written whole.
@@ -81,6 +87,7 @@ struct Raw<__nv_bfloat16, 2> { using type = unsigned; };
 template <typename T, int VEC>
 using raw_t = typename Raw<T, VEC>::type;
 
+// (arrays of VEC floats: the members of Vf below)
 __device__ __forceinline__ void unpack(float r, float (&v)[1]) { v[0] = r; }
 __device__ __forceinline__ void unpack(float2 r, float (&v)[2]) { v[0] = r.x; v[1] = r.y; }
 __device__ __forceinline__ void unpack(unsigned short r, float (&v)[1]) { v[0] = __uint_as_float((unsigned)r << 16); }
@@ -106,77 +113,163 @@ __device__ __forceinline__ void store(const Tensor &t, size_t off, const float (
     *reinterpret_cast<raw_t<T, VEC> *>(const_cast<T *>(static_cast<const T *>(t.p)) + off) = r;
 }
 
-// ------------------------------------------------------------ gates
-__device__ __forceinline__ float rsqrt_approx(float x) {
-    float r;
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+// ------------------------------------------------------------ arithmetic on VEC channels
+// Pairs of fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
+// scalar ones): the gates' arithmetic, not memory, bounds a kernel that issues them singly.
+template <int VEC>
+struct Vf {
+    float v[VEC];
+};
+HLA_DEVICE unsigned long long pair(const Vf<2> &x) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.v[0]), "f"(x.v[1]));
     return r;
 }
-// sigma(z) and 1 - sigma(z), both with a relative error of a few units in the last place of
-// the smaller: the larger is one minus it, so that a gate near one, whose error a long
-// product of gates multiplies, is off by its rounding only.  Below -87 the exponential
-// would pass the largest float; sigma is then under the smallest normal one.
-__device__ __forceinline__ void sigmoid2(float z, float &s, float &c) {
-    const float e = __expf(z < -87.f ? 87.f : -z), r = __fdividef(1.f, 1.f + e), er = e * r;
-    s = z > 0.f ? 1.f - er : r;
-    c = z > 0.f ? er : 1.f - r;
+HLA_DEVICE Vf<2> unpair(unsigned long long r) {
+    Vf<2> x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.v[0]), "=f"(x.v[1]) : "l"(r));
+    return x;
 }
-// 1 - exp(-u) for u >= 0.  Below 1/4 the difference would cancel: Taylor's series in nested
-// form to u^7, whose next term is under 2^-28 of the sum there.
-__device__ __forceinline__ float one_minus_exp(float u) {
-    if (u < 0.25f) {
-        float p = fmaf(-u, 1.f / 7.f, 1.f);
-        p = fmaf(-u * (1.f / 6.f), p, 1.f);
-        p = fmaf(-u * (1.f / 5.f), p, 1.f);
-        p = fmaf(-u * (1.f / 4.f), p, 1.f);
-        p = fmaf(-u * (1.f / 3.f), p, 1.f);
-        p = fmaf(-u * 0.5f, p, 1.f);
-        return u * p;
-    }
-    return 1.f - __expf(-u);
+template <int VEC>
+HLA_DEVICE Vf<VEC> splat(float c) {
+    Vf<VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = c;
+    return r;
+}
+HLA_DEVICE Vf<1> fma_(Vf<1> a, Vf<1> b, Vf<1> c) { return {fmaf(a.v[0], b.v[0], c.v[0])}; }
+HLA_DEVICE Vf<1> mul_(Vf<1> a, Vf<1> b) { return {a.v[0] * b.v[0]}; }
+HLA_DEVICE Vf<1> add_(Vf<1> a, Vf<1> b) { return {a.v[0] + b.v[0]}; }
+HLA_DEVICE Vf<2> fma_(const Vf<2> &a, const Vf<2> &b, const Vf<2> &c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(r);
+}
+HLA_DEVICE Vf<2> mul_(const Vf<2> &a, const Vf<2> &b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+HLA_DEVICE Vf<2> add_(const Vf<2> &a, const Vf<2> &b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+template <int VEC>
+HLA_DEVICE Vf<VEC> sub_(const Vf<VEC> &a, const Vf<VEC> &b) {  // a - b
+    return fma_(b, splat<VEC>(-1.f), a);
+}
+template <int VEC, class F>
+HLA_DEVICE Vf<VEC> each(const Vf<VEC> &a, F f) {
+    Vf<VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = f(a.v[i]);
+    return r;
+}
+HLA_DEVICE float rsqrt_approx(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+HLA_DEVICE float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// a_t and the factor of x_t
-template <int GATE>
-__device__ __forceinline__ void gate_fwd(float g, float r, float &a, float &f) {
-    if constexpr (GATE == HLA_GATE_GIVEN) {
-        a = g;
-        f = 1.f;
-    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        sigmoid2(g, a, f);
-    } else {
-        float s, c;
-        sigmoid2(g, s, c);
-        const float w = one_minus_exp(r * s), q = w * (2.f - w);  // 1 - a and 1 - a^2
-        a = 1.f - w;
-        f = q > 0.f ? q * rsqrt_approx(q) : q;  // q = 0: no input; a NaN stays one
+// ------------------------------------------------------------ gates
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigma(z) and 1 - sigma(z), both with a relative error of a few units in the last place:
+// the smaller is e / (1 + e), e = exp(-|z|) <= 1, and the larger is one minus it, so that a
+// gate near one, whose error a long product of gates multiplies, is off by its rounding only.
+template <int VEC>
+HLA_DEVICE void sigmoid2(const Vf<VEC> &z, Vf<VEC> &s, Vf<VEC> &c) {
+    const Vf<VEC> e = each(z, [](float x) { return ex2_approx(fabsf(x) * -kLog2e); });
+    const Vf<VEC> r = each(add_(e, splat<VEC>(1.f)), rcp_approx);
+    const Vf<VEC> lo = mul_(e, r), hi = sub_(splat<VEC>(1.f), lo);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const bool up = z.v[i] > 0.f;
+        s.v[i] = up ? hi.v[i] : lo.v[i];
+        c.v[i] = up ? lo.v[i] : hi.v[i];
     }
 }
-// Gradients with respect to x, g and (HLA_GATE_RATE) the rate, from gh = dL/dh_t, x_t and
-// y = h_{t-1}; a is the gate.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f,
-// da/du = -a.  f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
-template <int GATE>
-__device__ __forceinline__ void gate_bwd(float g, float r, float x, float y, float gh, float &a, float &dx, float &dg,
-                                         float &dr) {
+// sigma(z) alone, a few units in the last place off: far below zero the exponential is
+// infinite and the quotient zero.
+template <int VEC>
+HLA_DEVICE Vf<VEC> sigmoid(const Vf<VEC> &z) {
+    const Vf<VEC> e = each(mul_(z, splat<VEC>(-kLog2e)), ex2_approx);
+    return each(add_(e, splat<VEC>(1.f)), rcp_approx);
+}
+// 1 - exp(-u) for u >= 0.  Below 1/16 the difference would cancel: Taylor's series to u^5,
+// whose next term is under 2^-29 of the sum there.
+template <int VEC>
+HLA_DEVICE Vf<VEC> one_minus_exp(const Vf<VEC> &u) {
+    const Vf<VEC> e = each(mul_(u, splat<VEC>(-kLog2e)), ex2_approx);
+    const Vf<VEC> far = sub_(splat<VEC>(1.f), e);
+    Vf<VEC> p = fma_(u, splat<VEC>(1.f / 120.f), splat<VEC>(-1.f / 24.f));
+    p = fma_(p, u, splat<VEC>(1.f / 6.f));
+    p = fma_(p, u, splat<VEC>(-0.5f));
+    p = fma_(p, u, splat<VEC>(1.f));
+    p = mul_(p, u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p.v[i] = u.v[i] < 0.0625f ? p.v[i] : far.v[i];
+    return p;
+}
+// 1 / sqrt(q) for q >= 0, finite at 0
+template <int VEC>
+HLA_DEVICE Vf<VEC> rsqrt0(const Vf<VEC> &q) {
+    return each(q, [](float x) { return rsqrt_approx(fmaxf(x, 1.2e-38f)); });
+}
+
+// a_t and b_t
+template <int GATE, int VEC>
+HLA_DEVICE void gate_fwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, Vf<VEC> &a, Vf<VEC> &b) {
     if constexpr (GATE == HLA_GATE_GIVEN) {
         a = g;
-        dx = gh;
-        dg = gh * y;
+        b = x;
     } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        float f;
-        sigmoid2(g, a, f);
-        dx = gh * f;
-        dg = gh * (y - x) * (a * f);
+        Vf<VEC> c;
+        sigmoid2(g, a, c);
+        b = mul_(c, x);
     } else {
-        float s, c;
+        const Vf<VEC> w = one_minus_exp(mul_(r, sigmoid(g)));  // 1 - a
+        a = sub_(splat<VEC>(1.f), w);
+        const Vf<VEC> q = fma_(w, a, w);  // 1 - a^2
+        b = mul_(mul_(q, rsqrt0(q)), x);
+    }
+}
+// a_t alone, the same bits as gate_fwd's
+template <int GATE, int VEC>
+HLA_DEVICE Vf<VEC> gate_a(const Vf<VEC> &g, const Vf<VEC> &r) {
+    Vf<VEC> a, b;
+    gate_fwd<GATE>(g, r, splat<VEC>(0.f), a, b);
+    return a;
+}
+// Gradients with respect to x, g and (HLA_GATE_RATE) the rate, from gh = dL/dh_t, x_t,
+// y = h_{t-1} and a_t.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f, da/du = -a.
+// f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
+template <int GATE, int VEC>
+HLA_DEVICE void gate_bwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, const Vf<VEC> &y, const Vf<VEC> &gh,
+                         const Vf<VEC> &a, Vf<VEC> &dx, Vf<VEC> &dg, Vf<VEC> &dr) {
+    if constexpr (GATE == HLA_GATE_GIVEN) {
+        dx = gh;
+        dg = mul_(gh, y);
+    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
+        Vf<VEC> s, c;
         sigmoid2(g, s, c);
-        const float u = r * s, w = one_minus_exp(u), q = w * (2.f - w);
-        a = 1.f - w;
-        const float rf = q == 0.f ? 0.f : rsqrt_approx(q);
-        dx = gh * (q * rf);
-        const float du = gh * a * fmaf(x * a, rf, -y);
-        dg = du * u * c;
-        dr = du * s;
+        dx = mul_(gh, c);
+        dg = mul_(mul_(dx, s), sub_(y, x));
+    } else {
+        Vf<VEC> s, c;
+        sigmoid2(g, s, c);
+        const Vf<VEC> u = mul_(r, s), w = one_minus_exp(u), q = fma_(w, a, w);
+        const Vf<VEC> rf = rsqrt0(q);
+        dx = mul_(gh, mul_(q, rf));
+        const Vf<VEC> du = mul_(mul_(gh, a), sub_(mul_(mul_(x, a), rf), y));
+        dg = mul_(du, mul_(u, c));
+        dr = mul_(du, s);
     }
 }
 
@@ -324,8 +417,80 @@ __device__ __forceinline__ int length_of(const Args &a, int b) {
 }
 
 // ------------------------------------------------------------ forward
+template <int GATE, int VEC>
+HLA_DEVICE Vf<VEC> rate_of(const Args &a, int ch) {
+    Vf<VEC> r = splat<VEC>(0.f);
+    if constexpr (GATE == HLA_GATE_RATE) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            if (ch + v < a.d) r.v[v] = a.rate[ch + v];
+    }
+    return r;
+}
+// The state before this warp's tokens: the tile's, taken through the maps of the warps before.
+template <int VEC>
+HLA_DEVICE Vf<VEC> before_warp(const Shared<VEC> &sh, int warp, int lane) {
+    Vf<VEC> h;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        h.v[v] = sh.carry[lane * VEC + v];
+        for (int w = 0; w < warp; ++w) {
+            const float2 mp = sh.agg[w][lane * VEC + v];
+            h.v[v] = fmaf(mp.x, h.v[v], mp.y);
+        }
+    }
+    return h;
+}
+
+// One tile: loads, gates, the warps' maps, the state before the tile, outputs.  FULL: every
+// thread of the CTA has all its TS tokens, so nothing is predicated.
+template <typename T, int GATE, int VEC, bool FULL>
+HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, int b, int c0, int t0, int m, int len) {
+    constexpr int TS = kTS<T, FWD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
+    const size_t so = (size_t)b * a.d;
+    raw_t<T, VEC> xr[TS] = {}, gr[TS] = {};
+    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch, go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch;
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+        if (FULL || i < m) gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+        if (FULL || i < m) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
+    const Vf<VEC> r = rate_of<GATE, VEC>(a, ch);
+    Vf<VEC> ea[TS], eb[TS], A = splat<VEC>(1.f), Bv = splat<VEC>(0.f);
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        Vf<VEC> x, g;
+        unpack(xr[i], x.v);
+        unpack(gr[i], g.v);
+        gate_fwd<GATE>(g, r, x, ea[i], eb[i]);
+        if (!FULL && i >= m) {
+            ea[i] = splat<VEC>(1.f);
+            eb[i] = splat<VEC>(0.f);
+        }
+        Bv = fma_(ea[i], Bv, eb[i]);
+        A = mul_(A, ea[i]);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A.v[v], Bv.v[v]);
+    __syncthreads();
+    const bool last = pos == (len - 1) / kTileT<T, FWD>;
+    if (!look_back<VEC>(sh, a, chain, pos, 0, a.state_in ? a.state_in + so : nullptr, c0,
+                        last && a.out_state ? a.out_state + so : nullptr))
+        return;
+    Vf<VEC> h = before_warp<VEC>(sh, warp, lane);
+    const size_t yo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+        h = fma_(ea[i], h, eb[i]);
+        if (FULL || i < m) store<T, VEC>(a.o1, yo + (size_t)i * a.o1.st, h.v);
+    }
+}
+
 template <typename T, int GATE, int VEC>
-__global__ void __launch_bounds__(kThreads) gated_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
+    constexpr int TS = kTS<T, FWD>, TILE_T = kTileT<T, FWD>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
@@ -343,70 +508,103 @@ __global__ void __launch_bounds__(kThreads) gated_fwd_kernel(const Args a) {
     if (pos * TILE_T >= len) return;
     const int t0 = pos * TILE_T + warp * TS;
     const int m = ch < a.d ? min(TS, len - t0) : 0;  // tokens of this thread (may be <= 0)
+    if ((pos + 1) * TILE_T <= len && c0 + C <= a.d)  // the same for the whole CTA
+        fwd_tile<T, GATE, VEC, true>(sh, a, chain, pos, b, c0, t0, m, len);
+    else
+        fwd_tile<T, GATE, VEC, false>(sh, a, chain, pos, b, c0, t0, m, len);
+}
 
-    raw_t<T, VEC> xr[TS], gr[TS];
-    size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch, go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch;
+// ------------------------------------------------------------ backward
+template <typename T, int GATE, int VEC, bool FULL>
+HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, int tile, int b, int c0, int t0, int m,
+                         int len) {
+    constexpr int TS = kTS<T, BWD>;
+    constexpr int C = 32 * VEC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
+    const size_t so = (size_t)b * a.d;
+    raw_t<T, VEC> gr[TS] = {}, dr[TS] = {}, yr[TS] = {}, xr[TS] = {};
+    const size_t go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch, dyo = (size_t)b * a.dy.sb + (size_t)t0 * a.dy.st + ch;
+    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch;
+    // y one token earlier: h_{t-1}; the token before the first is state_in
+    const T *yp = static_cast<const T *>(a.y.p) + (size_t)b * a.y.sb + ch;
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
-        if (i < m) {
-            xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
+        if (FULL || i < m) {
             gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
+            dr[i] = load<T, VEC>(a.dy, dyo + (size_t)i * a.dy.st);
         }
     }
-    float r[VEC];
-    if constexpr (GATE == HLA_GATE_RATE) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) r[v] = ch + v < a.d ? a.rate[ch + v] : 0.f;
-    }
-    float ea[TS][VEC], eb[TS][VEC], A[VEC], Bv[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) { A[v] = 1.f; Bv[v] = 0.f; }
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
-        if (i < m) {
-            float x[VEC], g[VEC];
-            unpack(xr[i], x);
-            unpack(gr[i], g);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float f;
-                gate_fwd<GATE>(g[v], r[v], ea[i][v], f);
-                eb[i][v] = GATE == HLA_GATE_GIVEN ? x[v] : f * x[v];
-                Bv[v] = fmaf(ea[i][v], Bv[v], eb[i][v]);
-                A[v] *= ea[i][v];
-            }
+        if (FULL || i < m) {
+            if (i > 0 || t0 > 0)
+                yr[i] = __ldg(reinterpret_cast<const raw_t<T, VEC> *>(yp + ((size_t)t0 + i - 1) * a.y.st));
+            if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
         }
     }
+    const Vf<VEC> r = rate_of<GATE, VEC>(a, ch);
+    Vf<VEC> h0 = splat<VEC>(0.f), ea[TS], A = splat<VEC>(1.f), Bv = splat<VEC>(0.f);
+    if (t0 == 0 && a.state_in) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A[v], Bv[v]);
+        for (int v = 0; v < VEC; ++v)
+            if (ch + v < a.d) h0.v[v] = a.state_in[so + ch + v];
+    }
+#pragma unroll
+    for (int i = TS - 1; i >= 0; --i) {
+        Vf<VEC> g, dy;
+        unpack(gr[i], g.v);
+        unpack(dr[i], dy.v);
+        ea[i] = gate_a<GATE>(g, r);
+        if (!FULL && i >= m) ea[i] = splat<VEC>(1.f);
+        Bv = mul_(ea[i], add_(dy, Bv));
+        A = mul_(A, ea[i]);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A.v[v], Bv.v[v]);
     __syncthreads();
-    const bool last = pos == (len - 1) / TILE_T;
-    if (!look_back<VEC>(sh, a, chain, pos, 0, a.state_in ? a.state_in + so : nullptr, c0,
-                        last && a.out_state ? a.out_state + so : nullptr))
+    const int first = a.tiles - 1 - (len - 1) / kTileT<T, BWD>;
+    if (!look_back<VEC>(sh, a, chain, pos, first, a.d_state_out ? a.d_state_out + so : nullptr, c0,
+                        tile == 0 && a.out_state ? a.out_state + so : nullptr))
         return;
-    float h[VEC];
+    Vf<VEC> c = before_warp<VEC>(sh, warp, lane), sum = splat<VEC>(0.f);
+    const size_t dxo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch, dgo = (size_t)b * a.o2.sb + (size_t)t0 * a.o2.st + ch;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        h[v] = sh.carry[lane * VEC + v];
-        for (int w = 0; w < warp; ++w) {
-            const float2 mp = sh.agg[w][lane * VEC + v];
-            h[v] = fmaf(mp.x, h[v], mp.y);
+    for (int i = TS - 1; i >= 0; --i) {
+        Vf<VEC> g, dy, x = splat<VEC>(0.f), y, dx, dg, drv;
+        unpack(gr[i], g.v);
+        unpack(dr[i], dy.v);
+        unpack(yr[i], y.v);
+        if (i == 0 && t0 == 0) y = h0;
+        if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
+        const Vf<VEC> gh = add_(dy, c);
+        gate_bwd<GATE>(g, r, x, y, gh, ea[i], dx, dg, drv);
+        c = mul_(ea[i], gh);
+        if (FULL || i < m) {
+            if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
+            store<T, VEC>(a.o1, dxo + (size_t)i * a.o1.st, dx.v);
+            store<T, VEC>(a.o2, dgo + (size_t)i * a.o2.st, dg.v);
         }
     }
-    const size_t yo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
+    if constexpr (GATE == HLA_GATE_RATE) {
+        if (a.part) {  // the tile's sum of every channel, warps in order
+            __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TS; ++i) {
-        if (i < m) {
+            for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v].x = sum.v[v];
+            __syncthreads();
+            if (threadIdx.x < C) {
+                float s = 0.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = fmaf(ea[i][v], h[v], eb[i][v]);
-            store<T, VEC>(a.o1, yo + (size_t)i * a.o1.st, h);
+                for (int w = 0; w < WARPS; ++w) s += sh.agg[w][threadIdx.x].x;
+                Record *p = a.part + (chain * a.tiles + tile) * C + threadIdx.x;
+                *reinterpret_cast<float4 *>(p) = make_float4(s, 0.f, 0.f, 0.f);
+            }
         }
     }
 }
 
-// ------------------------------------------------------------ backward
 template <typename T, int GATE, int VEC>
-__global__ void __launch_bounds__(kThreads) gated_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const Args a) {
+    constexpr int TS = kTS<T, BWD>, TILE_T = kTileT<T, BWD>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
@@ -426,116 +624,23 @@ __global__ void __launch_bounds__(kThreads) gated_bwd_kernel(const Args a) {
     const int t0 = tile * TILE_T + (WARPS - 1 - warp) * TS;
     const int m = ch < a.d ? min(TS, len - t0) : 0;
 
-    raw_t<T, VEC> gr[TS], dr[TS], yr[TS], xr[TS];
-    const size_t go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch, dyo = (size_t)b * a.dy.sb + (size_t)t0 * a.dy.st + ch;
-    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch;
-    // y one token earlier: h_{t-1}; the token before the first is state_in
-    const T *yp = static_cast<const T *>(a.y.p) + (size_t)b * a.y.sb + ch;
-#pragma unroll
-    for (int i = 0; i < TS; ++i) {
-        if (i < m) {
-            gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
-            dr[i] = load<T, VEC>(a.dy, dyo + (size_t)i * a.dy.st);
-            if (t0 + i > 0)
-                yr[i] = __ldg(reinterpret_cast<const raw_t<T, VEC> *>(yp + (size_t)(t0 + i - 1) * a.y.st));
-            if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
-        }
-    }
-    float r[VEC], h0[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        r[v] = GATE == HLA_GATE_RATE && ch + v < a.d ? a.rate[ch + v] : 0.f;
-        h0[v] = t0 == 0 && a.state_in && ch + v < a.d ? a.state_in[so + ch + v] : 0.f;
-    }
-    float A[VEC], Bv[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) { A[v] = 1.f; Bv[v] = 0.f; }
-#pragma unroll
-    for (int i = TS - 1; i >= 0; --i) {
-        if (i < m) {
-            float g[VEC], dy[VEC];
-            unpack(gr[i], g);
-            unpack(dr[i], dy);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float ea, f;
-                gate_fwd<GATE>(g[v], r[v], ea, f);
-                Bv[v] = ea * (dy[v] + Bv[v]);
-                A[v] *= ea;
-            }
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A[v], Bv[v]);
-    __syncthreads();
-    const int first = a.tiles - 1 - (len - 1) / TILE_T;
-    if (!look_back<VEC>(sh, a, chain, pos, first, a.d_state_out ? a.d_state_out + so : nullptr, c0,
-                        tile == 0 && a.out_state ? a.out_state + so : nullptr))
-        return;
-    float c[VEC], sum[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        c[v] = sh.carry[lane * VEC + v];
-        sum[v] = 0.f;
-        for (int w = 0; w < warp; ++w) {
-            const float2 mp = sh.agg[w][lane * VEC + v];
-            c[v] = fmaf(mp.x, c[v], mp.y);
-        }
-    }
-    const size_t dxo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch, dgo = (size_t)b * a.o2.sb + (size_t)t0 * a.o2.st + ch;
-#pragma unroll
-    for (int i = TS - 1; i >= 0; --i) {
-        if (i < m) {
-            float g[VEC], dy[VEC], x[VEC], y[VEC], dx[VEC], dg[VEC];
-            unpack(gr[i], g);
-            unpack(dr[i], dy);
-            if (t0 + i > 0) {
-                unpack(yr[i], y);
-            } else {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) y[v] = h0[v];
-            }
-            if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float gh = dy[v] + c[v];
-                float ea, drv = 0.f;
-                gate_bwd<GATE>(g[v], r[v], GATE == HLA_GATE_GIVEN ? 0.f : x[v], y[v], gh, ea, dx[v], dg[v], drv);
-                sum[v] += drv;
-                c[v] = ea * gh;
-            }
-            store<T, VEC>(a.o1, dxo + (size_t)i * a.o1.st, dx);
-            store<T, VEC>(a.o2, dgo + (size_t)i * a.o2.st, dg);
-        }
-    }
-    if constexpr (GATE == HLA_GATE_RATE) {
-        if (a.part) {  // the tile's sum of every channel, warps in order
-            __syncthreads();
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v].x = sum[v];
-            __syncthreads();
-            if (threadIdx.x < C) {
-                float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) s += sh.agg[w][threadIdx.x].x;
-                Record *p = a.part + (chain * a.tiles + tile) * C + threadIdx.x;
-                *reinterpret_cast<float4 *>(p) = make_float4(s, 0.f, 0.f, 0.f);
-            }
-        }
-    }
+    if ((tile + 1) * TILE_T <= len && c0 + C <= a.d)
+        bwd_tile<T, GATE, VEC, true>(sh, a, chain, pos, tile, b, c0, t0, m, len);
+    else
+        bwd_tile<T, GATE, VEC, false>(sh, a, chain, pos, tile, b, c0, t0, m, len);
 }
 
 // d_rate[c] = sum of the tiles' partial sums, in an order fixed by the sizes: warp w of a
 // channel group takes tiles w, w + 8, ... of sequence 0, 1, ..., then the warps are added.
 template <int VEC>
-__global__ void __launch_bounds__(kThreads) gated_rate_kernel(const Args a, float *d_rate) {
+__global__ void __launch_bounds__(kThreads) gated_rate_kernel(const Args a, int tile_t, float *d_rate) {
     constexpr int C = 32 * VEC;
     __shared__ float red[WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < a.d) {
         for (int b = 0; b < a.B; ++b) {
-            const int used = (length_of(a, b) + TILE_T - 1) / TILE_T;
+            const int used = (int)(((long long)length_of(a, b) + tile_t - 1) / tile_t);
             const Record *p = a.part + (((size_t)b * a.slices + c / C) * a.tiles) * C + c % C;
             for (int t = warp; t < used; t += WARPS) s += __ldg(&p[(size_t)t * C].a);
         }
@@ -557,25 +662,24 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const Args a) {
     if (e >= cols * a.B) return;
     const int b = (int)(e / cols), ch = (int)(e % cols) * VEC;
     if (a.lengths && a.lengths[b] <= 0) return;
-    float x[VEC], g[VEC], h[VEC];
-    unpack(load<T, VEC>(a.x, (size_t)b * a.x.sb + ch), x);
-    unpack(load<T, VEC>(a.g, (size_t)b * a.g.sb + ch), g);
+    Vf<VEC> x, g, h, ea, eb;
+    unpack(load<T, VEC>(a.x, (size_t)b * a.x.sb + ch), x.v);
+    unpack(load<T, VEC>(a.g, (size_t)b * a.g.sb + ch), g.v);
     const size_t so = (size_t)b * a.d + ch;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        float ea, f;
-        gate_fwd<GATE>(g[v], GATE == HLA_GATE_RATE ? a.rate[ch + v] : 0.f, ea, f);
-        h[v] = fmaf(ea, a.state_in[so + v], GATE == HLA_GATE_GIVEN ? x[v] : f * x[v]);
-    }
+    for (int v = 0; v < VEC; ++v) h.v[v] = a.state_in[so + v];
+    gate_fwd<GATE>(g, rate_of<GATE, VEC>(a, ch), x, ea, eb);
+    h = fma_(ea, h, eb);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) a.out_state[so + v] = h[v];
-    store<T, VEC>(a.o1, (size_t)b * a.o1.sb + ch, h);
+    for (int v = 0; v < VEC; ++v) a.out_state[so + v] = h.v[v];
+    store<T, VEC>(a.o1, (size_t)b * a.o1.sb + ch, h.v);
 }
 
 // ------------------------------------------------------------ host
 template <int VEC>
 int slices_of(int d) { return (d + 32 * VEC - 1) / (32 * VEC); }
-int tiles_of(int n) { return (n + TILE_T - 1) / TILE_T; }
+int tiles_of(long long n, int tile) { return (int)((n + tile - 1) / tile); }
+int most_tiles(const hla_gated_params *p) { return tiles_of(p->n, kTileLeast); }
 
 // Two channels per lane when every row of every tensor starts on a two-channel boundary
 // and rows hold a whole number of them: a row segment is then 128 bytes (bf16) per warp
@@ -591,7 +695,7 @@ hla_status check(const hla_gated_params *p) {
     if (p->gate != HLA_GATE_GIVEN && p->gate != HLA_GATE_SIGMOID && p->gate != HLA_GATE_RATE)
         return report(HLA_ERR_ARG, "unknown gate");
     if (p->gate == HLA_GATE_RATE && !p->rate) return report(HLA_ERR_ARG, "HLA_GATE_RATE needs rate");
-    const double tiles = (double)((p->n + (long long)TILE_T - 1) / TILE_T), slices = (double)((p->d + 31LL) / 32);
+    const double tiles = most_tiles(p), slices = (double)((p->d + 31LL) / 32);
     if ((double)p->B * (tiles < 1 ? 1 : tiles) * slices > 2147483647.0 || (double)p->B * p->d > 1099511627776.0)
         return report(HLA_ERR_ARG, "problem too large");
     return HLA_OK;
@@ -626,7 +730,7 @@ Tensor view(const hla_tensor *t) {
 
 // Records of a call: the channel slots of all tiles, for the wider of the two layouts.
 size_t record_count(const hla_gated_params *p) {
-    const size_t tiles = tiles_of(p->n);
+    const size_t tiles = most_tiles(p);
     const size_t s1 = (size_t)slices_of<1>(p->d) * 32, s2 = (size_t)slices_of<2>(p->d) * 64;
     return (size_t)p->B * tiles * (s1 > s2 ? s1 : s2);
 }
@@ -635,27 +739,27 @@ size_t workspace_bytes_of(const hla_gated_params *p) {
     return p->n == 0 ? 0 : kHeaderBytes + 2 * record_count(p) * sizeof(Record);
 }
 
-enum Which { FWD, BWD, STEP };
+enum Which { W_FWD, W_BWD, W_STEP };
 
 template <typename T, int GATE, int VEC>
 cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
     a.slices = slices_of<VEC>(a.d);
-    a.tiles = tiles_of(a.n);
-    if (w == STEP) {
+    a.tiles = w == W_BWD ? tiles_of(a.n, kTileT<T, BWD>) : tiles_of(a.n, kTileT<T, FWD>);
+    if (w == W_STEP) {
         const size_t total = (size_t)a.B * ((a.d + VEC - 1) / VEC);
         gated_step_kernel<T, GATE, VEC><<<(unsigned)((total + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
     const unsigned grid = (unsigned)((size_t)a.B * a.slices * a.tiles);
     if (a.tiles <= 1) a.hdr = nullptr;  // no tile waits for another
-    if (w == FWD) {
+    if (w == W_FWD) {
         gated_fwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
     gated_bwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.part && GATE == HLA_GATE_RATE) {
-        gated_rate_kernel<VEC><<<(a.d + 31) / 32, kThreads, 0, st>>>(a, d_rate);
+        gated_rate_kernel<VEC><<<(a.d + 31) / 32, kThreads, 0, st>>>(a, kTileT<T, BWD>, d_rate);
         e = cudaGetLastError();
     }
     return e;
@@ -685,7 +789,7 @@ hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, flo
 // Splits the caller's workspace; the header is needed from two tiles on.
 hla_status take_workspace(const hla_gated_params *p, void *ws, size_t bytes, bool partials, Args &a) {
     const size_t need = workspace_bytes_of(p);
-    if (!ws && tiles_of(p->n) <= 1 && !partials) return HLA_OK;
+    if (!ws && most_tiles(p) <= 1 && !partials) return HLA_OK;
     if (!ws || bytes < need) return report(HLA_ERR_ARG, "workspace too small (hla_gated_workspace_size)");
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return report(HLA_ERR_ARG, "workspace must be 256-byte aligned");
     a.hdr = static_cast<Header *>(ws);
@@ -733,7 +837,7 @@ hla_status hla_gated_forward(const hla_gated_params *p, const hla_tensor *x, con
     a.state_in = state_in;
     a.out_state = state_out;
     const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    return dispatch(p, FWD, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr, st);
+    return dispatch(p, W_FWD, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr, st);
 }
 
 hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
@@ -775,7 +879,7 @@ hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, co
     const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
     bool pairs = p->d % 2 == 0 && pairable(dx, el) && pairable(dg, el);
     for (const hla_tensor *i : ins) pairs = pairs && pairable(i, el);
-    return dispatch(p, BWD, a, pairs, d_rate, st);
+    return dispatch(p, W_BWD, a, pairs, d_rate, st);
 }
 
 hla_status hla_gated_step(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
@@ -794,7 +898,7 @@ hla_status hla_gated_step(const hla_gated_params *p, const hla_tensor *x, const 
     a.state_in = state;
     a.out_state = state_out;
     const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    return dispatch(p, STEP, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr,
+    return dispatch(p, W_STEP, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr,
                     static_cast<cudaStream_t>(stream));
 }
 

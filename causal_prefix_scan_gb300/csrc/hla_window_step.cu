@@ -219,11 +219,209 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
     join<T, DP>(a, out, w.b, w.h0, w.heads);
 }
 
-template <typename T, int DP>
-cudaError_t launch(const StepArgs &a, cudaStream_t st) {
-    constexpr size_t bytes = (size_t)(2 * TS * (DP + 4) + HG * DP + 4 * HG * TS + TS * HG) * 4;
-    auto fn = step_kernel<T, DP>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// ------------------------------------------------------------ tensor cores
+// bf16 caches with 16-byte rows.  A warp takes 16 slots at a time, keeps its own running
+// maximum, sum and O for 8 heads, and needs no shared memory until the end: K and V go from
+// global memory straight into the operand registers of mma.m16n8k16, 16 bytes per load.
+//   S^T [16 slots x 8 heads] = K Q^T: rows g, g + 8 of K; the 16-byte chunk 4 c + q of a row
+//     serves two contraction steps (the order of the contraction index is free, Q's is the same);
+//   P^T passes from the accumulator's layout to that of the second operand by an 8 x 8
+//     transpose of packed pairs (movmatrix);
+//   O^T [16 columns x 8 heads] += V^T P^T: a thread loads four rows' chunk of columns 8 g ..
+//     8 g + 7 and packs pairs of rows; row g and g + 8 of product t are columns 8 g + 2 t, + 1.
+// (lane = 4 g + q.)  mma.sync suffices: the work per byte is that of 8 heads, and the loads
+// bound it; tcgen05 would want 128 rows of queries and the operands staged in shared memory.
+// The next 16 slots' K is loaded while this P is formed, their V while O is added up, so
+// a warp has 4 to 8 KB on their way at all times.
+constexpr int kWarps = 8, GS = 16;
+
+HLA_DEVICE void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+HLA_DEVICE uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+HLA_DEVICE uint4 load16(const __nv_bfloat16 *p) {  // streamed: read once
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+    return u;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 2) step_mma_kernel(const StepArgs a) {
+    constexpr int KC = DP / 32, VB = DP / 64;  // 16-byte chunks of a K row per thread, 64-column blocks
+    __shared__ Partial<DP> part[kWarps];
+    __shared__ Partial<DP> out;
+    const Place w(a);
+    if (w.p < 0) return;  // uniform over the cluster
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int rank = blockIdx.x % a.split, step = a.split * kWarps * GS;
+    using bf = __nv_bfloat16;
+    const bf *kc = static_cast<const bf *>(a.kc.p) + (size_t)w.b * a.kc.sb + (size_t)w.hk * a.kc.sh;
+    const bf *vc = static_cast<const bf *>(a.vc.p) + (size_t)w.b * a.vc.sb + (size_t)w.hk * a.vc.sh;
+    const bf *kn = static_cast<const bf *>(a.k.p) + (size_t)w.b * a.k.sb + (size_t)w.hk * a.k.sh;
+    const bf *vn = static_cast<const bf *>(a.v.p) + (size_t)w.b * a.v.sb + (size_t)w.hk * a.v.sh;
+    if (rank == 0 && w.h0 == w.hk * a.G) {  // the new row goes into the cache; readers take it from k, v
+        bf *ko = static_cast<bf *>(a.kc.p) + (kc - static_cast<const bf *>(a.kc.p)) + (size_t)w.slot * a.kc.st;
+        bf *vo = static_cast<bf *>(a.vc.p) + (vc - static_cast<const bf *>(a.vc.p)) + (size_t)w.slot * a.vc.st;
+        if (tid < a.d) ko[tid] = kn[tid];
+        if (tid >= 128 && tid - 128 < a.dv) vo[tid - 128] = vn[tid - 128];
+    }
+    // Q as the second operand: head g, the chunks of K's rows that this thread loads
+    uint32_t qb[KC][4];
+    {
+        const bf *qr = static_cast<const bf *>(a.q.p) + (size_t)w.b * a.q.sb + (size_t)(w.h0 + g) * a.q.sh;
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int x = (4 * c + q) * 8 + 2 * e;
+                uint32_t lo = 0, hi = 0;
+                if (g < w.heads && x < a.d) {
+                    lo = __bfloat16_as_ushort(qr[x]);
+                    hi = __bfloat16_as_ushort(qr[x + 1]);
+                }
+                qb[c][e] = lo | (hi << 16);
+            }
+    }
+    const float sc = a.scale * kLog2e;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 q, 2 q + 1 (l: this thread's slots)
+    float o[VB * 4][4] = {};
+    uint4 kr[2][KC], vr[4][VB];
+    auto row = [&](const bf *cache, const bf *fresh, long long st, int s) {
+        return s == w.slot ? fresh : cache + (size_t)s * st;
+    };
+    auto load_k = [&](int s0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int s = s0 + g + 8 * r;
+            const bf *p = row(kc, kn, a.kc.st, s);
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+                kr[r][c] = s < w.slots && (4 * c + q) * 8 < a.d ? load16(p + (4 * c + q) * 8) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto load_v = [&](int s0) {  // rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9; zeros where no slot is visible
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int s = s0 + 2 * q + (r & 1) + 8 * (r >> 1);
+            const bf *p = row(vc, vn, a.vc.st, s);
+#pragma unroll
+            for (int c = 0; c < VB; ++c)
+                vr[r][c] = s < w.slots && 64 * c + 8 * g < a.dv ? load16(p + 64 * c + 8 * g) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    int s0 = (rank * kWarps + warp) * GS;
+    if (s0 < w.slots) {
+        load_k(s0);
+        load_v(s0);
+    }
+    for (; s0 < w.slots; s0 += step) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const uint32_t a0[4] = {kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y};
+            const uint32_t a1[4] = {kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w};
+            mma16816(s, a0, qb[c][0], qb[c][1]);
+            mma16816(s, a1, qb[c][2], qb[c][3]);
+        }
+        const bool more = s0 + step < w.slots;
+        if (more) load_k(s0 + step);
+        // s[0], s[1]: slot g, heads 2 q, 2 q + 1; s[2], s[3]: slot g + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = s0 + g + 8 * (i >> 1) < w.slots ? s[i] * sc : -INFINITY;
+        // the reference maximum moves only when a score passes it by 2^8: P stays below 2^8
+        const bool move = s[0] > m[0] + 8.f || s[2] > m[0] + 8.f || s[1] > m[1] + 8.f || s[3] > m[1] + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = fmaxf(m[i], fmaxf(s[i], s[i + 2]));
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                f[i] = x == -INFINITY ? 1.f : ex2_approx(m[i] - x);
+                m[i] = x;
+                l[i] *= f[i];
+            }
+#pragma unroll
+            for (int t = 0; t < VB * 4; ++t) {
+                o[t][0] *= f[0];
+                o[t][1] *= f[1];
+                o[t][2] *= f[0];
+                o[t][3] *= f[1];
+            }
+        }
+        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+        s[0] = ex2_approx(s[0] - b0);
+        s[1] = ex2_approx(s[1] - b1);
+        s[2] = ex2_approx(s[2] - b0);
+        s[3] = ex2_approx(s[3] - b1);
+        l[0] += s[0] + s[2];
+        l[1] += s[1] + s[3];
+        const uint32_t p0 = transpose8(pack_bf16(s[0], s[1])), p1 = transpose8(pack_bf16(s[2], s[3]));
+#pragma unroll
+        for (int c = 0; c < VB; ++c) {
+            const uint32_t *r0 = reinterpret_cast<const uint32_t *>(&vr[0][c]), *r1 = reinterpret_cast<const uint32_t *>(&vr[1][c]);
+            const uint32_t *r2 = reinterpret_cast<const uint32_t *>(&vr[2][c]), *r3 = reinterpret_cast<const uint32_t *>(&vr[3][c]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t f[4] = {__byte_perm(r0[t], r1[t], 0x5410), __byte_perm(r0[t], r1[t], 0x7632),
+                                       __byte_perm(r2[t], r3[t], 0x5410), __byte_perm(r2[t], r3[t], 0x7632)};
+                mma16816(o[4 * c + t], f, p0, p1);
+            }
+        }
+        if (more) load_v(s0 + step);
+    }
+    // the warp's result, then the CTA's: the warps in order
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
+        if (g == 0) {
+            part[warp].m[2 * q + i] = m[i];
+            part[warp].l[2 * q + i] = l[i];
+        }
+#pragma unroll
+        for (int t = 0; t < VB * 4; ++t) {
+            const int col = 64 * (t >> 2) + 8 * g + 2 * (t & 3);
+            part[warp].o[2 * q + i][col] = o[t][i];
+            part[warp].o[2 * q + i][col + 1] = o[t][i + 2];
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < HG * DP; e += kThreads) {
+        const int h = e / DP, c = e % DP;
+        float mx = -INFINITY, lx = 0.f, ox = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, part[k].m[h]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const float f = ex2_approx(part[k].m[h] - base);
+            lx = fmaf(f, part[k].l[h], lx);
+            ox = fmaf(f, part[k].o[h][c], ox);
+        }
+        out.o[h][c] = ox;
+        if (c == 0) {
+            out.m[h] = mx;
+            out.l[h] = lx;
+        }
+    }
+    __syncthreads();
+    join<bf, DP>(a, out, w.b, w.h0, w.heads);
+}
+
+// One cluster of a.split CTAs per (sequence, key/value head, group of HG heads).
+template <typename K>
+cudaError_t launch_clusters(K fn, const StepArgs &a, size_t bytes, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (bytes > 0) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && a.split > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -244,9 +442,10 @@ cudaError_t launch(const StepArgs &a, cudaStream_t st) {
 template <typename T>
 cudaError_t by_width(const StepArgs &a, cudaStream_t st) {
     const int w = a.d > a.dv ? a.d : a.dv;
-    if (w <= 32) return launch<T, 32>(a, st);
-    if (w <= 64) return launch<T, 64>(a, st);
-    return launch<T, 128>(a, st);
+    const auto bytes = [](int dp) { return (size_t)(2 * TS * (dp + 4) + HG * dp + 4 * HG * TS + TS * HG) * 4; };
+    if (w <= 32) return launch_clusters(step_kernel<T, 32>, a, bytes(32), st);
+    if (w <= 64) return launch_clusters(step_kernel<T, 64>, a, bytes(64), st);
+    return launch_clusters(step_kernel<T, 128>, a, bytes(128), st);
 }
 
 }  // namespace
@@ -260,9 +459,11 @@ cudaError_t step(const StepArgs &in, hla_dtype dt, cudaStream_t st) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const long long pairs = (long long)a.B * a.Hkv * ((a.G + HG - 1) / HG);
-    const long long tiles = ((long long)a.sinks + a.window + TS - 1) / TS;
+    const int unit = a.wide ? kWarps * GS : TS;  // slots a CTA takes at a time
+    const long long tiles = ((long long)a.sinks + a.window + unit - 1) / unit;
     a.split = 1;
     while (a.split < 16 && pairs * a.split < 2LL * sms && a.split * 2 <= tiles) a.split *= 2;
+    if (a.wide) return a.d <= 64 && a.dv <= 64 ? launch_clusters(step_mma_kernel<64>, a, 0, st) : launch_clusters(step_mma_kernel<128>, a, 0, st);
     return dt == HLA_F32 ? by_width<float>(a, st) : by_width<__nv_bfloat16>(a, st);
 }
 

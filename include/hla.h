@@ -486,7 +486,7 @@ typedef struct {
 /* Bytes of device workspace hla_gated_forward and hla_gated_backward need (0 for invalid
  * parameters and n = 0).  Set to zero before its first use; every call leaves it ready for
  * the next one, of either direction and any sizes it is large enough for.  Calls sharing
- * one workspace must not overlap in time, and no other entry point may use it.  Up to 128
+ * one workspace must not overlap in time, and no other entry point may use it.  Up to 64
  * tokens the forward, and the backward without d_rate, take NULL as well. */
 HLA_API size_t hla_gated_workspace_size(const hla_gated_params *p);
 
