@@ -116,7 +116,11 @@ cudaError_t simt_bwd(const Args &a, cudaStream_t st) {
     dq_kernel<T, DP><<<(unsigned)((size_t)a.B * a.H * ((a.n + TQ - 1) / TQ)), kThreads, dq_bytes, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     dkv_kernel<T, DP><<<dim3((unsigned)((size_t)a.B * a.Hkv * ((a.nk + TK - 1) / TK)), a.far + 1), kThreads, dkv_bytes, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.far == 0) return e;
+    return cudaGetLastError();
+}
+// Adds the shares of the key tiles with first tokens.
+template <typename T>
+cudaError_t join_shares(const Args &a, cudaStream_t st) {
     const size_t el = (size_t)a.B * a.Hkv * a.far_keys * (a.d + a.dv);
     join_kernel<T><<<(unsigned)((el + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
     return cudaGetLastError();
@@ -153,10 +157,13 @@ __global__ void __launch_bounds__(128) fill_kernel(const Args a, View kc, View v
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t delta_bytes(const hla_window_params *p) { return align256((size_t)p->B * p->H * p->n * 4); }
-size_t backward_bytes(const hla_window_params *p) {
-    const size_t far = far_shares(p, TK);
-    return delta_bytes(p) +
-           (far ? (far + 1) * p->B * p->Hkv * (size_t)far_keys(p, TK) * (p->d + p->dv) * 4 : 0);
+size_t part_bytes(const hla_window_params *p, int tile) {
+    const size_t far = far_shares(p, tile);
+    return far ? (far + 1) * p->B * p->Hkv * (size_t)far_keys(p, tile) * (p->d + p->dv) * 4 : 0;
+}
+size_t backward_bytes(const hla_window_params *p) {  // for either path: the alignment decides between them
+    const size_t s = part_bytes(p, TK), t = p->in_dtype == HLA_BF16 ? part_bytes(p, kTcTile) : 0;
+    return delta_bytes(p) + (s > t ? s : t);
 }
 bool wide_rows(const hla_tensor *t) {
     return (reinterpret_cast<uintptr_t>(t->p) & 15u) == 0 && t->sb % 8 == 0 && t->sh % 8 == 0 && t->st % 8 == 0;
@@ -235,10 +242,21 @@ hla_status hla_window_backward(const hla_window_params *p, const hla_tensor *q, 
     a.lse = const_cast<float *>(lse);
     a.delta = static_cast<float *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + delta_bytes(p));
-    a.far = far_shares(p, TK);
-    a.far_keys = a.far ? far_keys(p, TK) : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == HLA_F32 ? simt<float>(a, true, st) : simt<__nv_bfloat16>(a, true, st);
+    cudaError_t e = dev_status_ptr(&a.err);
+    if (e != cudaSuccess) return report(HLA_ERR_CUDA, cudaGetErrorString(e));
+    e = cudaErrorNotSupported;
+    if (dt == HLA_BF16 && bwd_tc_takes(a)) {
+        a.far = far_shares(p, kTcTile);
+        a.far_keys = a.far ? far_keys(p, kTcTile) : 0;
+        e = bwd_tc(a, st);
+    }
+    if (e == cudaErrorNotSupported) {
+        a.far = far_shares(p, TK);
+        a.far_keys = a.far ? far_keys(p, TK) : 0;
+        e = dt == HLA_F32 ? simt<float>(a, true, st) : simt<__nv_bfloat16>(a, true, st);
+    }
+    if (e == cudaSuccess && a.far > 0) e = dt == HLA_F32 ? join_shares<float>(a, st) : join_shares<__nv_bfloat16>(a, st);
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 

@@ -66,6 +66,10 @@ cudaError_t step(const StepArgs &a, hla_dtype dt, cudaStream_t st);
 // nothing launched, when the driver cannot describe a tensor to the TMA unit
 bool fwd_tc_takes(const Args &a);
 cudaError_t fwd_tc(const Args &a, cudaStream_t st);
+// (with far shares the caller adds them up afterwards; kTcTile: the keys of one tile)
+constexpr int kTcTile = 128;
+bool bwd_tc_takes(const Args &a);
+cudaError_t bwd_tc(const Args &a, cudaStream_t st);
 
 }  // namespace win
 }  // namespace hla

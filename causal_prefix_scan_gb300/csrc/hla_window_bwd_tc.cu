@@ -1,0 +1,609 @@
+// hla_window_bwd_tc.cu -- backward of windowed attention for bf16 on the tensor cores.
+//
+// With P = exp(scale S - lse), S = Q K^T, dP = dO V^T, D = rowsum(dO o):
+//   dS = P (dP - D),   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO.
+// Two kernels, neither of which adds to memory that another CTA adds to, so every sum has a
+// fixed order: dq over tiles of 128 queries (walking the keys they see; also writes D) and dkv
+// over tiles of 128 keys (walking the queries that see them, all heads of the group).  S and
+// dP are formed in both: 7 products per pair of tiles instead of 5, in exchange for no
+// atomics and no fp32 buffer of dQ the size of Q.
+//
+// Roles (10 warps): 0-3 and 4-7 the elementwise part, one row per thread, columns [0,64) and
+// [64,128) of each tile; 8 MMA; 9 TMA.  The MMA order is chosen so that the tensor cores
+// always have the next product while the elementwise part works on the one before:
+//   dq:   S(j+1) | dQ(j) | dP(j+1)            dkv:  dV(j) | S(j+1) | dK(j) | dP(j+1)
+// P and dS are rounded to bf16 (half a step 2^-8 of each) and stay in TMEM over the columns
+// of S and dP that they were made from, as the first operand of the next product; sums are
+// fp32.  The scale is applied to the finished sums.
+#include "hla_window_tc.cuh"
+
+namespace hla {
+namespace win {
+namespace {
+
+using namespace tcw;
+
+constexpr int kThreads = 320, kWarpMma = 8, kWarpTma = 9;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+    Args a;
+    CUtensorMap mq, mk, mv, mg;
+};
+
+HLA_DEVICE void elem_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// A in TMEM as two blocks of 64 contraction rows (32 packed columns each) 64 columns apart.
+HLA_DEVICE void mma_ts(uint32_t d, uint32_t a, const uint8_t *b, uint32_t idesc, bool acc) {
+    mma_tm(d, a, b, idesc, 4, acc);
+    mma_tm(d, a + 64, b + 64 * 128, idesc, 4, true);
+}
+
+// Common set-up and end of both kernels.
+template <int NB>
+struct Cta {
+    uint8_t *base;
+    Waits ws;
+    uint32_t tb;
+    int warp;
+    HLA_DEVICE Cta(uint8_t *b, int off_bar, unsigned *err, int eight_a, int eight_b, int eight_c) : base(b) {
+        ws.bars = reinterpret_cast<uint64_t *>(b + off_bar);
+        uint32_t *misc = reinterpret_cast<uint32_t *>(b + off_bar + NB * 8);
+        ws.abort_p = reinterpret_cast<volatile int *>(misc + 1);
+        ws.err = err;
+        warp = threadIdx.x >> 5;
+        if (threadIdx.x == 0) {
+            misc[1] = 0u;
+            for (int i = 0; i < NB; ++i) mbar_init(ws.bar(i), i == eight_a || i == eight_b || i == eight_c ? 8 : 1);
+            fence_mbar_init();
+        }
+        if (warp == kWarpMma) {
+            tmem_alloc(misc, 512);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tb = misc[0];
+    }
+    HLA_DEVICE void finish() {
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == kWarpMma) tmem_dealloc(tb, 512);
+    }
+};
+
+// ------------------------------------------------------------ dq
+template <int DP>
+struct LayQ {
+    static constexpr int TILE = T * DP * 2;
+    static constexpr int NS = DP == 64 ? 8 : 4;  // ring slots, K and V tiles in turn
+    static constexpr int OFF_Q = 0, OFF_G = TILE, OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NS * TILE;
+    static constexpr int B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_SF = B_S + 1, B_DP = B_SF + 1,
+                         B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, NB = B_FIN + 1;
+    static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
+    static constexpr uint32_t S = 0, DPC = T, DQ = 2 * T;  // TMEM columns
+};
+
+template <int DP>
+__device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32_t tb, const KeyTiles &kt, int b, int h,
+                                        int i0, int rows) {
+    using L = LayQ<DP>;
+    const Args &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
+    const int r = i0 + (warp & 3) * 32 + lane, pos = a.p0 + r;
+    const bool live = r < rows;
+    const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t sa = tb + quad + L::S + half * 64, da = tb + quad + L::DPC + half * 64;
+    const size_t row = ((size_t)b * a.H + h) * a.n + r;
+    const float c = a.scale * kLog2e, base = live ? a.lse[row] * kLog2e : 0.f;
+    const float D = live ? a.delta[row] : 0.f;
+    bool ok = true;
+    uint32_t ph = 0;
+    for (int it = 0; it < kt.total; ++it, ph ^= 1u) {
+        const int j0 = kt[it] * T;
+        const bool masked = !(j0 + T - 1 <= a.p0 + i0 && (a.p0 + i0 + T - 1 - j0 < a.window || j0 + T <= a.sinks));
+        const int hi = pos - j0 + 1 - half * 64, sk = a.sinks - j0 - half * 64;
+        const int lo = (pos >= a.window ? pos - a.window + 1 - j0 : 0) - half * 64;
+        if (!(ok = ws.wait(L::B_S, ph))) break;
+        tc_fence_after();
+        float P[4][16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld16(sa + 16 * k, P[k]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_SF));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) P[k][e] = ex2_approx(fmaf(P[k][e], c, -base));
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (16 * k + e >= hi || (16 * k + e < lo && 16 * k + e >= sk)) P[k][e] = 0.f;
+            }
+        }
+        if (!(ok = ws.wait(L::B_DP, ph))) break;
+        tc_fence_after();
+        float v[2][16];
+        tmem_ld16(da, v[0]);
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            float pk[16];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                tmem_wait_ld();
+                if (k + g < 3) tmem_ld16(da + 16 * (k + g + 1), v[(g + 1) & 1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    // nothing where P is zero: behind the sequence dP may be anything
+                    const float x = P[k + g][e];
+                    v[g][e] = x == 0.f ? 0.f : x * (v[g][e] - D);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pk[8 * g + e] = __uint_as_float(pack_bf16(v[g][2 * e], v[g][2 * e + 1]));
+            }
+            tmem_st16(da + 8 * k, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_DS));
+    }
+    if (!ok || !ws.wait(L::B_O, 0u)) return;
+    tc_fence_after();
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.dq.p) + (size_t)b * a.dq.sb + (size_t)h * a.dq.sh + (size_t)r * a.dq.st;
+    const int dpad = (a.d + 15) & ~15;
+    for (int k = half * 16; k < dpad; k += 32) {
+        float x[16];
+        tmem_ld16(tb + quad + L::DQ + k, x);
+        tmem_wait_ld();
+        uint4 u[2];
+        uint32_t *w = reinterpret_cast<uint32_t *>(u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(x[2 * e] * a.scale, x[2 * e + 1] * a.scale);
+        if (live) {
+            *reinterpret_cast<uint4 *>(o + k) = u[0];
+            if (k + 8 < a.d) *reinterpret_cast<uint4 *>(o + k + 8) = u[1];
+        }
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const KeyTiles &kt,
+                                       int len) {
+    using L = LayQ<DP>;
+    const Args &a = p.a;
+    const int lane = threadIdx.x & 31, N = kt.total;
+    const uint32_t id_s = make_idesc(T, T, false, false), id_q = make_idesc(T, (a.d + 15) & ~15, false, true);
+    const int qk = (a.d + 15) / 16, gv = (a.dv + 15) / 16;
+    auto slot = [&](int idx) { return base + L::OFF_RING + (idx % L::NS) * L::TILE; };
+    auto full = [&](int idx) { return ws.wait(L::B_FULL + idx % L::NS, (uint32_t)(idx / L::NS) & 1u); };
+    auto free_slot = [&](int idx) { umma_commit_warp(ws.bar(L::B_EMPTY + idx % L::NS)); };
+    auto do_s = [&](int j) {
+        if (!full(2 * j)) return false;
+        // keys behind the sequence may be anything, and 0 times that is not 0 in dS K
+        if (len - kt[j] * T < T) zero_rows<DP>(slot(2 * j), len - kt[j] * T, lane);
+        mma_kk(tb + L::S, base + L::OFF_Q, slot(2 * j), id_s, qk, false);
+        umma_commit_warp(ws.bar(L::B_S));
+        return true;
+    };
+    auto do_dp = [&](int j) {
+        if (!full(2 * j + 1)) return false;
+        mma_kk(tb + L::DPC, base + L::OFF_G, slot(2 * j + 1), id_s, gv, false);
+        umma_commit_warp(ws.bar(L::B_DP));
+        free_slot(2 * j + 1);
+        return true;
+    };
+    bool ok = ws.wait(L::B_Q, 0u) && do_s(0) && do_dp(0);
+    for (int j = 0; j < N && ok; ++j) {
+        const uint32_t ph = (uint32_t)j & 1u;
+        if (j + 1 < N) {
+            ok = ws.wait(L::B_SF, ph);
+            tc_fence_after();
+            ok = ok && do_s(j + 1);
+        }
+        ok = ok && ws.wait(L::B_DS, ph);
+        if (!ok) break;
+        tc_fence_after();
+        mma_ts(tb + L::DQ, tb + L::DPC, slot(2 * j), id_q, j > 0);
+        free_slot(2 * j);
+        if (j + 1 < N) ok = do_dp(j + 1);
+    }
+    if (ok) umma_commit_warp(ws.bar(L::B_O));
+    umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
+    mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
+    __syncwarp();
+}
+
+template <int DP>
+__device__ __forceinline__ void dq_tma(const Params &p, const Waits &ws, uint8_t *base, const KeyTiles &kt, int b, int h,
+                                       int i0) {
+    using L = LayQ<DP>;
+    const Args &a = p.a;
+    const bool one = (threadIdx.x & 31) == 0;
+    const int hk = h / a.G;
+    if (one) {
+        mbar_expect_tx(ws.bar(L::B_Q), 2 * L::TILE);
+        load_tile<DP>(base + L::OFF_Q, &p.mq, a.q, ws.bar(L::B_Q), i0, h, b);
+        load_tile<DP>(base + L::OFF_G, &p.mg, a.go, ws.bar(L::B_Q), i0, h, b);
+    }
+    int idx = 0;
+    for (; idx < 2 * kt.total; ++idx) {
+        const int s = idx % L::NS, use = idx / L::NS;
+        if (use > 0 && !ws.wait(L::B_EMPTY + s, (uint32_t)(use - 1) & 1u)) break;
+        if (one) {
+            mbar_expect_tx(ws.bar(L::B_FULL + s), L::TILE);
+            const bool key = (idx & 1) == 0;
+            load_tile<DP>(base + L::OFF_RING + s * L::TILE, key ? &p.mk : &p.mv, key ? a.k : a.v, ws.bar(L::B_FULL + s),
+                          kt[idx >> 1] * T, hk, b);
+        }
+        __syncwarp();
+    }
+    // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
+    mbar_wait(ws.bar(L::B_Q), 0u, ws.err);
+    for (int k = max(0, idx - L::NS); k < idx; ++k)
+        mbar_wait(ws.bar(L::B_FULL + k % L::NS), (uint32_t)(k / L::NS) & 1u, ws.err);
+    __syncwarp();
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_constant__ Params p) {
+    using L = LayQ<DP>;
+    extern __shared__ __align__(1024) uint8_t base[];
+    const Args &a = p.a;
+    const int tiles = (a.n + T - 1) / T, u = blockIdx.x % (a.B * a.H), h = u % a.H, b = u / a.H;
+    const int i0 = (tiles - 1 - (int)(blockIdx.x / (a.B * a.H))) * T;  // long rows first
+    const int len = length_of(a, b), rows = min(a.n, len - a.p0);
+    if (i0 >= rows) return;
+    const KeyTiles kt(a, a.p0 + i0, a.p0 + min(i0 + T, rows) - 1, T);
+    Cta<L::NB> c(base, L::OFF_BAR, a.err, L::B_SF, L::B_DS, -1);
+    if (c.warp == kWarpTma) {
+        dq_tma<DP>(p, c.ws, base, kt, b, h, i0);
+    } else if (c.warp == kWarpMma) {
+        dq_mma<DP>(p, c.ws, base, c.tb, kt, len);
+    } else {
+        dq_elem<DP>(p, c.ws, c.tb, kt, b, h, i0, rows);
+    }
+    c.finish();
+}
+
+// ------------------------------------------------------------ dk, dv
+template <int DP>
+struct LayK {
+    static constexpr int TILE = T * DP * 2;
+    static constexpr int NS = DP == 64 ? 4 : 2;  // stages of one Q and one dO tile
+    static constexpr int OFF_K = 0, OFF_V = TILE, OFF_RING = 2 * TILE, OFF_ROW = OFF_RING + 2 * NS * TILE;
+    static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * T * 4;  // lse and D of the queries, two stages
+    static constexpr int B_K = 0, B_FQ = 1, B_FG = B_FQ + NS, B_EMPTY = B_FG + NS, B_S = B_EMPTY + NS, B_P = B_S + 1,
+                         B_DP = B_P + 1, B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, NB = B_FIN + 1;
+    static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
+    static constexpr uint32_t S = 0, DPC = T, DV = 2 * T, DK = 2 * T + DP;  // TMEM columns
+};
+
+// The (head, query tile) pairs of one key tile: query tiles [q_lo, q_lo + each) of every head.
+struct Walk {
+    int q_lo, each, total;
+    HLA_DEVICE int head(int i) const { return i / each; }
+    HLA_DEVICE int tile(int i) const { return q_lo + i % each; }
+};
+
+template <int DP>
+__device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8_t *smem, uint32_t tb, const Walk &w, int b,
+                                         int hk, int j0, int len, int rows, int share, bool split) {
+    using L = LayK<DP>;
+    const Args &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
+    const int j = j0 + (warp & 3) * 32 + lane;
+    const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t sa = tb + quad + L::S + half * 64, da = tb + quad + L::DPC + half * 64;
+    float *rowv = reinterpret_cast<float *>(smem + L::OFF_ROW);  // [2 stages][lse * log2e, D][128]
+    const float c = a.scale * kLog2e;
+    bool ok = true;
+    uint32_t ph = 0;
+    auto fetch = [&](int it) {  // threads 0-127 lse, 128-255 D
+        const int r = w.tile(it) * T + (tid & 127);
+        const size_t at = ((size_t)b * a.H + hk * a.G + w.head(it)) * a.n + r;
+        return r < rows ? (tid < 128 ? a.lse[at] * kLog2e : a.delta[at]) : 0.f;
+    };
+    float next = w.total > 0 ? fetch(0) : 0.f;
+    for (int it = 0; it < w.total; ++it, ph ^= 1u) {
+        float *cur = rowv + (it & 1) * 2 * T;
+        cur[tid] = next;
+        elem_sync();
+        if (it + 1 < w.total) next = fetch(it + 1);
+        const int i0 = w.tile(it) * T, p_lo = a.p0 + i0;
+        const bool masked = !(j0 + T - 1 <= p_lo && (p_lo + T - 1 - j0 < a.window || j0 + T <= a.sinks) && i0 + T <= rows);
+        // visible queries of key j: columns [lo, hi)
+        const int lo = j - p_lo - half * 64;
+        const int hi = (j < a.sinks ? rows - i0 : (int)min((long long)rows - i0, (long long)j - p_lo + a.window)) - half * 64;
+        // after an expired wait the loop goes on, so that the barrier above stays matched
+        if (!ok || !(ok = ws.wait(L::B_S, ph))) continue;
+        tc_fence_after();
+        float P[4][16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld16(sa + 16 * k, P[k]);
+        tmem_wait_ld();
+        const float *lse = cur + half * 64, *D = cur + T + half * 64;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(lse + 16 * k + e);
+                P[k][e] = ex2_approx(fmaf(P[k][e], c, -x.x));
+                P[k][e + 1] = ex2_approx(fmaf(P[k][e + 1], c, -x.y));
+                P[k][e + 2] = ex2_approx(fmaf(P[k][e + 2], c, -x.z));
+                P[k][e + 3] = ex2_approx(fmaf(P[k][e + 3], c, -x.w));
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (16 * k + e < lo || 16 * k + e >= hi) P[k][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            float pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                pk[e] = __uint_as_float(pack_bf16(P[k + (e >> 3)][2 * (e & 7)], P[k + (e >> 3)][2 * (e & 7) + 1]));
+            tmem_st16(sa + 8 * k, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_P));
+        if (!(ok = ws.wait(L::B_DP, ph))) continue;
+        tc_fence_after();
+        float v[2][16];
+        tmem_ld16(da, v[0]);
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            float pk[16];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                tmem_wait_ld();
+                if (k + g < 3) tmem_ld16(da + 16 * (k + g + 1), v[(g + 1) & 1]);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(D + 16 * (k + g) + e);
+                    const float dd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const float y = P[k + g][e + f];
+                        v[g][e + f] = y == 0.f ? 0.f : y * (v[g][e + f] - dd[f]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pk[8 * g + e] = __uint_as_float(pack_bf16(v[g][2 * e], v[g][2 * e + 1]));
+            }
+            tmem_st16(da + 8 * k, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_DS));
+    }
+    if (!ok) return;
+    if (w.total > 0) {
+        if (!ws.wait(L::B_O, 0u)) return;
+        tc_fence_after();
+    }
+    // threads 0-127 dv, 128-255 dk of one key each
+    const bool key = half == 1;
+    const int width = key ? a.d : a.dv;
+    const float f = key ? a.scale : 1.f;
+    const View &out = key ? a.dk : a.dv_;
+    const bool live = j < len;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out.p) + (size_t)b * out.sb + (size_t)hk * out.sh + (size_t)j * out.st;
+    float *part = a.part + (((size_t)share * a.B * a.Hkv + (size_t)b * a.Hkv + hk) * a.far_keys + j) * (a.d + a.dv) + (key ? 0 : a.d);
+    for (int k = 0; k < ((width + 15) & ~15); k += 16) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        if (w.total > 0) {
+            tmem_ld16(tb + quad + (key ? L::DK : L::DV) + k, x);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= f;
+        if (!live) continue;
+        if (split) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                if (k + e < width) *reinterpret_cast<float4 *>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else {
+            uint4 u[2];
+            uint32_t *y = reinterpret_cast<uint32_t *>(u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+            *reinterpret_cast<uint4 *>(o + k) = u[0];
+            if (k + 8 < width) *reinterpret_cast<uint4 *>(o + k + 8) = u[1];
+        }
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Walk &w, int rows) {
+    using L = LayK<DP>;
+    const Args &a = p.a;
+    const int lane = threadIdx.x & 31, N = w.total;
+    const uint32_t id_s = make_idesc(T, T, false, false);
+    const uint32_t id_v = make_idesc(T, (a.dv + 15) & ~15, false, true), id_k = make_idesc(T, (a.d + 15) & ~15, false, true);
+    const int qk = (a.d + 15) / 16, gv = (a.dv + 15) / 16;
+    auto tq = [&](int i) { return base + L::OFF_RING + (i % L::NS) * 2 * L::TILE; };
+    auto tg = [&](int i) { return tq(i) + L::TILE; };
+    auto par = [&](int i) { return (uint32_t)(i / L::NS) & 1u; };
+    // queries behind the sequence may be anything, and 0 times that is not 0 in dS^T Q, P^T dO
+    auto live = [&](int i) { return rows - w.tile(i) * T; };
+    auto do_s = [&](int i) {
+        if (!ws.wait(L::B_FQ + i % L::NS, par(i))) return false;
+        if (live(i) < T) zero_rows<DP>(tq(i), live(i), lane);
+        mma_kk(tb + L::S, base + L::OFF_K, tq(i), id_s, qk, false);
+        umma_commit_warp(ws.bar(L::B_S));
+        return true;
+    };
+    auto do_dp = [&](int i) {
+        if (!ws.wait(L::B_FG + i % L::NS, par(i))) return false;
+        if (live(i) < T) zero_rows<DP>(tg(i), live(i), lane);
+        mma_kk(tb + L::DPC, base + L::OFF_V, tg(i), id_s, gv, false);
+        umma_commit_warp(ws.bar(L::B_DP));
+        return true;
+    };
+    bool ok = N == 0 || (ws.wait(L::B_K, 0u) && do_s(0) && do_dp(0));
+    for (int i = 0; i < N && ok; ++i) {
+        const uint32_t ph = (uint32_t)i & 1u;
+        if (!(ok = ws.wait(L::B_P, ph))) break;
+        tc_fence_after();
+        mma_ts(tb + L::DV, tb + L::S, tg(i), id_v, i > 0);
+        if (i + 1 < N && !(ok = do_s(i + 1))) break;
+        if (!(ok = ws.wait(L::B_DS, ph))) break;
+        tc_fence_after();
+        mma_ts(tb + L::DK, tb + L::DPC, tq(i), id_k, i > 0);
+        umma_commit_warp(ws.bar(L::B_EMPTY + i % L::NS));
+        if (i + 1 < N) ok = do_dp(i + 1);
+    }
+    if (ok) umma_commit_warp(ws.bar(L::B_O));
+    umma_commit_warp(ws.bar(L::B_FIN));
+    mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
+    __syncwarp();
+}
+
+template <int DP>
+__device__ __forceinline__ void dkv_tma(const Params &p, const Waits &ws, uint8_t *base, const Walk &w, int b, int hk, int j0) {
+    using L = LayK<DP>;
+    const Args &a = p.a;
+    const bool one = (threadIdx.x & 31) == 0;
+    if (w.total == 0) return;
+    if (one) {
+        mbar_expect_tx(ws.bar(L::B_K), 2 * L::TILE);
+        load_tile<DP>(base + L::OFF_K, &p.mk, a.k, ws.bar(L::B_K), j0, hk, b);
+        load_tile<DP>(base + L::OFF_V, &p.mv, a.v, ws.bar(L::B_K), j0, hk, b);
+    }
+    int i = 0;
+    for (; i < w.total; ++i) {
+        const int s = i % L::NS, use = i / L::NS, h = hk * a.G + w.head(i), i0 = w.tile(i) * T;
+        if (use > 0 && !ws.wait(L::B_EMPTY + s, (uint32_t)(use - 1) & 1u)) break;
+        if (one) {
+            uint8_t *d = base + L::OFF_RING + s * 2 * L::TILE;
+            mbar_expect_tx(ws.bar(L::B_FQ + s), L::TILE);
+            load_tile<DP>(d, &p.mq, a.q, ws.bar(L::B_FQ + s), i0, h, b);
+            mbar_expect_tx(ws.bar(L::B_FG + s), L::TILE);
+            load_tile<DP>(d + L::TILE, &p.mg, a.go, ws.bar(L::B_FG + s), i0, h, b);
+        }
+        __syncwarp();
+    }
+    mbar_wait(ws.bar(L::B_K), 0u, ws.err);
+    for (int k = max(0, i - L::NS); k < i; ++k) {
+        mbar_wait(ws.bar(L::B_FQ + k % L::NS), (uint32_t)(k / L::NS) & 1u, ws.err);
+        mbar_wait(ws.bar(L::B_FG + k % L::NS), (uint32_t)(k / L::NS) & 1u, ws.err);
+    }
+    __syncwarp();
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_constant__ Params p) {
+    using L = LayK<DP>;
+    extern __shared__ __align__(1024) uint8_t base[];
+    const Args &a = p.a;
+    const int share = blockIdx.y, pairs = a.B * a.Hkv, bk = blockIdx.x % pairs, hk = bk % a.Hkv, b = bk / a.Hkv;
+    const int j0 = (int)(blockIdx.x / pairs) * T;
+    const int len = length_of(a, b), rows = max(min(a.n, len - a.p0), 0);
+    const bool first = j0 < a.far_keys;  // holds first tokens whose sums are split
+    if ((share > 0 && !first) || j0 >= len) return;
+    // query tiles of the window, then the far ones (see the CUDA-core kernel)
+    const int r_lo = max(0, j0 - a.p0), r_win = (int)max(0LL, min((long long)rows, (long long)j0 + T - 1 + a.window - a.p0));
+    const int q_mid = max((r_win + T - 1) / T, r_lo / T);
+    int q_lo = r_lo / T, q_hi = q_mid;
+    const int end = (rows + T - 1) / T;
+    if (share > 0) {
+        const int all = max(end - q_mid, 0), each = (all + a.far - 1) / a.far;
+        q_lo = min(q_mid + (share - 1) * each, end);
+        q_hi = min(q_lo + each, end);
+    }
+    q_hi = min(q_hi, end);
+    Walk w;
+    w.q_lo = q_lo;
+    w.each = max(q_hi - q_lo, 0);
+    w.total = w.each * a.G;
+    Cta<L::NB> c(base, L::OFF_BAR, a.err, L::B_P, L::B_DS, -1);
+    if (c.warp == kWarpTma) {
+        dkv_tma<DP>(p, c.ws, base, w, b, hk, j0);
+    } else if (c.warp == kWarpMma) {
+        dkv_mma<DP>(p, c.ws, base, c.tb, w, rows);
+    } else {
+        dkv_elem<DP>(p, c.ws, base, c.tb, w, b, hk, j0, len, rows, share, first && a.far > 0);
+    }
+    c.finish();
+}
+
+// D = rowsum(do o): 16 lanes per row, 8 columns per lane.
+__global__ void __launch_bounds__(256) window_delta_kernel(const Args a) {
+    const size_t row = (size_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int c = (threadIdx.x & 15) * 8;
+    if (row >= (size_t)a.B * a.H * a.n) return;  // a warp's two rows may differ: no full-warp shuffle below
+    const int i = (int)(row % a.n), h = (int)(row / a.n % a.H), b = (int)(row / a.n / a.H);
+    const bool live = a.p0 + i < length_of(a, b);
+    float s = 0.f;
+    if (live && c < a.dv) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o.p) + (size_t)b * a.o.sb +
+                                                         (size_t)h * a.o.sh + (size_t)i * a.o.st + c);
+        const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.go.p) + (size_t)b * a.go.sb +
+                                                         (size_t)h * a.go.sh + (size_t)i * a.go.st + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+            s = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), s);
+        }
+    }
+    const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) s += __shfl_xor_sync(mask, s, k);
+    if (live && c == 0) a.delta[row] = s;
+}
+
+template <int DP>
+cudaError_t launch(Params &p, cudaStream_t st) {
+    using Q = LayQ<DP>;
+    using K = LayK<DP>;
+    static_assert(Q::SMEM <= 227 * 1024 && K::SMEM <= 227 * 1024, "shared memory");
+    const Args &a = p.a;
+    if (!encode(&p.mq, a.q, a.d, a.n, a.H, a.B, T) || !encode(&p.mk, a.k, a.d, a.nk, a.Hkv, a.B, T) ||
+        !encode(&p.mv, a.v, a.dv, a.nk, a.Hkv, a.B, T) || !encode(&p.mg, a.go, a.dv, a.n, a.H, a.B, T))
+        return cudaErrorNotSupported;
+    cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(window_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+    if (e != cudaSuccess) return e;
+    const size_t rows = (size_t)a.B * a.H * a.n;
+    window_delta_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    window_dq_kernel<DP><<<(unsigned)((size_t)a.B * a.H * ((a.n + T - 1) / T)), kThreads, Q::SMEM, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    window_dkv_kernel<DP><<<dim3((unsigned)((size_t)a.B * a.Hkv * ((a.nk + T - 1) / T)), a.far + 1), kThreads, K::SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+
+bool rows16(const View &v) {
+    return (reinterpret_cast<uintptr_t>(v.p) & 15u) == 0 && v.sb % 8 == 0 && v.sh % 8 == 0 && v.st % 8 == 0;
+}
+
+}  // namespace
+
+bool bwd_tc_takes(const Args &a) {
+    return a.d % 8 == 0 && a.dv % 8 == 0 && mappable(a.q) && mappable(a.k) && mappable(a.v) && mappable(a.go) && rows16(a.o) &&
+           rows16(a.dq) && rows16(a.dk) && rows16(a.dv_);
+}
+
+cudaError_t bwd_tc(const Args &a, cudaStream_t st) {
+    Params p;
+    memset(&p, 0, sizeof p);
+    p.a = a;
+    return a.d <= 64 && a.dv <= 64 ? launch<64>(p, st) : launch<128>(p, st);
+}
+
+}  // namespace win
+}  // namespace hla
