@@ -20,9 +20,10 @@
 // same fmaf, so a state has the same bits wherever the look-back found its start: results
 // do not depend on timing.  Reading the inputs a second time instead (maps, scan, states)
 // would move 5/3 of the forward's bytes.
-#include "hla_internal.h"
+#include "hla_gated.cuh"
 
 namespace hla {
+namespace gated {
 namespace {
 
 constexpr int WARPS = 8;
@@ -37,241 +38,13 @@ constexpr int kTileT = WARPS * kTS<T, DIR>;  // tokens of one tile
 constexpr int kTileLeast = WARPS * 8;
 constexpr int BACK = 8;               // windows of WARPS earlier tiles kept by one look-back
 
-// Published map or state of one channel of one tile, 16 bytes, read and written whole.
-// `tag` is 4 * (number of the call) + kind; anything else is left over from another call.
-struct __align__(16) Record {
-    float a, b;
-    unsigned long long tag;
-};
+// `tag` of a record: 4 * (number of the call) + kind; anything else is left over from
+// another call.
 enum : unsigned long long { REC_MAP = 1, REC_STATE = 2 };
 
 // Workspace: header, then one record per channel slot of every tile, then (backward with
 // HLA_GATE_RATE) one partial sum per channel slot of every tile, in records with tag 0.
-// Header word 0 counts tickets over all calls, word 1 is the count at which this call
-// began: both only grow, so no call number ever returns.
-struct Header {
-    unsigned long long tickets, base;
-};
 constexpr size_t kHeaderBytes = 256;
-
-struct Tensor {
-    const void *p;
-    long long sb, st;
-};
-
-struct Args {
-    int B, n, d, tiles, slices;
-    const float *rate;
-    const int *lengths;
-    Tensor x, g, y, dy, o1, o2;   // o1: y or dx, o2: dg
-    const float *state_in;        // [B][d]: before the first token (NULL: zeros)
-    const float *d_state_out;     // [B][d]: gradient of the state after the last (NULL: zeros)
-    float *out_state;             // state after the last token, or d_state_in (NULL: skip)
-    Header *hdr;
-    Record *rec, *part;           // part: NULL when the rates' gradient is not wanted
-    unsigned *err;
-};
-
-// ------------------------------------------------------------ element access
-// VEC adjacent channels of one token as they lie in memory.
-template <typename T, int VEC>
-struct Raw;
-template <>
-struct Raw<float, 1> { using type = float; };
-template <>
-struct Raw<float, 2> { using type = float2; };
-template <>
-struct Raw<__nv_bfloat16, 1> { using type = unsigned short; };
-template <>
-struct Raw<__nv_bfloat16, 2> { using type = unsigned; };
-template <typename T, int VEC>
-using raw_t = typename Raw<T, VEC>::type;
-
-// (arrays of VEC floats: the members of Vf below)
-__device__ __forceinline__ void unpack(float r, float (&v)[1]) { v[0] = r; }
-__device__ __forceinline__ void unpack(float2 r, float (&v)[2]) { v[0] = r.x; v[1] = r.y; }
-__device__ __forceinline__ void unpack(unsigned short r, float (&v)[1]) { v[0] = __uint_as_float((unsigned)r << 16); }
-__device__ __forceinline__ void unpack(unsigned r, float (&v)[2]) {
-    v[0] = __uint_as_float(r << 16);
-    v[1] = __uint_as_float(r & 0xFFFF0000u);
-}
-__device__ __forceinline__ void pack(const float (&v)[1], float &r) { r = v[0]; }
-__device__ __forceinline__ void pack(const float (&v)[2], float2 &r) { r = make_float2(v[0], v[1]); }
-__device__ __forceinline__ void pack(const float (&v)[1], unsigned short &r) {
-    r = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-}
-__device__ __forceinline__ void pack(const float (&v)[2], unsigned &r) { r = pack_bf16(v[0], v[1]); }
-
-template <typename T, int VEC>
-__device__ __forceinline__ raw_t<T, VEC> load(const Tensor &t, size_t off) {
-    return __ldg(reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(t.p) + off));
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store(const Tensor &t, size_t off, const float (&v)[VEC]) {
-    raw_t<T, VEC> r;
-    pack(v, r);
-    *reinterpret_cast<raw_t<T, VEC> *>(const_cast<T *>(static_cast<const T *>(t.p)) + off) = r;
-}
-
-// ------------------------------------------------------------ arithmetic on VEC channels
-// Pairs of fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
-// scalar ones): the gates' arithmetic, not memory, bounds a kernel that issues them singly.
-template <int VEC>
-struct Vf {
-    float v[VEC];
-};
-HLA_DEVICE unsigned long long pair(const Vf<2> &x) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.v[0]), "f"(x.v[1]));
-    return r;
-}
-HLA_DEVICE Vf<2> unpair(unsigned long long r) {
-    Vf<2> x;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.v[0]), "=f"(x.v[1]) : "l"(r));
-    return x;
-}
-template <int VEC>
-HLA_DEVICE Vf<VEC> splat(float c) {
-    Vf<VEC> r;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = c;
-    return r;
-}
-HLA_DEVICE Vf<1> fma_(Vf<1> a, Vf<1> b, Vf<1> c) { return {fmaf(a.v[0], b.v[0], c.v[0])}; }
-HLA_DEVICE Vf<1> mul_(Vf<1> a, Vf<1> b) { return {a.v[0] * b.v[0]}; }
-HLA_DEVICE Vf<1> add_(Vf<1> a, Vf<1> b) { return {a.v[0] + b.v[0]}; }
-HLA_DEVICE Vf<2> fma_(const Vf<2> &a, const Vf<2> &b, const Vf<2> &c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
-    return unpair(r);
-}
-HLA_DEVICE Vf<2> mul_(const Vf<2> &a, const Vf<2> &b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
-    return unpair(r);
-}
-HLA_DEVICE Vf<2> add_(const Vf<2> &a, const Vf<2> &b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
-    return unpair(r);
-}
-template <int VEC>
-HLA_DEVICE Vf<VEC> sub_(const Vf<VEC> &a, const Vf<VEC> &b) {  // a - b
-    return fma_(b, splat<VEC>(-1.f), a);
-}
-template <int VEC, class F>
-HLA_DEVICE Vf<VEC> each(const Vf<VEC> &a, F f) {
-    Vf<VEC> r;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = f(a.v[i]);
-    return r;
-}
-HLA_DEVICE float rsqrt_approx(float x) {
-    float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-HLA_DEVICE float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// ------------------------------------------------------------ gates
-constexpr float kLog2e = 1.4426950408889634f;
-
-// sigma(z) and 1 - sigma(z), both with a relative error of a few units in the last place:
-// the smaller is e / (1 + e), e = exp(-|z|) <= 1, and the larger is one minus it, so that a
-// gate near one, whose error a long product of gates multiplies, is off by its rounding only.
-template <int VEC>
-HLA_DEVICE void sigmoid2(const Vf<VEC> &z, Vf<VEC> &s, Vf<VEC> &c) {
-    const Vf<VEC> e = each(z, [](float x) { return ex2_approx(fabsf(x) * -kLog2e); });
-    const Vf<VEC> r = each(add_(e, splat<VEC>(1.f)), rcp_approx);
-    const Vf<VEC> lo = mul_(e, r), hi = sub_(splat<VEC>(1.f), lo);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const bool up = z.v[i] > 0.f;
-        s.v[i] = up ? hi.v[i] : lo.v[i];
-        c.v[i] = up ? lo.v[i] : hi.v[i];
-    }
-}
-// sigma(z) alone, a few units in the last place off: far below zero the exponential is
-// infinite and the quotient zero.
-template <int VEC>
-HLA_DEVICE Vf<VEC> sigmoid(const Vf<VEC> &z) {
-    const Vf<VEC> e = each(mul_(z, splat<VEC>(-kLog2e)), ex2_approx);
-    return each(add_(e, splat<VEC>(1.f)), rcp_approx);
-}
-// 1 - exp(-u) for u >= 0.  Below 1/16 the difference would cancel: Taylor's series to u^5,
-// whose next term is under 2^-29 of the sum there.
-template <int VEC>
-HLA_DEVICE Vf<VEC> one_minus_exp(const Vf<VEC> &u) {
-    const Vf<VEC> e = each(mul_(u, splat<VEC>(-kLog2e)), ex2_approx);
-    const Vf<VEC> far = sub_(splat<VEC>(1.f), e);
-    Vf<VEC> p = fma_(u, splat<VEC>(1.f / 120.f), splat<VEC>(-1.f / 24.f));
-    p = fma_(p, u, splat<VEC>(1.f / 6.f));
-    p = fma_(p, u, splat<VEC>(-0.5f));
-    p = fma_(p, u, splat<VEC>(1.f));
-    p = mul_(p, u);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p.v[i] = u.v[i] < 0.0625f ? p.v[i] : far.v[i];
-    return p;
-}
-// 1 / sqrt(q) for q >= 0, finite at 0
-template <int VEC>
-HLA_DEVICE Vf<VEC> rsqrt0(const Vf<VEC> &q) {
-    return each(q, [](float x) { return rsqrt_approx(fmaxf(x, 1.2e-38f)); });
-}
-
-// a_t and b_t
-template <int GATE, int VEC>
-HLA_DEVICE void gate_fwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, Vf<VEC> &a, Vf<VEC> &b) {
-    if constexpr (GATE == HLA_GATE_GIVEN) {
-        a = g;
-        b = x;
-    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        Vf<VEC> c;
-        sigmoid2(g, a, c);
-        b = mul_(c, x);
-    } else {
-        const Vf<VEC> w = one_minus_exp(mul_(r, sigmoid(g)));  // 1 - a
-        a = sub_(splat<VEC>(1.f), w);
-        const Vf<VEC> q = fma_(w, a, w);  // 1 - a^2
-        b = mul_(mul_(q, rsqrt0(q)), x);
-    }
-}
-// a_t alone, the same bits as gate_fwd's
-template <int GATE, int VEC>
-HLA_DEVICE Vf<VEC> gate_a(const Vf<VEC> &g, const Vf<VEC> &r) {
-    Vf<VEC> a, b;
-    gate_fwd<GATE>(g, r, splat<VEC>(0.f), a, b);
-    return a;
-}
-// Gradients with respect to x, g and (HLA_GATE_RATE) the rate, from gh = dL/dh_t, x_t,
-// y = h_{t-1} and a_t.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f, da/du = -a.
-// f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
-template <int GATE, int VEC>
-HLA_DEVICE void gate_bwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, const Vf<VEC> &y, const Vf<VEC> &gh,
-                         const Vf<VEC> &a, Vf<VEC> &dx, Vf<VEC> &dg, Vf<VEC> &dr) {
-    if constexpr (GATE == HLA_GATE_GIVEN) {
-        dx = gh;
-        dg = mul_(gh, y);
-    } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        Vf<VEC> s, c;
-        sigmoid2(g, s, c);
-        dx = mul_(gh, c);
-        dg = mul_(mul_(dx, s), sub_(y, x));
-    } else {
-        Vf<VEC> s, c;
-        sigmoid2(g, s, c);
-        const Vf<VEC> u = mul_(r, s), w = one_minus_exp(u), q = fma_(w, a, w);
-        const Vf<VEC> rf = rsqrt0(q);
-        dx = mul_(gh, mul_(q, rf));
-        const Vf<VEC> du = mul_(mul_(gh, a), sub_(mul_(mul_(x, a), rf), y));
-        dg = mul_(du, mul_(u, c));
-        dr = mul_(du, s);
-    }
-}
 
 // ------------------------------------------------------------ look-back
 __device__ __forceinline__ void publish(Record *p, float a, float b, unsigned long long tag) {
@@ -410,23 +183,7 @@ __device__ __forceinline__ void take_place(Shared<VEC> &sh, const Args &a) {
     __syncthreads();
 }
 
-__device__ __forceinline__ int length_of(const Args &a, int b) {
-    if (!a.lengths) return a.n;
-    const int L = a.lengths[b];
-    return L < 0 ? 0 : L > a.n ? a.n : L;
-}
-
 // ------------------------------------------------------------ forward
-template <int GATE, int VEC>
-HLA_DEVICE Vf<VEC> rate_of(const Args &a, int ch) {
-    Vf<VEC> r = splat<VEC>(0.f);
-    if constexpr (GATE == HLA_GATE_RATE) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-            if (ch + v < a.d) r.v[v] = a.rate[ch + v];
-    }
-    return r;
-}
 // The state before this warp's tokens: the tile's, taken through the maps of the warps before.
 template <int VEC>
 HLA_DEVICE Vf<VEC> before_warp(const Shared<VEC> &sh, int warp, int lane) {
@@ -774,9 +531,15 @@ hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, flo
     a.B = p->B; a.n = p->n; a.d = p->d;
     a.rate = p->rate;
     a.lengths = p->lengths;
+    int dev = 0, sms = 0;
     cudaError_t e = dev_status_ptr(&a.err);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) {
-        if (p->in_dtype == HLA_F32)
+        if (w != W_STEP && pairs && stream_takes(a, sms))
+            e = w == W_FWD ? stream_forward(a, p->in_dtype, p->gate, st)
+                           : stream_backward(a, p->in_dtype, p->gate, d_rate, st);
+        else if (p->in_dtype == HLA_F32)
             e = pairs ? by_gate<float, 2>(p->gate, w, a, d_rate, st) : by_gate<float, 1>(p->gate, w, a, d_rate, st);
         else
             e = pairs ? by_gate<__nv_bfloat16, 2>(p->gate, w, a, d_rate, st)
@@ -801,9 +564,11 @@ hla_status take_workspace(const hla_gated_params *p, void *ws, size_t bytes, boo
 bool even_state(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
+}  // namespace gated
 }  // namespace hla
 
 using namespace hla;
+using namespace hla::gated;
 
 extern "C" {
 

@@ -1,0 +1,314 @@
+// hla_gated_stream.cu -- gated recurrence where the channels of all sequences alone fill the
+// device: one CTA takes 16 channels of one sequence and walks its tokens from end to end with
+// the state on chip, so no CTA waits for another and nothing but the inputs and outputs
+// moves.  A tile is NW warps x 4 groups x TS tokens; lane = 8 (group) + pair of channels, so
+// a group's row is one 32-byte sector (bf16).  Per tile: gates and maps in registers, a scan of
+// the four groups by shuffles, of the warps through shared memory (one barrier), then the
+// outputs.  The next tile's inputs are loaded into the registers of the present one as they
+// become free, so memory works while the tile is computed.
+#include <type_traits>
+
+#include "hla_gated.cuh"
+
+namespace hla {
+namespace gated {
+namespace {
+
+constexpr int VEC = 2, GL = 8, GROUPS = 32 / GL, CW = GL * VEC, TS = 8;
+constexpr int kWarpsFwd = 12, kWarpsBwd = 8;
+
+template <int NW>
+struct Shared {
+    float4 map[2][NW][GL];  // the warps' maps (A, A', B, B'), two tiles in turn
+    float2 carry[2][GL];    // state before the tile
+};
+
+HLA_DEVICE Vf<2> shfl_up(const Vf<2> &x, int by) {
+    return {__shfl_up_sync(0xffffffffu, x.v[0], by), __shfl_up_sync(0xffffffffu, x.v[1], by)};
+}
+
+// From the map (A, B) of this thread's tokens to the state before them; the state after the
+// tile goes into sh.carry for the next one.  `k` counts tiles.
+template <int NW>
+HLA_DEVICE Vf<2> state_before(Shared<NW> &sh, int k, Vf<2> A, Vf<2> B) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / GL, c = lane % GL;
+#pragma unroll
+    for (int by = GL; by < 32; by <<= 1) {
+        const Vf<2> a = shfl_up(A, by), b = shfl_up(B, by);
+        if (lane >= by) {
+            B = fma_(A, b, B);
+            A = mul_(A, a);
+        }
+    }
+    if (grp == GROUPS - 1) sh.map[k & 1][warp][c] = make_float4(A.v[0], A.v[1], B.v[0], B.v[1]);
+    Vf<2> ea = shfl_up(A, GL), eb = shfl_up(B, GL);
+    if (grp == 0) {
+        ea = splat<2>(1.f);
+        eb = splat<2>(0.f);
+    }
+    __syncthreads();
+    const float2 c0 = sh.carry[k & 1][c];
+    Vf<2> h = {c0.x, c0.y};
+    for (int w = 0; w < warp; ++w) {
+        const float4 m = sh.map[k & 1][w][c];
+        h = fma_(Vf<2>{m.x, m.y}, h, Vf<2>{m.z, m.w});
+    }
+    if (warp == NW - 1 && grp == GROUPS - 1) {
+        const Vf<2> after = fma_(A, h, B);
+        sh.carry[(k + 1) & 1][c] = make_float2(after.v[0], after.v[1]);
+    }
+    return fma_(ea, h, eb);
+}
+
+HLA_DEVICE Vf<2> load_state(const float *p, size_t off, bool ok) {
+    Vf<2> s = splat<2>(0.f);
+    if (p && ok) s = {p[off], p[off + 1]};
+    return s;
+}
+
+// ------------------------------------------------------------ forward
+template <typename T, int GATE, int NW>
+__global__ void __launch_bounds__(NW * 32, 2) stream_fwd_kernel(const Args a) {
+    constexpr int TT = NW * GROUPS * TS;
+    __shared__ Shared<NW> sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / a.slices, ch = (int)(blockIdx.x % a.slices) * CW + lane % GL * VEC;
+    const bool mine = ch < a.d;
+    const int len = length_of(a, b);
+    const size_t so = (size_t)b * a.d + ch;
+    if (warp == NW - 1 && lane >= 32 - GL) {
+        const Vf<2> s = load_state(a.state_in, so, mine);
+        sh.carry[0][lane % GL] = make_float2(s.v[0], s.v[1]);
+    }
+    const int t0 = (warp * GROUPS + lane / GL) * TS;  // first token of this thread in a tile
+    const bool whole = (int)(blockIdx.x % a.slices) * CW + CW <= a.d;
+    const T *xp = static_cast<const T *>(a.x.p) + (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch;
+    const T *gp = static_cast<const T *>(a.g.p) + (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch;
+    T *yp = const_cast<T *>(static_cast<const T *>(a.o1.p)) + (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
+    using R = raw_t<T, VEC>;
+    auto ld = [](const T *p) { return __ldg(reinterpret_cast<const R *>(p)); };
+    R xr[TS] = {}, gr[TS] = {};
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+        if (mine && t0 + i < len) {
+            gr[i] = ld(gp + (size_t)i * a.g.st);
+            xr[i] = ld(xp + (size_t)i * a.x.st);
+        }
+    const Vf<2> r = rate_of<GATE, VEC>(a, ch);
+    int k = 0;
+    // FULL: this tile and the next have all their tokens and the slice all its channels
+    auto tile = [&](int base, auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        xp += (size_t)TT * a.x.st;
+        gp += (size_t)TT * a.g.st;
+        Vf<2> ea[TS], eb[TS], A = splat<2>(1.f), B = splat<2>(0.f);
+#pragma unroll
+        for (int i = 0; i < TS; ++i) {
+            Vf<2> x, g;
+            unpack(xr[i], x.v);
+            unpack(gr[i], g.v);
+            gate_fwd<GATE>(g, r, x, ea[i], eb[i]);
+            if (!FULL && base + t0 + i >= len) {
+                ea[i] = splat<2>(1.f);
+                eb[i] = splat<2>(0.f);
+            }
+            if (FULL || (mine && base + TT + t0 + i < len)) {
+                gr[i] = ld(gp + (size_t)i * a.g.st);
+                xr[i] = ld(xp + (size_t)i * a.x.st);
+            }
+            B = fma_(ea[i], B, eb[i]);
+            A = mul_(A, ea[i]);
+        }
+        Vf<2> h = state_before(sh, k++, A, B);
+#pragma unroll
+        for (int i = 0; i < TS; ++i) {
+            h = fma_(ea[i], h, eb[i]);
+            if (FULL || (mine && base + t0 + i < len)) {
+                R o;
+                pack(h.v, o);
+                *reinterpret_cast<R *>(yp + (size_t)i * a.o1.st) = o;
+            }
+        }
+        yp += (size_t)TT * a.o1.st;
+    };
+    int base = 0;
+    if (whole)
+        for (; base + 2 * TT <= len; base += TT) tile(base, std::true_type());
+    for (; base < len; base += TT) tile(base, std::false_type());
+    __syncthreads();
+    if (a.out_state && warp == 0 && lane < GL && mine) {
+        const float2 s = sh.carry[k & 1][lane];
+        a.out_state[so] = s.x;
+        a.out_state[so + 1] = s.y;
+    }
+}
+
+// ------------------------------------------------------------ backward
+template <typename T, int GATE, int NW>
+__global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
+    constexpr int TT = NW * GROUPS * TS;
+    __shared__ Shared<NW> sh;
+    __shared__ float2 red[NW][GL];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / a.slices, ch = (int)(blockIdx.x % a.slices) * CW + lane % GL * VEC;
+    const bool mine = ch < a.d;
+    const int len = length_of(a, b);
+    const size_t so = (size_t)b * a.d + ch;
+    if (warp == NW - 1 && lane >= 32 - GL) {
+        const Vf<2> s = load_state(a.d_state_out, so, mine);
+        sh.carry[0][lane % GL] = make_float2(s.v[0], s.v[1]);
+    }
+    // the first group takes a tile's last tokens: groups and warps follow the scan's direction
+    const int t0 = (NW * GROUPS - 1 - (warp * GROUPS + lane / GL)) * TS;
+    const bool whole = (int)(blockIdx.x % a.slices) * CW + CW <= a.d;
+    int base = len > 0 ? (len - 1) / TT * TT : 0;
+    const size_t first = (size_t)base + t0;
+    const T *gp = static_cast<const T *>(a.g.p) + (size_t)b * a.g.sb + first * a.g.st + ch;
+    const T *dp = static_cast<const T *>(a.dy.p) + (size_t)b * a.dy.sb + first * a.dy.st + ch;
+    const T *xp = static_cast<const T *>(a.x.p) + (size_t)b * a.x.sb + first * a.x.st + ch;
+    const T *yp = static_cast<const T *>(a.y.p) + (size_t)b * a.y.sb + first * a.y.st + ch;  // read one token earlier
+    T *op = const_cast<T *>(static_cast<const T *>(a.o1.p)) + (size_t)b * a.o1.sb + first * a.o1.st + ch;
+    T *qp = const_cast<T *>(static_cast<const T *>(a.o2.p)) + (size_t)b * a.o2.sb + first * a.o2.st + ch;
+    using R = raw_t<T, VEC>;
+    auto ld = [](const T *p) { return __ldg(reinterpret_cast<const R *>(p)); };
+    R gr[TS] = {}, dr[TS] = {}, yr[TS] = {}, xr[TS] = {};
+    auto fetch = [&](int i, int t) {  // token t = its tile's base + t0 + i
+        gr[i] = ld(gp + (size_t)i * a.g.st);
+        dr[i] = ld(dp + (size_t)i * a.dy.st);
+        if (i > 0 || t > 0) yr[i] = ld(yp + (size_t)i * a.y.st - a.y.st);
+        if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = ld(xp + (size_t)i * a.x.st);
+    };
+#pragma unroll
+    for (int i = TS - 1; i >= 0; --i)
+        if (mine && base + t0 + i < len) fetch(i, base + t0 + i);
+    const Vf<2> r = rate_of<GATE, VEC>(a, ch);
+    const Vf<2> h0 = load_state(a.state_in, so, mine && t0 == 0);
+    Vf<2> sum = splat<2>(0.f);
+    int k = 0;
+    // FULL: the tile has all its tokens (every earlier one has) and the slice all its channels
+    auto tile = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        Vf<2> ea[TS], A = splat<2>(1.f), B = splat<2>(0.f);
+#pragma unroll
+        for (int i = TS - 1; i >= 0; --i) {
+            Vf<2> g, dy;
+            unpack(gr[i], g.v);
+            unpack(dr[i], dy.v);
+            ea[i] = gate_a<GATE>(g, r);
+            if (!FULL && (!mine || base + t0 + i >= len)) {
+                ea[i] = splat<2>(1.f);
+                dy = splat<2>(0.f);
+            }
+            B = mul_(ea[i], add_(dy, B));
+            A = mul_(A, ea[i]);
+        }
+        Vf<2> c = state_before(sh, k++, A, B);
+        const bool more = base > 0;  // then the next tile is whole
+        gp -= (size_t)TT * a.g.st;
+        dp -= (size_t)TT * a.dy.st;
+        yp -= (size_t)TT * a.y.st;
+        if constexpr (GATE != HLA_GATE_GIVEN) xp -= (size_t)TT * a.x.st;
+#pragma unroll
+        for (int i = TS - 1; i >= 0; --i) {
+            Vf<2> g, dy, x = splat<2>(0.f), y, dx, dg, drv;
+            unpack(gr[i], g.v);
+            unpack(dr[i], dy.v);
+            unpack(yr[i], y.v);
+            if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
+            if (i == 0 && base + t0 == 0) y = h0;
+            if (more && (FULL || mine)) fetch(i, base - TT + t0 + i);
+            const Vf<2> gh = add_(dy, c);
+            gate_bwd<GATE>(g, r, x, y, gh, ea[i], dx, dg, drv);
+            if (FULL || (mine && base + t0 + i < len)) {
+                c = mul_(ea[i], gh);
+                if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
+                R o, q;
+                pack(dx.v, o);
+                pack(dg.v, q);
+                *reinterpret_cast<R *>(op + (size_t)i * a.o1.st) = o;
+                *reinterpret_cast<R *>(qp + (size_t)i * a.o2.st) = q;
+            }
+        }
+        op -= (size_t)TT * a.o1.st;
+        qp -= (size_t)TT * a.o2.st;
+    };
+    if (len > 0) {
+        if (!whole || base + TT > len) {
+            tile(std::false_type());
+            base -= TT;
+        }
+        if (whole)
+            for (; base >= 0; base -= TT) tile(std::true_type());
+        else
+            for (; base >= 0; base -= TT) tile(std::false_type());
+    }
+    __syncthreads();
+    if (a.out_state && warp == 0 && lane < GL && mine) {
+        const float2 s = sh.carry[k & 1][lane];
+        a.out_state[so] = s.x;
+        a.out_state[so + 1] = s.y;
+    }
+    if constexpr (GATE == HLA_GATE_RATE) {
+        if (a.part) {  // groups, then warps, in order
+#pragma unroll
+            for (int by = GL; by < 32; by <<= 1) {
+                sum.v[0] += __shfl_xor_sync(0xffffffffu, sum.v[0], by);
+                sum.v[1] += __shfl_xor_sync(0xffffffffu, sum.v[1], by);
+            }
+            if (lane < GL) red[warp][lane] = make_float2(sum.v[0], sum.v[1]);
+            __syncthreads();
+            if (warp == 0 && lane < GL && mine) {
+                float2 s = red[0][lane];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) {
+                    s.x += red[w][lane].x;
+                    s.y += red[w][lane].y;
+                }
+                *reinterpret_cast<float4 *>(a.part + so) = make_float4(s.x, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(a.part + so + 1) = make_float4(s.y, 0.f, 0.f, 0.f);
+            }
+        }
+    }
+}
+
+// d_rate[c] = the sequences' sums in order
+__global__ void __launch_bounds__(256) stream_rate_kernel(const Record *part, int B, int d, float *d_rate) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= d) return;
+    float s = 0.f;
+    for (int b = 0; b < B; ++b) s += part[(size_t)b * d + c].a;
+    d_rate[c] = s;
+}
+
+template <typename T, int GATE>
+cudaError_t launch(Args a, bool backward, cudaStream_t st) {
+    a.slices = (a.d + CW - 1) / CW;
+    const unsigned grid = (unsigned)((size_t)a.B * a.slices);
+    if (backward)
+        stream_bwd_kernel<T, GATE, kWarpsBwd><<<grid, kWarpsBwd * 32, 0, st>>>(a);
+    else
+        stream_fwd_kernel<T, GATE, kWarpsFwd><<<grid, kWarpsFwd * 32, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t by_gate(const Args &a, int gate, bool backward, cudaStream_t st) {
+    if (gate == HLA_GATE_GIVEN) return launch<T, HLA_GATE_GIVEN>(a, backward, st);
+    if (gate == HLA_GATE_SIGMOID) return launch<T, HLA_GATE_SIGMOID>(a, backward, st);
+    return launch<T, HLA_GATE_RATE>(a, backward, st);
+}
+
+}  // namespace
+
+bool stream_takes(const Args &a, int sms) { return (long long)a.B * ((a.d + CW - 1) / CW) >= sms; }
+cudaError_t stream_forward(const Args &a, hla_dtype t, int gate, cudaStream_t st) {
+    return t == HLA_F32 ? by_gate<float>(a, gate, false, st) : by_gate<__nv_bfloat16>(a, gate, false, st);
+}
+cudaError_t stream_backward(const Args &a, hla_dtype t, int gate, float *d_rate, cudaStream_t st) {
+    const cudaError_t e = t == HLA_F32 ? by_gate<float>(a, gate, true, st) : by_gate<__nv_bfloat16>(a, gate, true, st);
+    if (e != cudaSuccess || !d_rate) return e;
+    stream_rate_kernel<<<(a.d + 255) / 256, 256, 0, st>>>(a.part, a.B, a.d, d_rate);
+    return cudaGetLastError();
+}
+
+}  // namespace gated
+}  // namespace hla

@@ -99,6 +99,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
     const size_t row = ((size_t)b * a.H + h) * a.n + r;
     const float c = a.scale * kLog2e, base = live ? a.lse[row] * kLog2e : 0.f;
     const float D = live ? a.delta[row] : 0.f;
+    const unsigned long long c2 = pair2(c, c), b2 = pair2(-base, -base), d2 = pair2(-D, -D);
     bool ok = true;
     uint32_t ph = 0;
     for (int it = 0; it < kt.total; ++it, ph ^= 1u) {
@@ -108,44 +109,48 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
         const int lo = (pos >= a.window ? pos - a.window + 1 - j0 : 0) - half * 64;
         if (!(ok = ws.wait(L::B_S, ph))) break;
         tc_fence_after();
-        float P[4][16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld16(sa + 16 * k, P[k]);
+        float P[2][32];
+        tmem_ld32(sa, P[0]);
+        tmem_ld32(sa + 32, P[1]);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ws.bar(L::B_SF));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) P[k][e] = ex2_approx(fmaf(P[k][e], c, -base));
-            if (masked) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (16 * k + e >= hi || (16 * k + e < lo && 16 * k + e >= sk)) P[k][e] = 0.f;
+            for (int e = 0; e < 32; e += 2) {
+                float u, v;
+                unpair2(fma2(pair2(P[k][e], P[k][e + 1]), c2, b2), u, v);
+                P[k][e] = ex2_approx(u);
+                P[k][e + 1] = ex2_approx(v);
             }
+        if (masked) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k >= hi || (k < lo && k >= sk)) P[k >> 5][k & 31] = 0.f;
         }
         if (!(ok = ws.wait(L::B_DP, ph))) break;
         tc_fence_after();
-        float v[2][16];
-        tmem_ld16(da, v[0]);
+        float v[2][32];
+        tmem_ld32(da, v[0]);
+        tmem_ld32(da + 32, v[1]);
+        tmem_wait_ld();
+        if (masked) {  // nothing where P is zero: behind the sequence dP may be anything
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
+            for (int k = 0; k < 64; ++k)
+                if (P[k >> 5][k & 31] == 0.f) v[k >> 5][k & 31] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             float pk[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                tmem_wait_ld();
-                if (k + g < 3) tmem_ld16(da + 16 * (k + g + 1), v[(g + 1) & 1]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    // nothing where P is zero: behind the sequence dP may be anything
-                    const float x = P[k + g][e];
-                    v[g][e] = x == 0.f ? 0.f : x * (v[g][e] - D);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pk[8 * g + e] = __uint_as_float(pack_bf16(v[g][2 * e], v[g][2 * e + 1]));
+            for (int e = 0; e < 16; ++e) {
+                float x, y;
+                unpair2(mul2(pair2(P[k][2 * e], P[k][2 * e + 1]), add2(pair2(v[k][2 * e], v[k][2 * e + 1]), d2)), x, y);
+                pk[e] = __uint_as_float(pack_bf16(x, y));
             }
-            tmem_st16(da + 8 * k, pk);
+            tmem_st16(da + 16 * k, pk);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -299,14 +304,15 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
     const int j = j0 + (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t sa = tb + quad + L::S + half * 64, da = tb + quad + L::DPC + half * 64;
-    float *rowv = reinterpret_cast<float *>(smem + L::OFF_ROW);  // [2 stages][lse * log2e, D][128]
+    float *rowv = reinterpret_cast<float *>(smem + L::OFF_ROW);  // [2 stages][-lse * log2e, -D][128]
     const float c = a.scale * kLog2e;
+    const unsigned long long c2 = pair2(c, c);
     bool ok = true;
     uint32_t ph = 0;
     auto fetch = [&](int it) {  // threads 0-127 lse, 128-255 D
         const int r = w.tile(it) * T + (tid & 127);
         const size_t at = ((size_t)b * a.H + hk * a.G + w.head(it)) * a.n + r;
-        return r < rows ? (tid < 128 ? a.lse[at] * kLog2e : a.delta[at]) : 0.f;
+        return r < rows ? (tid < 128 ? a.lse[at] * -kLog2e : -a.delta[at]) : 0.f;
     };
     float next = w.total > 0 ? fetch(0) : 0.f;
     for (int it = 0; it < w.total; ++it, ph ^= 1u) {
@@ -322,34 +328,33 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         // after an expired wait the loop goes on, so that the barrier above stays matched
         if (!ok || !(ok = ws.wait(L::B_S, ph))) continue;
         tc_fence_after();
-        float P[4][16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld16(sa + 16 * k, P[k]);
+        float P[2][32];
+        tmem_ld32(sa, P[0]);
+        tmem_ld32(sa + 32, P[1]);
         tmem_wait_ld();
-        const float *lse = cur + half * 64, *D = cur + T + half * 64;
+        const float *lse = cur + half * 64, *D = cur + T + half * 64;  // both negated
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(lse + 16 * k + e);
-                P[k][e] = ex2_approx(fmaf(P[k][e], c, -x.x));
-                P[k][e + 1] = ex2_approx(fmaf(P[k][e + 1], c, -x.y));
-                P[k][e + 2] = ex2_approx(fmaf(P[k][e + 2], c, -x.z));
-                P[k][e + 3] = ex2_approx(fmaf(P[k][e + 3], c, -x.w));
+            for (int e = 0; e < 32; e += 4) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(lse + 32 * k + e);
+                float u[4];
+                unpair2(fma2(pair2(P[k][e], P[k][e + 1]), c2, x.x), u[0], u[1]);
+                unpair2(fma2(pair2(P[k][e + 2], P[k][e + 3]), c2, x.y), u[2], u[3]);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) P[k][e + f] = ex2_approx(u[f]);
             }
-            if (masked) {
+        if (masked) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (16 * k + e < lo || 16 * k + e >= hi) P[k][e] = 0.f;
-            }
+            for (int k = 0; k < 64; ++k)
+                if (k < lo || k >= hi) P[k >> 5][k & 31] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
+        for (int k = 0; k < 2; ++k) {
             float pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                pk[e] = __uint_as_float(pack_bf16(P[k + (e >> 3)][2 * (e & 7)], P[k + (e >> 3)][2 * (e & 7) + 1]));
-            tmem_st16(sa + 8 * k, pk);
+            for (int e = 0; e < 16; ++e) pk[e] = __uint_as_float(pack_bf16(P[k][2 * e], P[k][2 * e + 1]));
+            tmem_st16(sa + 16 * k, pk);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -357,29 +362,28 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         if (lane == 0) mbar_arrive(ws.bar(L::B_P));
         if (!(ok = ws.wait(L::B_DP, ph))) continue;
         tc_fence_after();
-        float v[2][16];
-        tmem_ld16(da, v[0]);
+        float v[2][32];
+        tmem_ld32(da, v[0]);
+        tmem_ld32(da + 32, v[1]);
+        tmem_wait_ld();
+        if (masked) {  // queries behind the sequence: nothing, whatever dP is
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
+            for (int k = 0; k < 64; ++k)
+                if (P[k >> 5][k & 31] == 0.f) v[k >> 5][k & 31] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             float pk[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                tmem_wait_ld();
-                if (k + g < 3) tmem_ld16(da + 16 * (k + g + 1), v[(g + 1) & 1]);
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(D + 16 * (k + g) + e);
-                    const float dd[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const float y = P[k + g][e + f];
-                        v[g][e + f] = y == 0.f ? 0.f : y * (v[g][e + f] - dd[f]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pk[8 * g + e] = __uint_as_float(pack_bf16(v[g][2 * e], v[g][2 * e + 1]));
+            for (int e = 0; e < 16; e += 2) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(D + 32 * k + 2 * e);
+                float u, w2, y, z;
+                unpair2(mul2(pair2(P[k][2 * e], P[k][2 * e + 1]), add2(pair2(v[k][2 * e], v[k][2 * e + 1]), x.x)), u, w2);
+                unpair2(mul2(pair2(P[k][2 * e + 2], P[k][2 * e + 3]), add2(pair2(v[k][2 * e + 2], v[k][2 * e + 3]), x.y)), y, z);
+                pk[e] = __uint_as_float(pack_bf16(u, w2));
+                pk[e + 1] = __uint_as_float(pack_bf16(y, z));
             }
-            tmem_st16(da + 8 * k, pk);
+            tmem_st16(da + 16 * k, pk);
         }
         tmem_wait_st();
         tc_fence_before();

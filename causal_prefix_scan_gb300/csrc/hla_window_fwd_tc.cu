@@ -6,7 +6,7 @@
 // softmax of one row per thread (running maximum and sum in fp32), P packed to bf16 over
 // S's own columns, O += P V with P read from TMEM.  While the softmax of one query tile
 // runs, the tensor cores work on the other.  Warps 0-3 and 4-7: softmax of tile 0 and 1;
-// warp 8: MMA; warp 9: TMA into a ring of key and value tiles.
+// warp 8: MMA; warp 9: TMA into a ring of key and value tiles (10, 11: none).
 //
 // The running maximum used in the exponent only moves when a row's maximum passes it by
 // more than 2^8: P then stays below 2^8, and O in TMEM is rescaled a few times per row
@@ -19,7 +19,10 @@ namespace {
 
 using namespace tcw;
 
-constexpr int kThreads = 320, kWarpMma = 8, kWarpTma = 9;
+constexpr int kThreads = 384, kWarpMma = 8, kWarpTma = 9;
+// Registers per thread of the softmax warpgroups, which hold a row of S, and of the third
+// warpgroup: with the 168 that each of the 384 threads is launched with, 2 x 200 + 104 = 3 x 168.
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kSlack = 8.f;
 
 struct Params {
@@ -107,22 +110,10 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
     const int pos = a.p0 + r;
     const uint32_t sa = tb + ((uint32_t)(32 * (warp & 3)) << 16) + L::S0 + t * T;
     const uint32_t oa = tb + ((uint32_t)(32 * (warp & 3)) << 16) + L::O0 + t * DP;
-    const float sc = fabsf(a.scale) * kLog2e, c = a.scale == 0.f ? 1.f : sc;
+    const float c = a.scale * kLog2e;
+    const unsigned long long c2 = pair2(c, c);
     const int dvp = (a.dv + 15) & ~15;
     const int p_lo = a.p0 + row0, p_hi = p_lo + T - 1;
-    // the scores of 16 keys as the softmax takes them: with a negative scale the largest
-    // product is the smallest score, with scale 0 all are 0; -inf where nothing is visible
-    auto prepare = [&](float(&v)[16], int k0, bool masked, int lo, int hi, int sk) {
-        if (a.scale <= 0.f) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = a.scale == 0.f ? 0.f : -v[e];
-        }
-        if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (k0 + e > hi || (k0 + e < lo && k0 + e >= sk)) v[e] = -INFINITY;
-        }
-    };
     float m = -INFINITY, l = 0.f;  // reference maximum (base 2, scaled), sum
     uint32_t ph = 0;
     bool begun = false, ok = true;
@@ -135,21 +126,22 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
         const int j0 = kt * T;
         const bool masked = !(j0 + T - 1 <= p_lo && (p_hi - j0 < a.window || j0 + T <= a.sinks));
         const int hi = pos - j0, sk = a.sinks - j0, lo = pos >= a.window ? pos - a.window + 1 - j0 : -1;
-        // S is read twice, 16 columns at a time with the next 16 on their way (held whole, a
-        // row and what is made of it do not fit the registers): for the maximum, then for P.
-        // P takes the columns [0, 64), always behind the ones already read for it.
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        float buf[2][16];
-        tmem_ld16(sa, buf[0]);
+        float s[4][32];
 #pragma unroll
-        for (int k = 0; k < T / 16; ++k) {
-            tmem_wait_ld();
-            tmem_ld16(sa + (k + 1) % (T / 16) * 16, buf[(k + 1) & 1]);  // at the end the first columns again
-            float(&v)[16] = buf[k & 1];
-            prepare(v, k * 16, masked, lo, hi, sk);
+        for (int k = 0; k < 4; ++k) tmem_ld32(sa + 32 * k, s[k]);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e & 3] = fmaxf(x[e & 3], v[e]);
+            for (int k = 0; k < T; ++k)
+                if (k > hi || (k < lo && k >= sk)) s[k >> 5][k & 31] = -INFINITY;
         }
+        float x[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
+#pragma unroll
+        for (int e = 1; e < 31; e += 2)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = max3(x[k], s[k][e], s[k][e + 1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], s[k][31]);
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
         const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, move)) {
@@ -160,27 +152,25 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
             if (begun) scale_cols(oa, dvp, f);
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float sum[2] = {0.f, 0.f};
+        const unsigned long long b2 = pair2(-base, -base);
+        unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int k = 0; k < T / 16; k += 2) {
+        for (int k = 0; k < 4; ++k) {
             float pk[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                tmem_wait_ld();
-                if (k + g + 1 < T / 16) tmem_ld16(sa + (k + g + 1) * 16, buf[(g + 1) & 1]);
-                float(&v)[16] = buf[g];
-                prepare(v, (k + g) * 16, masked, lo, hi, sk);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = ex2_approx(fmaf(v[2 * e], c, -base)), w2 = ex2_approx(fmaf(v[2 * e + 1], c, -base));
-                    sum[0] += u;
-                    sum[1] += w2;
-                    pk[8 * g + e] = __uint_as_float(pack_bf16(u, w2));
-                }
+            for (int e = 0; e < 16; ++e) {
+                float u, v;
+                unpair2(fma2(pair2(s[k][2 * e], s[k][2 * e + 1]), c2, b2), u, v);
+                u = ex2_approx(u);
+                v = ex2_approx(v);
+                sum[e & 1] = add2(sum[e & 1], pair2(u, v));
+                pk[e] = __uint_as_float(pack_bf16(u, v));
             }
-            tmem_st16(sa + k * 8, pk);
+            tmem_st16(sa + 16 * k, pk);
         }
-        l += sum[0] + sum[1];
+        float l0, l1;
+        unpair2(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -319,11 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = misc[0];
-    if (warp == kWarpTma) {
-        tma_role<DP>(p, w, ws, base);
-    } else if (warp == kWarpMma) {
-        mma_role<DP>(p, w, ws, base, tb);
+    if (warp >= kWarpMma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kWarpTma) tma_role<DP>(p, w, ws, base);
+        if (warp == kWarpMma) mma_role<DP>(p, w, ws, base, tb);
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax_role<DP>(p, w, ws, tb, warp >> 2);
     }
     tc_fence_before();
@@ -351,7 +342,8 @@ cudaError_t launch(Params &p, cudaStream_t st) {
 }  // namespace
 
 bool fwd_tc_takes(const Args &a) {
-    return a.d % 8 == 0 && a.dv % 8 == 0 && tcw::mappable(a.q) && tcw::mappable(a.k) && tcw::mappable(a.v) &&
+    // a positive scale: the largest product is then the largest score
+    return a.scale > 0.f && a.d % 8 == 0 && a.dv % 8 == 0 && tcw::mappable(a.q) && tcw::mappable(a.k) && tcw::mappable(a.v) &&
            (reinterpret_cast<uintptr_t>(a.o.p) & 15u) == 0 && a.o.sb % 8 == 0 && a.o.sh % 8 == 0 && a.o.st % 8 == 0;
 }
 

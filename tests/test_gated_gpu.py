@@ -346,3 +346,37 @@ def test_wrapper_refusals():
         hla.gated_forward(x, x, workspace=hla.new_workspace(256))
     with pytest.raises(ValueError):
         hla.gated_forward(c["x"].cpu(), c["g"].cpu())
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,n,d,ragged", [(40, 1, 66, False), (2, 700, 1280, False), (13, 1500, 214, True), (3, 383, 1000, True),
+                                          (1, 769, 2600, False)])
+def test_many_channels(B, n, d, ragged, gate, dtype):
+    """Enough channels that each CTA walks its sequence from end to end."""
+    c = inputs(B, n, d, gate, dtype, seed=n)
+    L = None
+    if ragged:
+        L = torch.tensor([n, 0, 1, n - 1, n // 2, 255, 256, 257, 384, 5, n, 100, 3][:B], dtype=torch.int32, device="cuda").clamp(max=n)
+    y, s, r = check(c, lengths=L)
+    if ragged:  # nothing is written behind the lengths
+        dead = (torch.arange(n, device="cuda")[None, :, None] >= L[:, None, None]).expand_as(y)
+        mark = torch.full_like(y, 7.0)
+        hla.gated_forward(c["x"], c["g"], gate, c["rate"], lengths=L, out=mark)
+        o = torch.full_like(y, 7.0), torch.full_like(y, 7.0)
+        hla.gated_backward(c["x"], c["g"], y, c["dy"], gate, c["rate"], lengths=L, out=o)
+        assert all(bool((t[dead] == 7).all()) for t in (mark,) + o)
+
+
+def test_offsets_beyond_32_bits_with_many_channels():
+    st, n, d = 1 << 28, 20, 2560
+    buf = torch.empty((n - 1) * st + d, dtype=BF16, device="cuda")
+    x = torch.as_strided(buf, (1, n, d), (0, st, 1))
+    c = inputs(1, n, d, "sigmoid", BF16)
+    x.copy_(c["x"])
+    y = hla.gated_forward(x, c["g"], "sigmoid")
+    ry, _, Ey, _ = ref.gated_forward(c["x"], c["g"], "sigmoid")
+    ref.close(y, ry, Ey, "y")
+    r = hla.gated_backward(x, c["g"], y, c["dy"], "sigmoid")
+    want = ref.gated_backward(c["x"], c["g"], y, c["dy"], "sigmoid")
+    ref.close(r.dg, *want["dg"], "dg")
