@@ -107,6 +107,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
         const bool masked = !(j0 + T - 1 <= a.p0 + i0 && (a.p0 + i0 + T - 1 - j0 < a.window || j0 + T <= a.sinks));
         const int hi = pos - j0 + 1 - half * 64, sk = a.sinks - j0 - half * 64;
         const int lo = (pos >= a.window ? pos - a.window + 1 - j0 : 0) - half * 64;
+        const uint32_t bits[2] = {visible_bits(0, lo, hi, sk), visible_bits(32, lo, hi, sk)};
         if (!(ok = ws.wait(L::B_S, ph))) break;
         tc_fence_after();
         float P[2][32];
@@ -127,8 +128,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
             }
         if (masked) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k >= hi || (k < lo && k >= sk)) P[k >> 5][k & 31] = 0.f;
+            for (int k = 0; k < 2; ++k) mask32(P[k], bits[k], 0.f);
         }
         if (!(ok = ws.wait(L::B_DP, ph))) break;
         tc_fence_after();
@@ -136,10 +136,9 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
         tmem_ld32(da, v[0]);
         tmem_ld32(da + 32, v[1]);
         tmem_wait_ld();
-        if (masked) {  // nothing where P is zero: behind the sequence dP may be anything
+        if (masked) {  // behind the sequence dP may be anything
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (P[k >> 5][k & 31] == 0.f) v[k >> 5][k & 31] = 0.f;
+            for (int k = 0; k < 2; ++k) mask32(v[k], bits[k], 0.f);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -325,6 +324,7 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         // visible queries of key j: columns [lo, hi)
         const int lo = j - p_lo - half * 64;
         const int hi = (j < a.sinks ? rows - i0 : (int)min((long long)rows - i0, (long long)j - p_lo + a.window)) - half * 64;
+        const uint32_t bits[2] = {visible_bits(0, lo, hi, 0), visible_bits(32, lo, hi, 0)};
         // after an expired wait the loop goes on, so that the barrier above stays matched
         if (!ok || !(ok = ws.wait(L::B_S, ph))) continue;
         tc_fence_after();
@@ -346,8 +346,7 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
             }
         if (masked) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k < lo || k >= hi) P[k >> 5][k & 31] = 0.f;
+            for (int k = 0; k < 2; ++k) mask32(P[k], bits[k], 0.f);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -368,8 +367,7 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         tmem_wait_ld();
         if (masked) {  // queries behind the sequence: nothing, whatever dP is
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (P[k >> 5][k & 31] == 0.f) v[k >> 5][k & 31] = 0.f;
+            for (int k = 0; k < 2; ++k) mask32(v[k], bits[k], 0.f);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

@@ -36,7 +36,7 @@ struct Lay {
     static constexpr int TILE = T * DP * 2;
     static constexpr int NS = DP == 64 ? 8 : 4;  // ring slots
     static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NS * TILE;
-    static constexpr int B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2, B_O = B_P + 2,
+    static constexpr int B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2, B_O = B_P + 4,
                          B_FIN = B_O + 2, NB = B_FIN + 1;
     static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
     static constexpr uint32_t S0 = 0, O0 = 2 * T;  // TMEM columns: S of both tiles, O of both
@@ -80,6 +80,11 @@ struct Work {
         }
         head = min(sink_tiles, first);
         total = last < 0 ? 0 : head + last - first + 1;
+    }
+    // Columns of key tile kt that tile t works on: all, or before its window only those of
+    // the first tokens, in chunks of 32.
+    HLA_DEVICE int columns(const Args &a, int t, int kt) const {
+        return kt >= (t ? lo[1] : lo[0]) ? T : min(T, (a.sinks - kt * T + 31) & ~31);
     }
     HLA_DEVICE int key_tile(int i) const { return i < head ? i : first + i - head; }
     HLA_DEVICE bool active(int t, int kt) const {
@@ -126,23 +131,36 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
         const int j0 = kt * T;
         const bool masked = !(j0 + T - 1 <= p_lo && (p_hi - j0 < a.window || j0 + T <= a.sinks));
         const int hi = pos - j0, sk = a.sinks - j0, lo = pos >= a.window ? pos - a.window + 1 - j0 : -1;
+        const int chunks = w.columns(a, t, kt) >> 5;
         float s[4][32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(sa + 32 * k, s[k]);
+        for (int k = 0; k < 4; ++k)
+            if (k < chunks) tmem_ld32(sa + 32 * k, s[k]);
         tmem_wait_ld();
         if (masked) {
 #pragma unroll
-            for (int k = 0; k < T; ++k)
-                if (k > hi || (k < lo && k >= sk)) s[k >> 5][k & 31] = -INFINITY;
+            for (int k = 0; k < 4; ++k)
+                if (k < chunks) mask32(s[k], visible_bits(32 * k, lo, hi + 1, sk), -INFINITY);
         }
-        float x[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
+        float mx = -INFINITY;
+        if (chunks == 4) {
+            float x[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
 #pragma unroll
-        for (int e = 1; e < 31; e += 2)
+            for (int e = 1; e < 31; e += 2)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = max3(x[k], s[k][e], s[k][e + 1]);
+                for (int k = 0; k < 4; ++k) x[k] = max3(x[k], s[k][e], s[k][e + 1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], s[k][31]);
-        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
+            for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], s[k][31]);
+            mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < chunks) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mx = max3(mx, s[k][e], s[k][e + 1]);
+                }
+        }
+        mx *= c;
         const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, move)) {
             const float mn = move ? mx : m;
@@ -156,25 +174,29 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
         unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            float pk[16];
+            if (k < chunks) {
+                float pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float u, v;
-                unpair2(fma2(pair2(s[k][2 * e], s[k][2 * e + 1]), c2, b2), u, v);
-                u = ex2_approx(u);
-                v = ex2_approx(v);
-                sum[e & 1] = add2(sum[e & 1], pair2(u, v));
-                pk[e] = __uint_as_float(pack_bf16(u, v));
+                for (int e = 0; e < 16; ++e) {
+                    float u, v;
+                    unpair2(fma2(pair2(s[k][2 * e], s[k][2 * e + 1]), c2, b2), u, v);
+                    u = ex2_approx(u);
+                    v = ex2_approx(v);
+                    sum[e & 1] = add2(sum[e & 1], pair2(u, v));
+                    pk[e] = __uint_as_float(pack_bf16(u, v));
+                }
+                tmem_st16(sa + 16 * k, pk);
             }
-            tmem_st16(sa + 16 * k, pk);
+            if (k & 1) {  // half of P: its products can begin
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ws.bar(L::B_P + 2 * t + (k >> 1)));
+            }
         }
         float l0, l1;
         unpair2(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ws.bar(L::B_P + t));
         begun = true;
     }
     if (!begun || !ok) return;
@@ -204,7 +226,6 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
     using L = Lay<DP>;
     const Args &a = p.a;
     const int lane = threadIdx.x & 31;
-    const uint32_t id_s = make_idesc(T, T, false, false);
     const uint32_t id_o = make_idesc(T, (a.dv + 15) & ~15, false, true);
     const int qk_steps = (a.d + 15) / 16;
     bool pend[2] = {false, false}, begun[2] = {false, false};
@@ -225,11 +246,17 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
                     const int live = w.len - w.key_tile(i - 1) * T;
                     if (ok && live < T) zero_rows<DP>(slot(2 * (i - 1) + 1), live, lane);
                 }
-                if (ok) ok = ws.wait(L::B_P + t, php[t]);
+                const int steps = w.columns(a, t, w.key_tile(i - 1)) / 16;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {  // the halves of P as they come
+                    if (ok) ok = ws.wait(L::B_P + 2 * t + g, php[t]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_tm(tb + L::O0 + t * DP, tb + L::S0 + t * T + 32 * g, slot(2 * (i - 1) + 1) + 64 * 128 * g, id_o,
+                           max(0, min(4, steps - 4 * g)), begun[t] || g > 0);
+                }
                 if (!ok) break;
                 php[t] ^= 1u;
-                tc_fence_after();
-                mma_tm(tb + L::O0 + t * DP, tb + L::S0 + t * T, slot(2 * (i - 1) + 1), id_o, T / 16, begun[t]);
                 begun[t] = true;
                 pend[t] = false;
                 if (i == w.total || kt > w.hi[t]) umma_commit_warp(ws.bar(L::B_O + t));
@@ -240,7 +267,8 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
                     k_here = true;
                 }
                 if (!ok) break;
-                mma_kk(tb + L::S0 + t * T, base + L::OFF_Q + t * L::TILE, slot(2 * i), id_s, qk_steps, false);
+                mma_kk(tb + L::S0 + t * T, base + L::OFF_Q + t * L::TILE, slot(2 * i),
+                       make_idesc(T, w.columns(a, t, kt), false, false), qk_steps, false);
                 umma_commit_warp(ws.bar(L::B_S + t));
                 pend[t] = true;
             }
@@ -295,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         misc[1] = 0u;
-        for (int i = 0; i < L::NB; ++i) mbar_init(ws.bar(i), i == L::B_P || i == L::B_P + 1 ? 4 : 1);
+        for (int i = 0; i < L::NB; ++i) mbar_init(ws.bar(i), i >= L::B_P && i < L::B_P + 4 ? 4 : 1);
         fence_mbar_init();
         tma_prefetch_desc(&p.mq);
         tma_prefetch_desc(&p.mk);

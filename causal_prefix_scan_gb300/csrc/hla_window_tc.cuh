@@ -135,6 +135,17 @@ HLA_DEVICE float max3(float a, float b, float c) {
     return r;
 }
 
+// Of 32 columns c0 .. c0 + 31, those in [lo, hi) or in [0, min(sk, hi)) as bits.  Masks go by
+// bit tests: comparisons joined by && and || come out as a branch per element.
+HLA_DEVICE uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+HLA_DEVICE uint32_t visible_bits(int c0, int lo, int hi, int sk) {
+    return low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(sk - c0));
+}
+HLA_DEVICE void mask32(float (&v)[32], uint32_t bits, float other) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : other;
+}
+
 // Zeroes rows [r0, 128) of a tile (one warp) and shows the tensor cores the result.
 template <int DP>
 HLA_DEVICE void zero_rows(uint8_t *tile, int r0, int lane) {
