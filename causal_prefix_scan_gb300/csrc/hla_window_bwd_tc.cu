@@ -35,8 +35,8 @@ HLA_DEVICE void elem_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A in TMEM as two blocks of 64 contraction rows (32 packed columns each) 64 columns apart.
 HLA_DEVICE void mma_ts(uint32_t d, uint32_t a, const uint8_t *b, uint32_t idesc, bool acc) {
-    mma_tm(d, a, b, idesc, 4, acc);
-    mma_tm(d, a + 64, b + 64 * 128, idesc, 4, true);
+    mma_tm64(d, a, b, 0, idesc, acc);
+    mma_tm64(d, a + 64, b, 64, idesc, true);
 }
 
 // Common set-up and end of both kernels.
@@ -182,7 +182,8 @@ __device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t
     const Args &a = p.a;
     const int lane = threadIdx.x & 31, N = kt.total;
     const uint32_t id_s = make_idesc(T, T, false, false), id_q = make_idesc(T, (a.d + 15) & ~15, false, true);
-    const int qk = (a.d + 15) / 16, gv = (a.dv + 15) / 16;
+    const bool qk = a.d > 64, gv = a.dv > 64;
+    tb = uniform(tb);
     auto slot = [&](int idx) { return base + L::OFF_RING + (idx % L::NS) * L::TILE; };
     auto full = [&](int idx) { return ws.wait(L::B_FULL + idx % L::NS, (uint32_t)(idx / L::NS) & 1u); };
     auto free_slot = [&](int idx) { umma_commit_warp(ws.bar(L::B_EMPTY + idx % L::NS)); };
@@ -190,13 +191,13 @@ __device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t
         if (!full(2 * j)) return false;
         // keys behind the sequence may be anything, and 0 times that is not 0 in dS K
         if (len - kt[j] * T < T) zero_rows<DP>(slot(2 * j), len - kt[j] * T, lane);
-        mma_kk(tb + L::S, base + L::OFF_Q, slot(2 * j), id_s, qk, false);
+        mma_kk<DP>(tb + L::S, base + L::OFF_Q, slot(2 * j), id_s, qk);
         umma_commit_warp(ws.bar(L::B_S));
         return true;
     };
     auto do_dp = [&](int j) {
         if (!full(2 * j + 1)) return false;
-        mma_kk(tb + L::DPC, base + L::OFF_G, slot(2 * j + 1), id_s, gv, false);
+        mma_kk<DP>(tb + L::DPC, base + L::OFF_G, slot(2 * j + 1), id_s, gv);
         umma_commit_warp(ws.bar(L::B_DP));
         free_slot(2 * j + 1);
         return true;
@@ -434,7 +435,8 @@ __device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_
     const int lane = threadIdx.x & 31, N = w.total;
     const uint32_t id_s = make_idesc(T, T, false, false);
     const uint32_t id_v = make_idesc(T, (a.dv + 15) & ~15, false, true), id_k = make_idesc(T, (a.d + 15) & ~15, false, true);
-    const int qk = (a.d + 15) / 16, gv = (a.dv + 15) / 16;
+    const bool qk = a.d > 64, gv = a.dv > 64;
+    tb = uniform(tb);
     auto tq = [&](int i) { return base + L::OFF_RING + (i % L::NS) * 2 * L::TILE; };
     auto tg = [&](int i) { return tq(i) + L::TILE; };
     auto par = [&](int i) { return (uint32_t)(i / L::NS) & 1u; };
@@ -443,14 +445,14 @@ __device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_
     auto do_s = [&](int i) {
         if (!ws.wait(L::B_FQ + i % L::NS, par(i))) return false;
         if (live(i) < T) zero_rows<DP>(tq(i), live(i), lane);
-        mma_kk(tb + L::S, base + L::OFF_K, tq(i), id_s, qk, false);
+        mma_kk<DP>(tb + L::S, base + L::OFF_K, tq(i), id_s, qk);
         umma_commit_warp(ws.bar(L::B_S));
         return true;
     };
     auto do_dp = [&](int i) {
         if (!ws.wait(L::B_FG + i % L::NS, par(i))) return false;
         if (live(i) < T) zero_rows<DP>(tg(i), live(i), lane);
-        mma_kk(tb + L::DPC, base + L::OFF_V, tg(i), id_s, gv, false);
+        mma_kk<DP>(tb + L::DPC, base + L::OFF_V, tg(i), id_s, gv);
         umma_commit_warp(ws.bar(L::B_DP));
         return true;
     };

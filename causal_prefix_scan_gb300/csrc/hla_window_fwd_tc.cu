@@ -132,18 +132,16 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
         const bool masked = !(j0 + T - 1 <= p_lo && (p_hi - j0 < a.window || j0 + T <= a.sinks));
         const int hi = pos - j0, sk = a.sinks - j0, lo = pos >= a.window ? pos - a.window + 1 - j0 : -1;
         const int chunks = w.columns(a, t, kt) >> 5;
-        float s[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < chunks) tmem_ld32(sa + 32 * k, s[k]);
-        tmem_wait_ld();
-        if (masked) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < chunks) mask32(s[k], visible_bits(32 * k, lo, hi + 1, sk), -INFINITY);
-        }
         float mx = -INFINITY;
+        float s[4][32];
         if (chunks == 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld32(sa + 32 * k, s[k]);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mask32(s[k], visible_bits(32 * k, lo, hi + 1, sk), -INFINITY);
+            }
             float x[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
 #pragma unroll
             for (int e = 1; e < 31; e += 2)
@@ -153,12 +151,14 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
             for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], s[k][31]);
             mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         } else {
+#pragma unroll 1
+            for (int k = 0; k < chunks; ++k) {
+                tmem_ld32(sa + 32 * k, s[0]);
+                tmem_wait_ld();
+                mask32(s[0], visible_bits(32 * k, lo, hi + 1, sk), -INFINITY);
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k < chunks) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx = max3(mx, s[k][e], s[k][e + 1]);
-                }
+                for (int e = 0; e < 32; e += 2) mx = max3(mx, s[0][e], s[0][e + 1]);
+            }
         }
         mx *= c;
         const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
@@ -172,27 +172,42 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Work &w, con
         const float base = m == -INFINITY ? 0.f : m;
         const unsigned long long b2 = pair2(-base, -base);
         unsigned long long sum[2] = {0ull, 0ull};
+        auto probabilities = [&](const float(&v)[32], uint32_t to) {  // 32 columns of P
+            float pk[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k < chunks) {
-                float pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float u, v;
-                    unpair2(fma2(pair2(s[k][2 * e], s[k][2 * e + 1]), c2, b2), u, v);
-                    u = ex2_approx(u);
-                    v = ex2_approx(v);
-                    sum[e & 1] = add2(sum[e & 1], pair2(u, v));
-                    pk[e] = __uint_as_float(pack_bf16(u, v));
-                }
-                tmem_st16(sa + 16 * k, pk);
+            for (int e = 0; e < 16; ++e) {
+                float x, y;
+                unpair2(fma2(pair2(v[2 * e], v[2 * e + 1]), c2, b2), x, y);
+                x = ex2_approx(x);
+                y = ex2_approx(y);
+                sum[e & 1] = add2(sum[e & 1], pair2(x, y));
+                pk[e] = __uint_as_float(pack_bf16(x, y));
             }
-            if (k & 1) {  // half of P: its products can begin
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ws.bar(L::B_P + 2 * t + (k >> 1)));
+            tmem_st16(to, pk);
+        };
+        auto hand_over = [&](int half) {  // half of P is there: its products can begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ws.bar(L::B_P + 2 * t + half));
+        };
+        if (chunks == 4) {
+            probabilities(s[0], sa);
+            probabilities(s[1], sa + 16);
+            hand_over(0);
+            probabilities(s[2], sa + 32);
+            probabilities(s[3], sa + 48);
+            hand_over(1);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < chunks; ++k) {
+                tmem_ld32(sa + 32 * k, s[0]);
+                tmem_wait_ld();
+                mask32(s[0], visible_bits(32 * k, lo, hi + 1, sk), -INFINITY);
+                probabilities(s[0], sa + 16 * k);
             }
+            hand_over(0);
+            hand_over(1);
         }
         float l0, l1;
         unpair2(add2(sum[0], sum[1]), l0, l1);
@@ -227,7 +242,8 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
     const Args &a = p.a;
     const int lane = threadIdx.x & 31;
     const uint32_t id_o = make_idesc(T, (a.dv + 15) & ~15, false, true);
-    const int qk_steps = (a.d + 15) / 16;
+    const bool wide = a.d > 64;
+    tb = uniform(tb);
     bool pend[2] = {false, false}, begun[2] = {false, false};
     uint32_t php[2] = {0, 0};
     bool ok = ws.wait(L::B_Q, 0u);
@@ -246,14 +262,16 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
                     const int live = w.len - w.key_tile(i - 1) * T;
                     if (ok && live < T) zero_rows<DP>(slot(2 * (i - 1) + 1), live, lane);
                 }
-                const int steps = w.columns(a, t, w.key_tile(i - 1)) / 16;
+                const int chunks = uniform(w.columns(a, t, w.key_tile(i - 1)) / 32);
+                const uint64_t dv = make_sdesc(smem_u32(slot(2 * (i - 1) + 1)), T * 128u, 1024u);
+                const uint32_t o = tb + L::O0 + t * DP, s = tb + L::S0 + t * T;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {  // the halves of P as they come
                     if (ok) ok = ws.wait(L::B_P + 2 * t + g, php[t]);
                     if (!ok) break;
                     tc_fence_after();
-                    mma_tm(tb + L::O0 + t * DP, tb + L::S0 + t * T + 32 * g, slot(2 * (i - 1) + 1) + 64 * 128 * g, id_o,
-                           max(0, min(4, steps - 4 * g)), begun[t] || g > 0);
+                    if (2 * g < chunks) mma_ts32(o, s + 32 * g, dv + 512 * g, id_o, begun[t] || g > 0);
+                    if (2 * g + 1 < chunks) mma_ts32(o, s + 32 * g + 16, dv + 512 * g + 256, id_o, true);
                 }
                 if (!ok) break;
                 php[t] ^= 1u;
@@ -267,8 +285,8 @@ __device__ __forceinline__ void mma_role(const Params &p, const Work &w, const W
                     k_here = true;
                 }
                 if (!ok) break;
-                mma_kk(tb + L::S0 + t * T, base + L::OFF_Q + t * L::TILE, slot(2 * i),
-                       make_idesc(T, w.columns(a, t, kt), false, false), qk_steps, false);
+                mma_kk<DP>(tb + L::S0 + t * T, base + L::OFF_Q + t * L::TILE, slot(2 * i),
+                           make_idesc(T, uniform(w.columns(a, t, kt)), false, false), wide);
                 umma_commit_warp(ws.bar(L::B_S + t));
                 pend[t] = true;
             }

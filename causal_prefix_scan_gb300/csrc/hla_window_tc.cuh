@@ -77,27 +77,50 @@ struct Waits {
     }
 };
 
-// ---- MMA groups, issued by a whole warp (one elected lane).  `steps` contraction steps of 16.
-// D [128 x N] (+)= A [128 x K] B [N x K]^T: both K-major tiles of 128 rows (B: RB rows)
-template <int RB = T>
-HLA_DEVICE void mma_kk(uint32_t d, const uint8_t *a, const uint8_t *b, uint32_t idesc, int steps, bool acc) {
+// ---- MMA groups, issued by a whole warp with warp-uniform operands: one lane is elected for a
+// group, and a group is one block of instructions (issued one by one from a loop, they took
+// longer to issue than to run).
+// D [128 x N] (+)= A B^T over 64 contraction columns: both K-major tiles
+HLA_DEVICE void mma_ss64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p, e, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+        " add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+}
+// D [128 x N] (+)= A B over 32 contraction rows of B: A packed bf16 in TMEM (16 columns), B MN-major
+HLA_DEVICE void mma_ts32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p, e, t;\n .reg .b64 b1;\n .reg .b32 a1;\n"
+        " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.s64 b1, %2, 128;\n add.u32 a1, %1, 8;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+}
+// The whole width of two tiles of 128 rows (64 columns per block; zero columns behind the
+// tensors' own are multiplied too): `wide` takes both blocks of DP = 128.
+template <int DP>
+HLA_DEVICE void mma_kk(uint32_t d, const uint8_t *a, const uint8_t *b, uint32_t idesc, bool wide) {
     const uint64_t da = make_sdesc(smem_u32(a), 16u, 1024u), db = make_sdesc(smem_u32(b), 16u, 1024u);
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t in = (uint32_t)(s & 3) * 2u;
-        umma_f16_warp(d, da + (uint32_t)(s >> 2) * (T * 8u) + in, db + (uint32_t)(s >> 2) * (RB * 8u) + in, idesc,
-                      acc || s > 0 ? 1u : 0u);
-    }
+    mma_ss64(d, da, db, idesc, false);
+    if (DP > 64 && wide) mma_ss64(d, da + T * 8, db + T * 8, idesc, true);
 }
-// D [128 x N] (+)= A [128 x K] B [K x N]: A packed bf16 in TMEM, B MN-major (its rows contract)
-HLA_DEVICE void mma_tm(uint32_t d, uint32_t a, const uint8_t *b, uint32_t idesc, int steps, bool acc) {
-    const uint64_t db = make_sdesc(smem_u32(b), T * 128u, 1024u);
-    for (int s = 0; s < steps; ++s)
-        asm volatile(
-            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-            "r"(a + (uint32_t)s * 8u), "l"(db + (uint64_t)(s * 128)), "r"(idesc), "r"((acc || s > 0) ? 1u : 0u)
-            : "memory");
+// 64 contraction rows from row r0 of an MN-major tile, A in TMEM
+HLA_DEVICE void mma_tm64(uint32_t d, uint32_t a, const uint8_t *b, int r0, uint32_t idesc, bool acc) {
+    const uint64_t db = make_sdesc(smem_u32(b) + (uint32_t)r0 * 128u, T * 128u, 1024u);
+    mma_ts32(d, a, db, idesc, acc);
+    mma_ts32(d, a + 16, db + 256, idesc, true);
 }
+// A warp-uniform value, known as such to the compiler.
+HLA_DEVICE uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // 32 columns of 32-bit words, this warp's lanes.
 HLA_DEVICE void tmem_ld32(uint32_t taddr, float (&v)[32]) {
