@@ -412,12 +412,11 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] *= f;
-        if (!live) continue;
-        if (split) {
+        if (live && split) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
                 if (k + e < width) *reinterpret_cast<float4 *>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        } else {
+        } else if (live) {
             uint4 u[2];
             uint32_t *y = reinterpret_cast<uint32_t *>(u);
 #pragma unroll
@@ -425,6 +424,7 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
             *reinterpret_cast<uint4 *>(o + k) = u[0];
             if (k + 8 < width) *reinterpret_cast<uint4 *>(o + k + 8) = u[1];
         }
+        __syncwarp();
     }
 }
 
