@@ -33,10 +33,13 @@ struct Params {
 
 HLA_DEVICE void elem_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// A in TMEM as two blocks of 64 contraction rows (32 packed columns each) 64 columns apart.
-HLA_DEVICE void mma_ts(uint32_t d, uint32_t a, const uint8_t *b, uint32_t idesc, bool acc) {
-    mma_tm64(d, a, b, 0, idesc, acc);
-    mma_tm64(d, a + 64, b, 64, idesc, true);
+// D (+)= A B over the 128 rows of B: A in TMEM as two blocks of 64 contraction rows (32 packed
+// columns each) 64 columns apart.
+HLA_DEVICE void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    mma_ts32(d, a, b, idesc, acc);
+    mma_ts32(d, a + 16, b + 256, idesc, true);
+    mma_ts32(d, a + 64, b + 512, idesc, true);
+    mma_ts32(d, a + 80, b + 768, idesc, true);
 }
 
 // Common set-up and end of both kernels.
@@ -81,7 +84,7 @@ struct LayQ {
     static constexpr int NS = DP == 64 ? 8 : 4;  // ring slots, K and V tiles in turn
     static constexpr int OFF_Q = 0, OFF_G = TILE, OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NS * TILE;
     static constexpr int B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_SF = B_S + 1, B_DP = B_SF + 1,
-                         B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, NB = B_FIN + 1;
+                         B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, B_RAW = B_FIN + 1, NB = B_RAW + 1;
     static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
     static constexpr uint32_t S = 0, DPC = T, DQ = 2 * T;  // TMEM columns
 };
@@ -99,7 +102,6 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
     const size_t row = ((size_t)b * a.H + h) * a.n + r;
     const float c = a.scale * kLog2e, base = live ? a.lse[row] * kLog2e : 0.f;
     const float D = live ? a.delta[row] : 0.f;
-    const unsigned long long c2 = pair2(c, c), b2 = pair2(-base, -base), d2 = pair2(-D, -D);
     bool ok = true;
     uint32_t ph = 0;
     for (int it = 0; it < kt.total; ++it, ph ^= 1u) {
@@ -120,12 +122,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float u, v;
-                unpair2(fma2(pair2(P[k][e], P[k][e + 1]), c2, b2), u, v);
-                P[k][e] = ex2_approx(u);
-                P[k][e + 1] = ex2_approx(v);
-            }
+            for (int e = 0; e < 32; ++e) P[k][e] = ex2_approx(fmaf(P[k][e], c, -base));
         if (masked) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) mask32(P[k], bits[k], 0.f);
@@ -145,9 +142,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
             float pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                float x, y;
-                unpair2(mul2(pair2(P[k][2 * e], P[k][2 * e + 1]), add2(pair2(v[k][2 * e], v[k][2 * e + 1]), d2)), x, y);
-                pk[e] = __uint_as_float(pack_bf16(x, y));
+                pk[e] = __uint_as_float(pack_bf16(P[k][2 * e] * (v[k][2 * e] - D), P[k][2 * e + 1] * (v[k][2 * e + 1] - D)));
             }
             tmem_st16(da + 16 * k, pk);
         }
@@ -176,46 +171,45 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
 }
 
 template <int DP>
-__device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const KeyTiles &kt,
-                                       int len) {
+__device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, int N) {
     using L = LayQ<DP>;
     const Args &a = p.a;
-    const int lane = threadIdx.x & 31, N = kt.total;
     const uint32_t id_s = make_idesc(T, T, false, false), id_q = make_idesc(T, (a.d + 15) & ~15, false, true);
     const bool qk = a.d > 64, gv = a.dv > 64;
-    tb = uniform(tb);
-    auto slot = [&](int idx) { return base + L::OFF_RING + (idx % L::NS) * L::TILE; };
-    auto full = [&](int idx) { return ws.wait(L::B_FULL + idx % L::NS, (uint32_t)(idx / L::NS) & 1u); };
-    auto free_slot = [&](int idx) { umma_commit_warp(ws.bar(L::B_EMPTY + idx % L::NS)); };
-    auto do_s = [&](int j) {
-        if (!full(2 * j)) return false;
-        // keys behind the sequence may be anything, and 0 times that is not 0 in dS K
-        if (len - kt[j] * T < T) zero_rows<DP>(slot(2 * j), len - kt[j] * T, lane);
-        mma_kk<DP>(tb + L::S, base + L::OFF_Q, slot(2 * j), id_s, qk);
+    const uint64_t q = kmajor(base + L::OFF_Q), g = kmajor(base + L::OFF_G), ring_k = kmajor(base + L::OFF_RING),
+                   ring_m = mnmajor(base + L::OFF_RING);
+    constexpr uint32_t STEP = L::TILE >> 4;
+    Ring<L::NS> ring;  // the next tile: keys and values in turn
+    uint32_t k_slot = 0;
+    auto do_s = [&]() {
+        if (!ws.wait(L::B_FULL + ring.slot, ring.phase)) return false;
+        k_slot = ring.slot;
+        mma_kk<DP>(tb + L::S, q, ring_k + ring.slot * STEP, id_s, qk);
         umma_commit_warp(ws.bar(L::B_S));
+        ring.next();
         return true;
     };
-    auto do_dp = [&](int j) {
-        if (!full(2 * j + 1)) return false;
-        mma_kk<DP>(tb + L::DPC, base + L::OFF_G, slot(2 * j + 1), id_s, gv);
+    auto do_dp = [&]() {
+        if (!ws.wait(L::B_FULL + ring.slot, ring.phase)) return false;
+        mma_kk<DP>(tb + L::DPC, g, ring_k + ring.slot * STEP, id_s, gv);
         umma_commit_warp(ws.bar(L::B_DP));
-        free_slot(2 * j + 1);
+        umma_commit_warp(ws.bar(L::B_EMPTY + ring.slot));
+        ring.next();
         return true;
     };
-    bool ok = ws.wait(L::B_Q, 0u) && do_s(0) && do_dp(0);
+    bool ok = ws.wait(L::B_Q, 0u) && do_s() && do_dp();
     for (int j = 0; j < N && ok; ++j) {
-        const uint32_t ph = (uint32_t)j & 1u;
+        const uint32_t ph = (uint32_t)j & 1u, slot = k_slot;
         if (j + 1 < N) {
-            ok = ws.wait(L::B_SF, ph);
+            if (!(ok = ws.wait(L::B_SF, ph))) break;
             tc_fence_after();
-            ok = ok && do_s(j + 1);
+            if (!(ok = do_s())) break;
         }
-        ok = ok && ws.wait(L::B_DS, ph);
-        if (!ok) break;
+        if (!(ok = ws.wait(L::B_DS, ph))) break;
         tc_fence_after();
-        mma_ts(tb + L::DQ, tb + L::DPC, slot(2 * j), id_q, j > 0);
-        free_slot(2 * j);
-        if (j + 1 < N) ok = do_dp(j + 1);
+        mma_ts(tb + L::DQ, tb + L::DPC, ring_m + slot * STEP, id_q, j > 0);
+        umma_commit_warp(ws.bar(L::B_EMPTY + slot));
+        if (j + 1 < N) ok = do_dp();
     }
     if (ok) umma_commit_warp(ws.bar(L::B_O));
     umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
@@ -225,27 +219,37 @@ __device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t
 
 template <int DP>
 __device__ __forceinline__ void dq_tma(const Params &p, const Waits &ws, uint8_t *base, const KeyTiles &kt, int b, int h,
-                                       int i0) {
+                                       int i0, int len) {
     using L = LayQ<DP>;
     const Args &a = p.a;
-    const bool one = (threadIdx.x & 31) == 0;
-    const int hk = h / a.G;
-    if (one) {
+    const int lane = threadIdx.x & 31, hk = h / a.G;
+    if (lane == 0) {
         mbar_expect_tx(ws.bar(L::B_Q), 2 * L::TILE);
         load_tile<DP>(base + L::OFF_Q, &p.mq, a.q, ws.bar(L::B_Q), i0, h, b);
         load_tile<DP>(base + L::OFF_G, &p.mg, a.go, ws.bar(L::B_Q), i0, h, b);
     }
+    Ring<L::NS> ring;
+    uint32_t raw = 0;
     int idx = 0;
     for (; idx < 2 * kt.total; ++idx) {
-        const int s = idx % L::NS, use = idx / L::NS;
-        if (use > 0 && !ws.wait(L::B_EMPTY + s, (uint32_t)(use - 1) & 1u)) break;
-        if (one) {
-            mbar_expect_tx(ws.bar(L::B_FULL + s), L::TILE);
-            const bool key = (idx & 1) == 0;
-            load_tile<DP>(base + L::OFF_RING + s * L::TILE, key ? &p.mk : &p.mv, key ? a.k : a.v, ws.bar(L::B_FULL + s),
-                          kt[idx >> 1] * T, hk, b);
+        const uint32_t s = ring.slot;
+        if (idx >= L::NS && !ws.wait(L::B_EMPTY + s, ring.phase ^ 1u)) break;
+        const bool key = (idx & 1) == 0;
+        const int j0 = kt[idx >> 1] * T;
+        const bool clean = key && len - j0 < T;  // dS K contracts over the keys: zeros behind the sequence
+        const int full = clean ? L::B_RAW : L::B_FULL + (int)s;
+        if (lane == 0) {
+            mbar_expect_tx(ws.bar(full), L::TILE);
+            load_tile<DP>(base + L::OFF_RING + s * L::TILE, key ? &p.mk : &p.mv, key ? a.k : a.v, ws.bar(full), j0, hk, b);
         }
         __syncwarp();
+        if (clean) {
+            if (!ws.wait(L::B_RAW, raw)) break;
+            raw ^= 1u;
+            zero_rows<DP>(base + L::OFF_RING + s * L::TILE, len - j0, lane);
+            if (lane == 0) mbar_arrive(ws.bar(L::B_FULL + s));
+        }
+        ring.next();
     }
     // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
     mbar_wait(ws.bar(L::B_Q), 0u, ws.err);
@@ -266,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
     const KeyTiles kt(a, a.p0 + i0, a.p0 + min(i0 + T, rows) - 1, T);
     Cta<L::NB> c(base, L::OFF_BAR, a.err, L::B_SF, L::B_DS, -1);
     if (c.warp == kWarpTma) {
-        dq_tma<DP>(p, c.ws, base, kt, b, h, i0);
+        dq_tma<DP>(p, c.ws, base, kt, b, h, i0, len);
     } else if (c.warp == kWarpMma) {
-        dq_mma<DP>(p, c.ws, base, c.tb, kt, len);
+        dq_mma<DP>(p, c.ws, base, uniform(c.tb), (int)uniform(kt.total));
     } else {
         dq_elem<DP>(p, c.ws, c.tb, kt, b, h, i0, rows);
     }
@@ -283,7 +287,7 @@ struct LayK {
     static constexpr int OFF_K = 0, OFF_V = TILE, OFF_RING = 2 * TILE, OFF_ROW = OFF_RING + 2 * NS * TILE;
     static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * T * 4;  // lse and D of the queries, two stages
     static constexpr int B_K = 0, B_FQ = 1, B_FG = B_FQ + NS, B_EMPTY = B_FG + NS, B_S = B_EMPTY + NS, B_P = B_S + 1,
-                         B_DP = B_P + 1, B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, NB = B_FIN + 1;
+                         B_DP = B_P + 1, B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, B_RAW = B_FIN + 1, NB = B_RAW + 1;
     static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
     static constexpr uint32_t S = 0, DPC = T, DV = 2 * T, DK = 2 * T + DP;  // TMEM columns
 };
@@ -306,7 +310,6 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
     const uint32_t sa = tb + quad + L::S + half * 64, da = tb + quad + L::DPC + half * 64;
     float *rowv = reinterpret_cast<float *>(smem + L::OFF_ROW);  // [2 stages][-lse * log2e, -D][128]
     const float c = a.scale * kLog2e;
-    const unsigned long long c2 = pair2(c, c);
     bool ok = true;
     uint32_t ph = 0;
     auto fetch = [&](int it) {  // threads 0-127 lse, 128-255 D
@@ -338,12 +341,11 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(lse + 32 * k + e);
-                float u[4];
-                unpair2(fma2(pair2(P[k][e], P[k][e + 1]), c2, x.x), u[0], u[1]);
-                unpair2(fma2(pair2(P[k][e + 2], P[k][e + 3]), c2, x.y), u[2], u[3]);
-#pragma unroll
-                for (int f = 0; f < 4; ++f) P[k][e + f] = ex2_approx(u[f]);
+                const float4 x = *reinterpret_cast<const float4 *>(lse + 32 * k + e);
+                P[k][e] = ex2_approx(fmaf(P[k][e], c, x.x));
+                P[k][e + 1] = ex2_approx(fmaf(P[k][e + 1], c, x.y));
+                P[k][e + 2] = ex2_approx(fmaf(P[k][e + 2], c, x.z));
+                P[k][e + 3] = ex2_approx(fmaf(P[k][e + 3], c, x.w));
             }
         if (masked) {
 #pragma unroll
@@ -375,12 +377,10 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
             float pk[16];
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(D + 32 * k + 2 * e);
-                float u, w2, y, z;
-                unpair2(mul2(pair2(P[k][2 * e], P[k][2 * e + 1]), add2(pair2(v[k][2 * e], v[k][2 * e + 1]), x.x)), u, w2);
-                unpair2(mul2(pair2(P[k][2 * e + 2], P[k][2 * e + 3]), add2(pair2(v[k][2 * e + 2], v[k][2 * e + 3]), x.y)), y, z);
-                pk[e] = __uint_as_float(pack_bf16(u, w2));
-                pk[e + 1] = __uint_as_float(pack_bf16(y, z));
+                const float4 x = *reinterpret_cast<const float4 *>(D + 32 * k + 2 * e);
+                pk[e] = __uint_as_float(pack_bf16(P[k][2 * e] * (v[k][2 * e] + x.x), P[k][2 * e + 1] * (v[k][2 * e + 1] + x.y)));
+                pk[e + 1] = __uint_as_float(
+                    pack_bf16(P[k][2 * e + 2] * (v[k][2 * e + 2] + x.z), P[k][2 * e + 3] * (v[k][2 * e + 3] + x.w)));
             }
             tmem_st16(da + 16 * k, pk);
         }
@@ -429,45 +429,44 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
 }
 
 template <int DP>
-__device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Walk &w, int rows) {
+__device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, int N) {
     using L = LayK<DP>;
     const Args &a = p.a;
-    const int lane = threadIdx.x & 31, N = w.total;
     const uint32_t id_s = make_idesc(T, T, false, false);
     const uint32_t id_v = make_idesc(T, (a.dv + 15) & ~15, false, true), id_k = make_idesc(T, (a.d + 15) & ~15, false, true);
     const bool qk = a.d > 64, gv = a.dv > 64;
-    tb = uniform(tb);
-    auto tq = [&](int i) { return base + L::OFF_RING + (i % L::NS) * 2 * L::TILE; };
-    auto tg = [&](int i) { return tq(i) + L::TILE; };
-    auto par = [&](int i) { return (uint32_t)(i / L::NS) & 1u; };
-    // queries behind the sequence may be anything, and 0 times that is not 0 in dS^T Q, P^T dO
-    auto live = [&](int i) { return rows - w.tile(i) * T; };
-    auto do_s = [&](int i) {
-        if (!ws.wait(L::B_FQ + i % L::NS, par(i))) return false;
-        if (live(i) < T) zero_rows<DP>(tq(i), live(i), lane);
-        mma_kk<DP>(tb + L::S, base + L::OFF_K, tq(i), id_s, qk);
+    const uint64_t kd = kmajor(base + L::OFF_K), vd = kmajor(base + L::OFF_V), ring_k = kmajor(base + L::OFF_RING),
+                   ring_m = mnmajor(base + L::OFF_RING);
+    constexpr uint32_t STEP = L::TILE >> 4;  // a stage is Q and dO: two steps
+    Ring<L::NS> qs, gs;  // the stage that Q and dO are next taken from
+    auto do_s = [&]() {
+        if (!ws.wait(L::B_FQ + qs.slot, qs.phase)) return false;
+        mma_kk<DP>(tb + L::S, kd, ring_k + 2 * qs.slot * STEP, id_s, qk);
         umma_commit_warp(ws.bar(L::B_S));
+        qs.next();
         return true;
     };
-    auto do_dp = [&](int i) {
-        if (!ws.wait(L::B_FG + i % L::NS, par(i))) return false;
-        if (live(i) < T) zero_rows<DP>(tg(i), live(i), lane);
-        mma_kk<DP>(tb + L::DPC, base + L::OFF_V, tg(i), id_s, gv);
+    auto do_dp = [&]() {
+        if (!ws.wait(L::B_FG + gs.slot, gs.phase)) return false;
+        mma_kk<DP>(tb + L::DPC, vd, ring_k + (2 * gs.slot + 1) * STEP, id_s, gv);
         umma_commit_warp(ws.bar(L::B_DP));
+        gs.next();
         return true;
     };
-    bool ok = N == 0 || (ws.wait(L::B_K, 0u) && do_s(0) && do_dp(0));
+    bool ok = N == 0 || (ws.wait(L::B_K, 0u) && do_s() && do_dp());
+    uint32_t stage = 0;
     for (int i = 0; i < N && ok; ++i) {
         const uint32_t ph = (uint32_t)i & 1u;
         if (!(ok = ws.wait(L::B_P, ph))) break;
         tc_fence_after();
-        mma_ts(tb + L::DV, tb + L::S, tg(i), id_v, i > 0);
-        if (i + 1 < N && !(ok = do_s(i + 1))) break;
+        mma_ts(tb + L::DV, tb + L::S, ring_m + (2 * stage + 1) * STEP, id_v, i > 0);
+        if (i + 1 < N && !(ok = do_s())) break;
         if (!(ok = ws.wait(L::B_DS, ph))) break;
         tc_fence_after();
-        mma_ts(tb + L::DK, tb + L::DPC, tq(i), id_k, i > 0);
-        umma_commit_warp(ws.bar(L::B_EMPTY + i % L::NS));
-        if (i + 1 < N) ok = do_dp(i + 1);
+        mma_ts(tb + L::DK, tb + L::DPC, ring_m + 2 * stage * STEP, id_k, i > 0);
+        umma_commit_warp(ws.bar(L::B_EMPTY + stage));
+        if (i + 1 < N) ok = do_dp();
+        stage = stage + 1 == L::NS ? 0 : stage + 1;
     }
     if (ok) umma_commit_warp(ws.bar(L::B_O));
     umma_commit_warp(ws.bar(L::B_FIN));
@@ -476,28 +475,49 @@ __device__ __forceinline__ void dkv_mma(const Params &p, const Waits &ws, uint8_
 }
 
 template <int DP>
-__device__ __forceinline__ void dkv_tma(const Params &p, const Waits &ws, uint8_t *base, const Walk &w, int b, int hk, int j0) {
+__device__ __forceinline__ void dkv_tma(const Params &p, const Waits &ws, uint8_t *base, const Walk &w, int b, int hk, int j0,
+                                        int rows) {
     using L = LayK<DP>;
     const Args &a = p.a;
-    const bool one = (threadIdx.x & 31) == 0;
+    const int lane = threadIdx.x & 31;
     if (w.total == 0) return;
-    if (one) {
+    if (lane == 0) {
         mbar_expect_tx(ws.bar(L::B_K), 2 * L::TILE);
         load_tile<DP>(base + L::OFF_K, &p.mk, a.k, ws.bar(L::B_K), j0, hk, b);
         load_tile<DP>(base + L::OFF_V, &p.mv, a.v, ws.bar(L::B_K), j0, hk, b);
     }
+    Ring<L::NS> ring;
+    uint32_t raw = 0;
     int i = 0;
     for (; i < w.total; ++i) {
-        const int s = i % L::NS, use = i / L::NS, h = hk * a.G + w.head(i), i0 = w.tile(i) * T;
-        if (use > 0 && !ws.wait(L::B_EMPTY + s, (uint32_t)(use - 1) & 1u)) break;
-        if (one) {
-            uint8_t *d = base + L::OFF_RING + s * 2 * L::TILE;
-            mbar_expect_tx(ws.bar(L::B_FQ + s), L::TILE);
-            load_tile<DP>(d, &p.mq, a.q, ws.bar(L::B_FQ + s), i0, h, b);
-            mbar_expect_tx(ws.bar(L::B_FG + s), L::TILE);
-            load_tile<DP>(d + L::TILE, &p.mg, a.go, ws.bar(L::B_FG + s), i0, h, b);
+        const uint32_t s = ring.slot;
+        const int h = hk * a.G + w.head(i), i0 = w.tile(i) * T;
+        if (i >= L::NS && !ws.wait(L::B_EMPTY + s, ring.phase ^ 1u)) break;
+        uint8_t *d = base + L::OFF_RING + s * 2 * L::TILE;
+        const bool clean = rows - i0 < T;  // dS^T Q and P^T dO contract over the queries: zeros behind the sequence
+        const int fq = clean ? L::B_RAW : L::B_FQ + (int)s, fg = clean ? L::B_RAW : L::B_FG + (int)s;
+        if (lane == 0) {
+            if (clean) {
+                mbar_expect_tx(ws.bar(L::B_RAW), 2 * L::TILE);
+            } else {
+                mbar_expect_tx(ws.bar(fq), L::TILE);
+                mbar_expect_tx(ws.bar(fg), L::TILE);
+            }
+            load_tile<DP>(d, &p.mq, a.q, ws.bar(fq), i0, h, b);
+            load_tile<DP>(d + L::TILE, &p.mg, a.go, ws.bar(fg), i0, h, b);
         }
         __syncwarp();
+        if (clean) {
+            if (!ws.wait(L::B_RAW, raw)) break;
+            raw ^= 1u;
+            zero_rows<DP>(d, rows - i0, lane);
+            zero_rows<DP>(d + L::TILE, rows - i0, lane);
+            if (lane == 0) {
+                mbar_arrive(ws.bar(L::B_FQ + s));
+                mbar_arrive(ws.bar(L::B_FG + s));
+            }
+        }
+        ring.next();
     }
     mbar_wait(ws.bar(L::B_K), 0u, ws.err);
     for (int k = max(0, i - L::NS); k < i; ++k) {
@@ -534,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     w.total = w.each * a.G;
     Cta<L::NB> c(base, L::OFF_BAR, a.err, L::B_P, L::B_DS, -1);
     if (c.warp == kWarpTma) {
-        dkv_tma<DP>(p, c.ws, base, w, b, hk, j0);
+        dkv_tma<DP>(p, c.ws, base, w, b, hk, j0, rows);
     } else if (c.warp == kWarpMma) {
-        dkv_mma<DP>(p, c.ws, base, c.tb, w, rows);
+        dkv_mma<DP>(p, c.ws, base, uniform(c.tb), (int)uniform(w.total));
     } else {
         dkv_elem<DP>(p, c.ws, base, c.tb, w, b, hk, j0, len, rows, share, first && a.far > 0);
     }

@@ -22,9 +22,9 @@ namespace {
 
 using namespace tcw;
 
-// Registers per thread of the softmax warps and of the last warpgroup: 4 x 104 + 64 = 5 x 96,
-// the 96 that each of the 640 threads is launched with.
-constexpr int kThreads = 640, kWarpMma = 16, kWarpTma = 17, kRegsSoftmax = 104, kRegsOther = 64;
+// Registers per thread of the softmax warpgroups, which hold a row of S, and of the third
+// warpgroup: with the 168 that each of the 384 threads is launched with, 2 x 200 + 104 = 3 x 168.
+constexpr int kThreads = 384, kWarpMma = 8, kWarpTma = 10, kRegsSoftmax = 200, kRegsOther = 104;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kSlack = 8.f;
 
 struct Params {
@@ -32,18 +32,17 @@ struct Params {
     CUtensorMap mq, mk, mv;
     int pair_heads;  // the two tiles are two heads of a group (else two row tiles of a head)
     int items;
-    int wide_out;    // rows of o start at multiples of 32 bytes
 };
 
 template <int DP>
 struct Lay {
     static constexpr int TILE = T * DP * 2;
     static constexpr int NS = DP == 64 ? 8 : 4;  // ring slots
-    static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_ROW = OFF_RING + NS * TILE;
-    static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 2 * T * 4;  // [two uses in turn][tile][half][row]
-    // barriers of a query tile: Q landed, Q free, S ready, P ready, O ready, O read
+    static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_STAGE = OFF_RING + NS * TILE;  // 4 KB per softmax warp
+    static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
+    // barriers of a query tile: Q landed, Q free, S ready, halves of P ready, O ready, O read
     static constexpr int B_FULL = 0, B_EMPTY = B_FULL + NS, B_Q = B_EMPTY + NS, B_QE = B_Q + 2, B_S = B_QE + 2, B_P = B_S + 2,
-                         B_O = B_P + 2, B_OE = B_O + 2, B_FIN = B_OE + 2, NB = B_FIN + 1;
+                         B_O = B_P + 4, B_OE = B_O + 2, B_FIN = B_OE + 2, B_RAW = B_FIN + 2, NB = B_RAW + 1;
     static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
     static constexpr uint32_t S0 = 0, O0 = 2 * T;  // TMEM columns: S of both tiles, O of both
 };
@@ -66,7 +65,7 @@ struct Work {
         hk = h[0] / a.G;
         row[0] = rt * step;
         row[1] = p.pair_heads ? row[0] : row[0] + T;
-        len = length_of(a, b);
+        len = (int)uniform(length_of(a, b));
         rows = min(a.n, len - a.p0);
         sink_tiles = a.sinks > 0 ? (a.sinks - 1) / T + 1 : 0;
         int last = -1;
@@ -98,88 +97,69 @@ struct Work {
     }
 };
 
-// Barrier of the two warpgroups of query tile t.
-HLA_DEVICE void pair_sync(int t) {
-    if (t == 0)
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-    else
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-}
-
 template <int DP>
-__device__ __forceinline__ void softmax_role(const Params &p, const Waits &ws, uint8_t *smem, uint32_t tb, int t, int half) {
+__device__ __forceinline__ void softmax_role(const Params &p, const Waits &ws, uint8_t *smem, uint32_t tb, int t) {
     using L = Lay<DP>;
     const Args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t sa = tb + quad + L::S0 + t * T;         // S of the tile, P over it
     const uint32_t oa = tb + quad + L::O0 + t * DP;
-    float *rows_sm = reinterpret_cast<float *>(smem + L::OFF_ROW);
+    uint8_t *stage = smem + L::OFF_STAGE + warp * 4096;
     const float c = a.scale * kLog2e;
-    const unsigned long long c2 = pair2(c, c);
     const int dvp = (a.dv + 15) & ~15;
-    uint32_t phs = 0, pho = 0, turn = 0;
-    bool ok = true;
-    // x of this row's other half (every thread of the tile's two warpgroups calls this)
-    auto other_half = [&](float x) {
-        float *at = rows_sm + ((turn & 1) * 4 + t * 2) * T;
-        ++turn;
-        at[half * T + rr] = x;
-        pair_sync(t);
-        return at[(half ^ 1) * T + rr];
-    };
-    // After an expired wait the loops go on without their work, so that the barriers between
-    // the warpgroups stay matched; every further wait returns at once.
+    uint32_t phs = 0, pho = 0;
     for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
         const Work w(p, item);
         if (!(t ? w.on[1] : w.on[0])) continue;
         const int row0 = t ? w.row[1] : w.row[0], head = t ? w.h[1] : w.h[0];
         const int r = row0 + rr, pos = a.p0 + r, p_lo = a.p0 + row0, p_hi = p_lo + T - 1;
-        float m = -INFINITY, l = 0.f;  // reference maximum (base 2, scaled), sum of this half
+        float m = -INFINITY, l = 0.f;  // reference maximum (base 2, scaled), sum
         bool begun = false;
         for (int i = 0; i < w.total; ++i) {
             const int kt = w.key_tile(i);
             if (!w.active(t, kt)) continue;
-            const int j0 = kt * T, col = 64 * half;
+            const int j0 = kt * T, chunks = w.chunks(a, t, kt);
             const bool masked = !(j0 + T - 1 <= p_lo && (p_hi - j0 < a.window || j0 + T <= a.sinks));
             const int hi = pos - j0 + 1, sk = a.sinks - j0, lo = pos >= a.window ? pos - a.window + 1 - j0 : -1;
-            const int n = min(2, max(0, w.chunks(a, t, kt) - 2 * half));  // chunks of this half
-            ok = ok && ws.wait(L::B_S + t, phs);
+            if (!ws.wait(L::B_S + t, phs)) return;
             phs ^= 1u;
             tc_fence_after();
-            float s[2][32];
             float mx = -INFINITY;
-            if (ok && n == 2) {
-                tmem_ld32(sa + col, s[0]);
-                tmem_ld32(sa + col + 32, s[1]);
+            float s[4][32];
+            if (chunks == 4) {  // a whole tile is held in registers
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(sa + 32 * k, s[k]);
                 tmem_wait_ld();
                 if (masked) {
-                    mask32(s[0], visible_bits(col, lo, hi, sk), -INFINITY);
-                    mask32(s[1], visible_bits(col + 32, lo, hi, sk), -INFINITY);
-                }
-                float x[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
 #pragma unroll
-                for (int e = 2; e < 32; e += 2) {
-                    x[(e >> 1) & 1] = max3(x[(e >> 1) & 1], s[0][e], s[0][e + 1]);
-                    x[2 + ((e >> 1) & 1)] = max3(x[2 + ((e >> 1) & 1)], s[1][e], s[1][e + 1]);
+                    for (int k = 0; k < 4; ++k) mask32(s[k], visible_bits(32 * k, lo, hi, sk), -INFINITY);
                 }
-                mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            } else if (ok && n == 1) {
-                tmem_ld32(sa + col, s[0]);
-                tmem_wait_ld();
-                mask32(s[0], visible_bits(col, lo, hi, sk), -INFINITY);
+                float x[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mx = max3(mx, s[0][e], s[0][e + 1]);
+                for (int e = 1; e < 31; e += 2)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = max3(x[k], s[k][e], s[k][e + 1]);
+                mx = max3(max3(x[0], s[0][31], x[1]), max3(s[1][31], x[2], s[2][31]), fmaxf(x[3], s[3][31]));
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < chunks; ++k) {
+                    tmem_ld32(sa + 32 * k, s[0]);
+                    tmem_wait_ld();
+                    mask32(s[0], visible_bits(32 * k, lo, hi, sk), -INFINITY);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mx = max3(mx, s[0][e], s[0][e + 1]);
+                }
             }
-            mx = fmaxf(mx, other_half(mx)) * c;
+            mx *= c;
             const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
-            if (__any_sync(0xffffffffu, move)) {  // the same rows, and so the same vote, in both halves
+            if (__any_sync(0xffffffffu, move)) {
                 const float mn = move ? mx : m;
                 const float f = move ? ex2_approx(m - mn) : 1.f;
                 l *= f;
                 m = mn;
-                if (begun) {  // each half rescales every other 16 columns of O
-                    for (int k = 16 * half; k < dvp; k += 32) {
+                if (begun) {
+                    for (int k = 0; k < dvp; k += 16) {
                         float v[16];
                         tmem_ld16(oa + k, v);
                         tmem_wait_ld();
@@ -187,143 +167,165 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Waits &ws, u
                         for (int e = 0; e < 16; ++e) v[e] *= f;
                         tmem_st16(oa + k, v);
                     }
+                    tmem_wait_st();
                 }
             }
             begun = true;
             const float base = m == -INFINITY ? 0.f : m;
-            const unsigned long long b2 = pair2(-base, -base);
-            unsigned long long sum[2] = {0ull, 0ull};
-            auto probabilities = [&](const float(&v)[32], uint32_t to) {  // 32 columns of P
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            // 32 columns of P.  One operation at a time: as pairs (fma.rn.f32x2, add.rn.f32x2) they
+            // take as long in the pipe, and moves to form the pairs besides (5.1 cycles per
+            // element against 3.4)
+            auto probabilities = [&](const float(&v)[32], uint32_t to) {
                 float pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float x, y;
-                    unpair2(fma2(pair2(v[2 * e], v[2 * e + 1]), c2, b2), x, y);
-                    x = ex2_approx(x);
-                    y = ex2_approx(y);
-                    sum[e & 1] = add2(sum[e & 1], pair2(x, y));
+                    const float x = ex2_approx(fmaf(v[2 * e], c, -base)), y = ex2_approx(fmaf(v[2 * e + 1], c, -base));
+                    sum[e & 1] += x;
+                    sum[2 + (e & 1)] += y;
                     pk[e] = __uint_as_float(pack_bf16(x, y));
                 }
                 tmem_st16(to, pk);
             };
-            // P's half goes over the half of S it was made from (columns 0-31 and 64-95)
-            if (n >= 1) probabilities(s[0], sa + col);
-            if (n == 2) probabilities(s[1], sa + col + 16);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ws.bar(L::B_P + t));
-            float l0, l1;
-            unpair2(add2(sum[0], sum[1]), l0, l1);
-            l += l0 + l1;
+            auto hand_over = [&](int half) {  // half of P is there: its products can begin
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ws.bar(L::B_P + 2 * t + half));
+            };
+            if (chunks == 4) {
+                probabilities(s[0], sa);
+                probabilities(s[1], sa + 16);
+                hand_over(0);
+                probabilities(s[2], sa + 32);
+                probabilities(s[3], sa + 48);
+                hand_over(1);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < chunks; ++k) {
+                    tmem_ld32(sa + 32 * k, s[0]);
+                    tmem_wait_ld();
+                    mask32(s[0], visible_bits(32 * k, lo, hi, sk), -INFINITY);
+                    probabilities(s[0], sa + 16 * k);
+                }
+                hand_over(0);
+                hand_over(1);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        l += other_half(l);
-        ok = ok && ws.wait(L::B_O + t, pho);
+        if (!ws.wait(L::B_O + t, pho)) return;
         pho ^= 1u;
         tc_fence_after();
-        const bool live = r < w.rows && ok;
         const float inv = 1.f / l;
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o.p) + (size_t)w.b * a.o.sb + (size_t)head * a.o.sh + (size_t)r * a.o.st;
-        for (int k = 16 * half; k < dvp; k += 32) {
-            float v[16];
-            tmem_ld16(oa + k, v);
-            tmem_wait_ld();
-            uint32_t u[8];
+        // Through shared memory, so that a store writes whole rows: 64 columns of the warp's 32
+        // rows at a time, 16-byte pieces swizzled by the row (a row per thread straight from
+        // the registers touched 32 lines per store and took 4 us per item).
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o.p) + (size_t)w.b * a.o.sb + (size_t)head * a.o.sh +
+                           (size_t)(row0 + (warp & 3) * 32) * a.o.st;
+        const int live = w.rows - row0 - (warp & 3) * 32;  // rows of this warp inside the sequence
+#pragma unroll 1
+        for (int c0 = 0; c0 < a.dv; c0 += 64) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
-            if (live && p.wide_out && k + 16 <= a.dv) {  // a whole 32-byte sector
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + k), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                             "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                             : "memory");
-            } else if (live) {
-                *reinterpret_cast<uint4 *>(o + k) = make_uint4(u[0], u[1], u[2], u[3]);
-                if (k + 8 < a.dv) *reinterpret_cast<uint4 *>(o + k + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+            for (int g = 0; g < 2; ++g) {
+                float v[32];
+                tmem_ld32(oa + c0 + 32 * g, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 u;
+                    u.x = pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv);
+                    u.y = pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
+                    u.z = pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv);
+                    u.w = pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * g + e) ^ (lane & 7)) << 4)) = u;
+                }
+            }
+            __syncwarp();
+            const int col = c0 + 8 * (lane & 7);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 4 * e + (lane >> 3);
+                const uint4 u = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                if (row < live && col < a.dv) *reinterpret_cast<uint4 *>(o + (size_t)row * a.o.st + col) = u;
             }
             __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ws.bar(L::B_OE + t));
-        if (live && half == 0 && a.lse) a.lse[((size_t)w.b * a.H + head) * a.n + r] = (m + log2f(l)) * kLn2;
+        if (r < w.rows && a.lse) a.lse[((size_t)w.b * a.H + head) * a.n + r] = (m + log2f(l)) * kLn2;
     }
 }
 
+// The products of query tile t.
 template <int DP>
-__device__ __forceinline__ void mma_role(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb) {
+__device__ __forceinline__ void mma_role(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, int t) {
     using L = Lay<DP>;
     const Args &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const uint32_t id_o = make_idesc(T, (a.dv + 15) & ~15, false, true);
-    const bool wide = a.d > 64;
-    tb = uniform(tb);
-    uint32_t php[2] = {0, 0}, uses[2] = {0, 0};  // P's phase; items that used the tile
-    int ring = 0;                                // ring index of this item's first key tile
+    const uint32_t id_o = make_idesc(T, (a.dv + 15) & ~15, false, true), id_s = make_idesc(T, T, false, false);
+    const bool wide = DP > 64 && a.d > 64;
+    constexpr uint32_t STEP = L::TILE >> 4;
+    const uint64_t q_desc = kmajor(base + L::OFF_Q) + t * STEP, k_desc = kmajor(base + L::OFF_RING),
+                   v_desc = mnmajor(base + L::OFF_RING);
+    const uint32_t s = tb + L::S0 + t * T, o = tb + L::O0 + t * DP;
+    uint32_t php = 0, uses = 0;  // P's phase; items that used the tile
+    Ring<L::NS> ring;            // the next key tile's slot; its values' is the one behind
     bool ok = true;
-    auto slot = [&](int idx) { return base + L::OFF_RING + (idx % L::NS) * L::TILE; };
-    auto full = [&](int idx) { return ws.wait(L::B_FULL + idx % L::NS, (uint32_t)(idx / L::NS) & 1u); };
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
         const Work w(p, item);
-        bool pend[2] = {false, false}, begun[2] = {false, false}, q_here[2] = {false, false};
-        for (int i = 0; i <= w.total && ok; ++i) {  // the last round only finishes O
-            if (w.total == 0) break;
-            const int kt = i < w.total ? w.key_tile(i) : -1;
-            bool k_here = false, v_here = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (pend[t] && ok) {
-                    const int vi = ring + 2 * i - 1;
-                    if (!v_here) {
-                        ok = full(vi);
-                        v_here = true;
-                        // values behind the sequence may be anything, and 0 times that is not 0
-                        const int live = w.len - w.key_tile(i - 1) * T;
-                        if (ok && live < T) zero_rows<DP>(slot(vi), live, lane);
-                    }
-                    // O of the tile's last item has been read
-                    if (ok && !begun[t] && uses[t] > 0) ok = ws.wait(L::B_OE + t, (uses[t] - 1) & 1u);
-                    if (ok) ok = ws.wait(L::B_P + t, php[t]);
-                    if (!ok) break;
-                    php[t] ^= 1u;
-                    tc_fence_after();
-                    const int chunks = uniform(w.chunks(a, t, w.key_tile(i - 1)));
-                    const uint64_t dv = make_sdesc(smem_u32(slot(vi)), T * 128u, 1024u);
-                    const uint32_t o = tb + L::O0 + t * DP, s = tb + L::S0 + t * T;
-                    mma_ts32(o, s, dv, id_o, begun[t]);
-                    if (chunks > 1) mma_ts32(o, s + 16, dv + 256, id_o, true);
-                    if (chunks > 2) mma_ts32(o, s + 64, dv + 512, id_o, true);
-                    if (chunks > 3) mma_ts32(o, s + 80, dv + 768, id_o, true);
-                    begun[t] = true;
-                    pend[t] = false;
-                    if (i == w.total || kt > (t ? w.hi[1] : w.hi[0])) {
-                        umma_commit_warp(ws.bar(L::B_O + t));
-                        ++uses[t];
-                    }
-                }
-                if (i < w.total && ok && w.active(t, kt)) {
-                    if (!k_here) {
-                        ok = full(ring + 2 * i);
-                        k_here = true;
-                    }
-                    if (ok && !q_here[t]) {
-                        ok = ws.wait(L::B_Q + t, uses[t] & 1u);
-                        q_here[t] = true;
-                    }
-                    if (!ok) break;
-                    mma_kk<DP>(tb + L::S0 + t * T, base + L::OFF_Q + t * L::TILE, slot(ring + 2 * i),
-                               make_idesc(T, 32 * uniform(w.chunks(a, t, kt)), false, false), wide);
-                    umma_commit_warp(ws.bar(L::B_S + t));
-                    pend[t] = true;
-                    if (kt == (t ? w.hi[1] : w.hi[0])) umma_commit_warp(ws.bar(L::B_QE + t));
-                }
+        const int hi = t ? w.hi[1] : w.hi[0];
+        int chunks = 0;  // of the S that the next P comes from; 0: none
+        bool begun = false, q_here = false;
+        uint32_t v_slot = 0, v_phase = 0;
+        for (int i = 0; i <= w.total && w.total > 0; ++i) {  // the last round only finishes O
+            const int kt = i < w.total ? w.key_tile(i) : 0x7fffffff;
+            const int next = w.active(t, kt) ? w.chunks(a, t, kt) : 0;
+            const uint32_t k_slot = ring.slot, k_phase = ring.phase;
+            const uint64_t kd = k_desc + k_slot * STEP, vd = v_desc + v_slot * STEP;
+            const uint32_t id = next == 4 ? id_s : make_idesc(T, 32 * next, false, false);
+            // every tile's arrival is waited for, used or not: its slot is released below
+            if (i > 0 && !(ok = ws.wait(L::B_FULL + v_slot, v_phase))) break;
+            if (i < w.total && !(ok = ws.wait(L::B_FULL + k_slot, k_phase))) break;
+            if (next > 0 && !q_here) {
+                if (!(ok = ws.wait(L::B_Q + t, uses & 1u))) break;
+                q_here = true;
             }
-            if (!ok) break;
-            if (i > 0) umma_commit_warp(ws.bar(L::B_EMPTY + (ring + 2 * i - 1) % L::NS));
-            if (i < w.total) umma_commit_warp(ws.bar(L::B_EMPTY + (ring + 2 * i) % L::NS));
+            if (chunks > 0) {
+                // before the first product: O of the tile's last item has been read
+                if (!begun && uses > 0 && !(ok = ws.wait(L::B_OE + t, (uses - 1) & 1u))) break;
+                if (!(ok = ws.wait(L::B_P + 2 * t, php))) break;
+                tc_fence_after();
+                mma_ts32(o, s, vd, id_o, begun);
+                if (chunks > 1) mma_ts32(o, s + 16, vd + 256, id_o, true);
+                if (!(ok = ws.wait(L::B_P + 2 * t + 1, php))) break;
+                tc_fence_after();
+                if (chunks > 2) mma_ts32(o, s + 32, vd + 512, id_o, true);
+                if (chunks > 3) mma_ts32(o, s + 48, vd + 768, id_o, true);
+                php ^= 1u;
+                begun = true;
+            }
+            if (next > 0) {
+                mma_kk<DP>(s, q_desc, kd, id, wide);
+                umma_commit_warp(ws.bar(L::B_S + t));
+                if (kt == hi) umma_commit_warp(ws.bar(L::B_QE + t));
+            }
+            if (chunks > 0 && kt > hi) {
+                umma_commit_warp(ws.bar(L::B_O + t));
+                ++uses;
+            }
+            chunks = next;
+            if (i > 0) umma_commit_warp(ws.bar(L::B_EMPTY + v_slot));
+            if (i < w.total) {
+                umma_commit_warp(ws.bar(L::B_EMPTY + k_slot));
+                ring.next();
+                v_slot = ring.slot;
+                v_phase = ring.phase;
+                ring.next();
+            }
         }
-        ring += 2 * w.total;
     }
-    umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
-    mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
+    umma_commit_warp(ws.bar(L::B_FIN + t));  // every MMA issued completes before TMEM is released
+    mbar_wait(ws.bar(L::B_FIN + t), 0u, ws.err);
     __syncwarp();
 }
 
@@ -332,21 +334,32 @@ __device__ __forceinline__ void tma_role(const Params &p, const Waits &ws, uint8
     using L = Lay<DP>;
     const Args &a = p.a;
     const bool one = (threadIdx.x & 31) == 0;
-    uint32_t uses[2] = {0, 0};
-    int idx = 0;
+    uint32_t uses[2] = {0, 0}, raw = 0;
+    Ring<L::NS> ring;
+    int loads = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
         const Work w(p, item);
-        for (int i = 0; i < 2 * w.total && ok; ++i, ++idx) {
-            const int s = idx % L::NS, use = idx / L::NS;
-            if (use > 0 && !(ok = ws.wait(L::B_EMPTY + s, (uint32_t)(use - 1) & 1u))) break;
+        for (int i = 0; i < 2 * w.total && ok; ++i) {
+            const uint32_t s = ring.slot;
+            if (loads >= L::NS && !(ok = ws.wait(L::B_EMPTY + s, ring.phase ^ 1u))) break;
+            const bool key = (i & 1) == 0;
+            const int kt = w.key_tile(i >> 1), live = w.len - kt * T;
+            const bool clean = !key && live < T;  // values behind the sequence: zeros before the MMAs see them
+            const int full = clean ? L::B_RAW : L::B_FULL + (int)s;
             if (one) {
-                mbar_expect_tx(ws.bar(L::B_FULL + s), L::TILE);
-                const bool key = (i & 1) == 0;
-                load_tile<DP>(base + L::OFF_RING + s * L::TILE, key ? &p.mk : &p.mv, key ? a.k : a.v, ws.bar(L::B_FULL + s),
-                              w.key_tile(i >> 1) * T, w.hk, w.b);
+                mbar_expect_tx(ws.bar(full), L::TILE);
+                load_tile<DP>(base + L::OFF_RING + s * L::TILE, key ? &p.mk : &p.mv, key ? a.k : a.v, ws.bar(full), kt * T, w.hk, w.b);
             }
             __syncwarp();
+            if (clean) {
+                if (!(ok = ws.wait(L::B_RAW, raw))) break;
+                raw ^= 1u;
+                zero_rows<DP>(base + L::OFF_RING + s * L::TILE, live, threadIdx.x & 31);
+                if (one) mbar_arrive(ws.bar(L::B_FULL + s));
+            }
+            ring.next();
+            ++loads;
             if (i > 0) continue;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {  // behind the first key tile, which needs no wait for the last item's Q
@@ -364,7 +377,7 @@ __device__ __forceinline__ void tma_role(const Params &p, const Waits &ws, uint8
     // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
     for (int t = 0; t < 2; ++t)
         if (uses[t] > 0) mbar_wait(ws.bar(L::B_Q + t), (uses[t] - 1) & 1u, ws.err);
-    for (int k = max(0, idx - L::NS); k < idx; ++k)
+    for (int k = max(0, loads - L::NS); k < loads; ++k)
         mbar_wait(ws.bar(L::B_FULL + k % L::NS), (uint32_t)(k / L::NS) & 1u, ws.err);
     __syncwarp();
 }
@@ -380,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     if (threadIdx.x == 0) {
         misc[1] = 0u;
         for (int i = 0; i < L::NB; ++i)
-            mbar_init(ws.bar(i), (i >= L::B_P && i < L::B_P + 2) || (i >= L::B_OE && i < L::B_OE + 2) ? 8 : 1);
+            mbar_init(ws.bar(i), (i >= L::B_P && i < L::B_P + 4) || (i >= L::B_OE && i < L::B_OE + 2) ? 4
+                                 : i >= L::B_EMPTY && i < L::B_EMPTY + L::NS                           ? 2
+                                                                                                       : 1);
         fence_mbar_init();
         tma_prefetch_desc(&p.mq);
         tma_prefetch_desc(&p.mk);
@@ -397,10 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     if (warp >= kWarpMma) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kWarpTma) tma_role<DP>(p, ws, base);
-        if (warp == kWarpMma) mma_role<DP>(p, ws, base, tb);
+        if (warp == kWarpMma) mma_role<DP>(p, ws, base, uniform(tb), 0);
+        if (warp == kWarpMma + 1) mma_role<DP>(p, ws, base, uniform(tb), 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_role<DP>(p, ws, base, tb, warp >> 3, (warp >> 2) & 1);
+        softmax_role<DP>(p, ws, base, tb, warp >> 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -441,7 +457,6 @@ cudaError_t fwd_tc(const Args &a, cudaStream_t st) {
     // two heads of one group see the same keys; with an odd group two row tiles of one head
     // share most of theirs
     p.pair_heads = a.G % 2 == 0;
-    p.wide_out = reinterpret_cast<uintptr_t>(a.o.p) % 32 == 0 && a.o.sb % 16 == 0 && a.o.sh % 16 == 0 && a.o.st % 16 == 0;
     return a.d <= 64 && a.dv <= 64 ? launch<64>(p, st) : launch<128>(p, st);
 }
 

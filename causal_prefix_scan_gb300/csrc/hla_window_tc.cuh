@@ -52,34 +52,42 @@ HLA_DEVICE void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Bounded, warp-uniform waits: a poll sleeps in hardware until the phase completes; the
-// CTA's abort flag or the time limit end it (the latter raises the device status word).
+// Bounded, warp-uniform waits: a poll sleeps in hardware until the phase
+// completes or its time is up; the CTA's abort flag or a number of polls (2 s) end the wait,
+// and the latter raises the device status word.
 struct Waits {
     uint64_t *bars;
     volatile int *abort_p;
     unsigned *err;
     HLA_DEVICE uint64_t *bar(int i) const { return bars + i; }
     HLA_DEVICE bool wait(int b, uint32_t parity) const {
-        bool ok = mbar_try_wait(bars + b, parity);
-        if (!ok) ok = slow(b, parity);
-        return __all_sync(0xffffffffu, ok);
-    }
-    HLA_DEVICE bool slow(int b, uint32_t parity) const {
-        const uint64_t t0 = globaltimer_ns();
-        while (!*abort_p) {
-            if (mbar_try_wait(bars + b, parity)) return true;
-            if (globaltimer_ns() - t0 > (uint64_t)kWaitLimitUs * 1000u) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bars + b, parity))) return true;
+        for (int polls = 0; !*abort_p; ++polls) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bars + b, parity))) return true;
+            if (polls == 2000) {
                 atomicOr(err, DEV_TIMEOUT);
                 *abort_p = 1;
             }
+            __syncwarp();
         }
         return false;
     }
 };
+// Slot and phase of a ring of NS slots, counted up use by use.
+template <int NS>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    HLA_DEVICE void next() {
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
-// ---- MMA groups, issued by a whole warp with warp-uniform operands: one lane is elected for a
-// group, and a group is one block of instructions (issued one by one from a loop, they took
-// longer to issue than to run).
+// ---- MMA groups, issued by a whole warp in uniform control flow with uniform operands: one
+// lane is elected for a group.  The operands then stay in uniform registers (17 cycles per
+// instruction against 45 when one thread issues them); a group is one block of instructions.
 // D [128 x N] (+)= A B^T over 64 contraction columns: both K-major tiles
 HLA_DEVICE void mma_ss64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
@@ -97,60 +105,31 @@ HLA_DEVICE void mma_ss64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, boo
 // D [128 x N] (+)= A B over 32 contraction rows of B: A packed bf16 in TMEM (16 columns), B MN-major
 HLA_DEVICE void mma_ts32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p, e, t;\n .reg .b64 b1;\n .reg .b32 a1;\n"
-        " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-        " add.s64 b1, %2, 128;\n add.u32 a1, %1, 8;\n"
+        "{\n .reg .pred p, e, t;\n .reg .b64 b1;\n .reg .b32 a1;\n elect.sync _|e, 0xffffffff;\n"
+        " setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n add.s64 b1, %2, 128;\n add.u32 a1, %1, 8;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
 }
-// The whole width of two tiles of 128 rows (64 columns per block; zero columns behind the
-// tensors' own are multiplied too): `wide` takes both blocks of DP = 128.
-template <int DP>
-HLA_DEVICE void mma_kk(uint32_t d, const uint8_t *a, const uint8_t *b, uint32_t idesc, bool wide) {
-    const uint64_t da = make_sdesc(smem_u32(a), 16u, 1024u), db = make_sdesc(smem_u32(b), 16u, 1024u);
-    mma_ss64(d, da, db, idesc, false);
-    if (DP > 64 && wide) mma_ss64(d, da + T * 8, db + T * 8, idesc, true);
-}
-// 64 contraction rows from row r0 of an MN-major tile, A in TMEM
-HLA_DEVICE void mma_tm64(uint32_t d, uint32_t a, const uint8_t *b, int r0, uint32_t idesc, bool acc) {
-    const uint64_t db = make_sdesc(smem_u32(b) + (uint32_t)r0 * 128u, T * 128u, 1024u);
-    mma_ts32(d, a, db, idesc, acc);
-    mma_ts32(d, a + 16, db + 256, idesc, true);
-}
 // A warp-uniform value, known as such to the compiler.
 HLA_DEVICE uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+// Descriptors of a tile of 128 rows: contraction over its columns, or over its rows.
+HLA_DEVICE uint64_t kmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), 16u, 1024u); }
+HLA_DEVICE uint64_t mnmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), T * 128u, 1024u); }
+// The whole width of two tiles (64 columns per block; zero columns behind the tensors' own are
+// multiplied too): `wide` takes both blocks of DP = 128.
+template <int DP>
+HLA_DEVICE void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool wide) {
+    mma_ss64(d, a, b, idesc, false);
+    if (DP > 64 && wide) mma_ss64(d, a + T * 8, b + T * 8, idesc, true);
+}
 
 // 32 columns of 32-bit words, this warp's lanes.
 HLA_DEVICE void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
                  : "r"(taddr));
-}
-// Two fp32 operations in one instruction.
-HLA_DEVICE unsigned long long pair2(float a, float b) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-HLA_DEVICE void unpair2(unsigned long long r, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-HLA_DEVICE unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-HLA_DEVICE unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-HLA_DEVICE unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 HLA_DEVICE float max3(float a, float b, float c) {
     float r;
@@ -169,7 +148,8 @@ HLA_DEVICE void mask32(float (&v)[32], uint32_t bits, float other) {
     for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : other;
 }
 
-// Zeroes rows [r0, 128) of a tile (one warp) and shows the tensor cores the result.
+// Zeroes rows [r0, 128) of a tile (one warp) and shows the tensor cores the result: rows behind
+// a sequence may be anything, and 0 times that is not 0 where they are contracted over.
 template <int DP>
 HLA_DEVICE void zero_rows(uint8_t *tile, int r0, int lane) {
 #pragma unroll
