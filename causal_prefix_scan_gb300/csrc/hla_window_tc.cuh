@@ -114,15 +114,15 @@ HLA_DEVICE void mma_ts32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, boo
 }
 // A warp-uniform value, known as such to the compiler.
 HLA_DEVICE uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-// Descriptors of a tile of 128 rows: contraction over its columns, or over its rows.
+// Descriptors of a tile: contraction over its columns, or over its rows.
 HLA_DEVICE uint64_t kmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), 16u, 1024u); }
-HLA_DEVICE uint64_t mnmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), T * 128u, 1024u); }
-// The whole width of two tiles (64 columns per block; zero columns behind the tensors' own are
-// multiplied too): `wide` takes both blocks of DP = 128.
-template <int DP>
+HLA_DEVICE uint64_t mnmajor(const uint8_t *tile, int rows = T) { return make_sdesc(smem_u32(tile), rows * 128u, 1024u); }
+// The whole width of two tiles, of T and RB rows (64 columns per block; zero columns behind the
+// tensors' own are multiplied too): `wide` takes both blocks of DP = 128.
+template <int DP, int RB = T>
 HLA_DEVICE void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool wide) {
     mma_ss64(d, a, b, idesc, false);
-    if (DP > 64 && wide) mma_ss64(d, a + T * 8, b + T * 8, idesc, true);
+    if (DP > 64 && wide) mma_ss64(d, a + T * 8, b + RB * 8, idesc, true);
 }
 
 // 32 columns of 32-bit words, this warp's lanes.
@@ -148,14 +148,14 @@ HLA_DEVICE void mask32(float (&v)[32], uint32_t bits, float other) {
     for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : other;
 }
 
-// Zeroes rows [r0, 128) of a tile (one warp) and shows the tensor cores the result: rows behind
+// Zeroes rows [r0, ROWS) of a tile (one warp) and shows the tensor cores the result: rows behind
 // a sequence may be anything, and 0 times that is not 0 where they are contracted over.
-template <int DP>
+template <int DP, int ROWS = T>
 HLA_DEVICE void zero_rows(uint8_t *tile, int r0, int lane) {
 #pragma unroll
     for (int c = 0; c < DP; c += 64)
-        for (int e = (r0 << 3) + lane; e < T * 8; e += 32)
-            reinterpret_cast<uint4 *>(tile + (c >> 6) * T * 128)[e] = make_uint4(0, 0, 0, 0);
+        for (int e = (r0 << 3) + lane; e < ROWS * 8; e += 32)
+            reinterpret_cast<uint4 *>(tile + (c >> 6) * ROWS * 128)[e] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
 }
