@@ -3,7 +3,7 @@
 // With P = exp(scale S - lse), S = Q K^T, dP = dO V^T, D = rowsum(dO o):
 //   dS = P (dP - D),   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO.
 // Two kernels, neither of which adds to memory that another CTA adds to, so every sum has a
-// fixed order: dq over tiles of 128 queries (walking the keys they see; also writes D) and dkv
+// fixed order: dq over tiles of 128 queries (walking the keys they see; also forms D) and dkv
 // over tiles of 128 keys (walking the queries that see them, all heads of the group).  S and
 // dP are formed in both: 7 products per pair of tiles instead of 5, in exchange for no
 // atomics and no fp32 buffer of dQ the size of Q.
@@ -28,7 +28,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
     Args a;
-    CUtensorMap mq, mk, mv, mg;
+    CUtensorMap mq, mk, mv, mg, mo;
 };
 
 HLA_DEVICE void elem_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -82,16 +82,17 @@ template <int DP>
 struct LayQ {
     static constexpr int TILE = T * DP * 2;
     static constexpr int NS = DP == 64 ? 8 : 4;  // ring slots, K and V tiles in turn
-    static constexpr int OFF_Q = 0, OFF_G = TILE, OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NS * TILE;
-    static constexpr int B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_SF = B_S + 1, B_DP = B_SF + 1,
+    static constexpr int OFF_Q = 0, OFF_G = TILE, OFF_O = 2 * TILE, OFF_RING = 3 * TILE, OFF_BAR = OFF_RING + NS * TILE;
+    static_assert(3 * TILE >= 8 * 4096, "the results leave through the inputs' tiles");
+    static constexpr int B_Q = 0, B_GO = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_SF = B_S + 1, B_DP = B_SF + 1,
                          B_DS = B_DP + 1, B_O = B_DS + 1, B_FIN = B_O + 1, B_RAW = B_FIN + 1, NB = B_RAW + 1;
     static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
     static constexpr uint32_t S = 0, DPC = T, DQ = 2 * T;  // TMEM columns
 };
 
 template <int DP>
-__device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32_t tb, const KeyTiles &kt, int b, int h,
-                                        int i0, int rows) {
+__device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const KeyTiles &kt,
+                                        int b, int h, int i0, int rows) {
     using L = LayQ<DP>;
     const Args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
@@ -100,8 +101,18 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t sa = tb + quad + L::S + half * 64, da = tb + quad + L::DPC + half * 64;
     const size_t row = ((size_t)b * a.H + h) * a.n + r;
-    const float c = a.scale * kLog2e, base = live ? a.lse[row] * kLog2e : 0.f;
-    const float D = live ? a.delta[row] : 0.f;
+    const float c = a.scale * kLog2e, lse = live ? a.lse[row] * kLog2e : 0.f;
+    // D = rowsum(dO o) of the thread's row, also for the dkv kernel
+    if (!ws.wait(L::B_GO, 0u)) return;
+    float D = 0.f;
+    for (int k = 0; k < ((a.dv + 7) & ~7); k += 8) {
+        float x[8], y[8];
+        tile_load_row8(base + L::OFF_G, T, (warp & 3) * 32 + lane, k, x);
+        tile_load_row8(base + L::OFF_O, T, (warp & 3) * 32 + lane, k, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) D = fmaf(x[e], y[e], D);
+    }
+    if (live && half == 0) a.delta[row] = D;
     bool ok = true;
     uint32_t ph = 0;
     for (int it = 0; it < kt.total; ++it, ph ^= 1u) {
@@ -122,7 +133,7 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) P[k][e] = ex2_approx(fmaf(P[k][e], c, -base));
+            for (int e = 0; e < 32; ++e) P[k][e] = ex2_approx(fmaf(P[k][e], c, -lse));
         if (masked) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) mask32(P[k], bits[k], 0.f);
@@ -153,21 +164,9 @@ __device__ __forceinline__ void dq_elem(const Params &p, const Waits &ws, uint32
     }
     if (!ok || !ws.wait(L::B_O, 0u)) return;
     tc_fence_after();
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.dq.p) + (size_t)b * a.dq.sb + (size_t)h * a.dq.sh + (size_t)r * a.dq.st;
-    const int dpad = (a.d + 15) & ~15;
-    for (int k = half * 16; k < dpad; k += 32) {
-        float x[16];
-        tmem_ld16(tb + quad + L::DQ + k, x);
-        tmem_wait_ld();
-        uint4 u[2];
-        uint32_t *w = reinterpret_cast<uint32_t *>(u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(x[2 * e] * a.scale, x[2 * e + 1] * a.scale);
-        if (live) {
-            *reinterpret_cast<uint4 *>(o + k) = u[0];
-            if (k + 8 < a.d) *reinterpret_cast<uint4 *>(o + k + 8) = u[1];
-        }
-    }
+    const int r0 = i0 + (warp & 3) * 32;  // every product is done: the inputs' tiles are free
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.dq.p) + (size_t)b * a.dq.sb + (size_t)h * a.dq.sh + (size_t)r0 * a.dq.st;
+    store_rows<DP / 2>(base + warp * 4096, tb + quad + L::DQ + DP / 2 * half, a.scale, o, a.dq.st, rows - r0, DP / 2 * half, a.d);
 }
 
 template <int DP>
@@ -197,7 +196,7 @@ __device__ __forceinline__ void dq_mma(const Params &p, const Waits &ws, uint8_t
         ring.next();
         return true;
     };
-    bool ok = ws.wait(L::B_Q, 0u) && do_s() && do_dp();
+    bool ok = ws.wait(L::B_Q, 0u) && do_s() && ws.wait(L::B_GO, 0u) && do_dp();
     for (int j = 0; j < N && ok; ++j) {
         const uint32_t ph = (uint32_t)j & 1u, slot = k_slot;
         if (j + 1 < N) {
@@ -224,9 +223,11 @@ __device__ __forceinline__ void dq_tma(const Params &p, const Waits &ws, uint8_t
     const Args &a = p.a;
     const int lane = threadIdx.x & 31, hk = h / a.G;
     if (lane == 0) {
-        mbar_expect_tx(ws.bar(L::B_Q), 2 * L::TILE);
+        mbar_expect_tx(ws.bar(L::B_Q), L::TILE);
         load_tile<DP>(base + L::OFF_Q, &p.mq, a.q, ws.bar(L::B_Q), i0, h, b);
-        load_tile<DP>(base + L::OFF_G, &p.mg, a.go, ws.bar(L::B_Q), i0, h, b);
+        mbar_expect_tx(ws.bar(L::B_GO), 2 * L::TILE);
+        load_tile<DP>(base + L::OFF_G, &p.mg, a.go, ws.bar(L::B_GO), i0, h, b);
+        load_tile<DP>(base + L::OFF_O, &p.mo, a.o, ws.bar(L::B_GO), i0, h, b);
     }
     Ring<L::NS> ring;
     uint32_t raw = 0;
@@ -253,6 +254,7 @@ __device__ __forceinline__ void dq_tma(const Params &p, const Waits &ws, uint8_t
     }
     // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
     mbar_wait(ws.bar(L::B_Q), 0u, ws.err);
+    mbar_wait(ws.bar(L::B_GO), 0u, ws.err);
     for (int k = max(0, idx - L::NS); k < idx; ++k)
         mbar_wait(ws.bar(L::B_FULL + k % L::NS), (uint32_t)(k / L::NS) & 1u, ws.err);
     __syncwarp();
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
     } else if (c.warp == kWarpMma) {
         dq_mma<DP>(p, c.ws, base, uniform(c.tb), (int)uniform(kt.total));
     } else {
-        dq_elem<DP>(p, c.ws, c.tb, kt, b, h, i0, rows);
+        dq_elem<DP>(p, c.ws, base, c.tb, kt, b, h, i0, rows);
     }
     c.finish();
 }
@@ -400,31 +402,33 @@ __device__ __forceinline__ void dkv_elem(const Params &p, const Waits &ws, uint8
     const float f = key ? a.scale : 1.f;
     const View &out = key ? a.dk : a.dv_;
     const bool live = j < len;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out.p) + (size_t)b * out.sb + (size_t)hk * out.sh + (size_t)j * out.st;
-    float *part = a.part + (((size_t)share * a.B * a.Hkv + (size_t)b * a.Hkv + hk) * a.far_keys + j) * (a.d + a.dv) + (key ? 0 : a.d);
-    for (int k = 0; k < ((width + 15) & ~15); k += 16) {
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
-        if (w.total > 0) {
-            tmem_ld16(tb + quad + (key ? L::DK : L::DV) + k, x);
+    const uint32_t acc = tb + quad + (key ? L::DK : L::DV);
+    if (split) {
+        float *part = a.part + (((size_t)share * a.B * a.Hkv + (size_t)b * a.Hkv + hk) * a.far_keys + j) * (a.d + a.dv) + (key ? 0 : a.d);
+        for (int k = 0; k < ((width + 15) & ~15); k += 16) {
+            float x[16];
+            tmem_ld16(acc + k, x);
             tmem_wait_ld();
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    if (k + e < width)
+                        *reinterpret_cast<float4 *>(part + k + e) =
+                            w.total > 0 ? make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            __syncwarp();
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= f;
-        if (live && split) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                if (k + e < width) *reinterpret_cast<float4 *>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        } else if (live) {
-            uint4 u[2];
-            uint32_t *y = reinterpret_cast<uint32_t *>(u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-            *reinterpret_cast<uint4 *>(o + k) = u[0];
-            if (k + 8 < width) *reinterpret_cast<uint4 *>(o + k + 8) = u[1];
+        return;
+    }
+    const int r0 = j0 + (warp & 3) * 32;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out.p) + (size_t)b * out.sb + (size_t)hk * out.sh + (size_t)r0 * out.st;
+    if (w.total > 0) {  // every product is done: the keys' and values' tiles are free
+        for (int c0 = 0; c0 < width; c0 += 64) store_rows<64>(smem + warp * 4096, acc + c0, f, o, out.st, len - r0, c0, width);
+    } else {  // no query sees these keys
+        for (int e = lane; e < 32 * (width / 8); e += 32) {
+            const int row = e / (width / 8), col = e % (width / 8) * 8;
+            if (r0 + row < len) *reinterpret_cast<uint4 *>(o + (size_t)row * out.st + col) = make_uint4(0, 0, 0, 0);
         }
-        __syncwarp();
     }
 }
 
@@ -563,32 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     c.finish();
 }
 
-// D = rowsum(do o): 16 lanes per row, 8 columns per lane.
-__global__ void __launch_bounds__(256) window_delta_kernel(const Args a) {
-    const size_t row = (size_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int c = (threadIdx.x & 15) * 8;
-    if (row >= (size_t)a.B * a.H * a.n) return;  // a warp's two rows may differ: no full-warp shuffle below
-    const int i = (int)(row % a.n), h = (int)(row / a.n % a.H), b = (int)(row / a.n / a.H);
-    const bool live = a.p0 + i < length_of(a, b);
-    float s = 0.f;
-    if (live && c < a.dv) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o.p) + (size_t)b * a.o.sb +
-                                                         (size_t)h * a.o.sh + (size_t)i * a.o.st + c);
-        const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.go.p) + (size_t)b * a.go.sb +
-                                                         (size_t)h * a.go.sh + (size_t)i * a.go.st + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-            s = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), s);
-        }
-    }
-    const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-    for (int k = 8; k > 0; k >>= 1) s += __shfl_xor_sync(mask, s, k);
-    if (live && c == 0) a.delta[row] = s;
-}
-
 template <int DP>
 cudaError_t launch(Params &p, cudaStream_t st) {
     using Q = LayQ<DP>;
@@ -596,15 +574,13 @@ cudaError_t launch(Params &p, cudaStream_t st) {
     static_assert(Q::SMEM <= 227 * 1024 && K::SMEM <= 227 * 1024, "shared memory");
     const Args &a = p.a;
     if (!encode(&p.mq, a.q, a.d, a.n, a.H, a.B, T) || !encode(&p.mk, a.k, a.d, a.nk, a.Hkv, a.B, T) ||
-        !encode(&p.mv, a.v, a.dv, a.nk, a.Hkv, a.B, T) || !encode(&p.mg, a.go, a.dv, a.n, a.H, a.B, T))
+        !encode(&p.mv, a.v, a.dv, a.nk, a.Hkv, a.B, T) || !encode(&p.mg, a.go, a.dv, a.n, a.H, a.B, T) ||
+        !encode(&p.mo, a.o, a.dv, a.n, a.H, a.B, T))
         return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(window_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
     if (e != cudaSuccess) return e;
-    const size_t rows = (size_t)a.B * a.H * a.n;
-    window_delta_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     window_dq_kernel<DP><<<(unsigned)((size_t)a.B * a.H * ((a.n + T - 1) / T)), kThreads, Q::SMEM, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     window_dkv_kernel<DP><<<dim3((unsigned)((size_t)a.B * a.Hkv * ((a.nk + T - 1) / T)), a.far + 1), kThreads, K::SMEM, st>>>(p);
@@ -618,7 +594,7 @@ bool rows16(const View &v) {
 }  // namespace
 
 bool bwd_tc_takes(const Args &a) {
-    return a.d % 8 == 0 && a.dv % 8 == 0 && mappable(a.q) && mappable(a.k) && mappable(a.v) && mappable(a.go) && rows16(a.o) &&
+    return a.d % 8 == 0 && a.dv % 8 == 0 && mappable(a.q) && mappable(a.k) && mappable(a.v) && mappable(a.go) && mappable(a.o) &&
            rows16(a.dq) && rows16(a.dk) && rows16(a.dv_);
 }
 

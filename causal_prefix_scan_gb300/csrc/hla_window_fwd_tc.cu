@@ -213,39 +213,11 @@ __device__ __forceinline__ void softmax_role(const Params &p, const Waits &ws, u
         pho ^= 1u;
         tc_fence_after();
         const float inv = 1.f / l;
-        // Through shared memory, so that a store writes whole rows: 64 columns of the warp's 32
-        // rows at a time, 16-byte pieces swizzled by the row (a row per thread straight from
-        // the registers touched 32 lines per store and took 4 us per item).
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o.p) + (size_t)w.b * a.o.sb + (size_t)head * a.o.sh +
                            (size_t)(row0 + (warp & 3) * 32) * a.o.st;
-        const int live = w.rows - row0 - (warp & 3) * 32;  // rows of this warp inside the sequence
 #pragma unroll 1
-        for (int c0 = 0; c0 < a.dv; c0 += 64) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                float v[32];
-                tmem_ld32(oa + c0 + 32 * g, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 u;
-                    u.x = pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv);
-                    u.y = pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
-                    u.z = pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv);
-                    u.w = pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
-                    *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * g + e) ^ (lane & 7)) << 4)) = u;
-                }
-            }
-            __syncwarp();
-            const int col = c0 + 8 * (lane & 7);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 4 * e + (lane >> 3);
-                const uint4 u = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                if (row < live && col < a.dv) *reinterpret_cast<uint4 *>(o + (size_t)row * a.o.st + col) = u;
-            }
-            __syncwarp();
-        }
+        for (int c0 = 0; c0 < a.dv; c0 += 64)
+            store_rows<64>(stage, oa + c0, inv, o, a.o.st, w.rows - row0 - (warp & 3) * 32, c0, a.dv);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ws.bar(L::B_OE + t));
