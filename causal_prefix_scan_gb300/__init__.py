@@ -15,7 +15,9 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from collections import namedtuple
 from dataclasses import dataclass
@@ -175,7 +177,8 @@ def _ptr(x) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without the object around it
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -574,13 +577,15 @@ GatedGradients = namedtuple("GatedGradients", "dx dg d_rate d_state_in")
 
 def _expect(t, name, shape, dtype, device, contiguous=False):
     """Shape, type and device of one argument; its channels have to be adjacent."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if contiguous and not t.is_contiguous():
+    if t.is_contiguous():
+        return
+    if contiguous:
         raise ValueError(f"{name} must be contiguous")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the elements of the last dimension must be adjacent")
@@ -591,31 +596,43 @@ def _current(t):
     import torch
     if not t.is_cuda:
         raise ValueError("CUDA tensors are needed")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    dev = t.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on(stream):
     """What a call allocates belongs to the stream the call runs on."""
-    import contextlib
-
-    import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
+    import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _t2(t):
     """[B, d] rows, or [B, n, d]."""
     s = t.stride()
-    return ctypes.byref(hla_tensor(t.data_ptr(), s[0], 0, s[1] if len(s) == 3 else 0))
+    return hla_tensor(t.data_ptr(), s[0], 0, s[1] if len(s) == 3 else 0)
 
 
 def _t4(t):
     """[B, H, w] rows, or [B, H, n, w]."""
     s = t.stride()
-    return ctypes.byref(hla_tensor(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0))
+    return hla_tensor(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
+
+
+def _zeroed(like, shapes):
+    """Zeroed tensors of these shapes in one allocation, each on a 256-byte boundary."""
+    import torch
+    unit = 256 // like.element_size()
+    sizes = [math.prod(s) for s in shapes]
+    parts = torch.zeros(sum(-(-n // unit) * unit for n in sizes), dtype=like.dtype, device=like.device).split(
+        [-(-n // unit) * unit for n in sizes])
+    return tuple((x if x.numel() == n else x[:n]).view(s) for x, n, s in zip(parts, sizes, shapes))
 
 
 def _int32(x, name):
@@ -631,10 +648,11 @@ def _gated_params(x, g, gate, rate, lengths, device):
         raise ValueError(f"gate must be one of {sorted(_GATES)}")
     import torch
     code = _dtype_code(x)
-    B, d = x.shape[0], x.shape[-1]
-    n = x.shape[1] if x.dim() == 3 else 1
-    _expect(x, "x", x.shape, x.dtype, device)
-    _expect(g, "g", x.shape, x.dtype, device)
+    shape, dtype = x.shape, x.dtype
+    B, d = shape[0], shape[-1]
+    n = shape[1] if len(shape) == 3 else 1
+    _expect(x, "x", shape, dtype, device)
+    _expect(g, "g", shape, dtype, device)
     if (rate is not None) != (gate == "rate"):
         raise ValueError("rate belongs to gate='rate', which needs it")
     if rate is not None:
@@ -712,8 +730,8 @@ def gated_backward(x, g, y, dy, gate: str = "given", rate=None, state_in=None, d
     with _on(stream):
         new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
         if out is None:
-            make = torch.zeros if lengths is not None else torch.empty
-            out = (make(x.shape, dtype=x.dtype, device=dev), make(x.shape, dtype=x.dtype, device=dev))
+            out = _zeroed(x, (x.shape, x.shape)) if lengths is not None else \
+                (torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty(x.shape, dtype=x.dtype, device=dev))
         dx, dg = out
         _expect(dx, "dx", x.shape, x.dtype, dev)
         _expect(dg, "dg", x.shape, x.dtype, dev)
@@ -807,8 +825,9 @@ def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: f
     _expect(lse, "lse", (p.B, p.H, p.n), torch.float32, dev, True)
     with _on(stream):
         if out is None:
-            make = torch.zeros if lengths is not None else torch.empty
-            out = tuple(make(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
+            shapes = (q.shape, k.shape, v.shape)
+            out = _zeroed(q, shapes) if lengths is not None else \
+                tuple(torch.empty(x, dtype=q.dtype, device=dev) for x in shapes)
         dq, dk, dv = out
         for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
             _expect(t, name, like.shape, q.dtype, dev)
