@@ -29,12 +29,12 @@ namespace {
 constexpr int WARPS = 8;
 constexpr int kThreads = WARPS * 32;
 // Tokens of one thread: as many as leave what it holds of them in registers at two CTAs per
-// SM (the backward's four inputs and the fp32 ones take twice the room).
+// SM (the backward's four inputs and pairs of fp32 channels take twice the room).
 enum Dir { FWD, BWD };
-template <typename T, Dir DIR>
-constexpr int kTS = DIR == FWD && sizeof(T) == 2 ? 16 : 8;
-template <typename T, Dir DIR>
-constexpr int kTileT = WARPS * kTS<T, DIR>;  // tokens of one tile
+template <typename T, Dir DIR, int VEC>
+constexpr int kTS = DIR == FWD && VEC * sizeof(T) <= 4 ? 16 : 8;
+template <typename T, Dir DIR, int VEC>
+constexpr int kTileT = WARPS * kTS<T, DIR, VEC>;  // tokens of one tile
 constexpr int kTileLeast = WARPS * 8;
 constexpr int BACK = 8;               // windows of WARPS earlier tiles kept by one look-back
 
@@ -185,9 +185,9 @@ __device__ __forceinline__ void take_place(Shared<VEC> &sh, const Args &a) {
 
 // ------------------------------------------------------------ forward
 // The state before this warp's tokens: the tile's, taken through the maps of the warps before.
-template <int VEC>
-HLA_DEVICE Vf<VEC> before_warp(const Shared<VEC> &sh, int warp, int lane) {
-    Vf<VEC> h;
+template <class V, int VEC>
+HLA_DEVICE V before_warp(const Shared<VEC> &sh, int warp, int lane) {
+    V h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         h.v[v] = sh.carry[lane * VEC + v];
@@ -203,7 +203,7 @@ HLA_DEVICE Vf<VEC> before_warp(const Shared<VEC> &sh, int warp, int lane) {
 // thread of the CTA has all its TS tokens, so nothing is predicated.
 template <typename T, int GATE, int VEC, bool FULL>
 HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, int b, int c0, int t0, int m, int len) {
-    constexpr int TS = kTS<T, FWD>;
+    constexpr int TS = kTS<T, FWD, VEC>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const size_t so = (size_t)b * a.d;
     raw_t<T, VEC> xr[TS] = {}, gr[TS] = {};
@@ -214,17 +214,17 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 #pragma unroll
     for (int i = 0; i < TS; ++i)
         if (FULL || i < m) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
-    const Vf<VEC> r = rate_of<GATE, VEC>(a, ch);
-    Vf<VEC> ea[TS], eb[TS], A = splat<VEC>(1.f), Bv = splat<VEC>(0.f);
+    const Fwd<VEC> r = rate_of<GATE, Fwd<VEC>>(a, ch);
+    Fwd<VEC> ea[TS], eb[TS], A = splat<Fwd<VEC>>(1.f), Bv = splat<Fwd<VEC>>(0.f);
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
-        Vf<VEC> x, g;
+        Fwd<VEC> x, g;
         unpack(xr[i], x.v);
         unpack(gr[i], g.v);
         gate_fwd<GATE>(g, r, x, ea[i], eb[i]);
         if (!FULL && i >= m) {
-            ea[i] = splat<VEC>(1.f);
-            eb[i] = splat<VEC>(0.f);
+            ea[i] = splat<Fwd<VEC>>(1.f);
+            eb[i] = splat<Fwd<VEC>>(0.f);
         }
         Bv = fma_(ea[i], Bv, eb[i]);
         A = mul_(A, ea[i]);
@@ -232,11 +232,11 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A.v[v], Bv.v[v]);
     __syncthreads();
-    const bool last = pos == (len - 1) / kTileT<T, FWD>;
+    const bool last = pos == (len - 1) / kTileT<T, FWD, VEC>;
     if (!look_back<VEC>(sh, a, chain, pos, 0, a.state_in ? a.state_in + so : nullptr, c0,
                         last && a.out_state ? a.out_state + so : nullptr))
         return;
-    Vf<VEC> h = before_warp<VEC>(sh, warp, lane);
+    Fwd<VEC> h = before_warp<Fwd<VEC>>(sh, warp, lane);
     const size_t yo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
@@ -247,7 +247,7 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 
 template <typename T, int GATE, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
-    constexpr int TS = kTS<T, FWD>, TILE_T = kTileT<T, FWD>;
+    constexpr int TS = kTS<T, FWD, VEC>, TILE_T = kTileT<T, FWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
 template <typename T, int GATE, int VEC, bool FULL>
 HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, int tile, int b, int c0, int t0, int m,
                          int len) {
-    constexpr int TS = kTS<T, BWD>;
+    constexpr int TS = kTS<T, BWD, VEC>;
     constexpr int C = 32 * VEC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const size_t so = (size_t)b * a.d;
@@ -299,8 +299,8 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
             if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
         }
     }
-    const Vf<VEC> r = rate_of<GATE, VEC>(a, ch);
-    Vf<VEC> h0 = splat<VEC>(0.f), ea[TS], A = splat<VEC>(1.f), Bv = splat<VEC>(0.f);
+    const Bwd<VEC> r = rate_of<GATE, Bwd<VEC>>(a, ch);
+    Bwd<VEC> h0 = splat<Bwd<VEC>>(0.f), kept[TS], A = splat<Bwd<VEC>>(1.f), Bv = splat<Bwd<VEC>>(0.f);
     if (t0 == 0 && a.state_in) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
@@ -308,34 +308,35 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     }
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
-        Vf<VEC> g, dy;
+        Bwd<VEC> g, dy;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
-        ea[i] = gate_a<GATE>(g, r);
-        if (!FULL && i >= m) ea[i] = splat<VEC>(1.f);
-        Bv = mul_(ea[i], add_(dy, Bv));
-        A = mul_(A, ea[i]);
+        kept[i] = gate_keep<GATE>(g, r);
+        if (!FULL && i >= m) kept[i] = splat<Bwd<VEC>>(kKeptOff<GATE>);
+        const Bwd<VEC> at = kept_a<GATE>(kept[i]);
+        Bv = mul_(at, add_(dy, Bv));
+        A = mul_(A, at);
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sh.agg[warp][lane * VEC + v] = make_float2(A.v[v], Bv.v[v]);
     __syncthreads();
-    const int first = a.tiles - 1 - (len - 1) / kTileT<T, BWD>;
+    const int first = a.tiles - 1 - (len - 1) / kTileT<T, BWD, VEC>;
     if (!look_back<VEC>(sh, a, chain, pos, first, a.d_state_out ? a.d_state_out + so : nullptr, c0,
                         tile == 0 && a.out_state ? a.out_state + so : nullptr))
         return;
-    Vf<VEC> c = before_warp<VEC>(sh, warp, lane), sum = splat<VEC>(0.f);
+    Bwd<VEC> c = before_warp<Bwd<VEC>>(sh, warp, lane), sum = splat<Bwd<VEC>>(0.f);
     const size_t dxo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch, dgo = (size_t)b * a.o2.sb + (size_t)t0 * a.o2.st + ch;
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
-        Vf<VEC> g, dy, x = splat<VEC>(0.f), y, dx, dg, drv;
+        Bwd<VEC> g, dy, x = splat<Bwd<VEC>>(0.f), y, dx, dg, drv;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
         unpack(yr[i], y.v);
         if (i == 0 && t0 == 0) y = h0;
         if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
-        const Vf<VEC> gh = add_(dy, c);
-        gate_bwd<GATE>(g, r, x, y, gh, ea[i], dx, dg, drv);
-        c = mul_(ea[i], gh);
+        const Bwd<VEC> gh = add_(dy, c);
+        gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv);
+        c = mul_(kept_a<GATE>(kept[i]), gh);
         if (FULL || i < m) {
             if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
             store<T, VEC>(a.o1, dxo + (size_t)i * a.o1.st, dx.v);
@@ -361,7 +362,7 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 
 template <typename T, int GATE, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const Args a) {
-    constexpr int TS = kTS<T, BWD>, TILE_T = kTileT<T, BWD>;
+    constexpr int TS = kTS<T, BWD, VEC>, TILE_T = kTileT<T, BWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
@@ -419,13 +420,13 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const Args a) {
     if (e >= cols * a.B) return;
     const int b = (int)(e / cols), ch = (int)(e % cols) * VEC;
     if (a.lengths && a.lengths[b] <= 0) return;
-    Vf<VEC> x, g, h, ea, eb;
+    Fwd<VEC> x, g, h, ea, eb;
     unpack(load<T, VEC>(a.x, (size_t)b * a.x.sb + ch), x.v);
     unpack(load<T, VEC>(a.g, (size_t)b * a.g.sb + ch), g.v);
     const size_t so = (size_t)b * a.d + ch;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.v[v] = a.state_in[so + v];
-    gate_fwd<GATE>(g, rate_of<GATE, VEC>(a, ch), x, ea, eb);
+    gate_fwd<GATE>(g, rate_of<GATE, Fwd<VEC>>(a, ch), x, ea, eb);
     h = fma_(ea, h, eb);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) a.out_state[so + v] = h.v[v];
@@ -441,8 +442,10 @@ int most_tiles(const hla_gated_params *p) { return tiles_of(p->n, kTileLeast); }
 // Two channels per lane when every row of every tensor starts on a two-channel boundary
 // and rows hold a whole number of them: a row segment is then 128 bytes (bf16) per warp
 // and load.  One channel per lane otherwise (odd widths or strides, offset pointers).
-bool pairable(const hla_tensor *t, size_t el) {
-    return !t || !t->p || ((reinterpret_cast<uintptr_t>(t->p) % (2 * el)) == 0 && t->sb % 2 == 0 && t->st % 2 == 0);
+bool pairable(const hla_tensor *t, const hla_gated_params *p) {
+    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
+    return !t || !t->p || ((reinterpret_cast<uintptr_t>(t->p) % (2 * el)) == 0 && (p->B == 1 || t->sb % 2 == 0) &&
+                           (p->n == 1 || t->st % 2 == 0));
 }
 
 hla_status check(const hla_gated_params *p) {
@@ -501,7 +504,7 @@ enum Which { W_FWD, W_BWD, W_STEP };
 template <typename T, int GATE, int VEC>
 cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
     a.slices = slices_of<VEC>(a.d);
-    a.tiles = w == W_BWD ? tiles_of(a.n, kTileT<T, BWD>) : tiles_of(a.n, kTileT<T, FWD>);
+    a.tiles = w == W_BWD ? tiles_of(a.n, kTileT<T, BWD, VEC>) : tiles_of(a.n, kTileT<T, FWD, VEC>);
     if (w == W_STEP) {
         const size_t total = (size_t)a.B * ((a.d + VEC - 1) / VEC);
         gated_step_kernel<T, GATE, VEC><<<(unsigned)((total + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
@@ -516,7 +519,7 @@ cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
     gated_bwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.part && GATE == HLA_GATE_RATE) {
-        gated_rate_kernel<VEC><<<(a.d + 31) / 32, kThreads, 0, st>>>(a, kTileT<T, BWD>, d_rate);
+        gated_rate_kernel<VEC><<<(a.d + 31) / 32, kThreads, 0, st>>>(a, kTileT<T, BWD, VEC>, d_rate);
         e = cudaGetLastError();
     }
     return e;
@@ -601,8 +604,7 @@ hla_status hla_gated_forward(const hla_gated_params *p, const hla_tensor *x, con
     a.x = view(x); a.g = view(g); a.o1 = view(y);
     a.state_in = state_in;
     a.out_state = state_out;
-    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    return dispatch(p, W_FWD, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr, st);
+    return dispatch(p, W_FWD, a, p->d % 2 == 0 && pairable(x, p) && pairable(g, p) && pairable(y, p), nullptr, st);
 }
 
 hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, const hla_tensor *g, const hla_tensor *y,
@@ -641,9 +643,8 @@ hla_status hla_gated_backward(const hla_gated_params *p, const hla_tensor *x, co
     a.state_in = state_in;
     a.d_state_out = d_state_out;
     a.out_state = d_state_in;
-    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    bool pairs = p->d % 2 == 0 && pairable(dx, el) && pairable(dg, el);
-    for (const hla_tensor *i : ins) pairs = pairs && pairable(i, el);
+    bool pairs = p->d % 2 == 0 && pairable(dx, p) && pairable(dg, p);
+    for (const hla_tensor *i : ins) pairs = pairs && pairable(i, p);
     return dispatch(p, W_BWD, a, pairs, d_rate, st);
 }
 
@@ -662,8 +663,7 @@ hla_status hla_gated_step(const hla_gated_params *p, const hla_tensor *x, const 
     a.x = view(x); a.g = view(g); a.o1 = view(y);
     a.state_in = state;
     a.out_state = state_out;
-    const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    return dispatch(p, W_STEP, a, p->d % 2 == 0 && pairable(x, el) && pairable(g, el) && pairable(y, el), nullptr,
+    return dispatch(p, W_STEP, a, p->d % 2 == 0 && pairable(x, p) && pairable(g, p) && pairable(y, p), nullptr,
                     static_cast<cudaStream_t>(stream));
 }
 

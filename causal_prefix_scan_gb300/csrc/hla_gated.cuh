@@ -78,57 +78,81 @@ __device__ __forceinline__ void store(const Tensor &t, size_t off, const float (
 }
 
 // ------------------------------------------------------------ arithmetic on VEC channels
-// Pairs of fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
-// scalar ones): the gates' arithmetic, not memory, bounds a kernel that issues them singly.
-template <int VEC>
+// PAIR: two fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
+// scalar ones).  The forward kernels use it: fewer instructions to issue (32,768 tokens x 4,096
+// channels 247 -> 233 us).  The backward ones do not: pairs bind their operands to aligned
+// register pairs, which costs spilled registers there (2 x 8,192 x 4,096: 471 against 241 us).
+template <int VEC, bool PAIR>
 struct Vf {
+    static constexpr int N = VEC;
     float v[VEC];
 };
-HLA_DEVICE unsigned long long pair(const Vf<2> &x) {
+template <int VEC>
+using Fwd = Vf<VEC, VEC == 2>;
+template <int VEC>
+using Bwd = Vf<VEC, false>;
+using Pair = Vf<2, true>;
+
+HLA_DEVICE unsigned long long pair(const Pair &x) {
     unsigned long long r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.v[0]), "f"(x.v[1]));
     return r;
 }
-HLA_DEVICE Vf<2> unpair(unsigned long long r) {
-    Vf<2> x;
+HLA_DEVICE Pair unpair(unsigned long long r) {
+    Pair x;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x.v[0]), "=f"(x.v[1]) : "l"(r));
     return x;
 }
-template <int VEC>
-HLA_DEVICE Vf<VEC> splat(float c) {
-    Vf<VEC> r;
+template <class V, class F>
+HLA_DEVICE V each(const V &a, F f) {
+    V r;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = c;
+    for (int i = 0; i < V::N; ++i) r.v[i] = f(a.v[i]);
     return r;
 }
-HLA_DEVICE Vf<1> fma_(Vf<1> a, Vf<1> b, Vf<1> c) { return {fmaf(a.v[0], b.v[0], c.v[0])}; }
-HLA_DEVICE Vf<1> mul_(Vf<1> a, Vf<1> b) { return {a.v[0] * b.v[0]}; }
-HLA_DEVICE Vf<1> add_(Vf<1> a, Vf<1> b) { return {a.v[0] + b.v[0]}; }
-HLA_DEVICE Vf<2> fma_(const Vf<2> &a, const Vf<2> &b, const Vf<2> &c) {
+template <class V>
+HLA_DEVICE V splat(float c) {
+    return each(V{}, [c](float) { return c; });
+}
+template <int VEC>
+HLA_DEVICE Vf<VEC, false> fma_(const Vf<VEC, false> &a, const Vf<VEC, false> &b, const Vf<VEC, false> &c) {
+    Vf<VEC, false> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = fmaf(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+template <int VEC>
+HLA_DEVICE Vf<VEC, false> mul_(const Vf<VEC, false> &a, const Vf<VEC, false> &b) {
+    Vf<VEC, false> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = a.v[i] * b.v[i];
+    return r;
+}
+template <int VEC>
+HLA_DEVICE Vf<VEC, false> add_(const Vf<VEC, false> &a, const Vf<VEC, false> &b) {
+    Vf<VEC, false> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = a.v[i] + b.v[i];
+    return r;
+}
+HLA_DEVICE Pair fma_(const Pair &a, const Pair &b, const Pair &c) {
     unsigned long long r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
     return unpair(r);
 }
-HLA_DEVICE Vf<2> mul_(const Vf<2> &a, const Vf<2> &b) {
+HLA_DEVICE Pair mul_(const Pair &a, const Pair &b) {
     unsigned long long r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
     return unpair(r);
 }
-HLA_DEVICE Vf<2> add_(const Vf<2> &a, const Vf<2> &b) {
+HLA_DEVICE Pair add_(const Pair &a, const Pair &b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
     return unpair(r);
 }
-template <int VEC>
-HLA_DEVICE Vf<VEC> sub_(const Vf<VEC> &a, const Vf<VEC> &b) {  // a - b
-    return fma_(b, splat<VEC>(-1.f), a);
-}
-template <int VEC, class F>
-HLA_DEVICE Vf<VEC> each(const Vf<VEC> &a, F f) {
-    Vf<VEC> r;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = f(a.v[i]);
-    return r;
+template <class V>
+HLA_DEVICE V sub_(const V &a, const V &b) {  // a - b
+    return fma_(b, splat<V>(-1.f), a);
 }
 HLA_DEVICE float rsqrt_approx(float x) {
     float r;
@@ -147,13 +171,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // sigma(z) and 1 - sigma(z), both with a relative error of a few units in the last place:
 // the smaller is e / (1 + e), e = exp(-|z|) <= 1, and the larger is one minus it, so that a
 // gate near one, whose error a long product of gates multiplies, is off by its rounding only.
-template <int VEC>
-HLA_DEVICE void sigmoid2(const Vf<VEC> &z, Vf<VEC> &s, Vf<VEC> &c) {
-    const Vf<VEC> e = each(z, [](float x) { return ex2_approx(fabsf(x) * -kLog2e); });
-    const Vf<VEC> r = each(add_(e, splat<VEC>(1.f)), rcp_approx);
-    const Vf<VEC> lo = mul_(e, r), hi = sub_(splat<VEC>(1.f), lo);
+template <class V>
+HLA_DEVICE void sigmoid2(const V &z, V &s, V &c) {
+    const V e = each(z, [](float x) { return ex2_approx(fabsf(x) * -kLog2e); });
+    const V r = each(add_(e, splat<V>(1.f)), rcp_approx);
+    const V lo = mul_(e, r), hi = sub_(splat<V>(1.f), lo);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < V::N; ++i) {
         const bool up = z.v[i] > 0.f;
         s.v[i] = up ? hi.v[i] : lo.v[i];
         c.v[i] = up ? lo.v[i] : hi.v[i];
@@ -161,88 +185,98 @@ HLA_DEVICE void sigmoid2(const Vf<VEC> &z, Vf<VEC> &s, Vf<VEC> &c) {
 }
 // sigma(z) alone, a few units in the last place off: far below zero the exponential is
 // infinite and the quotient zero.
-template <int VEC>
-HLA_DEVICE Vf<VEC> sigmoid(const Vf<VEC> &z) {
-    const Vf<VEC> e = each(mul_(z, splat<VEC>(-kLog2e)), ex2_approx);
-    return each(add_(e, splat<VEC>(1.f)), rcp_approx);
+template <class V>
+HLA_DEVICE V sigmoid(const V &z) {
+    const V e = each(mul_(z, splat<V>(-kLog2e)), ex2_approx);
+    return each(add_(e, splat<V>(1.f)), rcp_approx);
 }
 // 1 - exp(-u) for u >= 0.  Below 1/16 the difference would cancel: Taylor's series to u^5,
 // whose next term is under 2^-29 of the sum there.
-template <int VEC>
-HLA_DEVICE Vf<VEC> one_minus_exp(const Vf<VEC> &u) {
-    const Vf<VEC> e = each(mul_(u, splat<VEC>(-kLog2e)), ex2_approx);
-    const Vf<VEC> far = sub_(splat<VEC>(1.f), e);
-    Vf<VEC> p = fma_(u, splat<VEC>(1.f / 120.f), splat<VEC>(-1.f / 24.f));
-    p = fma_(p, u, splat<VEC>(1.f / 6.f));
-    p = fma_(p, u, splat<VEC>(-0.5f));
-    p = fma_(p, u, splat<VEC>(1.f));
+template <class V>
+HLA_DEVICE V one_minus_exp(const V &u) {
+    const V e = each(mul_(u, splat<V>(-kLog2e)), ex2_approx);
+    const V far = sub_(splat<V>(1.f), e);
+    V p = fma_(u, splat<V>(1.f / 120.f), splat<V>(-1.f / 24.f));
+    p = fma_(p, u, splat<V>(1.f / 6.f));
+    p = fma_(p, u, splat<V>(-0.5f));
+    p = fma_(p, u, splat<V>(1.f));
     p = mul_(p, u);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) p.v[i] = u.v[i] < 0.0625f ? p.v[i] : far.v[i];
+    for (int i = 0; i < V::N; ++i) p.v[i] = u.v[i] < 0.0625f ? p.v[i] : far.v[i];
     return p;
 }
 // 1 / sqrt(q) for q >= 0, finite at 0
-template <int VEC>
-HLA_DEVICE Vf<VEC> rsqrt0(const Vf<VEC> &q) {
+template <class V>
+HLA_DEVICE V rsqrt0(const V &q) {
     return each(q, [](float x) { return rsqrt_approx(fmaxf(x, 1.2e-38f)); });
 }
 
 // a_t and b_t
-template <int GATE, int VEC>
-HLA_DEVICE void gate_fwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, Vf<VEC> &a, Vf<VEC> &b) {
+template <int GATE, class V>
+HLA_DEVICE void gate_fwd(const V &g, const V &r, const V &x, V &a, V &b) {
     if constexpr (GATE == HLA_GATE_GIVEN) {
         a = g;
         b = x;
     } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        Vf<VEC> c;
+        V c;
         sigmoid2(g, a, c);
         b = mul_(c, x);
     } else {
-        const Vf<VEC> w = one_minus_exp(mul_(r, sigmoid(g)));  // 1 - a
-        a = sub_(splat<VEC>(1.f), w);
-        const Vf<VEC> q = fma_(w, a, w);  // 1 - a^2
+        const V w = one_minus_exp(mul_(r, sigmoid(g)));  // 1 - a
+        a = sub_(splat<V>(1.f), w);
+        const V q = fma_(w, a, w);  // 1 - a^2
         b = mul_(mul_(q, rsqrt0(q)), x);
     }
 }
-// a_t alone, the same bits as gate_fwd's
-template <int GATE, int VEC>
-HLA_DEVICE Vf<VEC> gate_a(const Vf<VEC> &g, const Vf<VEC> &r) {
-    Vf<VEC> a, b;
-    gate_fwd<GATE>(g, r, splat<VEC>(0.f), a, b);
+// What the backward pass keeps of a token's gate: a, or 1 - a with HLA_GATE_RATE, from which a
+// follows with the bits of gate_fwd's and the gradients without a second exponential.
+template <int GATE, class V>
+HLA_DEVICE V gate_keep(const V &g, const V &r) {
+    if constexpr (GATE == HLA_GATE_RATE) return one_minus_exp(mul_(r, sigmoid(g)));
+    V a, b;
+    gate_fwd<GATE>(g, r, splat<V>(0.f), a, b);
     return a;
 }
+template <int GATE, class V>
+HLA_DEVICE V kept_a(const V &k) {
+    if constexpr (GATE == HLA_GATE_RATE) return sub_(splat<V>(1.f), k);
+    return k;
+}
+template <int GATE>
+constexpr float kKeptOff = GATE == HLA_GATE_RATE ? 0.f : 1.f;  // a token that is not there: a = 1
+
 // Gradients with respect to x, g and (HLA_GATE_RATE) the rate, from gh = dL/dh_t, x_t,
-// y = h_{t-1} and a_t.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f, da/du = -a.
+// y = h_{t-1} and gate_keep's k.  With f = sqrt(1 - a^2), a = exp(-u): df/du = a^2 / f, da/du = -a.
 // f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
-template <int GATE, int VEC>
-HLA_DEVICE void gate_bwd(const Vf<VEC> &g, const Vf<VEC> &r, const Vf<VEC> &x, const Vf<VEC> &y, const Vf<VEC> &gh,
-                         const Vf<VEC> &a, Vf<VEC> &dx, Vf<VEC> &dg, Vf<VEC> &dr) {
+template <int GATE, class V>
+HLA_DEVICE void gate_bwd(const V &g, const V &r, const V &x, const V &y, const V &gh,
+                         const V &k, V &dx, V &dg, V &dr) {
     if constexpr (GATE == HLA_GATE_GIVEN) {
         dx = gh;
         dg = mul_(gh, y);
     } else if constexpr (GATE == HLA_GATE_SIGMOID) {
-        Vf<VEC> s, c;
+        V s, c;
         sigmoid2(g, s, c);
         dx = mul_(gh, c);
         dg = mul_(mul_(dx, s), sub_(y, x));
     } else {
-        Vf<VEC> s, c;
+        V s, c;
         sigmoid2(g, s, c);
-        const Vf<VEC> u = mul_(r, s), w = one_minus_exp(u), q = fma_(w, a, w);
-        const Vf<VEC> rf = rsqrt0(q);
+        const V a = kept_a<GATE>(k), q = fma_(k, a, k);
+        const V rf = rsqrt0(q);
         dx = mul_(gh, mul_(q, rf));
-        const Vf<VEC> du = mul_(mul_(gh, a), sub_(mul_(mul_(x, a), rf), y));
-        dg = mul_(du, mul_(u, c));
+        const V du = mul_(mul_(gh, a), sub_(mul_(mul_(x, a), rf), y));
         dr = mul_(du, s);
+        dg = mul_(mul_(dr, r), c);
     }
 }
 
-template <int GATE, int VEC>
-HLA_DEVICE Vf<VEC> rate_of(const Args &a, int ch) {
-    Vf<VEC> r = splat<VEC>(0.f);
+template <int GATE, class V>
+HLA_DEVICE V rate_of(const Args &a, int ch) {
+    V r = splat<V>(0.f);
     if constexpr (GATE == HLA_GATE_RATE) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
+        for (int v = 0; v < V::N; ++v)
             if (ch + v < a.d) r.v[v] = a.rate[ch + v];
     }
     return r;

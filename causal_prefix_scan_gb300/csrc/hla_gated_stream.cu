@@ -15,7 +15,7 @@ namespace gated {
 namespace {
 
 constexpr int VEC = 2, GL = 8, GROUPS = 32 / GL, CW = GL * VEC, TS = 8;
-constexpr int kWarpsFwd = 12, kWarpsBwd = 8;
+constexpr int kWarpsFwd = 12, kWarpsBwd = 8;  // of a CTA
 
 template <int NW>
 struct Shared {
@@ -23,45 +23,47 @@ struct Shared {
     float2 carry[2][GL];    // state before the tile
 };
 
-HLA_DEVICE Vf<2> shfl_up(const Vf<2> &x, int by) {
+template <class V>
+HLA_DEVICE V shfl_up(const V &x, int by) {
     return {__shfl_up_sync(0xffffffffu, x.v[0], by), __shfl_up_sync(0xffffffffu, x.v[1], by)};
 }
 
 // From the map (A, B) of this thread's tokens to the state before them; the state after the
 // tile goes into sh.carry for the next one.  `k` counts tiles.
-template <int NW>
-HLA_DEVICE Vf<2> state_before(Shared<NW> &sh, int k, Vf<2> A, Vf<2> B) {
+template <int NW, class V>
+HLA_DEVICE V state_before(Shared<NW> &sh, int k, V A, V B) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / GL, c = lane % GL;
 #pragma unroll
     for (int by = GL; by < 32; by <<= 1) {
-        const Vf<2> a = shfl_up(A, by), b = shfl_up(B, by);
+        const V a = shfl_up(A, by), b = shfl_up(B, by);
         if (lane >= by) {
             B = fma_(A, b, B);
             A = mul_(A, a);
         }
     }
     if (grp == GROUPS - 1) sh.map[k & 1][warp][c] = make_float4(A.v[0], A.v[1], B.v[0], B.v[1]);
-    Vf<2> ea = shfl_up(A, GL), eb = shfl_up(B, GL);
+    V ea = shfl_up(A, GL), eb = shfl_up(B, GL);
     if (grp == 0) {
-        ea = splat<2>(1.f);
-        eb = splat<2>(0.f);
+        ea = splat<V>(1.f);
+        eb = splat<V>(0.f);
     }
     __syncthreads();
     const float2 c0 = sh.carry[k & 1][c];
-    Vf<2> h = {c0.x, c0.y};
+    V h = {c0.x, c0.y};
     for (int w = 0; w < warp; ++w) {
         const float4 m = sh.map[k & 1][w][c];
-        h = fma_(Vf<2>{m.x, m.y}, h, Vf<2>{m.z, m.w});
+        h = fma_(V{m.x, m.y}, h, V{m.z, m.w});
     }
     if (warp == NW - 1 && grp == GROUPS - 1) {
-        const Vf<2> after = fma_(A, h, B);
+        const V after = fma_(A, h, B);
         sh.carry[(k + 1) & 1][c] = make_float2(after.v[0], after.v[1]);
     }
     return fma_(ea, h, eb);
 }
 
-HLA_DEVICE Vf<2> load_state(const float *p, size_t off, bool ok) {
-    Vf<2> s = splat<2>(0.f);
+template <class V>
+HLA_DEVICE V load_state(const float *p, size_t off, bool ok) {
+    V s = splat<V>(0.f);
     if (p && ok) s = {p[off], p[off + 1]};
     return s;
 }
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_fwd_kernel(const Args a) {
     const int len = length_of(a, b);
     const size_t so = (size_t)b * a.d + ch;
     if (warp == NW - 1 && lane >= 32 - GL) {
-        const Vf<2> s = load_state(a.state_in, so, mine);
+        const Fwd<2> s = load_state<Fwd<2>>(a.state_in, so, mine);
         sh.carry[0][lane % GL] = make_float2(s.v[0], s.v[1]);
     }
     const int t0 = (warp * GROUPS + lane / GL) * TS;  // first token of this thread in a tile
@@ -94,23 +96,23 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_fwd_kernel(const Args a) {
             gr[i] = ld(gp + (size_t)i * a.g.st);
             xr[i] = ld(xp + (size_t)i * a.x.st);
         }
-    const Vf<2> r = rate_of<GATE, VEC>(a, ch);
+    const Fwd<2> r = rate_of<GATE, Fwd<2>>(a, ch);
     int k = 0;
     // FULL: this tile and the next have all their tokens and the slice all its channels
     auto tile = [&](int base, auto full) {
         constexpr bool FULL = decltype(full)::value;
         xp += (size_t)TT * a.x.st;
         gp += (size_t)TT * a.g.st;
-        Vf<2> ea[TS], eb[TS], A = splat<2>(1.f), B = splat<2>(0.f);
+        Fwd<2> ea[TS], eb[TS], A = splat<Fwd<2>>(1.f), B = splat<Fwd<2>>(0.f);
 #pragma unroll
         for (int i = 0; i < TS; ++i) {
-            Vf<2> x, g;
+            Fwd<2> x, g;
             unpack(xr[i], x.v);
             unpack(gr[i], g.v);
             gate_fwd<GATE>(g, r, x, ea[i], eb[i]);
             if (!FULL && base + t0 + i >= len) {
-                ea[i] = splat<2>(1.f);
-                eb[i] = splat<2>(0.f);
+                ea[i] = splat<Fwd<2>>(1.f);
+                eb[i] = splat<Fwd<2>>(0.f);
             }
             if (FULL || (mine && base + TT + t0 + i < len)) {
                 gr[i] = ld(gp + (size_t)i * a.g.st);
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_fwd_kernel(const Args a) {
             B = fma_(ea[i], B, eb[i]);
             A = mul_(A, ea[i]);
         }
-        Vf<2> h = state_before(sh, k++, A, B);
+        Fwd<2> h = state_before(sh, k++, A, B);
 #pragma unroll
         for (int i = 0; i < TS; ++i) {
             h = fma_(ea[i], h, eb[i]);
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
     const int len = length_of(a, b);
     const size_t so = (size_t)b * a.d + ch;
     if (warp == NW - 1 && lane >= 32 - GL) {
-        const Vf<2> s = load_state(a.d_state_out, so, mine);
+        const Bwd<2> s = load_state<Bwd<2>>(a.d_state_out, so, mine);
         sh.carry[0][lane % GL] = make_float2(s.v[0], s.v[1]);
     }
     // the first group takes a tile's last tokens: groups and warps follow the scan's direction
@@ -181,28 +183,29 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i)
         if (mine && base + t0 + i < len) fetch(i, base + t0 + i);
-    const Vf<2> r = rate_of<GATE, VEC>(a, ch);
-    const Vf<2> h0 = load_state(a.state_in, so, mine && t0 == 0);
-    Vf<2> sum = splat<2>(0.f);
+    const Bwd<2> r = rate_of<GATE, Bwd<2>>(a, ch);
+    const Bwd<2> h0 = load_state<Bwd<2>>(a.state_in, so, mine && t0 == 0);
+    Bwd<2> sum = splat<Bwd<2>>(0.f);
     int k = 0;
     // FULL: the tile has all its tokens (every earlier one has) and the slice all its channels
     auto tile = [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
-        Vf<2> ea[TS], A = splat<2>(1.f), B = splat<2>(0.f);
+        Bwd<2> kept[TS], A = splat<Bwd<2>>(1.f), B = splat<Bwd<2>>(0.f);
 #pragma unroll
         for (int i = TS - 1; i >= 0; --i) {
-            Vf<2> g, dy;
+            Bwd<2> g, dy;
             unpack(gr[i], g.v);
             unpack(dr[i], dy.v);
-            ea[i] = gate_a<GATE>(g, r);
+            kept[i] = gate_keep<GATE>(g, r);
             if (!FULL && (!mine || base + t0 + i >= len)) {
-                ea[i] = splat<2>(1.f);
-                dy = splat<2>(0.f);
+                kept[i] = splat<Bwd<2>>(kKeptOff<GATE>);
+                dy = splat<Bwd<2>>(0.f);
             }
-            B = mul_(ea[i], add_(dy, B));
-            A = mul_(A, ea[i]);
+            const Bwd<2> at = kept_a<GATE>(kept[i]);
+            B = mul_(at, add_(dy, B));
+            A = mul_(A, at);
         }
-        Vf<2> c = state_before(sh, k++, A, B);
+        Bwd<2> c = state_before(sh, k++, A, B);
         const bool more = base > 0;  // then the next tile is whole
         gp -= (size_t)TT * a.g.st;
         dp -= (size_t)TT * a.dy.st;
@@ -210,17 +213,17 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
         if constexpr (GATE != HLA_GATE_GIVEN) xp -= (size_t)TT * a.x.st;
 #pragma unroll
         for (int i = TS - 1; i >= 0; --i) {
-            Vf<2> g, dy, x = splat<2>(0.f), y, dx, dg, drv;
+            Bwd<2> g, dy, x = splat<Bwd<2>>(0.f), y, dx, dg, drv;
             unpack(gr[i], g.v);
             unpack(dr[i], dy.v);
             unpack(yr[i], y.v);
             if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
             if (i == 0 && base + t0 == 0) y = h0;
             if (more && (FULL || mine)) fetch(i, base - TT + t0 + i);
-            const Vf<2> gh = add_(dy, c);
-            gate_bwd<GATE>(g, r, x, y, gh, ea[i], dx, dg, drv);
+            const Bwd<2> gh = add_(dy, c);
+            gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv);
             if (FULL || (mine && base + t0 + i < len)) {
-                c = mul_(ea[i], gh);
+                c = mul_(kept_a<GATE>(kept[i]), gh);
                 if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
                 R o, q;
                 pack(dx.v, o);
