@@ -207,24 +207,24 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const size_t so = (size_t)b * a.d;
     raw_t<T, VEC> xr[TS] = {}, gr[TS] = {};
-    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch, go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch;
+    const Slice<T, VEC> xs(a.x, b, c0, t0, lane), gs(a.g, b, c0, t0, lane), ys(a.o1, b, c0, t0, lane);
 #pragma unroll
     for (int i = 0; i < TS; ++i)
-        if (FULL || i < m) gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
+        if (FULL || i < m) gr[i] = gs.load(i);
 #pragma unroll
     for (int i = 0; i < TS; ++i)
-        if (FULL || i < m) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
-    const Fwd<VEC> r = rate_of<GATE, Fwd<VEC>>(a, ch);
-    Fwd<VEC> ea[TS], eb[TS], A = splat<Fwd<VEC>>(1.f), Bv = splat<Fwd<VEC>>(0.f);
+        if (FULL || i < m) xr[i] = xs.load(i);
+    const Num<T, VEC> r = rate_of<GATE, Num<T, VEC>>(a, ch);
+    Num<T, VEC> ea[TS], eb[TS], A = splat<Num<T, VEC>>(1.f), Bv = splat<Num<T, VEC>>(0.f);
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
-        Fwd<VEC> x, g;
+        Num<T, VEC> x, g;
         unpack(xr[i], x.v);
         unpack(gr[i], g.v);
         gate_fwd<GATE>(g, r, x, ea[i], eb[i]);
         if (!FULL && i >= m) {
-            ea[i] = splat<Fwd<VEC>>(1.f);
-            eb[i] = splat<Fwd<VEC>>(0.f);
+            ea[i] = splat<Num<T, VEC>>(1.f);
+            eb[i] = splat<Num<T, VEC>>(0.f);
         }
         Bv = fma_(ea[i], Bv, eb[i]);
         A = mul_(A, ea[i]);
@@ -236,12 +236,11 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     if (!look_back<VEC>(sh, a, chain, pos, 0, a.state_in ? a.state_in + so : nullptr, c0,
                         last && a.out_state ? a.out_state + so : nullptr))
         return;
-    Fwd<VEC> h = before_warp<Fwd<VEC>>(sh, warp, lane);
-    const size_t yo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch;
+    Num<T, VEC> h = before_warp<Num<T, VEC>>(sh, warp, lane);
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
         h = fma_(ea[i], h, eb[i]);
-        if (FULL || i < m) store<T, VEC>(a.o1, yo + (size_t)i * a.o1.st, h.v);
+        if (FULL || i < m) ys.store(i, h.v);
     }
 }
 
@@ -251,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
-    const size_t chains = (size_t)a.B * a.slices;
-    const int pos = (int)(sh.ticket / chains);
-    const size_t chain = sh.ticket % chains;
+    const unsigned chains = (unsigned)a.B * a.slices, ticket = __shfl_sync(0xffffffffu, (unsigned)sh.ticket, 0);
+    const int pos = (int)(ticket / chains);
+    const unsigned chain = ticket % chains;
     const int b = (int)(chain / a.slices), c0 = (int)(chain % a.slices) * C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const int len = length_of(a, b);
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
             if (c0 + c < a.d) a.out_state[so + c0 + c] = a.state_in ? a.state_in[so + c0 + c] : 0.f;
     }
     if (pos * TILE_T >= len) return;
-    const int t0 = pos * TILE_T + warp * TS;
+    const int t0 = pos * TILE_T + __shfl_sync(0xffffffffu, warp, 0) * TS;  // the warp's, in uniform registers
     const int m = ch < a.d ? min(TS, len - t0) : 0;  // tokens of this thread (may be <= 0)
     if ((pos + 1) * TILE_T <= len && c0 + C <= a.d)  // the same for the whole CTA
         fwd_tile<T, GATE, VEC, true>(sh, a, chain, pos, b, c0, t0, m, len);
@@ -280,27 +279,25 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const size_t so = (size_t)b * a.d;
     raw_t<T, VEC> gr[TS] = {}, dr[TS] = {}, yr[TS] = {}, xr[TS] = {};
-    const size_t go = (size_t)b * a.g.sb + (size_t)t0 * a.g.st + ch, dyo = (size_t)b * a.dy.sb + (size_t)t0 * a.dy.st + ch;
-    const size_t xo = (size_t)b * a.x.sb + (size_t)t0 * a.x.st + ch;
-    // y one token earlier: h_{t-1}; the token before the first is state_in
-    const T *yp = static_cast<const T *>(a.y.p) + (size_t)b * a.y.sb + ch;
+    const Slice<T, VEC> gs(a.g, b, c0, t0, lane), ds(a.dy, b, c0, t0, lane), xs(a.x, b, c0, t0, lane),
+        ys(a.y, b, c0, t0 - 1, lane),  // y one token earlier: h_{t-1}; the token before the first is state_in
+        os(a.o1, b, c0, t0, lane), qs(a.o2, b, c0, t0, lane);
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
         if (FULL || i < m) {
-            gr[i] = load<T, VEC>(a.g, go + (size_t)i * a.g.st);
-            dr[i] = load<T, VEC>(a.dy, dyo + (size_t)i * a.dy.st);
+            gr[i] = gs.load(i);
+            dr[i] = ds.load(i);
         }
     }
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
         if (FULL || i < m) {
-            if (i > 0 || t0 > 0)
-                yr[i] = __ldg(reinterpret_cast<const raw_t<T, VEC> *>(yp + ((size_t)t0 + i - 1) * a.y.st));
-            if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = load<T, VEC>(a.x, xo + (size_t)i * a.x.st);
+            if (i > 0 || t0 > 0) yr[i] = ys.load(i);
+            if constexpr (GATE != HLA_GATE_GIVEN) xr[i] = xs.load(i);
         }
     }
-    const Bwd<VEC> r = rate_of<GATE, Bwd<VEC>>(a, ch);
-    Bwd<VEC> h0 = splat<Bwd<VEC>>(0.f), kept[TS], A = splat<Bwd<VEC>>(1.f), Bv = splat<Bwd<VEC>>(0.f);
+    const Num<T, VEC> r = rate_of<GATE, Num<T, VEC>>(a, ch);
+    Num<T, VEC> h0 = splat<Num<T, VEC>>(0.f), kept[TS], A = splat<Num<T, VEC>>(1.f), Bv = splat<Num<T, VEC>>(0.f);
     if (t0 == 0 && a.state_in) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
@@ -308,12 +305,12 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     }
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
-        Bwd<VEC> g, dy;
+        Num<T, VEC> g, dy;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
         kept[i] = gate_keep<GATE>(g, r);
-        if (!FULL && i >= m) kept[i] = splat<Bwd<VEC>>(kKeptOff<GATE>);
-        const Bwd<VEC> at = kept_a<GATE>(kept[i]);
+        if (!FULL && i >= m) kept[i] = splat<Num<T, VEC>>(kKeptOff<GATE>);
+        const Num<T, VEC> at = kept_a<GATE>(kept[i]);
         Bv = mul_(at, add_(dy, Bv));
         A = mul_(A, at);
     }
@@ -324,23 +321,22 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     if (!look_back<VEC>(sh, a, chain, pos, first, a.d_state_out ? a.d_state_out + so : nullptr, c0,
                         tile == 0 && a.out_state ? a.out_state + so : nullptr))
         return;
-    Bwd<VEC> c = before_warp<Bwd<VEC>>(sh, warp, lane), sum = splat<Bwd<VEC>>(0.f);
-    const size_t dxo = (size_t)b * a.o1.sb + (size_t)t0 * a.o1.st + ch, dgo = (size_t)b * a.o2.sb + (size_t)t0 * a.o2.st + ch;
+    Num<T, VEC> c = before_warp<Num<T, VEC>>(sh, warp, lane), sum = splat<Num<T, VEC>>(0.f);
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
-        Bwd<VEC> g, dy, x = splat<Bwd<VEC>>(0.f), y, dx, dg, drv;
+        Num<T, VEC> g, dy, x = splat<Num<T, VEC>>(0.f), y, dx, dg, drv;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
         unpack(yr[i], y.v);
         if (i == 0 && t0 == 0) y = h0;
         if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
-        const Bwd<VEC> gh = add_(dy, c);
+        const Num<T, VEC> gh = add_(dy, c);
         gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv);
         c = mul_(kept_a<GATE>(kept[i]), gh);
         if (FULL || i < m) {
             if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
-            store<T, VEC>(a.o1, dxo + (size_t)i * a.o1.st, dx.v);
-            store<T, VEC>(a.o2, dgo + (size_t)i * a.o2.st, dg.v);
+            os.store(i, dx.v);
+            qs.store(i, dg.v);
         }
     }
     if constexpr (GATE == HLA_GATE_RATE) {
@@ -366,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const Args a) {
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
     take_place(sh, a);
-    const size_t chains = (size_t)a.B * a.slices;
-    const int pos = (int)(sh.ticket / chains);   // counts from the last tile
-    const size_t chain = sh.ticket % chains;
+    const unsigned chains = (unsigned)a.B * a.slices, ticket = __shfl_sync(0xffffffffu, (unsigned)sh.ticket, 0);
+    const int pos = (int)(ticket / chains);  // counts from the last tile
+    const unsigned chain = ticket % chains;
     const int b = (int)(chain / a.slices), c0 = (int)(chain % a.slices) * C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = c0 + lane * VEC;
     const int len = length_of(a, b), tile = a.tiles - 1 - pos;
@@ -379,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const Args a) {
     }
     if (tile * TILE_T >= len) return;
     // warp 0 takes the tile's last tokens: the warps follow the scan's direction
-    const int t0 = tile * TILE_T + (WARPS - 1 - warp) * TS;
+    const int t0 = tile * TILE_T + (WARPS - 1 - __shfl_sync(0xffffffffu, warp, 0)) * TS;
     const int m = ch < a.d ? min(TS, len - t0) : 0;
 
     if ((tile + 1) * TILE_T <= len && c0 + C <= a.d)
@@ -420,13 +416,13 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const Args a) {
     if (e >= cols * a.B) return;
     const int b = (int)(e / cols), ch = (int)(e % cols) * VEC;
     if (a.lengths && a.lengths[b] <= 0) return;
-    Fwd<VEC> x, g, h, ea, eb;
+    Num<T, VEC> x, g, h, ea, eb;
     unpack(load<T, VEC>(a.x, (size_t)b * a.x.sb + ch), x.v);
     unpack(load<T, VEC>(a.g, (size_t)b * a.g.sb + ch), g.v);
     const size_t so = (size_t)b * a.d + ch;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.v[v] = a.state_in[so + v];
-    gate_fwd<GATE>(g, rate_of<GATE, Fwd<VEC>>(a, ch), x, ea, eb);
+    gate_fwd<GATE>(g, rate_of<GATE, Num<T, VEC>>(a, ch), x, ea, eb);
     h = fma_(ea, h, eb);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) a.out_state[so + v] = h.v[v];
@@ -539,7 +535,7 @@ hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, flo
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) {
-        if (w != W_STEP && pairs && stream_takes(a, sms))
+        if (w != W_STEP && pairs && stream_takes(a, p->in_dtype, sms))
             e = w == W_FWD ? stream_forward(a, p->in_dtype, p->gate, st)
                            : stream_backward(a, p->in_dtype, p->gate, d_rate, st);
         else if (p->in_dtype == HLA_F32)

@@ -70,6 +70,23 @@ template <typename T, int VEC>
 __device__ __forceinline__ raw_t<T, VEC> load(const Tensor &t, size_t off) {
     return __ldg(reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(t.p) + off));
 }
+// Rows seen by a whole warp: the row's address is the warp's (uniform registers), only the
+// channel differs from lane to lane.
+template <typename T, int VEC>
+struct Slice {
+    char *p;
+    long long st;
+    uint32_t ch;  // bytes
+    HLA_DEVICE Slice(const Tensor &t, int b, int c0, long long first, int lane)
+        : p(static_cast<char *>(const_cast<void *>(t.p)) + ((long long)b * t.sb + c0 + first * t.st) * (long long)sizeof(T)),
+          st(t.st * (long long)sizeof(T)), ch(lane * VEC * (uint32_t)sizeof(T)) {}
+    HLA_DEVICE raw_t<T, VEC> load(int i) const { return __ldg(reinterpret_cast<const raw_t<T, VEC> *>(p + i * st + ch)); }
+    HLA_DEVICE void store(int i, const float (&v)[VEC]) const {
+        raw_t<T, VEC> r;
+        pack(v, r);
+        *reinterpret_cast<raw_t<T, VEC> *>(p + i * st + ch) = r;
+    }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void store(const Tensor &t, size_t off, const float (&v)[VEC]) {
     raw_t<T, VEC> r;
@@ -79,18 +96,16 @@ __device__ __forceinline__ void store(const Tensor &t, size_t off, const float (
 
 // ------------------------------------------------------------ arithmetic on VEC channels
 // PAIR: two fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
-// scalar ones).  The forward kernels use it: fewer instructions to issue (32,768 tokens x 4,096
-// channels 247 -> 233 us).  The backward ones do not: pairs bind their operands to aligned
-// register pairs, which costs spilled registers there (2 x 8,192 x 4,096: 471 against 241 us).
+// scalar ones), fewer instructions to issue.  bf16 channels use it (32,768 x 4,096 forward 217
+// -> 207 us, 2 x 8,192 x 4,096 backward 235 -> 221 us); fp32 ones, whose inputs take twice the
+// registers, do not: pairs want aligned ones (4 x 2,048 x 4,096 forward 90 -> 82 us without).
 template <int VEC, bool PAIR>
 struct Vf {
     static constexpr int N = VEC;
     float v[VEC];
 };
-template <int VEC>
-using Fwd = Vf<VEC, VEC == 2>;
-template <int VEC>
-using Bwd = Vf<VEC, false>;
+template <typename T, int VEC>
+using Num = Vf<VEC, VEC == 2 && sizeof(T) == 2>;
 using Pair = Vf<2, true>;
 
 HLA_DEVICE unsigned long long pair(const Pair &x) {
@@ -290,7 +305,7 @@ HLA_DEVICE int length_of(const Args &a, int b) {
 // Streaming kernels (hla_gated_stream.cu), for channels in pairs: taken when the sequences'
 // channels alone give every SM a CTA.  The backward leaves the sequences' sums of the rates'
 // gradient in a.part [B][d] and adds them into d_rate (NULL: neither).
-bool stream_takes(const Args &a, int sms);
+bool stream_takes(const Args &a, hla_dtype t, int sms);
 cudaError_t stream_forward(const Args &a, hla_dtype t, int gate, cudaStream_t st);
 cudaError_t stream_backward(const Args &a, hla_dtype t, int gate, float *d_rate, cudaStream_t st);
 

@@ -84,7 +84,8 @@ Args make(const hla_window_params *p) {
     Args a{};
     a.B = p->B; a.H = p->H; a.Hkv = p->Hkv; a.G = p->H / p->Hkv;
     a.n = p->n; a.nk = p->nk; a.p0 = p->nk - p->n;
-    a.d = p->d; a.dv = p->dv; a.window = p->window; a.sinks = p->sinks;
+    a.d = p->d; a.dv = p->dv; a.window = p->window;
+    a.sinks = p->sinks < p->nk ? p->sinks : p->nk;  // more than there are tokens means the same
     a.scale = p->scale;
     a.lengths = p->lengths;
     return a;
@@ -138,14 +139,13 @@ cudaError_t simt(const Args &a, bool backward, cudaStream_t st) {
 template <typename E>
 __global__ void __launch_bounds__(128) fill_kernel(const Args a, View kc, View vc, int blocks) {
     const int u = blockIdx.x / blocks, hk = u % a.Hkv, b = u / a.Hkv, len = length_of(a, b);
-    const int cap = a.sinks + a.window;
-    for (int s = blockIdx.x % blocks * 4 + (threadIdx.x >> 5); s < cap; s += blocks * 4) {
-        int j = s;  // the last token below len that lies in slot s
-        if (s >= a.sinks && len > cap) {
-            const int r = s - a.sinks, last = len - 1 - a.sinks;  // (j - sinks) % window == r, j < len
+    const int cap = a.sinks + a.window, used = min(cap, len);
+    for (unsigned s = blockIdx.x % blocks * 4 + (threadIdx.x >> 5); s < (unsigned)used; s += blocks * 4) {
+        int j = (int)s;  // the last token below len that lies in slot s
+        if (j >= a.sinks && len > cap) {
+            const int r = j - a.sinks, last = len - 1 - a.sinks;  // (j - sinks) % window == r, j < len
             j = a.sinks + last - (last - r) % a.window;
         }
-        if (j >= len) continue;
         const E *k = static_cast<const E *>(a.k.p) + (size_t)b * a.k.sb + (size_t)hk * a.k.sh + (size_t)j * a.k.st;
         const E *v = static_cast<const E *>(a.v.p) + (size_t)b * a.v.sb + (size_t)hk * a.v.sh + (size_t)j * a.v.st;
         E *ko = static_cast<E *>(kc.p) + (size_t)b * kc.sb + (size_t)hk * kc.sh + (size_t)s * kc.st;

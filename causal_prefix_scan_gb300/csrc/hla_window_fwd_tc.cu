@@ -6,10 +6,15 @@
 // running maximum and sum, P packed to bf16 over S's own columns, O += P V with P read from
 // TMEM.  While the softmax of one query tile runs, the tensor cores work on the other.
 // Persistent: one CTA per SM goes through the items, so that an item's output and the next
-// one's first loads and products overlap.  Warps 0-15: softmax, four warps per (query tile,
-// half of the key columns), one row per thread, the halves' maxima exchanged through shared
-// memory (with whole rows per thread the softmax took longer than the products beside it);
-// warp 16: MMA; warp 17: TMA into a ring of key and value tiles.
+// one's first loads and products overlap (552 -> 523 us on h32 n16384 d128 w2048).  Warps 0-7:
+// softmax, four warps per query tile, one row per thread, so that maxima and sums need no
+// exchange; warp 8: MMA; warp 9: TMA into a ring of key and value tiles.
+//
+// The MMA warp takes the two tiles in strict turns, P V of one directly before its next S:
+// the tiles stay half a period apart, and the tensor cores have one tile's products while the
+// other's softmax runs.  With a warp per tile, or in the order in which P comes, they fall
+// into step (576 and 656 us against 444).  A key tile takes both query tiles together some
+// 3,500 cycles: their four products are 58 % of that, the waits between softmax and MMA the rest.
 //
 // The running maximum used in the exponent only moves when a row's maximum passes it by
 // more than 2^8: P then stays below 2^8, and O in TMEM is rescaled a few times per row

@@ -380,3 +380,17 @@ def test_offsets_beyond_32_bits_with_many_channels():
     r = hla.gated_backward(x, c["g"], y, c["dy"], "sigmoid")
     want = ref.gated_backward(c["x"], c["g"], y, c["dy"], "sigmoid")
     ref.close(r.dg, *want["dg"], "dg")
+
+
+@pytest.mark.parametrize("st", [5_590_000, 5_600_000])
+def test_many_channels_with_tokens_far_apart(st):
+    """Token strides on both sides of the largest whose offsets within a tile have 32 bits."""
+    n, d = 390, 2560  # more than a tile of tokens
+    c = inputs(1, n, d, "sigmoid", BF16, seed=4)
+    far = torch.empty((n - 1) * st + d, dtype=BF16, device="cuda").as_strided((1, n, d), (0, st, 1))
+    for name in ("x", "g", "dy"):
+        far.copy_(c[name])
+        check(dict(c, **{name: far}))
+    y = hla.gated_forward(c["x"], c["g"], "sigmoid", state_in=c["state_in"])
+    assert torch.equal(hla.gated_forward(c["x"], c["g"], "sigmoid", state_in=c["state_in"], out=far), far)
+    assert float((far.float() - y.float()).abs().max()) <= 2 ** -7 * float(y.float().abs().max())

@@ -75,6 +75,12 @@ def test_windows_around_the_tiles(window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window,sinks", [(5, 2 ** 31 - 1), (2 ** 31 - 1, 5), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_largest_window_and_sinks(window, sinks, dtype):
+    check(*inputs(1, 2, 1, 300, 300, 64, 64, dtype, seed=9), window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n,nk", [(260, 260), (100, 260)])
 def test_padded_batch(n, nk, dtype):
     """Rows behind a length hold NaN and infinities, and outputs there stay as they were."""
