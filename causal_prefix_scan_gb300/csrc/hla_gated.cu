@@ -10,16 +10,19 @@
 // scan in the other direction, of c_t = a_t gh_t (the gradient that token t hands to
 // token t-1): gh_t = dy_t + c_{t+1}, c_t = a_t c_{t+1} + a_t dy_t.
 //
-// Bound by HBM: every input element is read once and every output element written once
-// (x, g -> y; g, y, dy[, x] -> dx, dg), with a few fp32 operations on each.  One CTA takes
-// a tile of 8 warps x kTS tokens by 32 lanes x VEC channels, holds it in registers, and
-// gets the state before its tile from the tiles before it while its own loads are the only
-// traffic: each tile publishes its map (A, B) as soon as it has it, then looks back over
-// the published maps to the nearest published state, folds forward from there, and
-// publishes its own state.  The fold always runs state -> later tiles in order with the
-// same fmaf, so a state has the same bits wherever the look-back found its start: results
-// do not depend on timing.  Reading the inputs a second time instead (maps, scan, states)
-// would move 5/3 of the forward's bytes.
+// Every input element is read once and every output element written once (x, g -> y; g, y,
+// dy[, x] -> dx, dg), with a few fp32 operations on each.  One CTA takes a tile of 8 warps x
+// kTS tokens by 32 lanes x VEC channels, holds it in registers, and gets the state before its
+// tile from the tiles before it while its own loads are the only traffic: each tile publishes
+// its map (A, B) as soon as it has it, then looks back over the published maps to the nearest
+// published state, folds forward from there, and publishes its own state.  The fold always runs
+// state -> later tiles in order with the same fmaf, so a state has the same bits wherever the
+// look-back found its start: results do not depend on timing.  Reading the inputs a second time
+// instead (maps, scan, states) would move 5/3 of the forward's bytes.
+//
+// Measured: forward 3 x 5,003 x 1,001 fp32 (ragged) 52 us, 2.4 TB/s; 16,384 x 1,024 bf16 with
+// rates 46 us, 2.2 TB/s; backward 4 x 2,048 x 512 bf16 25 us, 2.0 TB/s.  What bounds it is the
+// path of one CTA, loads -> gates -> look-back -> stores, and how many CTAs are on it at once.
 #include "hla_gated.cuh"
 
 namespace hla {
@@ -28,11 +31,15 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int kThreads = WARPS * 32;
-// Tokens of one thread: as many as leave what it holds of them in registers at two CTAs per
-// SM (the backward's four inputs and pairs of fp32 channels take twice the room).
+// CTAs per SM, and tokens of one thread: as many as leave what it holds of them in registers
+// (the backward's four inputs take twice the room).  A CTA mostly waits, for its loads and for
+// the tiles before it: single channels gain from four per SM (3 x 5,003 x 1,001 fp32 forward 66
+// -> 52 us), pairs have room for two (three spill: 4 x 2,048 x 512 backward 26 -> 29 us).
 enum Dir { FWD, BWD };
+template <int VEC>
+constexpr int kCtas = VEC == 1 ? 4 : 2;
 template <typename T, Dir DIR, int VEC>
-constexpr int kTS = DIR == FWD && VEC * sizeof(T) <= 4 ? 16 : 8;
+constexpr int kTS = DIR == FWD ? 16 : 8;
 template <typename T, Dir DIR, int VEC>
 constexpr int kTileT = WARPS * kTS<T, DIR, VEC>;  // tokens of one tile
 constexpr int kTileLeast = WARPS * 8;
@@ -245,7 +252,7 @@ HLA_DEVICE void fwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 }
 
 template <typename T, int GATE, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtas<VEC>) gated_fwd_kernel(const Args a) {
     constexpr int TS = kTS<T, FWD, VEC>, TILE_T = kTileT<T, FWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
@@ -357,7 +364,7 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
 }
 
 template <typename T, int GATE, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtas<VEC>) gated_bwd_kernel(const Args a) {
     constexpr int TS = kTS<T, BWD, VEC>, TILE_T = kTileT<T, BWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
@@ -497,6 +504,11 @@ size_t workspace_bytes_of(const hla_gated_params *p) {
 
 enum Which { W_FWD, W_BWD, W_STEP };
 
+// The forward takes fp32 channels one per lane always: a row is 128 bytes per warp even so, and
+// twice the CTAs fit an SM (16,384 x 1,024 fp32 78 -> 52 us; the backward 102 us in pairs, 106 singly).
+template <typename T, int VEC>
+constexpr bool kFwdTakes = VEC * sizeof(T) <= 4;
+
 template <typename T, int GATE, int VEC>
 cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
     a.slices = slices_of<VEC>(a.d);
@@ -508,9 +520,11 @@ cudaError_t launch(Which w, Args a, float *d_rate, cudaStream_t st) {
     }
     const unsigned grid = (unsigned)((size_t)a.B * a.slices * a.tiles);
     if (a.tiles <= 1) a.hdr = nullptr;  // no tile waits for another
-    if (w == W_FWD) {
-        gated_fwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
-        return cudaGetLastError();
+    if constexpr (kFwdTakes<T, VEC>) {
+        if (w == W_FWD) {
+            gated_fwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
+            return cudaGetLastError();
+        }
     }
     gated_bwd_kernel<T, GATE, VEC><<<grid, kThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
@@ -539,7 +553,7 @@ hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, flo
             e = w == W_FWD ? stream_forward(a, p->in_dtype, p->gate, st)
                            : stream_backward(a, p->in_dtype, p->gate, d_rate, st);
         else if (p->in_dtype == HLA_F32)
-            e = pairs ? by_gate<float, 2>(p->gate, w, a, d_rate, st) : by_gate<float, 1>(p->gate, w, a, d_rate, st);
+            e = pairs && (w != W_FWD || kFwdTakes<float, 2>) ? by_gate<float, 2>(p->gate, w, a, d_rate, st) : by_gate<float, 1>(p->gate, w, a, d_rate, st);
         else
             e = pairs ? by_gate<__nv_bfloat16, 2>(p->gate, w, a, d_rate, st)
                       : by_gate<__nv_bfloat16, 1>(p->gate, w, a, d_rate, st);

@@ -6,6 +6,10 @@
 // up to 16 CTAs shares the slots of one pair: each runs a softmax over its own tiles of 64
 // slots, and the cluster joins the partial results through distributed shared memory, in
 // the order of the ranks (one launch, no workspace, the same bits on every call).
+//
+// Measured, bf16, 32 query and 8 key/value heads of width 128: 64 sequences with 1,024 + 16 slots
+// (ragged) 52 us, 4.5 TB/s; one sequence with 4,096 + 16 slots 14.8 us, 1.1 TB/s, which is the
+// latency of a launch in clusters, two dependent loads and the join, not bandwidth.
 #include "hla_window.h"
 
 #include <cooperative_groups.h>
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
 //   O^T [16 columns x 8 heads] += V^T P^T: a thread loads four rows' chunk of columns 8 g ..
 //     8 g + 7 and packs pairs of rows; row g and g + 8 of product t are columns 8 g + 2 t, + 1.
 // (lane = 4 g + q.)  mma.sync suffices: the work per byte is that of 8 heads, and the loads
-// bound it; tcgen05 would want 128 rows of queries and the operands staged in shared memory.
+// bound it (on the CUDA cores, step_kernel, the two sizes above take 852 and 64 us); tcgen05 would want 128 rows of queries and the operands staged in shared memory.
 // The next 16 slots' K is loaded while this P is formed, their V while O is added up, so
 // a warp has 4 to 8 KB on their way at all times.
 constexpr int kWarps = 8, GS = 16;
@@ -452,8 +456,9 @@ cudaError_t by_width(const StepArgs &a, cudaStream_t st) {
 
 cudaError_t step(const StepArgs &in, hla_dtype dt, cudaStream_t st) {
     StepArgs a = in;
-    // CTAs for a pair: enough that all pairs together give every SM some, no more than
-    // tiles of slots, a power of two up to 16
+    // CTAs for a pair: enough that all pairs together give every SM two, no more than tiles of
+    // slots, a power of two up to 16.  64 x 8 pairs: 1 CTA each 52 us, 2 59, 4 80; 8 pairs of
+    // 4,112 slots: 16 CTAs each 14.8 us, 8 14.6, 4 19.2.
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

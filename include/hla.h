@@ -546,8 +546,8 @@ typedef struct {
 } hla_window_params;
 
 /* o, and lse [B][H][n] fp32 contiguous (or NULL).  One launch.  bf16 with 16-byte aligned
- * rows (pointers, strides and widths in multiples of 8 elements) runs on the tensor cores,
- * everything else on the CUDA cores in fp32. */
+ * rows (pointers, strides and widths in multiples of 8 elements) and a positive scale runs
+ * on the tensor cores, everything else on the CUDA cores in fp32. */
 HLA_API hla_status hla_window_forward(const hla_window_params *p, const hla_tensor *q, const hla_tensor *k,
                                       const hla_tensor *v, const hla_tensor *o, float *lse, void *stream);
 
