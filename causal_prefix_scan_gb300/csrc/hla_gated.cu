@@ -458,6 +458,7 @@ hla_status check(const hla_gated_params *p) {
     if (p->gate != HLA_GATE_GIVEN && p->gate != HLA_GATE_SIGMOID && p->gate != HLA_GATE_RATE)
         return report(HLA_ERR_ARG, "unknown gate");
     if (p->gate == HLA_GATE_RATE && !p->rate) return report(HLA_ERR_ARG, "HLA_GATE_RATE needs rate");
+    if (p->n > 2147483647 - 1024) return report(HLA_ERR_ARG, "problem too large");  // token counters pass n by up to two tiles
     const double tiles = most_tiles(p), slices = (double)((p->d + 31LL) / 32);
     if ((double)p->B * (tiles < 1 ? 1 : tiles) * slices > 2147483647.0 || (double)p->B * p->d > 1099511627776.0)
         return report(HLA_ERR_ARG, "problem too large");

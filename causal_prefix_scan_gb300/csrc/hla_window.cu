@@ -35,7 +35,8 @@ hla_status check(const hla_window_params *p, bool step) {
     if (!std::isfinite(p->scale)) return report(HLA_ERR_ARG, "scale must be finite");
     if (step) {
         if (p->n != 1) return report(HLA_ERR_ARG, "a step takes one token: n must be 1");
-        if ((long long)p->sinks + p->window > 2147483647LL - 64) return report(HLA_ERR_ARG, "too many slots");
+        if ((long long)p->sinks + p->window > 2147483647LL - 4096)  // the kernels' slot counters have 32 bits
+            return report(HLA_ERR_ARG, "too many slots");
         if ((double)p->B * p->H > 2147483647.0 / 16) return report(HLA_ERR_ARG, "problem too large");
     } else {
         if (p->n < 0 || p->nk < p->n) return report(HLA_ERR_ARG, "need 0 <= n <= nk");

@@ -84,7 +84,7 @@ struct Place {
         heads = min(HG, a.G - g * HG);
         p = a.pos[b];
         const long long cap = (long long)a.sinks + a.window;
-        slots = (int)(p + 1 < cap ? p + 1 : cap);
+        slots = (int)(p < cap ? p + 1 : cap);
         slot = p < 0 ? 0 : p < a.sinks ? (int)p : a.sinks + (int)((p - a.sinks) % a.window);
     }
 };

@@ -33,7 +33,7 @@ def wp(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(n=-1), dict(d=0), dict(in_dtype=5), dict(gate=3), dict(gate=-1),
-                                dict(gate=hla.HLA_GATE_RATE), dict(B=1 << 30, n=1 << 30)])
+                                dict(gate=hla.HLA_GATE_RATE), dict(B=1 << 30, n=1 << 30), dict(n=2147483647)])
 def test_gated_params(lib, kw):
     p = gp(**kw)
     b = ctypes.byref(p)
@@ -114,6 +114,7 @@ def test_window_arguments(lib):
     assert step(vc=T(20480)) == ARG and step(kc=T(8192)) == ARG and step(o=T(4096)) == ARG
     assert step(kc=T(20480, st=0)) == ARG                               # slots overlap
     assert step(p=ctypes.byref(wp(n=1, window=2147483647, sinks=5))) == ARG
+    assert step(p=ctypes.byref(wp(n=1, window=2147483640, sinks=0))) == ARG  # counters of slots would overflow
     fill = lambda k=k, v=v, kc=kc, vc=vc: lib.hla_window_cache_fill(b, k, v, kc, vc, None)  # noqa: E731
     assert fill(k=None) == ARG and fill(vc=None) == ARG and fill(kc=T(8192)) == ARG and fill(vc=T(20480)) == ARG
 
