@@ -550,7 +550,7 @@ hla_status dispatch(const hla_gated_params *p, Which w, Args &a, bool pairs, flo
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) {
-        if (w != W_STEP && pairs && stream_takes(a, p->in_dtype, sms))
+        if (w != W_STEP && pairs && stream_takes(a, p->in_dtype, w == W_BWD, sms))
             e = w == W_FWD ? stream_forward(a, p->in_dtype, p->gate, st)
                            : stream_backward(a, p->in_dtype, p->gate, d_rate, st);
         else if (p->in_dtype == HLA_F32)

@@ -303,9 +303,9 @@ HLA_DEVICE int length_of(const Args &a, int b) {
 }
 
 // Streaming kernels (hla_gated_stream.cu), for channels in pairs: taken when the sequences'
-// channels alone give every SM a CTA.  The backward leaves the sequences' sums of the rates'
+// channels alone give (nearly) every SM a CTA.  The backward leaves the sequences' sums of the rates'
 // gradient in a.part [B][d] and adds them into d_rate (NULL: neither).
-bool stream_takes(const Args &a, hla_dtype t, int sms);
+bool stream_takes(const Args &a, hla_dtype t, bool backward, int sms);
 cudaError_t stream_forward(const Args &a, hla_dtype t, int gate, cudaStream_t st);
 cudaError_t stream_backward(const Args &a, hla_dtype t, int gate, float *d_rate, cudaStream_t st);
 

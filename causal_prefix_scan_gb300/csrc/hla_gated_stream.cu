@@ -315,18 +315,22 @@ cudaError_t by_gate(const Args &a, int gate, bool backward, cudaStream_t st) {
 
 }  // namespace
 
-// Against the look-back kernels (bf16 with rates, us, forward | backward):
-//   channels of all sequences / 16     here          look-back
-//     64  (16,384 x 1,024)             78 | 170      46 | 95
-//    128  (16,384 x 2,048)             85 | 181      85 | 177
-//    160  (2 x 8,192 x 1,280)          55 | 114      55 | 113
-//    256  (8,192 x 4,096)              57 | 116      81 | 168
-bool stream_takes(const Args &a, hla_dtype t, int sms) {
+// Against the look-back kernels (with rates, us): CTAs here, forward and backward of both.
+//                               bf16 here   look-back    fp32 here   look-back
+//    64  1 x 16,384 x 1,024      64 | 170     46 |  95
+//   104  1 x 16,384 x 1,664      69 | 177     70 | 141     82 | 206    75 | 154
+//   128  1 x 16,384 x 2,048      69 | 185     84 | 170     83 | 216    89 | 186
+//   144  2 x  8,192 x 1,152      39 |  98     50 | 101     47 | 114    53 | 111
+//   160  2 x  8,192 x 1,280      55 | 114     55 | 110
+//   256  1 x  8,192 x 4,096      57 | 117     81 | 163
+// The forward is ahead from about three quarters of the SMs on, the backward from all of them.
+bool stream_takes(const Args &a, hla_dtype t, bool backward, int sms) {
     constexpr int most = (kWarpsFwd > kWarpsBwd ? kWarpsFwd : kWarpsBwd) * GROUPS * TS;  // tokens of a tile
     const long long st_end = (1LL << 32) / (most * (t == HLA_F32 ? 4 : 2));              // a tile's offsets have 32 bits
     for (const Tensor *x : {&a.x, &a.g, &a.y, &a.dy, &a.o1, &a.o2})
         if (x->st >= st_end) return false;
-    return (long long)a.B * ((a.d + CW - 1) / CW) >= sms;
+    const long long ctas = (long long)a.B * ((a.d + CW - 1) / CW);
+    return 4 * ctas >= (backward ? 4 : 3) * sms;
 }
 cudaError_t stream_forward(const Args &a, hla_dtype t, int gate, cudaStream_t st) {
     return t == HLA_F32 ? by_gate<float>(a, gate, false, st) : by_gate<__nv_bfloat16>(a, gate, false, st);

@@ -9,7 +9,8 @@ namespace win {
 namespace {
 
 // Far shares of a key tile with first tokens (see dkv_kernel): its queries beyond the
-// window are divided so that a share is about as long as a tile's own window.
+// window are divided so that a share is about as long as a tile's own window (one share for
+// all of them: B2 H16 n8192 w1024 backward 857 us against 509, B3 H6 n1501 w301 66 against 45).
 constexpr int kFarMost = 32;
 int far_shares(const hla_window_params *p, int tile) {
     if (p->sinks == 0 || p->n == 0) return 0;
