@@ -17,7 +17,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import math
 import os
 from collections import namedtuple
 from dataclasses import dataclass
@@ -626,13 +625,11 @@ def _t4(t):
 
 
 def _zeroed(like, shapes):
-    """Zeroed tensors of these shapes in one allocation, each on a 256-byte boundary."""
+    """Zeroed tensors of these shapes, by one launch."""
     import torch
-    unit = 256 // like.element_size()
-    sizes = [math.prod(s) for s in shapes]
-    parts = torch.zeros(sum(-(-n // unit) * unit for n in sizes), dtype=like.dtype, device=like.device).split(
-        [-(-n // unit) * unit for n in sizes])
-    return tuple((x if x.numel() == n else x[:n]).view(s) for x, n, s in zip(parts, sizes, shapes))
+    out = tuple(torch.empty(s, dtype=like.dtype, device=like.device) for s in shapes)
+    torch._foreach_zero_(out)
+    return out
 
 
 def _int32(x, name):
