@@ -41,11 +41,11 @@ HLA_DEVICE void tma_load_4d(void *dst, const void *tmap, uint64_t *bar, int c0, 
         "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
-// A tile of `ROWS` rows and DP columns (DP / 64 boxes) at row r0 of (b, h).
-template <int DP, int ROWS = T>
+// A tile of T rows and DP columns (DP / 64 boxes) at row r0 of (b, h).
+template <int DP>
 HLA_DEVICE void load_tile(uint8_t *dst, const CUtensorMap *m, const View &v, uint64_t *bar, int r0, int h, int b) {
 #pragma unroll
-    for (int c = 0; c < DP; c += 64) tma_load_4d(dst + (c >> 6) * ROWS * 128, m, bar, c, r0, v.sh ? h : 0, v.sb ? b : 0);
+    for (int c = 0; c < DP; c += 64) tma_load_4d(dst + (c >> 6) * T * 128, m, bar, c, r0, v.sh ? h : 0, v.sb ? b : 0);
 }
 
 HLA_DEVICE void mbar_arrive(uint64_t *bar) {
@@ -116,13 +116,13 @@ HLA_DEVICE void mma_ts32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, boo
 HLA_DEVICE uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // Descriptors of a tile: contraction over its columns, or over its rows.
 HLA_DEVICE uint64_t kmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), 16u, 1024u); }
-HLA_DEVICE uint64_t mnmajor(const uint8_t *tile, int rows = T) { return make_sdesc(smem_u32(tile), rows * 128u, 1024u); }
-// The whole width of two tiles, of T and RB rows (64 columns per block; zero columns behind the
+HLA_DEVICE uint64_t mnmajor(const uint8_t *tile) { return make_sdesc(smem_u32(tile), T * 128u, 1024u); }
+// The whole width of two tiles (64 columns per block; zero columns behind the
 // tensors' own are multiplied too): `wide` takes both blocks of DP = 128.
-template <int DP, int RB = T>
+template <int DP>
 HLA_DEVICE void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool wide) {
     mma_ss64(d, a, b, idesc, false);
-    if (DP > 64 && wide) mma_ss64(d, a + T * 8, b + RB * 8, idesc, true);
+    if (DP > 64 && wide) mma_ss64(d, a + T * 8, b + T * 8, idesc, true);
 }
 
 // 32 columns of 32-bit words, this warp's lanes.
@@ -148,14 +148,14 @@ HLA_DEVICE void mask32(float (&v)[32], uint32_t bits, float other) {
     for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : other;
 }
 
-// Zeroes rows [r0, ROWS) of a tile (one warp) and shows the tensor cores the result: rows behind
+// Zeroes rows [r0, T) of a tile (one warp) and shows the tensor cores the result: rows behind
 // a sequence may be anything, and 0 times that is not 0 where they are contracted over.
-template <int DP, int ROWS = T>
+template <int DP>
 HLA_DEVICE void zero_rows(uint8_t *tile, int r0, int lane) {
 #pragma unroll
     for (int c = 0; c < DP; c += 64)
-        for (int e = (r0 << 3) + lane; e < ROWS * 8; e += 32)
-            reinterpret_cast<uint4 *>(tile + (c >> 6) * ROWS * 128)[e] = make_uint4(0, 0, 0, 0);
+        for (int e = (r0 << 3) + lane; e < T * 8; e += 32)
+            reinterpret_cast<uint4 *>(tile + (c >> 6) * T * 128)[e] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
 }
