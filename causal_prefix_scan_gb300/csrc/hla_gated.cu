@@ -24,6 +24,7 @@
 // rates 46 us, 2.2 TB/s; backward 4 x 2,048 x 512 bf16 25 us, 2.0 TB/s.  What bounds it is the
 // path of one CTA, loads -> gates -> look-back -> stores, and how many CTAs are on it at once.
 #include "hla_gated.cuh"
+#include "hla_look_back.h"
 
 namespace hla {
 namespace gated {
@@ -45,9 +46,8 @@ constexpr int kTileT = WARPS * kTS<T, DIR, VEC>;  // tokens of one tile
 constexpr int kTileLeast = WARPS * 8;
 constexpr int BACK = 8;               // windows of WARPS earlier tiles kept by one look-back
 
-// `tag` of a record: 4 * (number of the call) + kind; anything else is left over from
-// another call.
-enum : unsigned long long { REC_MAP = 1, REC_STATE = 2 };
+// `tag` of a record: 4 * (number of the call) + kind (hla_look_back.h); anything else is left
+// over from another call.
 
 // Workspace: header, then one record per channel slot of every tile, then (backward with
 // HLA_GATE_RATE) one partial sum per channel slot of every tile, in records with tag 0.
@@ -123,9 +123,10 @@ __device__ __forceinline__ bool look_back(Shared<VEC> &sh, const Args &a, size_t
         if (tid < C && init && c0 + tid < a.d) h = init[c0 + tid];
     } else {
         if (tid < C) publish(rec + (size_t)pos * C + tid, A, Bv, 4 * call + REC_MAP);
-        int found = -1;  // index in sh.back of the state this channel starts from
+        using Start = FoldStart<BACK, WARPS>;  // index in sh.back of the state this channel starts from
+        Start start;
         for (int r = 0;; ++r) {
-            const int slot = r < BACK ? r : BACK - 1;
+            const int slot = Start::slot(r);
             const int prev = pos - 1 - (slot * WARPS + warp);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool look_back(Shared<VEC> &sh, const Args &a, size_t
                 int kind = 0;
                 if (prev >= first) {
                     // past the kept windows: wait for the states of the last one
-                    ok = await_record(rec + (size_t)prev * C + c, call, r >= BACK, x, a.err) && ok;
+                    ok = await_record(rec + (size_t)prev * C + c, call, Start::states_only(r), x, a.err) && ok;
                     kind = (int)(x.tag & 3);
                 }
                 sh.back[slot * WARPS + warp][c] = make_float2(x.a, x.b);
@@ -144,17 +145,12 @@ __device__ __forceinline__ bool look_back(Shared<VEC> &sh, const Args &a, size_t
                 if (tid < C) publish(rec + (size_t)pos * C + tid, 1.f, __int_as_float(0x7fc00000), 4 * call + REC_STATE);
                 return false;
             }
-            if (tid < C && found < 0) {
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w)
-                    if (found < 0 && sh.kind[w][tid] == (int)REC_STATE) found = slot * WARPS + w;
-            }
-            if (__syncthreads_and(tid >= C || found >= 0)) break;
+            if (tid < C) start.look(r, [&](int w) { return sh.kind[w][tid]; });
+            if (__syncthreads_and(tid >= C || start.found >= 0)) break;
         }
-        if (tid < C) {
-            h = sh.back[found][tid].y;
-            for (int i = found - 1; i >= 0; --i) h = fmaf(sh.back[i][tid].x, h, sh.back[i][tid].y);
-        }
+        if (tid < C)
+            h = start.fold([&](int i) { return sh.back[i][tid].y; },
+                           [&](int i, float x) { return fmaf(sh.back[i][tid].x, x, sh.back[i][tid].y); });
     }
     if (tid < C) {
         sh.carry[tid] = h;
