@@ -311,9 +311,12 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
         Num<T, VEC> g, dy;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
-        kept[i] = gate_keep<GATE>(g, r);
-        if (!FULL && i >= m) kept[i] = splat<Num<T, VEC>>(kKeptOff<GATE>);
-        const Num<T, VEC> at = kept_a<GATE>(kept[i]);
+        Num<T, VEC> at;
+        kept[i] = gate_keep<GATE>(g, r, at);
+        if (!FULL && i >= m) {
+            kept[i] = splat<Num<T, VEC>>(kKeptOff<GATE>);
+            at = splat<Num<T, VEC>>(1.f);
+        }
         Bv = mul_(at, add_(dy, Bv));
         A = mul_(A, at);
     }
@@ -327,15 +330,15 @@ HLA_DEVICE void bwd_tile(Shared<VEC> &sh, const Args &a, size_t chain, int pos, 
     Num<T, VEC> c = before_warp<Num<T, VEC>>(sh, warp, lane), sum = splat<Num<T, VEC>>(0.f);
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
-        Num<T, VEC> g, dy, x = splat<Num<T, VEC>>(0.f), y, dx, dg, drv;
+        Num<T, VEC> g, dy, x = splat<Num<T, VEC>>(0.f), y, dx, dg, drv, at;
         unpack(gr[i], g.v);
         unpack(dr[i], dy.v);
         unpack(yr[i], y.v);
         if (i == 0 && t0 == 0) y = h0;
         if constexpr (GATE != HLA_GATE_GIVEN) unpack(xr[i], x.v);
         const Num<T, VEC> gh = add_(dy, c);
-        gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv);
-        c = mul_(kept_a<GATE>(kept[i]), gh);
+        gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv, at);
+        c = mul_(at, gh);
         if (FULL || i < m) {
             if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
             os.store(i, dx.v);

@@ -205,10 +205,14 @@ HLA_DEVICE V sigmoid(const V &z) {
     const V e = each(mul_(z, splat<V>(-kLog2e)), ex2_approx);
     return each(add_(e, splat<V>(1.f)), rcp_approx);
 }
-// 1 - exp(-u) for u >= 0.  Below 1/16 the difference would cancel: Taylor's series to u^5,
-// whose next term is under 2^-29 of the sum there.
+// a = exp(-u) and w = 1 - a for u >= 0, both to a few units in the last place beside what u is
+// off by.  Below 1/16 the difference would cancel: w by Taylor's series to u^5, whose next term is under
+// 2^-29 of the sum there, and a = 1 - w, off by its rounding only (a long product of gates near one
+// multiplies their errors).  Above, a is the exponential itself: 1 - w would leave a small a with an error of
+// 2^-25, of which d_state_in, dg and the rates' gradient, all in proportion to a, are made.
+constexpr float kNear = 0.0625f;
 template <class V>
-HLA_DEVICE V one_minus_exp(const V &u) {
+HLA_DEVICE void exp_gate(const V &u, V &a, V &w) {
     const V e = each(mul_(u, splat<V>(-kLog2e)), ex2_approx);
     const V far = sub_(splat<V>(1.f), e);
     V p = fma_(u, splat<V>(1.f / 120.f), splat<V>(-1.f / 24.f));
@@ -216,9 +220,13 @@ HLA_DEVICE V one_minus_exp(const V &u) {
     p = fma_(p, u, splat<V>(-0.5f));
     p = fma_(p, u, splat<V>(1.f));
     p = mul_(p, u);
+    const V near = sub_(splat<V>(1.f), p);
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) p.v[i] = u.v[i] < 0.0625f ? p.v[i] : far.v[i];
-    return p;
+    for (int i = 0; i < V::N; ++i) {
+        const bool small = u.v[i] < kNear;
+        w.v[i] = small ? p.v[i] : far.v[i];
+        a.v[i] = small ? near.v[i] : e.v[i];
+    }
 }
 // 1 / sqrt(q) for q >= 0, finite at 0
 template <class V>
@@ -237,25 +245,44 @@ HLA_DEVICE void gate_fwd(const V &g, const V &r, const V &x, V &a, V &b) {
         sigmoid2(g, a, c);
         b = mul_(c, x);
     } else {
-        const V w = one_minus_exp(mul_(r, sigmoid(g)));  // 1 - a
-        a = sub_(splat<V>(1.f), w);
+        V w;
+        exp_gate(mul_(r, sigmoid(g)), a, w);
         const V q = fma_(w, a, w);  // 1 - a^2
         b = mul_(mul_(q, rsqrt0(q)), x);
     }
 }
-// What the backward pass keeps of a token's gate: a, or 1 - a with HLA_GATE_RATE, from which a
-// follows with the bits of gate_fwd's and the gradients without a second exponential.
+// A token's a, and what the backward pass keeps of its gate: a, or with HLA_GATE_RATE
+// whichever of 1 - a (sign bit clear) and a (sign bit set) exp_gate formed first.  The other is one
+// minus it, with exp_gate's bits, and the gradients need no second exponential.
 template <int GATE, class V>
-HLA_DEVICE V gate_keep(const V &g, const V &r) {
-    if constexpr (GATE == HLA_GATE_RATE) return one_minus_exp(mul_(r, sigmoid(g)));
-    V a, b;
-    gate_fwd<GATE>(g, r, splat<V>(0.f), a, b);
-    return a;
+HLA_DEVICE V gate_keep(const V &g, const V &r, V &a) {
+    V b;
+    if constexpr (GATE == HLA_GATE_RATE) {
+        const V u = mul_(r, sigmoid(g));
+        exp_gate(u, a, b);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) b.v[i] = u.v[i] < kNear ? b.v[i] : -a.v[i];
+        return b;
+    } else {
+        gate_fwd<GATE>(g, r, splat<V>(0.f), a, b);
+        return a;
+    }
 }
-template <int GATE, class V>
-HLA_DEVICE V kept_a(const V &k) {
-    if constexpr (GATE == HLA_GATE_RATE) return sub_(splat<V>(1.f), k);
-    return k;
+// a and w = 1 - a of what gate_keep returned with HLA_GATE_RATE
+template <class V>
+HLA_DEVICE void kept_gate(V k, V &a, V &w) {
+    V one;
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+        // formed again, not held in registers since gate_keep formed it, as the compiler would
+        // (2 x 8,192 x 4,096 backward: 200 bytes of a thread's registers spilled)
+        asm("" : "+f"(k.v[i]));
+        one.v[i] = __float_as_int(k.v[i]) < 0 ? 0.f : 1.f;  // by the sign bit: a may be zero
+    }
+    a = sub_(one, k);
+    const V o = sub_(splat<V>(1.f), a);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) w.v[i] = __float_as_int(k.v[i]) < 0 ? o.v[i] : k.v[i];
 }
 template <int GATE>
 constexpr float kKeptOff = GATE == HLA_GATE_RATE ? 0.f : 1.f;  // a token that is not there: a = 1
@@ -265,19 +292,23 @@ constexpr float kKeptOff = GATE == HLA_GATE_RATE ? 0.f : 1.f;  // a token that i
 // f = 0 (sigma(g) underflowed) has the limit 0 for every product with du/dg, du/dr.
 template <int GATE, class V>
 HLA_DEVICE void gate_bwd(const V &g, const V &r, const V &x, const V &y, const V &gh,
-                         const V &k, V &dx, V &dg, V &dr) {
+                         const V &k, V &dx, V &dg, V &dr, V &a) {
     if constexpr (GATE == HLA_GATE_GIVEN) {
         dx = gh;
+        a = k;
         dg = mul_(gh, y);
     } else if constexpr (GATE == HLA_GATE_SIGMOID) {
         V s, c;
         sigmoid2(g, s, c);
         dx = mul_(gh, c);
+        a = k;
         dg = mul_(mul_(dx, s), sub_(y, x));
     } else {
         V s, c;
         sigmoid2(g, s, c);
-        const V a = kept_a<GATE>(k), q = fma_(k, a, k);
+        V w;
+        kept_gate(k, a, w);
+        const V q = fma_(w, a, w);
         const V rf = rsqrt0(q);
         dx = mul_(gh, mul_(q, rf));
         const V du = mul_(mul_(gh, a), sub_(mul_(mul_(x, a), rf), y));

@@ -209,12 +209,13 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
             Num<T, 2> g, dy;
             unpack(gr[i], g.v);
             unpack(dr[i], dy.v);
-            kept[i] = gate_keep<GATE>(g, r);
+            Num<T, 2> at;
+            kept[i] = gate_keep<GATE>(g, r, at);
             if (!FULL && (!mine || base + t0 + i >= len)) {
                 kept[i] = splat<Num<T, 2>>(kKeptOff<GATE>);
+                at = splat<Num<T, 2>>(1.f);
                 dy = splat<Num<T, 2>>(0.f);
             }
-            const Num<T, 2> at = kept_a<GATE>(kept[i]);
             B = mul_(at, add_(dy, B));
             A = mul_(A, at);
         }
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
         if constexpr (GATE != HLA_GATE_GIVEN) xs.move(-TT);
 #pragma unroll
         for (int i = TS - 1; i >= 0; --i) {
-            Num<T, 2> g, dy, x = splat<Num<T, 2>>(0.f), y, dx, dg, drv;
+            Num<T, 2> g, dy, x = splat<Num<T, 2>>(0.f), y, dx, dg, drv, at;
             unpack(gr[i], g.v);
             unpack(dr[i], dy.v);
             unpack(yr[i], y.v);
@@ -234,9 +235,9 @@ __global__ void __launch_bounds__(NW * 32, 2) stream_bwd_kernel(const Args a) {
             if (i == 0 && base + t0 == 0) y = h0;
             if (more && (FULL || mine)) fetch(i, base - TT + t0 + i);
             const Num<T, 2> gh = add_(dy, c);
-            gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv);
+            gate_bwd<GATE>(g, r, x, y, gh, kept[i], dx, dg, drv, at);
             if (FULL || (mine && base + t0 + i < len)) {
-                c = mul_(kept_a<GATE>(kept[i]), gh);
+                c = mul_(at, gh);
                 if constexpr (GATE == HLA_GATE_RATE) sum = add_(sum, drv);
                 R o, q;
                 pack(dx.v, o);
