@@ -11,7 +11,7 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
-// Sticky device status word (DEV_OK / DEV_TIMEOUT), one per device.
+// Sticky device status word (DEV_OK or DEV_* bits), one per device.
 __device__ unsigned g_dev_status = 0u;
 
 hla_status fail(hla_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -856,6 +856,8 @@ hla_status hla_sync_status(void *stream) {
         const unsigned zero = 0u;
         e = cudaMemcpyToSymbol(g_dev_status, &zero, sizeof zero);
         if (e != cudaSuccess) return cuda_fail(e, "clear status word");
+        if (v & hla::DEV_WORKSPACE)
+            return fail(HLA_ERR_ARG, "a workspace was not zeroed before its first use, or calls that share it overlapped (status 0x%x)", v);
         return fail(HLA_ERR_TIMEOUT, "a bounded device wait expired (status 0x%x)", v);
     }
     return HLA_OK;

@@ -20,8 +20,8 @@
 namespace hla {
 
 // ---------------------------------------------------------------- error flag
-// Sticky device-side status: set when a bounded wait expires.
-enum : unsigned { DEV_OK = 0u, DEV_TIMEOUT = 1u };
+// Sticky device-side status, bits: a bounded wait expired; a workspace's header was not ready.
+enum : unsigned { DEV_OK = 0u, DEV_TIMEOUT = 1u, DEV_WORKSPACE = 2u };
 
 // Upper bound on polls of a flag (cross-CTA waits) before the wait is declared failed.
 // With the sleep in those loops this is several seconds, far beyond any legitimate wait.

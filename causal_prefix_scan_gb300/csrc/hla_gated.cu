@@ -163,9 +163,11 @@ __device__ __forceinline__ bool look_back(Shared<VEC> &sh, const Args &a, size_t
 }
 
 // This CTA's place: tiles of one position across all chains come before those of the
-// next, in the order in which CTAs begin, so every tile that one waits for has begun.
+// next, in the order in which CTAs begin, so every tile that one waits for has begun.  False
+// when there is no such tile (the header was not zeroed, or belongs to a call that still runs):
+// the status word is raised, and the CTA has nothing to do.
 template <int VEC>
-__device__ __forceinline__ void take_place(Shared<VEC> &sh, const Args &a) {
+__device__ __forceinline__ bool take_place(Shared<VEC> &sh, const Args &a) {
     if (threadIdx.x == 0) {
         if (a.hdr) {
             volatile unsigned long long *base = &a.hdr->base;
@@ -178,12 +180,14 @@ __device__ __forceinline__ void take_place(Shared<VEC> &sh, const Args &a) {
                 __threadfence();
                 *base = t + 1;
             }
+            if (sh.ticket >= gridDim.x) atomicOr(a.err, DEV_WORKSPACE);
         } else {
             sh.ticket = blockIdx.x;
             sh.call = 0;
         }
     }
     __syncthreads();
+    return sh.ticket < gridDim.x;
 }
 
 // ------------------------------------------------------------ forward
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<VEC>) gated_fwd_kernel(const A
     constexpr int TS = kTS<T, FWD, VEC>, TILE_T = kTileT<T, FWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
-    take_place(sh, a);
+    if (!take_place(sh, a)) return;
     const unsigned chains = (unsigned)a.B * a.slices, ticket = __shfl_sync(0xffffffffu, (unsigned)sh.ticket, 0);
     const int pos = (int)(ticket / chains);
     const unsigned chain = ticket % chains;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<VEC>) gated_bwd_kernel(const A
     constexpr int TS = kTS<T, BWD, VEC>, TILE_T = kTileT<T, BWD, VEC>;
     constexpr int C = 32 * VEC;
     __shared__ Shared<VEC> sh;
-    take_place(sh, a);
+    if (!take_place(sh, a)) return;
     const unsigned chains = (unsigned)a.B * a.slices, ticket = __shfl_sync(0xffffffffu, (unsigned)sh.ticket, 0);
     const int pos = (int)(ticket / chains);  // counts from the last tile
     const unsigned chain = ticket % chains;

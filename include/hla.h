@@ -45,8 +45,8 @@
  *   - Every call is asynchronous on the given CUDA stream (`stream` is a
  *     cudaStream_t passed as void*; NULL is the legacy default stream).  The
  *     returned status covers argument validation and launch errors only.  A
- *     device-side failure (a bounded wait that expired) is recorded in a sticky
- *     device flag that hla_sync_status() reports.
+ *     device-side failure (a bounded wait that expired, a workspace that was not
+ *     ready) is recorded in a sticky device flag that hla_sync_status() reports.
  *   - On any status other than HLA_OK nothing was launched, except HLA_ERR_CUDA
  *     from a failed launch; hla_last_error() gives a message.
  *   - Layout: q is [B][H][n][d], k [B][Hkv][n][d], v [B][Hkv][n][dv], o
@@ -405,7 +405,9 @@ HLA_API hla_status hla_state3_combine(int count, int d, int dv, unsigned flags, 
 HLA_API hla_status hla_selftest_expired_wait(void *stream);
 
 /* Synchronise `stream`, then report and clear the sticky device flag: HLA_OK,
- * HLA_ERR_TIMEOUT if a bounded device wait expired since the last call, or
+ * HLA_ERR_TIMEOUT if a bounded device wait expired since the last call, HLA_ERR_ARG if a call
+ * of the gated recurrence found a workspace that was not zeroed or that another call was
+ * using (its results are then incomplete; zero the workspace before the next call), or
  * HLA_ERR_CUDA if the stream reported an error. */
 HLA_API hla_status hla_sync_status(void *stream);
 
