@@ -49,9 +49,6 @@ hla_status check(const hla_window_params *p, bool step) {
     return HLA_OK;
 }
 
-struct Dims {
-    long long B, H, n, w;
-};
 hla_status check_in(const hla_tensor *t, Dims s, hla_dtype dt, const char *what) {
     if (!t || !t->p) return report(HLA_ERR_ARG, what);
     if (reinterpret_cast<uintptr_t>(t->p) % (dt == HLA_F32 ? 4 : 2))
@@ -167,8 +164,8 @@ size_t backward_bytes(const hla_window_params *p) {  // for either path: the ali
     const size_t s = part_bytes(p, TK), t = p->in_dtype == HLA_BF16 ? part_bytes(p, kTcTile) : 0;
     return delta_bytes(p) + (s > t ? s : t);
 }
-bool wide_rows(const hla_tensor *t) {
-    return (reinterpret_cast<uintptr_t>(t->p) & 15u) == 0 && t->sb % 8 == 0 && t->sh % 8 == 0 && t->st % 8 == 0;
+bool wide_rows(const View &v) {
+    return (reinterpret_cast<uintptr_t>(v.p) & 15u) == 0 && v.sb % 8 == 0 && v.sh % 8 == 0 && v.st % 8 == 0;
 }
 
 }  // namespace
@@ -194,7 +191,7 @@ hla_status hla_window_forward(const hla_window_params *p, const hla_tensor *q, c
     if (o->p == q->p || o->p == k->p || o->p == v->p) return report(HLA_ERR_ARG, "o may not be an input");
     if (reinterpret_cast<uintptr_t>(lse) & 3u) return report(HLA_ERR_ARG, "lse is not aligned to its elements");
     Args a = make(p);
-    a.q = win::view(q); a.k = win::view(k); a.v = win::view(v); a.o = win::view(o);
+    a.q = win::view(q, dq); a.k = win::view(k, dk); a.v = win::view(v, dv); a.o = win::view(o, od);
     a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = dev_status_ptr(&a.err);
@@ -239,8 +236,8 @@ hla_status hla_window_backward(const hla_window_params *p, const hla_tensor *q, 
         return report(HLA_ERR_ARG, "workspace too small (hla_window_backward_workspace_size)");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return report(HLA_ERR_ARG, "workspace must be 256-byte aligned");
     Args a = make(p);
-    a.q = win::view(q); a.k = win::view(k); a.v = win::view(v); a.o = win::view(o); a.go = win::view(dout);
-    a.dq = win::view(dq); a.dk = win::view(dk); a.dv_ = win::view(dv);
+    a.q = win::view(q, qd); a.k = win::view(k, kd); a.v = win::view(v, vd); a.o = win::view(o, od); a.go = win::view(dout, od);
+    a.dq = win::view(dq, qd); a.dk = win::view(dk, kd); a.dv_ = win::view(dv, vd);
     a.lse = const_cast<float *>(lse);
     a.delta = static_cast<float *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + delta_bytes(p));
@@ -287,10 +284,10 @@ hla_status hla_window_step(const hla_window_params *p, const hla_tensor *q, cons
     a.d = p->d; a.dv = p->dv; a.window = p->window; a.sinks = p->sinks;
     a.scale = p->scale;
     a.pos = pos;
-    a.q = win::view(q); a.k = win::view(k); a.v = win::view(v);
-    a.kc = win::view(kc); a.vc = win::view(vc); a.o = win::view(o);
-    a.wide = dt == HLA_BF16 && p->d % 8 == 0 && p->dv % 8 == 0 && wide_rows(k) && wide_rows(v) && wide_rows(kc) &&
-             wide_rows(vc);
+    a.q = win::view(q, qd); a.k = win::view(k, kd); a.v = win::view(v, vd);
+    a.kc = win::view(kc, kcd); a.vc = win::view(vc, vcd); a.o = win::view(o, od);
+    a.wide = dt == HLA_BF16 && p->d % 8 == 0 && p->dv % 8 == 0 && wide_rows(a.k) && wide_rows(a.v) && wide_rows(a.kc) &&
+             wide_rows(a.vc);
     const cudaError_t e = win::step(a, dt, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
@@ -316,16 +313,17 @@ hla_status hla_window_cache_fill(const hla_window_params *p, const hla_tensor *k
     if (kc->p == vc->p || kc->p == k->p || kc->p == v->p || vc->p == k->p || vc->p == v->p)
         return report(HLA_ERR_ARG, "kc and vc must differ from each other and from k and v");
     Args a = make(&c);
-    a.k = win::view(k); a.v = win::view(v);
+    a.k = win::view(k, kd); a.v = win::view(v, vd);
+    const View ko = win::view(kc, kcd), vo = win::view(vc, vcd);
     const long long used = slots < p->nk ? slots : p->nk;  // later slots stay as they are
     const long long pairs = (long long)p->B * p->Hkv, most = 2147483647LL / pairs, quads = (used + 3) / 4;
     const int blocks = (int)(quads < 4096 ? (quads < most ? quads : most) : (4096 < most ? 4096 : most));
     const unsigned grid = (unsigned)(blocks * pairs);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dt == HLA_F32)
-        fill_kernel<float><<<grid, 128, 0, st>>>(a, win::view(kc), win::view(vc), blocks);
+        fill_kernel<float><<<grid, 128, 0, st>>>(a, ko, vo, blocks);
     else
-        fill_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a, win::view(kc), win::view(vc), blocks);
+        fill_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a, ko, vo, blocks);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }

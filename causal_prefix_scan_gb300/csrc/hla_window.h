@@ -9,8 +9,13 @@ struct View {
     void *p;
     long long sb, sh, st;
 };
-inline View view(const hla_tensor *t) {
-    return t ? View{t->p, t->sb, t->sh, t->st} : View{nullptr, 0, 0, 0};
+struct Dims {
+    long long B, H, n, w;  // sequences, heads, rows of a head, elements of a row
+};
+// The stride of a dimension with one element is never used: whatever it is, the kernels are
+// chosen by the others.
+inline View view(const hla_tensor *t, Dims s) {
+    return {t->p, s.B > 1 ? t->sb : 0, s.H > 1 ? t->sh : 0, s.n > 1 ? t->st : (s.w + 7) / 8 * 8};
 }
 
 struct Args {
