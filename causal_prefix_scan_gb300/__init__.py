@@ -604,12 +604,17 @@ def _current(t):
 _NO_CONTEXT = contextlib.nullcontext()
 
 
-def _on(stream):
-    """What a call allocates belongs to the stream the call runs on."""
+def _on(stream, device):
+    """What a call allocates belongs to the stream the call runs on, one of its tensors' device
+    (entering another device's stream would make that device the current one)."""
     if stream is None:
         return _NO_CONTEXT
     import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _t2(t):
@@ -680,7 +685,7 @@ def gated_workspace(x, stream=None):
     """A zeroed workspace for gated_forward and gated_backward of x [B,n,d]; each call leaves
     it ready for the next.  Calls that may overlap in time need one each."""
     B, n, d = x.shape
-    with _on(stream):
+    with _on(stream, x.device):
         return new_workspace(hla_gated_workspace_size(hla_gated_params(B, n, d, _dtype_code(x), 0, None, None)), x.device)
 
 
@@ -698,7 +703,7 @@ def gated_forward(x, g, gate: str = "given", rate=None, state_in=None, return_st
         raise ValueError("x must be [B, n, d]")
     p = _gated_params(x, g, gate, rate, lengths, dev)
     _optional(state_in, "state_in", (p.B, p.d), torch.float32, dev)
-    with _on(stream):
+    with _on(stream, dev):
         if out is None:
             out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
         else:
@@ -724,7 +729,7 @@ def gated_backward(x, g, y, dy, gate: str = "given", rate=None, state_in=None, d
     _expect(dy, "dy", x.shape, x.dtype, dev)
     _optional(state_in, "state_in", (p.B, p.d), torch.float32, dev)
     _optional(d_state_out, "d_state_out", (p.B, p.d), torch.float32, dev)
-    with _on(stream):
+    with _on(stream, dev):
         new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
         if out is None:
             out = _zeroed(x, (x.shape, x.shape)) if lengths is not None else \
@@ -755,7 +760,7 @@ def gated_step(state, x, g, gate: str = "given", rate=None, lengths=None, state_
         state_out = state
     else:
         _expect(state_out, "state_out", x.shape, torch.float32, dev, True)
-    with _on(stream):
+    with _on(stream, dev):
         if out is None:
             out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
         else:
@@ -790,7 +795,7 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = N
     import torch
     dev = _current(q)
     p = _window_params(q, k, v, window, sinks, scale, lengths, dev)
-    with _on(stream):
+    with _on(stream, dev):
         make = torch.zeros if lengths is not None else torch.empty
         if out is None:
             out = make((p.B, p.H, p.n, p.dv), dtype=q.dtype, device=dev)
@@ -805,7 +810,7 @@ def window_workspace(q, k, v, window: int, sinks: int = 0, stream=None):
     """A workspace for window_backward of these shapes."""
     import torch
     p = _window_params(q, k, v, window, sinks, None, None, q.device)
-    with _on(stream):
+    with _on(stream, q.device):
         return torch.empty(max(hla_window_backward_workspace_size(p), 1), dtype=torch.uint8, device=q.device)
 
 
@@ -820,7 +825,7 @@ def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: f
     _expect(o, "o", (p.B, p.H, p.n, p.dv), q.dtype, dev)
     _expect(dout, "dout", (p.B, p.H, p.n, p.dv), q.dtype, dev)
     _expect(lse, "lse", (p.B, p.H, p.n), torch.float32, dev, True)
-    with _on(stream):
+    with _on(stream, dev):
         if out is None:
             shapes = (q.shape, k.shape, v.shape)
             out = _zeroed(q, shapes) if lengths is not None else \
@@ -863,7 +868,8 @@ def window_cache_fill(kc, vc, k, v, window: int, sinks: int = 0, lengths=None, s
     p = _cache_params(kc, vc, kc.shape[1], window, sinks, None, lengths, k.shape[2], dev)
     _expect(k, "k", (p.B, p.Hkv, p.nk, p.d), kc.dtype, dev)
     _expect(v, "v", (p.B, p.Hkv, p.nk, p.dv), kc.dtype, dev)
-    hla_window_cache_fill(p, _t4(k), _t4(v), _t4(kc), _t4(vc), stream)
+    with _on(stream, dev):
+        hla_window_cache_fill(p, _t4(k), _t4(v), _t4(kc), _t4(vc), stream)
 
 
 def window_step(kc, vc, pos, q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, stream=None):
@@ -880,7 +886,7 @@ def window_step(kc, vc, pos, q, k, v, window: int, sinks: int = 0, scale: float 
     _expect(k, "k", (p.B, p.Hkv, p.d), kc.dtype, dev)
     _expect(v, "v", (p.B, p.Hkv, p.dv), kc.dtype, dev)
     _expect(pos, "pos", (p.B,), torch.int64, dev, True)
-    with _on(stream):
+    with _on(stream, dev):
         if out is None:
             out = torch.zeros((p.B, p.H, p.dv), dtype=q.dtype, device=dev)
         else:
