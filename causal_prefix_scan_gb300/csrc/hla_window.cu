@@ -8,22 +8,28 @@ namespace hla {
 namespace win {
 namespace {
 
+int far_keys(const hla_window_params *p, int tile) {
+    const int s = p->sinks < p->nk ? p->sinks : p->nk;
+    const long long up = ((long long)s + tile - 1) / tile * tile;
+    return (int)(up < p->nk ? up : p->nk);
+}
+
 // Far shares of a key tile with first tokens (see dkv_kernel): its queries beyond the
 // window are divided so that a share is about as long as a tile's own window (one share for
 // all of them: B2 H16 n8192 w1024 backward 857 us against 509, B3 H6 n1501 w301 66 against 45).
-constexpr int kFarMost = 32;
+// Each share is an fp32 copy of these tiles' dk and dv in the workspace, so there are no more than
+// give the far queries kFarCtas CTAs: many tiles fill the device with few shares (B8 H8 n8192 d128
+// w512 with 1,024 first tokens: 338 MB and 1,557 us, without the limit 1,009 MB and 1,994 us).
+constexpr int kFarMost = 32, kFarCtas = 2048;
 int far_shares(const hla_window_params *p, int tile) {
     if (p->sinks == 0 || p->n == 0) return 0;
     const long long far = (long long)p->nk - p->window;  // queries beyond the window of the first keys
     if (far <= 0) return 0;
     const long long win = p->window + tile;
     const long long s = (far + win - 1) / win;
-    return (int)(s > kFarMost ? kFarMost : s);
-}
-int far_keys(const hla_window_params *p, int tile) {
-    const int s = p->sinks < p->nk ? p->sinks : p->nk;
-    const long long up = ((long long)s + tile - 1) / tile * tile;
-    return (int)(up < p->nk ? up : p->nk);
+    const long long tiles = (long long)p->B * p->Hkv * ((far_keys(p, tile) + tile - 1LL) / tile);
+    const long long fill = kFarCtas / tiles > 1 ? kFarCtas / tiles : 1, most = fill < kFarMost ? fill : kFarMost;
+    return (int)(s > most ? most : s);
 }
 
 hla_status check(const hla_window_params *p, bool step) {
