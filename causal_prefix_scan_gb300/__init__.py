@@ -682,8 +682,9 @@ def _space(need, workspace, device, zeroed):
 
 
 def gated_workspace(x, stream=None):
-    """A zeroed workspace for gated_forward and gated_backward of x [B,n,d]; each call leaves
-    it ready for the next.  Calls that may overlap in time need one each."""
+    """A zeroed workspace for gated_forward and gated_backward of x [B,n,d], about half of B n d
+    bytes; each call leaves it ready for the next.  Calls that may overlap in time need one each.
+    A call of more than 64 tokens without one allocates and zeroes it anew."""
     B, n, d = x.shape
     with _on(stream, x.device):
         return new_workspace(hla_gated_workspace_size(hla_gated_params(B, n, d, _dtype_code(x), 0, None, None)), x.device)
@@ -807,7 +808,8 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = N
 
 
 def window_workspace(q, k, v, window: int, sinks: int = 0, stream=None):
-    """A workspace for window_backward of these shapes."""
+    """A workspace for window_backward of these shapes: B H n floats, and with first tokens up to
+    a few fp32 copies of their dk and dv."""
     import torch
     p = _window_params(q, k, v, window, sinks, None, None, q.device)
     with _on(stream, q.device):

@@ -21,7 +21,7 @@
 // instead (maps, scan, states) would move 5/3 of the forward's bytes.
 //
 // Measured: forward 3 x 5,003 x 1,001 fp32 (ragged) 52 us, 2.4 TB/s; 16,384 x 1,024 bf16 with
-// rates 46 us, 2.2 TB/s; backward 4 x 2,048 x 512 bf16 25 us, 2.0 TB/s.  What bounds it is the
+// rates 47 us, 2.1 TB/s; backward 4 x 2,048 x 512 bf16 25 us, 2.0 TB/s.  What bounds it is the
 // path of one CTA, loads -> gates -> look-back -> stores, and how many CTAs are on it at once.
 #include "hla_gated.cuh"
 #include "hla_look_back.h"
@@ -32,10 +32,11 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int kThreads = WARPS * 32;
-// CTAs per SM, and tokens of one thread: as many as leave what it holds of them in registers
-// (the backward's four inputs take twice the room).  A CTA mostly waits, for its loads and for
-// the tiles before it: single channels gain from four per SM (3 x 5,003 x 1,001 fp32 forward 66
-// -> 52 us), pairs have room for two (three spill: 4 x 2,048 x 512 backward 26 -> 29 us).
+// CTAs per SM, and tokens of one thread: about as many as leave what it holds of them in
+// registers (the backward's four inputs take twice the room; single channels spill 8 to 44 bytes,
+// pairs none).  A CTA mostly waits, for its loads and for the tiles before it: single channels gain
+// from four per SM (3 x 5,003 x 1,001 fp32 forward 66 -> 52 us), pairs have room for two (three
+// spill: 4 x 2,048 x 512 backward 26 -> 29 us).
 enum Dir { FWD, BWD };
 template <int VEC>
 constexpr int kCtas = VEC == 1 ? 4 : 2;

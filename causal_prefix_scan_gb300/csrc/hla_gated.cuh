@@ -96,8 +96,8 @@ __device__ __forceinline__ void store(const Tensor &t, size_t off, const float (
 
 // ------------------------------------------------------------ arithmetic on VEC channels
 // PAIR: two fp32 numbers go through one instruction (fma.rn.f32x2 and the like, rounded as the
-// scalar ones), fewer instructions to issue.  bf16 channels use it (32,768 x 4,096 forward 217
-// -> 207 us, 2 x 8,192 x 4,096 backward 235 -> 221 us); fp32 ones, whose inputs take twice the
+// scalar ones), fewer instructions to issue.  bf16 channels use it (32,768 x 4,096 forward 223
+// -> 211 us, 2 x 8,192 x 4,096 backward 238 -> 228 us); fp32 ones, whose inputs take twice the
 // registers, do not: pairs want aligned ones (4 x 2,048 x 4,096 forward 90 -> 82 us without).
 template <int VEC, bool PAIR>
 struct Vf {

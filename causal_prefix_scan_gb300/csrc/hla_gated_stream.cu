@@ -7,10 +7,12 @@
 // outputs.  The next tile's inputs are loaded into the registers of the present one as they
 // become free, so memory works while the tile is computed.
 //
-// Measured, bf16 with rates: forward 32,768 x 4,096 207 us (3.9 TB/s), backward 2 x 8,192 x
-// 4,096 221 us (3.6 TB/s).  Bound by issue: two exponentials, a reciprocal and a reciprocal root
-// per element beside some thirty other instructions, with 24 (16) warps per SM, all that the
-// registers allow; 12 (8) warps of 8 tokens per thread were the best of 4 to 16 of 2 to 8.
+// Measured, bf16 with rates: forward 32,768 x 4,096 211 us (3.8 TB/s), backward 2 x 8,192 x
+// 4,096 228 us (3.5 TB/s).  Bound by issue and the latencies under it: two exponentials, a reciprocal
+// and a reciprocal root per element beside some thirty other instructions, with 24 (16) warps per SM,
+// all that the registers allow (fp32 forward: 88 to 104 bytes spilled); 12 (8) warps of 8 tokens per
+// thread were the best of 4 to 16 of 2 to 8.  256 CTAs put two on 104 of the 152 SMs, whose issue
+// slots are 63 % (58 %) busy, and one on the others (32, 29 %).
 #include <type_traits>
 
 #include "hla_gated.cuh"
@@ -68,7 +70,7 @@ HLA_DEVICE V state_before(Shared<NW> &sh, int k, V A, V B) {
 
 // Rows are addressed as base + offset: the base (sequence, slice, tile) is the same for the
 // whole CTA, the 32-bit offset of a thread's token in the tile never changes (64-bit addresses
-// of every row cost a quarter of the instructions: forward 233 -> 207 us on 32,768 x 4,096).
+// of every row cost a quarter of the instructions, 26 us of the forward on 32,768 x 4,096).
 template <typename T>
 struct Rows {
     char *p;
@@ -318,13 +320,15 @@ cudaError_t by_gate(const Args &a, int gate, bool backward, cudaStream_t st) {
 
 // Against the look-back kernels (with rates, us): CTAs here, forward and backward of both.
 //                               bf16 here   look-back    fp32 here   look-back
-//    64  1 x 16,384 x 1,024      64 | 170     46 |  95
-//   104  1 x 16,384 x 1,664      69 | 177     70 | 141     82 | 206    75 | 154
-//   128  1 x 16,384 x 2,048      69 | 185     84 | 170     83 | 216    89 | 186
-//   144  2 x  8,192 x 1,152      39 |  98     50 | 101     47 | 114    53 | 111
-//   160  2 x  8,192 x 1,280      55 | 114     55 | 110
-//   256  1 x  8,192 x 4,096      57 | 117     81 | 163
-// The forward is ahead from about three quarters of the SMs on, the backward from all of them.
+//    64  1 x 16,384 x 1,024      66 | 173     47 | 100     77 | 183    52 | 108
+//   104  1 x 16,384 x 1,664      72 | 183     73 | 150     82 | 206    77 | 160
+//   128  1 x 16,384 x 2,048      71 | 190     87 | 180     82 | 214    91 | 192
+//   144  2 x  8,192 x 1,152      41 | 101     51 | 105     46 | 113    54 | 113
+//   160  2 x  8,192 x 1,280      56 | 117     55 | 115     70 | 116    59 | 123
+//   256  1 x  8,192 x 4,096      58 | 120     82 | 171     72 | 133    88 | 185
+//  1024  4 x  2,048 x 4,096      59 | 110     81 | 169     79 | 133    85 | 186
+// The forward is ahead from about three quarters of the SMs on (just past all of them, where a few
+// get a second CTA, it loses some of it again), the backward from about all of them.
 bool stream_takes(const Args &a, hla_dtype t, bool backward, int sms) {
     constexpr int most = (kWarpsFwd > kWarpsBwd ? kWarpsFwd : kWarpsBwd) * GROUPS * TS;  // tokens of a tile
     const long long st_end = (1LL << 32) / (most * (t == HLA_F32 ? 4 : 2));              // a tile's offsets have 32 bits

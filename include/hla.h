@@ -463,11 +463,11 @@ HLA_API hla_status hla_forward_chunked_noalloc(const hla_params *p, const void *
  * pages have no counterpart; stacks that use constant-state layers do.
  *
  * Tensors of this and the next section are strided: element (b, head, token, channel) at
- * p + b sb + head sh + token st + channel (strides in elements, not negative; sh is not
- * used here).  Pointers need the alignment of one element only; even strides and widths
- * with 4-byte (bf16) or 8-byte (fp32) pointers run twice as wide.  Inputs may be
- * broadcast (stride 0); the rows of an output must not share memory, and an output must
- * not overlap an input.
+ * p + b sb + head sh + token st + channel (strides in elements, not negative; that of a
+ * dimension with one element is not used, nor is sh here).  Pointers need the alignment of
+ * one element only; even strides and widths with 4-byte (bf16) or 8-byte (fp32) pointers run
+ * twice as wide (but for the fp32 forward of few channels).  Inputs may be broadcast (stride
+ * 0); the rows of an output must not share memory, and an output must not overlap an input.
  */
 typedef struct {
     void *p;
@@ -486,10 +486,11 @@ typedef struct {
 } hla_gated_params;
 
 /* Bytes of device workspace hla_gated_forward and hla_gated_backward need (0 for invalid
- * parameters and n = 0).  Set to zero before its first use; every call leaves it ready for
- * the next one, of either direction and any sizes it is large enough for.  Calls sharing
- * one workspace must not overlap in time, and no other entry point may use it.  Up to 64
- * tokens the forward, and the backward without d_rate, take NULL as well. */
+ * parameters and n = 0): about B n d / 2.  Set to zero before its first use; every call leaves
+ * it ready for the next one, of either direction and any sizes it is large enough for.  Calls
+ * sharing one workspace must not overlap in time, and no other entry point may use it
+ * (hla_sync_status reports a header that is found in use or never zeroed).  Up to 64 tokens
+ * the forward, and the backward without d_rate, take NULL as well. */
 HLA_API size_t hla_gated_workspace_size(const hla_gated_params *p);
 
 /*
@@ -554,7 +555,8 @@ HLA_API hla_status hla_window_forward(const hla_window_params *p, const hla_tens
                                       const hla_tensor *v, const hla_tensor *o, float *lse, void *stream);
 
 /* Gradients dq, dk, dv (written, not accumulated; with Hkv < H, dk and dv are the sums over
- * each group) from o and lse as the forward wrote them and dout.  workspace: at least
+ * each group) from o and lse as the forward wrote them and dout.  Needs n >= 1 where nk >= 1:
+ * with no queries the gradients are zero, which is the caller's to write.  workspace: at least
  * hla_window_backward_workspace_size(p) bytes, 256-byte aligned, no initial contents
  * needed.  The same bits on every call. */
 HLA_API size_t hla_window_backward_workspace_size(const hla_window_params *p);
