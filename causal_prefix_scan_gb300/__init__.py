@@ -610,8 +610,8 @@ def _on(stream, device):
     if stream is None:
         return _NO_CONTEXT
     import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    if isinstance(stream, int):  # (0 given to ExternalStream makes a stream of its own)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream)
