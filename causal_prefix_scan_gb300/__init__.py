@@ -2,7 +2,9 @@
 the asymmetric variant AHLA, the backward pass of the masked forward, and masked
 third-order HLA (forward and decode); beside them two more layers whose serving state
 has a constant size: a gated linear recurrence (``gated_*``) and softmax attention over a
-sliding window with first tokens that stay visible (``window_*``).
+sliding window with first tokens that stay visible (``window_*``); and the operators of a
+selective state space layer: its short causal convolution (``conv_*``), its scan
+(``ssm_*``) and the norm over groups of channels with an activated gate (``norm_*``).
 
 Thin ctypes binding over the C ABI in ``include/hla.h`` (library
 ``_lib/libhla_gb300.so``, built for sm_103a by ``_build.build()``).  Functions named
@@ -27,6 +29,7 @@ HLA_OK, HLA_ERR_ARG, HLA_ERR_UNSUPPORTED, HLA_ERR_CUDA, HLA_ERR_TIMEOUT = 0, 1, 
 HLA_F32, HLA_BF16 = 0, 1
 HLA_NORMALIZE, HLA_DECAY, HLA_UNMASKED, HLA_ASYMMETRIC = 1, 2, 4, 8
 HLA_GATE_GIVEN, HLA_GATE_SIGMOID, HLA_GATE_RATE = 0, 1, 2
+HLA_ACT_NONE, HLA_ACT_SILU = 0, 1
 
 __all__ = [
     "HLA_OK", "HLA_ERR_ARG", "HLA_ERR_UNSUPPORTED", "HLA_ERR_CUDA", "HLA_ERR_TIMEOUT",
@@ -44,6 +47,13 @@ __all__ = [
     "hla_window_cache_fill",
     "gated_workspace", "gated_forward", "gated_backward", "gated_step", "GatedGradients",
     "window_forward", "window_workspace", "window_backward", "window_cache", "window_cache_fill", "window_step",
+    "HLA_ACT_NONE", "HLA_ACT_SILU", "hla_conv_params", "hla_ssm_params", "hla_norm_params", "hla_ssm_gradients",
+    "hla_conv_forward", "hla_conv_backward_workspace_size", "hla_conv_backward", "hla_conv_step",
+    "hla_ssm_workspace_size", "hla_ssm_forward", "hla_ssm_backward", "hla_ssm_step",
+    "hla_norm_forward", "hla_norm_backward_workspace_size", "hla_norm_backward",
+    "conv_forward", "conv_workspace", "conv_backward", "conv_step", "ConvGradients",
+    "ssm_workspace", "ssm_forward", "ssm_backward", "ssm_step", "SsmGradients",
+    "norm_forward", "norm_workspace", "norm_backward", "NormGradients",
 ]
 
 # Every symbol include/hla.h declares.
@@ -54,7 +64,9 @@ EXPORTS = ("hla_forward_workspace_size", "hla_forward_chunked", "hla_state_combi
            "hla_selftest_expired_wait", "hla_forward_kernel", "hla_backward_chunked_state", "hla_state3_combine",
            "hla_gated_workspace_size", "hla_gated_forward", "hla_gated_backward", "hla_gated_step",
            "hla_window_forward", "hla_window_backward_workspace_size", "hla_window_backward", "hla_window_step",
-           "hla_window_cache_fill")
+           "hla_window_cache_fill", "hla_conv_forward", "hla_conv_backward_workspace_size", "hla_conv_backward",
+           "hla_conv_step", "hla_ssm_workspace_size", "hla_ssm_forward", "hla_ssm_backward", "hla_ssm_step",
+           "hla_norm_forward", "hla_norm_backward_workspace_size", "hla_norm_backward")
 
 
 class HlaError(RuntimeError):
@@ -95,6 +107,32 @@ class hla_window_params(ctypes.Structure):
                 ("nk", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int), ("in_dtype", ctypes.c_int),
                 ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
                 ("lengths", ctypes.c_void_p)]
+
+
+class hla_conv_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("n", ctypes.c_int), ("d", ctypes.c_int), ("width", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("activation", ctypes.c_int), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
+
+
+class hla_ssm_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("G", ctypes.c_int), ("n", ctypes.c_int),
+                ("P", ctypes.c_int), ("N", ctypes.c_int), ("in_dtype", ctypes.c_int), ("dt_softplus", ctypes.c_int),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p)]
+
+
+class hla_ssm_gradients(ctypes.Structure):
+    _fields_ = [("dx", hla_tensor), ("d_dt", hla_tensor), ("db", hla_tensor), ("dc", hla_tensor),
+                ("dA", ctypes.c_void_p), ("dD", ctypes.c_void_p), ("d_dt_bias", ctypes.c_void_p),
+                ("d_state_in", ctypes.c_void_p)]
+
+
+class hla_norm_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("n", ctypes.c_int), ("d", ctypes.c_int), ("groups", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("center", ctypes.c_int), ("activation", ctypes.c_int),
+                ("gate_first", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -156,6 +194,23 @@ def library(path: str | None = None):
     lib.hla_window_cache_fill.argtypes = [WP, T, T, T, T, vp]
     for fn in (lib.hla_gated_forward, lib.hla_gated_backward, lib.hla_gated_step, lib.hla_window_forward,
                lib.hla_window_backward, lib.hla_window_step, lib.hla_window_cache_fill):
+        fn.restype = ctypes.c_int
+    CP, SP, NP = (ctypes.POINTER(t) for t in (hla_conv_params, hla_ssm_params, hla_norm_params))
+    lib.hla_conv_forward.argtypes = [CP, T, T, vp, vp, vp]
+    lib.hla_conv_backward_workspace_size.argtypes = [CP]
+    lib.hla_conv_backward.argtypes = [CP, T, T, T, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.hla_conv_step.argtypes = [CP, T, T, vp, vp]
+    lib.hla_ssm_workspace_size.argtypes = [SP, i]
+    lib.hla_ssm_forward.argtypes = [SP, T, T, T, T, T, vp, vp, vp, sz, vp]
+    lib.hla_ssm_backward.argtypes = [SP, T, T, T, T, T, vp, vp, ctypes.POINTER(hla_ssm_gradients), vp, sz, vp]
+    lib.hla_ssm_step.argtypes = [SP, T, T, T, T, T, vp, vp]
+    lib.hla_norm_forward.argtypes = [NP, T, T, T, vp]
+    lib.hla_norm_backward_workspace_size.argtypes = [NP]
+    lib.hla_norm_backward.argtypes = [NP, T, T, T, T, T, vp, vp, vp, sz, vp]
+    for fn in (lib.hla_conv_backward_workspace_size, lib.hla_ssm_workspace_size, lib.hla_norm_backward_workspace_size):
+        fn.restype = sz
+    for fn in (lib.hla_conv_forward, lib.hla_conv_backward, lib.hla_conv_step, lib.hla_ssm_forward,
+               lib.hla_ssm_backward, lib.hla_ssm_step, lib.hla_norm_forward, lib.hla_norm_backward):
         fn.restype = ctypes.c_int
     lib.hla_status_string.argtypes = [ctypes.c_int]
     lib.hla_status_string.restype = ctypes.c_char_p
@@ -371,6 +426,59 @@ def hla_window_step(params: hla_window_params, q, k, v, kc, vc, pos, o, stream=N
 
 def hla_window_cache_fill(params: hla_window_params, k, v, kc, vc, stream=None) -> None:
     _check(library().hla_window_cache_fill(ctypes.byref(params), k, v, kc, vc, _stream(stream)))
+
+
+def hla_conv_forward(params: hla_conv_params, x, y, state_in=None, state_out=None, stream=None) -> None:
+    _check(library().hla_conv_forward(ctypes.byref(params), x, y, _ptr(state_in), _ptr(state_out), _stream(stream)))
+
+
+def hla_conv_backward_workspace_size(params: hla_conv_params) -> int:
+    return library().hla_conv_backward_workspace_size(ctypes.byref(params))
+
+
+def hla_conv_backward(params: hla_conv_params, x, dy, dx, state_in, d_state_out, d_weight, d_bias, d_state_in,
+                      workspace, workspace_bytes: int, stream=None) -> None:
+    _check(library().hla_conv_backward(ctypes.byref(params), x, dy, dx, _ptr(state_in), _ptr(d_state_out),
+                                       _ptr(d_weight), _ptr(d_bias), _ptr(d_state_in), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)))
+
+
+def hla_conv_step(params: hla_conv_params, x, y, state, stream=None) -> None:
+    _check(library().hla_conv_step(ctypes.byref(params), x, y, _ptr(state), _stream(stream)))
+
+
+def hla_ssm_workspace_size(params: hla_ssm_params, backward: bool) -> int:
+    return library().hla_ssm_workspace_size(ctypes.byref(params), 1 if backward else 0)
+
+
+def hla_ssm_forward(params: hla_ssm_params, x, dt, b, c, y, state_in, state_out, workspace, workspace_bytes: int,
+                    stream=None) -> None:
+    _check(library().hla_ssm_forward(ctypes.byref(params), x, dt, b, c, y, _ptr(state_in), _ptr(state_out),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def hla_ssm_backward(params: hla_ssm_params, x, dt, b, c, dy, state_in, d_state_out, grads: hla_ssm_gradients,
+                     workspace, workspace_bytes: int, stream=None) -> None:
+    _check(library().hla_ssm_backward(ctypes.byref(params), x, dt, b, c, dy, _ptr(state_in), _ptr(d_state_out),
+                                      ctypes.byref(grads), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def hla_ssm_step(params: hla_ssm_params, x, dt, b, c, y, state, stream=None) -> None:
+    _check(library().hla_ssm_step(ctypes.byref(params), x, dt, b, c, y, _ptr(state), _stream(stream)))
+
+
+def hla_norm_forward(params: hla_norm_params, x, gate, y, stream=None) -> None:
+    _check(library().hla_norm_forward(ctypes.byref(params), x, gate, y, _stream(stream)))
+
+
+def hla_norm_backward_workspace_size(params: hla_norm_params) -> int:
+    return library().hla_norm_backward_workspace_size(ctypes.byref(params))
+
+
+def hla_norm_backward(params: hla_norm_params, x, gate, dy, dx, d_gate, d_weight, d_bias, workspace,
+                      workspace_bytes: int, stream=None) -> None:
+    _check(library().hla_norm_backward(ctypes.byref(params), x, gate, dy, dx, d_gate, _ptr(d_weight), _ptr(d_bias),
+                                       _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------- tensor-level helpers
@@ -895,3 +1003,316 @@ def window_step(kc, vc, pos, q, k, v, window: int, sinks: int = 0, scale: float 
             _expect(out, "out", (p.B, p.H, p.dv), q.dtype, dev)
         hla_window_step(p, _t4(q), _t4(k), _t4(v), _t4(kc), _t4(vc), pos, _t4(out), stream)
     return out
+
+
+# ------------------------------------------------------- selective state space layer
+_ACTIVATIONS = {"none": HLA_ACT_NONE, "silu": HLA_ACT_SILU}
+ConvGradients = namedtuple("ConvGradients", "dx d_weight d_bias d_state_in")
+SsmGradients = namedtuple("SsmGradients", "dx d_dt dA dB dC dD d_dt_bias d_state_in")
+NormGradients = namedtuple("NormGradients", "dx d_gate d_weight d_bias")
+
+
+def _activation(name):
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    return _ACTIVATIONS[name]
+
+
+def _conv_params(x, weight, bias, activation, lengths, device):
+    import torch
+    code = _dtype_code(x)
+    B, d = x.shape[0], x.shape[-1]
+    _expect(x, "x", x.shape, x.dtype, device)
+    if weight.dim() != 2:
+        raise ValueError("weight must be [d, width]")
+    _expect(weight, "weight", (d, weight.shape[1]), torch.float32, device, True)
+    _optional(bias, "bias", (d,), torch.float32, device)
+    _optional(lengths, "lengths", (B,), torch.int32, device)
+    return hla_conv_params(B, x.shape[1] if x.dim() == 3 else 1, d, weight.shape[1], code, _activation(activation),
+                           _ptr(weight), _ptr(bias), _ptr(lengths))
+
+
+def conv_forward(x, weight, bias=None, activation: str = "none", state_in=None, return_state: bool = False,
+                 lengths=None, out=None, stream=None):
+    """Short causal convolution per channel: y_t = act(bias + sum_i weight[:, i] x_{t-(w-1)+i}) over
+    x [B,n,d] (bf16 or fp32, any strides with adjacent channels), weight [d,w] fp32 with w of 2 to
+    4, bias [d] fp32 or None, activation "none" or "silu".  state_in [B,w-1,d] (x's type): the
+    inputs before the first token, or None (zeros).  lengths [B] int32: tokens of each sequence
+    (rows behind them: zero in a new y, left as they were in ``out``).  Returns y (and the last
+    w - 1 inputs of each sequence)."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, n, d]")
+    p = _conv_params(x, weight, bias, activation, lengths, dev)
+    held = (p.B, p.width - 1, p.d)
+    _optional(state_in, "state_in", held, x.dtype, dev)
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        st = torch.empty(held, dtype=x.dtype, device=dev) if return_state else None
+        hla_conv_forward(p, _t2(x), _t2(out), state_in, st, stream)
+    return (out, st) if return_state else out
+
+
+def conv_workspace(x, weight, stream=None):
+    """A workspace for conv_backward of these shapes: the filters' gradients of every 256 tokens.
+    Calls that may overlap in time need one each."""
+    import torch
+    p = _conv_params(x, weight, None, "none", None, x.device)
+    with _on(stream, x.device):
+        return torch.empty(max(hla_conv_backward_workspace_size(p), 1), dtype=torch.uint8, device=x.device)
+
+
+def conv_backward(x, dy, weight, bias=None, activation: str = "none", state_in=None, d_state_out=None,
+                  want_dstate: bool = False, lengths=None, out=None, workspace=None, stream=None):
+    """Gradients of conv_forward from dy and d_state_out [B,w-1,d] (None: zero).  Returns
+    ConvGradients(dx, d_weight, d_bias, d_state_in): d_weight [d,w] and d_bias [d] fp32 (None
+    without a bias), d_state_in with want_dstate (else None).  ``out`` may hold dx."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, n, d]")
+    p = _conv_params(x, weight, bias, activation, lengths, dev)
+    held = (p.B, p.width - 1, p.d)
+    _expect(dy, "dy", x.shape, x.dtype, dev)
+    _optional(state_in, "state_in", held, x.dtype, dev)
+    _optional(d_state_out, "d_state_out", held, x.dtype, dev)
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "dx", x.shape, x.dtype, dev)
+        dw = torch.empty((p.d, p.width), dtype=torch.float32, device=dev)
+        db = torch.empty((p.d,), dtype=torch.float32, device=dev) if bias is not None else None
+        ds = torch.empty(held, dtype=x.dtype, device=dev) if want_dstate else None
+        ws, nbytes = _space(hla_conv_backward_workspace_size(p) if workspace is None else 0, workspace, dev, False)
+        hla_conv_backward(p, _t2(x), _t2(dy), _t2(out), state_in, d_state_out, dw, db, ds, ws, nbytes, stream)
+    return ConvGradients(out, dw, db, ds)
+
+
+def conv_step(state, x, weight, bias=None, activation: str = "none", lengths=None, out=None, stream=None):
+    """One token of every sequence: x [B,d], state [B,w-1,d] shifted by one in place.  lengths [B]
+    int32: 0 marks an idle sequence, whose rows of y (zero in a new one) and of the state are left
+    as they were.  Returns y [B,d]."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [B, d]")
+    p = _conv_params(x, weight, bias, activation, lengths, dev)
+    _expect(state, "state", (p.B, p.width - 1, p.d), x.dtype, dev, True)
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        hla_conv_step(p, _t2(x), _t2(out), state, stream)
+    return out
+
+
+def _t_steps(t):
+    """dt [B, H] or [B, H, n]: single elements, so any strides."""
+    s = t.stride()
+    return hla_tensor(t.data_ptr(), s[0], s[1], s[2] if len(s) == 3 else 0)
+
+
+def _like(x, zero):
+    """A new tensor of x's shape with tokens outside heads where x has them so."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if x.stride(1) < x.stride(2):
+        shape = (x.shape[0], x.shape[2], x.shape[1]) + x.shape[3:]
+        return make(shape, dtype=x.dtype, device=x.device).transpose(1, 2)
+    return make(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _expect_steps(t, name, shape, dtype, device):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, device):
+    import torch
+    code = _dtype_code(x)
+    tail = x.shape[2:-1]  # (n,), or nothing for a step
+    batch, H, P = x.shape[0], x.shape[1], x.shape[-1]
+    if B.dim() != x.dim():
+        raise ValueError("B and C must be [B, G, n, N] (a step's [B, G, N])")
+    G, N = B.shape[1], B.shape[-1]
+    _expect(x, "x", x.shape, x.dtype, device)
+    _expect_steps(dt, "dt", (batch, H) + tail, x.dtype, device)
+    _expect(B, "B", (batch, G) + tail + (N,), x.dtype, device)
+    _expect(C, "C", (batch, G) + tail + (N,), x.dtype, device)
+    _expect(A, "A", (H,), torch.float32, device, True)
+    _optional(D, "D", (H,), torch.float32, device)
+    _optional(dt_bias, "dt_bias", (H,), torch.float32, device)
+    _optional(lengths, "lengths", (batch,), torch.int32, device)
+    return hla_ssm_params(batch, H, G, tail[0] if tail else 1, P, N, code, 1 if dt_softplus else 0, _ptr(A), _ptr(D),
+                          _ptr(dt_bias), _ptr(lengths))
+
+
+def ssm_workspace(x, B, backward: bool = False, stream=None):
+    """A workspace for ssm_forward (or ssm_backward) of x [B,H,n,P] and B [B,G,n,N]: the states
+    between chunks of tokens; no initial contents.  Calls that may overlap in time need one each."""
+    import torch
+    p = hla_ssm_params(x.shape[0], x.shape[1], B.shape[1], x.shape[2], x.shape[3], B.shape[3], _dtype_code(x), 0, None,
+                       None, None, None)
+    with _on(stream, x.device):
+        return torch.empty(max(hla_ssm_workspace_size(p, backward), 1), dtype=torch.uint8, device=x.device)
+
+
+def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False, state_in=None,
+                return_state: bool = False, lengths=None, out=None, workspace=None, stream=None):
+    """Selective state space scan over x [B,H,n,P], dt [B,H,n], B, C [B,G,n,N] (bf16 or fp32, any
+    strides with adjacent channels, widths up to 128; head h reads group h // (H // G)):
+    h_t = exp(dt_t A) h_{t-1} + dt_t B_t x_t^T, y_t = C_t h_t + D x_t per head, with A [H] and D [H]
+    (or None) fp32 and dt as given, or softplus(dt + dt_bias) with dt_softplus (dt_bias [H] fp32 or
+    None).  state_in [B,H,N,P] fp32 or None (zeros); lengths [B] int32: tokens of each sequence
+    (rows behind them: zero in a new y, left as they were in ``out``).  A new y lies in memory as
+    x does (tokens outside heads, or heads outside tokens).  Returns y (and the final state)."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, n, P]")
+    p = _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, dev)
+    held = (p.B, p.H, p.N, p.P)
+    _optional(state_in, "state_in", held, torch.float32, dev)
+    with _on(stream, dev):
+        if out is None:
+            out = _like(x, lengths is not None)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        st = torch.empty(held, dtype=torch.float32, device=dev) if return_state else None
+        ws, nbytes = _space(hla_ssm_workspace_size(p, False) if workspace is None else 0, workspace, dev, False)
+        hla_ssm_forward(p, _t4(x), _t_steps(dt), _t4(B), _t4(C), _t4(out), state_in, st, ws, nbytes, stream)
+    return (out, st) if return_state else out
+
+
+def ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, dt_softplus: bool = False, state_in=None,
+                 d_state_out=None, want_dstate: bool = False, lengths=None, out=None, workspace=None, stream=None):
+    """Gradients of ssm_forward from dy and d_state_out [B,H,N,P] fp32 (None: zero).  Returns
+    SsmGradients(dx, d_dt, dA, dB, dC, dD, d_dt_bias, d_state_in): dA, dD, d_dt_bias [H] fp32 (the
+    latter two None without D, dt_bias), d_state_in fp32 with want_dstate (else None).  ``out`` may
+    hold four tensors for dx, d_dt, dB and dC."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, n, P]")
+    p = _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, dev)
+    held = (p.B, p.H, p.N, p.P)
+    _expect(dy, "dy", x.shape, x.dtype, dev)
+    _optional(state_in, "state_in", held, torch.float32, dev)
+    _optional(d_state_out, "d_state_out", held, torch.float32, dev)
+    with _on(stream, dev):
+        new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+        dx, ddt, dB, dC = out if out is not None else tuple(_like(t, lengths is not None) for t in (x, dt, B, C))
+        for t, name, like in ((dx, "dx", x), (dB, "dB", B), (dC, "dC", C)):
+            _expect(t, name, like.shape, x.dtype, dev)
+        _expect_steps(ddt, "d_dt", dt.shape, x.dtype, dev)
+        dA = new(p.H)
+        dD = new(p.H) if D is not None else None
+        db = new(p.H) if dt_bias is not None else None
+        ds = new(*held) if want_dstate else None
+        ws, nbytes = _space(hla_ssm_workspace_size(p, True) if workspace is None else 0, workspace, dev, False)
+        g = hla_ssm_gradients(_t4(dx), _t_steps(ddt), _t4(dB), _t4(dC), _ptr(dA), _ptr(dD), _ptr(db), _ptr(ds))
+        hla_ssm_backward(p, _t4(x), _t_steps(dt), _t4(B), _t4(C), _t4(dy), state_in, d_state_out, g, ws, nbytes, stream)
+    return SsmGradients(dx, ddt, dA, dB, dC, dD, db, ds)
+
+
+def ssm_step(state, x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False, lengths=None, out=None,
+             stream=None):
+    """One token of every sequence: x [B,H,P], dt [B,H], B, C [B,G,N]; state [B,H,N,P] fp32 is
+    updated in place.  lengths [B] int32: 0 marks an idle sequence, whose rows of y (zero in a new
+    one) and state are left as they were.  Returns y [B,H,P]."""
+    import torch
+    dev = _current(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, H, P]")
+    p = _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, dev)
+    _expect(state, "state", (p.B, p.H, p.N, p.P), torch.float32, dev, True)
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        hla_ssm_step(p, _t4(x), _t_steps(dt), _t4(B), _t4(C), _t4(out), state, stream)
+    return out
+
+
+def _norm_params(x, weight, bias, groups, eps, center, gate, gate_first, activation, lengths, device):
+    import torch
+    code = _dtype_code(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, n, d]")
+    B, n, d = x.shape
+    _expect(x, "x", x.shape, x.dtype, device)
+    if gate is not None:
+        _expect(gate, "gate", x.shape, x.dtype, device)
+    _optional(weight, "weight", (d,), torch.float32, device)
+    _optional(bias, "bias", (d,), torch.float32, device)
+    _optional(lengths, "lengths", (B,), torch.int32, device)
+    return hla_norm_params(B, n, d, _int32(groups, "groups"), code, 1 if center else 0, _activation(activation),
+                           1 if gate_first else 0, float(eps), _ptr(weight), _ptr(bias), _ptr(lengths))
+
+
+def norm_forward(x, weight=None, bias=None, groups: int = 1, eps: float = 1e-5, center: bool = True, gate=None,
+                 gate_first: bool = False, activation: str = "none", lengths=None, out=None, stream=None):
+    """Norm over groups of d / groups adjacent channels of each token of x [B,n,d] (bf16 or fp32,
+    any strides with adjacent channels): u = x, or x silu(gate) with gate_first; z = (u - mean) /
+    sqrt(var + eps), with center=False u / sqrt(mean(u^2) + eps); v = z weight + bias (fp32 [d] or
+    None).  y = v silu(gate) with a gate [B,n,d] that is not first, silu(v) with activation "silu"
+    and no gate, else v.  A gate needs activation "silu".  lengths [B] int32: rows behind them are
+    zero in a new y, left as they were in ``out``.  Returns y."""
+    import torch
+    dev = _current(x)
+    p = _norm_params(x, weight, bias, groups, eps, center, gate, gate_first, activation, lengths, dev)
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.zeros if lengths is not None else torch.empty)(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(out, "out", x.shape, x.dtype, dev)
+        hla_norm_forward(p, _t2(x), None if gate is None else _t2(gate), _t2(out), stream)
+    return out
+
+
+def norm_workspace(x, stream=None):
+    """A workspace for norm_backward of x [B,n,d], whatever its groups: partial sums for the scale's
+    and the shift's gradients.  Calls that may overlap in time need one each."""
+    import torch
+    p = hla_norm_params(*x.shape, 1, _dtype_code(x), 0, 0, 0, 0.0, None, None, None)
+    with _on(stream, x.device):
+        return torch.empty(max(hla_norm_backward_workspace_size(p), 1), dtype=torch.uint8, device=x.device)
+
+
+def norm_backward(x, dy, weight=None, bias=None, groups: int = 1, eps: float = 1e-5, center: bool = True, gate=None,
+                  gate_first: bool = False, activation: str = "none", lengths=None, out=None, workspace=None,
+                  stream=None):
+    """Gradients of norm_forward from x, gate and dy.  Returns NormGradients(dx, d_gate, d_weight,
+    d_bias): d_weight and d_bias [d] fp32 (None without weight, bias), d_gate None without a gate.
+    ``out`` may hold dx, or dx and d_gate with a gate."""
+    import torch
+    dev = _current(x)
+    p = _norm_params(x, weight, bias, groups, eps, center, gate, gate_first, activation, lengths, dev)
+    _expect(dy, "dy", x.shape, x.dtype, dev)
+    with _on(stream, dev):
+        if out is None:
+            make = torch.zeros if lengths is not None else torch.empty
+            out = tuple(make(x.shape, dtype=x.dtype, device=dev) for _ in range(1 if gate is None else 2))
+        elif gate is None:
+            out = (out,) if torch.is_tensor(out) else tuple(out)
+        dx, dg = out[0], out[1] if gate is not None else None
+        for t, name in ((dx, "dx"), (dg, "d_gate")):
+            if t is not None:
+                _expect(t, name, x.shape, x.dtype, dev)
+        dw = torch.empty((p.d,), dtype=torch.float32, device=dev) if weight is not None else None
+        db = torch.empty((p.d,), dtype=torch.float32, device=dev) if bias is not None else None
+        ws, nbytes = _space(hla_norm_backward_workspace_size(p) if workspace is None else 0, workspace, dev, False)
+        hla_norm_backward(p, _t2(x), None if gate is None else _t2(gate), _t2(dy), _t2(dx),
+                          None if dg is None else _t2(dg), dw, db, ws, nbytes, stream)
+    return NormGradients(dx, dg, dw, db)

@@ -1,0 +1,107 @@
+// hla_layer.cuh -- device helpers of the selective state space layer's kernels: typed vector
+// access, the activation, lengths, and sums of partial results in a fixed order.
+#pragma once
+#include "hla_strided.h"
+
+namespace hla {
+namespace layer {
+
+// sigma(z) from one exponential and one reciprocal, each a few units in the last place off; the
+// exponential overflows to infinity below -88, where sigma is 0 to the last bit that counts.
+HLA_DEVICE float sigmoid(float z) { return __fdividef(1.f, 1.f + ex2_approx(z * -1.4426950408889634f)); }
+HLA_DEVICE float silu(float z) { return z * sigmoid(z); }
+HLA_DEVICE float silu_slope(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }  // s = sigma(z)
+
+HLA_DEVICE int clamp_length(const int *lengths, int b, int n) {
+    if (!lengths) return n;
+    const int L = lengths[b];
+    return L < 0 ? 0 : L > n ? n : L;
+}
+
+// VEC adjacent elements as raw bits: 2 to 16 bytes.
+template <int BYTES>
+struct RawOf;
+template <>
+struct RawOf<2> { using type = unsigned short; };
+template <>
+struct RawOf<4> { using type = unsigned; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<16> { using type = uint4; };
+template <typename T, int VEC>
+using raw_t = typename RawOf<VEC * (int)sizeof(T)>::type;
+
+template <typename T, int VEC>
+HLA_DEVICE raw_t<T, VEC> load_raw(const T *p) { return *reinterpret_cast<const raw_t<T, VEC> *>(p); }
+template <typename T, int VEC>
+HLA_DEVICE void widen(const raw_t<T, VEC> &r, float (&v)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
+        const float *f = reinterpret_cast<const float *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = f[i];
+    } else {
+        const unsigned short *f = reinterpret_cast<const unsigned short *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float((unsigned)f[i] << 16);
+    }
+}
+template <typename T, int VEC>
+HLA_DEVICE raw_t<T, VEC> narrow(const float (&v)[VEC]) {
+    raw_t<T, VEC> r;
+    if constexpr (sizeof(T) == 4) {
+        float *f = reinterpret_cast<float *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = v[i];
+    } else if constexpr (VEC == 1) {
+        r = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else {
+        unsigned *f = reinterpret_cast<unsigned *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) f[i / 2] = pack_bf16(v[i], v[i + 1]);
+    }
+    return r;
+}
+template <typename T, int VEC>
+HLA_DEVICE void store_raw(T *p, const raw_t<T, VEC> &r) { *reinterpret_cast<raw_t<T, VEC> *>(p) = r; }
+
+// VEC floats of an aligned or single-channel array.
+template <int VEC>
+HLA_DEVICE void load_f32(const float *p, float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = __ldg(p + i);
+}
+
+// out[k] = sum over r of part[r][k], k < cols: 8 warps take rows w, w + 8, ..., then the warps are
+// added, so the order depends on the sizes alone.
+template <class Store>
+HLA_DEVICE void column_sums(const float *part, int rows, long long cols, Store store) {
+    __shared__ float red[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long c = (long long)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < cols) {
+        const float *p = part + c;
+        int r = warp;
+        for (; r + 24 < rows; r += 32) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __ldg(p + (size_t)(r + 8 * i) * cols);
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; r < rows; r += 8) s += __ldg(p + (size_t)r * cols);
+    }
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += red[w][lane];
+        store(c, t);
+    }
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace layer
+}  // namespace hla

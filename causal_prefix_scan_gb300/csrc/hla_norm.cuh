@@ -1,0 +1,117 @@
+// hla_norm.cuh -- norm over groups of adjacent channels of each token, with an activation or an
+// activated gate:
+//   u = x (or x silu(gate)),  z = (u - mean) r (or u r),  v = z w + bias,  y = v | silu(v) | v silu(gate).
+// Backward, with dv the gradient of v, g = dv w, and means over the group:
+//   du = r (g - z mean(g z) - mean(g))   (without the last term where the mean is not taken),
+//   dw = sum over tokens of dv z,  dbias = sum of dv.
+// Memory bounds both: a team of threads holds a group of one token in registers, E channels each,
+// so every element is read once and written once; statistics are two-pass over the registers, in
+// fp32.  A CTA keeps its channels from token to token (the scale, the shift and the sums for dw and
+// dbias stay in registers) and loads the next token before it reduces the present one.  Groups
+// wider than a team holds go through a kernel that reads them again for each pass.
+#pragma once
+#include "hla_layer.cuh"
+
+namespace hla {
+namespace norm {
+
+using namespace layer;
+
+enum Gate { GATE_NONE = 0, GATE_AFTER = 1, GATE_BEFORE = 2 };
+
+struct Args {
+    int B, n, d, groups, m;  // m = d / groups
+    int col_blocks, row_blocks;
+    int gate;
+    bool center, silu;
+    float eps;
+    const float *weight, *bias;
+    const int *lengths;
+    View x, z, y, dy, dx, dz;
+    float *part;  // [row_blocks][2][d]
+};
+
+// Most channels of a group that a team holds: E = 16 of 512 threads.
+constexpr int kHeld = 8192;
+
+// Rows that the CTA's row block takes: r, r + row_blocks, ... of those below their lengths.
+struct Rows {
+    const Args &a;
+    long long r, total;
+    int b, t;
+    HLA_DEVICE Rows(const Args &a_, int first) : a(a_), r((long long)first - a_.row_blocks), total((long long)a_.B * a_.n), b(0), t(0) { next(); }
+    HLA_DEVICE bool live() const { return r < total; }
+    HLA_DEVICE void next() {
+        for (r += a.row_blocks; r < total; r += a.row_blocks) {
+            b = (int)(r / a.n);
+            t = (int)(r - (long long)b * a.n);
+            if (!a.lengths || t < a.lengths[b]) return;
+        }
+    }
+};
+
+template <typename T>
+HLA_DEVICE const T *row_in(const View &v, int b, int t) {
+    return static_cast<const T *>(v.p) + (size_t)b * v.sb + (size_t)t * v.st;
+}
+template <typename T>
+HLA_DEVICE T *row_to(const View &v, int b, int t) {
+    return static_cast<T *>(v.p) + (size_t)b * v.sb + (size_t)t * v.st;
+}
+
+// Sums of two values over a team of TEAM threads; `red` holds one float2 for each warp of the
+// block, alternated by the caller so that one barrier per sum is enough.
+template <int TEAM>
+HLA_DEVICE float2 team_sum(float2 v, float2 *red) {
+    constexpr int LANES = TEAM < 32 ? TEAM : 32;
+#pragma unroll
+    for (int o = LANES >> 1; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if constexpr (TEAM > 32) {
+        constexpr int WARPS = TEAM / 32;
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) red[warp] = v;
+        __syncthreads();
+        const float2 *mine = red + warp / WARPS * WARPS;
+        v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            v.x += mine[w].x;
+            v.y += mine[w].y;
+        }
+    }
+    return v;
+}
+
+// `wide`: rows on 16-byte boundaries and groups of whole 16-byte pieces.
+cudaError_t backward(const Args &a, hla_dtype dt, bool wide, float *dw, float *db, cudaStream_t st);
+
+// The team of a group of m <= kHeld channels: the smallest that holds it.
+struct Team {
+    int threads, E;
+};
+inline Team team_of(int m) {
+    for (int t = 8; t <= 512; t *= 4)
+        for (int E = 8; E <= 16; E += 8)
+            if (m <= t * E) return {t, E};
+    return {256, 0};  // read again for each pass, one CTA per group
+}
+constexpr int kSms = 152;
+constexpr int block_of(int team) { return team > 256 ? team : 256; }
+// CTAs side by side over the channels of a token, and over the tokens: about as many as the
+// device runs at once (the sums for dw and dbias are kept per CTA).
+inline int columns_of(int groups, int m) {
+    const Team t = team_of(m);
+    if (!t.E) return groups;
+    const int per = block_of(t.threads) / t.threads;
+    return (groups + per - 1) / per;
+}
+inline int row_blocks_of(long long rows, int groups, int m, int threads_per_sm) {
+    const long long most = (long long)kSms * (threads_per_sm / block_of(team_of(m).threads)) / columns_of(groups, m);
+    return (int)(most < 1 ? 1 : most < rows ? most : rows);
+}
+
+}  // namespace norm
+}  // namespace hla

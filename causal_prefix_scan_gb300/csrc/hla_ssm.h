@@ -1,0 +1,121 @@
+// hla_ssm.h -- argument bundle and shared pieces of the selective state space scan's kernels.
+//
+// Per head, with the log decay a_t = dt_t A log2(e) (not below -256) and s its running sum inside
+// a chunk of Q tokens (inclusive; e = 2^s from the chunk's start to a token, r = 2^(s_end - s) from
+// the token to the chunk's end, L_tj = 2^(s_t - s_j) for j <= t):
+//   h' = 2^s_end h + B^T diag(dt r) X                    state after the chunk
+//   Y  = ((C B^T) o L diag(dt)) X + diag(e) C h + D X
+// and backward, with g the gradient of the state after the chunk and g' that of h:
+//   g' = 2^s_end g + C^T diag(e) dY
+//   M = (C B^T) o L,  S = (dY X^T) o L,  E = M o (dY X^T)
+//   dX = diag(dt) (M^T dY + diag(r) B g) + D dY
+//   dB = diag(dt) (S^T C + diag(r) X g^T),   dC = S diag(dt) B + diag(e) dY h^T   (sums over a group's heads)
+//   v_j = sum_t E_tj + r_j B_j.(X g^T)_j,  w_t = sum_j E_tj dt_j + e_t C_t.(dY h^T)_t
+//   da_t = 2^s_end <g, h> + sum_{i >= t} (w_i - dt_i vE_i) + sum_{j < t} dt_j vg_j
+//          (what passes token t from those before it to those behind it; vE, vg the two parts of v)
+//   d_dt = A da + v,  dA = sum dt da,  dD = sum dY.X
+// Every exponent is a sum of a's between two tokens, so nothing overflows while A <= 0 <= dt.
+#pragma once
+#include "hla_layer.cuh"
+
+namespace hla {
+namespace ssm {
+
+using namespace layer;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeast = -256.f;  // 2^-256 is 0 next to any other fp32 factor
+
+struct Args {
+    int B, H, G, R;  // R = H / G heads to a group
+    int n, P, N;
+    bool softplus;
+    const float *A, *D, *dt_bias;
+    const int *lengths;
+    View x, dt, b, c, y, dy, dx, ddt, db, dc;
+    const float *state_in, *d_state_out;
+    float *state_out, *d_state_in, *dA, *dD, *dbias;
+    // workspace
+    int nc;               // chunks of a sequence
+    int splits;           // backward: CTAs that share a group's heads
+    float *h, *g;         // [B][H][nc][N][P]: states and their gradients
+    float *factor;        // [B][H][nc]: 2^s_end
+    float *dbc;           // [splits][2][B][G][n][N]
+    float *sums;          // [B][nc][3][H]: parts of dA, dD, dt_bias' gradient
+    unsigned *err;
+};
+
+// dt as the recurrence takes it.
+HLA_DEVICE float softplus(float x) {  // log(1 + e^x), both parts a few units in the last place off
+    return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+}
+
+// One chunk's steps and running log decays.  The sum is kept in two parts, whole numbers (exact)
+// and a remainder below one half, so that a difference of neighbours behind a steep decay keeps
+// its bits: 2^(s_t - s_j) comes out within 2^-21 whatever s is.
+struct Decay {
+    float hi, lo;
+};
+HLA_DEVICE float factor(Decay t, Decay j) { return ex2_approx((t.hi - j.hi) + (t.lo - j.lo)); }
+HLA_DEVICE float factor(Decay t) { return ex2_approx(t.hi + t.lo); }
+
+template <typename T>
+HLA_DEVICE float step_of(const Args &a, int b, int h, int t, float bias, float &slope) {
+    const T *p = static_cast<const T *>(a.dt.p) + (size_t)b * a.dt.sb + (size_t)h * a.dt.sh + (size_t)t * a.dt.st;
+    float raw[1];
+    widen<T, 1>(load_raw<T, 1>(p), raw);
+    slope = 1.f;
+    if (!a.softplus) return raw[0];
+    const float x = raw[0] + bias;
+    slope = 1.f / (1.f + expf(-x));
+    return softplus(x);
+}
+
+// One warp computes a chunk of PER * 32 tokens from t0 on (zeros behind `len`), PER adjacent
+// tokens a lane.
+template <typename T, int PER>
+HLA_DEVICE void chunk_decays(const Args &a, int b, int h, int t0, int len, float *dt, Decay *s, float *slope) {
+    const int lane = threadIdx.x & 31;
+    const float A2 = a.A[h] * kLog2e, bias = a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f;
+    float d[PER], hi[PER], lo[PER];
+    float sh = 0.f, sl = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = t0 + lane * PER + i;
+        float sp = 0.f;
+        d[i] = t < len ? step_of<T>(a, b, h, t, bias, sp) : 0.f;
+        const float l = fmaxf(d[i] * A2, kLeast), w = rintf(l);
+        sh += w;
+        sl += l - w;
+        hi[i] = sh;
+        lo[i] = sl;
+        if (slope) slope[lane * PER + i] = sp;
+    }
+    float ph = sh, pl = sl;  // sums of the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float uh = __shfl_up_sync(0xffffffffu, ph, o), ul = __shfl_up_sync(0xffffffffu, pl, o);
+        if (lane >= o) {
+            ph += uh;
+            pl += ul;
+        }
+    }
+    ph -= sh;
+    pl -= sl;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const float l = lo[i] + pl, w = rintf(l);
+        dt[lane * PER + i] = d[i];
+        s[lane * PER + i] = {hi[i] + ph + w, l - w};
+    }
+}
+
+// CUDA cores (any strides, widths and types): chunks of 64 tokens, 32 where both widths pass 64.
+inline int simt_chunk(int P, int N) { return P > 64 && N > 64 ? 32 : 64; }
+cudaError_t simt_forward(const Args &a, hla_dtype dt, cudaStream_t st);
+cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st);
+// What both backward paths end with: dB, dC from their parts, dA, dD and dt_bias' gradient.
+cudaError_t join(const Args &a, hla_dtype dt, cudaStream_t st);
+
+}  // namespace ssm
+}  // namespace hla

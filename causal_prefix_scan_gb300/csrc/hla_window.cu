@@ -55,36 +55,6 @@ hla_status check(const hla_window_params *p, bool step) {
     return HLA_OK;
 }
 
-hla_status check_in(const hla_tensor *t, Dims s, hla_dtype dt, const char *what) {
-    if (!t || !t->p) return report(HLA_ERR_ARG, what);
-    if (reinterpret_cast<uintptr_t>(t->p) % (dt == HLA_F32 ? 4 : 2))
-        return report(HLA_ERR_ARG, "a tensor is not aligned to its elements");
-    if (t->sb < 0 || t->sh < 0 || t->st < 0) return report(HLA_ERR_ARG, "strides must not be negative");
-    if ((double)t->sb * (s.B - 1) + (double)t->sh * (s.H - 1) + (double)t->st * (s.n - 1) + s.w > 4e18)
-        return report(HLA_ERR_ARG, "a tensor is too large");
-    return HLA_OK;
-}
-// The rows of an output share no memory: taken from the smallest stride up, each stride
-// passes what lies inside it.
-hla_status check_out(const hla_tensor *t, Dims s, hla_dtype dt, const char *what) {
-    hla_status r = check_in(t, s, dt, what);
-    if (r != HLA_OK) return r;
-    long long st[3] = {t->st, t->sh, t->sb}, n[3] = {s.n, s.H, s.B}, inside = s.w;
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (st[j] < st[i]) {
-                const long long x = st[i], y = n[i];
-                st[i] = st[j]; n[i] = n[j];
-                st[j] = x; n[j] = y;
-            }
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        if (st[i] < inside) return report(HLA_ERR_ARG, "rows of an output overlap");
-        inside += st[i] * (n[i] - 1);
-    }
-    return HLA_OK;
-}
-
 Args make(const hla_window_params *p) {
     Args a{};
     a.B = p->B; a.H = p->H; a.Hkv = p->Hkv; a.G = p->H / p->Hkv;
@@ -191,13 +161,13 @@ hla_status hla_window_forward(const hla_window_params *p, const hla_tensor *q, c
     const hla_dtype dt = p->in_dtype;
     const Dims dq{p->B, p->H, p->n, p->d}, dk{p->B, p->Hkv, p->nk, p->d}, dv{p->B, p->Hkv, p->nk, p->dv},
         od{p->B, p->H, p->n, p->dv};
-    if ((s = win::check_in(q, dq, dt, "q must be set")) != HLA_OK || (s = win::check_in(k, dk, dt, "k must be set")) != HLA_OK ||
-        (s = win::check_in(v, dv, dt, "v must be set")) != HLA_OK || (s = win::check_out(o, od, dt, "o must be set")) != HLA_OK)
+    if ((s = check_in(q, dq, dt, "q must be set")) != HLA_OK || (s = check_in(k, dk, dt, "k must be set")) != HLA_OK ||
+        (s = check_in(v, dv, dt, "v must be set")) != HLA_OK || (s = check_out(o, od, dt, "o must be set")) != HLA_OK)
         return s;
     if (o->p == q->p || o->p == k->p || o->p == v->p) return report(HLA_ERR_ARG, "o may not be an input");
     if (reinterpret_cast<uintptr_t>(lse) & 3u) return report(HLA_ERR_ARG, "lse is not aligned to its elements");
     Args a = make(p);
-    a.q = win::view(q, dq); a.k = win::view(k, dk); a.v = win::view(v, dv); a.o = win::view(o, od);
+    a.q = view(q, dq); a.k = view(k, dk); a.v = view(v, dv); a.o = view(o, od);
     a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = dev_status_ptr(&a.err);
@@ -222,12 +192,12 @@ hla_status hla_window_backward(const hla_window_params *p, const hla_tensor *q, 
     const Dims qd{p->B, p->H, p->n, p->d}, kd{p->B, p->Hkv, p->nk, p->d}, vd{p->B, p->Hkv, p->nk, p->dv},
         od{p->B, p->H, p->n, p->dv};
     if (p->n == 0) return p->nk == 0 ? HLA_OK : report(HLA_ERR_ARG, "backward needs n >= 1 when nk >= 1");
-    if ((s = win::check_in(q, qd, dt, "q must be set")) != HLA_OK || (s = win::check_in(k, kd, dt, "k must be set")) != HLA_OK ||
-        (s = win::check_in(v, vd, dt, "v must be set")) != HLA_OK || (s = win::check_in(o, od, dt, "o must be set")) != HLA_OK ||
-        (s = win::check_in(dout, od, dt, "dout must be set")) != HLA_OK ||
-        (s = win::check_out(dq, qd, dt, "dq must be set")) != HLA_OK ||
-        (s = win::check_out(dk, kd, dt, "dk must be set")) != HLA_OK ||
-        (s = win::check_out(dv, vd, dt, "dv must be set")) != HLA_OK)
+    if ((s = check_in(q, qd, dt, "q must be set")) != HLA_OK || (s = check_in(k, kd, dt, "k must be set")) != HLA_OK ||
+        (s = check_in(v, vd, dt, "v must be set")) != HLA_OK || (s = check_in(o, od, dt, "o must be set")) != HLA_OK ||
+        (s = check_in(dout, od, dt, "dout must be set")) != HLA_OK ||
+        (s = check_out(dq, qd, dt, "dq must be set")) != HLA_OK ||
+        (s = check_out(dk, kd, dt, "dk must be set")) != HLA_OK ||
+        (s = check_out(dv, vd, dt, "dv must be set")) != HLA_OK)
         return s;
     if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u)) return report(HLA_ERR_ARG, "lse must be set and aligned");
     const hla_tensor *outs[3] = {dq, dk, dv}, *ins[5] = {q, k, v, o, dout};
@@ -242,8 +212,8 @@ hla_status hla_window_backward(const hla_window_params *p, const hla_tensor *q, 
         return report(HLA_ERR_ARG, "workspace too small (hla_window_backward_workspace_size)");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return report(HLA_ERR_ARG, "workspace must be 256-byte aligned");
     Args a = make(p);
-    a.q = win::view(q, qd); a.k = win::view(k, kd); a.v = win::view(v, vd); a.o = win::view(o, od); a.go = win::view(dout, od);
-    a.dq = win::view(dq, qd); a.dk = win::view(dk, kd); a.dv_ = win::view(dv, vd);
+    a.q = view(q, qd); a.k = view(k, kd); a.v = view(v, vd); a.o = view(o, od); a.go = view(dout, od);
+    a.dq = view(dq, qd); a.dk = view(dk, kd); a.dv_ = view(dv, vd);
     a.lse = const_cast<float *>(lse);
     a.delta = static_cast<float *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + delta_bytes(p));
@@ -274,11 +244,11 @@ hla_status hla_window_step(const hla_window_params *p, const hla_tensor *q, cons
     const long long slots = (long long)p->sinks + p->window;
     const Dims qd{p->B, p->H, 1, p->d}, kd{p->B, p->Hkv, 1, p->d}, vd{p->B, p->Hkv, 1, p->dv}, od{p->B, p->H, 1, p->dv},
         kcd{p->B, p->Hkv, slots, p->d}, vcd{p->B, p->Hkv, slots, p->dv};
-    if ((s = win::check_in(q, qd, dt, "q must be set")) != HLA_OK || (s = win::check_in(k, kd, dt, "k must be set")) != HLA_OK ||
-        (s = win::check_in(v, vd, dt, "v must be set")) != HLA_OK ||
-        (s = win::check_out(kc, kcd, dt, "kc must be set")) != HLA_OK ||
-        (s = win::check_out(vc, vcd, dt, "vc must be set")) != HLA_OK ||
-        (s = win::check_out(o, od, dt, "o must be set")) != HLA_OK)
+    if ((s = check_in(q, qd, dt, "q must be set")) != HLA_OK || (s = check_in(k, kd, dt, "k must be set")) != HLA_OK ||
+        (s = check_in(v, vd, dt, "v must be set")) != HLA_OK ||
+        (s = check_out(kc, kcd, dt, "kc must be set")) != HLA_OK ||
+        (s = check_out(vc, vcd, dt, "vc must be set")) != HLA_OK ||
+        (s = check_out(o, od, dt, "o must be set")) != HLA_OK)
         return s;
     if (!pos || (reinterpret_cast<uintptr_t>(pos) & 7u)) return report(HLA_ERR_ARG, "pos must be set and aligned");
     const hla_tensor *ins[3] = {q, k, v};
@@ -290,8 +260,8 @@ hla_status hla_window_step(const hla_window_params *p, const hla_tensor *q, cons
     a.d = p->d; a.dv = p->dv; a.window = p->window; a.sinks = p->sinks;
     a.scale = p->scale;
     a.pos = pos;
-    a.q = win::view(q, qd); a.k = win::view(k, kd); a.v = win::view(v, vd);
-    a.kc = win::view(kc, kcd); a.vc = win::view(vc, vcd); a.o = win::view(o, od);
+    a.q = view(q, qd); a.k = view(k, kd); a.v = view(v, vd);
+    a.kc = view(kc, kcd); a.vc = view(vc, vcd); a.o = view(o, od);
     a.wide = dt == HLA_BF16 && p->d % 8 == 0 && p->dv % 8 == 0 && wide_rows(a.k) && wide_rows(a.v) && wide_rows(a.kc) &&
              wide_rows(a.vc);
     const cudaError_t e = win::step(a, dt, static_cast<cudaStream_t>(stream));
@@ -312,15 +282,15 @@ hla_status hla_window_cache_fill(const hla_window_params *p, const hla_tensor *k
     if (p->nk == 0) return HLA_OK;
     const Dims kd{p->B, p->Hkv, p->nk, p->d}, vd{p->B, p->Hkv, p->nk, p->dv}, kcd{p->B, p->Hkv, slots, p->d},
         vcd{p->B, p->Hkv, slots, p->dv};
-    if ((s = win::check_in(k, kd, dt, "k must be set")) != HLA_OK || (s = win::check_in(v, vd, dt, "v must be set")) != HLA_OK ||
-        (s = win::check_out(kc, kcd, dt, "kc must be set")) != HLA_OK ||
-        (s = win::check_out(vc, vcd, dt, "vc must be set")) != HLA_OK)
+    if ((s = check_in(k, kd, dt, "k must be set")) != HLA_OK || (s = check_in(v, vd, dt, "v must be set")) != HLA_OK ||
+        (s = check_out(kc, kcd, dt, "kc must be set")) != HLA_OK ||
+        (s = check_out(vc, vcd, dt, "vc must be set")) != HLA_OK)
         return s;
     if (kc->p == vc->p || kc->p == k->p || kc->p == v->p || vc->p == k->p || vc->p == v->p)
         return report(HLA_ERR_ARG, "kc and vc must differ from each other and from k and v");
     Args a = make(&c);
-    a.k = win::view(k, kd); a.v = win::view(v, vd);
-    const View ko = win::view(kc, kcd), vo = win::view(vc, vcd);
+    a.k = view(k, kd); a.v = view(v, vd);
+    const View ko = view(kc, kcd), vo = view(vc, vcd);
     const long long used = slots < p->nk ? slots : p->nk;  // later slots stay as they are
     const long long pairs = (long long)p->B * p->Hkv, most = 2147483647LL / pairs, quads = (used + 3) / 4;
     const int blocks = (int)(quads < 4096 ? (quads < most ? quads : most) : (4096 < most ? 4096 : most));

@@ -1,22 +1,9 @@
 // hla_window.h -- argument bundles shared by the windowed-attention kernels.
 #pragma once
-#include "hla_internal.h"
+#include "hla_strided.h"
 
 namespace hla {
 namespace win {
-
-struct View {
-    void *p;
-    long long sb, sh, st;
-};
-struct Dims {
-    long long B, H, n, w;  // sequences, heads, rows of a head, elements of a row
-};
-// The stride of a dimension with one element is never used: whatever it is, the kernels are
-// chosen by the others.
-inline View view(const hla_tensor *t, Dims s) {
-    return {t->p, s.B > 1 ? t->sb : 0, s.H > 1 ? t->sh : 0, s.n > 1 ? t->st : (s.w + 7) / 8 * 8};
-}
 
 struct Args {
     int B, H, Hkv, G;  // G = H / Hkv query heads to a key/value head

@@ -586,6 +586,136 @@ HLA_API hla_status hla_window_step(const hla_window_params *p, const hla_tensor 
 HLA_API hla_status hla_window_cache_fill(const hla_window_params *p, const hla_tensor *k, const hla_tensor *v,
                                          const hla_tensor *kc, const hla_tensor *vc, void *stream);
 
+/*
+ * ------------------------------------------------------------------ selective state space layer
+ * Short causal convolution, one filter per channel of [B][n][d]: with xs the `width - 1` inputs
+ * of state_in followed by the tokens,
+ *   pre_t = bias + sum_i weight[c][i] xs_{t+i},   y_t = pre_t or silu(pre_t).
+ * fp32 arithmetic; y, dx and the states are rounded to the element type.
+ */
+typedef enum { HLA_ACT_NONE = 0, HLA_ACT_SILU = 1 } hla_activation;
+
+typedef struct {
+    int B, n, d;          /* sequences, tokens per sequence (n >= 0), channels               */
+    int width;            /* taps of a filter, 2..4                                          */
+    hla_dtype in_dtype;   /* element type of x, y, the states and their gradients            */
+    int activation;       /* an hla_activation                                               */
+    const float *weight;  /* [d][width] device fp32, the oldest input's tap first            */
+    const float *bias;    /* [d] device fp32, or NULL                                        */
+    const int *lengths;   /* [B] device: tokens of each sequence (clamped to 0..n), or NULL: n.
+                             Rows from the length on are neither read nor written.           */
+} hla_conv_params;
+
+/* x, y [B][n][d] (strided, see the gated recurrence).  state_in [B][width-1][d], contiguous, of
+ * the element type: the inputs before the first token, oldest first (NULL: zeros); state_out:
+ * the last width - 1 inputs of each sequence, or NULL; not state_in.  One launch. */
+HLA_API hla_status hla_conv_forward(const hla_conv_params *p, const hla_tensor *x, const hla_tensor *y,
+                                    const void *state_in, void *state_out, void *stream);
+
+/* Gradients: dx; d_weight [d][width] and d_bias [d] fp32 (d_bias may be NULL); d_state_in (or
+ * NULL) from dy and d_state_out (NULL: zeros), laid out as the states.  workspace: at least
+ * hla_conv_backward_workspace_size(p) bytes, 256-byte aligned, no initial contents needed.  Two
+ * launches; the same bits on every call. */
+HLA_API size_t hla_conv_backward_workspace_size(const hla_conv_params *p);
+HLA_API hla_status hla_conv_backward(const hla_conv_params *p, const hla_tensor *x, const hla_tensor *dy,
+                                     const hla_tensor *dx, const void *state_in, const void *d_state_out,
+                                     float *d_weight, float *d_bias, void *d_state_in, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* One token of every sequence (p->n must be 1; st is not used): x, y [B][d]; state is shifted by
+ * one in place.  With lengths, a sequence of length 0 is idle: its row of y and its state are
+ * left as they were. */
+HLA_API hla_status hla_conv_step(const hla_conv_params *p, const hla_tensor *x, const hla_tensor *y, void *state,
+                                 void *stream);
+
+/*
+ * Selective state space scan: per head h with the state h_t [N][P] (fp32) and the decay that
+ * each token's step dt chooses,
+ *   h_t = exp(dt_t A) h_{t-1} + dt_t b_t x_t^T,   y_t = c_t h_t + D x_t,
+ * dt_t as given, or softplus(dt_t + dt_bias).  x, y [B][H][n][P], dt [B][H][n], b, c [B][G][n][N]
+ * (strided; head h reads group h / (H / G)).  A <= 0 and dt >= 0 keep the state bounded; other
+ * values are computed as they are.  A step's log decay dt A log2(e) is taken as -256 where it is
+ * below that.
+ */
+typedef struct {
+    int B, H, G;            /* sequences, heads, groups of heads that share b and c (H % G == 0) */
+    int n;                  /* tokens per sequence (n >= 0)                                  */
+    int P, N;               /* widths of a head and of its state, 1..128                     */
+    hla_dtype in_dtype;     /* element type of x, dt, b, c, y and of their gradients         */
+    int dt_softplus;        /* 0 or 1                                                        */
+    const float *A;         /* [H] device fp32                                               */
+    const float *D;         /* [H] device fp32, or NULL (no such term)                       */
+    const float *dt_bias;   /* [H] device fp32, or NULL (zeros)                              */
+    const int *lengths;     /* [B] device: tokens of each sequence (clamped to 0..n), or NULL: n.
+                               Rows from the length on are neither read nor written.         */
+} hla_ssm_params;
+
+/* Bytes of workspace of hla_ssm_forward (backward 0) or hla_ssm_backward (1); 256-byte aligned,
+ * no initial contents needed; calls that may overlap in time need one each. */
+HLA_API size_t hla_ssm_workspace_size(const hla_ssm_params *p, int backward);
+
+/* The scan over n tokens.  state_in [B][H][N][P] fp32 or NULL (zeros); state_out after each
+ * sequence's last token, or NULL; not state_in.  bf16 with 16-byte aligned rows (pointers,
+ * strides and widths of x, b, c, y in multiples of 8 elements) runs on the tensor cores,
+ * everything else on the CUDA cores in fp32.  The same bits on every call. */
+HLA_API hla_status hla_ssm_forward(const hla_ssm_params *p, const hla_tensor *x, const hla_tensor *dt,
+                                   const hla_tensor *b, const hla_tensor *c, const hla_tensor *y,
+                                   const float *state_in, float *state_out, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Its gradients, written, not accumulated: dx, d_dt, db, dc (sums over each group's heads) like
+ * their tensors; dA [H], dD [H] (NULL without D), d_dt_bias [H] (or NULL) and d_state_in (or NULL)
+ * fp32, from dy and d_state_out (NULL: zeros).  The same bits on every call. */
+typedef struct {
+    hla_tensor dx, d_dt, db, dc;
+    float *dA, *dD, *d_dt_bias, *d_state_in;
+} hla_ssm_gradients;
+HLA_API hla_status hla_ssm_backward(const hla_ssm_params *p, const hla_tensor *x, const hla_tensor *dt,
+                                    const hla_tensor *b, const hla_tensor *c, const hla_tensor *dy,
+                                    const float *state_in, const float *d_state_out, const hla_ssm_gradients *grads,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of every sequence (p->n must be 1; st is not used): x, y [B][H][P], dt [B][H], b, c
+ * [B][G][N]; state [B][H][N][P] is updated in place.  With lengths, a sequence of length 0 is idle:
+ * its rows of y and its state are left as they were.  One launch. */
+HLA_API hla_status hla_ssm_step(const hla_ssm_params *p, const hla_tensor *x, const hla_tensor *dt,
+                                const hla_tensor *b, const hla_tensor *c, const hla_tensor *y, float *state,
+                                void *stream);
+
+/*
+ * Norm over groups of d / groups adjacent channels of each token of [B][n][d] (a causal layer's
+ * token may not see later ones, so each token has its own statistics):
+ *   u = x, or x silu(gate) with gate_first;   z = (u - mean) / sqrt(var + eps), or without
+ *   `center` z = u / sqrt(mean(u^2) + eps);   v = z weight + bias;
+ *   y = v silu(gate) with a gate that is not first, silu(v) with HLA_ACT_SILU and no gate, else v.
+ * fp32 arithmetic, rounded once.
+ */
+typedef struct {
+    int B, n, d;          /* sequences, tokens per sequence (n >= 0), channels               */
+    int groups;           /* d % groups == 0                                                 */
+    hla_dtype in_dtype;
+    int center;           /* 0 or 1                                                          */
+    int activation;       /* an hla_activation; with a gate HLA_ACT_SILU                     */
+    int gate_first;       /* 0 or 1; 1 needs a gate                                          */
+    float eps;            /* >= 0                                                            */
+    const float *weight;  /* [d] device fp32, or NULL (ones)                                 */
+    const float *bias;    /* [d] device fp32, or NULL (zeros)                                */
+    const int *lengths;   /* [B] device, as above                                            */
+} hla_norm_params;
+
+/* gate [B][n][d] or NULL.  One launch. */
+HLA_API hla_status hla_norm_forward(const hla_norm_params *p, const hla_tensor *x, const hla_tensor *gate,
+                                    const hla_tensor *y, void *stream);
+
+/* Gradients dx, d_gate (with a gate), d_weight and d_bias [d] fp32 (or NULL), from x, gate and dy.
+ * workspace: at least hla_norm_backward_workspace_size(p) bytes (the same for every number of
+ * groups), 256-byte aligned, no initial contents needed.  Two launches; the same bits on every call. */
+HLA_API size_t hla_norm_backward_workspace_size(const hla_norm_params *p);
+HLA_API hla_status hla_norm_backward(const hla_norm_params *p, const hla_tensor *x, const hla_tensor *gate,
+                                     const hla_tensor *dy, const hla_tensor *dx, const hla_tensor *d_gate,
+                                     float *d_weight, float *d_bias, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif
