@@ -177,8 +177,10 @@ extern "C" {
 
 size_t hla_ssm_workspace_size(const hla_ssm_params *p, int backward) {
     if (ssm::check(p) != HLA_OK || p->n == 0) return 0;
-    Args a = make(p);
-    return simt_space(a, backward != 0, nullptr);
+    Args a = make(p), t = a;  // for either path: the alignment decides between them
+    const size_t s = simt_space(a, backward != 0, nullptr);
+    const size_t c = p->in_dtype == HLA_BF16 ? tc_space(t, backward != 0, nullptr) : 0;
+    return s > c ? s : c;
 }
 
 hla_status hla_ssm_forward(const hla_ssm_params *p, const hla_tensor *x, const hla_tensor *dt, const hla_tensor *b,
@@ -205,8 +207,15 @@ hla_status hla_ssm_forward(const hla_ssm_params *p, const hla_tensor *x, const h
     if ((s = take_workspace(a, false, workspace, workspace_bytes, hla_ssm_workspace_size(p, 0))) != HLA_OK) return s;
     a.x = view(x, d.x); a.dt = view(dt, d.dt); a.b = view(b, d.b); a.c = view(c, d.b); a.y = view(y, d.x);
     a.state_in = state_in; a.state_out = state_out;
-    simt_space(a, false, static_cast<uint8_t *>(workspace));
-    const cudaError_t e = simt_forward(a, t, st);
+    cudaError_t e = cudaErrorNotSupported;
+    if (t == HLA_BF16 && tc_takes(a, false)) {
+        tc_space(a, false, static_cast<uint8_t *>(workspace));
+        e = tc_forward(a, st);
+    }
+    if (e == cudaErrorNotSupported) {
+        simt_space(a, false, static_cast<uint8_t *>(workspace));
+        e = simt_forward(a, t, st);
+    }
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 

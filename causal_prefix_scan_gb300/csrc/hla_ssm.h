@@ -117,5 +117,12 @@ cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st);
 // What both backward paths end with: dB, dC from their parts, dA, dD and dt_bias' gradient.
 cudaError_t join(const Args &a, hla_dtype dt, cudaStream_t st);
 
+// Tensor cores: bf16 whose rows start on 16-byte boundaries (tc_takes); the workspace's bytes, its
+// pointers set when `base` is given; cudaErrorNotSupported, with nothing launched, when the driver
+// cannot describe a tensor to the TMA unit.
+bool tc_takes(const Args &a, bool backward);
+size_t tc_space(Args &a, bool backward, uint8_t *base);
+cudaError_t tc_forward(const Args &a, cudaStream_t st);
+
 }  // namespace ssm
 }  // namespace hla

@@ -222,6 +222,14 @@ def test_many_heads_share_a_group():
     check(inputs(1, 24, 2, 70, 32, 16, F32, seed=4))
 
 
+@pytest.mark.parametrize("dtype,P,N", [(BF16, 64, 128), (BF16, 72, 64), (F32, 40, 24)])
+def test_long_sequences(dtype, P, N):
+    """A head's chunks shared by several CTAs; lengths that end inside the first, a middle and the last share."""
+    c = inputs(4, 1, 1, 2500, P, N, dtype, seed=6, rates=(0.05, 0.5))
+    check(c, torch.tensor([2500, 90, 1100, 2433], dtype=torch.int32, device="cuda"))
+    check(inputs(1, 2, 2, 2100, P, N, dtype, seed=7), state=False)
+
+
 def test_gradient_against_differences():
     c = inputs(1, 2, 1, 70, 8, 8, F32)
     f = lambda dt: (hla.ssm_forward(c["x"], dt, c["A"], c["B"], c["C"], dt_bias=c["dt_bias"], dt_softplus=True).double() * c["dy"].double()).sum()  # noqa: E731
