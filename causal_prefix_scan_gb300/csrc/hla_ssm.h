@@ -41,6 +41,7 @@ struct Args {
     float *h, *g;         // [B][H][nc][N][P]: states and their gradients
     float *factor;        // [B][H][nc]: 2^s_end
     float *dbc;           // [splits][2][B][G][n][N]
+    void *dec;            // [B][H][nc]: the chunks' weights (tensor cores)
     float *sums;          // [B][nc][3][H]: parts of dA, dD, dt_bias' gradient
     unsigned *err;
 };
@@ -60,36 +61,34 @@ HLA_DEVICE float factor(Decay t, Decay j) { return ex2_approx((t.hi - j.hi) + (t
 HLA_DEVICE float factor(Decay t) { return ex2_approx(t.hi + t.lo); }
 
 template <typename T>
-HLA_DEVICE float step_of(const Args &a, int b, int h, int t, float bias, float &slope) {
-    const T *p = static_cast<const T *>(a.dt.p) + (size_t)b * a.dt.sb + (size_t)h * a.dt.sh + (size_t)t * a.dt.st;
+HLA_DEVICE float raw_step(const Args &a, int b, int h, int t) {
     float raw[1];
-    widen<T, 1>(load_raw<T, 1>(p), raw);
+    widen<T, 1>(load_raw<T, 1>(static_cast<const T *>(a.dt.p) + (size_t)b * a.dt.sb + (size_t)h * a.dt.sh + (size_t)t * a.dt.st), raw);
+    return raw[0];
+}
+HLA_DEVICE float step_from(const Args &a, float raw, float bias, float &slope) {
     slope = 1.f;
-    if (!a.softplus) return raw[0];
-    const float x = raw[0] + bias;
-    slope = 1.f / (1.f + expf(-x));
-    return softplus(x);
+    if (!a.softplus) return raw;
+    slope = 1.f / (1.f + expf(-(raw + bias)));
+    return softplus(raw + bias);
+}
+template <typename T>
+HLA_DEVICE float step_of(const Args &a, int b, int h, int t, float bias, float &slope) {
+    return step_from(a, raw_step<T>(a, b, h, t), bias, slope);
 }
 
-// One warp computes a chunk of PER * 32 tokens from t0 on (zeros behind `len`), PER adjacent
-// tokens a lane.
-template <typename T, int PER>
-HLA_DEVICE void chunk_decays(const Args &a, int b, int h, int t0, int len, float *dt, Decay *s, float *slope) {
+// One warp, PER adjacent tokens of a chunk a lane: their steps d to running log decays s.
+template <int PER>
+HLA_DEVICE void scan_decays(const float (&d)[PER], float A2, Decay (&s)[PER]) {
     const int lane = threadIdx.x & 31;
-    const float A2 = a.A[h] * kLog2e, bias = a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f;
-    float d[PER], hi[PER], lo[PER];
-    float sh = 0.f, sl = 0.f;
+    float hi[PER], lo[PER], sh = 0.f, sl = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int t = t0 + lane * PER + i;
-        float sp = 0.f;
-        d[i] = t < len ? step_of<T>(a, b, h, t, bias, sp) : 0.f;
         const float l = fmaxf(d[i] * A2, kLeast), w = rintf(l);
         sh += w;
         sl += l - w;
         hi[i] = sh;
         lo[i] = sl;
-        if (slope) slope[lane * PER + i] = sp;
     }
     float ph = sh, pl = sl;  // sums of the lanes up to this one
 #pragma unroll
@@ -105,8 +104,29 @@ HLA_DEVICE void chunk_decays(const Args &a, int b, int h, int t0, int len, float
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const float l = lo[i] + pl, w = rintf(l);
+        s[i] = {hi[i] + ph + w, l - w};
+    }
+}
+
+// A chunk of PER * 32 tokens from t0 on (zeros behind `len`), by one warp.
+template <typename T, int PER>
+HLA_DEVICE void chunk_decays(const Args &a, int b, int h, int t0, int len, float *dt, Decay *s, float *slope) {
+    const int lane = threadIdx.x & 31;
+    const float bias = a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f;
+    float d[PER];
+    Decay r[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = t0 + lane * PER + i;
+        float sp = 0.f;
+        d[i] = t < len ? step_of<T>(a, b, h, t, bias, sp) : 0.f;
+        if (slope) slope[lane * PER + i] = sp;
+    }
+    scan_decays(d, a.A[h] * kLog2e, r);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
         dt[lane * PER + i] = d[i];
-        s[lane * PER + i] = {hi[i] + ph + w, l - w};
+        s[lane * PER + i] = r[i];
     }
 }
 

@@ -8,8 +8,8 @@
 // are then read twice, states only at the pieces' ends, and no CTA waits for another.
 //   Backward the same kernels run from the last chunk to the first on C and dY.
 //
-// Roles of a CTA (19 warps): 0-15 elementwise, a thread has one row (a token, or a row of the
-// state) and a quarter of its columns; 16 MMA; 17 TMA; 18 the chunk's weights.
+// The weighted rows' two parts are one operand of 128 columns (each row of B is read once for
+// both); their sums are added when they are read.
 #pragma once
 #include "hla_ssm_tc.cuh"
 
@@ -24,141 +24,177 @@ struct Params {
     CUtensorMap mx[2], mb[2], mc, my;
     float *pieces[2];         // [B][H][pieces][N][P]: sums, then start states
     float *factor;            // [B][H][pieces]: decay over a piece
+    const Dec *dec;           // [B][H][chunks]
     uint8_t *image[2];        // STATES: [B][H][PT][chunks][hi, lo][NB * 64 rows][64] tile images
 };
 
 HLA_DEVICE float *piece_state(const Params &p, int dir, const Piece &w) {
     return p.pieces[dir] + (((size_t)w.b * p.a.H + w.h) * p.plan.pieces + w.piece) * p.a.N * p.a.P;
 }
-// This thread's 16 columns of row n of an fp32 [N][P] state.
-HLA_DEVICE void load_state16(const Args &a, const float *s, int n, int c0, float (&v)[16]) {
+// This thread's 16 columns of row n of an fp32 [N][P] state (which may lie on any float).
+HLA_DEVICE void load_state(const Args &a, const float *s, int n, int c0, float2 (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s && n < a.N && c0 + i < a.P) {
-            const float *q = s + (size_t)n * a.P + c0 + i;
-            x = make_float4(q[0], q[1], q[2], q[3]);  // (a caller's state may lie on any float)
-        }
-        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+    for (int i = 0; i < 8; ++i) {  // (widths are multiples of 8)
+        const float *q = s + (size_t)n * a.P + c0 + 2 * i;
+        v[i] = s && n < a.N && c0 + 2 * i < a.P ? make_float2(q[0], q[1]) : make_float2(0.f, 0.f);
     }
 }
-HLA_DEVICE void store_state16(const Args &a, float *s, int n, int c0, const float (&v)[16]) {
+HLA_DEVICE void store_state(const Args &a, float *s, int n, int c0, const float2 (&v)[8]) {
     if (n >= a.N) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (c0 + i < a.P) s[(size_t)n * a.P + c0 + i] = v[i];
+    for (int i = 0; i < 8; ++i)
+        if (c0 + 2 * i < a.P) {
+            s[(size_t)n * a.P + c0 + 2 * i] = v[i].x;
+            s[(size_t)n * a.P + c0 + 2 * i + 1] = v[i].y;
+        }
+}
+// Columns [c, c + 16) of both parts' sums, added.
+HLA_DEVICE void load_parts16(uint32_t taddr, float2 (&v)[8]) {
+    float2 lo[8];
+    tmem_pairs16(taddr, v);
+    tmem_pairs16(taddr + 64, lo);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = add2(v[i], lo[i]);
+}
+// D [128 x 128] (+)= B^T (hi | lo) over a chunk's 128 tokens.
+HLA_DEVICE void mma_state(uint32_t d, uint64_t b, uint64_t w, bool acc) {
+    constexpr uint32_t id = make_idesc(T, T, true, true);
+    mma_mm64(d, b, w, id, acc);
+    mma_mm64(d, b + kRows64, w + kRows64, id, true);
+}
+
+// Phase of use i of a ring of NS slots.
+template <int NS>
+HLA_DEVICE uint32_t ring_phase(int i) { return (uint32_t)(i / NS) & 1u; }
+// A tile that ends behind the sequence comes by way of barrier `raw` and is cleared there.
+HLA_DEVICE bool clear_landed(const Waits &ws, int raw, uint32_t &phase, int bar, uint8_t *tile, int blocks, int rows) {
+    if (!ws.wait(raw, phase)) return false;
+    phase ^= 1u;
+    clear_rows(tile, blocks, rows);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(ws.bar(bar));
+    return true;
 }
 
 // ------------------------------------------------------------ sums of pieces
+// HB heads of a group go through a piece together and share its tiles of B: those are twice the
+// bytes of a head's X, and what an SM takes in bounds the kernel.
+constexpr int kSumThreads = 19 * 32;
 template <int NB>
 struct LaySum {
-    static constexpr int NS = 3;
-    static constexpr int STAGE = kHalf + NB * kHalf;  // X, then B
-    static constexpr int OFF_X = 0, OFF_W = NS * STAGE, OFF_DEC = OFF_W + 2 * 2 * kHalf;  // weighted rows: two of (hi, lo)
-    static constexpr int OFF_BAR = OFF_DEC + 2 * (int)sizeof(Dec);
-    static constexpr int B_FULL = 0, B_EMPTY = B_FULL + NS, B_DF = B_EMPTY + NS, B_DE = B_DF + 2, B_W = B_DE + 2, B_WE = B_W + 2,
-                         B_OUT = B_WE + 2, B_FIN = B_OUT + 1, B_RAW = B_FIN + 1, NBAR = B_RAW + 1;
+    static constexpr int NX = 3, NR = 3;  // stages of X and its weights, of B
+    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_DEC = OFF_W + 2 * 2 * kHalf;
+    static constexpr int OFF_BAR = OFF_DEC + NX * kDecBytes;
+    static constexpr int B_X = 0, B_XE = B_X + NX, B_R = B_XE + NX, B_RE = B_R + NR, B_W = B_RE + NR, B_WE = B_W + 2, B_OUT = B_WE + 2,
+                         B_FIN = B_OUT + 1, B_RAW = B_FIN + 1, B_RAWX = B_RAW + 1, NBAR = B_RAWX + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
 
-template <int NB>
-__global__ void __launch_bounds__(kThreads, 1) ssm_sum_kernel(const __grid_constant__ Params p) {
+template <int NB, int HB>
+__global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_constant__ Params p) {
     using L = LaySum<NB>;
     extern __shared__ __align__(1024) uint8_t base[];
     const Args &a = p.a;
     const int dir = gridDim.y == 2 ? blockIdx.y : 0;
-    const Piece w = piece_of(a, p.plan, blockIdx.x);
+    const Piece w = piece_of(a, p.plan, blockIdx.x, HB);  // of heads w.h .. w.h + HB - 1
     if (dir ? w.piece == 0 || w.piece >= w.used : w.piece + 1 >= w.used) return;  // no piece starts from it
-    const int K = w.hi - w.lo;
+    const int K = w.hi - w.lo, steps = K * HB;
     auto chunk = [&](int k) { return dir ? w.lo + k : w.hi - 1 - k; };  // towards larger decays
     Cta<L::NBAR> cta(base, L::OFF_BAR, a.err, [](int i) {
-        return (i >= L::B_W && i < L::B_WE) || (i >= L::B_DE && i < L::B_W) ? kElemWarps : i >= L::B_EMPTY && i < L::B_DF ? kElemWarps + 1 : 1;
+        return (i >= L::B_W && i < L::B_WE) || (i >= L::B_XE && i < L::B_R) ? kElemWarps : 1;
     });
     const Waits &ws = cta.ws;
     const int warp = cta.warp, lane = threadIdx.x & 31;
-    Dec *dec = reinterpret_cast<Dec *>(base + L::OFF_DEC);
-    if (warp == kWarpDec) {
-        Decay off{0.f, 0.f};
-        for (int k = 0; k < K; ++k) {
-            Dec &d = dec[k & 1];
-            if (k >= 2 && !ws.wait(L::B_DE + (k & 1), (uint32_t)((k >> 1) & 1) ^ 1u)) break;
-            fill_dec(a, d, w.b, w.h, chunk(k) * T, w.len, dir == 1, off);
-            const Decay end = d.s[T - 1];
-            const float lo = off.lo + end.lo, r = rintf(lo);
-            off = {off.hi + end.hi + r, lo - r};
-            if (lane == 0) mbar_arrive(ws.bar(L::B_DF + (k & 1)));
-        }
-        if (w.pt == 0 && dir == 0 && lane == 0) p.factor[((size_t)w.b * a.H + w.h) * p.plan.pieces + w.piece] = factor(off);
-        if (w.pt == 0 && dir == 1 && lane == 0 && w.piece + 1 == w.used)  // the forward direction leaves this one out
-            p.factor[((size_t)w.b * a.H + w.h) * p.plan.pieces + w.piece] = factor(off);
-    } else if (warp == kWarpTma) {
+    if (warp == kWarpTma || warp == kWarpTmaX) {  // B; X and its weights: neither waits for the other's slots
+        const bool is_x = warp == kWarpTmaX;
+        const int loads = is_x ? steps : K, NS = is_x ? L::NX : L::NR, full = is_x ? L::B_X : L::B_R, empty = is_x ? L::B_XE : L::B_RE;
+        static_assert(L::NX == L::NR, "phases are counted alike");
         uint32_t raw = 0;
-        int k = 0;
-        for (; k < K; ++k) {
-            const int s = k % L::NS;
-            if (k >= L::NS && !ws.wait(L::B_EMPTY + s, (uint32_t)((k / L::NS) & 1) ^ 1u)) break;
-            const int t0 = chunk(k) * T;
-            const bool clean = w.len - t0 < T;
-            const int full = clean ? L::B_RAW : L::B_FULL + s;
-            uint8_t *x = base + s * L::STAGE;
+        int i = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (; i < loads && ok; ++i) {
+            const int s = i % L::NX, c = chunk(is_x ? i / HB : i), t0 = c * T, h = w.h + (is_x ? i % HB : 0);
+            const bool clear = w.len - t0 < T;
+            if (i >= NS && !(ok = ws.wait(empty + s, ring_phase<L::NX>(i) ^ 1u))) break;
+            uint8_t *t = base + (is_x ? L::OFF_X + s * kHalf : L::OFF_R + s * NB * kHalf);
             if (lane == 0) {
-                mbar_expect_tx(ws.bar(full), L::STAGE);
-                load_tile<1>(x, &p.mx[dir], p.vx[dir], ws.bar(full), 64 * w.pt, t0, w.h, w.b);
-                load_tile<NB>(x + kHalf, &p.mb[dir], p.vb[dir], ws.bar(full), 0, t0, w.h / a.R, w.b);
+                uint64_t *bar = ws.bar(!clear ? full + s : is_x ? L::B_RAWX : L::B_RAW);
+                if (is_x) {
+                    mbar_expect_tx(bar, kHalf + kDecBytes);
+                    bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, h, c), kDecBytes, bar);
+                    load_tile<1>(t, &p.mx[dir], p.vx[dir], bar, 64 * w.pt, t0, h, w.b);
+                } else {
+                    mbar_expect_tx(bar, NB * kHalf);
+                    load_tile<NB>(t, &p.mb[dir], p.vb[dir], bar, 0, t0, w.h / a.R, w.b);
+                }
             }
             __syncwarp();
-            if (clean) {
-                if (!ws.wait(L::B_RAW, raw)) break;
-                raw ^= 1u;
-                clear_rows<1 + NB>(x, w.len - t0);
-                if (lane == 0) mbar_arrive(ws.bar(L::B_FULL + s));
-            }
+            if (clear) ok = clear_landed(ws, is_x ? L::B_RAWX : L::B_RAW, raw, full + s, t, is_x ? 1 : NB, w.len - t0);
         }
-        for (int i = max(0, k - L::NS); i < k; ++i) mbar_wait(ws.bar(L::B_FULL + i % L::NS), (uint32_t)(i / L::NS) & 1u, a.err);
+        // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
+        if (ok)
+            for (int e = max(0, i - NS); e < i; ++e) mbar_wait(ws.bar(full + e % L::NX), ring_phase<L::NX>(e), a.err);
         __syncwarp();
     } else if (warp == kWarpMma) {
-        const uint32_t tb = uniform(cta.tb), id = make_idesc(T, 64, true, true);
+        const uint32_t tb = uniform(cta.tb);
         bool ok = true;
-        for (int k = 0; k < K && ok; ++k) {
-            const int s = k % L::NS;
-            if (!(ok = ws.wait(L::B_FULL + s, (uint32_t)(k / L::NS) & 1u) && ws.wait(L::B_W + (k & 1), (uint32_t)(k >> 1) & 1u))) break;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int k = i / HB, j = i % HB, rs = k % L::NR;
+            if (!(ok = ws.wait(L::B_R + rs, ring_phase<L::NR>(k)) && ws.wait(L::B_W + (i & 1), (uint32_t)(i >> 1) & 1u))) break;
             tc_fence_after();
-            const uint64_t A = mnmajor(base + s * L::STAGE + kHalf), W = mnmajor(base + L::OFF_W + (k & 1) * 2 * kHalf);
-            mma_mm64(tb, A, W, id, k > 0);
-            mma_mm64(tb, A + kRows64, W + kRows64, id, true);
-            mma_mm64(tb, A, W + kBlock, id, true);
-            mma_mm64(tb, A + kRows64, W + kBlock + kRows64, id, true);
-            umma_commit_warp(ws.bar(L::B_WE + (k & 1)));
-            umma_commit_warp(ws.bar(L::B_EMPTY + s));
+            mma_state(tb + j * T, mnmajor(base + L::OFF_R + rs * NB * kHalf), mnmajor(base + L::OFF_W + (i & 1) * 2 * kHalf), k > 0);
+            umma_commit_warp(ws.bar(L::B_WE + (i & 1)));
+            if (j == HB - 1) umma_commit_warp(ws.bar(L::B_RE + rs));
         }
         if (ok) umma_commit_warp(ws.bar(L::B_OUT));
-        umma_commit_warp(ws.bar(L::B_FIN));
+        umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
         mbar_wait(ws.bar(L::B_FIN), 0u, a.err);
         __syncwarp();
     } else {
         const int q = warp & 3, cq = warp >> 2, row = 32 * q + lane;
+        float off[HB];  // decay between the chunk and the piece's end (backward its start)
+#pragma unroll
+        for (int j = 0; j < HB; ++j) off[j] = 1.f;
         bool ok = true;
-        for (int k = 0; k < K; ++k) {
-            const int s = k % L::NS, e = k & 1;
-            if (!(ok = ws.wait(L::B_DF + e, (uint32_t)(k >> 1) & 1u) && ws.wait(L::B_FULL + s, (uint32_t)(k / L::NS) & 1u))) break;
-            if (k >= 2 && !(ok = ws.wait(L::B_WE + e, (uint32_t)((k >> 1) & 1) ^ 1u))) break;
+#pragma unroll 1
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % L::NX, e = i & 1, head = i % HB;
+            if (!(ok = ws.wait(L::B_X + s, ring_phase<L::NX>(i)))) break;
+            if (i >= 2 && !(ok = ws.wait(L::B_WE + e, (uint32_t)((i >> 1) & 1) ^ 1u))) break;
+            const Dec &d = *reinterpret_cast<const Dec *>(base + L::OFF_DEC + s * kDecBytes);
+            float f = dir ? d.to[row] : d.w[row];
+#pragma unroll
+            for (int j = 0; j < HB; ++j)
+                if (j == head) {
+                    f *= off[j];
+                    off[j] *= d.end;
+                }
             uint8_t *hi = base + L::OFF_W + e * 2 * kHalf;
-            scale_split16(base + s * L::STAGE, hi, hi + kHalf, row, 16 * cq, dec[e].w[row]);
+            scale_split16(base + L::OFF_X + s * kHalf, hi, hi + kHalf, row, 16 * cq, f);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(ws.bar(L::B_W + e));
-                mbar_arrive(ws.bar(L::B_DE + e));
-                mbar_arrive(ws.bar(L::B_EMPTY + s));
+                mbar_arrive(ws.bar(L::B_XE + s));
             }
+        }
+        // (backward the piece that the forward walk leaves out)
+        if (ok && threadIdx.x == 0 && w.pt == 0 && (dir == 0 || w.piece + 1 == w.used)) {
+#pragma unroll
+            for (int j = 0; j < HB; ++j) p.factor[((size_t)w.b * a.H + w.h + j) * p.plan.pieces + w.piece] = off[j];
         }
         if (ok && ws.wait(L::B_OUT, 0u)) {
             tc_fence_after();
             if (q < 2 * NB) {
-                float v[16];
-                tmem_ld16(cta.tb + ((uint32_t)(32 * q) << 16) + 16 * cq, v);
-                tmem_wait_ld();
-                store_state16(a, piece_state(p, dir, w), row, 64 * w.pt + 16 * cq, v);
+#pragma unroll
+                for (int j = 0; j < HB; ++j) {
+                    float2 v[8];
+                    load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + j * T + 16 * cq, v);
+                    Piece u = w;
+                    u.h += j;
+                    store_state(a, piece_state(p, dir, u), row, 64 * w.pt + 16 * cq, v);
+                }
             }
         }
     }
@@ -196,223 +232,218 @@ static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid
 }
 
 // ------------------------------------------------------------ walk along a piece
+// OUT (forward): the outputs; otherwise (backward, both directions): the state at each chunk as a
+// pair of bf16 tile images.  Roles (20 warps): 0-15 elementwise, 16 MMA, 17 TMA loads of B and C, 18 of X, 19 stores.
+// The elementwise warps take a chunk's steps in an order that leaves the tensor cores a step's time
+// for each product: M of chunk k; state behind k, and its bf16 rows; weighted rows of k + 1; y of k.
+constexpr int kCarryThreads = 20 * 32;
+constexpr float kBlockRange = 60.f;  // log2 of the decay over 32 tokens up to which both halves of a factor are plain numbers
 template <int NB, bool OUT>
 struct LayCarry {
-    static constexpr int NR = OUT ? 3 : 2;  // ring of B and C tiles in turn (STATES: one tile a chunk)
-    static constexpr int OFF_X = 0, OFF_R = 2 * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_H = OFF_W + 2 * kHalf;
-    static constexpr int HB = NB * kHalf / 2;                      // a state's bf16 rows: 64 NB of them
-    static constexpr int OFF_Y = OFF_H + (OUT ? NB * kHalf / 2 : 0);  // OUT: y on its way out; STATES: the state's two parts
-    static constexpr int OFF_DEC = OFF_Y + (OUT ? kHalf : 2 * HB);
-    static constexpr int OFF_BAR = OFF_DEC + 2 * (int)sizeof(Dec);
-    static constexpr int B_X = 0, B_XE = 2, B_R = 4, B_RE = B_R + NR, B_DF = B_RE + NR, B_DE = B_DF + 2, B_W = B_DE + 2, B_D = B_W + 1,
-                         B_CB = B_D + 1, B_M = B_CB + 1, B_A1 = B_M + 1, B_A2 = B_A1 + 1, B_H = B_A2 + 1, B_FIN = B_H + 1,
-                         B_RAW = B_FIN + 1, NBAR = B_RAW + 1;
+    static constexpr int EACH = OUT ? 2 : 1;           // ring tiles of a chunk: C and B, or one
+    static constexpr int NX = OUT ? 3 : 2, NR = OUT ? 3 : 2, NW = OUT ? 1 : 2;
+    static constexpr int HB = NB * kHalf / 2;          // a state's bf16 rows: 64 NB of them
+    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_H = OFF_W + NW * 2 * kHalf;
+    static constexpr int OFF_DEC = OFF_H + (OUT ? HB : 2 * HB);  // OUT: the state; otherwise its two parts on their way out
+    static constexpr int OFF_BAR = OFF_DEC + NX * kDecBytes;
+    static constexpr int B_X = 0, B_XE = B_X + NX, B_R = B_XE + NX, B_RE = B_R + NR, B_W = B_RE + NR, B_D = B_W + 2, B_A2 = B_D + 2,
+                         B_Y = B_A2 + 1, B_YE = B_Y + NX, B_CB = B_YE + 1, B_M = B_CB + 1, B_A1 = B_M + 1, B_H = B_A1 + 1,
+                         B_FIN = B_H + 1, B_RAW = B_FIN + 1, B_RAWX = B_RAW + 1, NBAR = B_RAWX + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
-    static constexpr uint32_t CB = 0, M = T, D = T + 64, A1 = 2 * T, A2 = 2 * T + 64;  // TMEM columns (A2 twice)
+    static constexpr uint32_t CB = 0, M = T, A1 = T + 64, D = 2 * T, A2 = 3 * T;  // TMEM columns (D twice, or A2 twice)
+    HLA_DEVICE static int arrivals(int i) {
+        return (!OUT && i >= B_XE && i < B_R) || i == B_W || i == B_W + 1 || (i >= B_Y && i < B_YE) || i == B_M || i == B_H ? kElemWarps : 1;
+    }
+};
+struct Walk {  // the chunks of a piece in the order they are taken
+    Piece w;
+    int dir, K;
+    HLA_DEVICE int chunk(int k) const { return dir ? w.hi - 1 - k : w.lo + k; }
 };
 
 template <int NB, bool OUT>
-__device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Piece &w, int dir, int K) {
+__device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Walk &z) {
     using L = LayCarry<NB, OUT>;
     const Args &a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, cq = warp >> 2, row = 32 * q + lane;
+    const Piece &w = z.w;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, cq = warp >> 2, row = 32 * q + lane, c0 = 16 * cq;
     const uint32_t lanes = tb + ((uint32_t)(32 * q) << 16);
-    const Dec *dec = reinterpret_cast<const Dec *>(base + L::OFF_DEC);
-    const int col = 64 * w.pt + 16 * cq;
+    const int col = 64 * w.pt + c0;
     const bool holds = q < 2 * NB;  // rows of the state
-    float carry[16];
-    {
-        const size_t unit = ((size_t)w.b * a.H + w.h) * a.N * a.P;
-        const float *init = dir ? a.d_state_out : a.state_in;
-        load_state16(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, dir, w) : init ? init + unit : nullptr, row, col, carry);
-    }
-    auto put_state = [&]() {  // OUT: the state, for C h
-        if (holds) tile_store_row16(base + L::OFF_H, 64 * NB, row, 16 * cq, carry);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ws.bar(L::B_H));
-    };
     const float skip = OUT && a.D ? a.D[w.h] : 0.f;
-    bool ok = true;
-    if (OUT && K > 0) put_state();
-    for (int k = 0; k < K; ++k) {
-        const int e = k & 1, c = dir ? w.hi - 1 - k : w.lo + k;
-        const uint32_t ph = (uint32_t)k & 1u, ph2 = (uint32_t)(k >> 1) & 1u;
-        const Dec &d = dec[e];
-        if constexpr (!OUT) {  // the state before (the gradient behind) this chunk
-            if (threadIdx.x == 0) bulk_wait_read();
-            elem_sync();
-            if (holds) {
-                uint8_t *im = base + L::OFF_Y;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint4 h, l;
-                    split2(carry[8 * g], carry[8 * g + 1], h.x, l.x);
-                    split2(carry[8 * g + 2], carry[8 * g + 3], h.y, l.y);
-                    split2(carry[8 * g + 4], carry[8 * g + 5], h.z, l.z);
-                    split2(carry[8 * g + 6], carry[8 * g + 7], h.w, l.w);
-                    const uint32_t off = tile_off(64 * NB, row, 16 * cq + 8 * g);
-                    *reinterpret_cast<uint4 *>(im + off) = h;
-                    *reinterpret_cast<uint4 *>(im + L::HB + off) = l;
-                }
-            }
-            fence_async_smem();
-            elem_sync();
-            if (threadIdx.x == 0) {
-                const size_t at = (((size_t)w.b * a.H + w.h) * p.plan.PT + w.pt) * a.nc + c;
-                bulk_store(p.image[dir] + at * 2 * L::HB, base + L::OFF_Y, 2 * L::HB);
-                bulk_commit();
-            }
-        }
-        // after an expired wait the loop goes on, so that the barriers above and below stay matched
-        ok = ok && ws.wait(L::B_DF + e, ph2) && ws.wait(L::B_X + e, ph2);
-        const uint8_t *x = base + L::OFF_X + e * kHalf;
-        if (ok) scale_split16(x, base + L::OFF_W, base + L::OFF_W + kHalf, row, 16 * cq, d.w[row]);
+    float2 carry[8];
+    {
+        const float *init = z.dir ? a.d_state_out : a.state_in;
+        load_state(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, z.dir, w) : init ? init + ((size_t)w.b * a.H + w.h) * a.N * a.P : nullptr,
+                   row, col, carry);
+    }
+    auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + k % L::NX * kDecBytes); };
+    auto show = [&](int bar, int bar2) {  // what this warp wrote, to the tensor cores and TMA
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ws.bar(L::B_W));
-        if constexpr (OUT) {  // M = (C B^T) o L diag(dt), bf16, over 32 columns
-            ok = ok && ws.wait(L::B_CB, ph);
+        if (lane == 0) {
+            mbar_arrive(ws.bar(bar));
+            if (bar2 >= 0) mbar_arrive(ws.bar(bar2));
+        }
+    };
+    auto put_state = [&](int k) {  // the state before (the gradient behind) chunk k
+        if constexpr (OUT) {
+            if (holds) {
+                store_row8(base + L::OFF_H, 64 * NB, row, c0, carry);
+                store_row8(base + L::OFF_H, 64 * NB, row, c0 + 8, carry + 4);
+            }
+        } else {
+            if (k > 0 && !ws.wait(L::B_YE, (uint32_t)(k - 1) & 1u)) return false;
+            if (holds) {
+                store_split8(base + L::OFF_H, base + L::OFF_H + L::HB, 64 * NB, row, c0, carry);
+                store_split8(base + L::OFF_H, base + L::OFF_H + L::HB, 64 * NB, row, c0 + 8, carry + 4);
+            }
+            show(L::B_Y + k % L::NX, -1);
+        }
+        return true;
+    };
+    float ahead = 1.f;  // decay over the chunk whose rows were weighted last
+    auto scale = [&](int k) {
+        const int s = k % L::NX, e = L::NW == 2 ? k & 1 : 0;
+        if (!ws.wait(L::B_X + s, ring_phase<L::NX>(k))) return false;
+        const Dec &d = dec(k);
+        uint8_t *hi = base + L::OFF_W + e * 2 * kHalf;
+        scale_split16(base + L::OFF_X + s * kHalf, hi, hi + kHalf, row, c0, z.dir ? d.to[row] : d.w[row]);
+        ahead = d.end;
+        show(L::B_W + e, OUT ? L::B_H : L::B_XE + s);  // OUT: together with the state, one fence for both
+        return true;
+    };
+    bool ok = z.K == 0 || (put_state(0) && scale(0));
+#pragma unroll 1
+    for (int k = 0; k < z.K && ok; ++k) {
+        const uint32_t ph = (uint32_t)k & 1u;
+        const int e = L::NW == 2 ? k & 1 : 0;
+        const float end = ahead;
+        if constexpr (OUT) {
+            // M = (C B^T) o L diag(dt), bf16: this thread's 32 columns, nothing above the diagonal
+            if (!(ok = ws.wait(L::B_CB, ph))) break;
             tc_fence_after();
-            float pk[16];
-            if (cq > q || !ok) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = 0.f;
-            } else {
-                float v[32];
-                tmem_ld32(lanes + L::CB + 32 * cq, v);
-                const Decay s = d.s[row];
-                if (cq < q) {
-                    const float u = factor(s, d.s[32 * cq + 31]);
+            const Dec &d = dec(k);
+            const Decay s = d.s[row];
+            float2 v[16];
+            if (cq <= q) {
+                tmem_pairs16(lanes + L::CB + 32 * cq, reinterpret_cast<float2(&)[8]>(v[0]));
+                tmem_pairs16(lanes + L::CB + 32 * cq + 16, reinterpret_cast<float2(&)[8]>(v[8]));
+                const Decay last = d.s[32 * cq + 31];
+                if (cq < q || d.s[32 * cq].hi - last.hi <= kBlockRange) {
+                    // 2^(s_t - s_j) as 2^(s_t - s_r) 2^(s_r - s_j), r the last token of the columns
+                    const float2 u = both(factor(s, last));
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(d.v + 32 * cq + i);
-                        pk[i / 2] = __uint_as_float(pack_bf16(v[i] * (u * f.x), v[i + 1] * (u * f.y)));
-                        pk[i / 2 + 1] = __uint_as_float(pack_bf16(v[i + 2] * (u * f.z), v[i + 3] * (u * f.w)));
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = *reinterpret_cast<const float4 *>(d.v + 32 * cq + 4 * i);
+                        v[2 * i] = mul2(v[2 * i], mul2(u, make_float2(f.x, f.y)));
+                        v[2 * i + 1] = mul2(v[2 * i + 1], mul2(u, make_float2(f.z, f.w)));
                     }
                 } else {
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float f = v[i] * (factor(s, d.s[32 * cq + i]) * d.dt[32 * cq + i]);
-                        v[i] = i <= lane ? f : 0.f;
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 sj = *reinterpret_cast<const float4 *>(d.s + 32 * cq + 2 * i);
+                        const float2 dt = *reinterpret_cast<const float2 *>(d.dt + 32 * cq + 2 * i);
+                        v[i] = mul2(v[i], mul2(make_float2(factor(s, {sj.x, sj.y}), factor(s, {sj.z, sj.w})), dt));
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16(v[2 * i], v[2 * i + 1]));
                 }
             }
+            // (behind the diagonal a factor may be anything)
+            const uint32_t bits = cq < q ? 0xffffffffu : cq > q ? 0u : low_bits(lane + 1);
+            float pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = __uint_as_float(pack_bf16(bits & (1u << (2 * i)) ? v[i].x : 0.f, bits & (2u << (2 * i)) ? v[i].y : 0.f));
             tmem_st16(lanes + L::M + 16 * cq, pk);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ws.bar(L::B_M));
+        } else {
+            if (k + 1 < z.K && !(ok = scale(k + 1))) break;
         }
         // the state behind the chunk
-        ok = ok && ws.wait(L::B_D, ph);
+        if (!(ok = ws.wait(L::B_D + e, L::NW == 2 ? ring_phase<2>(k) : ph))) break;
         tc_fence_after();
-        if (holds && ok) {
-            float v[16];
-            tmem_ld16(lanes + L::D + 16 * cq, v);
-            tmem_wait_ld();
-            const float f = d.end;
+        if (holds) {
+            float2 v[8];
+            load_parts16(lanes + L::D + e * T + c0, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) carry[i] = fmaf(f, carry[i], v[i]);
-        }
-        if constexpr (OUT) {
-            ok = ok && ws.wait(L::B_A2, ph);
-            if (k + 1 < K) put_state();
-            ok = ok && ws.wait(L::B_A1, ph);
-            tc_fence_after();
-            float y[16], z[16], xr[16];
-            tmem_ld16(lanes + L::A1 + 16 * cq, y);
-            tmem_ld16(lanes + L::A2 + 64 * e + 16 * cq, z);
-            unpack8(*reinterpret_cast<const uint4 *>(x + tile_off(T, row, 16 * cq)), xr);
-            unpack8(*reinterpret_cast<const uint4 *>(x + tile_off(T, row, 16 * cq + 8)), xr + 8);
-            tmem_wait_ld();
-            const float to = d.to[row];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = fmaf(skip, xr[i], fmaf(to, z[i], y[i]));
-            const int t0 = c * T;
-            if (threadIdx.x == 0) bulk_wait_read();
-            elem_sync();
-            tile_store_row16(base + L::OFF_Y, T, row, 16 * cq, y);
-            fence_async_smem();
-            elem_sync();
-            if (ok && w.len - t0 >= T) {
-                if (threadIdx.x == 0) {
-                    tma_store_4d(base + L::OFF_Y, &p.my, 64 * w.pt, t0, a.y.sh ? w.h : 0, a.y.sb ? w.b : 0);
-                    bulk_commit();
-                }
-            } else if (ok) {  // rows behind the sequence stay as they are
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.y.p) + (size_t)w.b * a.y.sb + (size_t)w.h * a.y.sh;
-                for (int i = threadIdx.x; i < T * 8; i += kElemWarps * 32) {
-                    const int r = i >> 3, cc = 64 * w.pt + 8 * (i & 7);
-                    if (t0 + r < w.len && cc < a.P)
-                        *reinterpret_cast<uint4 *>(out + (size_t)(t0 + r) * a.y.st + cc) =
-                            *reinterpret_cast<const uint4 *>(base + L::OFF_Y + tile_off(T, r, 8 * (i & 7)));
-                }
-            }
-            tc_fence_before();
+            for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], v[i]);
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(ws.bar(L::B_XE + e));
-            mbar_arrive(ws.bar(L::B_DE + e));
+        if constexpr (OUT) {
+            if (!(ok = ws.wait(L::B_A2, ph))) break;
+            if (k + 1 < z.K) ok = put_state(k + 1) && scale(k + 1);
+            // y = M x + 2^s C h + D x, over x: its weighted rows and M x are done
+            if (!ok || !(ok = ws.wait(L::B_A1, ph))) break;
+            tc_fence_after();
+            const float to = dec(k).to[row];
+            uint8_t *x = base + L::OFF_X + k % L::NX * kHalf;
+            float2 y[8], c[8], f[8];
+            tmem_pairs16(lanes + L::A1 + c0, y);
+            tmem_pairs16(lanes + L::A2 + 64 * (k & 1) + c0, c);
+            unpack8(*reinterpret_cast<const uint4 *>(x + tile_off(T, row, c0)), f);
+            unpack8(*reinterpret_cast<const uint4 *>(x + tile_off(T, row, c0 + 8)), f + 4);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fma2(both(skip), f[i], fma2(both(to), c[i], y[i]));
+            store_row8(x, T, row, c0, y);
+            store_row8(x, T, row, c0 + 8, y + 4);
+            tc_fence_before();
+            show(L::B_Y + k % L::NX, -1);
+        } else if (k + 1 < z.K) {
+            ok = put_state(k + 1);
         }
     }
-    const int last = dir ? 0 : max(w.used - 1, 0);
-    float *fin = dir ? a.d_state_in : a.state_out;
-    if (ok && fin && w.piece == last && holds) store_state16(a, fin + ((size_t)w.b * a.H + w.h) * a.N * a.P, row, col, carry);
-    if (threadIdx.x == 0) bulk_wait_all();
+    const int last = z.dir ? 0 : max(w.used - 1, 0);
+    float *fin = z.dir ? a.d_state_in : a.state_out;
+    if (ok && fin && w.piece == last && holds) store_state(a, fin + ((size_t)w.b * a.H + w.h) * a.N * a.P, row, col, carry);
 }
 
+// In the order in which the elementwise warps ask for them: M x of chunk k and C B^T of k + 1, 2^s C h
+// of k + 1, the state's sums over k + 1.
 template <int NB, bool OUT>
-__device__ __forceinline__ void carry_mma(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, int K) {
+__device__ __forceinline__ void carry_mma(const Waits &ws, uint8_t *base, uint32_t tb, int K) {
     using L = LayCarry<NB, OUT>;
-    const uint32_t id_d = make_idesc(T, 64, true, true), id_cb = make_idesc(T, T, false, false), id_y = make_idesc(T, 64, false, true);
-    const uint64_t W = mnmajor(base + L::OFF_W), H = make_sdesc(smem_u32(base + L::OFF_H), 64 * NB * 128u, 1024u);
-    constexpr int EACH = OUT ? 2 : 1;  // ring tiles of a chunk
-    auto slot = [](int i) { return i % L::NR; };
-    auto full = [&](int i) { return ws.wait(L::B_R + slot(i), (uint32_t)(i / L::NR) & 1u); };
-    auto tile = [&](int i) { return base + L::OFF_R + slot(i) * NB * kHalf; };
+    constexpr uint32_t id_y = make_idesc(T, 64, false, true), id_cb = make_idesc(T, T, false, false);
+    const uint64_t H = make_sdesc(smem_u32(base + L::OFF_H), 64 * NB * 128u, 1024u);
+    auto full = [&](int i) { return ws.wait(L::B_R + i % L::NR, ring_phase<L::NR>(i)); };
+    auto tile = [&](int i) { return base + L::OFF_R + (i % L::NR) * NB * kHalf; };
     auto do_cb = [&](int k) {
         if (!full(2 * k) || !full(2 * k + 1)) return false;
-        const uint64_t b = kmajor(tile(2 * k)), c = kmajor(tile(2 * k + 1));
+        const uint64_t c = kmajor(tile(2 * k)), b = kmajor(tile(2 * k + 1));
         mma_ss64(tb + L::CB, c, b, id_cb, false);
         if (NB > 1) mma_ss64(tb + L::CB, c + kBlock, b + kBlock, id_cb, true);
         umma_commit_warp(ws.bar(L::B_CB));
         return true;
     };
     bool ok = !OUT || K == 0 || do_cb(0);
+#pragma unroll 1
     for (int k = 0; k < K && ok; ++k) {
-        const int e = k & 1;
-        const uint32_t ph = (uint32_t)k & 1u;
         if constexpr (OUT) {
-            if (!(ok = ws.wait(L::B_H, ph))) break;
+            if (!(ok = ws.wait(L::B_H, (uint32_t)k & 1u))) break;
             tc_fence_after();
-            const uint64_t c = kmajor(tile(2 * k + 1));
-            mma_km64(tb + L::A2 + 64 * e, c, H, id_y, false);
-            if (NB > 1) mma_km64(tb + L::A2 + 64 * e, c + kBlock, H + kRows64, id_y, true);
+            const uint64_t c = kmajor(tile(2 * k));
+            const uint32_t A2 = tb + L::A2 + 64 * (k & 1);
+            mma_km64(A2, c, H, id_y, false);
+            if (NB > 1) mma_km64(A2, c + kBlock, H + kRows64, id_y, true);
             umma_commit_warp(ws.bar(L::B_A2));
-            umma_commit_warp(ws.bar(L::B_RE + slot(2 * k + 1)));
+            umma_commit_warp(ws.bar(L::B_RE + 2 * k % L::NR));
         }
-        if (!(ok = full(EACH * k) && ws.wait(L::B_W, ph))) break;
+        const int r = L::EACH * k + L::EACH - 1, e = L::NW == 2 ? k & 1 : 0;
+        if (!(ok = full(r) && ws.wait(L::B_W + e, L::NW == 2 ? ring_phase<2>(k) : (uint32_t)k & 1u))) break;
         tc_fence_after();
-        const uint64_t b = mnmajor(tile(EACH * k));
-        mma_mm64(tb + L::D, b, W, id_d, false);
-        mma_mm64(tb + L::D, b + kRows64, W + kRows64, id_d, true);
-        mma_mm64(tb + L::D, b, W + kBlock, id_d, true);
-        mma_mm64(tb + L::D, b + kRows64, W + kBlock + kRows64, id_d, true);
-        umma_commit_warp(ws.bar(L::B_D));
-        umma_commit_warp(ws.bar(L::B_RE + slot(EACH * k)));
+        mma_state(tb + L::D + e * T, mnmajor(tile(r)), mnmajor(base + L::OFF_W + e * 2 * kHalf), false);
+        umma_commit_warp(ws.bar(L::B_D + e));
+        umma_commit_warp(ws.bar(L::B_RE + r % L::NR));
         if constexpr (OUT) {
-            if (!(ok = ws.wait(L::B_X + e, (uint32_t)(k >> 1) & 1u) && ws.wait(L::B_M, ph))) break;
+            if (!(ok = ws.wait(L::B_X + k % L::NX, ring_phase<L::NX>(k)) && ws.wait(L::B_M, (uint32_t)k & 1u))) break;
             tc_fence_after();
-            mma_ts128(tb + L::A1, tb + L::M, mnmajor(base + L::OFF_X + e * kHalf), id_y);
+            mma_ts128(tb + L::A1, tb + L::M, mnmajor(base + L::OFF_X + k % L::NX * kHalf), id_y);
             umma_commit_warp(ws.bar(L::B_A1));
-            umma_commit_warp(ws.bar(L::B_XE + e));
             if (k + 1 < K) ok = do_cb(k + 1);
         }
     }
@@ -422,91 +453,166 @@ __device__ __forceinline__ void carry_mma(const Params &p, const Waits &ws, uint
 }
 
 template <int NB, bool OUT>
-__device__ __forceinline__ void carry_tma(const Params &p, const Waits &ws, uint8_t *base, const Piece &w, int dir, int K) {
+__device__ __forceinline__ void carry_load(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
     using L = LayCarry<NB, OUT>;
     const Args &a = p.a;
-    const int lane = threadIdx.x & 31;
-    constexpr int EACH = OUT ? 2 : 1;
+    const Piece &w = z.w;
+    const int lane = threadIdx.x & 31, tiles = L::EACH * z.K;
     uint32_t raw = 0;
-    int k = 0, issued = 0;  // ring tiles
+    int r = 0;
     bool ok = true;
-    for (; k < K; ++k) {
-        const int e = k & 1, t0 = (dir ? w.hi - 1 - k : w.lo + k) * T;
-        const bool clean = w.len - t0 < T;
-        if (k >= 2 && !ws.wait(L::B_XE + e, (uint32_t)((k >> 1) & 1) ^ 1u)) break;
-        uint8_t *x = base + L::OFF_X + e * kHalf;
-        auto load = [&](uint8_t *dst, int bar, bool clear, uint32_t bytes, auto issue) {
-            const int full = clear ? L::B_RAW : bar;
-            if (lane == 0) {
-                mbar_expect_tx(ws.bar(full), bytes);
-                issue(full);
-            }
-            __syncwarp();
-            if (!clear) return true;
-            if (!ws.wait(L::B_RAW, raw)) return false;
-            raw ^= 1u;
-            if (bytes == kHalf)
-                clear_rows<1>(dst, w.len - t0);
-            else
-                clear_rows<NB>(dst, w.len - t0);
-            if (lane == 0) mbar_arrive(ws.bar(bar));
-            return true;
-        };
-        if (!(ok = load(x, L::B_X + e, clean, kHalf, [&](int f) { load_tile<1>(x, &p.mx[dir], p.vx[dir], ws.bar(f), 64 * w.pt, t0, w.h, w.b); }))) {
-            ++k;
-            break;
+#pragma unroll 1
+    for (; r < tiles && ok; ++r) {
+        const int s = r % L::NR, t0 = z.chunk(r / L::EACH) * T;
+        const bool is_c = OUT && r % 2 == 0, clear = w.len - t0 < T && !is_c;  // rows of C reach their own tokens only
+        if (r >= L::NR && !(ok = ws.wait(L::B_RE + s, ring_phase<L::NR>(r) ^ 1u))) break;
+        uint8_t *t = base + L::OFF_R + s * NB * kHalf;
+        if (lane == 0) {
+            uint64_t *bar = ws.bar(clear ? L::B_RAW : L::B_R + s);
+            mbar_expect_tx(bar, NB * kHalf);
+            load_tile<NB>(t, is_c ? &p.mc : &p.mb[z.dir], is_c ? a.c : p.vb[z.dir], bar, 0, t0, w.h / a.R, w.b);
         }
-        for (int i = 0; i < EACH && ok; ++i) {
-            const int s = issued % L::NR;
-            if (issued >= L::NR && !(ok = ws.wait(L::B_RE + s, (uint32_t)((issued / L::NR) & 1) ^ 1u))) break;
-            uint8_t *r = base + L::OFF_R + s * NB * kHalf;
-            ++issued;
-            ok = load(r, L::B_R + s, clean && i == 0, NB * kHalf, [&](int f) {
-                load_tile<NB>(r, i ? &p.mc : &p.mb[dir], i ? a.c : p.vb[dir], ws.bar(f), 0, t0, w.h / a.R, w.b);
-            });
-        }
-        if (!ok) {
-            ++k;
-            break;
-        }
+        __syncwarp();
+        if (clear) ok = clear_landed(ws, L::B_RAW, raw, L::B_R + s, t, NB, w.len - t0);
     }
     // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
-    if (ok) {
-        for (int i = max(0, k - 2); i < k; ++i) mbar_wait(ws.bar(L::B_X + (i & 1)), (uint32_t)(i >> 1) & 1u, a.err);
-        for (int i = max(0, issued - L::NR); i < issued; ++i) mbar_wait(ws.bar(L::B_R + i % L::NR), (uint32_t)(i / L::NR) & 1u, a.err);
-    }
+    if (ok)
+        for (int i = max(0, r - L::NR); i < r; ++i) mbar_wait(ws.bar(L::B_R + i % L::NR), ring_phase<L::NR>(i), a.err);
     __syncwarp();
 }
 
 template <int NB, bool OUT>
-__global__ void __launch_bounds__(kThreads, 1) ssm_carry_kernel(const __grid_constant__ Params p) {
+__device__ __forceinline__ void carry_load_x(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
+    using L = LayCarry<NB, OUT>;
+    const Args &a = p.a;
+    const Piece &w = z.w;
+    const int lane = threadIdx.x & 31;
+    uint32_t raw = 0;
+    int k = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (; k < z.K && ok; ++k) {
+        const int s = k % L::NX, c = z.chunk(k), t0 = c * T;
+        const bool clear = w.len - t0 < T;
+        if (k >= L::NX && !(ok = ws.wait(L::B_XE + s, ring_phase<L::NX>(k) ^ 1u))) break;
+        uint8_t *x = base + L::OFF_X + s * kHalf;
+        if (lane == 0) {
+            uint64_t *bar = ws.bar(clear ? L::B_RAWX : L::B_X + s);
+            mbar_expect_tx(bar, kHalf + kDecBytes);
+            bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, w.h, c), kDecBytes, bar);
+            load_tile<1>(x, &p.mx[z.dir], p.vx[z.dir], bar, 64 * w.pt, t0, w.h, w.b);
+        }
+        __syncwarp();
+        if (clear) ok = clear_landed(ws, L::B_RAWX, raw, L::B_X + s, x, 1, w.len - t0);
+    }
+    if (ok)
+        for (int i = max(0, k - L::NX); i < k; ++i) mbar_wait(ws.bar(L::B_X + i % L::NX), ring_phase<L::NX>(i), a.err);
+    __syncwarp();
+}
+
+template <int NB, bool OUT>
+__device__ __forceinline__ void carry_store(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
+    using L = LayCarry<NB, OUT>;
+    const Args &a = p.a;
+    const Piece &w = z.w;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int k = 0; k < z.K; ++k) {
+        const int s = k % L::NX, c = z.chunk(k), t0 = c * T;
+        if (!ws.wait(L::B_Y + s, ring_phase<L::NX>(k))) break;
+        if constexpr (OUT) {
+            const uint8_t *y = base + L::OFF_X + s * kHalf;
+            if (w.len - t0 >= T) {
+                if (lane == 0) {
+                    tma_store_4d(y, &p.my, 64 * w.pt, t0, a.y.sh ? w.h : 0, a.y.sb ? w.b : 0);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+            } else {  // rows behind the sequence stay as they are
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.y.p) + (size_t)w.b * a.y.sb + (size_t)w.h * a.y.sh;
+                for (int i = lane; i < (w.len - t0) * 8; i += 32) {
+                    const int r = i >> 3, cc = 64 * w.pt + 8 * (i & 7);
+                    if (cc < a.P)
+                        *reinterpret_cast<uint4 *>(out + (size_t)(t0 + r) * a.y.st + cc) =
+                            *reinterpret_cast<const uint4 *>(y + tile_off(T, r, 8 * (i & 7)));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ws.bar(L::B_XE + s));
+        } else {
+            if (lane == 0) {
+                const size_t at = (((size_t)w.b * a.H + w.h) * p.plan.PT + w.pt) * a.nc + c;
+                bulk_store(p.image[z.dir] + at * 2 * L::HB, base + L::OFF_H, 2 * L::HB);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(ws.bar(L::B_YE));
+            }
+            __syncwarp();
+        }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+}
+
+template <int NB, bool OUT>
+__global__ void __launch_bounds__(kCarryThreads, 1) ssm_carry_kernel(const __grid_constant__ Params p) {
     using L = LayCarry<NB, OUT>;
     extern __shared__ __align__(1024) uint8_t base[];
-    const Args &a = p.a;
-    const int dir = OUT ? 0 : blockIdx.y;
-    const Piece w = piece_of(a, p.plan, blockIdx.x);
-    if (w.piece >= max(w.used, 1)) return;
-    const int K = w.hi - w.lo;
-    Cta<L::NBAR> cta(base, L::OFF_BAR, a.err, [](int i) {
-        return (i >= L::B_DE && i <= L::B_W) || i == L::B_M || i == L::B_H ? kElemWarps
-               : i == L::B_XE || i == L::B_XE + 1                           ? kElemWarps + (OUT ? 1 : 0)
-                                                                            : 1;
-    });
-    if (cta.warp == kWarpDec) {
-        Dec *dec = reinterpret_cast<Dec *>(base + L::OFF_DEC);
-        for (int k = 0; k < K; ++k) {
-            if (k >= 2 && !cta.ws.wait(L::B_DE + (k & 1), (uint32_t)((k >> 1) & 1) ^ 1u)) break;
-            fill_dec(a, dec[k & 1], w.b, w.h, (dir ? w.hi - 1 - k : w.lo + k) * T, w.len, dir == 1, {0.f, 0.f});
-            if ((threadIdx.x & 31) == 0) mbar_arrive(cta.ws.bar(L::B_DF + (k & 1)));
-        }
-    } else if (cta.warp == kWarpTma) {
-        carry_tma<NB, OUT>(p, cta.ws, base, w, dir, K);
-    } else if (cta.warp == kWarpMma) {
-        carry_mma<NB, OUT>(p, cta.ws, base, uniform(cta.tb), K);
-    } else {
-        carry_elem<NB, OUT>(p, cta.ws, base, cta.tb, w, dir, K);
-    }
+    Walk z;
+    z.dir = OUT ? 0 : blockIdx.y;
+    z.w = piece_of(p.a, p.plan, blockIdx.x, 1);
+    if (z.w.piece >= max(z.w.used, 1)) return;
+    z.K = z.w.hi - z.w.lo;
+    Cta<L::NBAR> cta(base, L::OFF_BAR, p.a.err, [](int i) { return L::arrivals(i); });
+    if (cta.warp < kElemWarps)
+        carry_elem<NB, OUT>(p, cta.ws, base, cta.tb, z);
+    else if (cta.warp == kWarpMma)
+        carry_mma<NB, OUT>(cta.ws, base, uniform(cta.tb), (int)uniform(z.K));
+    else if (cta.warp == kWarpTma)
+        carry_load<NB, OUT>(p, cta.ws, base, z);
+    else if (cta.warp == kWarpTmaX)
+        carry_load_x<NB, OUT>(p, cta.ws, base, z);
+    else
+        carry_store<NB, OUT>(p, cta.ws, base, z);
     cta.finish();
+}
+
+// Heads that share a CTA in the sums of pieces: as many as leave CTAs for the device.
+inline int heads_together(const Args &a, const Plan &plan, int dirs) {
+    const long long ctas = (long long)a.B * a.H * plan.PT * plan.pieces * dirs;
+    return a.R % 4 == 0 && ctas / 4 >= kSms * 3 / 4 ? 4 : a.R % 2 == 0 && ctas / 2 >= kSms * 3 / 4 ? 2 : 1;
+}
+template <int NB, int HB>
+cudaError_t launch_sums(const Params &p, int dirs, cudaStream_t st) {
+    using S = LaySum<NB>;
+    static_assert(S::SMEM <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(ssm_sum_kernel<NB, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    const Args &a = p.a;
+    ssm_sum_kernel<NB, HB><<<dim3((unsigned)((size_t)a.B * (a.H / HB) * p.plan.PT * p.plan.pieces), dirs), kSumThreads, S::SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+// The weights of all chunks, then the states that pieces start from (dirs 2: and their gradients).
+template <int NB>
+cudaError_t starts(const Params &p, int dirs, cudaStream_t st) {
+    const Args &a = p.a;
+    cudaError_t e = weights(a, const_cast<Dec *>(p.dec), st);
+    if (e != cudaSuccess || p.plan.pieces == 1) return e;
+    const int hb = heads_together(a, p.plan, dirs);
+    e = hb == 4 ? launch_sums<NB, 4>(p, dirs, st) : hb == 2 ? launch_sums<NB, 2>(p, dirs, st) : launch_sums<NB, 1>(p, dirs, st);
+    if (e != cudaSuccess) return e;
+    ssm_piece_scan_kernel<<<dim3((unsigned)((size_t)a.B * a.H * ((a.N * a.P + 255) / 256)), dirs), 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+template <int NB, bool OUT>
+cudaError_t walk(const Params &p, cudaStream_t st) {
+    using C = LayCarry<NB, OUT>;
+    static_assert(C::SMEM <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(ssm_carry_kernel<NB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const Args &a = p.a;
+    ssm_carry_kernel<NB, OUT><<<dim3((unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces), OUT ? 1 : 2), kCarryThreads, C::SMEM, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace tcs

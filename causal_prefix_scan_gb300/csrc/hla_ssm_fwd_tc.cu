@@ -11,26 +11,9 @@ namespace {
 using namespace tcs;
 
 template <int NB>
-cudaError_t launch(Params &p, cudaStream_t st) {
-    const Args &a = p.a;
-    using S = LaySum<NB>;
-    using C = LayCarry<NB, true>;
-    static_assert(S::SMEM <= 227 * 1024 && C::SMEM <= 227 * 1024, "shared memory");
-    if (!encode(&p.mx[0], a.x, a.P, a.n, a.H, a.B, T) || !encode(&p.mb[0], a.b, a.N, a.n, a.G, a.B, T) ||
-        !encode(&p.mc, a.c, a.N, a.n, a.G, a.B, T) || !encode(&p.my, a.y, a.P, a.n, a.H, a.B, T))
-        return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(ssm_sum_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_carry_kernel<NB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    const unsigned ctas = (unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces);
-    if (p.plan.pieces > 1) {
-        ssm_sum_kernel<NB><<<ctas, kThreads, S::SMEM, st>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        ssm_piece_scan_kernel<<<(unsigned)((size_t)a.B * a.H * ((a.N * a.P + 255) / 256)), 256, 0, st>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    ssm_carry_kernel<NB, true><<<ctas, kThreads, C::SMEM, st>>>(p);
-    return cudaGetLastError();
+cudaError_t launch(const Params &p, cudaStream_t st) {
+    const cudaError_t e = starts<NB>(p, 1, st);
+    return e == cudaSuccess ? walk<NB, true>(p, st) : e;
 }
 
 }  // namespace
@@ -49,10 +32,11 @@ size_t tc_space(Args &a, bool backward, uint8_t *base) {
         at += align256(floats * 4);
         return p;
     };
+    a.dec = take((size_t)a.B * a.H * a.nc * (sizeof(Dec) / 4));
     const size_t units = plan.pieces > 1 ? (size_t)a.B * a.H * plan.pieces : 0;
     a.h = take(units * a.N * a.P);
     a.factor = take(units);
-    return at + 256;
+    return at;
 }
 
 cudaError_t tc_forward(const Args &a, cudaStream_t st) {
@@ -64,8 +48,12 @@ cudaError_t tc_forward(const Args &a, cudaStream_t st) {
     p.vb[0] = a.b;
     p.pieces[0] = a.h;
     p.factor = a.factor;
-    cudaError_t e = dev_status_ptr(&p.a.err);
+    p.dec = static_cast<const Dec *>(a.dec);
+    const cudaError_t e = dev_status_ptr(&p.a.err);
     if (e != cudaSuccess) return e;
+    if (!encode(&p.mx[0], a.x, a.P, a.n, a.H, a.B, T) || !encode(&p.mb[0], a.b, a.N, a.n, a.G, a.B, T) ||
+        !encode(&p.mc, a.c, a.N, a.n, a.G, a.B, T) || !encode(&p.my, a.y, a.P, a.n, a.H, a.B, T))
+        return cudaErrorNotSupported;
     return a.N <= 64 ? launch<1>(p, st) : launch<2>(p, st);
 }
 

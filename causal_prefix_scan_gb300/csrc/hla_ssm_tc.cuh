@@ -1,6 +1,8 @@
 // hla_ssm_tc.cuh -- what the tensor-core kernels of the selective state space scan share (bf16,
 // chunks of 128 tokens, 64 columns of a head at a time; formulas in hla_ssm.h).
 #pragma once
+#include <cstddef>
+
 #include "hla_ssm.h"
 #include "hla_window_tc.cuh"
 
@@ -10,20 +12,19 @@ namespace tcs {
 
 using win::tcw::encode;
 using win::tcw::kmajor;
+using win::tcw::low_bits;
 using win::tcw::mappable;
 using win::tcw::mbar_arrive;
 using win::tcw::mma_ss64;
 using win::tcw::mma_ts32;
 using win::tcw::mnmajor;
 using win::tcw::tma_load_4d;
-using win::tcw::tmem_ld32;
 using win::tcw::uniform;
-using win::tcw::Waits;
 
 constexpr int kSms = 152;            // pieces are cut for these (results then do not depend on the device)
 constexpr int T = 128;               // tokens of a chunk
 constexpr int kHalf = T * 128;       // bytes of 128 rows of 64 bf16 columns
-constexpr int kElemWarps = 16, kWarpMma = 16, kWarpTma = 17, kWarpDec = 18, kThreads = 19 * 32;
+constexpr int kElemWarps = 16, kWarpMma = 16, kWarpTma = 17, kWarpTmaX = 18, kWarpStore = 19;
 
 // D [128 x N] (+)= A B over 64 rows of both (MN-major tiles).
 HLA_DEVICE void mma_mm64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -62,6 +63,12 @@ HLA_DEVICE void mma_ts128(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
 }
 constexpr uint32_t kBlock = kHalf >> 4, kRows64 = 64 * 128 >> 4;  // descriptor steps: 64 columns, 64 rows
 
+HLA_DEVICE void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
+                 "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
 HLA_DEVICE void tma_store_4d(const void *src, const void *tmap, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(tmap),
                  "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
@@ -75,7 +82,29 @@ HLA_DEVICE void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-HLA_DEVICE void elem_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kElemWarps * 32) : "memory"); }
+// Bounded, warp-uniform waits as win::tcw::Waits, what follows a first poll out of line: these
+// kernels' roles go through long code once per chunk, and what does not fit the instruction cache
+// stalls every warp (101 KB of it: 4,500 to 7,000 cycles a chunk).
+static __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_p, unsigned *err) {
+    for (int polls = 0; !*abort_p; ++polls) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (polls == 2000) {
+            atomicOr(err, DEV_TIMEOUT);
+            *abort_p = 1;
+        }
+        __syncwarp();
+    }
+    return false;
+}
+struct Waits {
+    uint64_t *bars;
+    volatile int *abort_p;
+    unsigned *err;
+    HLA_DEVICE uint64_t *bar(int i) const { return bars + i; }
+    HLA_DEVICE bool wait(int b, uint32_t parity) const {
+        return __all_sync(0xffffffffu, mbar_try_wait(bars + b, parity)) || wait_on(bars + b, parity, abort_p, err);
+    }
+};
 
 // BLOCKS x 64 columns from column c0 on, rows t0 .. t0 + 127 of head h.
 template <int BLOCKS>
@@ -85,62 +114,136 @@ HLA_DEVICE void load_tile(uint8_t *dst, const CUtensorMap *m, const View &v, uin
 }
 // Zeroes rows [r0, T) of a tile (one warp): rows behind a sequence may be anything, and 0 times
 // that is not 0 where they are contracted over.
-template <int BLOCKS>
-HLA_DEVICE void clear_rows(uint8_t *tile, int r0) {
-#pragma unroll
-    for (int c = 0; c < BLOCKS; ++c)
+HLA_DEVICE void clear_rows(uint8_t *tile, int blocks, int r0) {
+#pragma unroll 1
+    for (int c = 0; c < blocks; ++c)
+#pragma unroll 1
         for (int e = (r0 << 3) + (int)(threadIdx.x & 31); e < T * 8; e += 32)
             reinterpret_cast<uint4 *>(tile + c * kHalf)[e] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
 }
-HLA_DEVICE void unpack8(const uint4 u, float *v) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+// Pairs of fp32: one instruction for two lanes' worth of arithmetic.
+HLA_DEVICE float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+HLA_DEVICE float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+HLA_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+HLA_DEVICE float2 both(float x) { return make_float2(x, x); }
+HLA_DEVICE uint32_t pack2(float2 v) { return pack_bf16(v.x, v.y); }
+HLA_DEVICE float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+HLA_DEVICE void unpack8(const uint4 u, float2 *v) {
+    v[0] = unpack2(u.x); v[1] = unpack2(u.y); v[2] = unpack2(u.z); v[3] = unpack2(u.w);
 }
 // v as two bf16 parts: hi + lo is v within 2^-17.
-HLA_DEVICE void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+HLA_DEVICE void split2(float2 v, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(v);
+    const float2 h = unpack2(hi ^ 0x80008000u);  // its negative
+    lo = pack2(add2(v, h));
 }
-// 16 columns (c0 a multiple of 16) of row r of a 64-column tile, in two parts.
-HLA_DEVICE void store_split16(uint8_t *hi, uint8_t *lo, int r, int c0, const float (&v)[16]) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        uint4 h, l;
-        split2(v[8 * g], v[8 * g + 1], h.x, l.x);
-        split2(v[8 * g + 2], v[8 * g + 3], h.y, l.y);
-        split2(v[8 * g + 4], v[8 * g + 5], h.z, l.z);
-        split2(v[8 * g + 6], v[8 * g + 7], h.w, l.w);
-        const uint32_t off = tile_off(T, r, c0 + 8 * g);
-        *reinterpret_cast<uint4 *>(hi + off) = h;
-        *reinterpret_cast<uint4 *>(lo + off) = l;
-    }
+// 8 columns (c0 a multiple of 8) of row r of a 64-column tile with `rows` rows, in two parts.
+HLA_DEVICE void store_split8(uint8_t *hi, uint8_t *lo, int rows, int r, int c0, const float2 *v) {
+    uint4 h, l;
+    split2(v[0], h.x, l.x);
+    split2(v[1], h.y, l.y);
+    split2(v[2], h.z, l.z);
+    split2(v[3], h.w, l.w);
+    const uint32_t off = tile_off(rows, r, c0);
+    *reinterpret_cast<uint4 *>(hi + off) = h;
+    *reinterpret_cast<uint4 *>(lo + off) = l;
 }
-// The same row of a bf16 tile times f, in two parts.
+HLA_DEVICE void store_row8(uint8_t *tile, int rows, int r, int c0, const float2 *v) {
+    *reinterpret_cast<uint4 *>(tile + tile_off(rows, r, c0)) = make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
+}
+// 16 columns of row r of a bf16 tile times f, in two parts.
 HLA_DEVICE void scale_split16(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int r, int c0, float f) {
-    float v[16];
-    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0)), v);
-    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0 + 8)), v + 8);
+    const uint4 u0 = *reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0));
+    const uint4 u1 = *reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0 + 8));
+    float2 v[8];
+    unpack8(u0, v);
+    unpack8(u1, v + 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= f;
-    store_split16(hi, lo, r, c0, v);
+    for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(f));
+    store_split8(hi, lo, T, r, c0, v);
+    store_split8(hi, lo, T, r, c0 + 8, v + 4);
 }
+// 16 columns of an accumulator in TMEM, as pairs.
+HLA_DEVICE void tmem_pairs16(uint32_t taddr, float2 (&v)[8]) { tmem_ld16(taddr, reinterpret_cast<float(&)[16]>(v)); }
 
-// What a chunk's tokens weigh, in shared memory.
+// What a chunk's tokens weigh, [B][H][chunks] in the workspace: formed once by weights_kernel (a
+// warp's chain of loads, softplus and scan takes longer than the rest of a chunk's work: with a
+// warp of each CTA for it, n16384 h64 p64 s128 took 457 us), copied by the TMA unit.
 struct Dec {
     Decay s[T];
     float dt[T];
     float to[T];     // 2^s_t: from the chunk's start
-    float w[T];      // weight of the token's row in the state: dt 2^(s_end - s), or 2^s backward
+    float w[T];      // dt 2^(s_end - s): the token's weight in the state
     float v[T];      // dt 2^(s_r - s), r the last token of its block of 32: M = CB v 2^(s_t - s_r) behind the block
     float end;       // 2^s_end
     float pad[3];
+    float slope[T];  // of dt over its raw value; for the gradients only
 };
+constexpr int kDecBytes = offsetof(Dec, slope);  // what the walks take
+HLA_DEVICE const Dec *dec_of(const Args &a, const Dec *dec, int b, int h, int c) { return dec + ((size_t)b * a.H + h) * a.nc + c; }
+
+// One CTA for 32 heads of a chunk: their steps through shared memory, whichever of heads and tokens
+// lie side by side; then a warp for each head, four adjacent tokens a lane.
+static __global__ void __launch_bounds__(256) ssm_weights_kernel(const Args a, Dec *dec) {
+    __shared__ float raw[T][33];
+    const int groups = (a.H + 31) / 32, h0 = blockIdx.x % groups * 32, c = blockIdx.x / groups % a.nc, b = blockIdx.x / groups / a.nc;
+    const int len = clamp_length(a.lengths, b, a.n), t0 = c * T, heads = min(32, a.H - h0), live = min(T, len - t0);
+    if (live <= 0) return;
+    const bool by_head = a.dt.sh < a.dt.st;
+    for (int e = threadIdx.x; e < T * 32; e += 256) {
+        const int t = by_head ? e >> 5 : e & (T - 1), h = by_head ? e & 31 : e >> 7;
+        if (t < live && h < heads) raw[t][h] = raw_step<__nv_bfloat16>(a, b, h0 + h, t0 + t);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < heads; i += 8) {
+        const int h = h0 + i;
+        const float bias = a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f;
+        float d[4], sl[4];
+        Decay s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sl[k] = 0.f;
+            d[k] = 4 * lane + k < live ? step_from(a, raw[4 * lane + k][i], bias, sl[k]) : 0.f;
+        }
+        scan_decays(d, a.A[h] * kLog2e, s);
+        Dec *o = dec + ((size_t)b * a.H + h) * a.nc + c;
+        auto from = [&](int l) { return Decay{__shfl_sync(0xffffffffu, s[3].hi, l), __shfl_sync(0xffffffffu, s[3].lo, l)}; };
+        const Decay end = from(31), block = from(lane | 7);
+        float4 *q = reinterpret_cast<float4 *>(o->s + 4 * lane);
+        q[0] = make_float4(s[0].hi, s[0].lo, s[1].hi, s[1].lo);
+        q[1] = make_float4(s[2].hi, s[2].lo, s[3].hi, s[3].lo);
+        auto put = [&](float *p, auto f) { *reinterpret_cast<float4 *>(p + 4 * lane) = make_float4(f(0), f(1), f(2), f(3)); };
+        put(o->dt, [&](int k) { return d[k]; });
+        put(o->to, [&](int k) { return factor(s[k]); });
+        put(o->w, [&](int k) { return d[k] * factor(end, s[k]); });
+        put(o->v, [&](int k) { return d[k] * factor(block, s[k]); });
+        put(o->slope, [&](int k) { return sl[k]; });
+        if (lane == 0) o->end = factor(end);
+    }
+}
+inline cudaError_t weights(const Args &a, Dec *dec, cudaStream_t st) {
+    ssm_weights_kernel<<<(unsigned)((size_t)a.B * a.nc * ((a.H + 31) / 32)), 256, 0, st>>>(a, dec);
+    return cudaGetLastError();
+}
 
 // Work of one CTA: columns [64 pt, 64 pt + 64) of a head's state over the chunks [lo, hi) of one piece.
 struct Piece {
@@ -149,12 +252,13 @@ struct Piece {
 struct Plan {
     int pieces, per, PT;  // chunks of a piece, column tiles of a head
 };
-HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u) {
+HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u, int heads) {
+    const int sets = a.H / heads;
     Piece r;
     r.pt = u % p.PT;
-    r.h = u / p.PT % a.H;
-    r.piece = u / p.PT / a.H % p.pieces;
-    r.b = u / p.PT / a.H / p.pieces;
+    r.h = u / p.PT % sets * heads;
+    r.piece = u / p.PT / sets % p.pieces;
+    r.b = u / p.PT / sets / p.pieces;
     r.len = clamp_length(a.lengths, r.b, a.n);
     const int chunks = (r.len + T - 1) / T;
     r.used = (chunks + p.per - 1) / p.per;
@@ -219,27 +323,6 @@ struct Cta {
         if (warp == kWarpMma) tmem_dealloc(tb, 512);
     }
 };
-
-// The decay warp: one chunk's weights.  `back`: rows weigh by 2^s (towards the chunk's start);
-// `off`: decay from the chunk's end to the piece's end (or from the piece's start to the chunk's).
-HLA_DEVICE void fill_dec(const Args &a, Dec &d, int b, int h, int t0, int len, bool back, Decay off) {
-    const int lane = threadIdx.x & 31;
-    chunk_decays<__nv_bfloat16, T / 32>(a, b, h, t0, len, d.dt, d.s, nullptr);
-    __syncwarp();
-    const Decay end = d.s[T - 1];
-#pragma unroll
-    for (int i = 0; i < T / 32; ++i) {
-        const int t = lane + 32 * i;
-        const Decay s = d.s[t];
-        const float dt = d.dt[t];
-        d.to[t] = factor(s);
-        d.w[t] = back ? ex2_approx((s.hi + off.hi) + (s.lo + off.lo))
-                      : dt * ex2_approx((end.hi - s.hi + off.hi) + (end.lo - s.lo + off.lo));
-        d.v[t] = dt * factor(d.s[32 * i + 31], s);
-    }
-    if (lane == 0) d.end = factor(end);
-    __syncwarp();
-}
 
 }  // namespace tcs
 
