@@ -263,8 +263,15 @@ hla_status hla_ssm_backward(const hla_ssm_params *p, const hla_tensor *x, const 
     a.dx = view(&g.dx, d.x); a.ddt = view(&g.d_dt, d.dt); a.db = view(&g.db, d.b); a.dc = view(&g.dc, d.b);
     a.state_in = state_in; a.d_state_out = d_state_out;
     a.d_state_in = g.d_state_in; a.dA = g.dA; a.dD = g.dD; a.dbias = g.d_dt_bias;
-    simt_space(a, true, static_cast<uint8_t *>(workspace));
-    const cudaError_t e = simt_backward(a, t, st);
+    cudaError_t e = cudaErrorNotSupported;
+    if (t == HLA_BF16 && tc_takes(a, true)) {
+        tc_space(a, true, static_cast<uint8_t *>(workspace));
+        e = tc_backward(a, st);
+    }
+    if (e == cudaErrorNotSupported) {
+        simt_space(a, true, static_cast<uint8_t *>(workspace));
+        e = simt_backward(a, t, st);
+    }
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 

@@ -20,7 +20,8 @@ cudaError_t launch(const Params &p, cudaStream_t st) {
 
 bool tc_takes(const Args &a, bool backward) {
     const bool in = a.P % 8 == 0 && a.N % 8 == 0 && mappable(a.x) && mappable(a.b) && mappable(a.c);
-    return in && !backward && mappable(a.y);
+    if (!backward) return in && mappable(a.y);
+    return in && mappable(a.dy) && mappable(a.dx) && rows16(a.db, 2) && rows16(a.dc, 2);
 }
 
 size_t tc_space(Args &a, bool backward, uint8_t *base) {
@@ -36,6 +37,15 @@ size_t tc_space(Args &a, bool backward, uint8_t *base) {
     const size_t units = plan.pieces > 1 ? (size_t)a.B * a.H * plan.pieces : 0;
     a.h = take(units * a.N * a.P);
     a.factor = take(units);
+    if (backward) {
+        a.g = take(units * a.N * a.P);
+        const size_t image = (size_t)a.B * a.H * plan.PT * a.nc * (a.N <= 64 ? 1 : 2) * (kHalf / 4);  // two parts of 64 rows each
+        a.image[0] = reinterpret_cast<unsigned char *>(take(image));
+        a.image[1] = reinterpret_cast<unsigned char *>(take(image));
+        a.splits = tc_splits(a);
+        a.dbc = take(a.splits > 1 ? (size_t)a.splits * 2 * a.B * a.G * a.n * a.N : 0);
+        a.sums = take((size_t)a.B * a.nc * 3 * a.H);
+    }
     return at;
 }
 

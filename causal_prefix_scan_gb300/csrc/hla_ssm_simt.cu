@@ -429,15 +429,15 @@ cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st) {
         e = dt == HLA_F32 ? run_backward<float, 64>(a, st) : run_backward<__nv_bfloat16, 64>(a, st);
     else
         e = dt == HLA_F32 ? run_backward<float, 32>(a, st) : run_backward<__nv_bfloat16, 32>(a, st);
-    return e == cudaSuccess ? join(a, dt, st) : e;
+    return e == cudaSuccess ? join(a, dt, true, st) : e;
 }
 
-cudaError_t join(const Args &a, hla_dtype dt, cudaStream_t st) {
+cudaError_t join(const Args &a, hla_dtype dt, bool parts, cudaStream_t st) {
     const size_t blocks = ((size_t)a.B * a.G * a.n + 7) / 8;
     const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096), 2);
-    if (dt == HLA_F32)
+    if (parts && dt == HLA_F32)
         ssm_join_kernel<float><<<grid, 256, 0, st>>>(a);
-    else
+    else if (parts)
         ssm_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -61,6 +61,19 @@ HLA_DEVICE void mma_ts128(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     mma_ts32(d, a + 32, b + 512, idesc, true);
     mma_ts32(d, a + 48, b + 768, idesc, true);
 }
+// D += A B over 64 columns, A packed bf16 in 32 columns of TMEM, B K-major.
+HLA_DEVICE void mma_tk64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred e, t;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n elect.sync _|e, 0xffffffff;\n"
+        " setp.eq.b32 t, 0, 0;\n add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
 constexpr uint32_t kBlock = kHalf >> 4, kRows64 = 64 * 128 >> 4;  // descriptor steps: 64 columns, 64 rows
 
 HLA_DEVICE void tmem_st8(uint32_t taddr, const float (&v)[8]) {
@@ -195,7 +208,9 @@ struct Dec {
     float v[T];      // dt 2^(s_r - s), r the last token of its block of 32: M = CB v 2^(s_t - s_r) behind the block
     float end;       // 2^s_end
     float pad[3];
-    float slope[T];  // of dt over its raw value; for the gradients only
+    // for the gradients only:
+    float slope[T];  // of dt over its raw value
+    float fw[T];     // 2^(s - s_b), b the first token of its block of 32: L = 2^(s_b - s_j) fw in front of the block
 };
 constexpr int kDecBytes = offsetof(Dec, slope);  // what the walks take
 HLA_DEVICE const Dec *dec_of(const Args &a, const Dec *dec, int b, int h, int c) { return dec + ((size_t)b * a.H + h) * a.nc + c; }
@@ -228,6 +243,7 @@ static __global__ void __launch_bounds__(256) ssm_weights_kernel(const Args a, D
         Dec *o = dec + ((size_t)b * a.H + h) * a.nc + c;
         auto from = [&](int l) { return Decay{__shfl_sync(0xffffffffu, s[3].hi, l), __shfl_sync(0xffffffffu, s[3].lo, l)}; };
         const Decay end = from(31), block = from(lane | 7);
+        const Decay first{__shfl_sync(0xffffffffu, s[0].hi, lane & ~7), __shfl_sync(0xffffffffu, s[0].lo, lane & ~7)};
         float4 *q = reinterpret_cast<float4 *>(o->s + 4 * lane);
         q[0] = make_float4(s[0].hi, s[0].lo, s[1].hi, s[1].lo);
         q[1] = make_float4(s[2].hi, s[2].lo, s[3].hi, s[3].lo);
@@ -237,6 +253,7 @@ static __global__ void __launch_bounds__(256) ssm_weights_kernel(const Args a, D
         put(o->w, [&](int k) { return d[k] * factor(end, s[k]); });
         put(o->v, [&](int k) { return d[k] * factor(block, s[k]); });
         put(o->slope, [&](int k) { return sl[k]; });
+        put(o->fw, [&](int k) { return factor(s[k], first); });
         if (lane == 0) o->end = factor(end);
     }
 }

@@ -13,6 +13,10 @@ absolute values (every product positive), and the store adds half a step of the 
       sums of k terms by k u.  On the tensor cores bf16 operands are exact; the weights M, S are
       rounded to bf16 once (half a step 2^-9 of the value below a power of two, 2^-8 at most) and so
       is a state that enters y, dx, dB, dC; a state that is kept enters in two bf16 parts (2^-17).
+      Underflow: a factor, or a part of a weighted operand, below 2^-126 is 0.  Each output is a sum of
+      at most n N P (n + 1) products of such a factor with one element each of x, B, C, dy, a state,
+      D, A and dt, so it moves by at most 2^-126 times that count and the largest elements: below
+      1e-20 for every test here, and nothing but values of 1e-15 and less can tell.
   Gradient of the log decays: differences of sums over a chunk (of at most 128 tokens), so its
       bound takes those sums.
   Norm: sums of m terms, each statistic relative to the spread of u: mean(|u|) m u enters z
@@ -177,9 +181,13 @@ def ssm(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, state=None, len
     n, P, N = x.shape[2], x.shape[3], B.shape[3]
     nc = -(-n // 32)
     k = (1024 + N + P + 16 * nc + x.shape[0] * nc) * U
+    top = lambda t: 1.0 if t is None else 1.0 + float(torch.where(torch.isfinite(t.double()), t.double(), 0.0).abs().max()) if t.numel() else 1.0  # noqa: E731
+    under = 2.0 ** -126 * n * (n + 1) * N * P
+    for t in (x, B, C, D, A, steps, state, dy, dstate):
+        under *= top(t)
     out = {}
     for name, v in val.items():
-        e = k * size[name]
+        e = k * size[name] + under
         if tensor_cores:
             e = e + (2.0 ** -7 if name in ROUNDED else 2.0 ** -15) * size[name]
         out[name] = (v, e)
