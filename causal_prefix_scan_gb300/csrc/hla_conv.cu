@@ -29,13 +29,10 @@ struct Args {
     float *part;  // [B * tiles][width + 1][d]
 };
 
-// Tokens of one warp, and of them those loaded ahead of their use (16 bytes a thread and token
-// leave room for eight: 64 KB in flight per SM).
+// Tokens of one warp, and of them those loaded ahead of their use.
+constexpr int kRun = 32, kRunBack = 32;
 template <typename T, int VEC>
-constexpr int kRun = 16;
-template <typename T, int VEC>
-constexpr int kAhead = VEC == 8 ? 8 : 16 / VEC > 4 ? 8 : 4;
-constexpr int kRunBack = 32;
+constexpr int kAhead = VEC * sizeof(T) >= 16 ? 4 : 8;
 
 template <typename T>
 HLA_DEVICE const T *row_of(const View &v, int b, long long t, int c) {
@@ -69,7 +66,7 @@ struct Filter {
 
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a) {
-    constexpr int RUN = kRun<T, VEC>, U = kAhead<T, VEC>;
+    constexpr int U = kAhead<T, VEC>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = ((int)(blockIdx.x % a.groups) * 32 + lane) * VEC;
     const int rest = blockIdx.x / a.groups, tile = rest % a.tiles, b = rest / a.tiles;
@@ -78,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a)
     if (a.sout && tile == 0 && warp < W - 1)  // the last W - 1 inputs
         store_raw<T, VEC>(static_cast<T *>(a.sout) + ((size_t)b * (W - 1) + warp) * a.d + c,
                           input_at<T, VEC, W>(a, b, len + warp, c));
-    const int t0 = (tile * kWarps + warp) * RUN, end = min(t0 + RUN, len);
+    const int t0 = (tile * kWarps + warp) * kRun, end = min(t0 + kRun, len);
     if (t0 >= end) return;
     const Filter<VEC, W> f(a, c);
     float xw[W - 1][VEC];
@@ -86,12 +83,20 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a)
     for (int i = 0; i < W - 1; ++i) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xw[i]);
     const T *in = row_of<T>(a.x, b, t0, c);
     T *out = row_out<T>(a.y, b, t0, c);
+    raw_t<T, VEC> next[U];
+    auto fetch = [&](int u) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (u + i < end) next[i] = load_raw<T, VEC>(in + (size_t)i * a.x.st);
+        in += (size_t)U * a.x.st;
+    };
+    fetch(t0);
+#pragma unroll 1
     for (int u = t0; u < end; u += U) {
         raw_t<T, VEC> raw[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (u + i < end) raw[i] = load_raw<T, VEC>(in + (size_t)i * a.x.st);
-        in += (size_t)U * a.x.st;
+        for (int i = 0; i < U; ++i) raw[i] = next[i];
+        if (u + U < end) fetch(u + U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (u + i >= end) break;
@@ -121,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a)
 // towards the filter's gradient; dxs_u leaves once g_u is known.
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads, 2) conv_backward_kernel(const Args a) {
-    constexpr int U = 4;
+    constexpr int U = VEC * sizeof(T) >= 8 ? 4 : 8;
     __shared__ float red[kWarps][(W + 1) * 32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x % a.groups, c = (group * 32 + lane) * VEC;
@@ -272,13 +277,15 @@ int tiles_of(int n, int run) { return (int)(((long long)n + kWarps * run - 1) / 
 template <typename T, int VEC, int W>
 cudaError_t launch(Which w, Args a, float *dw, float *db, cudaStream_t st) {
     a.groups = (a.d + 32 * VEC - 1) / (32 * VEC);
-    if (w == W_STEP) {
+    if (w == W_STEP || VEC == 8) {
         const size_t work = (size_t)a.B * ((a.d + VEC - 1) / VEC);
         conv_step_kernel<T, VEC, W><<<(unsigned)((work + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+    } else if constexpr (VEC == 8) {
+        return cudaErrorInvalidValue;  // (steps alone)
     } else if (w == W_FWD) {
-        a.tiles = tiles_of(a.n, kRun<T, VEC>);
+        a.tiles = tiles_of(a.n, kRun);
         conv_forward_kernel<T, VEC, W><<<(unsigned)((size_t)a.B * a.tiles * a.groups), kThreads, 0, st>>>(a);
-    } else if constexpr (VEC <= 4) {  // what eight channels accumulate does not fit the registers
+    } else {
         a.tiles = tiles_of(a.n, kRunBack);
         conv_backward_kernel<T, VEC, W><<<(unsigned)((size_t)a.B * a.tiles * a.groups), kThreads, 0, st>>>(a);
         const cudaError_t e = cudaGetLastError();
@@ -302,7 +309,7 @@ hla_status check(const hla_conv_params *p) {
     if (p->activation != HLA_ACT_NONE && p->activation != HLA_ACT_SILU) return report(HLA_ERR_ARG, "unknown activation");
     if (p->width < 1) return report(HLA_ERR_ARG, "need width >= 1");
     if (p->n > 2147483647 - 1024) return report(HLA_ERR_ARG, "problem too large");  // token counters pass n by a tile
-    const double rows = (double)p->B * (tiles_of(p->n, kRun<float, 1>) + 1);
+    const double rows = (double)p->B * (tiles_of(p->n, kRun) + 1);
     if (rows * ((p->d + 31) / 32) > 2147483647.0 || (double)p->d * 5 > 2147483647.0)
         return report(HLA_ERR_ARG, "problem too large");
     if (p->width < 2 || p->width > 4) return report(HLA_ERR_UNSUPPORTED, "widths of 2 to 4 taps are supported");
@@ -342,9 +349,9 @@ hla_status run(const hla_conv_params *p, Which w, const Args &a, std::initialize
     cudaError_t e;
     if (p->in_dtype == HLA_F32) {
         e = takes(p, rows, states, 4) ? by_width<float, 4>(p->width, w, a, dw, db, st) : by_width<float, 1>(p->width, w, a, dw, db, st);
-    } else if (w != W_BWD && takes(p, rows, states, 8)) {
+    } else if (w == W_STEP && takes(p, rows, states, 8)) {
         e = by_width<__nv_bfloat16, 8>(p->width, w, a, dw, db, st);
-    } else if (takes(p, rows, states, 4)) {
+    } else if (w != W_BWD && takes(p, rows, states, 4)) {
         e = by_width<__nv_bfloat16, 4>(p->width, w, a, dw, db, st);
     } else {
         e = takes(p, rows, states, 2) ? by_width<__nv_bfloat16, 2>(p->width, w, a, dw, db, st)

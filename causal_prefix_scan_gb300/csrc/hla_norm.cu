@@ -7,62 +7,42 @@ namespace hla {
 namespace norm {
 namespace {
 
-constexpr int kThreadsPerSm = 1024;
+constexpr int kThreadsPerSm = 1280;
 
 template <typename T, int VEC, int E, int TEAM>
-__global__ void __launch_bounds__(block_of(TEAM), kThreadsPerSm / block_of(TEAM) / 2) norm_forward_kernel(const Args a) {
+__global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kThreadsPerSm : 1024) / block_of(TEAM)) norm_forward_kernel(const Args a) {
     constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM;
     __shared__ float2 red[2][block_of(TEAM) / 32];
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
     bool ok[K];
-    float w[E], bias[E];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * TEAM + tl) * VEC;
-        ok[k] = g < a.groups && c < a.m;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            w[k * VEC + v] = ok[k] && a.weight ? __ldg(a.weight + (size_t)g * a.m + c + v) : 1.f;
-            bias[k * VEC + v] = ok[k] && a.bias ? __ldg(a.bias + (size_t)g * a.m + c + v) : 0.f;
-        }
-    }
+    for (int k = 0; k < K; ++k) ok[k] = g < a.groups && (k * TEAM + tl) * VEC < a.m;
     const size_t at = (size_t)g * a.m + (size_t)tl * VEC;
-    raw_t<T, VEC> nx[K], nz[K];
-    auto fetch = [&](const Rows &r) {
-        const T *x = row_in<T>(a.x, r.b, r.t) + at;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (ok[k]) nx[k] = load_raw<T, VEC>(x + k * TEAM * VEC);
-        if (a.gate == GATE_NONE) return;
-        const T *z = row_in<T>(a.z, r.b, r.t) + at;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (ok[k]) nz[k] = load_raw<T, VEC>(z + k * TEAM * VEC);
-    };
     const float inv = 1.f / (float)a.m;
-    Rows r(a, blockIdx.x / a.col_blocks);
-    if (r.live()) fetch(r);
     int turn = 0;
-    while (r.live()) {
+    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
         const int b = r.b, t = r.t;
         float u[E];
-        raw_t<T, VEC> z[K];
+        raw_t<T, VEC> x[K], z[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (ok[k]) {
+                x[k] = load_raw<T, VEC>(row_in<T>(a.x, b, t) + at + k * TEAM * VEC);
+                if (a.gate != GATE_NONE) z[k] = load_raw<T, VEC>(row_in<T>(a.z, b, t) + at + k * TEAM * VEC);
+            }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float x[VEC];
-            widen<T, VEC>(nx[k], x);
-            z[k] = nz[k];
+            float f[VEC];
+            widen<T, VEC>(x[k], f);
             if (a.gate == GATE_BEFORE) {
                 float gz[VEC];
                 widen<T, VEC>(z[k], gz);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) x[v] *= silu(gz[v]);
+                for (int v = 0; v < VEC; ++v) f[v] *= silu(gz[v]);
             }
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) u[k * VEC + v] = ok[k] ? x[v] : 0.f;
+            for (int v = 0; v < VEC; ++v) u[k * VEC + v] = ok[k] ? f[v] : 0.f;
         }
-        r.next();
-        if (r.live()) fetch(r);
         if (a.center) {
             float s = 0.f;
 #pragma unroll
@@ -81,11 +61,13 @@ __global__ void __launch_bounds__(block_of(TEAM), kThreadsPerSm / block_of(TEAM)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!ok[k]) continue;
-            float o[VEC], gz[VEC];
+            float o[VEC], gz[VEC], w[VEC], bias[VEC];
+            scale_of<VEC>(a.weight, at + k * TEAM * VEC, true, 1.f, w);
+            scale_of<VEC>(a.bias, at + k * TEAM * VEC, true, 0.f, bias);
             if (a.gate == GATE_AFTER) widen<T, VEC>(z[k], gz);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                o[v] = fmaf(u[k * VEC + v] * rs, w[k * VEC + v], bias[k * VEC + v]);
+                o[v] = fmaf(u[k * VEC + v] * rs, w[v], bias[v]);
                 if (a.gate == GATE_AFTER)
                     o[v] *= silu(gz[v]);
                 else if (a.gate == GATE_NONE && a.silu)
@@ -198,12 +180,12 @@ Args make(const hla_norm_params *p, bool gated, int threads_per_sm) {
 }
 bool wide_rows(const hla_norm_params *p, const Args &a, std::initializer_list<const View *> rows) {
     const size_t el = p->in_dtype == HLA_F32 ? 4 : 2;
-    if (a.m * el % 16) return false;
+    if (a.m * el % 16 || (reinterpret_cast<uintptr_t>(a.weight) & 15u) || (reinterpret_cast<uintptr_t>(a.bias) & 15u)) return false;
     for (const View *v : rows)
         if (v->p && !rows16(*v, el)) return false;
     return true;
 }
-constexpr int kThreadsPerSmBackward = 512, kMostRowBlocks = kSms * (kThreadsPerSmBackward / 256);
+constexpr int kThreadsPerSmBackward = 1024, kMostRowBlocks = kSms * (kThreadsPerSmBackward / 256);
 
 }  // namespace
 }  // namespace norm

@@ -6,9 +6,9 @@
 //   dw = sum over tokens of dv z,  dbias = sum of dv.
 // Memory bounds both: a team of threads holds a group of one token in registers, E channels each,
 // so every element is read once and written once; statistics are two-pass over the registers, in
-// fp32.  A CTA keeps its channels from token to token (the scale, the shift and the sums for dw and
-// dbias stay in registers) and loads the next token before it reduces the present one.  Groups
-// wider than a team holds go through a kernel that reads them again for each pass.
+// fp32.  A CTA keeps its channels from token to token (the sums for dw and dbias stay in
+// registers); while it reduces, the SM's other CTAs load.  Groups wider than a team holds go through
+// a kernel that reads them again for each pass.
 #pragma once
 #include "hla_layer.cuh"
 
@@ -57,6 +57,24 @@ HLA_DEVICE const T *row_in(const View &v, int b, int t) {
 template <typename T>
 HLA_DEVICE T *row_to(const View &v, int b, int t) {
     return static_cast<T *>(v.p) + (size_t)b * v.sb + (size_t)t * v.st;
+}
+
+// VEC adjacent scales or shifts (16-byte aligned where VEC is a multiple of 4).
+template <int VEC>
+HLA_DEVICE void scale_of(const float *p, size_t at, bool ok, float none, float (&v)[VEC]) {
+    if (!p || !ok) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = none;
+    } else if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + at + i));
+            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __ldg(p + at + i);
+    }
 }
 
 // Sums of two values over a team of TEAM threads; `red` holds one float2 for each warp of the

@@ -19,7 +19,7 @@ HLA_DEVICE Behind behind(const Args &a, float dy, float v, float gate) {
 }
 
 template <typename T, int VEC, int E, int TEAM>
-__global__ void __launch_bounds__(block_of(TEAM), 512 / block_of(TEAM)) norm_backward_kernel(const Args a) {
+__global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? 1024 : 512) / block_of(TEAM)) norm_backward_kernel(const Args a) {
     constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM;
     __shared__ float2 red[2][block_of(TEAM) / 32];
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
@@ -31,34 +31,22 @@ __global__ void __launch_bounds__(block_of(TEAM), 512 / block_of(TEAM)) norm_bac
     for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
     const size_t at = (size_t)g * a.m + (size_t)tl * VEC;
     const float inv = 1.f / (float)a.m;
-    raw_t<T, VEC> nx[K], nd[K], nz[K];
-    auto fetch = [&](const Rows &r) {
-        const T *x = row_in<T>(a.x, r.b, r.t) + at, *d = row_in<T>(a.dy, r.b, r.t) + at;
+    int turn = 0;
+    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
+        const int b = r.b, t = r.t;
+        float u[E], q[E];  // the norm's input, then itself; gradients
+        raw_t<T, VEC> x[K], z[K], d[K];
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (ok[k]) {
-                nx[k] = load_raw<T, VEC>(x + k * TEAM * VEC);
-                nd[k] = load_raw<T, VEC>(d + k * TEAM * VEC);
+                x[k] = load_raw<T, VEC>(row_in<T>(a.x, b, t) + at + k * TEAM * VEC);
+                d[k] = load_raw<T, VEC>(row_in<T>(a.dy, b, t) + at + k * TEAM * VEC);
+                if (a.gate != GATE_NONE) z[k] = load_raw<T, VEC>(row_in<T>(a.z, b, t) + at + k * TEAM * VEC);
             }
-        if (a.gate == GATE_NONE) return;
-        const T *z = row_in<T>(a.z, r.b, r.t) + at;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (ok[k]) nz[k] = load_raw<T, VEC>(z + k * TEAM * VEC);
-    };
-    Rows r(a, blockIdx.x / a.col_blocks);
-    if (r.live()) fetch(r);
-    int turn = 0;
-    while (r.live()) {
-        const int b = r.b, t = r.t;
-        float u[E], q[E];  // the norm's input, then itself; gradients
-        raw_t<T, VEC> x[K], z[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float f[VEC];
-            x[k] = nx[k];
-            z[k] = nz[k];
-            widen<T, VEC>(nx[k], f);
+            widen<T, VEC>(x[k], f);
             if (a.gate == GATE_BEFORE) {
                 float gz[VEC];
                 widen<T, VEC>(z[k], gz);
@@ -67,12 +55,10 @@ __global__ void __launch_bounds__(block_of(TEAM), 512 / block_of(TEAM)) norm_bac
             }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) u[k * VEC + v] = ok[k] ? f[v] : 0.f;
-            widen<T, VEC>(nd[k], f);
+            widen<T, VEC>(d[k], f);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) q[k * VEC + v] = f[v];
         }
-        r.next();
-        if (r.live()) fetch(r);
         if (a.center) {
             float s = 0.f;
 #pragma unroll
@@ -90,17 +76,17 @@ __global__ void __launch_bounds__(block_of(TEAM), 512 / block_of(TEAM)) norm_bac
         float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float gz[VEC], dz[VEC];
+            float gz[VEC], dz[VEC], w[VEC], c[VEC];
             if (a.gate == GATE_AFTER) widen<T, VEC>(z[k], gz);
+            scale_of<VEC>(a.weight, at + k * TEAM * VEC, ok[k], 1.f, w);
+            scale_of<VEC>(a.bias, at + k * TEAM * VEC, ok[k], 0.f, c);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const int e = k * VEC + v;
-                const float w = ok[k] && a.weight ? __ldg(a.weight + at + k * TEAM * VEC + v) : 1.f;
-                const float c = ok[k] && a.bias ? __ldg(a.bias + at + k * TEAM * VEC + v) : 0.f;
                 u[e] *= rs;
-                const Behind o = behind(a, q[e], fmaf(u[e], w, c), a.gate == GATE_AFTER ? gz[v] : 0.f);
+                const Behind o = behind(a, q[e], fmaf(u[e], w[v], c[v]), a.gate == GATE_AFTER ? gz[v] : 0.f);
                 dz[v] = o.dgate;
-                q[e] = ok[k] ? o.dv * w : 0.f;
+                q[e] = ok[k] ? o.dv * w[v] : 0.f;
                 if (ok[k]) {
                     dw[e] = fmaf(o.dv, u[e], dw[e]);
                     db[e] += o.dv;

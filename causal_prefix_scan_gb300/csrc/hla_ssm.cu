@@ -10,7 +10,7 @@ namespace {
 // written once, which bounds it.  LP lanes take VEC adjacent columns each and step down the rows;
 // the rows' sums for y meet in shared memory.  A CTA takes all columns of a head, or a few of them
 // where the heads alone would leave SMs idle: columns need no sums between CTAs.
-constexpr int kStepThreads = 256, kStepAhead = 8;
+constexpr int kStepThreads = 256, kStepAhead = 4;
 
 template <typename T, int VEC, int LP>
 __global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(const Args a, float *state, int parts) {

@@ -347,8 +347,10 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         umma_commit_warp(ws.bar(L::B_SE));
         if (!(ok = ws.wait(L::B_YT, ph))) break;
         tc_fence_after();
-        mma_tk64(tb + L::DC, tb + L::YT, Hk, id_k);
+        mma_tk64(tb + L::DC, tb + L::YT, Hk, id_k);  // both parts: the weighted rows are then the only rounding
+        mma_tk64(tb + L::DC, tb + L::YT, Hk + (L::HB >> 4), id_k);
         mma_tk64(tb + L::DB, tb + L::XT, Gk, id_k);
+        mma_tk64(tb + L::DB, tb + L::XT, Gk + (L::HB >> 4), id_k);
         umma_commit_warp(ws.bar(L::B_HE));
         umma_commit_warp(ws.bar(L::B_GE));
         umma_commit_warp(ws.bar(L::B_XDE + sy));
