@@ -29,10 +29,7 @@ struct Args {
     float *part;  // [B * tiles][width + 1][d]
 };
 
-// Tokens of one warp, and of them those loaded ahead of their use.
-constexpr int kRun = 32, kRunBack = 32;
-template <typename T, int VEC>
-constexpr int kAhead = VEC * sizeof(T) >= 16 ? 4 : 8;
+constexpr int kRun = 32, kRunBack = 64;  // tokens of one warp
 
 template <typename T>
 HLA_DEVICE const T *row_of(const View &v, int b, long long t, int c) {
@@ -62,11 +59,18 @@ struct Filter {
             bias[v] = a.bias ? __ldg(a.bias + c + v) : 0.f;
         }
     }
+    // pre of the token whose inputs are xs[0 .. W - 1]
+    HLA_DEVICE void apply(const float (*xs)[VEC], float (&pre)[VEC]) const {
+        fma_v<VEC>(w[0], xs[0], bias, pre);
+#pragma unroll
+        for (int i = 1; i < W; ++i) fma_v<VEC>(w[i], xs[i], pre, pre);
+    }
 };
 
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a) {
-    constexpr int U = kAhead<T, VEC>;
+// Runs of kRun tokens in groups of U, the next group's loads ahead of the present one's work.
+template <typename T, int VEC, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads, VEC == 4 ? 2 : 4) conv_forward_kernel(const Args a) {
+    constexpr int U = VEC * sizeof(T) >= 16 ? 4 : 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = ((int)(blockIdx.x % a.groups) * 32 + lane) * VEC;
     const int rest = blockIdx.x / a.groups, tile = rest % a.tiles, b = rest / a.tiles;
@@ -75,58 +79,51 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const Args a)
     if (a.sout && tile == 0 && warp < W - 1)  // the last W - 1 inputs
         store_raw<T, VEC>(static_cast<T *>(a.sout) + ((size_t)b * (W - 1) + warp) * a.d + c,
                           input_at<T, VEC, W>(a, b, len + warp, c));
-    const int t0 = (tile * kWarps + warp) * kRun, end = min(t0 + kRun, len);
-    if (t0 >= end) return;
+    const int t0 = (tile * kWarps + warp) * kRun, count = min(kRun, len - t0);
+    if (count <= 0) return;
     const Filter<VEC, W> f(a, c);
-    float xw[W - 1][VEC];
+    float xs[W - 1 + U][VEC];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xw[i]);
+    for (int i = 0; i < W - 1; ++i) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xs[i]);
     const T *in = row_of<T>(a.x, b, t0, c);
     T *out = row_out<T>(a.y, b, t0, c);
-    raw_t<T, VEC> next[U];
+    raw_t<T, VEC> raw[U];
     auto fetch = [&](int u) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (u + i < end) next[i] = load_raw<T, VEC>(in + (size_t)i * a.x.st);
+            if (u + i < count) raw[i] = load_raw<T, VEC>(in + (size_t)i * a.x.st);
         in += (size_t)U * a.x.st;
     };
-    fetch(t0);
+    fetch(0);
 #pragma unroll 1
-    for (int u = t0; u < end; u += U) {
-        raw_t<T, VEC> raw[U];
+    for (int u = 0; u < count; u += U) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) raw[i] = next[i];
-        if (u + U < end) fetch(u + U);
+        for (int i = 0; i < U; ++i) widen<T, VEC>(raw[i], xs[W - 1 + i]);
+        if (u + U < count) fetch(u + U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (u + i >= end) break;
-            float x[VEC], y[VEC];
-            widen<T, VEC>(raw[i], x);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float s = fmaf(f.w[W - 1][v], x[v], f.bias[v]);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) s = fmaf(f.w[k][v], xw[k][v], s);
-                y[v] = s;
-#pragma unroll
-                for (int k = 0; k + 1 < W - 1; ++k) xw[k][v] = xw[k + 1][v];
-                xw[W - 2][v] = x[v];
-            }
-            if (a.silu) {
+            float y[VEC];
+            f.apply(xs + i, y);
+            if (SILU) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) y[v] = silu(y[v]);
             }
-            store_raw<T, VEC>(out + (size_t)i * a.y.st, narrow<T, VEC>(y));
+            if (u + i < count) store_raw<T, VEC>(out + (size_t)i * a.y.st, narrow<T, VEC>(y));
         }
         out += (size_t)U * a.y.st;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) xs[i][v] = xs[U + i][v];
     }
 }
 
-// One warp's run: g of tokens t0 .. t0 + kRunBack + W - 2, of which the first kRunBack count
-// towards the filter's gradient; dxs_u leaves once g_u is known.
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, 2) conv_backward_kernel(const Args a) {
-    constexpr int U = VEC * sizeof(T) >= 8 ? 4 : 8;
+// One warp's run of kRunBack tokens: their g counts towards the filter's gradient, and g of the
+// W - 1 tokens behind them is formed again, so that dxs_u leaves once g_u is known.  Groups of U
+// tokens, inputs ahead.
+template <typename T, int VEC, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kernel(const Args a) {
+    constexpr int U = 4;
     __shared__ float red[kWarps][(W + 1) * 32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x % a.groups, c = (group * 32 + lane) * VEC;
@@ -135,83 +132,80 @@ __global__ void __launch_bounds__(kThreads, 2) conv_backward_kernel(const Args a
     const int t0 = (tile * kWarps + warp) * kRunBack;
     float dw[W + 1][VEC];  // taps, then bias
 #pragma unroll
-    for (int i = 0; i <= W; ++i)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) dw[i][v] = 0.f;
+    for (int i = 0; i <= W; ++i) fill_v<VEC>(0.f, dw[i]);
     if (c < a.d && (t0 < len || t0 == 0)) {
         const Filter<VEC, W> f(a, c);
-        float xw[W][VEC], g[W][VEC];  // xs_t .. xs_{t+W-1}; g_{t-W+1} .. g_t
+        float xs[W - 1 + U][VEC], g[W - 1 + U][VEC];  // xs_u .. ; g_{u-W+1} ..
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            if (t0 + i < len + W - 1) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xw[i + 1]);
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) g[i][v] = 0.f;
-        const int last = t0 + kRunBack + W - 1;  // tokens [t0, last)
-        for (int u = t0; u < last; u += U) {
-            raw_t<T, VEC> rx[U], rd[U];
+        for (int i = 0; i < W - 1; ++i) {
+            fill_v<VEC>(0.f, xs[i]);
+            fill_v<VEC>(0.f, g[i]);
+            if (t0 + i < len + W - 1) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xs[i]);
+        }
+        const int behind = min(t0 + kRunBack, len), last = min(t0 + kRunBack, len) + W - 1;  // dxs_u for u < last
+        const int loads = min(last, len);
+        raw_t<T, VEC> rx[U], rd[U];
+        const T *xp = row_of<T>(a.x, b, t0, c), *dp = row_of<T>(a.dy, b, t0, c);
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < U; ++i)
-                if (u + i < min(last, len)) {
-                    rx[i] = load_raw<T, VEC>(row_of<T>(a.x, b, u + i, c));
-                    rd[i] = load_raw<T, VEC>(row_of<T>(a.dy, b, u + i, c));
+                if (t + i < loads) {
+                    rx[i] = load_raw<T, VEC>(xp + (size_t)i * a.x.st);
+                    rd[i] = load_raw<T, VEC>(dp + (size_t)i * a.dy.st);
                 }
+            xp += (size_t)U * a.x.st;
+            dp += (size_t)U * a.dy.st;
+        };
+        fetch(t0);
+#pragma unroll 1
+        for (int t = t0; t < last; t += U) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int t = u + i;
-                if (t >= last || t >= len + W - 1) break;
+                widen<T, VEC>(rx[i], xs[W - 1 + i]);
+                widen<T, VEC>(rd[i], g[W - 1 + i]);
+            }
+            if (t + U < last) fetch(t + U);
 #pragma unroll
-                for (int k = 0; k + 1 < W; ++k)
+            for (int i = 0; i < U; ++i) {
+                float(&gt)[VEC] = g[W - 1 + i];
+                if (SILU) {
+                    float pre[VEC];
+                    f.apply(xs + i, pre);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        xw[k][v] = xw[k + 1][v];
-                        g[k][v] = g[k + 1][v];
-                    }
-                if (t < len) {
-                    widen<T, VEC>(rx[i], xw[W - 1]);
-                    widen<T, VEC>(rd[i], g[W - 1]);
-                    if (a.silu) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) {
-                            float s = fmaf(f.w[W - 1][v], xw[W - 1][v], f.bias[v]);
-#pragma unroll
-                            for (int k = 0; k < W - 1; ++k) s = fmaf(f.w[k][v], xw[k][v], s);
-                            g[W - 1][v] *= silu_slope(s, sigmoid(s));
-                        }
-                    }
-                    if (t < t0 + kRunBack) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-                            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(g[W - 1][v], xw[k][v], dw[k][v]);
-                            dw[W][v] += g[W - 1][v];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) g[W - 1][v] = 0.f;
+                    for (int v = 0; v < VEC; ++v) gt[v] *= silu_slope(pre[v], sigmoid(pre[v]));
                 }
-                const int s = t - (W - 1);  // dxs_t: row s of dx, or of the state's gradient
-                if (s < t0 && t0 > 0) continue;
+                if (t + i >= len) fill_v<VEC>(0.f, gt);  // (whatever was in the registers)
+                if (t + i < behind) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) fma_v<VEC>(gt, xs[i + k], dw[k], dw[k]);
+                    add_v<VEC>(dw[W], gt, dw[W]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = t + i, s = u - (W - 1);  // dxs_u: row s of dx, or of the state's gradient
+                if (u >= last || (s < t0 && t0 > 0)) continue;
                 float o[VEC];
+                mul_v<VEC>(f.w[0], g[W - 1 + i], o);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    o[v] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < W; ++k) o[v] = fmaf(f.w[k][v], g[W - 1 - k][v], o[v]);
-                }
-                if (t >= len && a.dsout) {
+                for (int k = 1; k < W; ++k) fma_v<VEC>(f.w[k], g[W - 1 + i - k], o, o);
+                if (u >= len && a.dsout) {
                     float e[VEC];
-                    widen<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.dsout) + ((size_t)b * (W - 1) + (t - len)) * a.d + c), e);
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) o[v] += e[v];
+                    widen<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.dsout) + ((size_t)b * (W - 1) + (u - len)) * a.d + c), e);
+                    add_v<VEC>(o, e, o);
                 }
                 if (s >= 0)
                     store_raw<T, VEC>(row_out<T>(a.dx, b, s, c), narrow<T, VEC>(o));
                 else if (a.dsin)
-                    store_raw<T, VEC>(static_cast<T *>(a.dsin) + ((size_t)b * (W - 1) + t) * a.d + c, narrow<T, VEC>(o));
+                    store_raw<T, VEC>(static_cast<T *>(a.dsin) + ((size_t)b * (W - 1) + u) * a.d + c, narrow<T, VEC>(o));
             }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    xs[i][v] = xs[U + i][v];
+                    g[i][v] = g[U + i][v];
+                }
         }
     }
 #pragma unroll
@@ -277,17 +271,28 @@ int tiles_of(int n, int run) { return (int)(((long long)n + kWarps * run - 1) / 
 template <typename T, int VEC, int W>
 cudaError_t launch(Which w, Args a, float *dw, float *db, cudaStream_t st) {
     a.groups = (a.d + 32 * VEC - 1) / (32 * VEC);
-    if (w == W_STEP || VEC == 8) {
+    // bf16 prompts go two channels at a time: with what four of them hold in registers too few warps
+    // fit an SM (n32768 d4352 forward 153 -> 115 us)
+    constexpr bool STEPS_ALONE = sizeof(T) == 2 && VEC > 2;
+    if (w == W_STEP) {
         const size_t work = (size_t)a.B * ((a.d + VEC - 1) / VEC);
         conv_step_kernel<T, VEC, W><<<(unsigned)((work + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
-    } else if constexpr (VEC == 8) {
-        return cudaErrorInvalidValue;  // (steps alone)
+    } else if constexpr (STEPS_ALONE) {
+        return cudaErrorInvalidValue;
     } else if (w == W_FWD) {
         a.tiles = tiles_of(a.n, kRun);
-        conv_forward_kernel<T, VEC, W><<<(unsigned)((size_t)a.B * a.tiles * a.groups), kThreads, 0, st>>>(a);
+        const unsigned grid = (unsigned)((size_t)a.B * a.tiles * a.groups);
+        if (a.silu)
+            conv_forward_kernel<T, VEC, W, true><<<grid, kThreads, 0, st>>>(a);
+        else
+            conv_forward_kernel<T, VEC, W, false><<<grid, kThreads, 0, st>>>(a);
     } else {
         a.tiles = tiles_of(a.n, kRunBack);
-        conv_backward_kernel<T, VEC, W><<<(unsigned)((size_t)a.B * a.tiles * a.groups), kThreads, 0, st>>>(a);
+        const unsigned grid = (unsigned)((size_t)a.B * a.tiles * a.groups);
+        if (a.silu)
+            conv_backward_kernel<T, VEC, W, true><<<grid, kThreads, 0, st>>>(a);
+        else
+            conv_backward_kernel<T, VEC, W, false><<<grid, kThreads, 0, st>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         const long long cols = (long long)a.d * (W + 1);
@@ -351,7 +356,7 @@ hla_status run(const hla_conv_params *p, Which w, const Args &a, std::initialize
         e = takes(p, rows, states, 4) ? by_width<float, 4>(p->width, w, a, dw, db, st) : by_width<float, 1>(p->width, w, a, dw, db, st);
     } else if (w == W_STEP && takes(p, rows, states, 8)) {
         e = by_width<__nv_bfloat16, 8>(p->width, w, a, dw, db, st);
-    } else if (w != W_BWD && takes(p, rows, states, 4)) {
+    } else if (w == W_STEP && takes(p, rows, states, 4)) {
         e = by_width<__nv_bfloat16, 4>(p->width, w, a, dw, db, st);
     } else {
         e = takes(p, rows, states, 2) ? by_width<__nv_bfloat16, 2>(p->width, w, a, dw, db, st)

@@ -65,6 +65,76 @@ HLA_DEVICE raw_t<T, VEC> narrow(const float (&v)[VEC]) {
 template <typename T, int VEC>
 HLA_DEVICE void store_raw(T *p, const raw_t<T, VEC> &r) { *reinterpret_cast<raw_t<T, VEC> *>(p) = r; }
 
+// Pairs of fp32: one instruction for two lanes' worth of arithmetic.
+HLA_DEVICE float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+HLA_DEVICE float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+HLA_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+HLA_DEVICE float2 both(float x) { return make_float2(x, x); }
+// The same on VEC channels: a b + c, a b, a + b, elementwise.
+template <int VEC>
+HLA_DEVICE void fma_v(const float (&a)[VEC], const float (&b)[VEC], const float (&c)[VEC], float (&r)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 x = fma2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+            r[i] = x.x;
+            r[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[i] = fmaf(a[i], b[i], c[i]);
+    }
+}
+template <int VEC>
+HLA_DEVICE void mul_v(const float (&a)[VEC], const float (&b)[VEC], float (&r)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 x = mul2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            r[i] = x.x;
+            r[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[i] = a[i] * b[i];
+    }
+}
+template <int VEC>
+HLA_DEVICE void add_v(const float (&a)[VEC], const float (&b)[VEC], float (&r)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 x = add2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            r[i] = x.x;
+            r[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[i] = a[i] + b[i];
+    }
+}
+template <int VEC>
+HLA_DEVICE void fill_v(float x, float (&r)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r[i] = x;
+}
+
 // VEC floats of an aligned or single-channel array.
 template <int VEC>
 HLA_DEVICE void load_f32(const float *p, float (&v)[VEC]) {

@@ -1,4 +1,4 @@
-// hla_norm.cu -- forward of the grouped norm (see hla_norm.cuh), and its entry points.
+// hla_norm.cu -- entry points of the grouped norm (see hla_norm.cuh).
 #include <cmath>
 
 #include "hla_norm.cuh"
@@ -7,143 +7,14 @@ namespace hla {
 namespace norm {
 namespace {
 
-constexpr int kThreadsPerSm = 1280;
-
-template <typename T, int VEC, int E, int TEAM>
-__global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kThreadsPerSm : 1024) / block_of(TEAM)) norm_forward_kernel(const Args a) {
-    constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM;
-    __shared__ float2 red[2][block_of(TEAM) / 32];
-    const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
-    bool ok[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) ok[k] = g < a.groups && (k * TEAM + tl) * VEC < a.m;
-    const size_t at = (size_t)g * a.m + (size_t)tl * VEC;
-    const float inv = 1.f / (float)a.m;
-    int turn = 0;
-    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
-        const int b = r.b, t = r.t;
-        float u[E];
-        raw_t<T, VEC> x[K], z[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (ok[k]) {
-                x[k] = load_raw<T, VEC>(row_in<T>(a.x, b, t) + at + k * TEAM * VEC);
-                if (a.gate != GATE_NONE) z[k] = load_raw<T, VEC>(row_in<T>(a.z, b, t) + at + k * TEAM * VEC);
-            }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float f[VEC];
-            widen<T, VEC>(x[k], f);
-            if (a.gate == GATE_BEFORE) {
-                float gz[VEC];
-                widen<T, VEC>(z[k], gz);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) f[v] *= silu(gz[v]);
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) u[k * VEC + v] = ok[k] ? f[v] : 0.f;
+__global__ void __launch_bounds__(256) norm_sums_kernel(const float *part, int rows, int d, float *dw, float *db) {
+    column_sums(part, rows, 2LL * d, [=](long long k, float s) {
+        if (k < d) {
+            if (dw) dw[k] = s;
+        } else if (db) {
+            db[k - d] = s;
         }
-        if (a.center) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s += u[e];
-            const float mean = team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x * inv;
-            turn ^= 1;
-#pragma unroll
-            for (int e = 0; e < E; ++e) u[e] = ok[e / VEC] ? u[e] - mean : 0.f;
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(u[e], u[e], s);
-        const float rs = rsqrtf(fmaf(team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x, inv, a.eps));
-        turn ^= 1;
-        T *y = row_to<T>(a.y, b, t) + at;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!ok[k]) continue;
-            float o[VEC], gz[VEC], w[VEC], bias[VEC];
-            scale_of<VEC>(a.weight, at + k * TEAM * VEC, true, 1.f, w);
-            scale_of<VEC>(a.bias, at + k * TEAM * VEC, true, 0.f, bias);
-            if (a.gate == GATE_AFTER) widen<T, VEC>(z[k], gz);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                o[v] = fmaf(u[k * VEC + v] * rs, w[v], bias[v]);
-                if (a.gate == GATE_AFTER)
-                    o[v] *= silu(gz[v]);
-                else if (a.gate == GATE_NONE && a.silu)
-                    o[v] = silu(o[v]);
-            }
-            store_raw<T, VEC>(y + k * TEAM * VEC, narrow<T, VEC>(o));
-        }
-    }
-}
-
-// Groups wider than a team holds: one CTA per group and token, three passes.
-template <typename T>
-__global__ void __launch_bounds__(256) norm_forward_long_kernel(const Args a) {
-    __shared__ float2 red[2][8];
-    const int g = blockIdx.x % a.col_blocks;
-    const size_t at = (size_t)g * a.m;
-    const float inv = 1.f / (float)a.m;
-    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
-        const T *x = row_in<T>(a.x, r.b, r.t) + at;
-        const T *z = a.gate != GATE_NONE ? row_in<T>(a.z, r.b, r.t) + at : nullptr;
-        auto value = [&](int c, float &gate) {
-            float v[1];
-            widen<T, 1>(load_raw<T, 1>(x + c), v);
-            float u = v[0];
-            gate = 1.f;
-            if (z) {
-                widen<T, 1>(load_raw<T, 1>(z + c), v);
-                gate = silu(v[0]);
-            }
-            return a.gate == GATE_BEFORE ? u * gate : u;
-        };
-        float mean = 0.f, s = 0.f, gate;
-        if (a.center) {
-            for (int c = threadIdx.x; c < a.m; c += 256) s += value(c, gate);
-            mean = team_sum<256>(make_float2(s, 0.f), red[0]).x * inv;
-        }
-        s = 0.f;
-        for (int c = threadIdx.x; c < a.m; c += 256) {
-            const float u = value(c, gate) - mean;
-            s = fmaf(u, u, s);
-        }
-        const float rs = rsqrtf(fmaf(team_sum<256>(make_float2(s, 0.f), red[1]).x, inv, a.eps));
-        T *y = row_to<T>(a.y, r.b, r.t) + at;
-        for (int c = threadIdx.x; c < a.m; c += 256) {
-            const float u = value(c, gate) - mean;
-            float o[1] = {fmaf(u * rs, a.weight ? __ldg(a.weight + at + c) : 1.f, a.bias ? __ldg(a.bias + at + c) : 0.f)};
-            if (a.gate == GATE_AFTER) o[0] *= gate;
-            if (a.gate == GATE_NONE && a.silu) o[0] = silu(o[0]);
-            store_raw<T, 1>(y + c, narrow<T, 1>(o));
-        }
-        __syncthreads();
-    }
-}
-
-template <typename T, int VEC, int E, int TEAM>
-void launch(const Args &a, cudaStream_t st) {
-    norm_forward_kernel<T, VEC, E, TEAM><<<(unsigned)(a.col_blocks * a.row_blocks), block_of(TEAM), 0, st>>>(a);
-}
-template <typename T, int VEC, int E>
-void by_team(const Args &a, int team, cudaStream_t st) {
-    if (team == 8) return launch<T, VEC, E, 8>(a, st);
-    if (team == 32) return launch<T, VEC, E, 32>(a, st);
-    if (team == 128) return launch<T, VEC, E, 128>(a, st);
-    launch<T, VEC, E, 512>(a, st);
-}
-template <typename T>
-cudaError_t forward(const Args &a, bool wide, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    const Team t = team_of(a.m);
-    if (!t.E)
-        norm_forward_long_kernel<T><<<(unsigned)(a.col_blocks * a.row_blocks), 256, 0, st>>>(a);
-    else if (t.E == 8)
-        wide ? by_team<T, V, 8>(a, t.threads, st) : by_team<T, 1, 8>(a, t.threads, st);
-    else
-        wide ? by_team<T, V, 16>(a, t.threads, st) : by_team<T, 1, 16>(a, t.threads, st);
-    return cudaGetLastError();
+    });
 }
 
 hla_status check(const hla_norm_params *p) {
@@ -185,7 +56,7 @@ bool wide_rows(const hla_norm_params *p, const Args &a, std::initializer_list<co
         if (v->p && !rows16(*v, el)) return false;
     return true;
 }
-constexpr int kThreadsPerSmBackward = 1024, kMostRowBlocks = kSms * (kThreadsPerSmBackward / 256);
+constexpr int kMostRowBlocks = kSms * (kBackwardThreads / 256);
 
 }  // namespace
 }  // namespace norm
@@ -208,12 +79,13 @@ hla_status hla_norm_forward(const hla_norm_params *p, const hla_tensor *x, const
         (s = check_out(y, d, dt, "y must be set")) != HLA_OK)
         return s;
     if (y->p == x->p || (gate && y->p == gate->p)) return report(HLA_ERR_ARG, "y may not be an input");
-    Args a = make(p, gate != nullptr, kThreadsPerSm);
+    Args a = make(p, gate != nullptr, kForwardThreads);
     a.x = view(x, d); a.y = view(y, d);
     if (gate) a.z = view(gate, d);
     const bool wide = wide_rows(p, a, {&a.x, &a.y, &a.z});
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dt == HLA_F32 ? forward<float>(a, wide, st) : forward<__nv_bfloat16>(a, wide, st);
+    dt == HLA_F32 ? forward_f32(a, wide, st) : forward_bf16(a, wide, st);
+    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -252,11 +124,17 @@ hla_status hla_norm_backward(const hla_norm_params *p, const hla_tensor *x, cons
     if (!workspace || workspace_bytes < hla_norm_backward_workspace_size(p))
         return report(HLA_ERR_ARG, "workspace too small (hla_norm_backward_workspace_size)");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return report(HLA_ERR_ARG, "workspace must be 256-byte aligned");
-    Args a = make(p, gate != nullptr, kThreadsPerSmBackward);
+    Args a = make(p, gate != nullptr, kBackwardThreads);
     a.x = view(x, d); a.dy = view(dy, d); a.dx = view(dx, d);
     if (gate) a.z = view(gate, d), a.dz = view(d_gate, d);
     a.part = static_cast<float *>(workspace);
-    const cudaError_t e = backward(a, dt, wide_rows(p, a, {&a.x, &a.dy, &a.dx, &a.z, &a.dz}), d_weight, d_bias, st);
+    const bool wide = wide_rows(p, a, {&a.x, &a.dy, &a.dx, &a.z, &a.dz});
+    dt == HLA_F32 ? backward_f32(a, wide, st) : backward_bf16(a, wide, st);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && (d_weight || d_bias)) {
+        norm_sums_kernel<<<(unsigned)((2LL * a.d + 31) / 32), 256, 0, st>>>(a.part, a.row_blocks, a.d, d_weight, d_bias);
+        e = cudaGetLastError();
+    }
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
 

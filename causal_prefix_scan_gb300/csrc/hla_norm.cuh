@@ -34,18 +34,27 @@ struct Args {
 // Most channels of a group that a team holds: E = 16 of 512 threads.
 constexpr int kHeld = 8192;
 
-// Rows that the CTA's row block takes: r, r + row_blocks, ... of those below their lengths.
+// Rows that the CTA's row block takes: every row_blocks-th of all rows that are below their lengths.
+// (Counted on by additions: a division for each row is a tenth of a narrow group's work.)
 struct Rows {
     const Args &a;
-    long long r, total;
     int b, t;
-    HLA_DEVICE Rows(const Args &a_, int first) : a(a_), r((long long)first - a_.row_blocks), total((long long)a_.B * a_.n), b(0), t(0) { next(); }
-    HLA_DEVICE bool live() const { return r < total; }
+    HLA_DEVICE Rows(const Args &a_, int first) : a(a_), b(first / a_.n), t(first % a_.n) { settle(); }
+    HLA_DEVICE bool live() const { return b < a.B; }
     HLA_DEVICE void next() {
-        for (r += a.row_blocks; r < total; r += a.row_blocks) {
-            b = (int)(r / a.n);
-            t = (int)(r - (long long)b * a.n);
-            if (!a.lengths || t < a.lengths[b]) return;
+        t += a.row_blocks;
+        settle();
+    }
+    HLA_DEVICE void settle() {
+        while (b < a.B) {
+            if (t >= a.n) {
+                t -= a.n;
+                ++b;
+            } else if (!a.lengths || t < a.lengths[b]) {
+                return;
+            } else {
+                t += a.row_blocks;
+            }
         }
     }
 };
@@ -104,19 +113,23 @@ HLA_DEVICE float2 team_sum(float2 v, float2 *red) {
 }
 
 // `wide`: rows on 16-byte boundaries and groups of whole 16-byte pieces.
-cudaError_t backward(const Args &a, hla_dtype dt, bool wide, float *dw, float *db, cudaStream_t st);
+void forward_f32(const Args &a, bool wide, cudaStream_t st);
+void forward_bf16(const Args &a, bool wide, cudaStream_t st);
+void backward_f32(const Args &a, bool wide, cudaStream_t st);
+void backward_bf16(const Args &a, bool wide, cudaStream_t st);
 
-// The team of a group of m <= kHeld channels: the smallest that holds it.
+// The team of a group of m <= kHeld channels: eight channels a thread, sixteen for the widest.
 struct Team {
     int threads, E;
 };
 inline Team team_of(int m) {
-    for (int t = 8; t <= 512; t *= 4)
-        for (int E = 8; E <= 16; E += 8)
-            if (m <= t * E) return {t, E};
+    for (int t = 8; t <= 512; t *= 2)
+        if (m <= 8 * t) return {t, 8};
+    if (m <= kHeld) return {512, 16};
     return {256, 0};  // read again for each pass, one CTA per group
 }
-constexpr int kSms = 152;
+// Threads per SM that the kernels are built for.
+constexpr int kSms = 152, kForwardThreads = 1280, kBackwardThreads = 1024;
 constexpr int block_of(int team) { return team > 256 ? team : 256; }
 // CTAs side by side over the channels of a token, and over the tokens: about as many as the
 // device runs at once (the sums for dw and dbias are kept per CTA).
@@ -129,6 +142,25 @@ inline int columns_of(int groups, int m) {
 inline int row_blocks_of(long long rows, int groups, int m, int threads_per_sm) {
     const long long most = (long long)kSms * (threads_per_sm / block_of(team_of(m).threads)) / columns_of(groups, m);
     return (int)(most < 1 ? 1 : most < rows ? most : rows);
+}
+
+// Launch<T, VEC, E, TEAM, GATE>::go of a call's sizes.
+template <template <typename, int, int, int, int> class Launch, typename T, int VEC, int E, int TEAM>
+void by_gate(const Args &a, cudaStream_t st) {
+    if (a.gate == GATE_NONE) return Launch<T, VEC, E, TEAM, GATE_NONE>::go(a, st);
+    if (a.gate == GATE_AFTER) return Launch<T, VEC, E, TEAM, GATE_AFTER>::go(a, st);
+    Launch<T, VEC, E, TEAM, GATE_BEFORE>::go(a, st);
+}
+template <template <typename, int, int, int, int> class Launch, typename T, int VEC>
+void by_team(const Args &a, Team t, cudaStream_t st) {
+    if (t.E == 16) return by_gate<Launch, T, VEC, 16, 512>(a, st);
+    if (t.threads == 8) return by_gate<Launch, T, VEC, 8, 8>(a, st);
+    if (t.threads == 16) return by_gate<Launch, T, VEC, 8, 16>(a, st);
+    if (t.threads == 32) return by_gate<Launch, T, VEC, 8, 32>(a, st);
+    if (t.threads == 64) return by_gate<Launch, T, VEC, 8, 64>(a, st);
+    if (t.threads == 128) return by_gate<Launch, T, VEC, 8, 128>(a, st);
+    if (t.threads == 256) return by_gate<Launch, T, VEC, 8, 256>(a, st);
+    by_gate<Launch, T, VEC, 8, 512>(a, st);
 }
 
 }  // namespace norm

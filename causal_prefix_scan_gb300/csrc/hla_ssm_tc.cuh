@@ -136,27 +136,6 @@ HLA_DEVICE void clear_rows(uint8_t *tile, int blocks, int r0) {
     fence_async_smem();
     __syncwarp();
 }
-// Pairs of fp32: one instruction for two lanes' worth of arithmetic.
-HLA_DEVICE float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-HLA_DEVICE float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}\n"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-HLA_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
-        " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}\n"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-HLA_DEVICE float2 both(float x) { return make_float2(x, x); }
 HLA_DEVICE uint32_t pack2(float2 v) { return pack_bf16(v.x, v.y); }
 HLA_DEVICE float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 HLA_DEVICE void unpack8(const uint4 u, float2 *v) {
