@@ -42,8 +42,9 @@ struct Args {
     float *factor;        // [B][H][nc]: 2^s_end
     float *dbc;           // [splits][2][B][G][n][N]
     void *dec;            // [B][H][nc]: the chunks' weights (tensor cores)
-    unsigned char *image[2];  // the chunks' states and their gradients (tensor cores, backward)
-    float *sums;          // [B][nc][3][H]: parts of dA, dD, dt_bias' gradient
+    unsigned char *image[2];  // tensor cores, backward: the chunks' states and their gradients, and fp32 sums of tokens and borders
+    float *inter, *aside, *dots, *own, *dd;
+    float *sums;          // [rows][3][H]: parts of dA, dD, dt_bias' gradient
     unsigned *err;
 };
 
@@ -136,7 +137,7 @@ inline int simt_chunk(int P, int N) { return P > 64 && N > 64 ? 32 : 64; }
 cudaError_t simt_forward(const Args &a, hla_dtype dt, cudaStream_t st);
 cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st);
 // What both backward paths end with: dB, dC from their parts if there are any, dA, dD and dt_bias' gradient.
-cudaError_t join(const Args &a, hla_dtype dt, bool parts, cudaStream_t st);
+cudaError_t join(const Args &a, hla_dtype dt, bool parts, int rows, cudaStream_t st);
 
 // Tensor cores: bf16 whose rows start on 16-byte boundaries (tc_takes); the workspace's bytes, its
 // pointers set when `base` is given; cudaErrorNotSupported, with nothing launched, when the driver

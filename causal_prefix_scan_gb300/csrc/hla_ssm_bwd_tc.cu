@@ -1,17 +1,20 @@
 // hla_ssm_bwd_tc.cu -- backward of the selective state space scan for bf16 on the tensor cores
 // (formulas in hla_ssm.h).
 //
-// The walks of hla_ssm_carry.cuh leave, for every chunk and head, the state before it and the
-// gradient behind it as pairs of bf16 tile images.  grad_kernel then takes a chunk of one group:
-// B, C and C B^T (in registers) stay, the heads pass by 64 columns at a time.  Per head, rows j and
-// columns t:
-//   X dY^T                       -> M^T, S^T (bf16, with dt_j), sums of E = M o (dY X^T) in fp32
-//   Z = C h, B g (both parts)    -> w, v: what enters the gradients of dt, A and dt_bias is fp32
-//   M^T dY, S^T C, S B, (e dY) h^T, (w X) g^T: dX per head, dB and dC accumulated in TMEM
+// states_kernel walks the pieces of hla_ssm_carry.cuh forward and then back and leaves, for every
+// chunk and head, the state before it and the gradient behind it as bf16 tile images, and in fp32
+// what they make of the tokens' own rows and of each other: w', v' and <g, h>, which the gradients of
+// dt, A and dt_bias need.
+// grad_kernel then takes a chunk of one group: B, C and C B^T (in registers) stay, the heads pass by
+// 64 columns at a time.  Per head, rows j and columns t:
+//   X dY^T                      -> M^T, S^T (bf16, with dt_j), sums of E = M o (dY X^T) in fp32
+//   B g, M^T dY                 -> dX
+//   S^T C, S B, (e dY) h^T, (w X) g^T: dB and dC, accumulated in TMEM over the heads
 // so that dB and dC leave once per CTA.  A chunk's heads are shared by several CTAs only where
-// chunks alone are too few; their parts are then added by a kernel of its own.
-// Roles (20 warps): 0-15 elementwise, 16 MMA, 17 loads of X, dY and weights, 18 of B, C and the
-// images, 19 stores dX and turns the sums into d_dt, dA, dD and dt_bias' gradient.
+// chunks alone are too few; their parts are then added by a kernel of its own.  finish_kernel puts
+// the sums together.
+// Roles of grad_kernel (20 warps): 0-15 elementwise, 16 MMA, 17 loads of X, dY and weights, 18 of B, C
+// and the images, 19 stores dX and the sums.
 #include <cstring>
 
 #include "hla_ssm_carry.cuh"
@@ -22,6 +25,290 @@ namespace {
 
 using namespace tcs;
 
+// ------------------------------------------------------------ states of the chunks
+// A piece forward and then back: on the way forward the state before each chunk, on the way back the
+// gradient behind it, both as bf16 tile images, and in fp32 what they make of every token's own rows:
+// w' = 2^s dY.(C h), v' = 2^(s_end - s) X.(B g).  The state meets C (or B) in three bf16 parts, like the
+// rows that enter it.  Each thread lays its part of the state aside on the way forward and forms its
+// share of <g, h> with it on the way back.  (With <g, h> followed from chunk to chunk by what w' and
+// v' add up to, its error runs through all tokens behind it: dA came out 3e-5 off.)
+// Roles (20 warps): 0-15 elementwise, 16 MMA, 17 loads of the rows that enter, 18 of those that meet
+// the state and the images' stores, 19 loads of B and C.
+constexpr int kStatesThreads = 20 * 32, kWarpLoadBc = 19;
+template <int NB>
+struct LayStates {
+    static constexpr int NX = 2;                   // stages of the rows that enter, with the weights
+    static constexpr int HB = NB * kHalf / 2;      // one part of a state
+    static constexpr int OFF_X = 0, OFF_Y = NX * kHalf, OFF_P = OFF_Y + kHalf, OFF_Q = OFF_P + NB * kHalf, OFF_W = OFF_Q + NB * kHalf,
+                         OFF_H = OFF_W + 3 * kHalf, OFF_DEC = OFF_H + 3 * HB, OFF_BAR = OFF_DEC + NX * kDecBytes;
+    static constexpr int B_X = 0, B_XE = B_X + NX, B_Y = B_XE + NX, B_YE = B_Y + 1, B_P = B_YE + 1, B_PE = B_P + 1, B_Q = B_PE + 1, B_QE = B_Q + 1,
+                         B_W = B_QE + 1, B_D = B_W + 1, B_Z = B_D + 1, B_SE = B_Z + 1, B_FIN = B_SE + 1, B_RAWX = B_FIN + 1, B_RAWY = B_RAWX + 1,
+                         B_RAWB = B_RAWY + 1, NBAR = B_RAWB + 1;
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
+    static constexpr uint32_t D = 0, Z = 192;  // TMEM columns
+    HLA_DEVICE static int arrivals(int i) { return (i >= B_XE && i < B_Y) || i == B_YE || i == B_W ? kElemWarps : 1; }
+};
+struct StatesParams {
+    Params p;
+    uint8_t *image[2];  // [B][H][PT][chunks][64 NB rows][64]
+    float *inter;       // [dir][PT][4][B][H][chunks * T]: w', v' by quarters of the columns
+    float4 *aside;      // [B][H][PT][chunks][4][512]: states, by the threads that formed them
+    float *dots;        // [B][H][chunks][PT][16]: <g, h> by warps
+};
+struct Walk {  // 2 K visits to the chunks of a piece
+    Piece w;
+    int K;
+    HLA_DEVICE int dir(int k) const { return k >= K; }
+    HLA_DEVICE int chunk(int k) const { return k < K ? w.lo + k : w.hi - 1 - (k - K); }
+};
+
+HLA_DEVICE float dot16(const float2 (&x)[8], const float2 (&y)[8]) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fma2(x[i], y[i], s);
+    return s.x + s.y;
+}
+HLA_DEVICE float lanes_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+HLA_DEVICE void load_row16(const uint8_t *tile, int rows, int r, int c0, float2 (&v)[8]) {
+    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(rows, r, c0)), v);
+    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(rows, r, c0 + 8)), v + 4);
+}
+
+template <int NB>
+__device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits &ws, uint8_t *base, uint32_t tb, const Walk &z) {
+    using L = LayStates<NB>;
+    const Params &p = sp.p;
+    const Args &a = p.a;
+    const Piece &w = z.w;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, cq = warp >> 2, row = 32 * q + lane, c0 = 16 * cq;
+    const uint32_t lanes = tb + ((uint32_t)(32 * q) << 16);
+    const int col = 64 * w.pt + c0, visits = 2 * z.K;
+    const bool holds = q < 2 * NB;  // rows of the state
+    const size_t unit = (size_t)w.b * a.H + w.h, NP = (size_t)a.N * a.P, plane = (size_t)a.B * a.H * a.nc * T;
+    float2 carry[8];
+    auto begin = [&](int dir) {
+        const float *init = dir ? a.d_state_out : a.state_in;
+        load_state(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, dir, w) : init ? init + unit * NP : nullptr, row, col, carry);
+    };
+    auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + (k & 1) * kDecBytes); };
+    auto aside = [&](int c) { return sp.aside + ((unit * p.plan.PT + w.pt) * a.nc + c) * 2048 + threadIdx.x; };
+    float ahead = 1.f;
+    auto prepare = [&](int k) {  // the state before (the gradient behind) the chunk, and the rows that enter it
+        const int c = z.chunk(k);
+        if (k == z.K) begin(1);
+        float4 h[4];
+        if (holds) {
+            if (k >= z.K) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = aside(c)[512 * i];
+            }
+            store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0, carry);
+            store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0 + 8, carry + 4);
+            if (k < z.K) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) aside(c)[512 * i] = make_float4(carry[2 * i].x, carry[2 * i].y, carry[2 * i + 1].x, carry[2 * i + 1].y);
+            }
+        }
+        if (!ws.wait(L::B_X + (k & 1), ring_phase<2>(k))) return false;
+        const Dec &d = dec(k);
+        scale_split16(base + L::OFF_X + (k & 1) * kHalf, base + L::OFF_W, row, c0, z.dir(k) ? d.to[row] : d.w[row]);
+        ahead = d.end;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_W));
+        if (k >= z.K) {
+            float s = 0.f;
+            if (holds) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s = fmaf(h[i].x, carry[2 * i].x, s);
+                    s = fmaf(h[i].y, carry[2 * i].y, s);
+                    s = fmaf(h[i].z, carry[2 * i + 1].x, s);
+                    s = fmaf(h[i].w, carry[2 * i + 1].y, s);
+                }
+            }
+            s = lanes_sum(s);
+            if (lane == 0) sp.dots[((unit * a.nc + c) * p.plan.PT + w.pt) * 16 + warp] = s;
+        }
+        return true;
+    };
+    begin(0);
+    bool ok = visits == 0 || prepare(0);
+#pragma unroll 1
+    for (int k = 0; k < visits && ok; ++k) {
+        const uint32_t ph = (uint32_t)k & 1u;
+        const float end = ahead;
+        if (!(ok = ws.wait(L::B_D, ph))) break;
+        tc_fence_after();
+        float2 v[8];
+        if (holds) {
+            load_parts16(lanes + L::D + c0, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], v[i]);
+        }
+        if (!(ok = ws.wait(L::B_Y, ph) && ws.wait(L::B_Z, ph))) break;
+        tc_fence_after();
+        load_parts16(lanes + L::Z + c0, v);
+        {
+            float2 y[8];
+            load_row16(base + L::OFF_Y, T, row, c0, y);
+            const Dec &d = dec(k);
+            const int dir = z.dir(k);
+            const float f = dir ? factor(d.s[T - 1], d.s[row]) : d.to[row];
+            sp.inter[((size_t)(dir * p.plan.PT + w.pt) * 4 + cq) * plane + (unit * a.nc + z.chunk(k)) * T + row] = f * dot16(v, y);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(ws.bar(L::B_YE));
+            mbar_arrive(ws.bar(L::B_XE + (k & 1)));
+        }
+        if (k + 1 < visits) ok = ws.wait(L::B_SE, ph) && prepare(k + 1);
+    }
+    if (visits == 0) begin(1);  // (no tokens: the gradient passes as it is)
+    if (ok && w.piece == 0 && a.d_state_in && holds) store_state(a, a.d_state_in + unit * NP, row, col, carry);
+}
+
+template <int NB>
+__device__ __forceinline__ void states_mma(const Waits &ws, uint8_t *base, uint32_t tb, int K) {
+    using L = LayStates<NB>;
+    constexpr uint32_t id = make_idesc(T, 192, false, true);
+    const uint64_t H = make_sdesc(smem_u32(base + L::OFF_H), L::HB, 1024u), W = mnmajor(base + L::OFF_W);
+    const uint64_t P = mnmajor(base + L::OFF_P), Q = kmajor(base + L::OFF_Q);
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        const uint32_t ph = (uint32_t)k & 1u;
+        if (!ws.wait(L::B_W, ph) || !ws.wait(L::B_P, ph)) break;
+        tc_fence_after();
+        mma_state(tb + L::D, P, W, false);
+        umma_commit_warp(ws.bar(L::B_D));
+        umma_commit_warp(ws.bar(L::B_PE));
+        if (!ws.wait(L::B_Q, ph)) break;
+        mma_km64(tb + L::Z, Q, H, id, false);
+        if (NB > 1) mma_km64(tb + L::Z, Q + kBlock, H + kRows64, id, true);
+        umma_commit_warp(ws.bar(L::B_Z));
+        umma_commit_warp(ws.bar(L::B_QE));
+    }
+    umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
+    mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
+    __syncwarp();
+}
+
+// One warp's stream of tiles through SLOTS slots, with barriers for landed, free and raw.
+template <int BLOCKS, int SLOTS, class First, class Issue>
+HLA_DEVICE void stream(const Waits &ws, int K, int full, int empty, int rawb, uint8_t *tiles, int len, First first, Issue issue) {
+    uint32_t raw = 0;
+    int k = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (; k < K && ok; ++k) {
+        const int s = k % SLOTS, t0 = first(k);
+        if (k >= SLOTS && !(ok = ws.wait(empty + s, ring_phase<SLOTS>(k) ^ 1u))) break;
+        const bool clear = len - t0 < T;
+        uint8_t *t = tiles + s * BLOCKS * kHalf;
+        if ((threadIdx.x & 31) == 0) issue(k, t, ws.bar(clear ? rawb : full + s));
+        __syncwarp();
+        if (clear) ok = clear_landed(ws, rawb, raw, full + s, t, BLOCKS, len - t0);
+    }
+    // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
+    if (ok)
+        for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(ws.bar(full + i % SLOTS), ring_phase<SLOTS>(i), ws.err);
+    __syncwarp();
+}
+
+template <int NB>
+__device__ __forceinline__ void states_load(const StatesParams &sp, const Waits &ws, uint8_t *base, const Walk &z, int warp) {
+    using L = LayStates<NB>;
+    const Params &p = sp.p;
+    const Args &a = p.a;
+    const Piece &w = z.w;
+    const int g = w.h / a.R, lane = threadIdx.x & 31, visits = 2 * z.K;
+    auto first = [&](int k) { return z.chunk(k) * T; };
+    uint32_t raw = 0;
+    bool ok = true;
+    if (warp == kWarpTma) {
+        stream<1, L::NX>(ws, visits, L::B_X, L::B_XE, L::B_RAWX, base + L::OFF_X, w.len, first, [&](int k, uint8_t *t, uint64_t *bar) {
+            mbar_expect_tx(bar, kHalf + kDecBytes);
+            bulk_load(base + L::OFF_DEC + (k & 1) * kDecBytes, dec_of(a, p.dec, w.b, w.h, z.chunk(k)), kDecBytes, bar);
+            load_tile<1>(t, &p.mx[z.dir(k)], p.vx[z.dir(k)], bar, 64 * w.pt, first(k), w.h, w.b);
+        });
+    } else if (warp == kWarpTmaX) {  // the rows that meet the state; the state's image leaves in between
+        int k = 0;
+#pragma unroll 1
+        for (; k < visits && ok; ++k) {
+            const int t0 = first(k), d = 1 - z.dir(k);
+            const bool clear = w.len - t0 < T;
+            if (k > 0 && !(ok = ws.wait(L::B_YE, ((uint32_t)k & 1u) ^ 1u))) break;
+            if (lane == 0) {
+                uint64_t *bar = ws.bar(clear ? L::B_RAWY : L::B_Y);
+                mbar_expect_tx(bar, kHalf);
+                load_tile<1>(base + L::OFF_Y, &p.mx[d], p.vx[d], bar, 64 * w.pt, t0, w.h, w.b);
+            }
+            __syncwarp();
+            if (clear) ok = clear_landed(ws, L::B_RAWY, raw, L::B_Y, base + L::OFF_Y, 1, w.len - t0);
+            if (!ok || !(ok = ws.wait(L::B_W, (uint32_t)k & 1u))) {
+                ++k;
+                break;
+            }
+            if (lane == 0) {
+                const size_t at = (((size_t)w.b * a.H + w.h) * p.plan.PT + w.pt) * a.nc + z.chunk(k);
+                bulk_store(sp.image[z.dir(k)] + at * L::HB, base + L::OFF_H, L::HB);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(ws.bar(L::B_SE));
+            }
+            __syncwarp();
+        }
+        if (ok && k > 0) mbar_wait(ws.bar(L::B_Y), (uint32_t)(k - 1) & 1u, ws.err);
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    } else {  // the two tiles of a chunk in turn
+        int r = 0;
+#pragma unroll 1
+        for (; r < 2 * visits && ok; ++r) {
+            const int second = r & 1, k = r >> 1, t0 = first(k), d = second ? 1 - z.dir(k) : z.dir(k), full = second ? L::B_Q : L::B_P;
+            const bool clear = w.len - t0 < T;
+            if (k > 0 && !(ok = ws.wait(second ? L::B_QE : L::B_PE, ((uint32_t)k & 1u) ^ 1u))) break;
+            uint8_t *t = base + (second ? L::OFF_Q : L::OFF_P);
+            if (lane == 0) {
+                uint64_t *bar = ws.bar(clear ? L::B_RAWB : full);
+                mbar_expect_tx(bar, NB * kHalf);
+                load_tile<NB>(t, &p.mb[d], p.vb[d], bar, 0, t0, g, w.b);
+            }
+            __syncwarp();
+            if (clear) ok = clear_landed(ws, L::B_RAWB, raw, full, t, NB, w.len - t0);
+        }
+        if (ok && visits > 0) {
+            mbar_wait(ws.bar(L::B_P), (uint32_t)(visits - 1) & 1u, ws.err);
+            mbar_wait(ws.bar(L::B_Q), (uint32_t)(visits - 1) & 1u, ws.err);
+        }
+        __syncwarp();
+    }
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kStatesThreads, 1) ssm_states_kernel(const __grid_constant__ StatesParams sp) {
+    using L = LayStates<NB>;
+    extern __shared__ __align__(1024) uint8_t base[];
+    Walk z;
+    z.w = piece_of(sp.p.a, sp.p.plan, blockIdx.x, 1);
+    if (z.w.piece >= max(z.w.used, 1)) return;
+    z.K = z.w.hi - z.w.lo;
+    Cta<L::NBAR> cta(base, L::OFF_BAR, sp.p.a.err, [](int i) { return L::arrivals(i); });
+    if (cta.warp < kElemWarps)
+        states_elem<NB>(sp, cta.ws, base, cta.tb, z);
+    else if (cta.warp == kWarpMma)
+        states_mma<NB>(cta.ws, base, uniform(cta.tb), (int)uniform(2 * z.K));
+    else
+        states_load<NB>(sp, cta.ws, base, z, cta.warp);
+    cta.finish();
+}
+
+// ------------------------------------------------------------ gradients of a chunk
 constexpr int kGradThreads = 20 * 32;
 
 struct GradParams {
@@ -31,27 +318,28 @@ struct GradParams {
     CUtensorMap mx, mdy, mb, mc, mdx;
     const Dec *dec;
     const uint8_t *h, *g;  // images
+    float *own;            // [w, vE][B][H][chunks * T]: sums of E
+    float *dd;             // [B][H][chunks]: dY.X
 };
 
 template <int NB>
 struct LayGrad {
-    static constexpr int HB = NB * kHalf / 2, NS = 3;  // dY and X of the heads in turn through three slots
+    static constexpr int HB = NB * kHalf / 2, NS = 4;  // dY and X of the heads in turn through four slots
     static constexpr int OFF_B = 0, OFF_C = NB * kHalf, OFF_S = 2 * NB * kHalf, OFF_XD = OFF_S + 2 * kHalf, OFF_H = OFF_XD + NS * kHalf,
-                         OFF_G = OFF_H + 2 * HB;
-    static constexpr int OFF_DEC = OFF_G + 2 * HB, OFF_SUM = OFF_DEC + 2 * (int)sizeof(Dec);
-    static constexpr int SUM_FLOATS = 16 * T + 32;  // [w by quadrant, vE, wz, vg][4][128], through [16], dD [16]
+                         OFF_G = OFF_H + HB;
+    static constexpr int OFF_DEC = OFF_G + HB, OFF_SUM = OFF_DEC + 2 * (int)sizeof(Dec);
+    static constexpr int SUM_FLOATS = 8 * T + 16;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], dD [16]
     static constexpr int OFF_BAR = OFF_SUM + SUM_FLOATS * 4;
     static constexpr int B_XD = 0, B_XDE = B_XD + NS, B_DEC = B_XDE + NS, B_DECE = B_DEC + 2, B_H = B_DECE + 2, B_HE = B_H + 1,
                          B_G = B_HE + 1, B_GE = B_G + 1, B_BC = B_GE + 1, B_CB = B_BC + 1, B_DYX = B_CB + 1, B_DE = B_DYX + 1,
-                         B_Z = B_DE + 1, B_GB = B_Z + 1, B_MS = B_GB + 1, B_XM = B_MS + 1, B_SE = B_XM + 1, B_YT = B_SE + 1,
-                         B_Y = B_YT + 1, B_SUM = B_Y + 2, B_SUME = B_SUM + 1, B_FIN = B_SUME + 1, B_RAW = B_FIN + 1, B_RAW2 = B_RAW + 1,
-                         NBAR = B_RAW2 + 1;
+                         B_GB = B_DE + 1, B_MS = B_GB + 1, B_XM = B_MS + 1, B_SE = B_XM + 1, B_YT = B_SE + 1, B_Y = B_YT + 1,
+                         B_SUM = B_Y + 2, B_SUME = B_SUM + 1, B_FIN = B_SUME + 1, B_RAW = B_FIN + 1, B_RAW2 = B_RAW + 1, NBAR = B_RAW2 + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
-    static constexpr uint32_t DC = 0, DB = T, DYX = 2 * T, M = 2 * T, XM = 2 * T + 64, Z = 3 * T, GB = 3 * T + 64, YT = Z, XT = Z + 32;
+    static constexpr uint32_t DC = 0, DB = T, DYX = 2 * T, M = 2 * T, XM = 2 * T + 64, YT = 3 * T, XT = YT + 32, GB = 3 * T + 64;
     HLA_DEVICE static int arrivals(int i) {
-        return (i >= B_XDE && i < B_DEC) || i == B_DECE || i == B_DECE + 1 || i == B_HE || i == B_GE ? kElemWarps + 1
-               : i == B_DE || i == B_MS || i == B_YT || i == B_Y || i == B_Y + 1 || i == B_SUM                    ? kElemWarps
-                                                                                                   : 1;
+        return (i >= B_XDE && i < B_DEC) || i == B_DECE || i == B_DECE + 1                                 ? kElemWarps + 1
+               : i == B_DE || i == B_MS || i == B_YT || i == B_Y || i == B_Y + 1 || i == B_SUM ? kElemWarps
+                                                                                               : 1;
     }
 };
 
@@ -59,8 +347,6 @@ struct Job {  // one chunk of a group, the heads [h0, h1), U = heads x column ti
     int b, g, c, len, t0, live, split, h0, U;
 };
 HLA_DEVICE int head_of(const GradParams &p, const Job &j, int u) { return j.h0 + u / p.PT; }
-
-HLA_DEVICE void quad_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
 
 // Sums over the warp's lanes of 16 columns: lane l < 16 (and l + 16) ends with column l.
 HLA_DEVICE float lane_sums16(float (&v)[16]) {
@@ -76,17 +362,6 @@ HLA_DEVICE float lane_sums16(float (&v)[16]) {
     }
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
-HLA_DEVICE float dot16(const float2 (&x)[8], const float2 (&y)[8]) {
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fma2(x[i], y[i], s);
-    return s.x + s.y;
-}
-HLA_DEVICE void load_row16(const uint8_t *tile, int rows, int r, int c0, float2 (&v)[8]) {
-    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(rows, r, c0)), v);
-    unpack8(*reinterpret_cast<const uint4 *>(tile + tile_off(rows, r, c0 + 8)), v + 4);
-}
-
 template <int NB>
 __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, uint8_t *base, uint32_t tb, const Job &job) {
     using L = LayGrad<NB>;
@@ -94,7 +369,7 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, cq = warp >> 2, row = 32 * q + lane, c0 = 16 * cq;
     const uint32_t lanes = tb + ((uint32_t)(32 * q) << 16);
     float *sums = reinterpret_cast<float *>(base + L::OFF_SUM);
-    float *sum_w = sums + q * T + 32 * cq, *sum_ve = sums + 4 * T + cq * T, *sum_wz = sums + 8 * T + cq * T, *sum_vg = sums + 12 * T + cq * T;
+    float *sum_w = sums + q * T + 32 * cq, *sum_ve = sums + 4 * T + cq * T;
     const bool active = cq >= q;  // tokens t of this warp's columns at or behind its rows j
     float2 cb[16];
     bool ok = ws.wait(L::B_CB, 0u);
@@ -175,80 +450,43 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ws.bar(L::B_MS));
-        // w from the state before the chunk; <g, h>
-        ok = ok && ws.wait(L::B_XD + sy, ring_phase<L::NS>(2 * u)) && ws.wait(L::B_XD + sx, ring_phase<L::NS>(2 * u + 1)) &&
-             ws.wait(L::B_H, ph) && ws.wait(L::B_G, ph);
+        // the weighted rows of dY and X, for the states' shares of dC and dB
+        ok = ok && ws.wait(L::B_XD + sy, ring_phase<L::NS>(2 * u)) && ws.wait(L::B_XD + sx, ring_phase<L::NS>(2 * u + 1));
+        if (u > 0) ok = ok && ws.wait(L::B_HE, ph ^ 1u);  // the last head's have been used
         float2 yr[8], xr[8];
         load_row16(dy, T, row, c0, yr);
         load_row16(x, T, row, c0, xr);
-        float through = 0.f;
-        if (q < 2 * NB) {
-            float2 h1[8], h2[8], g1[8], g2[8];
-            load_row16(base + L::OFF_H, 64 * NB, row, c0, h1);
-            load_row16(base + L::OFF_H + L::HB, 64 * NB, row, c0, h2);
-            load_row16(base + L::OFF_G, 64 * NB, row, c0, g1);
-            load_row16(base + L::OFF_G + L::HB, 64 * NB, row, c0, g2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h1[i] = add2(h1[i], h2[i]);
-                g1[i] = add2(g1[i], g2[i]);
-            }
-            through = dot16(h1, g1);
-        }
-        float dd = dot16(xr, yr);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            through += __shfl_xor_sync(0xffffffffu, through, o);
-            dd += __shfl_xor_sync(0xffffffffu, dd, o);
-        }
-        if (lane == 0) {
-            sums[16 * T + warp] = through;
-            sums[16 * T + 16 + warp] = dd;
-            mbar_arrive(ws.bar(L::B_HE));
-            mbar_arrive(ws.bar(L::B_GE));
-        }
-        ok = ok && ws.wait(L::B_Z, ph);
-        tc_fence_after();
-        float2 v[8];
-        tmem_pairs16(lanes + L::Z + c0, v);
-        tmem_wait_ld();
-        sum_wz[row] = dot16(v, yr);
-        quad_sync(q);  // the weighted rows go over Z
-        tc_fence_after();
+        const float2 to = both(d.to[row]), w = both(d.w[row]), D = both(a.D ? a.D[h] : 0.f);
         {
-            const float2 to = both(d.to[row]), w = both(d.w[row]);
             float ty[8], tx[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 ty[i] = __uint_as_float(pack2(mul2(yr[i], to)));
                 tx[i] = __uint_as_float(pack2(mul2(xr[i], w)));
             }
+            tc_fence_after();
             tmem_st8(lanes + L::YT + 8 * cq, ty);
             tmem_st8(lanes + L::XT + 8 * cq, tx);
-            tmem_wait_st();
         }
+        const float dd = lanes_sum(dot16(xr, yr));
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
+            sums[8 * T + warp] = dd;
             mbar_arrive(ws.bar(L::B_YT));
             mbar_arrive(ws.bar(L::B_XDE + sy));
-        }
-        // v from the gradient behind the chunk; dX
-        ok = ok && ws.wait(L::B_GB, ph);
-        tc_fence_after();
-        tmem_pairs16(lanes + L::GB + c0, v);
-        tmem_wait_ld();
-        sum_vg[row] = dot16(v, xr);
-        {
-            const float2 D = both(a.D ? a.D[h] : 0.f), w = both(d.w[row]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) yr[i] = fma2(D, yr[i], mul2(w, v[i]));
-        }
-        __syncwarp();
-        if (lane == 0) {
             mbar_arrive(ws.bar(L::B_SUM));
             mbar_arrive(ws.bar(L::B_DECE + (u & 1)));
         }
+        // dX = M^T dY (with dt) + w B g + D dY, over X
+        ok = ok && ws.wait(L::B_GB, ph);
+        tc_fence_after();
+        float2 v[8];
+        tmem_pairs16(lanes + L::GB + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) yr[i] = fma2(D, yr[i], mul2(w, v[i]));
         ok = ok && ws.wait(L::B_XM, ph);
         tc_fence_after();
         tmem_pairs16(lanes + L::XM + c0, v);
@@ -306,15 +544,7 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
                        id_nn = make_idesc(T, 64 * NB, true, true), id_k = make_idesc(T, 64 * NB, false, false);
     const uint64_t Bk = kmajor(base + L::OFF_B), Ck = kmajor(base + L::OFF_C), Bm = mnmajor(base + L::OFF_B), Cm = mnmajor(base + L::OFF_C);
     const uint64_t Sk = kmajor(base + L::OFF_S), Sm = mnmajor(base + L::OFF_S);
-    // both parts of an image: rows n by columns p, contracted over rows or over columns
-    const uint64_t Hm = make_sdesc(smem_u32(base + L::OFF_H), 64 * NB * 128u, 1024u), Gm = make_sdesc(smem_u32(base + L::OFF_G), 64 * NB * 128u, 1024u);
-    const uint64_t Hk = kmajor(base + L::OFF_H), Gk = kmajor(base + L::OFF_G);
-    auto by_state = [&](uint32_t d, uint64_t rows, uint64_t image) {  // [128 x 64] = rows (hi + lo)
-        mma_km64(d, rows, image, id_y, false);
-        if (NB > 1) mma_km64(d, rows + kBlock, image + kRows64, id_y, true);
-        mma_km64(d, rows, image + (L::HB >> 4), id_y, true);
-        if (NB > 1) mma_km64(d, rows + kBlock, image + (L::HB >> 4) + kRows64, id_y, true);
-    };
+    const uint64_t Gm = make_sdesc(smem_u32(base + L::OFF_G), L::HB, 1024u), Hk = kmajor(base + L::OFF_H), Gk = kmajor(base + L::OFF_G);
     bool ok = ws.wait(L::B_BC, 0u);
     if (ok) {
         mma_ss64(tb + L::DYX, Bk, Ck, id_tt, false);
@@ -330,11 +560,9 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         tc_fence_after();
         mma_ss64(tb + L::DYX, kmajor(x), kmajor(dy), id_tt, false);
         umma_commit_warp(ws.bar(L::B_DYX));
-        if (!(ok = ws.wait(L::B_H, ph))) break;
-        by_state(tb + L::Z, Ck, Hm);
-        umma_commit_warp(ws.bar(L::B_Z));
         if (!(ok = ws.wait(L::B_G, ph))) break;
-        by_state(tb + L::GB, Bk, Gm);
+        mma_km64(tb + L::GB, Bk, Gm, id_y, false);
+        if (NB > 1) mma_km64(tb + L::GB, Bk + kBlock, Gm + kRows64, id_y, true);
         umma_commit_warp(ws.bar(L::B_GB));
         if (!(ok = ws.wait(L::B_MS, ph))) break;
         tc_fence_after();
@@ -345,12 +573,10 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         mma_km64(tb + L::DB, Sk, Cm, id_n, u > 0);   // S^T C
         mma_km64(tb + L::DB, Sk + kBlock, Cm + kRows64, id_n, true);
         umma_commit_warp(ws.bar(L::B_SE));
-        if (!(ok = ws.wait(L::B_YT, ph))) break;
+        if (!(ok = ws.wait(L::B_YT, ph) && ws.wait(L::B_H, ph))) break;
         tc_fence_after();
-        mma_tk64(tb + L::DC, tb + L::YT, Hk, id_k);  // both parts: the weighted rows are then the only rounding
-        mma_tk64(tb + L::DC, tb + L::YT, Hk + (L::HB >> 4), id_k);
+        mma_tk64(tb + L::DC, tb + L::YT, Hk, id_k);
         mma_tk64(tb + L::DB, tb + L::XT, Gk, id_k);
-        mma_tk64(tb + L::DB, tb + L::XT, Gk + (L::HB >> 4), id_k);
         umma_commit_warp(ws.bar(L::B_HE));
         umma_commit_warp(ws.bar(L::B_GE));
         umma_commit_warp(ws.bar(L::B_XDE + sy));
@@ -421,14 +647,14 @@ __device__ __forceinline__ void grad_load_state(const GradParams &p, const Waits
         const size_t at = (((size_t)job.b * p.a.H + head_of(p, job, u)) * p.PT + u % p.PT) * p.a.nc + job.c;
         if (u > 0 && !(ok = ws.wait(L::B_HE, ph ^ 1u))) break;
         if (lane == 0) {
-            mbar_expect_tx(ws.bar(L::B_H), 2 * L::HB);
-            bulk_load(base + L::OFF_H, p.h + at * 2 * L::HB, 2 * L::HB, ws.bar(L::B_H));
+            mbar_expect_tx(ws.bar(L::B_H), L::HB);
+            bulk_load(base + L::OFF_H, p.h + at * L::HB, L::HB, ws.bar(L::B_H));
         }
         __syncwarp();
         if (u > 0 && !(ok = ws.wait(L::B_GE, ph ^ 1u))) break;
         if (lane == 0) {
-            mbar_expect_tx(ws.bar(L::B_G), 2 * L::HB);
-            bulk_load(base + L::OFF_G, p.g + at * 2 * L::HB, 2 * L::HB, ws.bar(L::B_G));
+            mbar_expect_tx(ws.bar(L::B_G), L::HB);
+            bulk_load(base + L::OFF_G, p.g + at * L::HB, L::HB, ws.bar(L::B_G));
         }
         __syncwarp();
     }
@@ -440,122 +666,45 @@ __device__ __forceinline__ void grad_load_state(const GradParams &p, const Waits
     __syncwarp();
 }
 
-// dX of each head's columns to memory; then, after a head's last columns, the gradients of its
-// steps from the sums: four adjacent tokens a lane.
+// dX of each head's columns to memory; after a head's last columns the sums of E, four adjacent
+// tokens a lane.
 template <int NB>
 __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, uint8_t *base, const Job &job) {
     using L = LayGrad<NB>;
     const Args &a = p.a;
     const int lane = threadIdx.x & 31;
     const float *sums = reinterpret_cast<const float *>(base + L::OFF_SUM);
-    float w[4], ve[4], vg[4], through = 0.f, dd = 0.f;
+    float4 w, ve;
+    float dd = 0.f;
 #pragma unroll 1
     for (int u = 0; u < job.U; ++u) {
         const uint32_t ph = (uint32_t)u & 1u;
         const int h = head_of(p, job, u), pt = u % p.PT, sx = (2 * u + 1) % L::NS;
-        const Dec &d = *reinterpret_cast<const Dec *>(base + L::OFF_DEC + (u & 1) * sizeof(Dec));
         if (!ws.wait(L::B_DEC + (u & 1), ring_phase<2>(u)) || !ws.wait(L::B_SUM, ph)) break;
         if (pt == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ve[i] = vg[i] = 0.f;
-            through = dd = 0.f;
+            w = ve = make_float4(0.f, 0.f, 0.f, 0.f);
+            dd = 0.f;
         }
-        const Decay end = d.s[T - 1];
-        Decay s[4];
-        float dt[4], sl[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * lane + i;
-            s[i] = d.s[t];
-            dt[i] = d.dt[t];
-            sl[i] = d.slope[t];
-            float x = 0.f, y = 0.f, z = 0.f, g = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x += sums[k * T + t];
-                y += sums[4 * T + k * T + t];
-                z += sums[8 * T + k * T + t];
-                g += sums[12 * T + k * T + t];
-            }
-            w[i] += fmaf(d.to[t], z, x);
-            ve[i] += y;
-            vg[i] = fmaf(factor(end, s[i]), g, vg[i]);
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(sums + k * T + 4 * lane), y = *reinterpret_cast<const float4 *>(sums + (4 + k) * T + 4 * lane);
+            w.x += x.x; w.y += x.y; w.z += x.z; w.w += x.w;
+            ve.x += y.x; ve.y += y.y; ve.z += y.z; ve.w += y.w;
         }
-        float th = lane < 16 ? sums[16 * T + lane] : 0.f, dx = lane < 16 ? sums[16 * T + 16 + lane] : 0.f;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            th += __shfl_xor_sync(0xffffffffu, th, o);
-            dx += __shfl_xor_sync(0xffffffffu, dx, o);
-        }
-        through = fmaf(d.end, th, through);
-        dd += dx;
+        dd += lanes_sum(lane < 16 ? sums[8 * T + lane] : 0.f);
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(ws.bar(L::B_SUME));
             mbar_arrive(ws.bar(L::B_DECE + (u & 1)));
         }
         if (pt == p.PT - 1) {
-            float suf[4], pre[4], s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int i = 3; i >= 0; --i) {
-                s1 += fmaf(-dt[i], ve[i], w[i]);
-                suf[i] = s1;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                pre[i] = s2;
-                s2 = fmaf(dt[i], vg[i], s2);
-            }
-            float xs = s1, xp = s2;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
-                if (lane + o < 32) xs += us;
-                if (lane >= o) xp += up;
-            }
-            xs -= s1;
-            xp -= s2;
-            through = __shfl_sync(0xffffffffu, through, 0);
-            const float A = a.A[h];
-            float sA = 0.f, sb = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * lane + i;
-                const float da = through + (suf[i] + xs) + (pre[i] + xp), g = fmaf(A, da, ve[i] + vg[i]) * sl[i];
-                if (t < job.live) {
-                    static_cast<__nv_bfloat16 *>(a.ddt.p)[(size_t)job.b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)(job.t0 + t) * a.ddt.st] = __float2bfloat16_rn(g);
-                    sA = fmaf(da, dt[i], sA);
-                    sb += g;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                sA += __shfl_xor_sync(0xffffffffu, sA, o);
-                sb += __shfl_xor_sync(0xffffffffu, sb, o);
-            }
-            if (lane == 0) {
-                float *out = a.sums + ((size_t)job.b * a.nc + job.c) * 3 * a.H + h;
-                out[0] = sA;
-                out[a.H] = dd;
-                out[2 * a.H] = sb;
-            }
+            const size_t at = ((size_t)job.b * a.H + h) * a.nc + job.c, plane = (size_t)a.B * a.H * a.nc * T;
+            reinterpret_cast<float4 *>(p.own + at * T)[lane] = w;
+            reinterpret_cast<float4 *>(p.own + plane + at * T)[lane] = ve;
+            if (lane == 0) p.dd[at] = dd;
         }
         if (!ws.wait(L::B_Y + (u & 1), ring_phase<2>(u))) break;
-        const uint8_t *x = base + L::OFF_XD + sx * kHalf;
-        if (job.live == T) {
-            if (lane == 0) {
-                tma_store_4d(x, &p.mdx, 64 * pt, job.t0, a.dx.sh ? h : 0, a.dx.sb ? job.b : 0);
-                bulk_commit();
-                bulk_wait_read();
-            }
-        } else {  // rows behind the sequence stay as they are
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dx.p) + (size_t)job.b * a.dx.sb + (size_t)h * a.dx.sh + (size_t)job.t0 * a.dx.st;
-            for (int i = lane; i < job.live * 8; i += 32) {
-                const int r = i >> 3, cc = 64 * pt + 8 * (i & 7);
-                if (cc < a.P) *reinterpret_cast<uint4 *>(out + (size_t)r * a.dx.st + cc) = *reinterpret_cast<const uint4 *>(x + tile_off(T, r, 8 * (i & 7)));
-            }
-        }
-        __syncwarp();
+        store_tile(base + L::OFF_XD + sx * kHalf, &p.mdx, a.dx, pt, job.t0, job.live, h, job.b, a.P);
         if (lane == 0) mbar_arrive(ws.bar(L::B_XDE + sx));
     }
     if (lane == 0) bulk_wait_all();
@@ -578,11 +727,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_grad_tc_kernel(const __gr
     j.h0 = j.g * a.R + (int)((long long)a.R * j.split / p.splits);
     const int h1 = j.g * a.R + (int)((long long)a.R * (j.split + 1) / p.splits);
     j.U = (h1 - j.h0) * p.PT;
-    if (j.live <= 0) {
-        float *out = a.sums + ((size_t)j.b * a.nc + j.c) * 3 * a.H;
-        for (int h = j.h0 + threadIdx.x; h < h1; h += kGradThreads) out[h] = out[a.H + h] = out[2 * a.H + h] = 0.f;
-        return;
-    }
+    if (j.live <= 0) return;
     Cta<L::NBAR> cta(base, L::OFF_BAR, a.err, [](int i) { return L::arrivals(i); });
     if (cta.warp < kElemWarps)
         grad_elem<NB>(p, cta.ws, base, cta.tb, j);
@@ -597,16 +742,115 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_grad_tc_kernel(const __gr
     cta.finish();
 }
 
+// ------------------------------------------------------------ gradients of the steps
+// A warp for a chunk of a head; a CTA's chunks are those of one piece.
+constexpr int kFinishWarps = 8;
+__global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __grid_constant__ StatesParams sp, const float *own, const float *dd) {
+    __shared__ float part[3][kFinishWarps];
+    const Params &p = sp.p;
+    const Args &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int piece = blockIdx.x % p.plan.pieces, h = blockIdx.x / p.plan.pieces % a.H, b = blockIdx.x / p.plan.pieces / a.H;
+    const int len = clamp_length(a.lengths, b, a.n), chunks = (len + T - 1) / T, PT = p.plan.PT;
+    const int lo = min(piece * p.plan.per, chunks), hi = min(lo + p.plan.per, chunks);
+    const size_t unit = (size_t)b * a.H + h, plane = (size_t)a.B * a.H * a.nc * T;
+    float sA = 0.f, sD = 0.f, sb = 0.f;
+    const float A = a.A[h];
+#pragma unroll 1
+    for (int c = lo + warp; c < hi; c += kFinishWarps) {
+        const Dec &d = *dec_of(a, p.dec, b, h, c);
+        const size_t at = unit * a.nc + c;
+        float w[4], vi[4], vo[4], dt[4], sl[4];  // four adjacent tokens
+        auto read = [&](const float *q, float (&v)[4]) {
+            const float4 x = reinterpret_cast<const float4 *>(q)[lane];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        };
+        read(own + at * T, w);
+        read(own + plane + at * T, vo);
+        read(d.dt, dt);
+        read(d.slope, sl);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vi[i] = 0.f;
+        float th = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < PT; ++k) {
+            if (lane < 16) th += sp.dots[(at * PT + k) * 16 + lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x[4], y[4];
+                read(sp.inter + (size_t)(k * 4 + j) * plane + at * T, x);
+                read(sp.inter + (size_t)((PT + k) * 4 + j) * plane + at * T, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] += x[i];
+                    vi[i] += y[i];
+                }
+            }
+        }
+        th = lanes_sum(th) * d.end;
+        float suf[4], pre[4], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            s1 += fmaf(-dt[i], vo[i], w[i]);
+            suf[i] = s1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            pre[i] = s2;
+            s2 = fmaf(dt[i], vi[i], s2);
+        }
+        float xs = s1, xp = s2;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
+            if (lane + o < 32) xs += us;
+            if (lane >= o) xp += up;
+        }
+        xs -= s1;
+        xp -= s2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = c * T + 4 * lane + i;
+            const float da = th + (suf[i] + xs) + (pre[i] + xp), g = fmaf(A, da, vo[i] + vi[i]) * sl[i];
+            if (t < len) {
+                static_cast<__nv_bfloat16 *>(a.ddt.p)[(size_t)b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)t * a.ddt.st] = __float2bfloat16_rn(g);
+                sA = fmaf(da, dt[i], sA);
+                sb += g;
+            }
+        }
+        if (lane == 0) sD += dd[at];
+    }
+    sA = lanes_sum(sA);
+    sb = lanes_sum(sb);
+    if (lane == 0) {
+        part[0][warp] = sA;
+        part[1][warp] = sD;
+        part[2][warp] = sb;
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFinishWarps; ++i) s += part[threadIdx.x][i];
+        a.sums[((size_t)b * p.plan.pieces + piece) * 3 * a.H + threadIdx.x * a.H + h] = s;
+    }
+}
+
 template <int NB>
-cudaError_t launch(const Params &p, const GradParams &g, cudaStream_t st) {
+cudaError_t launch(const StatesParams &sp, const GradParams &g, cudaStream_t st) {
+    using S = LayStates<NB>;
     using L = LayGrad<NB>;
-    static_assert(L::SMEM <= 227 * 1024, "shared memory");
-    cudaError_t e = starts<NB>(p, 2, st);
-    if (e == cudaSuccess) e = walk<NB, false>(p, st);
+    static_assert(S::SMEM <= 227 * 1024 && L::SMEM <= 227 * 1024, "shared memory");
+    const Args &a = sp.p.a;
+    cudaError_t e = starts<NB>(sp.p, 2, st);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_states_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_grad_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    const Args &a = p.a;
+    ssm_states_kernel<NB><<<(unsigned)((size_t)a.B * a.H * sp.p.plan.PT * sp.p.plan.pieces), kStatesThreads, S::SMEM, st>>>(sp);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ssm_grad_tc_kernel<NB><<<(unsigned)((size_t)a.B * a.nc * a.G * g.splits), kGradThreads, L::SMEM, st>>>(g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ssm_finish_kernel<<<(unsigned)((size_t)a.B * a.H * sp.p.plan.pieces), kFinishWarps * 32, 0, st>>>(sp, g.own, g.dd);
     return cudaGetLastError();
 }
 
@@ -629,10 +873,11 @@ int tc_splits(const Args &a) {
 }
 
 cudaError_t tc_backward(const Args &a, cudaStream_t st) {
-    Params p;
+    StatesParams sp;
     GradParams g;
-    memset(&p, 0, sizeof p);
+    memset(&sp, 0, sizeof sp);
     memset(&g, 0, sizeof g);
+    Params &p = sp.p;
     p.a = a;
     cudaError_t e = dev_status_ptr(&p.a.err);
     if (e != cudaSuccess) return e;
@@ -642,20 +887,25 @@ cudaError_t tc_backward(const Args &a, cudaStream_t st) {
     p.pieces[0] = a.h; p.pieces[1] = a.g;
     p.factor = a.factor;
     p.dec = static_cast<const Dec *>(a.dec);
-    p.image[0] = a.image[0]; p.image[1] = a.image[1];
+    sp.image[0] = a.image[0]; sp.image[1] = a.image[1];
+    sp.inter = a.inter;
+    sp.aside = reinterpret_cast<float4 *>(a.aside);
+    sp.dots = a.dots;
     g.a = p.a;
     g.PT = p.plan.PT;
     g.splits = a.splits;
     g.vx = a.x; g.vdy = a.dy; g.vb = a.b; g.vc = a.c;
     g.dec = p.dec;
     g.h = a.image[0]; g.g = a.image[1];
+    g.own = a.own;
+    g.dd = a.dd;
     if (!encode(&p.mx[0], a.x, a.P, a.n, a.H, a.B, T) || !encode(&p.mx[1], a.dy, a.P, a.n, a.H, a.B, T) ||
         !encode(&p.mb[0], a.b, a.N, a.n, a.G, a.B, T) || !encode(&p.mb[1], a.c, a.N, a.n, a.G, a.B, T) ||
         !encode(&g.mdx, a.dx, a.P, a.n, a.H, a.B, T))
         return cudaErrorNotSupported;
     g.mx = p.mx[0]; g.mdy = p.mx[1]; g.mb = p.mb[0]; g.mc = p.mb[1];
-    e = a.N <= 64 ? launch<1>(p, g, st) : launch<2>(p, g, st);
-    return e == cudaSuccess ? join(a, HLA_BF16, a.splits > 1, st) : e;
+    e = a.N <= 64 ? launch<1>(sp, g, st) : launch<2>(sp, g, st);
+    return e == cudaSuccess ? join(a, HLA_BF16, a.splits > 1, a.B * p.plan.pieces, st) : e;
 }
 
 }  // namespace ssm

@@ -3,13 +3,16 @@
 // A head's chunks are cut into pieces.  sum_kernel forms what a piece adds to the state (one
 // accumulator in TMEM over the whole piece: every token weighs by its decay to the piece's end, so
 // nothing is rescaled), scan_kernel turns the sums into the states at the pieces' starts, and
-// carry_kernel walks each piece's chunks from its start: state' = 2^s_end state + B^T (w X), the
-// weighted rows w X in two bf16 parts, so that the state carries fp32 (2^-17 of each term).  Tokens
-// are then read twice, states only at the pieces' ends, and no CTA waits for another.
-//   Backward the same kernels run from the last chunk to the first on C and dY.
+// carry_kernel walks each piece's chunks from its start: state' = 2^s_end state + B^T (w X).  Tokens
+// are read twice, states only at the pieces' ends, and no CTA waits for another.  Backward the sums
+// also run from the last chunk to the first on C and dY.
 //
-// The weighted rows' two parts are one operand of 128 columns (each row of B is read once for
-// both); their sums are added when they are read.
+// The weighted rows w X enter as three bf16 parts whose sum is the fp32 product (with two, states
+// were 2.4e-6 off): one operand of 192 columns, so that each row of B is read once for all; the
+// parts' sums are added when they are read.
+//
+// Roles of a CTA: 16 elementwise warps, in which a thread has one row (a token, or a row of the
+// state) and a quarter of its columns; one MMA warp; TMA warps, one for each stream of tiles.
 #pragma once
 #include "hla_ssm_tc.cuh"
 
@@ -25,7 +28,6 @@ struct Params {
     float *pieces[2];         // [B][H][pieces][N][P]: sums, then start states
     float *factor;            // [B][H][pieces]: decay over a piece
     const Dec *dec;           // [B][H][chunks]
-    uint8_t *image[2];        // STATES: [B][H][PT][chunks][hi, lo][NB * 64 rows][64] tile images
 };
 
 HLA_DEVICE float *piece_state(const Params &p, int dir, const Piece &w) {
@@ -48,18 +50,19 @@ HLA_DEVICE void store_state(const Args &a, float *s, int n, int c0, const float2
             s[(size_t)n * a.P + c0 + 2 * i + 1] = v[i].y;
         }
 }
-// Columns [c, c + 16) of both parts' sums, added.
+// Columns [c, c + 16) of the three parts' sums, added.
 HLA_DEVICE void load_parts16(uint32_t taddr, float2 (&v)[8]) {
-    float2 lo[8];
+    float2 m[8], l[8];
     tmem_pairs16(taddr, v);
-    tmem_pairs16(taddr + 64, lo);
+    tmem_pairs16(taddr + 64, m);
+    tmem_pairs16(taddr + 128, l);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = add2(v[i], lo[i]);
+    for (int i = 0; i < 8; ++i) v[i] = add2(v[i], add2(m[i], l[i]));
 }
-// D [128 x 128] (+)= B^T (hi | lo) over a chunk's 128 tokens.
+// D [128 x 192] (+)= B^T (parts) over a chunk's 128 tokens.
 HLA_DEVICE void mma_state(uint32_t d, uint64_t b, uint64_t w, bool acc) {
-    constexpr uint32_t id = make_idesc(T, T, true, true);
+    constexpr uint32_t id = make_idesc(T, 192, true, true);
     mma_mm64(d, b, w, id, acc);
     mma_mm64(d, b + kRows64, w + kRows64, id, true);
 }
@@ -82,8 +85,8 @@ HLA_DEVICE bool clear_landed(const Waits &ws, int raw, uint32_t &phase, int bar,
 constexpr int kSumThreads = 19 * 32;
 template <int NB>
 struct LaySum {
-    static constexpr int NX = 3, NR = 3;  // stages of X and its weights, of B
-    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_DEC = OFF_W + 2 * 2 * kHalf;
+    static constexpr int NX = 3, NR = 2;  // stages of X and its weights, of B
+    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_DEC = OFF_W + 2 * 3 * kHalf;
     static constexpr int OFF_BAR = OFF_DEC + NX * kDecBytes;
     static constexpr int B_X = 0, B_XE = B_X + NX, B_R = B_XE + NX, B_RE = B_R + NR, B_W = B_RE + NR, B_WE = B_W + 2, B_OUT = B_WE + 2,
                          B_FIN = B_OUT + 1, B_RAW = B_FIN + 1, B_RAWX = B_RAW + 1, NBAR = B_RAWX + 1;
@@ -108,15 +111,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
     if (warp == kWarpTma || warp == kWarpTmaX) {  // B; X and its weights: neither waits for the other's slots
         const bool is_x = warp == kWarpTmaX;
         const int loads = is_x ? steps : K, NS = is_x ? L::NX : L::NR, full = is_x ? L::B_X : L::B_R, empty = is_x ? L::B_XE : L::B_RE;
-        static_assert(L::NX == L::NR, "phases are counted alike");
         uint32_t raw = 0;
         int i = 0;
         bool ok = true;
 #pragma unroll 1
         for (; i < loads && ok; ++i) {
-            const int s = i % L::NX, c = chunk(is_x ? i / HB : i), t0 = c * T, h = w.h + (is_x ? i % HB : 0);
+            const int s = i % NS, c = chunk(is_x ? i / HB : i), t0 = c * T, h = w.h + (is_x ? i % HB : 0);
             const bool clear = w.len - t0 < T;
-            if (i >= NS && !(ok = ws.wait(empty + s, ring_phase<L::NX>(i) ^ 1u))) break;
+            if (i >= NS && !(ok = ws.wait(empty + s, ((uint32_t)(i / NS) & 1u) ^ 1u))) break;
             uint8_t *t = base + (is_x ? L::OFF_X + s * kHalf : L::OFF_R + s * NB * kHalf);
             if (lane == 0) {
                 uint64_t *bar = ws.bar(!clear ? full + s : is_x ? L::B_RAWX : L::B_RAW);
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
         }
         // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
         if (ok)
-            for (int e = max(0, i - NS); e < i; ++e) mbar_wait(ws.bar(full + e % L::NX), ring_phase<L::NX>(e), a.err);
+            for (int e = max(0, i - NS); e < i; ++e) mbar_wait(ws.bar(full + e % NS), (uint32_t)(e / NS) & 1u, a.err);
         __syncwarp();
     } else if (warp == kWarpMma) {
         const uint32_t tb = uniform(cta.tb);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
             const int k = i / HB, j = i % HB, rs = k % L::NR;
             if (!(ok = ws.wait(L::B_R + rs, ring_phase<L::NR>(k)) && ws.wait(L::B_W + (i & 1), (uint32_t)(i >> 1) & 1u))) break;
             tc_fence_after();
-            mma_state(tb + j * T, mnmajor(base + L::OFF_R + rs * NB * kHalf), mnmajor(base + L::OFF_W + (i & 1) * 2 * kHalf), k > 0);
+            mma_state(tb + j * 192, mnmajor(base + L::OFF_R + rs * NB * kHalf), mnmajor(base + L::OFF_W + (i & 1) * 3 * kHalf), k > 0);
             umma_commit_warp(ws.bar(L::B_WE + (i & 1)));
             if (j == HB - 1) umma_commit_warp(ws.bar(L::B_RE + rs));
         }
@@ -170,8 +172,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
                     f *= off[j];
                     off[j] *= d.end;
                 }
-            uint8_t *hi = base + L::OFF_W + e * 2 * kHalf;
-            scale_split16(base + L::OFF_X + s * kHalf, hi, hi + kHalf, row, 16 * cq, f);
+            scale_split16(base + L::OFF_X + s * kHalf, base + L::OFF_W + e * 3 * kHalf, row, 16 * cq, f);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
 #pragma unroll
                 for (int j = 0; j < HB; ++j) {
                     float2 v[8];
-                    load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + j * T + 16 * cq, v);
+                    load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + j * 192 + 16 * cq, v);
                     Piece u = w;
                     u.h += j;
                     store_state(a, piece_state(p, dir, u), row, 64 * w.pt + 16 * cq, v);
@@ -232,154 +233,128 @@ static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid
 }
 
 // ------------------------------------------------------------ walk along a piece
-// OUT (forward): the outputs; otherwise (backward, both directions): the state at each chunk as a
-// pair of bf16 tile images.  Roles (20 warps): 0-15 elementwise, 16 MMA, 17 TMA loads of B and C, 18 of X, 19 stores.
-// The elementwise warps take a chunk's steps in an order that leaves the tensor cores a step's time
-// for each product: M of chunk k; state behind k, and its bf16 rows; weighted rows of k + 1; y of k.
+// The outputs of the forward.  The elementwise warps take a chunk's steps in an order that leaves
+// the tensor cores a step's time for each product: M of chunk k; state behind k, and its bf16 rows;
+// weighted rows of k + 1; y of k, which leaves by TMA from x's own tile.  (All steps one after the
+// other took 4,500 cycles a chunk, two groups of warps at once 4,300, this order 3,300.)
 constexpr int kCarryThreads = 20 * 32;
 constexpr float kBlockRange = 60.f;  // log2 of the decay over 32 tokens up to which both halves of a factor are plain numbers
-template <int NB, bool OUT>
+template <int NB>
 struct LayCarry {
-    static constexpr int EACH = OUT ? 2 : 1;           // ring tiles of a chunk: C and B, or one
-    static constexpr int NX = OUT ? 3 : 2, NR = OUT ? 3 : 2, NW = OUT ? 1 : 2;
-    static constexpr int HB = NB * kHalf / 2;          // a state's bf16 rows: 64 NB of them
-    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_H = OFF_W + NW * 2 * kHalf;
-    static constexpr int OFF_DEC = OFF_H + (OUT ? HB : 2 * HB);  // OUT: the state; otherwise its two parts on their way out
+    static constexpr int NX = 3, NR = 3;       // stages of X, ring of C and B tiles in turn
+    static constexpr int HB = NB * kHalf / 2;  // a state's bf16 rows: 64 NB of them
+    static constexpr int OFF_X = 0, OFF_R = NX * kHalf, OFF_W = OFF_R + NR * NB * kHalf, OFF_H = OFF_W + 3 * kHalf, OFF_DEC = OFF_H + HB;
     static constexpr int OFF_BAR = OFF_DEC + NX * kDecBytes;
-    static constexpr int B_X = 0, B_XE = B_X + NX, B_R = B_XE + NX, B_RE = B_R + NR, B_W = B_RE + NR, B_D = B_W + 2, B_A2 = B_D + 2,
-                         B_Y = B_A2 + 1, B_YE = B_Y + NX, B_CB = B_YE + 1, B_M = B_CB + 1, B_A1 = B_M + 1, B_H = B_A1 + 1,
-                         B_FIN = B_H + 1, B_RAW = B_FIN + 1, B_RAWX = B_RAW + 1, NBAR = B_RAWX + 1;
+    static constexpr int B_X = 0, B_XE = B_X + NX, B_R = B_XE + NX, B_RE = B_R + NR, B_W = B_RE + NR, B_D = B_W + 1, B_A2 = B_D + 1,
+                         B_Y = B_A2 + 1, B_CB = B_Y + NX, B_M = B_CB + 1, B_A1 = B_M + 1, B_FIN = B_A1 + 1, B_RAW = B_FIN + 1,
+                         B_RAWX = B_RAW + 1, NBAR = B_RAWX + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
-    static constexpr uint32_t CB = 0, M = T, A1 = T + 64, D = 2 * T, A2 = 3 * T;  // TMEM columns (D twice, or A2 twice)
-    HLA_DEVICE static int arrivals(int i) {
-        return (!OUT && i >= B_XE && i < B_R) || i == B_W || i == B_W + 1 || (i >= B_Y && i < B_YE) || i == B_M || i == B_H ? kElemWarps : 1;
-    }
-};
-struct Walk {  // the chunks of a piece in the order they are taken
-    Piece w;
-    int dir, K;
-    HLA_DEVICE int chunk(int k) const { return dir ? w.hi - 1 - k : w.lo + k; }
+    static constexpr uint32_t CB = 0, M = 0, A1 = T, A2 = T + 64, D = 2 * T + 64;  // TMEM columns (M over C B^T; A2 twice)
+    HLA_DEVICE static int arrivals(int i) { return i == B_W || (i >= B_Y && i < B_CB) || i == B_M ? kElemWarps : 1; }
 };
 
-template <int NB, bool OUT>
-__device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Walk &z) {
-    using L = LayCarry<NB, OUT>;
+template <int NB>
+__device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uint8_t *base, uint32_t tb, const Piece &w, int K) {
+    using L = LayCarry<NB>;
     const Args &a = p.a;
-    const Piece &w = z.w;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, cq = warp >> 2, row = 32 * q + lane, c0 = 16 * cq;
     const uint32_t lanes = tb + ((uint32_t)(32 * q) << 16);
     const int col = 64 * w.pt + c0;
     const bool holds = q < 2 * NB;  // rows of the state
-    const float skip = OUT && a.D ? a.D[w.h] : 0.f;
+    const float skip = a.D ? a.D[w.h] : 0.f;
     float2 carry[8];
-    {
-        const float *init = z.dir ? a.d_state_out : a.state_in;
-        load_state(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, z.dir, w) : init ? init + ((size_t)w.b * a.H + w.h) * a.N * a.P : nullptr,
-                   row, col, carry);
-    }
+    load_state(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, 0, w)
+                  : a.state_in                    ? a.state_in + ((size_t)w.b * a.H + w.h) * a.N * a.P
+                                                  : nullptr, row, col, carry);
     auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + k % L::NX * kDecBytes); };
-    auto show = [&](int bar, int bar2) {  // what this warp wrote, to the tensor cores and TMA
+    auto show = [&](int bar) {  // what this warp wrote, to the tensor cores and TMA
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(ws.bar(bar));
-            if (bar2 >= 0) mbar_arrive(ws.bar(bar2));
-        }
-    };
-    auto put_state = [&](int k) {  // the state before (the gradient behind) chunk k
-        if constexpr (OUT) {
-            if (holds) {
-                store_row8(base + L::OFF_H, 64 * NB, row, c0, carry);
-                store_row8(base + L::OFF_H, 64 * NB, row, c0 + 8, carry + 4);
-            }
-        } else {
-            if (k > 0 && !ws.wait(L::B_YE, (uint32_t)(k - 1) & 1u)) return false;
-            if (holds) {
-                store_split8(base + L::OFF_H, base + L::OFF_H + L::HB, 64 * NB, row, c0, carry);
-                store_split8(base + L::OFF_H, base + L::OFF_H + L::HB, 64 * NB, row, c0 + 8, carry + 4);
-            }
-            show(L::B_Y + k % L::NX, -1);
-        }
-        return true;
+        if (lane == 0) mbar_arrive(ws.bar(bar));
     };
     float ahead = 1.f;  // decay over the chunk whose rows were weighted last
-    auto scale = [&](int k) {
-        const int s = k % L::NX, e = L::NW == 2 ? k & 1 : 0;
+    auto prepare = [&](int k) {  // the state before chunk k and its weighted rows
+        const int s = k % L::NX;
+        if (holds) {
+            store_row8(base + L::OFF_H, 64 * NB, row, c0, carry);
+            store_row8(base + L::OFF_H, 64 * NB, row, c0 + 8, carry + 4);
+        }
         if (!ws.wait(L::B_X + s, ring_phase<L::NX>(k))) return false;
         const Dec &d = dec(k);
-        uint8_t *hi = base + L::OFF_W + e * 2 * kHalf;
-        scale_split16(base + L::OFF_X + s * kHalf, hi, hi + kHalf, row, c0, z.dir ? d.to[row] : d.w[row]);
+        scale_split16(base + L::OFF_X + s * kHalf, base + L::OFF_W, row, c0, d.w[row]);
         ahead = d.end;
-        show(L::B_W + e, OUT ? L::B_H : L::B_XE + s);  // OUT: together with the state, one fence for both
+        show(L::B_W);
         return true;
     };
-    bool ok = z.K == 0 || (put_state(0) && scale(0));
+    bool ok = K == 0 || prepare(0);
 #pragma unroll 1
-    for (int k = 0; k < z.K && ok; ++k) {
+    for (int k = 0; k < K; ++k) {  // (after an expired wait the loop goes on, so that the quads' barrier stays matched)
         const uint32_t ph = (uint32_t)k & 1u;
-        const int e = L::NW == 2 ? k & 1 : 0;
         const float end = ahead;
-        if constexpr (OUT) {
-            // M = (C B^T) o L diag(dt), bf16: this thread's 32 columns, nothing above the diagonal
-            if (!(ok = ws.wait(L::B_CB, ph))) break;
-            tc_fence_after();
+        // M = (C B^T) o L diag(dt), bf16: this thread's 32 columns, nothing above the diagonal
+        ok = ok && ws.wait(L::B_CB, ph);
+        tc_fence_after();
+        float pk[16];
+        if (cq <= q && ok) {
             const Dec &d = dec(k);
-            const Decay s = d.s[row];
-            float2 v[16];
-            if (cq <= q) {
-                tmem_pairs16(lanes + L::CB + 32 * cq, reinterpret_cast<float2(&)[8]>(v[0]));
-                tmem_pairs16(lanes + L::CB + 32 * cq + 16, reinterpret_cast<float2(&)[8]>(v[8]));
-                const Decay last = d.s[32 * cq + 31];
-                if (cq < q || d.s[32 * cq].hi - last.hi <= kBlockRange) {
-                    // 2^(s_t - s_j) as 2^(s_t - s_r) 2^(s_r - s_j), r the last token of the columns
-                    const float2 u = both(factor(s, last));
-                    tmem_wait_ld();
+            const Decay s = d.s[row], last = d.s[32 * cq + 31];
+            const bool plain = cq < q || d.s[32 * cq].hi - last.hi <= kBlockRange;
+            const float2 u = both(plain ? factor(s, last) : 1.f);
+            const uint32_t bits = cq < q ? 0xffffffffu : low_bits(lane + 1);  // (behind the diagonal a factor may be anything)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 f = *reinterpret_cast<const float4 *>(d.v + 32 * cq + 4 * i);
+            for (int g = 0; g < 2; ++g) {
+                const int c = 32 * cq + 16 * g;
+                float2 v[8];
+                tmem_pairs16(lanes + L::CB + c, v);
+                tmem_wait_ld();
+                if (plain) {  // 2^(s_t - s_j) as 2^(s_t - s_r) 2^(s_r - s_j), r the last token of the columns
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = *reinterpret_cast<const float4 *>(d.v + c + 4 * i);
                         v[2 * i] = mul2(v[2 * i], mul2(u, make_float2(f.x, f.y)));
                         v[2 * i + 1] = mul2(v[2 * i + 1], mul2(u, make_float2(f.z, f.w)));
                     }
                 } else {
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 sj = *reinterpret_cast<const float4 *>(d.s + 32 * cq + 2 * i);
-                        const float2 dt = *reinterpret_cast<const float2 *>(d.dt + 32 * cq + 2 * i);
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 sj = *reinterpret_cast<const float4 *>(d.s + c + 2 * i);
+                        const float2 dt = *reinterpret_cast<const float2 *>(d.dt + c + 2 * i);
                         v[i] = mul2(v[i], mul2(make_float2(factor(s, {sj.x, sj.y}), factor(s, {sj.z, sj.w})), dt));
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t m = bits >> (16 * g + 2 * i);
+                    pk[8 * g + i] = __uint_as_float(pack_bf16(m & 1u ? v[i].x : 0.f, m & 2u ? v[i].y : 0.f));
+                }
             }
-            // (behind the diagonal a factor may be anything)
-            const uint32_t bits = cq < q ? 0xffffffffu : cq > q ? 0u : low_bits(lane + 1);
-            float pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pk[i] = __uint_as_float(pack_bf16(bits & (1u << (2 * i)) ? v[i].x : 0.f, bits & (2u << (2 * i)) ? v[i].y : 0.f));
-            tmem_st16(lanes + L::M + 16 * cq, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ws.bar(L::B_M));
         } else {
-            if (k + 1 < z.K && !(ok = scale(k + 1))) break;
-        }
-        // the state behind the chunk
-        if (!(ok = ws.wait(L::B_D + e, L::NW == 2 ? ring_phase<2>(k) : ph))) break;
-        tc_fence_after();
-        if (holds) {
-            float2 v[8];
-            load_parts16(lanes + L::D + e * T + c0, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], v[i]);
+            for (int i = 0; i < 16; ++i) pk[i] = 0.f;
+        }
+        quad_sync(q);  // every warp of these rows has read what M overwrites
+        tc_fence_after();
+        tmem_st16(lanes + L::M + 16 * cq, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_M));
+        // the state behind the chunk
+        ok = ok && ws.wait(L::B_D, ph);
+        tc_fence_after();
+        if (holds && ok) {
+            float2 x[8];
+            load_parts16(lanes + L::D + c0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], x[i]);
         }
         tc_fence_before();
-        if constexpr (OUT) {
-            if (!(ok = ws.wait(L::B_A2, ph))) break;
-            if (k + 1 < z.K) ok = put_state(k + 1) && scale(k + 1);
-            // y = M x + 2^s C h + D x, over x: its weighted rows and M x are done
-            if (!ok || !(ok = ws.wait(L::B_A1, ph))) break;
-            tc_fence_after();
+        ok = ok && ws.wait(L::B_A2, ph);
+        if (k + 1 < K) ok = ok && prepare(k + 1);
+        // y = M x + 2^s C h + D x, over x: its weighted rows and M x are done
+        ok = ok && ws.wait(L::B_A1, ph);
+        tc_fence_after();
+        if (ok) {
             const float to = dec(k).to[row];
             uint8_t *x = base + L::OFF_X + k % L::NX * kHalf;
             float2 y[8], c[8], f[8];
@@ -392,24 +367,21 @@ __device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uin
             for (int i = 0; i < 8; ++i) y[i] = fma2(both(skip), f[i], fma2(both(to), c[i], y[i]));
             store_row8(x, T, row, c0, y);
             store_row8(x, T, row, c0 + 8, y + 4);
-            tc_fence_before();
-            show(L::B_Y + k % L::NX, -1);
-        } else if (k + 1 < z.K) {
-            ok = put_state(k + 1);
         }
+        tc_fence_before();
+        show(L::B_Y + k % L::NX);
     }
-    const int last = z.dir ? 0 : max(w.used - 1, 0);
-    float *fin = z.dir ? a.d_state_in : a.state_out;
-    if (ok && fin && w.piece == last && holds) store_state(a, fin + ((size_t)w.b * a.H + w.h) * a.N * a.P, row, col, carry);
+    if (ok && a.state_out && w.piece == max(w.used - 1, 0) && holds)
+        store_state(a, a.state_out + ((size_t)w.b * a.H + w.h) * a.N * a.P, row, col, carry);
 }
 
 // In the order in which the elementwise warps ask for them: M x of chunk k and C B^T of k + 1, 2^s C h
 // of k + 1, the state's sums over k + 1.
-template <int NB, bool OUT>
+template <int NB>
 __device__ __forceinline__ void carry_mma(const Waits &ws, uint8_t *base, uint32_t tb, int K) {
-    using L = LayCarry<NB, OUT>;
+    using L = LayCarry<NB>;
     constexpr uint32_t id_y = make_idesc(T, 64, false, true), id_cb = make_idesc(T, T, false, false);
-    const uint64_t H = make_sdesc(smem_u32(base + L::OFF_H), 64 * NB * 128u, 1024u);
+    const uint64_t H = make_sdesc(smem_u32(base + L::OFF_H), L::HB, 1024u), W = mnmajor(base + L::OFF_W);
     auto full = [&](int i) { return ws.wait(L::B_R + i % L::NR, ring_phase<L::NR>(i)); };
     auto tile = [&](int i) { return base + L::OFF_R + (i % L::NR) * NB * kHalf; };
     auto do_cb = [&](int k) {
@@ -420,57 +392,49 @@ __device__ __forceinline__ void carry_mma(const Waits &ws, uint8_t *base, uint32
         umma_commit_warp(ws.bar(L::B_CB));
         return true;
     };
-    bool ok = !OUT || K == 0 || do_cb(0);
+    bool ok = K == 0 || do_cb(0);
 #pragma unroll 1
     for (int k = 0; k < K && ok; ++k) {
-        if constexpr (OUT) {
-            if (!(ok = ws.wait(L::B_H, (uint32_t)k & 1u))) break;
-            tc_fence_after();
-            const uint64_t c = kmajor(tile(2 * k));
-            const uint32_t A2 = tb + L::A2 + 64 * (k & 1);
-            mma_km64(A2, c, H, id_y, false);
-            if (NB > 1) mma_km64(A2, c + kBlock, H + kRows64, id_y, true);
-            umma_commit_warp(ws.bar(L::B_A2));
-            umma_commit_warp(ws.bar(L::B_RE + 2 * k % L::NR));
-        }
-        const int r = L::EACH * k + L::EACH - 1, e = L::NW == 2 ? k & 1 : 0;
-        if (!(ok = full(r) && ws.wait(L::B_W + e, L::NW == 2 ? ring_phase<2>(k) : (uint32_t)k & 1u))) break;
+        if (!(ok = ws.wait(L::B_W, (uint32_t)k & 1u))) break;
         tc_fence_after();
-        mma_state(tb + L::D + e * T, mnmajor(tile(r)), mnmajor(base + L::OFF_W + e * 2 * kHalf), false);
-        umma_commit_warp(ws.bar(L::B_D + e));
-        umma_commit_warp(ws.bar(L::B_RE + r % L::NR));
-        if constexpr (OUT) {
-            if (!(ok = ws.wait(L::B_X + k % L::NX, ring_phase<L::NX>(k)) && ws.wait(L::B_M, (uint32_t)k & 1u))) break;
-            tc_fence_after();
-            mma_ts128(tb + L::A1, tb + L::M, mnmajor(base + L::OFF_X + k % L::NX * kHalf), id_y);
-            umma_commit_warp(ws.bar(L::B_A1));
-            if (k + 1 < K) ok = do_cb(k + 1);
-        }
+        const uint64_t c = kmajor(tile(2 * k));
+        const uint32_t A2 = tb + L::A2 + 64 * (k & 1);
+        mma_km64(A2, c, H, id_y, false);
+        if (NB > 1) mma_km64(A2, c + kBlock, H + kRows64, id_y, true);
+        umma_commit_warp(ws.bar(L::B_A2));
+        umma_commit_warp(ws.bar(L::B_RE + 2 * k % L::NR));
+        mma_state(tb + L::D, mnmajor(tile(2 * k + 1)), W, false);
+        umma_commit_warp(ws.bar(L::B_D));
+        umma_commit_warp(ws.bar(L::B_RE + (2 * k + 1) % L::NR));
+        if (!(ok = ws.wait(L::B_X + k % L::NX, ring_phase<L::NX>(k)) && ws.wait(L::B_M, (uint32_t)k & 1u))) break;
+        tc_fence_after();
+        mma_ts128(tb + L::A1, tb + L::M, mnmajor(base + L::OFF_X + k % L::NX * kHalf), id_y);
+        umma_commit_warp(ws.bar(L::B_A1));
+        if (k + 1 < K) ok = do_cb(k + 1);
     }
     umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
     mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
     __syncwarp();
 }
 
-template <int NB, bool OUT>
-__device__ __forceinline__ void carry_load(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
-    using L = LayCarry<NB, OUT>;
+template <int NB>
+__device__ __forceinline__ void carry_load(const Params &p, const Waits &ws, uint8_t *base, const Piece &w, int K) {
+    using L = LayCarry<NB>;
     const Args &a = p.a;
-    const Piece &w = z.w;
-    const int lane = threadIdx.x & 31, tiles = L::EACH * z.K;
+    const int lane = threadIdx.x & 31;
     uint32_t raw = 0;
     int r = 0;
     bool ok = true;
 #pragma unroll 1
-    for (; r < tiles && ok; ++r) {
-        const int s = r % L::NR, t0 = z.chunk(r / L::EACH) * T;
-        const bool is_c = OUT && r % 2 == 0, clear = w.len - t0 < T && !is_c;  // rows of C reach their own tokens only
+    for (; r < 2 * K && ok; ++r) {
+        const int s = r % L::NR, t0 = (w.lo + r / 2) * T;
+        const bool is_c = r % 2 == 0, clear = w.len - t0 < T && !is_c;  // rows of C reach their own tokens only
         if (r >= L::NR && !(ok = ws.wait(L::B_RE + s, ring_phase<L::NR>(r) ^ 1u))) break;
         uint8_t *t = base + L::OFF_R + s * NB * kHalf;
         if (lane == 0) {
             uint64_t *bar = ws.bar(clear ? L::B_RAW : L::B_R + s);
             mbar_expect_tx(bar, NB * kHalf);
-            load_tile<NB>(t, is_c ? &p.mc : &p.mb[z.dir], is_c ? a.c : p.vb[z.dir], bar, 0, t0, w.h / a.R, w.b);
+            load_tile<NB>(t, is_c ? &p.mc : &p.mb[0], is_c ? a.c : p.vb[0], bar, 0, t0, w.h / a.R, w.b);
         }
         __syncwarp();
         if (clear) ok = clear_landed(ws, L::B_RAW, raw, L::B_R + s, t, NB, w.len - t0);
@@ -481,26 +445,25 @@ __device__ __forceinline__ void carry_load(const Params &p, const Waits &ws, uin
     __syncwarp();
 }
 
-template <int NB, bool OUT>
-__device__ __forceinline__ void carry_load_x(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
-    using L = LayCarry<NB, OUT>;
+template <int NB>
+__device__ __forceinline__ void carry_load_x(const Params &p, const Waits &ws, uint8_t *base, const Piece &w, int K) {
+    using L = LayCarry<NB>;
     const Args &a = p.a;
-    const Piece &w = z.w;
     const int lane = threadIdx.x & 31;
     uint32_t raw = 0;
     int k = 0;
     bool ok = true;
 #pragma unroll 1
-    for (; k < z.K && ok; ++k) {
-        const int s = k % L::NX, c = z.chunk(k), t0 = c * T;
+    for (; k < K && ok; ++k) {
+        const int s = k % L::NX, t0 = (w.lo + k) * T;
         const bool clear = w.len - t0 < T;
         if (k >= L::NX && !(ok = ws.wait(L::B_XE + s, ring_phase<L::NX>(k) ^ 1u))) break;
         uint8_t *x = base + L::OFF_X + s * kHalf;
         if (lane == 0) {
             uint64_t *bar = ws.bar(clear ? L::B_RAWX : L::B_X + s);
             mbar_expect_tx(bar, kHalf + kDecBytes);
-            bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, w.h, c), kDecBytes, bar);
-            load_tile<1>(x, &p.mx[z.dir], p.vx[z.dir], bar, 64 * w.pt, t0, w.h, w.b);
+            bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, w.h, w.lo + k), kDecBytes, bar);
+            load_tile<1>(x, &p.mx[0], p.vx[0], bar, 64 * w.pt, t0, w.h, w.b);
         }
         __syncwarp();
         if (clear) ok = clear_landed(ws, L::B_RAWX, raw, L::B_X + s, x, 1, w.len - t0);
@@ -510,77 +473,66 @@ __device__ __forceinline__ void carry_load_x(const Params &p, const Waits &ws, u
     __syncwarp();
 }
 
-template <int NB, bool OUT>
-__device__ __forceinline__ void carry_store(const Params &p, const Waits &ws, uint8_t *base, const Walk &z) {
-    using L = LayCarry<NB, OUT>;
-    const Args &a = p.a;
-    const Piece &w = z.w;
+// 128 rows of 64 columns of a head, from a tile in shared memory, by one warp: whole chunks by TMA;
+// rows behind the sequence stay as they are.  Returns once the tile may be overwritten.
+HLA_DEVICE void store_tile(const uint8_t *tile, const CUtensorMap *m, const View &v, int pt, int t0, int live, int h, int b, int P) {
+    const int lane = threadIdx.x & 31;
+    if (live >= T) {
+        if (lane == 0) {
+            tma_store_4d(tile, m, 64 * pt, t0, v.sh ? h : 0, v.sb ? b : 0);
+            bulk_commit();
+            bulk_wait_read();
+        }
+    } else {
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(v.p) + (size_t)b * v.sb + (size_t)h * v.sh + (size_t)t0 * v.st;
+        for (int i = lane; i < live * 8; i += 32) {
+            const int r = i >> 3, c = 64 * pt + 8 * (i & 7);
+            if (c < P) *reinterpret_cast<uint4 *>(out + (size_t)r * v.st + c) = *reinterpret_cast<const uint4 *>(tile + tile_off(T, r, 8 * (i & 7)));
+        }
+    }
+    __syncwarp();
+}
+
+template <int NB>
+__device__ __forceinline__ void carry_store(const Params &p, const Waits &ws, uint8_t *base, const Piece &w, int K) {
+    using L = LayCarry<NB>;
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int k = 0; k < z.K; ++k) {
-        const int s = k % L::NX, c = z.chunk(k), t0 = c * T;
+    for (int k = 0; k < K; ++k) {
+        const int s = k % L::NX, t0 = (w.lo + k) * T;
         if (!ws.wait(L::B_Y + s, ring_phase<L::NX>(k))) break;
-        if constexpr (OUT) {
-            const uint8_t *y = base + L::OFF_X + s * kHalf;
-            if (w.len - t0 >= T) {
-                if (lane == 0) {
-                    tma_store_4d(y, &p.my, 64 * w.pt, t0, a.y.sh ? w.h : 0, a.y.sb ? w.b : 0);
-                    bulk_commit();
-                    bulk_wait_read();
-                }
-            } else {  // rows behind the sequence stay as they are
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.y.p) + (size_t)w.b * a.y.sb + (size_t)w.h * a.y.sh;
-                for (int i = lane; i < (w.len - t0) * 8; i += 32) {
-                    const int r = i >> 3, cc = 64 * w.pt + 8 * (i & 7);
-                    if (cc < a.P)
-                        *reinterpret_cast<uint4 *>(out + (size_t)(t0 + r) * a.y.st + cc) =
-                            *reinterpret_cast<const uint4 *>(y + tile_off(T, r, 8 * (i & 7)));
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ws.bar(L::B_XE + s));
-        } else {
-            if (lane == 0) {
-                const size_t at = (((size_t)w.b * a.H + w.h) * p.plan.PT + w.pt) * a.nc + c;
-                bulk_store(p.image[z.dir] + at * 2 * L::HB, base + L::OFF_H, 2 * L::HB);
-                bulk_commit();
-                bulk_wait_read();
-                mbar_arrive(ws.bar(L::B_YE));
-            }
-            __syncwarp();
-        }
+        store_tile(base + L::OFF_X + s * kHalf, &p.my, p.a.y, w.pt, t0, w.len - t0, w.h, w.b, p.a.P);
+        if (lane == 0) mbar_arrive(ws.bar(L::B_XE + s));
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
 }
 
-template <int NB, bool OUT>
+template <int NB>
 __global__ void __launch_bounds__(kCarryThreads, 1) ssm_carry_kernel(const __grid_constant__ Params p) {
-    using L = LayCarry<NB, OUT>;
+    using L = LayCarry<NB>;
     extern __shared__ __align__(1024) uint8_t base[];
-    Walk z;
-    z.dir = OUT ? 0 : blockIdx.y;
-    z.w = piece_of(p.a, p.plan, blockIdx.x, 1);
-    if (z.w.piece >= max(z.w.used, 1)) return;
-    z.K = z.w.hi - z.w.lo;
+    const Piece w = piece_of(p.a, p.plan, blockIdx.x, 1);
+    if (w.piece >= max(w.used, 1)) return;
+    const int K = w.hi - w.lo;
     Cta<L::NBAR> cta(base, L::OFF_BAR, p.a.err, [](int i) { return L::arrivals(i); });
     if (cta.warp < kElemWarps)
-        carry_elem<NB, OUT>(p, cta.ws, base, cta.tb, z);
+        carry_elem<NB>(p, cta.ws, base, cta.tb, w, K);
     else if (cta.warp == kWarpMma)
-        carry_mma<NB, OUT>(cta.ws, base, uniform(cta.tb), (int)uniform(z.K));
+        carry_mma<NB>(cta.ws, base, uniform(cta.tb), (int)uniform(K));
     else if (cta.warp == kWarpTma)
-        carry_load<NB, OUT>(p, cta.ws, base, z);
+        carry_load<NB>(p, cta.ws, base, w, K);
     else if (cta.warp == kWarpTmaX)
-        carry_load_x<NB, OUT>(p, cta.ws, base, z);
+        carry_load_x<NB>(p, cta.ws, base, w, K);
     else
-        carry_store<NB, OUT>(p, cta.ws, base, z);
+        carry_store<NB>(p, cta.ws, base, w, K);
     cta.finish();
 }
 
 // Heads that share a CTA in the sums of pieces: as many as leave CTAs for the device.
 inline int heads_together(const Args &a, const Plan &plan, int dirs) {
     const long long ctas = (long long)a.B * a.H * plan.PT * plan.pieces * dirs;
-    return a.R % 4 == 0 && ctas / 4 >= kSms * 3 / 4 ? 4 : a.R % 2 == 0 && ctas / 2 >= kSms * 3 / 4 ? 2 : 1;
+    return a.R % 2 == 0 && ctas / 2 >= kSms * 3 / 4 ? 2 : 1;
 }
 template <int NB, int HB>
 cudaError_t launch_sums(const Params &p, int dirs, cudaStream_t st) {
@@ -598,23 +550,11 @@ cudaError_t starts(const Params &p, int dirs, cudaStream_t st) {
     const Args &a = p.a;
     cudaError_t e = weights(a, const_cast<Dec *>(p.dec), st);
     if (e != cudaSuccess || p.plan.pieces == 1) return e;
-    const int hb = heads_together(a, p.plan, dirs);
-    e = hb == 4 ? launch_sums<NB, 4>(p, dirs, st) : hb == 2 ? launch_sums<NB, 2>(p, dirs, st) : launch_sums<NB, 1>(p, dirs, st);
+    e = heads_together(a, p.plan, dirs) == 2 ? launch_sums<NB, 2>(p, dirs, st) : launch_sums<NB, 1>(p, dirs, st);
     if (e != cudaSuccess) return e;
     ssm_piece_scan_kernel<<<dim3((unsigned)((size_t)a.B * a.H * ((a.N * a.P + 255) / 256)), dirs), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
-template <int NB, bool OUT>
-cudaError_t walk(const Params &p, cudaStream_t st) {
-    using C = LayCarry<NB, OUT>;
-    static_assert(C::SMEM <= 227 * 1024, "shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(ssm_carry_kernel<NB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    const Args &a = p.a;
-    ssm_carry_kernel<NB, OUT><<<dim3((unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces), OUT ? 1 : 2), kCarryThreads, C::SMEM, st>>>(p);
-    return cudaGetLastError();
-}
-
 }  // namespace tcs
 }  // namespace ssm
 }  // namespace hla

@@ -12,8 +12,14 @@ using namespace tcs;
 
 template <int NB>
 cudaError_t launch(const Params &p, cudaStream_t st) {
-    const cudaError_t e = starts<NB>(p, 1, st);
-    return e == cudaSuccess ? walk<NB, true>(p, st) : e;
+    using C = LayCarry<NB>;
+    static_assert(C::SMEM <= 227 * 1024, "shared memory");
+    cudaError_t e = starts<NB>(p, 1, st);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_carry_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const Args &a = p.a;
+    ssm_carry_kernel<NB><<<(unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces), kCarryThreads, C::SMEM, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -39,12 +45,17 @@ size_t tc_space(Args &a, bool backward, uint8_t *base) {
     a.factor = take(units);
     if (backward) {
         a.g = take(units * a.N * a.P);
-        const size_t image = (size_t)a.B * a.H * plan.PT * a.nc * (a.N <= 64 ? 1 : 2) * (kHalf / 4);  // two parts of 64 rows each
+        const size_t heads = (size_t)a.B * a.H, image = heads * plan.PT * a.nc * (a.N <= 64 ? 1 : 2) * (kHalf / 8);  // 64 rows of 128 bytes each
         a.image[0] = reinterpret_cast<unsigned char *>(take(image));
         a.image[1] = reinterpret_cast<unsigned char *>(take(image));
+        a.inter = take(2 * plan.PT * 4 * heads * a.nc * T);
+        a.aside = take(heads * plan.PT * a.nc * 8192);
+        a.dots = take(heads * a.nc * plan.PT * 16);
+        a.own = take(2 * heads * a.nc * T);
+        a.dd = take(heads * a.nc);
         a.splits = tc_splits(a);
         a.dbc = take(a.splits > 1 ? (size_t)a.splits * 2 * a.B * a.G * a.n * a.N : 0);
-        a.sums = take((size_t)a.B * a.nc * 3 * a.H);
+        a.sums = take((size_t)a.B * plan.pieces * 3 * a.H);
     }
     return at;
 }

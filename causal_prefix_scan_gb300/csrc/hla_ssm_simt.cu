@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const Args a) {
         }
     }
 }
-__global__ void __launch_bounds__(256) ssm_sums_kernel(const Args a) {
-    column_sums(a.sums, a.B * a.nc, 3LL * a.H, [=](long long k, float s) {
+__global__ void __launch_bounds__(256) ssm_sums_kernel(const Args a, int rows) {
+    column_sums(a.sums, rows, 3LL * a.H, [=](long long k, float s) {
         float *out = k < a.H ? a.dA : k < 2 * a.H ? a.dD : a.dbias;
         if (out) out[k % a.H] = s;
     });
@@ -429,10 +429,10 @@ cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st) {
         e = dt == HLA_F32 ? run_backward<float, 64>(a, st) : run_backward<__nv_bfloat16, 64>(a, st);
     else
         e = dt == HLA_F32 ? run_backward<float, 32>(a, st) : run_backward<__nv_bfloat16, 32>(a, st);
-    return e == cudaSuccess ? join(a, dt, true, st) : e;
+    return e == cudaSuccess ? join(a, dt, true, a.B * a.nc, st) : e;
 }
 
-cudaError_t join(const Args &a, hla_dtype dt, bool parts, cudaStream_t st) {
+cudaError_t join(const Args &a, hla_dtype dt, bool parts, int rows, cudaStream_t st) {
     const size_t blocks = ((size_t)a.B * a.G * a.n + 7) / 8;
     const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096), 2);
     if (parts && dt == HLA_F32)
@@ -441,7 +441,7 @@ cudaError_t join(const Args &a, hla_dtype dt, bool parts, cudaStream_t st) {
         ssm_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    ssm_sums_kernel<<<(unsigned)((3LL * a.H + 31) / 32), 256, 0, st>>>(a);
+    ssm_sums_kernel<<<(unsigned)((3LL * a.H + 31) / 32), 256, 0, st>>>(a, rows);
     return cudaGetLastError();
 }
 

@@ -74,6 +74,7 @@ HLA_DEVICE void mma_tk64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
 }
+HLA_DEVICE void quad_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }  // the four warps of 32 rows
 constexpr uint32_t kBlock = kHalf >> 4, kRows64 = 64 * 128 >> 4;  // descriptor steps: 64 columns, 64 rows
 
 HLA_DEVICE void tmem_st8(uint32_t taddr, const float (&v)[8]) {
@@ -141,28 +142,31 @@ HLA_DEVICE float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 
 HLA_DEVICE void unpack8(const uint4 u, float2 *v) {
     v[0] = unpack2(u.x); v[1] = unpack2(u.y); v[2] = unpack2(u.z); v[3] = unpack2(u.w);
 }
-// v as two bf16 parts: hi + lo is v within 2^-17.
-HLA_DEVICE void split2(float2 v, uint32_t &hi, uint32_t &lo) {
+// v as three bf16 parts, whose sum is v to the last bit (above 2^-110).
+HLA_DEVICE void split3(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     hi = pack2(v);
-    const float2 h = unpack2(hi ^ 0x80008000u);  // its negative
-    lo = pack2(add2(v, h));
+    v = add2(v, unpack2(hi ^ 0x80008000u));  // less what the part holds
+    mid = pack2(v);
+    v = add2(v, unpack2(mid ^ 0x80008000u));
+    lo = pack2(v);
 }
-// 8 columns (c0 a multiple of 8) of row r of a 64-column tile with `rows` rows, in two parts.
-HLA_DEVICE void store_split8(uint8_t *hi, uint8_t *lo, int rows, int r, int c0, const float2 *v) {
-    uint4 h, l;
-    split2(v[0], h.x, l.x);
-    split2(v[1], h.y, l.y);
-    split2(v[2], h.z, l.z);
-    split2(v[3], h.w, l.w);
-    const uint32_t off = tile_off(rows, r, c0);
-    *reinterpret_cast<uint4 *>(hi + off) = h;
-    *reinterpret_cast<uint4 *>(lo + off) = l;
+// 8 columns (c0 a multiple of 8) of row r of a 64-column tile with `rows` rows, its parts `step` bytes apart.
+HLA_DEVICE void store_split8(uint8_t *tile, int step, int rows, int r, int c0, const float2 *v) {
+    uint4 h, m, l;
+    split3(v[0], h.x, m.x, l.x);
+    split3(v[1], h.y, m.y, l.y);
+    split3(v[2], h.z, m.z, l.z);
+    split3(v[3], h.w, m.w, l.w);
+    uint8_t *at = tile + tile_off(rows, r, c0);
+    *reinterpret_cast<uint4 *>(at) = h;
+    *reinterpret_cast<uint4 *>(at + step) = m;
+    *reinterpret_cast<uint4 *>(at + 2 * step) = l;
 }
 HLA_DEVICE void store_row8(uint8_t *tile, int rows, int r, int c0, const float2 *v) {
     *reinterpret_cast<uint4 *>(tile + tile_off(rows, r, c0)) = make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
 }
-// 16 columns of row r of a bf16 tile times f, in two parts.
-HLA_DEVICE void scale_split16(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int r, int c0, float f) {
+// 16 columns of row r of a bf16 tile times f, in three parts kHalf bytes apart.
+HLA_DEVICE void scale_split16(const uint8_t *tile, uint8_t *to, int r, int c0, float f) {
     const uint4 u0 = *reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0));
     const uint4 u1 = *reinterpret_cast<const uint4 *>(tile + tile_off(T, r, c0 + 8));
     float2 v[8];
@@ -170,8 +174,8 @@ HLA_DEVICE void scale_split16(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int
     unpack8(u1, v + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(f));
-    store_split8(hi, lo, T, r, c0, v);
-    store_split8(hi, lo, T, r, c0 + 8, v + 4);
+    store_split8(to, kHalf, T, r, c0, v);
+    store_split8(to, kHalf, T, r, c0 + 8, v + 4);
 }
 // 16 columns of an accumulator in TMEM, as pairs.
 HLA_DEVICE void tmem_pairs16(uint32_t taddr, float2 (&v)[8]) { tmem_ld16(taddr, reinterpret_cast<float(&)[16]>(v)); }
