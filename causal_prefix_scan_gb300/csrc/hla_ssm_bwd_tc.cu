@@ -318,7 +318,7 @@ struct GradParams {
     CUtensorMap mx, mdy, mb, mc, mdx;
     const Dec *dec;
     const uint8_t *h, *g;  // images
-    float *own;            // [w, vE][B][H][chunks * T]: sums of E
+    float *own;            // [w, vE, diagonal][B][H][chunks * T]: sums of E
     float *dd;             // [B][H][chunks]: dY.X
 };
 
@@ -328,7 +328,7 @@ struct LayGrad {
     static constexpr int OFF_B = 0, OFF_C = NB * kHalf, OFF_S = 2 * NB * kHalf, OFF_XD = OFF_S + 2 * kHalf, OFF_H = OFF_XD + NS * kHalf,
                          OFF_G = OFF_H + HB;
     static constexpr int OFF_DEC = OFF_G + HB, OFF_SUM = OFF_DEC + 2 * (int)sizeof(Dec);
-    static constexpr int SUM_FLOATS = 8 * T + 16;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], dD [16]
+    static constexpr int SUM_FLOATS = 9 * T + 16;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], E's diagonal [128], dD [16]
     static constexpr int OFF_BAR = OFF_SUM + SUM_FLOATS * 4;
     static constexpr int B_XD = 0, B_XDE = B_XD + NS, B_DEC = B_XDE + NS, B_DECE = B_DEC + 2, B_H = B_DECE + 2, B_HE = B_H + 1,
                          B_G = B_HE + 1, B_GE = B_G + 1, B_BC = B_GE + 1, B_CB = B_BC + 1, B_DYX = B_CB + 1, B_DE = B_DYX + 1,
@@ -397,12 +397,12 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         const Decay s = d.s[row];
         const float dt = d.dt[row];
         uint32_t pk[16];
-        float ve = 0.f;
+        float ve = 0.f, diag = 0.f;
         if (active && ok) {
             const Decay first = d.s[32 * cq];
             const bool plain = cq > q || first.hi - d.s[32 * cq + 31].hi <= kBlockRange;
             const float2 f0 = both(plain ? factor(first, s) : 1.f);
-            const uint32_t bits = cq > q ? 0xffffffffu : ~low_bits(lane);  // t >= j
+            const uint32_t bits = cq > q ? 0xffffffffu : ~low_bits(lane), past = cq > q ? 0xffffffffu : ~low_bits(lane + 1);  // t >= j, t > j
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 float2 v[8];
@@ -423,9 +423,13 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
                     f.x = bits & (1u << (16 * g + 2 * i)) ? f.x : 0.f;  // (above the diagonal a factor may be anything)
                     f.y = bits & (2u << (16 * g + 2 * i)) ? f.y : 0.f;
                     const float2 m = mul2(cb[8 * g + i], f), sv = mul2(v[i], f), ee = mul2(m, v[i]);
-                    ve += ee.x + ee.y;
-                    e[2 * i] = ee.x * dt;
-                    e[2 * i + 1] = ee.y * dt;
+                    // E's diagonal is kept apart: it cancels in the gradient of the decays, which differences
+                    // of these sums give, and where decays are steep it is most of them
+                    const float ex = past & (1u << (16 * g + 2 * i)) ? ee.x : 0.f, ey = past & (2u << (16 * g + 2 * i)) ? ee.y : 0.f;
+                    diag += (ee.x - ex) + (ee.y - ey);
+                    ve += ex + ey;
+                    e[2 * i] = ex * dt;
+                    e[2 * i + 1] = ey * dt;
                     pk[8 * g + i] = pack2(mul2(m, both(dt)));
                     sp[i] = pack2(mul2(sv, both(dt)));
                 }
@@ -442,6 +446,7 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
             sum_w[lane] = 0.f;
         }
         sum_ve[row] = ve;
+        if (cq == q) sums[8 * T + row] = diag;
         quad_sync(q);  // every warp of these rows has read its columns of the product that M^T overwrites
         tc_fence_after();
         tmem_st16(lanes + L::M + 16 * cq, reinterpret_cast<float(&)[16]>(pk));
@@ -473,7 +478,7 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            sums[8 * T + warp] = dd;
+            sums[9 * T + warp] = dd;
             mbar_arrive(ws.bar(L::B_YT));
             mbar_arrive(ws.bar(L::B_XDE + sy));
             mbar_arrive(ws.bar(L::B_SUM));
@@ -674,7 +679,7 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
     const Args &a = p.a;
     const int lane = threadIdx.x & 31;
     const float *sums = reinterpret_cast<const float *>(base + L::OFF_SUM);
-    float4 w, ve;
+    float4 w, ve, dg;
     float dd = 0.f;
 #pragma unroll 1
     for (int u = 0; u < job.U; ++u) {
@@ -682,7 +687,7 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
         const int h = head_of(p, job, u), pt = u % p.PT, sx = (2 * u + 1) % L::NS;
         if (!ws.wait(L::B_DEC + (u & 1), ring_phase<2>(u)) || !ws.wait(L::B_SUM, ph)) break;
         if (pt == 0) {
-            w = ve = make_float4(0.f, 0.f, 0.f, 0.f);
+            w = ve = dg = make_float4(0.f, 0.f, 0.f, 0.f);
             dd = 0.f;
         }
 #pragma unroll
@@ -691,7 +696,9 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
             w.x += x.x; w.y += x.y; w.z += x.z; w.w += x.w;
             ve.x += y.x; ve.y += y.y; ve.z += y.z; ve.w += y.w;
         }
-        dd += lanes_sum(lane < 16 ? sums[8 * T + lane] : 0.f);
+        const float4 x = *reinterpret_cast<const float4 *>(sums + 8 * T + 4 * lane);
+        dg.x += x.x; dg.y += x.y; dg.z += x.z; dg.w += x.w;
+        dd += lanes_sum(lane < 16 ? sums[9 * T + lane] : 0.f);
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(ws.bar(L::B_SUME));
@@ -701,6 +708,7 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
             const size_t at = ((size_t)job.b * a.H + h) * a.nc + job.c, plane = (size_t)a.B * a.H * a.nc * T;
             reinterpret_cast<float4 *>(p.own + at * T)[lane] = w;
             reinterpret_cast<float4 *>(p.own + plane + at * T)[lane] = ve;
+            reinterpret_cast<float4 *>(p.own + 2 * plane + at * T)[lane] = dg;
             if (lane == 0) p.dd[at] = dd;
         }
         if (!ws.wait(L::B_Y + (u & 1), ring_phase<2>(u))) break;
@@ -760,13 +768,14 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __g
     for (int c = lo + warp; c < hi; c += kFinishWarps) {
         const Dec &d = *dec_of(a, p.dec, b, h, c);
         const size_t at = unit * a.nc + c;
-        float w[4], vi[4], vo[4], dt[4], sl[4];  // four adjacent tokens
+        float w[4], vi[4], vo[4], dg[4], dt[4], sl[4];  // four adjacent tokens
         auto read = [&](const float *q, float (&v)[4]) {
             const float4 x = reinterpret_cast<const float4 *>(q)[lane];
             v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
         };
         read(own + at * T, w);
         read(own + plane + at * T, vo);
+        read(own + 2 * plane + at * T, dg);
         read(d.dt, dt);
         read(d.slope, sl);
 #pragma unroll
@@ -788,21 +797,21 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __g
             }
         }
         th = lanes_sum(th) * d.end;
-        float suf[4], pre[4], s1 = 0.f, s2 = 0.f;
+        double suf[4], pre[4], s1 = 0., s2 = 0.;  // differences of sums
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
-            s1 += fmaf(-dt[i], vo[i], w[i]);
+            s1 += (double)w[i] - (double)dt[i] * vo[i];
             suf[i] = s1;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             pre[i] = s2;
-            s2 = fmaf(dt[i], vi[i], s2);
+            s2 += (double)dt[i] * vi[i];
         }
-        float xs = s1, xp = s2;
+        double xs = s1, xp = s2;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
+            const double us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
             if (lane + o < 32) xs += us;
             if (lane >= o) xp += up;
         }
@@ -811,7 +820,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __g
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = c * T + 4 * lane + i;
-            const float da = th + (suf[i] + xs) + (pre[i] + xp), g = fmaf(A, da, vo[i] + vi[i]) * sl[i];
+            const float da = (float)(th + (suf[i] + xs) + (pre[i] + xp)), g = fmaf(A, da, (vo[i] + dg[i]) + vi[i]) * sl[i];
             if (t < len) {
                 static_cast<__nv_bfloat16 *>(a.ddt.p)[(size_t)b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)t * a.ddt.st] = __float2bfloat16_rn(g);
                 sA = fmaf(da, dt[i], sA);

@@ -51,7 +51,7 @@ size_t tc_space(Args &a, bool backward, uint8_t *base) {
         a.inter = take(2 * plan.PT * 4 * heads * a.nc * T);
         a.aside = take(heads * plan.PT * a.nc * 8192);
         a.dots = take(heads * a.nc * plan.PT * 16);
-        a.own = take(2 * heads * a.nc * T);
+        a.own = take(3 * heads * a.nc * T);
         a.dd = take(heads * a.nc);
         a.splits = tc_splits(a);
         a.dbc = take(a.splits > 1 ? (size_t)a.splits * 2 * a.B * a.G * a.n * a.N : 0);

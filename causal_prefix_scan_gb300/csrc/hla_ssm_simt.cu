@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) ssm_out_kernel(const Args a) {
 template <typename T, int Q>
 __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ float dt[Q], slope[Q], w[Q], ve[Q], vg[Q], red[8];
+    __shared__ float dt[Q], slope[Q], w[Q], ve[Q], vg[Q], diag[Q], red[8];
     __shared__ Decay s[Q];
     const int split = blockIdx.x % a.splits, c = blockIdx.x / a.splits % a.nc, g = blockIdx.x / a.splits / a.nc % a.G,
               b = blockIdx.x / a.splits / a.nc / a.G;
@@ -202,7 +202,10 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
                 const float L = j <= t ? factor(s[t], s[j]) : 0.f, m = CB[t * ldq + j] * L;
                 M[t * ldq + j] = j <= t ? m : 0.f;
                 S[t * ldq + j] = j <= t ? x * L : 0.f;
-                E[t * ldq + j] = j <= t ? m * x : 0.f;
+                // E's diagonal is kept apart: it cancels in the gradient of the decays, which differences of
+                // E's sums give, and where decays are steep it is most of them
+                E[t * ldq + j] = j < t ? m * x : 0.f;
+                if (j == t) diag[t] = m * x;
             });
         });
         // dY h^T: its share of dC, and of w
@@ -306,23 +309,23 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
         if (warp == 0) {
             // suffix sums of w - dt vE (the token among them), prefix sums of dt vg (without it)
             constexpr int PER = Q / 32;
-            float suf[PER], pre[PER], a_suf = 0.f, a_pre = 0.f;
+            double suf[PER], pre[PER], a_suf = 0., a_pre = 0.;
 #pragma unroll
             for (int i = PER - 1; i >= 0; --i) {
                 const int t = lane * PER + i;
-                a_suf += w[t] - dt[t] * ve[t];
+                a_suf += (double)w[t] - (double)dt[t] * ve[t];
                 suf[i] = a_suf;
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int t = lane * PER + i;
                 pre[i] = a_pre;
-                a_pre += dt[t] * vg[t];
+                a_pre += (double)dt[t] * vg[t];
             }
-            float xs = a_suf, xp = a_pre;
+            double xs = a_suf, xp = a_pre;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
+                const double us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
                 if (lane + o < 32) xs += us;
                 if (lane >= o) xp += up;
             }
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int t = lane * PER + i;
-                const float da = through + (suf[i] + xs) + (pre[i] + xp), d = (fmaf(A, da, ve[t] + vg[t])) * slope[t];
+                const float da = (float)(through + (suf[i] + xs) + (pre[i] + xp)), d = fmaf(A, da, (ve[t] + diag[t]) + vg[t]) * slope[t];
                 if (t < live) {
                     tile::st_t(static_cast<T *>(a.ddt.p) + (size_t)b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)(t0 + t) * a.ddt.st, 0, d);
                     sA = fmaf(da, dt[t], sA);
