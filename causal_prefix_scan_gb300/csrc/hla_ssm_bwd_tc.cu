@@ -42,11 +42,11 @@ struct LayStates {
     static constexpr int OFF_X = 0, OFF_Y = NX * kHalf, OFF_P = OFF_Y + kHalf, OFF_Q = OFF_P + NB * kHalf, OFF_W = OFF_Q + NB * kHalf,
                          OFF_H = OFF_W + 3 * kHalf, OFF_DEC = OFF_H + 3 * HB, OFF_BAR = OFF_DEC + NX * kDecBytes;
     static constexpr int B_X = 0, B_XE = B_X + NX, B_Y = B_XE + NX, B_YE = B_Y + 1, B_P = B_YE + 1, B_PE = B_P + 1, B_Q = B_PE + 1, B_QE = B_Q + 1,
-                         B_W = B_QE + 1, B_D = B_W + 1, B_Z = B_D + 1, B_SE = B_Z + 1, B_FIN = B_SE + 1, B_RAWX = B_FIN + 1, B_RAWY = B_RAWX + 1,
+                         B_W = B_QE + 1, B_H = B_W + 1, B_D = B_H + 1, B_Z = B_D + 1, B_SE = B_Z + 1, B_FIN = B_SE + 1, B_RAWX = B_FIN + 1, B_RAWY = B_RAWX + 1,
                          B_RAWB = B_RAWY + 1, NBAR = B_RAWB + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
     static constexpr uint32_t D = 0, Z = 192;  // TMEM columns
-    HLA_DEVICE static int arrivals(int i) { return (i >= B_XE && i < B_Y) || i == B_YE || i == B_W ? kElemWarps : 1; }
+    HLA_DEVICE static int arrivals(int i) { return (i >= B_XE && i < B_Y) || i == B_YE || i == B_W || i == B_H ? kElemWarps : 1; }
 };
 struct StatesParams {
     Params p;
@@ -96,31 +96,42 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
     };
     auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + (k & 1) * kDecBytes); };
     auto aside = [&](int c) { return sp.aside + ((unit * p.plan.PT + w.pt) * a.nc + c) * 2048 + threadIdx.x; };
-    float ahead = 1.f;
-    auto prepare = [&](int k) {  // the state before (the gradient behind) the chunk, and the rows that enter it
-        const int c = z.chunk(k);
+    // The rows that enter do not depend on the state: they are scaled a visit ahead, while the state meets
+    // Q, and their product runs while the next state is split (a visit 5500 -> 3300 clocks).
+    auto scale = [&](int k) {
+        if (!ws.wait(L::B_X + (k & 1), ring_phase<2>(k))) return false;
+        const Dec &d = dec(k);
+        scale_split16(base + L::OFF_X + (k & 1) * kHalf, base + L::OFF_W, row, c0, z.dir(k) ? d.to[row] : d.w[row]);
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_W));
+        return true;
+    };
+    begin(0);
+    bool ok = visits == 0 || scale(0);
+#pragma unroll 1
+    for (int k = 0; k < visits && ok; ++k) {
+        const uint32_t ph = (uint32_t)k & 1u;
+        const int c = z.chunk(k), dir = z.dir(k);
+        const Dec &d = dec(k);
+        // the state before (the gradient behind) the chunk
         if (k == z.K) begin(1);
         float4 h[4];
+        if (k > 0 && !(ok = ws.wait(L::B_SE, ph ^ 1u))) break;
         if (holds) {
-            if (k >= z.K) {
+            if (dir) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = aside(c)[512 * i];
             }
             store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0, carry);
             store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0 + 8, carry + 4);
-            if (k < z.K) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) aside(c)[512 * i] = make_float4(carry[2 * i].x, carry[2 * i].y, carry[2 * i + 1].x, carry[2 * i + 1].y);
-            }
         }
-        if (!ws.wait(L::B_X + (k & 1), ring_phase<2>(k))) return false;
-        const Dec &d = dec(k);
-        scale_split16(base + L::OFF_X + (k & 1) * kHalf, base + L::OFF_W, row, c0, z.dir(k) ? d.to[row] : d.w[row]);
-        ahead = d.end;
         fence_async_smem();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ws.bar(L::B_W));
-        if (k >= z.K) {
+        if (lane == 0) mbar_arrive(ws.bar(L::B_H));
+        if (dir) {
             float s = 0.f;
             if (holds) {
 #pragma unroll
@@ -133,41 +144,34 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
             }
             s = lanes_sum(s);
             if (lane == 0) sp.dots[((unit * a.nc + c) * p.plan.PT + w.pt) * 16 + warp] = s;
+        } else if (holds) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) aside(c)[512 * i] = make_float4(carry[2 * i].x, carry[2 * i].y, carry[2 * i + 1].x, carry[2 * i + 1].y);
         }
-        return true;
-    };
-    begin(0);
-    bool ok = visits == 0 || prepare(0);
-#pragma unroll 1
-    for (int k = 0; k < visits && ok; ++k) {
-        const uint32_t ph = (uint32_t)k & 1u;
-        const float end = ahead;
         if (!(ok = ws.wait(L::B_D, ph))) break;
         tc_fence_after();
         float2 v[8];
         if (holds) {
             load_parts16(lanes + L::D + c0, v);
+            const float end = d.end;
 #pragma unroll
             for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], v[i]);
         }
+        if (k + 1 < visits && !(ok = scale(k + 1))) break;
         if (!(ok = ws.wait(L::B_Y, ph) && ws.wait(L::B_Z, ph))) break;
         tc_fence_after();
         load_parts16(lanes + L::Z + c0, v);
         {
             float2 y[8];
             load_row16(base + L::OFF_Y, T, row, c0, y);
-            const Dec &d = dec(k);
-            const int dir = z.dir(k);
             const float f = dir ? factor(d.s[T - 1], d.s[row]) : d.to[row];
-            sp.inter[((size_t)(dir * p.plan.PT + w.pt) * 4 + cq) * plane + (unit * a.nc + z.chunk(k)) * T + row] = f * dot16(v, y);
+            sp.inter[((size_t)(dir * p.plan.PT + w.pt) * 4 + cq) * plane + (unit * a.nc + c) * T + row] = f * dot16(v, y);
         }
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(ws.bar(L::B_YE));
             mbar_arrive(ws.bar(L::B_XE + (k & 1)));
         }
-        if (k + 1 < visits) ok = ws.wait(L::B_SE, ph) && prepare(k + 1);
     }
     if (visits == 0) begin(1);  // (no tokens: the gradient passes as it is)
     if (ok && w.piece == 0 && a.d_state_in && holds) store_state(a, a.d_state_in + unit * NP, row, col, carry);
@@ -187,7 +191,8 @@ __device__ __forceinline__ void states_mma(const Waits &ws, uint8_t *base, uint3
         mma_state(tb + L::D, P, W, false);
         umma_commit_warp(ws.bar(L::B_D));
         umma_commit_warp(ws.bar(L::B_PE));
-        if (!ws.wait(L::B_Q, ph)) break;
+        if (!ws.wait(L::B_H, ph) || !ws.wait(L::B_Q, ph)) break;
+        tc_fence_after();
         mma_km64(tb + L::Z, Q, H, id, false);
         if (NB > 1) mma_km64(tb + L::Z, Q + kBlock, H + kRows64, id, true);
         umma_commit_warp(ws.bar(L::B_Z));
@@ -250,7 +255,7 @@ __device__ __forceinline__ void states_load(const StatesParams &sp, const Waits 
             }
             __syncwarp();
             if (clear) ok = clear_landed(ws, L::B_RAWY, raw, L::B_Y, base + L::OFF_Y, 1, w.len - t0);
-            if (!ok || !(ok = ws.wait(L::B_W, (uint32_t)k & 1u))) {
+            if (!ok || !(ok = ws.wait(L::B_H, (uint32_t)k & 1u))) {
                 ++k;
                 break;
             }
@@ -328,7 +333,7 @@ struct LayGrad {
     static constexpr int OFF_B = 0, OFF_C = NB * kHalf, OFF_S = 2 * NB * kHalf, OFF_XD = OFF_S + 2 * kHalf, OFF_H = OFF_XD + NS * kHalf,
                          OFF_G = OFF_H + HB;
     static constexpr int OFF_DEC = OFF_G + HB, OFF_SUM = OFF_DEC + 2 * (int)sizeof(Dec);
-    static constexpr int SUM_FLOATS = 9 * T + 16;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], E's diagonal [128], dD [16]
+    static constexpr int SUM_FLOATS = 13 * T;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], [dY.X by columns' quarter][4][128], C.B [128]
     static constexpr int OFF_BAR = OFF_SUM + SUM_FLOATS * 4;
     static constexpr int B_XD = 0, B_XDE = B_XD + NS, B_DEC = B_XDE + NS, B_DECE = B_DEC + 2, B_H = B_DECE + 2, B_HE = B_H + 1,
                          B_G = B_HE + 1, B_GE = B_G + 1, B_BC = B_GE + 1, B_CB = B_BC + 1, B_DYX = B_CB + 1, B_DE = B_DYX + 1,
@@ -380,6 +385,12 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         tmem_wait_ld();
     }
     tc_fence_before();
+    if (cq == q) {  // this row's own
+        float c = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c = lane == 2 * i ? cb[i].x : lane == 2 * i + 1 ? cb[i].y : c;
+        sums[12 * T + row] = c;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(ws.bar(L::B_DE));  // the products' columns are free
     uint8_t *S = base + L::OFF_S;
@@ -397,7 +408,7 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         const Decay s = d.s[row];
         const float dt = d.dt[row];
         uint32_t pk[16];
-        float ve = 0.f, diag = 0.f;
+        float ve = 0.f;
         if (active && ok) {
             const Decay first = d.s[32 * cq];
             const bool plain = cq > q || first.hi - d.s[32 * cq + 31].hi <= kBlockRange;
@@ -423,10 +434,10 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
                     f.x = bits & (1u << (16 * g + 2 * i)) ? f.x : 0.f;  // (above the diagonal a factor may be anything)
                     f.y = bits & (2u << (16 * g + 2 * i)) ? f.y : 0.f;
                     const float2 m = mul2(cb[8 * g + i], f), sv = mul2(v[i], f), ee = mul2(m, v[i]);
-                    // E's diagonal is kept apart: it cancels in the gradient of the decays, which differences
-                    // of these sums give, and where decays are steep it is most of them
+                    // E's diagonal, C.B dY.X of one token, is formed apart: it cancels in the gradient of the
+                    // decays, which differences of these sums give, and where decays are steep it is most of
+                    // them (within the sums: dA 2.0e-6 off, dt_bias 8.5e-6, b2 n8192; apart 4.7e-7, 1.2e-6)
                     const float ex = past & (1u << (16 * g + 2 * i)) ? ee.x : 0.f, ey = past & (2u << (16 * g + 2 * i)) ? ee.y : 0.f;
-                    diag += (ee.x - ex) + (ee.y - ey);
                     ve += ex + ey;
                     e[2 * i] = ex * dt;
                     e[2 * i + 1] = ey * dt;
@@ -446,7 +457,6 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
             sum_w[lane] = 0.f;
         }
         sum_ve[row] = ve;
-        if (cq == q) sums[8 * T + row] = diag;
         quad_sync(q);  // every warp of these rows has read its columns of the product that M^T overwrites
         tc_fence_after();
         tmem_st16(lanes + L::M + 16 * cq, reinterpret_cast<float(&)[16]>(pk));
@@ -473,12 +483,11 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
             tmem_st8(lanes + L::YT + 8 * cq, ty);
             tmem_st8(lanes + L::XT + 8 * cq, tx);
         }
-        const float dd = lanes_sum(dot16(xr, yr));
+        sums[(8 + cq) * T + row] = dot16(xr, yr);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            sums[9 * T + warp] = dd;
             mbar_arrive(ws.bar(L::B_YT));
             mbar_arrive(ws.bar(L::B_XDE + sy));
             mbar_arrive(ws.bar(L::B_SUM));
@@ -696,9 +705,15 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
             w.x += x.x; w.y += x.y; w.z += x.z; w.w += x.w;
             ve.x += y.x; ve.y += y.y; ve.z += y.z; ve.w += y.w;
         }
-        const float4 x = *reinterpret_cast<const float4 *>(sums + 8 * T + 4 * lane);
-        dg.x += x.x; dg.y += x.y; dg.z += x.z; dg.w += x.w;
-        dd += lanes_sum(lane < 16 ? sums[9 * T + lane] : 0.f);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 8; k < 12; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(sums + k * T + 4 * lane);
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+        const float4 x = *reinterpret_cast<const float4 *>(sums + 12 * T + 4 * lane);
+        dg.x = fmaf(x.x, s.x, dg.x); dg.y = fmaf(x.y, s.y, dg.y); dg.z = fmaf(x.z, s.z, dg.z); dg.w = fmaf(x.w, s.w, dg.w);
+        dd += (s.x + s.y) + (s.z + s.w);
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(ws.bar(L::B_SUME));
@@ -709,6 +724,7 @@ __device__ __forceinline__ void grad_sums(const GradParams &p, const Waits &ws, 
             reinterpret_cast<float4 *>(p.own + at * T)[lane] = w;
             reinterpret_cast<float4 *>(p.own + plane + at * T)[lane] = ve;
             reinterpret_cast<float4 *>(p.own + 2 * plane + at * T)[lane] = dg;
+            dd = lanes_sum(dd);
             if (lane == 0) p.dd[at] = dd;
         }
         if (!ws.wait(L::B_Y + (u & 1), ring_phase<2>(u))) break;
@@ -797,30 +813,32 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __g
             }
         }
         th = lanes_sum(th) * d.end;
-        double suf[4], pre[4], s1 = 0., s2 = 0.;  // differences of sums
+        float suf[4], pre[4], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
-            s1 += (double)w[i] - (double)dt[i] * vo[i];
+            s1 += fmaf(-dt[i], vo[i], w[i]);
             suf[i] = s1;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             pre[i] = s2;
-            s2 += (double)dt[i] * vi[i];
+            s2 = fmaf(dt[i], vi[i], s2);
         }
-        double xs = s1, xp = s2;
+        float xs = s1, xp = s2;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
+            const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
             if (lane + o < 32) xs += us;
             if (lane >= o) xp += up;
         }
-        xs -= s1;
-        xp -= s2;
+        xs = __shfl_down_sync(0xffffffffu, xs, 1);  // of the lanes behind, in front
+        xp = __shfl_up_sync(0xffffffffu, xp, 1);
+        if (lane == 31) xs = 0.f;
+        if (lane == 0) xp = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = c * T + 4 * lane + i;
-            const float da = (float)(th + (suf[i] + xs) + (pre[i] + xp)), g = fmaf(A, da, (vo[i] + dg[i]) + vi[i]) * sl[i];
+            const float da = th + (suf[i] + xs) + (pre[i] + xp), g = fmaf(A, da, (vo[i] + dg[i]) + vi[i]) * sl[i];
             if (t < len) {
                 static_cast<__nv_bfloat16 *>(a.ddt.p)[(size_t)b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)t * a.ddt.st] = __float2bfloat16_rn(g);
                 sA = fmaf(da, dt[i], sA);

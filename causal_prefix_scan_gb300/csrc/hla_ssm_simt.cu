@@ -309,34 +309,36 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
         if (warp == 0) {
             // suffix sums of w - dt vE (the token among them), prefix sums of dt vg (without it)
             constexpr int PER = Q / 32;
-            double suf[PER], pre[PER], a_suf = 0., a_pre = 0.;
+            float suf[PER], pre[PER], a_suf = 0.f, a_pre = 0.f;
 #pragma unroll
             for (int i = PER - 1; i >= 0; --i) {
                 const int t = lane * PER + i;
-                a_suf += (double)w[t] - (double)dt[t] * ve[t];
+                a_suf += fmaf(-dt[t], ve[t], w[t]);
                 suf[i] = a_suf;
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int t = lane * PER + i;
                 pre[i] = a_pre;
-                a_pre += (double)dt[t] * vg[t];
+                a_pre = fmaf(dt[t], vg[t], a_pre);
             }
-            double xs = a_suf, xp = a_pre;
+            float xs = a_suf, xp = a_pre;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
+                const float us = __shfl_down_sync(0xffffffffu, xs, o), up = __shfl_up_sync(0xffffffffu, xp, o);
                 if (lane + o < 32) xs += us;
                 if (lane >= o) xp += up;
             }
-            xs -= a_suf;
-            xp -= a_pre;
+            xs = __shfl_down_sync(0xffffffffu, xs, 1);  // of the lanes behind, in front
+            xp = __shfl_up_sync(0xffffffffu, xp, 1);
+            if (lane == 31) xs = 0.f;
+            if (lane == 0) xp = 0.f;
             float sA = 0.f, sb = 0.f;
             const float A = a.A[h];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int t = lane * PER + i;
-                const float da = (float)(through + (suf[i] + xs) + (pre[i] + xp)), d = fmaf(A, da, (ve[t] + diag[t]) + vg[t]) * slope[t];
+                const float da = through + (suf[i] + xs) + (pre[i] + xp), d = fmaf(A, da, (ve[t] + diag[t]) + vg[t]) * slope[t];
                 if (t < live) {
                     tile::st_t(static_cast<T *>(a.ddt.p) + (size_t)b * a.ddt.sb + (size_t)h * a.ddt.sh + (size_t)(t0 + t) * a.ddt.st, 0, d);
                     sA = fmaf(da, dt[t], sA);
