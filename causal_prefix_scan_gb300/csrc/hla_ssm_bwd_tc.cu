@@ -37,10 +37,10 @@ using namespace tcs;
 constexpr int kStatesThreads = 20 * 32, kWarpLoadBc = 19;
 template <int NB>
 struct LayStates {
-    static constexpr int NX = 2;                   // stages of the rows that enter, with the weights
+    static constexpr int NX = 2, ND = 4;           // stages of the rows that enter, of the weights
     static constexpr int HB = NB * kHalf / 2;      // one part of a state
     static constexpr int OFF_X = 0, OFF_Y = NX * kHalf, OFF_P = OFF_Y + kHalf, OFF_Q = OFF_P + NB * kHalf, OFF_W = OFF_Q + NB * kHalf,
-                         OFF_H = OFF_W + 3 * kHalf, OFF_DEC = OFF_H + 3 * HB, OFF_BAR = OFF_DEC + NX * kDecBytes;
+                         OFF_H = OFF_W + 3 * kHalf, OFF_DEC = OFF_H + 3 * HB, OFF_BAR = OFF_DEC + ND * kDecBytes;
     static constexpr int B_X = 0, B_XE = B_X + NX, B_Y = B_XE + NX, B_YE = B_Y + 1, B_P = B_YE + 1, B_PE = B_P + 1, B_Q = B_PE + 1, B_QE = B_Q + 1,
                          B_W = B_QE + 1, B_H = B_W + 1, B_D = B_H + 1, B_Z = B_D + 1, B_SE = B_Z + 1, B_FIN = B_SE + 1, B_RAWX = B_FIN + 1, B_RAWY = B_RAWX + 1,
                          B_RAWB = B_RAWY + 1, NBAR = B_RAWB + 1;
@@ -62,6 +62,7 @@ struct Walk {  // 2 K visits to the chunks of a piece
     HLA_DEVICE int chunk(int k) const { return k < K ? w.lo + k : w.hi - 1 - (k - K); }
 };
 
+HLA_DEVICE void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 HLA_DEVICE float dot16(const float2 (&x)[8], const float2 (&y)[8]) {
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -94,7 +95,7 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
         const float *init = dir ? a.d_state_out : a.state_in;
         load_state(a, p.plan.pieces > 1 && w.used > 0 ? piece_state(p, dir, w) : init ? init + unit * NP : nullptr, row, col, carry);
     };
-    auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + (k & 1) * kDecBytes); };
+    auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + k % L::ND * kDecBytes); };
     auto aside = [&](int c) { return sp.aside + ((unit * p.plan.PT + w.pt) * a.nc + c) * 2048 + threadIdx.x; };
     // The rows that enter do not depend on the state: they are scaled a visit ahead, while the state meets
     // Q, and their product runs while the next state is split (a visit 5500 -> 3300 clocks).
@@ -105,7 +106,10 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ws.bar(L::B_W));
+        if (lane == 0) {
+            mbar_arrive(ws.bar(L::B_W));
+            mbar_arrive(ws.bar(L::B_XE + (k & 1)));  // (every warp is also through with visit k - 2, whose weights leave next)
+        }
         return true;
     };
     begin(0);
@@ -157,6 +161,10 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
 #pragma unroll
             for (int i = 0; i < 8; ++i) carry[i] = fma2(both(end), carry[i], v[i]);
         }
+        if (k + 1 >= z.K && k + 1 < visits && holds) {  // laid aside long ago
+#pragma unroll
+            for (int i = 0; i < 4; ++i) prefetch_l2(aside(z.chunk(k + 1)) + 512 * i);
+        }
         if (k + 1 < visits && !(ok = scale(k + 1))) break;
         if (!(ok = ws.wait(L::B_Y, ph) && ws.wait(L::B_Z, ph))) break;
         tc_fence_after();
@@ -168,10 +176,7 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
             sp.inter[((size_t)(dir * p.plan.PT + w.pt) * 4 + cq) * plane + (unit * a.nc + c) * T + row] = f * dot16(v, y);
         }
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(ws.bar(L::B_YE));
-            mbar_arrive(ws.bar(L::B_XE + (k & 1)));
-        }
+        if (lane == 0) mbar_arrive(ws.bar(L::B_YE));
     }
     if (visits == 0) begin(1);  // (no tokens: the gradient passes as it is)
     if (ok && w.piece == 0 && a.d_state_in && holds) store_state(a, a.d_state_in + unit * NP, row, col, carry);
@@ -238,7 +243,7 @@ __device__ __forceinline__ void states_load(const StatesParams &sp, const Waits 
     if (warp == kWarpTma) {
         stream<1, L::NX>(ws, visits, L::B_X, L::B_XE, L::B_RAWX, base + L::OFF_X, w.len, first, [&](int k, uint8_t *t, uint64_t *bar) {
             mbar_expect_tx(bar, kHalf + kDecBytes);
-            bulk_load(base + L::OFF_DEC + (k & 1) * kDecBytes, dec_of(a, p.dec, w.b, w.h, z.chunk(k)), kDecBytes, bar);
+            bulk_load(base + L::OFF_DEC + k % L::ND * kDecBytes, dec_of(a, p.dec, w.b, w.h, z.chunk(k)), kDecBytes, bar);
             load_tile<1>(t, &p.mx[z.dir(k)], p.vx[z.dir(k)], bar, 64 * w.pt, first(k), w.h, w.b);
         });
     } else if (warp == kWarpTmaX) {  // the rows that meet the state; the state's image leaves in between
