@@ -128,8 +128,8 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = aside(c)[512 * i];
             }
-            store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0, carry);
-            store_split8(base + L::OFF_H, L::HB, 64 * NB, row, c0 + 8, carry + 4);
+            store_split8<true>(base + L::OFF_H, L::HB, 64 * NB, row, c0, carry);
+            store_split8<true>(base + L::OFF_H, L::HB, 64 * NB, row, c0 + 8, carry + 4);
         }
         fence_async_smem();
         tc_fence_before();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kStatesThreads, 1) ssm_states_kernel(const __g
     using L = LayStates<NB>;
     extern __shared__ __align__(1024) uint8_t base[];
     Walk z;
-    z.w = piece_of(sp.p.a, sp.p.plan, blockIdx.x, 1);
+    z.w = piece_of(sp.p.a, sp.p.plan, blockIdx.x);
     if (z.w.piece >= max(z.w.used, 1)) return;
     z.K = z.w.hi - z.w.lo;
     Cta<L::NBAR> cta(base, L::OFF_BAR, sp.p.a.err, [](int i) { return L::arrivals(i); });

@@ -80,8 +80,10 @@ HLA_DEVICE bool clear_landed(const Waits &ws, int raw, uint32_t &phase, int bar,
 }
 
 // ------------------------------------------------------------ sums of pieces
-// HB heads of a group go through a piece together and share its tiles of B: those are twice the
-// bytes of a head's X, and what an SM takes in bounds the kernel.
+// Shared memory bounds the kernel: a chunk's tiles, weighted parts and products' operands are 190 KB
+// in and out of it, 1,500 of the 1,900 cycles that a chunk takes.  (Two heads of a group through one
+// CTA share B's tiles, but leave half as many CTAs: n16384 h64 p64 s128 82 us against 74, b2 n8192 h32
+// both ways 60 against 39.)
 constexpr int kSumThreads = 19 * 32;
 template <int NB>
 struct LaySum {
@@ -93,15 +95,15 @@ struct LaySum {
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
 };
 
-template <int NB, int HB>
+template <int NB>
 __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_constant__ Params p) {
     using L = LaySum<NB>;
     extern __shared__ __align__(1024) uint8_t base[];
     const Args &a = p.a;
     const int dir = gridDim.y == 2 ? blockIdx.y : 0;
-    const Piece w = piece_of(a, p.plan, blockIdx.x, HB);  // of heads w.h .. w.h + HB - 1
+    const Piece w = piece_of(a, p.plan, blockIdx.x);
     if (dir ? w.piece == 0 || w.piece >= w.used : w.piece + 1 >= w.used) return;  // no piece starts from it
-    const int K = w.hi - w.lo, steps = K * HB;
+    const int K = w.hi - w.lo;
     auto chunk = [&](int k) { return dir ? w.lo + k : w.hi - 1 - k; };  // towards larger decays
     Cta<L::NBAR> cta(base, L::OFF_BAR, a.err, [](int i) {
         return (i >= L::B_W && i < L::B_WE) || (i >= L::B_XE && i < L::B_R) ? kElemWarps : 1;
@@ -110,13 +112,13 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
     const int warp = cta.warp, lane = threadIdx.x & 31;
     if (warp == kWarpTma || warp == kWarpTmaX) {  // B; X and its weights: neither waits for the other's slots
         const bool is_x = warp == kWarpTmaX;
-        const int loads = is_x ? steps : K, NS = is_x ? L::NX : L::NR, full = is_x ? L::B_X : L::B_R, empty = is_x ? L::B_XE : L::B_RE;
+        const int NS = is_x ? L::NX : L::NR, full = is_x ? L::B_X : L::B_R, empty = is_x ? L::B_XE : L::B_RE;
         uint32_t raw = 0;
         int i = 0;
         bool ok = true;
 #pragma unroll 1
-        for (; i < loads && ok; ++i) {
-            const int s = i % NS, c = chunk(is_x ? i / HB : i), t0 = c * T, h = w.h + (is_x ? i % HB : 0);
+        for (; i < K && ok; ++i) {
+            const int s = i % NS, c = chunk(i), t0 = c * T;
             const bool clear = w.len - t0 < T;
             if (i >= NS && !(ok = ws.wait(empty + s, ((uint32_t)(i / NS) & 1u) ^ 1u))) break;
             uint8_t *t = base + (is_x ? L::OFF_X + s * kHalf : L::OFF_R + s * NB * kHalf);
@@ -124,8 +126,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
                 uint64_t *bar = ws.bar(!clear ? full + s : is_x ? L::B_RAWX : L::B_RAW);
                 if (is_x) {
                     mbar_expect_tx(bar, kHalf + kDecBytes);
-                    bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, h, c), kDecBytes, bar);
-                    load_tile<1>(t, &p.mx[dir], p.vx[dir], bar, 64 * w.pt, t0, h, w.b);
+                    bulk_load(base + L::OFF_DEC + s * kDecBytes, dec_of(a, p.dec, w.b, w.h, c), kDecBytes, bar);
+                    load_tile<1>(t, &p.mx[dir], p.vx[dir], bar, 64 * w.pt, t0, w.h, w.b);
                 } else {
                     mbar_expect_tx(bar, NB * kHalf);
                     load_tile<NB>(t, &p.mb[dir], p.vb[dir], bar, 0, t0, w.h / a.R, w.b);
@@ -141,13 +143,13 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
     } else if (warp == kWarpMma) {
         const uint32_t tb = uniform(cta.tb);
         bool ok = true;
-        for (int i = 0; i < steps && ok; ++i) {
-            const int k = i / HB, j = i % HB, rs = k % L::NR;
-            if (!(ok = ws.wait(L::B_R + rs, ring_phase<L::NR>(k)) && ws.wait(L::B_W + (i & 1), (uint32_t)(i >> 1) & 1u))) break;
+        for (int i = 0; i < K && ok; ++i) {
+            const int rs = i % L::NR;
+            if (!(ok = ws.wait(L::B_R + rs, ring_phase<L::NR>(i)) && ws.wait(L::B_W + (i & 1), (uint32_t)(i >> 1) & 1u))) break;
             tc_fence_after();
-            mma_state(tb + j * 192, mnmajor(base + L::OFF_R + rs * NB * kHalf), mnmajor(base + L::OFF_W + (i & 1) * 3 * kHalf), k > 0);
+            mma_state(tb, mnmajor(base + L::OFF_R + rs * NB * kHalf), mnmajor(base + L::OFF_W + (i & 1) * 3 * kHalf), i > 0);
             umma_commit_warp(ws.bar(L::B_WE + (i & 1)));
-            if (j == HB - 1) umma_commit_warp(ws.bar(L::B_RE + rs));
+            umma_commit_warp(ws.bar(L::B_RE + rs));
         }
         if (ok) umma_commit_warp(ws.bar(L::B_OUT));
         umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
@@ -155,23 +157,16 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
         __syncwarp();
     } else {
         const int q = warp & 3, cq = warp >> 2, row = 32 * q + lane;
-        float off[HB];  // decay between the chunk and the piece's end (backward its start)
-#pragma unroll
-        for (int j = 0; j < HB; ++j) off[j] = 1.f;
+        float off = 1.f;  // decay between the chunk and the piece's end (backward its start)
         bool ok = true;
 #pragma unroll 1
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % L::NX, e = i & 1, head = i % HB;
+        for (int i = 0; i < K; ++i) {
+            const int s = i % L::NX, e = i & 1;
             if (!(ok = ws.wait(L::B_X + s, ring_phase<L::NX>(i)))) break;
             if (i >= 2 && !(ok = ws.wait(L::B_WE + e, (uint32_t)((i >> 1) & 1) ^ 1u))) break;
             const Dec &d = *reinterpret_cast<const Dec *>(base + L::OFF_DEC + s * kDecBytes);
-            float f = dir ? d.to[row] : d.w[row];
-#pragma unroll
-            for (int j = 0; j < HB; ++j)
-                if (j == head) {
-                    f *= off[j];
-                    off[j] *= d.end;
-                }
+            const float f = off * (dir ? d.to[row] : d.w[row]);
+            off *= d.end;
             scale_split16(base + L::OFF_X + s * kHalf, base + L::OFF_W + e * 3 * kHalf, row, 16 * cq, f);
             fence_async_smem();
             __syncwarp();
@@ -181,53 +176,50 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
             }
         }
         // (backward the piece that the forward walk leaves out)
-        if (ok && threadIdx.x == 0 && w.pt == 0 && (dir == 0 || w.piece + 1 == w.used)) {
-#pragma unroll
-            for (int j = 0; j < HB; ++j) p.factor[((size_t)w.b * a.H + w.h + j) * p.plan.pieces + w.piece] = off[j];
-        }
+        if (ok && threadIdx.x == 0 && w.pt == 0 && (dir == 0 || w.piece + 1 == w.used)) p.factor[((size_t)w.b * a.H + w.h) * p.plan.pieces + w.piece] = off;
         if (ok && ws.wait(L::B_OUT, 0u)) {
             tc_fence_after();
             if (q < 2 * NB) {
-#pragma unroll
-                for (int j = 0; j < HB; ++j) {
-                    float2 v[8];
-                    load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + j * 192 + 16 * cq, v);
-                    Piece u = w;
-                    u.h += j;
-                    store_state(a, piece_state(p, dir, u), row, 64 * w.pt + 16 * cq, v);
-                }
+                float2 v[8];
+                load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + 16 * cq, v);
+                store_state(a, piece_state(p, dir, w), row, 64 * w.pt + 16 * cq, v);
             }
         }
     }
     cta.finish();
 }
 
-// Sums to the states that pieces start from, in place: blockIdx.y 0 from the first piece on, 1 from
-// the last one back.
+// Sums to the states that pieces start from, in place, four elements a thread: blockIdx.y 0 from the
+// first piece on, 1 from the last one back.
 static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid_constant__ Params p) {
     const Args &a = p.a;
-    const int NP = a.N * a.P, blocks = (NP + 255) / 256, e = blockIdx.x % blocks * 256 + threadIdx.x, u = blockIdx.x / blocks;
-    if (e >= NP) return;
+    const int NP = a.N * a.P, blocks = (NP + 1023) / 1024, e = blockIdx.x % blocks * 1024 + 4 * threadIdx.x, u = blockIdx.x / blocks;
+    if (e >= NP) return;  // (N and P are multiples of 8)
     const int dir = blockIdx.y, chunks = (clamp_length(a.lengths, u / a.H, a.n) + T - 1) / T;
     const int used = (chunks + p.plan.per - 1) / p.plan.per;
     const float *init = dir ? a.d_state_out : a.state_in;
-    float *s = p.pieces[dir] + (size_t)u * p.plan.pieces * NP + e, h = init ? init[(size_t)u * NP + e] : 0.f;
+    float4 *s = reinterpret_cast<float4 *>(p.pieces[dir] + (size_t)u * p.plan.pieces * NP + e), h = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (init) {  // (on any float)
+        init += (size_t)u * NP + e;
+        h = make_float4(init[0], init[1], init[2], init[3]);
+    }
     const float *f = p.factor + (size_t)u * p.plan.pieces;
     constexpr int U = 8;
     for (int i = 0; i < used; i += U) {
-        float v[U], g[U];
+        float4 v[U];
+        float g[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (i + k + 1 < used) {  // the last piece of the walk hands on nothing
                 const int c = dir ? used - 1 - i - k : i + k;
-                v[k] = s[(size_t)c * NP];
+                v[k] = s[(size_t)c * (NP / 4)];
                 g[k] = f[c];
             }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (i + k >= used) break;
-            s[(size_t)(dir ? used - 1 - i - k : i + k) * NP] = h;
-            if (i + k + 1 < used) h = fmaf(g[k], h, v[k]);
+            s[(size_t)(dir ? used - 1 - i - k : i + k) * (NP / 4)] = h;
+            if (i + k + 1 < used) h = make_float4(fmaf(g[k], h.x, v[k].x), fmaf(g[k], h.y, v[k].y), fmaf(g[k], h.z, v[k].z), fmaf(g[k], h.w, v[k].w));
         }
     }
 }
@@ -512,7 +504,7 @@ template <int NB>
 __global__ void __launch_bounds__(kCarryThreads, 1) ssm_carry_kernel(const __grid_constant__ Params p) {
     using L = LayCarry<NB>;
     extern __shared__ __align__(1024) uint8_t base[];
-    const Piece w = piece_of(p.a, p.plan, blockIdx.x, 1);
+    const Piece w = piece_of(p.a, p.plan, blockIdx.x);
     if (w.piece >= max(w.used, 1)) return;
     const int K = w.hi - w.lo;
     Cta<L::NBAR> cta(base, L::OFF_BAR, p.a.err, [](int i) { return L::arrivals(i); });
@@ -529,30 +521,18 @@ __global__ void __launch_bounds__(kCarryThreads, 1) ssm_carry_kernel(const __gri
     cta.finish();
 }
 
-// Heads that share a CTA in the sums of pieces: as many as leave CTAs for the device.
-inline int heads_together(const Args &a, const Plan &plan, int dirs) {
-    const long long ctas = (long long)a.B * a.H * plan.PT * plan.pieces * dirs;
-    return a.R % 2 == 0 && ctas / 2 >= kSms * 3 / 4 ? 2 : 1;
-}
-template <int NB, int HB>
-cudaError_t launch_sums(const Params &p, int dirs, cudaStream_t st) {
-    using S = LaySum<NB>;
-    static_assert(S::SMEM <= 227 * 1024, "shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(ssm_sum_kernel<NB, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e != cudaSuccess) return e;
-    const Args &a = p.a;
-    ssm_sum_kernel<NB, HB><<<dim3((unsigned)((size_t)a.B * (a.H / HB) * p.plan.PT * p.plan.pieces), dirs), kSumThreads, S::SMEM, st>>>(p);
-    return cudaGetLastError();
-}
 // The weights of all chunks, then the states that pieces start from (dirs 2: and their gradients).
 template <int NB>
 cudaError_t starts(const Params &p, int dirs, cudaStream_t st) {
     const Args &a = p.a;
     cudaError_t e = weights(a, const_cast<Dec *>(p.dec), st);
     if (e != cudaSuccess || p.plan.pieces == 1) return e;
-    e = heads_together(a, p.plan, dirs) == 2 ? launch_sums<NB, 2>(p, dirs, st) : launch_sums<NB, 1>(p, dirs, st);
-    if (e != cudaSuccess) return e;
-    ssm_piece_scan_kernel<<<dim3((unsigned)((size_t)a.B * a.H * ((a.N * a.P + 255) / 256)), dirs), 256, 0, st>>>(p);
+    using S = LaySum<NB>;
+    static_assert(S::SMEM <= 227 * 1024, "shared memory");
+    if ((e = cudaFuncSetAttribute(ssm_sum_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM)) != cudaSuccess) return e;
+    ssm_sum_kernel<NB><<<dim3((unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces), dirs), kSumThreads, S::SMEM, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ssm_piece_scan_kernel<<<dim3((unsigned)((size_t)a.B * a.H * ((a.N * a.P + 1023) / 1024)), dirs), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 }  // namespace tcs

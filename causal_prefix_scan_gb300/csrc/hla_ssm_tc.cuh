@@ -142,21 +142,25 @@ HLA_DEVICE float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 
 HLA_DEVICE void unpack8(const uint4 u, float2 *v) {
     v[0] = unpack2(u.x); v[1] = unpack2(u.y); v[2] = unpack2(u.z); v[3] = unpack2(u.w);
 }
-// v as three bf16 parts, whose sum is v to the last bit (above 2^-110).
+// v as three bf16 parts, whose sum is v to the last bit (above 2^-110): the first one rounded where
+// it is of use alone, each other cut off, which is a byte permutation where rounding converts.
+HLA_DEVICE uint32_t cut2(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+HLA_DEVICE float2 less(float2 v, uint32_t part) { return fma2(unpack2(part), both(-1.f), v); }
+template <bool ROUND>
 HLA_DEVICE void split3(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    hi = pack2(v);
-    v = add2(v, unpack2(hi ^ 0x80008000u));  // less what the part holds
-    mid = pack2(v);
-    v = add2(v, unpack2(mid ^ 0x80008000u));
-    lo = pack2(v);
+    hi = ROUND ? pack2(v) : cut2(v);
+    v = less(v, hi);
+    mid = cut2(v);
+    lo = cut2(less(v, mid));
 }
 // 8 columns (c0 a multiple of 8) of row r of a 64-column tile with `rows` rows, its parts `step` bytes apart.
+template <bool ROUND>
 HLA_DEVICE void store_split8(uint8_t *tile, int step, int rows, int r, int c0, const float2 *v) {
     uint4 h, m, l;
-    split3(v[0], h.x, m.x, l.x);
-    split3(v[1], h.y, m.y, l.y);
-    split3(v[2], h.z, m.z, l.z);
-    split3(v[3], h.w, m.w, l.w);
+    split3<ROUND>(v[0], h.x, m.x, l.x);
+    split3<ROUND>(v[1], h.y, m.y, l.y);
+    split3<ROUND>(v[2], h.z, m.z, l.z);
+    split3<ROUND>(v[3], h.w, m.w, l.w);
     uint8_t *at = tile + tile_off(rows, r, c0);
     *reinterpret_cast<uint4 *>(at) = h;
     *reinterpret_cast<uint4 *>(at + step) = m;
@@ -174,8 +178,8 @@ HLA_DEVICE void scale_split16(const uint8_t *tile, uint8_t *to, int r, int c0, f
     unpack8(u1, v + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(f));
-    store_split8(to, kHalf, T, r, c0, v);
-    store_split8(to, kHalf, T, r, c0 + 8, v + 4);
+    store_split8<false>(to, kHalf, T, r, c0, v);
+    store_split8<false>(to, kHalf, T, r, c0 + 8, v + 4);
 }
 // 16 columns of an accumulator in TMEM, as pairs.
 HLA_DEVICE void tmem_pairs16(uint32_t taddr, float2 (&v)[8]) { tmem_ld16(taddr, reinterpret_cast<float(&)[16]>(v)); }
@@ -198,21 +202,25 @@ struct Dec {
 constexpr int kDecBytes = offsetof(Dec, slope);  // what the walks take
 HLA_DEVICE const Dec *dec_of(const Args &a, const Dec *dec, int b, int h, int c) { return dec + ((size_t)b * a.H + h) * a.nc + c; }
 
-// One CTA for 32 heads of a chunk: their steps through shared memory, whichever of heads and tokens
+// One CTA for 8 heads of a chunk: their steps through shared memory, whichever of heads and tokens
 // lie side by side; then a warp for each head, four adjacent tokens a lane.
-static __global__ void __launch_bounds__(256) ssm_weights_kernel(const Args a, Dec *dec) {
-    __shared__ float raw[T][33];
-    const int groups = (a.H + 31) / 32, h0 = blockIdx.x % groups * 32, c = blockIdx.x / groups % a.nc, b = blockIdx.x / groups / a.nc;
-    const int len = clamp_length(a.lengths, b, a.n), t0 = c * T, heads = min(32, a.H - h0), live = min(T, len - t0);
+constexpr int kWeightHeads = 8;
+static __global__ void __launch_bounds__(kWeightHeads * 32) ssm_weights_kernel(const Args a, Dec *dec) {
+    constexpr int W = kWeightHeads;
+    __shared__ float raw[T][W + 1];
+    const int groups = (a.H + W - 1) / W, h0 = blockIdx.x % groups * W, c = blockIdx.x / groups % a.nc, b = blockIdx.x / groups / a.nc;
+    const int len = clamp_length(a.lengths, b, a.n), t0 = c * T, heads = min(W, a.H - h0), live = min(T, len - t0);
     if (live <= 0) return;
     const bool by_head = a.dt.sh < a.dt.st;
-    for (int e = threadIdx.x; e < T * 32; e += 256) {
-        const int t = by_head ? e >> 5 : e & (T - 1), h = by_head ? e & 31 : e >> 7;
+#pragma unroll
+    for (int e = threadIdx.x; e < T * W; e += W * 32) {
+        const int t = by_head ? e / W : e & (T - 1), h = by_head ? e % W : e >> 7;
         if (t < live && h < heads) raw[t][h] = raw_step<__nv_bfloat16>(a, b, h0 + h, t0 + t);
     }
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < heads; i += 8) {
+    const int i = threadIdx.x >> 5;
+    if (i < heads) {
         const int h = h0 + i;
         const float bias = a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f;
         float d[4], sl[4];
@@ -241,7 +249,7 @@ static __global__ void __launch_bounds__(256) ssm_weights_kernel(const Args a, D
     }
 }
 inline cudaError_t weights(const Args &a, Dec *dec, cudaStream_t st) {
-    ssm_weights_kernel<<<(unsigned)((size_t)a.B * a.nc * ((a.H + 31) / 32)), 256, 0, st>>>(a, dec);
+    ssm_weights_kernel<<<(unsigned)((size_t)a.B * a.nc * ((a.H + kWeightHeads - 1) / kWeightHeads)), kWeightHeads * 32, 0, st>>>(a, dec);
     return cudaGetLastError();
 }
 
@@ -252,13 +260,12 @@ struct Piece {
 struct Plan {
     int pieces, per, PT;  // chunks of a piece, column tiles of a head
 };
-HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u, int heads) {
-    const int sets = a.H / heads;
+HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u) {
     Piece r;
     r.pt = u % p.PT;
-    r.h = u / p.PT % sets * heads;
-    r.piece = u / p.PT / sets % p.pieces;
-    r.b = u / p.PT / sets / p.pieces;
+    r.h = u / p.PT % a.H;
+    r.piece = u / p.PT / a.H % p.pieces;
+    r.b = u / p.PT / a.H / p.pieces;
     r.len = clamp_length(a.lengths, r.b, a.n);
     const int chunks = (r.len + T - 1) / T;
     r.used = (chunks + p.per - 1) / p.per;
