@@ -304,6 +304,12 @@ HLA_DEVICE float ex2_approx(float y) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
     return r;
 }
+// 1 / x with the hardware approximation (one unit in the last place).
+HLA_DEVICE float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // g^x for x >= 0 with g in [0,1]; lg = log2(g) (may be -inf).  0^0 = 1.
 HLA_DEVICE float gpow(float lg, float x) { return x == 0.f ? 1.f : ex2_approx(lg * x); }
 

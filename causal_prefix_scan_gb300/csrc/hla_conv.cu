@@ -8,6 +8,8 @@
 // it) down a run of tokens with the last inputs and the filter in registers; runs read width - 1
 // rows of their neighbours again (they hit the caches), and the backward computes g of width - 1
 // tokens behind its run again.
+#include <type_traits>
+
 #include "hla_layer.cuh"
 
 namespace hla {
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 4 ? 2 : 4) conv_forward_kerne
 
 // One warp's run of kRunBack tokens: their g counts towards the filter's gradient, and g of the
 // W - 1 tokens behind them is formed again, so that dxs_u leaves once g_u is known.  Groups of U
-// tokens, inputs ahead.
+// tokens, inputs ahead; the groups inside a run go without the questions that its ends ask.
 template <typename T, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kernel(const Args a) {
     constexpr int U = 4;
@@ -157,8 +159,10 @@ __global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kern
             dp += (size_t)U * a.dy.st;
         };
         fetch(t0);
-#pragma unroll 1
-        for (int t = t0; t < last; t += U) {
+        T *out = static_cast<T *>(a.dx.p) + (ptrdiff_t)b * (ptrdiff_t)a.dx.sb + (ptrdiff_t)(t0 - (W - 1)) * (ptrdiff_t)a.dx.st + c;  // row s of u = t0
+        // A group of tokens; `inner`: all of them count, and all their dxs are rows of dx.
+        auto group = [&](int t, auto inner) {
+            constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 widen<T, VEC>(rx[i], xs[W - 1 + i]);
@@ -169,13 +173,15 @@ __global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kern
             for (int i = 0; i < U; ++i) {
                 float(&gt)[VEC] = g[W - 1 + i];
                 if (SILU) {
-                    float pre[VEC];
+                    float pre[VEC], s[VEC], r[VEC];
                     f.apply(xs + i, pre);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) gt[v] *= silu_slope(pre[v], sigmoid(pre[v]));
+                    for (int v = 0; v < VEC; ++v) s[v] = sigmoid(pre[v]);
+                    silu_slope_v<VEC>(pre, s, r);
+                    mul_v<VEC>(gt, r, gt);
                 }
-                if (t + i >= len) fill_v<VEC>(0.f, gt);  // (whatever was in the registers)
-                if (t + i < behind) {
+                if (!INNER && t + i >= len) fill_v<VEC>(0.f, gt);  // (whatever was in the registers)
+                if (INNER || t + i < behind) {
 #pragma unroll
                     for (int k = 0; k < W; ++k) fma_v<VEC>(gt, xs[i + k], dw[k], dw[k]);
                     add_v<VEC>(dw[W], gt, dw[W]);
@@ -184,21 +190,22 @@ __global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kern
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int u = t + i, s = u - (W - 1);  // dxs_u: row s of dx, or of the state's gradient
-                if (u >= last || (s < t0 && t0 > 0)) continue;
+                if (!INNER && (u >= last || (s < t0 && t0 > 0))) continue;
                 float o[VEC];
                 mul_v<VEC>(f.w[0], g[W - 1 + i], o);
 #pragma unroll
                 for (int k = 1; k < W; ++k) fma_v<VEC>(f.w[k], g[W - 1 + i - k], o, o);
-                if (u >= len && a.dsout) {
+                if (!INNER && u >= len && a.dsout) {
                     float e[VEC];
                     widen<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.dsout) + ((size_t)b * (W - 1) + (u - len)) * a.d + c), e);
                     add_v<VEC>(o, e, o);
                 }
-                if (s >= 0)
-                    store_raw<T, VEC>(row_out<T>(a.dx, b, s, c), narrow<T, VEC>(o));
+                if (INNER || s >= 0)
+                    store_raw<T, VEC>(out + (ptrdiff_t)i * (ptrdiff_t)a.dx.st, narrow<T, VEC>(o));
                 else if (a.dsin)
                     store_raw<T, VEC>(static_cast<T *>(a.dsin) + ((size_t)b * (W - 1) + u) * a.d + c, narrow<T, VEC>(o));
             }
+            out += (ptrdiff_t)U * (ptrdiff_t)a.dx.st;
 #pragma unroll
             for (int i = 0; i < W - 1; ++i)
 #pragma unroll
@@ -206,6 +213,13 @@ __global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kern
                     xs[i][v] = xs[U + i][v];
                     g[i][v] = g[U + i][v];
                 }
+        };
+#pragma unroll 1
+        for (int t = t0; t < last; t += U) {
+            if (t > t0 && t + U <= behind)
+                group(t, std::true_type());
+            else
+                group(t, std::false_type());
         }
     }
 #pragma unroll

@@ -174,11 +174,6 @@ HLA_DEVICE float rsqrt_approx(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-HLA_DEVICE float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // ------------------------------------------------------------ gates
 constexpr float kLog2e = 1.4426950408889634f;

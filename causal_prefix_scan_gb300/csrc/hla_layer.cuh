@@ -8,7 +8,7 @@ namespace layer {
 
 // sigma(z) from one exponential and one reciprocal, each a few units in the last place off; the
 // exponential overflows to infinity below -88, where sigma is 0 to the last bit that counts.
-HLA_DEVICE float sigmoid(float z) { return __fdividef(1.f, 1.f + ex2_approx(z * -1.4426950408889634f)); }
+HLA_DEVICE float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(z * -1.4426950408889634f)); }
 HLA_DEVICE float silu(float z) { return z * sigmoid(z); }
 HLA_DEVICE float silu_slope(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }  // s = sigma(z)
 
@@ -133,6 +133,15 @@ template <int VEC>
 HLA_DEVICE void fill_v(float x, float (&r)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) r[i] = x;
+}
+template <int VEC>
+HLA_DEVICE void silu_slope_v(const float (&z)[VEC], const float (&s)[VEC], float (&r)[VEC]) {  // s = sigma(z)
+    float m[VEC], one[VEC];
+    fill_v<VEC>(1.f, one);
+    fill_v<VEC>(-1.f, m);
+    fma_v<VEC>(s, m, one, r);
+    fma_v<VEC>(z, r, one, r);
+    mul_v<VEC>(r, s, r);
 }
 
 // VEC floats of an aligned or single-channel array.

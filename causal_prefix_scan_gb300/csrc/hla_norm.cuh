@@ -86,28 +86,35 @@ HLA_DEVICE void scale_of(const float *p, size_t at, bool ok, float none, float (
     }
 }
 
-// Sums of two values over a team of TEAM threads; `red` holds one float2 for each warp of the
-// block, alternated by the caller so that one barrier per sum is enough.
-template <int TEAM>
-HLA_DEVICE float2 team_sum(float2 v, float2 *red) {
+HLA_DEVICE float plus(float a, float b) { return a + b; }
+HLA_DEVICE float2 plus(float2 a, float2 b) { return add2(a, b); }
+HLA_DEVICE float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+HLA_DEVICE float2 across(float2 v, int o) { return make_float2(across(v.x, o), across(v.y, o)); }
+// Sum of a value, or of two, over a team of TEAM threads; `red` (on a 16-byte boundary) holds one
+// float2 for each warp of the block, alternated by the caller so that one barrier per sum is enough.
+template <int TEAM, class V>
+HLA_DEVICE V team_sum(V v, float2 *red) {
     constexpr int LANES = TEAM < 32 ? TEAM : 32;
 #pragma unroll
-    for (int o = LANES >> 1; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    for (int o = LANES >> 1; o > 0; o >>= 1) v = plus(v, across(v, o));
     if constexpr (TEAM > 32) {
-        constexpr int WARPS = TEAM / 32;
+        constexpr int WARPS = TEAM / 32, WIDE = WARPS * (int)sizeof(V) / 16;
         const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[warp] = v;
+        V *all = reinterpret_cast<V *>(red);
+        if ((threadIdx.x & 31) == 0) all[warp] = v;
         __syncthreads();
-        const float2 *mine = red + warp / WARPS * WARPS;
-        v = make_float2(0.f, 0.f);
+        const V *mine = all + warp / WARPS * WARPS;
+        alignas(16) V w[WARPS];
+        if constexpr (WIDE > 0) {
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            v.x += mine[w].x;
-            v.y += mine[w].y;
+            for (int i = 0; i < WIDE; ++i) reinterpret_cast<float4 *>(w)[i] = reinterpret_cast<const float4 *>(mine)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) w[i] = mine[i];
         }
+        v = w[0];
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) v = plus(v, w[i]);
     }
     return v;
 }

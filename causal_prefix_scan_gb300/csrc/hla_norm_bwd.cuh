@@ -23,7 +23,7 @@ template <typename T, int VEC, int E, int TEAM, int GATE>
 __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 512) / block_of(TEAM)) norm_backward_kernel(const Args a) {
     constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM, STEP = TEAM * VEC;
     using Raw = raw_t<T, VEC>;
-    __shared__ float2 red[2][block_of(TEAM) / 32];
+    __shared__ alignas(16) float2 red[2][block_of(TEAM) / 32];
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
     bool ok[K];
     float dw[K][VEC], db[K][VEC];
@@ -67,19 +67,20 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s += u[k][v];
-            const float mean = team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x * inv;
+            const float mean = team_sum<TEAM>(s, red[turn]) * inv;
             turn ^= 1;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) u[k][v] = ok[k] ? u[k][v] - mean : 0.f;
         }
-        float s = 0.f;
+        float sq[VEC], s = 0.f;
+        fill_v<VEC>(0.f, sq);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) fma_v<VEC>(u[k], u[k], sq, sq);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) s = fmaf(u[k][v], u[k][v], s);
-        const float rs = rsqrtf(fmaf(team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x, inv, a.eps));
+        for (int v = 0; v < VEC; ++v) s += sq[v];
+        const float rs = rsqrtf(fmaf(team_sum<TEAM>(s, red[turn]), inv, a.eps));
         turn ^= 1;
         float fr[VEC], s1[VEC], s0[VEC];
         fill_v<VEC>(rs, fr);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
 // each channel's sums stay with the thread that owns it, in the workspace.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_backward_long_kernel(const Args a) {
-    __shared__ float2 red[3][8];
+    __shared__ alignas(16) float2 red[3][8];
     const int g = blockIdx.x % a.col_blocks;
     const size_t at = (size_t)g * a.m;
     const float inv = 1.f / (float)a.m;
@@ -179,14 +180,14 @@ __global__ void __launch_bounds__(256) norm_backward_long_kernel(const Args a) {
         float mean = 0.f, s = 0.f;
         if (a.center) {
             for (int c = threadIdx.x; c < a.m; c += 256) s += value(c);
-            mean = team_sum<256>(make_float2(s, 0.f), red[0]).x * inv;
+            mean = team_sum<256>(s, red[0]) * inv;
         }
         s = 0.f;
         for (int c = threadIdx.x; c < a.m; c += 256) {
             const float u = value(c) - mean;
             s = fmaf(u, u, s);
         }
-        const float rs = rsqrtf(fmaf(team_sum<256>(make_float2(s, 0.f), red[1]).x, inv, a.eps));
+        const float rs = rsqrtf(fmaf(team_sum<256>(s, red[1]), inv, a.eps));
         float2 sums = make_float2(0.f, 0.f);
         for (int c = threadIdx.x; c < a.m; c += 256) {
             const float u = (value(c) - mean) * rs, w = a.weight ? __ldg(a.weight + at + c) : 1.f;

@@ -9,7 +9,7 @@ namespace {
 template <typename T, int VEC, int E, int TEAM, int GATE>
 __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 1024) / block_of(TEAM)) norm_forward_kernel(const Args a) {
     constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM;
-    __shared__ float2 red[2][block_of(TEAM) / 32];
+    __shared__ alignas(16) float2 red[2][block_of(TEAM) / 32];
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
     bool ok[K];
 #pragma unroll
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 10
             float s = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) s += u[e];
-            const float mean = team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x * inv;
+            const float mean = team_sum<TEAM>(s, red[turn]) * inv;
             turn ^= 1;
 #pragma unroll
             for (int e = 0; e < E; ++e) u[e] = ok[e / VEC] ? u[e] - mean : 0.f;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 10
         float s = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) s = fmaf(u[e], u[e], s);
-        const float rs = rsqrtf(fmaf(team_sum<TEAM>(make_float2(s, 0.f), red[turn]).x, inv, a.eps));
+        const float rs = rsqrtf(fmaf(team_sum<TEAM>(s, red[turn]), inv, a.eps));
         turn ^= 1;
         T *y = row_to<T>(a.y, b, t) + at;
 #pragma unroll
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 10
 // Groups wider than a team holds: one CTA per group and token, three passes.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_forward_long_kernel(const Args a) {
-    __shared__ float2 red[2][8];
+    __shared__ alignas(16) float2 red[2][8];
     const int g = blockIdx.x % a.col_blocks;
     const size_t at = (size_t)g * a.m;
     const float inv = 1.f / (float)a.m;
@@ -99,14 +99,14 @@ __global__ void __launch_bounds__(256) norm_forward_long_kernel(const Args a) {
         float mean = 0.f, s = 0.f, gate;
         if (a.center) {
             for (int c = threadIdx.x; c < a.m; c += 256) s += value(c, gate);
-            mean = team_sum<256>(make_float2(s, 0.f), red[0]).x * inv;
+            mean = team_sum<256>(s, red[0]) * inv;
         }
         s = 0.f;
         for (int c = threadIdx.x; c < a.m; c += 256) {
             const float u = value(c, gate) - mean;
             s = fmaf(u, u, s);
         }
-        const float rs = rsqrtf(fmaf(team_sum<256>(make_float2(s, 0.f), red[1]).x, inv, a.eps));
+        const float rs = rsqrtf(fmaf(team_sum<256>(s, red[1]), inv, a.eps));
         T *y = row_to<T>(a.y, r.b, r.t) + at;
         for (int c = threadIdx.x; c < a.m; c += 256) {
             const float u = value(c, gate) - mean;
