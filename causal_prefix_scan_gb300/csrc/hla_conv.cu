@@ -4,7 +4,7 @@
 //   g_t = dy_t act'(pre_t),   dxs_u = sum_i w_i g_{u-i} (+ d_state_out, rows u >= length),
 //   dw_i = sum_t g_t xs_{t+i},   dbias = sum_t g_t.
 // A few operations on each element, so memory bounds it: each element is read once and each result
-// written once.  A warp takes 32 vectors of adjacent channels (16 bytes each where the rows allow
+// written once.  A warp takes 32 pairs of adjacent channels (single ones where the rows do not allow
 // it) down a run of tokens with the last inputs and the filter in registers; runs read width - 1
 // rows of their neighbours again (they hit the caches), and the backward computes g of width - 1
 // tokens behind its run again.
@@ -71,8 +71,8 @@ struct Filter {
 
 // Runs of kRun tokens in groups of U, the next group's loads ahead of the present one's work.
 template <typename T, int VEC, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads, VEC == 4 ? 2 : 4) conv_forward_kernel(const Args a) {
-    constexpr int U = VEC * sizeof(T) >= 16 ? 4 : 8;
+__global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a) {
+    constexpr int U = 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = ((int)(blockIdx.x % a.groups) * 32 + lane) * VEC;
     const int rest = blockIdx.x / a.groups, tile = rest % a.tiles, b = rest / a.tiles;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 4 ? 2 : 4) conv_forward_kerne
 // W - 1 tokens behind them is formed again, so that dxs_u leaves once g_u is known.  Groups of U
 // tokens, inputs ahead; the groups inside a run go without the questions that its ends ask.
 template <typename T, int VEC, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads, VEC <= 2 ? 3 : 2) conv_backward_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a) {
     constexpr int U = 4;
     __shared__ float red[kWarps][(W + 1) * 32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -285,9 +285,10 @@ int tiles_of(int n, int run) { return (int)(((long long)n + kWarps * run - 1) / 
 template <typename T, int VEC, int W>
 cudaError_t launch(Which w, Args a, float *dw, float *db, cudaStream_t st) {
     a.groups = (a.d + 32 * VEC - 1) / (32 * VEC);
-    // bf16 prompts go two channels at a time: with what four of them hold in registers too few warps
-    // fit an SM (n32768 d4352 forward 153 -> 115 us)
-    constexpr bool STEPS_ALONE = sizeof(T) == 2 && VEC > 2;
+    // Prompts go two channels at a time: with what four of them hold in registers too few warps fit an
+    // SM (forward bf16 n32768 d4352 153 -> 115 us, fp32 b2 n8192 d4352 107 -> 87, its backward 219 -> 182).
+    // Steps hold one token and go by 16 bytes.
+    constexpr bool STEPS_ALONE = VEC > 2;
     if (w == W_STEP) {
         const size_t work = (size_t)a.B * ((a.d + VEC - 1) / VEC);
         conv_step_kernel<T, VEC, W><<<(unsigned)((work + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
@@ -365,16 +366,18 @@ bool takes(const hla_conv_params *p, std::initializer_list<const View *> rows, s
 
 hla_status run(const hla_conv_params *p, Which w, const Args &a, std::initializer_list<const View *> rows,
                std::initializer_list<const void *> states, float *dw, float *db, cudaStream_t st) {
-    cudaError_t e;
+    const bool step = w == W_STEP;
+    auto go = [&](auto by, int vec) { return takes(p, rows, states, vec) ? by(p->width, w, a, dw, db, st) : cudaErrorNotSupported; };
+    cudaError_t e = cudaErrorNotSupported;
     if (p->in_dtype == HLA_F32) {
-        e = takes(p, rows, states, 4) ? by_width<float, 4>(p->width, w, a, dw, db, st) : by_width<float, 1>(p->width, w, a, dw, db, st);
-    } else if (w == W_STEP && takes(p, rows, states, 8)) {
-        e = by_width<__nv_bfloat16, 8>(p->width, w, a, dw, db, st);
-    } else if (w == W_STEP && takes(p, rows, states, 4)) {
-        e = by_width<__nv_bfloat16, 4>(p->width, w, a, dw, db, st);
+        if (step) e = go(by_width<float, 4>, 4);
+        if (e == cudaErrorNotSupported) e = go(by_width<float, 2>, 2);
+        if (e == cudaErrorNotSupported) e = go(by_width<float, 1>, 1);
     } else {
-        e = takes(p, rows, states, 2) ? by_width<__nv_bfloat16, 2>(p->width, w, a, dw, db, st)
-                                      : by_width<__nv_bfloat16, 1>(p->width, w, a, dw, db, st);
+        if (step) e = go(by_width<__nv_bfloat16, 8>, 8);
+        if (step && e == cudaErrorNotSupported) e = go(by_width<__nv_bfloat16, 4>, 4);
+        if (e == cudaErrorNotSupported) e = go(by_width<__nv_bfloat16, 2>, 2);
+        if (e == cudaErrorNotSupported) e = go(by_width<__nv_bfloat16, 1>, 1);
     }
     return e == cudaSuccess ? HLA_OK : report(HLA_ERR_CUDA, cudaGetErrorString(e));
 }
