@@ -913,7 +913,7 @@ cudaError_t tc_backward(const Args &a, cudaStream_t st) {
     p.a = a;
     cudaError_t e = dev_status_ptr(&p.a.err);
     if (e != cudaSuccess) return e;
-    p.plan = plan_of(a, kSms);
+    p.plan = plan_of(a, true);
     p.vx[0] = a.x; p.vx[1] = a.dy;
     p.vb[0] = a.b; p.vb[1] = a.c;
     p.pieces[0] = a.h; p.pieces[1] = a.g;

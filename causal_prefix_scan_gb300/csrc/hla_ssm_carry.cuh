@@ -1,8 +1,8 @@
 // hla_ssm_carry.cuh -- tensor-core kernels that carry a state along a head's chunks.
 //
-// A head's chunks are cut into pieces.  sum_kernel forms what a piece adds to the state (one
-// accumulator in TMEM over the whole piece: every token weighs by its decay to the piece's end, so
-// nothing is rescaled), scan_kernel turns the sums into the states at the pieces' starts, and
+// A head's chunks are cut into pieces.  sum_kernel forms what a piece, or a part of one, adds to the
+// state (one accumulator in TMEM over all its chunks: every token weighs by its decay to their end, so
+// nothing is rescaled), scan_kernel turns the sums into the states at their starts, and
 // carry_kernel walks each piece's chunks from its start: state' = 2^s_end state + B^T (w X).  Tokens
 // are read twice, states only at the pieces' ends, and no CTA waits for another.  Backward the sums
 // also run from the last chunk to the first on C and dY.
@@ -25,13 +25,17 @@ struct Params {
     Plan plan;
     View vx[2], vb[2];        // x and b; backward dy and c
     CUtensorMap mx[2], mb[2], mc, my;
-    float *pieces[2];         // [B][H][pieces][N][P]: sums, then start states
-    float *factor;            // [B][H][pieces]: decay over a piece
+    float *pieces[2];         // [B][H][parts][N][P]: sums, then start states
+    float *factor;            // [B][H][parts]: decay over a part
     const Dec *dec;           // [B][H][chunks]
 };
 
+HLA_DEVICE float *part_state(const Params &p, int dir, const Piece &w, int part) {
+    return p.pieces[dir] + (((size_t)w.b * p.a.H + w.h) * p.plan.pieces * p.plan.cuts + part) * p.a.N * p.a.P;
+}
+// What a piece starts from: the state before its first part, or the gradient behind its last one.
 HLA_DEVICE float *piece_state(const Params &p, int dir, const Piece &w) {
-    return p.pieces[dir] + (((size_t)w.b * p.a.H + w.h) * p.plan.pieces + w.piece) * p.a.N * p.a.P;
+    return part_state(p, dir, w, dir ? (w.hi - 1) / p.plan.part : w.piece * p.plan.cuts);
 }
 // This thread's 16 columns of row n of an fp32 [N][P] state (which may lie on any float).
 HLA_DEVICE void load_state(const Args &a, const float *s, int n, int c0, float2 (&v)[8]) {
@@ -101,8 +105,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
     extern __shared__ __align__(1024) uint8_t base[];
     const Args &a = p.a;
     const int dir = gridDim.y == 2 ? blockIdx.y : 0;
-    const Piece w = piece_of(a, p.plan, blockIdx.x);
-    if (dir ? w.piece == 0 || w.piece >= w.used : w.piece + 1 >= w.used) return;  // no piece starts from it
+    const Piece w = piece_of(a, p.plan.parts(), blockIdx.x);
+    const int of = w.piece / p.plan.cuts, pieces = (w.used + p.plan.cuts - 1) / p.plan.cuts;
+    if (dir ? of == 0 || w.piece >= w.used : of + 1 >= pieces) return;  // no piece starts from it
     const int K = w.hi - w.lo;
     auto chunk = [&](int k) { return dir ? w.lo + k : w.hi - 1 - k; };  // towards larger decays
     Cta<L::NBAR> cta(base, L::OFF_BAR, a.err, [](int i) {
@@ -175,50 +180,51 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
                 mbar_arrive(ws.bar(L::B_XE + s));
             }
         }
-        // (backward the piece that the forward walk leaves out)
-        if (ok && threadIdx.x == 0 && w.pt == 0 && (dir == 0 || w.piece + 1 == w.used)) p.factor[((size_t)w.b * a.H + w.h) * p.plan.pieces + w.piece] = off;
+        // (backward the parts that the forward sums leave out)
+        if (ok && threadIdx.x == 0 && w.pt == 0 && (dir == 0 || of + 1 == pieces)) p.factor[((size_t)w.b * a.H + w.h) * p.plan.pieces * p.plan.cuts + w.piece] = off;
         if (ok && ws.wait(L::B_OUT, 0u)) {
             tc_fence_after();
             if (q < 2 * NB) {
                 float2 v[8];
                 load_parts16(cta.tb + ((uint32_t)(32 * q) << 16) + 16 * cq, v);
-                store_state(a, piece_state(p, dir, w), row, 64 * w.pt + 16 * cq, v);
+                store_state(a, part_state(p, dir, w, w.piece), row, 64 * w.pt + 16 * cq, v);
             }
         }
     }
     cta.finish();
 }
 
-// Sums to the states that pieces start from, in place, four elements a thread: blockIdx.y 0 from the
-// first piece on, 1 from the last one back.
+// Sums to the states that parts start from, in place, four elements a thread: blockIdx.y 0 from the
+// first part on to the last piece's start, 1 from the last one back to the first piece's end.
 static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid_constant__ Params p) {
     const Args &a = p.a;
     const int NP = a.N * a.P, blocks = (NP + 1023) / 1024, e = blockIdx.x % blocks * 1024 + 4 * threadIdx.x, u = blockIdx.x / blocks;
     if (e >= NP) return;  // (N and P are multiples of 8)
     const int dir = blockIdx.y, chunks = (clamp_length(a.lengths, u / a.H, a.n) + T - 1) / T;
-    const int used = (chunks + p.plan.per - 1) / p.plan.per;
+    const int parts = (chunks + p.plan.part - 1) / p.plan.part, cuts = p.plan.cuts, last = (parts + cuts - 1) / cuts * cuts - cuts;
+    const int used = chunks == 0 ? 0 : dir ? max(parts - cuts, 0) + 1 : last + 1;
     const float *init = dir ? a.d_state_out : a.state_in;
-    float4 *s = reinterpret_cast<float4 *>(p.pieces[dir] + (size_t)u * p.plan.pieces * NP + e), h = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 *s = reinterpret_cast<float4 *>(p.pieces[dir] + (size_t)u * p.plan.pieces * cuts * NP + e), h = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) {  // (on any float)
         init += (size_t)u * NP + e;
         h = make_float4(init[0], init[1], init[2], init[3]);
     }
-    const float *f = p.factor + (size_t)u * p.plan.pieces;
+    const float *f = p.factor + (size_t)u * p.plan.pieces * cuts;
     constexpr int U = 8;
     for (int i = 0; i < used; i += U) {
         float4 v[U];
         float g[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (i + k + 1 < used) {  // the last piece of the walk hands on nothing
-                const int c = dir ? used - 1 - i - k : i + k;
+            if (i + k + 1 < used) {  // the last part of the walk hands on nothing
+                const int c = dir ? parts - 1 - i - k : i + k;
                 v[k] = s[(size_t)c * (NP / 4)];
                 g[k] = f[c];
             }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (i + k >= used) break;
-            s[(size_t)(dir ? used - 1 - i - k : i + k) * (NP / 4)] = h;
+            s[(size_t)(dir ? parts - 1 - i - k : i + k) * (NP / 4)] = h;
             if (i + k + 1 < used) h = make_float4(fmaf(g[k], h.x, v[k].x), fmaf(g[k], h.y, v[k].y), fmaf(g[k], h.z, v[k].z), fmaf(g[k], h.w, v[k].w));
         }
     }
@@ -530,7 +536,7 @@ cudaError_t starts(const Params &p, int dirs, cudaStream_t st) {
     using S = LaySum<NB>;
     static_assert(S::SMEM <= 227 * 1024, "shared memory");
     if ((e = cudaFuncSetAttribute(ssm_sum_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM)) != cudaSuccess) return e;
-    ssm_sum_kernel<NB><<<dim3((unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces), dirs), kSumThreads, S::SMEM, st>>>(p);
+    ssm_sum_kernel<NB><<<dim3((unsigned)((size_t)a.B * a.H * p.plan.PT * p.plan.pieces * p.plan.cuts), dirs), kSumThreads, S::SMEM, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ssm_piece_scan_kernel<<<dim3((unsigned)((size_t)a.B * a.H * ((a.N * a.P + 1023) / 1024)), dirs), 256, 0, st>>>(p);
     return cudaGetLastError();

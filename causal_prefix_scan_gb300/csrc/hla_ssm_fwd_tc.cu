@@ -31,7 +31,7 @@ bool tc_takes(const Args &a, bool backward) {
 }
 
 size_t tc_space(Args &a, bool backward, uint8_t *base) {
-    const Plan plan = plan_of(a, kSms);
+    const Plan plan = plan_of(a, backward);
     a.nc = (int)(((long long)a.n + T - 1) / T);
     size_t at = 0;
     auto take = [&](size_t floats) {
@@ -40,7 +40,7 @@ size_t tc_space(Args &a, bool backward, uint8_t *base) {
         return p;
     };
     a.dec = take((size_t)a.B * a.H * a.nc * (sizeof(Dec) / 4));
-    const size_t units = plan.pieces > 1 ? (size_t)a.B * a.H * plan.pieces : 0;
+    const size_t units = plan.pieces > 1 ? (size_t)a.B * a.H * plan.pieces * plan.cuts : 0;
     a.h = take(units * a.N * a.P);
     a.factor = take(units);
     if (backward) {
@@ -64,7 +64,7 @@ cudaError_t tc_forward(const Args &a, cudaStream_t st) {
     Params p;
     memset(&p, 0, sizeof p);
     p.a = a;
-    p.plan = plan_of(a, kSms);
+    p.plan = plan_of(a, false);
     p.vx[0] = a.x;
     p.vb[0] = a.b;
     p.pieces[0] = a.h;

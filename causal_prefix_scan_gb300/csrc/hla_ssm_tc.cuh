@@ -259,6 +259,8 @@ struct Piece {
 };
 struct Plan {
     int pieces, per, PT;  // chunks of a piece, column tiles of a head
+    int cuts, part;       // parts that a piece's sum is formed in, chunks of one: per = cuts part
+    HLA_DEVICE Plan parts() const { return {pieces * cuts, part, PT, 1, part}; }
 };
 HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u) {
     Piece r;
@@ -273,26 +275,31 @@ HLA_DEVICE Piece piece_of(const Args &a, const Plan &p, unsigned u) {
     r.hi = min(r.lo + p.per, chunks);
     return r;
 }
-// Pieces so that the rounds of CTAs over the SMs, each as long as a piece, are as few chunks in all
-// as can be: more pieces than fill the device once only where they fill it better.
-inline Plan plan_of(const Args &a, int sms) {
-    Plan p;
+// Pieces, and parts of their sums, so that the rounds of CTAs over the SMs, each as long as a piece,
+// are as few chunks in all as can be.  A chunk costs a sum half of what it costs the forward walk (1.3
+// against 2.5 us, n16384 h64 p64 s128) and, both directions taken, a quarter of the backward's; a CTA's
+// start and end cost it two.  (With sums of whole pieces seven pieces were best there, 239 us.)
+inline Plan plan_of(const Args &a, bool backward) {
+    Plan p{};
     p.PT = (a.P + 63) / 64;
-    const long long units = (long long)a.B * a.H * p.PT;
-    const int chunks = (int)(((long long)a.n + T - 1) / T);
-    long long best = -1;
-    p.pieces = 1;
-    p.per = chunks;
-    for (int k = 1; k <= 64 && k <= chunks; ++k) {
-        const int per = (chunks + k - 1) / k, real = (chunks + per - 1) / per;
-        const long long rounds = (units * real + sms - 1) / sms;
-        const long long cost = rounds * (per + 2) + (real > 1 ? rounds * per / 2 + 4 : 0);  // sums of pieces cost half a chunk each
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.pieces = real;
-            p.per = per;
+    const unsigned units = (unsigned)a.B * a.H * p.PT, chunks = ((unsigned)a.n + T - 1) / T;  // (launches of units x chunks fit a grid)
+    auto rounds = [](unsigned ctas) { return (ctas + kSms - 1) / kSms; };
+    unsigned long long best = ~0ull;
+    for (unsigned k = 1; k <= 64 && k <= chunks; ++k)
+        for (unsigned cuts = 1; cuts <= 8; ++cuts) {
+            const unsigned part = ((chunks + k - 1) / k + cuts - 1) / cuts, per = cuts * part, real = (chunks + per - 1) / per;
+            unsigned long long cost = 4ull * rounds(units * real) * (per + 2);
+            if (cost >= best) break;  // (more cuts make pieces no shorter)
+            if (real > 1) cost += (unsigned long long)rounds(units * (real - 1) * cuts * (backward ? 2 : 1)) * (part + 2) * (backward ? 1 : 2) + 16;
+            if (cost < best) {
+                best = cost;
+                p.pieces = (int)real;
+                p.per = (int)per;
+                p.cuts = (int)cuts;
+                p.part = (int)part;
+            }
+            if (real == 1) break;  // nothing to sum
         }
-    }
     return p;
 }
 

@@ -12,7 +12,8 @@ absolute values (every product positive), and the store adds half a step of the 
       undecayed term; 512 covers z up to 16, and what lies behind is below 2^-23 of it);
       sums of k terms by k u.  On the tensor cores bf16 operands are exact; the weights M, S are
       rounded to bf16 once (half a step 2^-9 of the value below a power of two, 2^-8 at most) and so
-      is a state that enters y, dx, dB, dC; a state that is kept enters in two bf16 parts (2^-17).
+      is a state that enters y, dx, dB, dC; a state that is kept, and what the gradients of dt, A and
+      dt_bias take of it, enters in three bf16 parts, whose sum is the fp32 value.
       Underflow: a factor, or a part of a weighted operand, below 2^-126 is 0.  Each output is a sum of
       at most n N P (n + 1) products of such a factor with one element each of x, B, C, dy, a state,
       D, A and dt, so it moves by at most 2^-126 times that count and the largest elements: below
@@ -168,7 +169,7 @@ def _scan(x, dt, slope_, A, B, C, D, state, lengths, dy, dstate, size):
 
 
 # names of outputs in which tensor-core operands are rounded to bf16 (twice at most: a weight or a
-# state, and the weighted input that meets it); the others see bf16 operands in two parts
+# state, and the weighted input that meets it)
 ROUNDED = {"y", "dx", "dB", "dC"}
 
 
@@ -188,8 +189,8 @@ def ssm(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, state=None, len
     out = {}
     for name, v in val.items():
         e = k * size[name] + under
-        if tensor_cores:
-            e = e + (2.0 ** -7 if name in ROUNDED else 2.0 ** -15) * size[name]
+        if tensor_cores and name in ROUNDED:
+            e = e + 2.0 ** -7 * size[name]
         out[name] = (v, e)
     return out
 
