@@ -341,14 +341,14 @@ struct LayGrad {
     static constexpr int SUM_FLOATS = 13 * T;  // [w by rows' quadrant][4][128], [vE by columns' quarter][4][128], [dY.X by columns' quarter][4][128], C.B [128]
     static constexpr int OFF_BAR = OFF_SUM + SUM_FLOATS * 4;
     static constexpr int B_XD = 0, B_XDE = B_XD + NS, B_DEC = B_XDE + NS, B_DECE = B_DEC + 2, B_H = B_DECE + 2, B_HE = B_H + 1,
-                         B_G = B_HE + 1, B_GE = B_G + 1, B_BC = B_GE + 1, B_CB = B_BC + 1, B_DYX = B_CB + 1, B_DE = B_DYX + 1,
+                         B_G = B_HE + 1, B_LO = B_G + 1, B_LE = B_LO + 1, B_BC = B_LE + 1, B_CB = B_BC + 1, B_DYX = B_CB + 1, B_DE = B_DYX + 1,
                          B_GB = B_DE + 1, B_MS = B_GB + 1, B_XM = B_MS + 1, B_SE = B_XM + 1, B_YT = B_SE + 1, B_Y = B_YT + 1,
                          B_SUM = B_Y + 2, B_SUME = B_SUM + 1, B_FIN = B_SUME + 1, B_RAW = B_FIN + 1, B_RAW2 = B_RAW + 1, NBAR = B_RAW2 + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
     static constexpr uint32_t DC = 0, DB = T, DYX = 2 * T, M = 2 * T, XM = 2 * T + 64, YT = 3 * T, XT = YT + 32, GB = 3 * T + 64;
     HLA_DEVICE static int arrivals(int i) {
         return (i >= B_XDE && i < B_DEC) || i == B_DECE || i == B_DECE + 1                                 ? kElemWarps + 1
-               : i == B_DE || i == B_MS || i == B_YT || i == B_Y || i == B_Y + 1 || i == B_SUM ? kElemWarps
+               : i == B_DE || i == B_MS || i == B_YT || i == B_LO || i == B_Y || i == B_Y + 1 || i == B_SUM ? kElemWarps
                                                                                                : 1;
     }
 };
@@ -477,12 +477,17 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         load_row16(dy, T, row, c0, yr);
         load_row16(x, T, row, c0, xr);
         const float2 to = both(d.to[row]), w = both(d.w[row]), D = both(a.D ? a.D[h] : 0.f);
+        float ly[8], lx[8];  // what rounding leaves of them
         {
             float ty[8], tx[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                ty[i] = __uint_as_float(pack2(mul2(yr[i], to)));
-                tx[i] = __uint_as_float(pack2(mul2(xr[i], w)));
+                const float2 fy = mul2(yr[i], to), fx = mul2(xr[i], w);
+                const uint32_t hy = pack2(fy), hx = pack2(fx);
+                ty[i] = __uint_as_float(hy);
+                tx[i] = __uint_as_float(hx);
+                ly[i] = __uint_as_float(pack2(less(fy, hy)));
+                lx[i] = __uint_as_float(pack2(less(fx, hx)));
             }
             tc_fence_after();
             tmem_st8(lanes + L::YT + 8 * cq, ty);
@@ -506,6 +511,12 @@ __device__ __forceinline__ void grad_elem(const GradParams &p, const Waits &ws, 
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) yr[i] = fma2(D, yr[i], mul2(w, v[i]));
+        tmem_st8(lanes + L::GB + c0, ly);  // in the columns that this warp has just read
+        tmem_st8(lanes + L::GB + c0 + 8, lx);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ws.bar(L::B_LO));
         ok = ok && ws.wait(L::B_XM, ph);
         tc_fence_after();
         tmem_pairs16(lanes + L::XM + c0, v);
@@ -570,6 +581,14 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         if (NB > 1) mma_ss64(tb + L::DYX, Bk + kBlock, Ck + kBlock, id_tt, true);
         umma_commit_warp(ws.bar(L::B_CB));
     }
+    auto rest = [&](int u) {  // the weighted rows' second parts
+        if (!ws.wait(L::B_LO, (uint32_t)u & 1u)) return false;
+        tc_fence_after();
+        mma_tk64<16>(tb + L::DC, tb + L::GB, Hk, id_k);
+        mma_tk64<16>(tb + L::DB, tb + L::GB + 8, Gk, id_k);
+        umma_commit_warp(ws.bar(L::B_LE));
+        return true;
+    };
 #pragma unroll 1
     for (int u = 0; u < U && ok; ++u) {
         const uint32_t ph = (uint32_t)u & 1u;
@@ -579,7 +598,8 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         tc_fence_after();
         mma_ss64(tb + L::DYX, kmajor(x), kmajor(dy), id_tt, false);
         umma_commit_warp(ws.bar(L::B_DYX));
-        if (!(ok = ws.wait(L::B_G, ph))) break;
+        if (u > 0 && !(ok = rest(u - 1))) break;
+        if (!(ok = ws.wait(L::B_G, ph))) break;  // (its load waits for rest's products, which read GB's columns)
         mma_km64(tb + L::GB, Bk, Gm, id_y, false);
         if (NB > 1) mma_km64(tb + L::GB, Bk + kBlock, Gm + kRows64, id_y, true);
         umma_commit_warp(ws.bar(L::B_GB));
@@ -594,12 +614,12 @@ __device__ __forceinline__ void grad_mma(const Waits &ws, uint8_t *base, uint32_
         umma_commit_warp(ws.bar(L::B_SE));
         if (!(ok = ws.wait(L::B_YT, ph) && ws.wait(L::B_H, ph))) break;
         tc_fence_after();
-        mma_tk64(tb + L::DC, tb + L::YT, Hk, id_k);
-        mma_tk64(tb + L::DB, tb + L::XT, Gk, id_k);
+        mma_tk64<8>(tb + L::DC, tb + L::YT, Hk, id_k);
+        mma_tk64<8>(tb + L::DB, tb + L::XT, Gk, id_k);
         umma_commit_warp(ws.bar(L::B_HE));
-        umma_commit_warp(ws.bar(L::B_GE));
         umma_commit_warp(ws.bar(L::B_XDE + sy));
     }
+    if (ok && U > 0) rest(U - 1);
     umma_commit_warp(ws.bar(L::B_FIN));  // every MMA issued completes before TMEM is released
     mbar_wait(ws.bar(L::B_FIN), 0u, ws.err);
     __syncwarp();
@@ -664,13 +684,12 @@ __device__ __forceinline__ void grad_load_state(const GradParams &p, const Waits
     for (; u < job.U && ok; ++u) {
         const uint32_t ph = (uint32_t)u & 1u;
         const size_t at = (((size_t)job.b * p.a.H + head_of(p, job, u)) * p.PT + u % p.PT) * p.a.nc + job.c;
-        if (u > 0 && !(ok = ws.wait(L::B_HE, ph ^ 1u))) break;
+        if (u > 0 && !(ok = ws.wait(L::B_LE, ph ^ 1u))) break;
         if (lane == 0) {
             mbar_expect_tx(ws.bar(L::B_H), L::HB);
             bulk_load(base + L::OFF_H, p.h + at * L::HB, L::HB, ws.bar(L::B_H));
         }
         __syncwarp();
-        if (u > 0 && !(ok = ws.wait(L::B_GE, ph ^ 1u))) break;
         if (lane == 0) {
             mbar_expect_tx(ws.bar(L::B_G), L::HB);
             bulk_load(base + L::OFF_G, p.g + at * L::HB, L::HB, ws.bar(L::B_G));

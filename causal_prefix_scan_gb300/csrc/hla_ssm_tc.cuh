@@ -61,17 +61,18 @@ HLA_DEVICE void mma_ts128(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     mma_ts32(d, a + 32, b + 512, idesc, true);
     mma_ts32(d, a + 48, b + 768, idesc, true);
 }
-// D += A B over 64 columns, A packed bf16 in 32 columns of TMEM, B K-major.
+// D += A B over 64 columns, A packed bf16 in four times 8 columns of TMEM, STEP apart, B K-major.
+template <int STEP>
 HLA_DEVICE void mma_tk64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
         "{\n .reg .pred e, t;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n elect.sync _|e, 0xffffffff;\n"
         " setp.eq.b32 t, 0, 0;\n add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
-        " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+        " add.u32 a1, %1, %4;\n add.u32 a2, %1, %5;\n add.u32 a3, %1, %6;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc)
+        "r"(a), "l"(b), "r"(idesc), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
         : "memory");
 }
 HLA_DEVICE void quad_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }  // the four warps of 32 rows
