@@ -18,10 +18,10 @@ namespace {
 
 using namespace layer;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kSms = 152;
 
 struct Args {
-    int B, n, d, tiles, groups;  // tiles of tokens, groups of channels
+    int B, n, d, run, tiles, groups;  // tokens of a warp, tiles of tokens, groups of channels
     bool silu;
     const float *weight, *bias;
     const int *lengths;
@@ -30,8 +30,6 @@ struct Args {
     void *sout, *dsin;
     float *part;  // [B * tiles][width + 1][d]
 };
-
-constexpr int kRun = 32, kRunBack = 64;  // tokens of one warp
 
 template <typename T>
 HLA_DEVICE const T *row_of(const View &v, int b, long long t, int c) {
@@ -69,7 +67,19 @@ struct Filter {
     }
 };
 
-// Runs of kRun tokens in groups of U, the next group's loads ahead of the present one's work.
+// Some lanes ask for the rows behind those in flight, one for each 128 bytes of a warp's row: its
+// first channel.
+template <typename T, int VEC>
+constexpr int lines_of() { return VEC * (int)sizeof(T) > 4 ? VEC * (int)sizeof(T) / 4 : 1; }
+template <typename T, int VEC>
+HLA_DEVICE int line_of(const Args &a, int group, int lane) {
+    constexpr int LINES = lines_of<T, VEC>();
+    return min(group * 32 * VEC + lane % LINES * (32 * VEC / LINES), a.d - 1);
+}
+
+// Runs of tokens in groups of U, the next group's loads ahead of the present one's work and the rows
+// behind those on their way to L2 (n32768 d4352 w4 bf16, silu: 100 us, 5.7 TB/s; without the rows
+// ahead and with runs of 32 tokens 114; fp32 b2 n8192 d4352 88 us, 6.5 TB/s).
 template <typename T, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a) {
     constexpr int U = 8;
@@ -81,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a)
     if (a.sout && tile == 0 && warp < W - 1)  // the last W - 1 inputs
         store_raw<T, VEC>(static_cast<T *>(a.sout) + ((size_t)b * (W - 1) + warp) * a.d + c,
                           input_at<T, VEC, W>(a, b, len + warp, c));
-    const int t0 = (tile * kWarps + warp) * kRun, count = min(kRun, len - t0);
+    const int t0 = (tile * kWarps + warp) * a.run, count = min(a.run, len - t0);
     if (count <= 0) return;
     const Filter<VEC, W> f(a, c);
     float xs[W - 1 + U][VEC];
@@ -89,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a)
     for (int i = 0; i < W - 1; ++i) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xs[i]);
     const T *in = row_of<T>(a.x, b, t0, c);
     T *out = row_out<T>(a.y, b, t0, c);
+    constexpr int LINES = lines_of<T, VEC>();
+    const int ahead = lane / LINES, line = line_of<T, VEC>(a, blockIdx.x % a.groups, lane);
     raw_t<T, VEC> raw[U];
     auto fetch = [&](int u) {
 #pragma unroll
@@ -102,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a)
 #pragma unroll
         for (int i = 0; i < U; ++i) widen<T, VEC>(raw[i], xs[W - 1 + i]);
         if (u + U < count) fetch(u + U);
+        if (ahead < U && u + 2 * U + ahead < count) prefetch_l2(row_of<T>(a.x, b, t0 + u + 2 * U + ahead, line));
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             float y[VEC];
@@ -120,18 +133,20 @@ __global__ void __launch_bounds__(kThreads, 4) conv_forward_kernel(const Args a)
     }
 }
 
-// One warp's run of kRunBack tokens: their g counts towards the filter's gradient, and g of the
+// One warp's run of tokens: their g counts towards the filter's gradient, and g of the
 // W - 1 tokens behind them is formed again, so that dxs_u leaves once g_u is known.  Groups of U
-// tokens, inputs ahead; the groups inside a run go without the questions that its ends ask.
+// tokens, inputs ahead; the groups inside a run go without the questions that its ends ask.  Issue and
+// the latency that 16 warps leave bound it: b2 n8192 d4352 w4 bf16, silu 116 us, 3.7 TB/s (fp32 147 us,
+// 5.8 TB/s).  With 24 warps, groups of 4 and no rows ahead it took 139; rows ahead at 24 warps spill, 170.
 template <typename T, int VEC, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a) {
-    constexpr int U = 4;
+__global__ void __launch_bounds__(kThreads, 2) conv_backward_kernel(const Args a) {
+    constexpr int U = 8;
     __shared__ float red[kWarps][(W + 1) * 32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x % a.groups, c = (group * 32 + lane) * VEC;
     const int rest = blockIdx.x / a.groups, tile = rest % a.tiles, b = rest / a.tiles;
     const int len = clamp_length(a.lengths, b, a.n);
-    const int t0 = (tile * kWarps + warp) * kRunBack;
+    const int t0 = (tile * kWarps + warp) * a.run;
     float dw[W + 1][VEC];  // taps, then bias
 #pragma unroll
     for (int i = 0; i <= W; ++i) fill_v<VEC>(0.f, dw[i]);
@@ -144,8 +159,10 @@ __global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a
             fill_v<VEC>(0.f, g[i]);
             if (t0 + i < len + W - 1) widen<T, VEC>(input_at<T, VEC, W>(a, b, t0 + i, c), xs[i]);
         }
-        const int behind = min(t0 + kRunBack, len), last = min(t0 + kRunBack, len) + W - 1;  // dxs_u for u < last
+        const int behind = min(t0 + a.run, len), last = behind + W - 1;  // dxs_u for u < last
         const int loads = min(last, len);
+        constexpr int LINES = lines_of<T, VEC>();
+        const int ahead = lane / LINES, line = line_of<T, VEC>(a, group, lane);
         raw_t<T, VEC> rx[U], rd[U];
         const T *xp = row_of<T>(a.x, b, t0, c), *dp = row_of<T>(a.dy, b, t0, c);
         auto fetch = [&](int t) {
@@ -161,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a
         fetch(t0);
         T *out = static_cast<T *>(a.dx.p) + (ptrdiff_t)b * (ptrdiff_t)a.dx.sb + (ptrdiff_t)(t0 - (W - 1)) * (ptrdiff_t)a.dx.st + c;  // row s of u = t0
         // A group of tokens; `inner`: all of them count, and all their dxs are rows of dx.
-        auto group = [&](int t, auto inner) {
+        auto tokens = [&](int t, auto inner) {
             constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
             for (int i = 0; i < U; ++i) {
@@ -169,6 +186,10 @@ __global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a
                 widen<T, VEC>(rd[i], g[W - 1 + i]);
             }
             if (t + U < last) fetch(t + U);
+            if (ahead < 2 * U) {
+                const int row = t + 3 * U + ahead / 2;
+                if (row < loads) prefetch_l2(ahead % 2 ? row_of<T>(a.dy, b, row, line) : row_of<T>(a.x, b, row, line));
+            }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 float(&gt)[VEC] = g[W - 1 + i];
@@ -217,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 3) conv_backward_kernel(const Args a
 #pragma unroll 1
         for (int t = t0; t < last; t += U) {
             if (t > t0 && t + U <= behind)
-                group(t, std::true_type());
+                tokens(t, std::true_type());
             else
-                group(t, std::false_type());
+                tokens(t, std::false_type());
         }
     }
 #pragma unroll
@@ -281,6 +302,14 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const Args a) {
 enum Which { W_FWD, W_BWD, W_STEP };
 
 int tiles_of(int n, int run) { return (int)(((long long)n + kWarps * run - 1) / (kWarps * run)); }
+// Tokens of a warp: long runs read less of their neighbours and begin less often, where they leave
+// some rounds of CTAs over the SMs (forward n32768 d4352 bf16 111 -> 100 us at 64, but b2 n8192 fp32 88 ->
+// 92; backward b2 n8192 125 -> 119 at 128).
+int run_of(int B, int n, int d, bool back) {
+    const int run = back ? 128 : 64;
+    const double ctas = (double)B * tiles_of(n, run) * ((d + 63) / 64);
+    return ctas >= kSms * (back ? 2 * 3 : 4 * 6) ? run : run / 2;
+}
 
 template <typename T, int VEC, int W>
 cudaError_t launch(Which w, Args a, float *dw, float *db, cudaStream_t st) {
@@ -295,14 +324,16 @@ cudaError_t launch(Which w, Args a, float *dw, float *db, cudaStream_t st) {
     } else if constexpr (STEPS_ALONE) {
         return cudaErrorInvalidValue;
     } else if (w == W_FWD) {
-        a.tiles = tiles_of(a.n, kRun);
+        a.run = run_of(a.B, a.n, a.d, false);
+        a.tiles = tiles_of(a.n, a.run);
         const unsigned grid = (unsigned)((size_t)a.B * a.tiles * a.groups);
         if (a.silu)
             conv_forward_kernel<T, VEC, W, true><<<grid, kThreads, 0, st>>>(a);
         else
             conv_forward_kernel<T, VEC, W, false><<<grid, kThreads, 0, st>>>(a);
     } else {
-        a.tiles = tiles_of(a.n, kRunBack);
+        a.run = run_of(a.B, a.n, a.d, true);
+        a.tiles = tiles_of(a.n, a.run);
         const unsigned grid = (unsigned)((size_t)a.B * a.tiles * a.groups);
         if (a.silu)
             conv_backward_kernel<T, VEC, W, true><<<grid, kThreads, 0, st>>>(a);
@@ -329,7 +360,7 @@ hla_status check(const hla_conv_params *p) {
     if (p->activation != HLA_ACT_NONE && p->activation != HLA_ACT_SILU) return report(HLA_ERR_ARG, "unknown activation");
     if (p->width < 1) return report(HLA_ERR_ARG, "need width >= 1");
     if (p->n > 2147483647 - 1024) return report(HLA_ERR_ARG, "problem too large");  // token counters pass n by a tile
-    const double rows = (double)p->B * (tiles_of(p->n, kRun) + 1);
+    const double rows = (double)p->B * (tiles_of(p->n, 32) + 1);
     if (rows * ((p->d + 31) / 32) > 2147483647.0 || (double)p->d * 5 > 2147483647.0)
         return report(HLA_ERR_ARG, "problem too large");
     if (p->width < 2 || p->width > 4) return report(HLA_ERR_UNSUPPORTED, "widths of 2 to 4 taps are supported");
@@ -423,7 +454,7 @@ hla_status hla_conv_forward(const hla_conv_params *p, const hla_tensor *x, const
 
 size_t hla_conv_backward_workspace_size(const hla_conv_params *p) {
     if (conv::check(p) != HLA_OK || p->n == 0) return 0;
-    return layer::align256((size_t)p->B * tiles_of(p->n, kRunBack) * (p->width + 1) * p->d * 4);
+    return layer::align256((size_t)p->B * tiles_of(p->n, run_of(p->B, p->n, p->d, true)) * (p->width + 1) * p->d * 4);
 }
 
 hla_status hla_conv_backward(const hla_conv_params *p, const hla_tensor *x, const hla_tensor *dy, const hla_tensor *dx,

@@ -18,6 +18,8 @@ HLA_DEVICE int clamp_length(const int *lengths, int b, int n) {
     return L < 0 ? 0 : L > n ? n : L;
 }
 
+HLA_DEVICE void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // VEC adjacent elements as raw bits: 2 to 16 bytes.
 template <int BYTES>
 struct RawOf;

@@ -9,6 +9,10 @@
 // fp32.  A CTA keeps its channels from token to token (the sums for dw and dbias stay in
 // registers); while it reduces, the SM's other CTAs load.  Groups wider than a team holds go through
 // a kernel that reads them again for each pass.
+// Measured, bf16: forward n16384 d4096 in 64 groups, gate behind, 79 us, 5.1 TB/s; backward b2 n8192
+// d4096 in one group, gate in front, 191 us, 3.5 TB/s: issue slots are 54 % busy there (two
+// exponentials and two reciprocals an element, three sums over 512 threads a token) and 64 registers a
+// thread leave no room for the next token's loads.  Asking L2 for the next token: 198 us (forward 86).
 #pragma once
 #include "hla_layer.cuh"
 

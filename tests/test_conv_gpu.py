@@ -103,6 +103,14 @@ def test_strides(layout, dtype):
     check(c, "silu", out=out, dx=dx)
 
 
+def test_long_runs():
+    """Many rounds of tiles, where each warp takes more tokens."""
+    c = inputs(57, 32761, 2, 4, BF16, seed=8)
+    L = torch.randint(0, 32762, (57,), generator=torch.Generator().manual_seed(8), dtype=torch.int32)
+    L[0], L[1] = 32761, 32767
+    check(c, "silu", L.cuda())
+
+
 def test_far_values():
     """Pre-activations from -1e4 to 1e4: the sigmoid's exponential overflows on one side."""
     c = inputs(1, 64, 8, 2, F32)

@@ -230,6 +230,14 @@ def test_long_sequences(dtype, P, N):
     check(inputs(1, 2, 2, 2100, P, N, dtype, seed=7), state=False)
 
 
+@pytest.mark.parametrize("B,H,n,lengths", [(1, 17, 1147, None), (5, 1, 3910, [3910, 3700, 2049, 1, 2100]), (3, 13, 2001, [2001, 385, 1500]),
+                                           (3, 13, 2048, [0, 2048, 768])])
+def test_pieces_in_parts(B, H, n, lengths):
+    """Shares of a head's chunks whose sums are formed in parts, one way and both ways."""
+    c = inputs(B, H, 1, n, 8, 16, BF16, seed=n, rates=(0.05, 0.5))
+    check(c, lengths and torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+
+
 def test_gradient_against_differences():
     c = inputs(1, 2, 1, 70, 8, 8, F32)
     f = lambda dt: (hla.ssm_forward(c["x"], dt, c["A"], c["B"], c["C"], dt_bias=c["dt_bias"], dt_softplus=True).double() * c["dy"].double()).sum()  # noqa: E731
