@@ -9,10 +9,10 @@
 // fp32.  A CTA keeps its channels from token to token (the sums for dw and dbias stay in
 // registers); while it reduces, the SM's other CTAs load.  Groups wider than a team holds go through
 // a kernel that reads them again for each pass.
-// Measured, bf16: forward n16384 d4096 in 64 groups, gate behind, 79 us, 5.1 TB/s; backward b2 n8192
-// d4096 in one group, gate in front, 191 us, 3.5 TB/s: issue slots are 54 % busy there (two
-// exponentials and two reciprocals an element, three sums over 512 threads a token) and 64 registers a
-// thread leave no room for the next token's loads.  Asking L2 for the next token: 198 us (forward 86).
+// Measured, bf16: forward n16384 d4096 in 64 groups, gate behind, 77 us, 5.2 TB/s; backward b2 n8192
+// d4096 in one group, gate in front, 171 us, 3.9 TB/s: issue slots and the three sums over 512
+// threads a token bound it.  The next token's rows come by way of shared memory and the gate's sigmoid
+// waits there for the end: 64 registers a thread hold neither (loaded when due and formed twice: 79 and 191).
 #pragma once
 #include "hla_layer.cuh"
 
@@ -87,6 +87,52 @@ HLA_DEVICE void scale_of(const float *p, size_t at, bool ok, float none, float (
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = __ldg(p + at + i);
+    }
+}
+
+// The next token's rows, on their way to shared memory while this one's are worked on: each thread
+// copies what it will read itself, so no barrier is needed.  Where a thread's vectors are 16 bytes and
+// the block's N rows of K vectors a thread fit.
+template <typename T, int VEC, int K, int BLOCK, int N>
+struct Ahead {
+    static constexpr bool ON = VEC * sizeof(T) == 16 && N * K * BLOCK * 16 <= 24 * 1024;
+    uint4 *slot;
+    HLA_DEVICE uint4 *at(int row, int k) const { return slot + (row * K + k) * BLOCK + threadIdx.x; }
+    HLA_DEVICE void ask(int row, int k, const T *p) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at(row, k))), "l"(p) : "memory");
+    }
+    HLA_DEVICE void wait() const { asm volatile("cp.async.wait_all;" ::: "memory"); }
+    HLA_DEVICE raw_t<T, VEC> take(int row, int k) const {
+        if constexpr (ON) return *at(row, k);
+        return {};
+    }
+};
+template <typename T, int VEC, int K, int BLOCK, int N>
+constexpr int ahead_slots() { return Ahead<T, VEC, K, BLOCK, N>::ON ? N * K * BLOCK : 1; }
+
+// VEC values of a thread that it will need again, in shared memory: [K][VEC / 4][BLOCK] float4, or
+// [K][BLOCK] single ones.
+template <int VEC, int BLOCK>
+HLA_DEVICE void lay_aside(float *keep, int k, const float (&v)[VEC]) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            reinterpret_cast<float4 *>(keep)[(k * (VEC / 4) + i) * BLOCK + threadIdx.x] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        static_assert(VEC == 1, "");
+        keep[k * BLOCK + threadIdx.x] = v[0];
+    }
+}
+template <int VEC, int BLOCK>
+HLA_DEVICE void take_back(const float *keep, int k, float (&v)[VEC]) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 f = reinterpret_cast<const float4 *>(keep)[(k * (VEC / 4) + i) * BLOCK + threadIdx.x];
+            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+        }
+    } else {
+        v[0] = keep[k * BLOCK + threadIdx.x];
     }
 }
 

@@ -24,6 +24,10 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
     constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM, STEP = TEAM * VEC;
     using Raw = raw_t<T, VEC>;
     __shared__ alignas(16) float2 red[2][block_of(TEAM) / 32];
+    constexpr int ROWS = GATE != GATE_NONE ? 3 : 2;
+    __shared__ uint4 slots[ahead_slots<T, VEC, K, block_of(TEAM), ROWS>()];
+    const Ahead<T, VEC, K, block_of(TEAM), ROWS> next{slots};
+    __shared__ alignas(16) float sig[GATE == GATE_BEFORE ? E * block_of(TEAM) : 4];  // the gate's sigmoid, for the end
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
     bool ok[K];
     float dw[K][VEC], db[K][VEC];
@@ -36,28 +40,46 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
     const size_t at = (size_t)g * a.m + (size_t)tl * VEC;
     const float inv = 1.f / (float)a.m;
     int turn = 0;
-    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
+    Rows r(a, blockIdx.x / a.col_blocks);
+    auto ask = [&] {
+        if (!next.ON || !r.live()) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (ok[k]) {
+                next.ask(0, k, row_in<T>(a.x, r.b, r.t) + at + k * STEP);
+                next.ask(1, k, row_in<T>(a.dy, r.b, r.t) + at + k * STEP);
+                if (GATE != GATE_NONE) next.ask(2, k, row_in<T>(a.z, r.b, r.t) + at + k * STEP);
+            }
+    };
+    ask();
+    while (r.live()) {
+        const int b = r.b, t = r.t;
         float u[K][VEC], q[K][VEC];  // the norm's input, then itself; gradients (zeros beside the group)
         Raw x[K], z[K], d[K];
-        const T *px = row_in<T>(a.x, r.b, r.t) + at, *pd = row_in<T>(a.dy, r.b, r.t) + at;
-        const T *pz = GATE != GATE_NONE ? row_in<T>(a.z, r.b, r.t) + at : nullptr;
+        const T *px = row_in<T>(a.x, b, t) + at, *pd = row_in<T>(a.dy, b, t) + at;
+        const T *pz = GATE != GATE_NONE ? row_in<T>(a.z, b, t) + at : nullptr;
+        if (next.ON) next.wait();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             x[k] = d[k] = z[k] = Raw{};
             if (ok[k]) {
-                x[k] = load_raw<T, VEC>(px + k * STEP);
-                d[k] = load_raw<T, VEC>(pd + k * STEP);
-                if (GATE != GATE_NONE) z[k] = load_raw<T, VEC>(pz + k * STEP);
+                x[k] = next.ON ? next.take(0, k) : load_raw<T, VEC>(px + k * STEP);
+                d[k] = next.ON ? next.take(1, k) : load_raw<T, VEC>(pd + k * STEP);
+                if (GATE != GATE_NONE) z[k] = next.ON ? next.take(2, k) : load_raw<T, VEC>(pz + k * STEP);
             }
         }
+        r.next();
+        ask();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             widen<T, VEC>(x[k], u[k]);
             if (GATE == GATE_BEFORE) {
-                float gz[VEC];
+                float gz[VEC], s[VEC];
                 widen<T, VEC>(z[k], gz);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) gz[v] = silu(gz[v]);
+                for (int v = 0; v < VEC; ++v) s[v] = sigmoid(gz[v]);
+                lay_aside<VEC, block_of(TEAM)>(sig, k, s);
+                mul_v<VEC>(gz, s, gz);
                 mul_v<VEC>(u[k], gz, u[k]);
             }
         }
@@ -103,7 +125,7 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
                     q[k][v] = o.dv;
                     dz[v] = o.dgate;
                 }
-                if (GATE == GATE_AFTER && ok[k]) store_raw<T, VEC>(row_to<T>(a.dz, r.b, r.t) + at + k * STEP, narrow<T, VEC>(dz));
+                if (GATE == GATE_AFTER && ok[k]) store_raw<T, VEC>(row_to<T>(a.dz, b, t) + at + k * STEP, narrow<T, VEC>(dz));
             }
             fma_v<VEC>(q[k], u[k], dw[k], dw[k]);
             add_v<VEC>(db[k], q[k], db[k]);
@@ -129,21 +151,18 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kBackwardThreads : 5
             fma_v<VEC>(u[k], c1, c0, o);
             fma_v<VEC>(q[k], fr, o, o);
             if (GATE == GATE_BEFORE) {
-                float gz[VEC], f[VEC], sl[VEC];
+                float gz[VEC], f[VEC], s[VEC], sl[VEC];
                 widen<T, VEC>(z[k], gz);
                 widen<T, VEC>(x[k], f);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float sg = sigmoid(gz[v]);
-                    sl[v] = silu_slope(gz[v], sg);
-                    gz[v] *= sg;
-                }
+                take_back<VEC, block_of(TEAM)>(sig, k, s);
+                silu_slope_v<VEC>(gz, s, sl);
+                mul_v<VEC>(gz, s, gz);
                 mul_v<VEC>(f, sl, f);
                 mul_v<VEC>(o, f, f);
                 mul_v<VEC>(o, gz, o);
-                store_raw<T, VEC>(row_to<T>(a.dz, r.b, r.t) + at + k * STEP, narrow<T, VEC>(f));
+                store_raw<T, VEC>(row_to<T>(a.dz, b, t) + at + k * STEP, narrow<T, VEC>(f));
             }
-            store_raw<T, VEC>(row_to<T>(a.dx, r.b, r.t) + at + k * STEP, narrow<T, VEC>(o));
+            store_raw<T, VEC>(row_to<T>(a.dx, b, t) + at + k * STEP, narrow<T, VEC>(o));
         }
     }
     float *part = a.part + (size_t)(blockIdx.x / a.col_blocks) * 2 * a.d + at;

@@ -8,8 +8,10 @@ namespace {
 
 template <typename T, int VEC, int E, int TEAM, int GATE>
 __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 1024) / block_of(TEAM)) norm_forward_kernel(const Args a) {
-    constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM;
+    constexpr int K = E / VEC, PER = block_of(TEAM) / TEAM, ROWS = GATE != GATE_NONE ? 2 : 1;
     __shared__ alignas(16) float2 red[2][block_of(TEAM) / 32];
+    __shared__ uint4 slots[ahead_slots<T, VEC, K, block_of(TEAM), ROWS>()];
+    const Ahead<T, VEC, K, block_of(TEAM), ROWS> next{slots};
     const int tl = threadIdx.x % TEAM, g = blockIdx.x % a.col_blocks * PER + threadIdx.x / TEAM;
     bool ok[K];
 #pragma unroll
@@ -17,16 +19,30 @@ __global__ void __launch_bounds__(block_of(TEAM), (E == 8 ? kForwardThreads : 10
     const size_t at = (size_t)g * a.m + (size_t)tl * VEC;
     const float inv = 1.f / (float)a.m;
     int turn = 0;
-    for (Rows r(a, blockIdx.x / a.col_blocks); r.live(); r.next()) {
-        const int b = r.b, t = r.t;
-        float u[E];
-        raw_t<T, VEC> x[K], z[K];
+    Rows r(a, blockIdx.x / a.col_blocks);
+    auto ask = [&] {
+        if (!next.ON || !r.live()) return;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (ok[k]) {
-                x[k] = load_raw<T, VEC>(row_in<T>(a.x, b, t) + at + k * TEAM * VEC);
-                if (GATE != GATE_NONE) z[k] = load_raw<T, VEC>(row_in<T>(a.z, b, t) + at + k * TEAM * VEC);
+                next.ask(0, k, row_in<T>(a.x, r.b, r.t) + at + k * TEAM * VEC);
+                if (GATE != GATE_NONE) next.ask(1, k, row_in<T>(a.z, r.b, r.t) + at + k * TEAM * VEC);
             }
+    };
+    ask();
+    while (r.live()) {
+        const int b = r.b, t = r.t;
+        float u[E];
+        raw_t<T, VEC> x[K], z[K];
+        if (next.ON) next.wait();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (ok[k]) {
+                x[k] = next.ON ? next.take(0, k) : load_raw<T, VEC>(row_in<T>(a.x, b, t) + at + k * TEAM * VEC);
+                if (GATE != GATE_NONE) z[k] = next.ON ? next.take(1, k) : load_raw<T, VEC>(row_in<T>(a.z, b, t) + at + k * TEAM * VEC);
+            }
+        r.next();
+        ask();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float f[VEC];
