@@ -1058,7 +1058,7 @@ def conv_forward(x, weight, bias=None, activation: str = "none", state_in=None, 
 
 
 def conv_workspace(x, weight, stream=None):
-    """A workspace for conv_backward of these shapes: the filters' gradients of every 256 tokens.
+    """A workspace for conv_backward of these shapes: partial sums of the filters' gradients.
     Calls that may overlap in time need one each."""
     import torch
     p = _conv_params(x, weight, None, "none", None, x.device)

@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_grad_tc_kernel(const __gr
 
 // ------------------------------------------------------------ gradients of the steps
 // A warp for a chunk of a head; a CTA's chunks are those of one piece.
-constexpr int kFinishWarps = 8;
-__global__ void __launch_bounds__(kFinishWarps * 32) ssm_finish_kernel(const __grid_constant__ StatesParams sp, const float *own, const float *dd) {
+constexpr int kFinishWarps = 16;
+__global__ void __launch_bounds__(kFinishWarps * 32, 1) ssm_finish_kernel(const __grid_constant__ StatesParams sp, const float *own, const float *dd) {
     __shared__ float part[3][kFinishWarps];
     const Params &p = sp.p;
     const Args &a = p.a;
