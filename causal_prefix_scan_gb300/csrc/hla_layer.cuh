@@ -146,13 +146,6 @@ HLA_DEVICE void silu_slope_v(const float (&z)[VEC], const float (&s)[VEC], float
     mul_v<VEC>(r, s, r);
 }
 
-// VEC floats of an aligned or single-channel array.
-template <int VEC>
-HLA_DEVICE void load_f32(const float *p, float (&v)[VEC]) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = __ldg(p + i);
-}
-
 // out[k] = sum over r of part[r][k], k < cols: 8 warps take rows w, w + 8, ..., then the warps are
 // added, so the order depends on the sizes alone.
 template <class Store>

@@ -24,7 +24,7 @@ using win::tcw::uniform;
 constexpr int kSms = 152;            // pieces are cut for these (results then do not depend on the device)
 constexpr int T = 128;               // tokens of a chunk
 constexpr int kHalf = T * 128;       // bytes of 128 rows of 64 bf16 columns
-constexpr int kElemWarps = 16, kWarpMma = 16, kWarpTma = 17, kWarpTmaX = 18, kWarpStore = 19;
+constexpr int kElemWarps = 16, kWarpMma = 16, kWarpTma = 17, kWarpTmaX = 18;
 
 // D [128 x N] (+)= A B over 64 rows of both (MN-major tiles).
 HLA_DEVICE void mma_mm64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
