@@ -86,6 +86,15 @@ def test_rows_behind_the_first_of_each_cta(rows):
     check(inputs(1, rows, 96, BF16, seed=rows), 2, "after", "silu", True)
 
 
+@pytest.mark.parametrize("gate,act", MODES)
+@pytest.mark.parametrize("d,groups,dtype", [(4096, 1, BF16), (1024, 1, F32), (520, 5, BF16)])
+def test_many_rows_of_each_cta(d, groups, dtype, gate, act):
+    """Rows that come ahead of their turn, dead ones between them left out."""
+    n = 700
+    L = torch.tensor([n, 333, n - 1], dtype=torch.int32, device="cuda")
+    check(inputs(3, n, d, dtype, seed=d), groups, gate, act, False, L)
+
+
 @pytest.mark.parametrize("layout", ["slice", "time_major", "odd_offset", "broadcast"])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strides(layout, dtype):
