@@ -54,8 +54,12 @@ HLA_DEVICE float softplus(float x) {  // log(1 + e^x), both parts a few units in
 }
 
 // One chunk's steps and running log decays.  The sum is kept in two parts, whole numbers (exact)
-// and a remainder below one half, so that a difference of neighbours behind a steep decay keeps
-// its bits: 2^(s_t - s_j) comes out within 2^-21 whatever s is.
+// and a remainder of at most one half, and whatever is added to either is settled at once, so that no
+// addition rounds by more than 2^-25: a remainder is rounded PER - 1 times by its lane, five times
+// across the warp and once when both meet.  2^(s_t - s_j) then comes out within 2^-20.5 for neighbours,
+// however far behind a steep decay they are, and for tokens d apart within d 2^-22 more, which is what
+// the roundings of A log2(e), of its products with dt and of s_t - s_j amount to.  (With remainders that are
+// settled once at the end, a warp's sum of them reaches 60: decays were up to 2^-17.9 off.)
 struct Decay {
     float hi, lo;
 };
@@ -83,12 +87,18 @@ HLA_DEVICE float step_of(const Args &a, int b, int h, int t, float bias, float &
 template <int PER>
 HLA_DEVICE void scan_decays(const float (&d)[PER], float A2, Decay (&s)[PER]) {
     const int lane = threadIdx.x & 31;
+    auto settle = [](float &h, float &l) {
+        const float w = rintf(l);
+        h += w;
+        l -= w;
+    };
     float hi[PER], lo[PER], sh = 0.f, sl = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const float l = fmaxf(d[i] * A2, kLeast), w = rintf(l);
         sh += w;
         sl += l - w;
+        settle(sh, sl);
         hi[i] = sh;
         lo[i] = sl;
     }
@@ -99,14 +109,16 @@ HLA_DEVICE void scan_decays(const float (&d)[PER], float A2, Decay (&s)[PER]) {
         if (lane >= o) {
             ph += uh;
             pl += ul;
+            settle(ph, pl);
         }
     }
-    ph -= sh;
-    pl -= sl;
+    ph = __shfl_up_sync(0xffffffffu, ph, 1);  // and of those before it
+    pl = __shfl_up_sync(0xffffffffu, pl, 1);
+    if (lane == 0) ph = pl = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const float l = lo[i] + pl, w = rintf(l);
-        s[i] = {hi[i] + ph + w, l - w};
+        s[i] = {hi[i] + ph, lo[i] + pl};
+        settle(s[i].hi, s[i].lo);
     }
 }
 
