@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(const Args a,
     float *st = state + ((size_t)b * a.H + h) * a.N * a.P + p;
     float slope, x[VEC], y[VEC];
     const float dt = step_of<T>(a, b, h, 0, a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f, slope);
-    const float decay = ex2_approx(fmaxf(dt * (a.A[h] * kLog2e), kLeast));
+    const float decay = ex2_approx(log_decay(dt, a.A[h] * kLog2e));
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         float f[1] = {0.f};

@@ -83,6 +83,10 @@ HLA_DEVICE float step_of(const Args &a, int b, int h, int t, float bias, float &
     return step_from(a, raw_step<T>(a, b, h, t), bias, slope);
 }
 
+// Log decay of one step, A2 = A log2(e).  A step of 0 keeps the state whatever A is (so do the rows
+// behind a sequence, which get one); a rate that is not a number stays one, where fmaxf would drop it.
+HLA_DEVICE float log_decay(float d, float A2) { return A2 != A2 ? A2 : d == 0.f ? 0.f : fmaxf(d * A2, kLeast); }
+
 // One warp, PER adjacent tokens of a chunk a lane: their steps d to running log decays s.
 template <int PER>
 HLA_DEVICE void scan_decays(const float (&d)[PER], float A2, Decay (&s)[PER]) {
@@ -95,7 +99,7 @@ HLA_DEVICE void scan_decays(const float (&d)[PER], float A2, Decay (&s)[PER]) {
     float hi[PER], lo[PER], sh = 0.f, sl = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const float l = fmaxf(d[i] * A2, kLeast), w = rintf(l);
+        const float l = log_decay(d[i], A2), w = rintf(l);
         sh += w;
         sl += l - w;
         settle(sh, sl);

@@ -635,7 +635,7 @@ HLA_API hla_status hla_conv_step(const hla_conv_params *p, const hla_tensor *x, 
  * dt_t as given, or softplus(dt_t + dt_bias).  x, y [B][H][n][P], dt [B][H][n], b, c [B][G][n][N]
  * (strided; head h reads group h / (H / G)).  A <= 0 and dt >= 0 keep the state bounded; other
  * values are computed as they are.  A step's log decay dt A log2(e) is taken as -256 where it is
- * below that.
+ * below that; a step of 0 leaves the state as it is, whatever A is.
  */
 typedef struct {
     int B, H, G;            /* sequences, heads, groups of heads that share b and c (H % G == 0) */

@@ -1,4 +1,5 @@
-"""Decays of the selective state space scan: how exactly they are formed."""
+"""Decays of the selective state space scan: how exactly they are formed, and values of A and dt at
+the borders of what they may be."""
 import math
 
 import pytest
@@ -6,9 +7,9 @@ import torch
 
 import causal_prefix_scan_gb300 as hla
 import state_space_ref as ref
+from test_ssm_gpu import BF16, F32, inputs
 
 pytestmark = pytest.mark.gpu
-BF16, F32 = torch.bfloat16, torch.float32
 
 
 def bound(d):
@@ -55,3 +56,39 @@ def test_decays_to_a_chunks_end_on_the_tensor_cores(seed):
     e = s[-1] - s
     off = (st[0, :, 0, 0].double() / (dt[0, 0].double() * torch.exp(-e)) - 1).abs()
     assert bool((off <= bound(e / math.log(2))).all()), float(off.max())
+
+
+@pytest.mark.parametrize("dtype,P", [(BF16, 64), (BF16, 9), (F32, 64)])
+def test_a_rate_that_is_not_a_number_reaches_its_head(dtype, P):
+    """... in the prompt, its gradients and a step, and no other head."""
+    c = inputs(1, 4, 2, 150, P, 16, dtype)
+    args, kw = [c[k] for k in ("x", "dt", "A", "B", "C")], dict(D=c["D"], dt_bias=c["dt_bias"], dt_softplus=True)
+    want = hla.ssm_forward(*args, state_in=c["state"], return_state=True, **kw)
+    args[2] = args[2].clone()
+    args[2][1] = float("nan")
+    y, s = hla.ssm_forward(*args, state_in=c["state"], return_state=True, **kw)
+    r = hla.ssm_backward(*args, c["dy"], state_in=c["state"], want_dstate=True, **kw)
+    hla.hla_sync_status()
+    assert bool(y[:, 1].isnan().all()) and bool(s[:, 1].isnan().all())
+    for h in (0, 2, 3):
+        assert torch.equal(y[:, h], want[0][:, h]) and torch.equal(s[:, h], want[1][:, h])
+    assert r.dA.isnan().tolist() == [False, True, False, False] and bool(r.d_state_in[:, 1].isnan().all())
+    st = c["state"].clone()
+    hla.ssm_step(st, *(t if t is args[2] else t[:, :, 0] for t in args), **kw)
+    assert bool(st[:, 1].isnan().all()) and not bool(st[:, [0, 2, 3]].isnan().any())
+
+
+@pytest.mark.parametrize("dtype,P", [(BF16, 64), (BF16, 9), (F32, 64)])
+@pytest.mark.parametrize("n", [1, 40, 128, 200])
+def test_a_rate_of_minus_infinity_forgets(n, dtype, P):
+    """Every token starts anew: what lies behind the last one of a chunk takes nothing away."""
+    c = inputs(2, 2, 1, n, P, 16, dtype, softplus=False)
+    c["A"] = torch.full((2,), -math.inf, device="cuda")
+    L = torch.tensor([n, (n + 1) // 2], dtype=torch.int32, device="cuda")
+    y, s = hla.ssm_forward(*(c[k] for k in ("x", "dt", "A", "B", "C")), state_in=c["state"], return_state=True, lengths=L)
+    hla.hla_sync_status()
+    for b in range(2):
+        t = int(L[b]) - 1
+        x, dt, bt = c["x"][b, :, t].double(), c["dt"][b, :, t].double(), c["B"][b, :, t].double()
+        want = (dt[:, None] * bt)[..., None] * x[:, None]
+        ref.close(s[b], want, 4 * ref.U * want.abs(), "state")
