@@ -238,7 +238,11 @@ static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid
 // n16384 h64 p64 s128: 145 us, 128 CTAs.  A chunk moves 400 KB through shared memory (operands of the
 // products 208, tiles in and out 96, weighted parts and rows 96), 3,200 of its 4,300 cycles.
 constexpr int kCarryThreads = 20 * 32;
-constexpr float kBlockRange = 60.f;  // log2 of the decay over 32 tokens up to which both halves of a factor are plain numbers
+// A factor 2^(s_t - s_j) goes in two halves by way of a token r.  With r between j and t neither leaves fp32's
+// range while y_t stays in it; inside a block of 32 tokens r lies beyond both: the halves are taken where
+// the block's decay is not below 2^-60 and, forward, where none grows (gradients ask for decays in range between
+// all tokens, so that the halves are).
+constexpr float kBlockRange = 60.f;
 template <int NB>
 struct LayCarry {
     static constexpr int NX = 3, NR = 3;       // stages of X, ring of C and B tiles in turn
@@ -298,7 +302,7 @@ __device__ __forceinline__ void carry_elem(const Params &p, const Waits &ws, uin
         if (cq <= q && ok) {
             const Dec &d = dec(k);
             const Decay s = d.s[row], last = d.s[32 * cq + 31];
-            const bool plain = cq < q || d.s[32 * cq].hi - last.hi <= kBlockRange;
+            const bool plain = cq < q || d.range[cq] <= kBlockRange;
             const float2 u = both(plain ? factor(s, last) : 1.f);
             const uint32_t bits = cq < q ? 0xffffffffu : low_bits(lane + 1);  // (behind the diagonal a factor may be anything)
 #pragma unroll

@@ -196,6 +196,7 @@ struct Dec {
     float v[T];      // dt 2^(s_r - s), r the last token of its block of 32: M = CB v 2^(s_t - s_r) behind the block
     float end;       // 2^s_end
     float pad[3];
+    float range[4];  // log2 of the decay over each block of 32, infinity where some decay of the chunk grows
     // for the gradients only:
     float slope[T];  // of dt over its raw value
     float fw[T];     // 2^(s - s_b), b the first token of its block of 32: L = 2^(s_b - s_j) fw in front of the block
@@ -231,7 +232,8 @@ static __global__ void __launch_bounds__(kWeightHeads * 32) ssm_weights_kernel(c
             sl[k] = 0.f;
             d[k] = 4 * lane + k < live ? step_from(a, raw[4 * lane + k][i], bias, sl[k]) : 0.f;
         }
-        scan_decays(d, a.A[h] * kLog2e, s);
+        const float A2 = a.A[h] * kLog2e;
+        scan_decays(d, A2, s);
         Dec *o = dec + ((size_t)b * a.H + h) * a.nc + c;
         auto from = [&](int l) { return Decay{__shfl_sync(0xffffffffu, s[3].hi, l), __shfl_sync(0xffffffffu, s[3].lo, l)}; };
         const Decay end = from(31), block = from(lane | 7);
@@ -246,6 +248,8 @@ static __global__ void __launch_bounds__(kWeightHeads * 32) ssm_weights_kernel(c
         put(o->v, [&](int k) { return d[k] * factor(block, s[k]); });
         put(o->slope, [&](int k) { return sl[k]; });
         put(o->fw, [&](int k) { return factor(s[k], first); });
+        const bool grows = __any_sync(0xffffffffu, fmaxf(fmaxf(d[0] * A2, d[1] * A2), fmaxf(d[2] * A2, d[3] * A2)) > 0.f);
+        if (lane % 8 == 0) o->range[lane / 8] = grows ? INFINITY : first.hi - block.hi;
         if (lane == 0) o->end = factor(end);
     }
 }

@@ -634,8 +634,10 @@ HLA_API hla_status hla_conv_step(const hla_conv_params *p, const hla_tensor *x, 
  *   h_t = exp(dt_t A) h_{t-1} + dt_t b_t x_t^T,   y_t = c_t h_t + D x_t,
  * dt_t as given, or softplus(dt_t + dt_bias).  x, y [B][H][n][P], dt [B][H][n], b, c [B][G][n][N]
  * (strided; head h reads group h / (H / G)).  A <= 0 and dt >= 0 keep the state bounded; other
- * values are computed as they are.  A step's log decay dt A log2(e) is taken as -256 where it is
- * below that; a step of 0 leaves the state as it is, whatever A is.
+ * values are computed as they are: y_t is right while decays add up to what fp32 holds between the
+ * tokens of a sequence up to t, gradients while they do so between all of its tokens.  A step's log decay
+ * dt A log2(e) is taken as -256 where it is below that; a step of 0 leaves the state as it is,
+ * whatever A is.
  */
 typedef struct {
     int B, H, G;            /* sequences, heads, groups of heads that share b and c (H % G == 0) */

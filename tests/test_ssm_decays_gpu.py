@@ -7,7 +7,7 @@ import torch
 
 import causal_prefix_scan_gb300 as hla
 import state_space_ref as ref
-from test_ssm_gpu import BF16, F32, inputs
+from test_ssm_gpu import BF16, F32, check, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,29 @@ def test_a_rate_of_minus_infinity_forgets(n, dtype, P):
         x, dt, bt = c["x"][b, :, t].double(), c["dt"][b, :, t].double(), c["B"][b, :, t].double()
         want = (dt[:, None] * bt)[..., None] * x[:, None]
         ref.close(s[b], want, 4 * ref.U * want.abs(), "state")
+
+
+@pytest.mark.parametrize("signs", [False, True])
+def test_growing_states_on_the_tensor_cores(signs):
+    """A > 0, and steps of both signs: the decays add up to 2^14 at most."""
+    c = inputs(1, 2, 1, 200, 64, 64, BF16, False)
+    c["A"] = c["A"].abs() / 16
+    c["dt"] = c["dt"].clamp(max=0.05)
+    if signs:
+        c["dt"] = torch.where(torch.arange(200, device="cuda") % 50 < 25, -c["dt"], c["dt"])
+    check(c)
+
+
+@pytest.mark.parametrize("dtype,P", [(BF16, 64), (BF16, 9), (F32, 64)])
+def test_tokens_ahead_of_an_overflow(dtype, P):
+    """Steps of 2^8 a token: the 17th leaves fp32's range, those ahead of it are as they would be alone."""
+    c = inputs(1, 2, 1, 100, P, 16, dtype, False)
+    c["A"] = torch.ones(2, device="cuda")
+    c["dt"] = torch.full_like(c["dt"], 5.5)
+    args = [c[k] for k in ("x", "dt", "A", "B", "C")]
+    y = hla.ssm_forward(*args, state_in=c["state"], D=c["D"])
+    short = [t if t is c["A"] else t[:, :, :12] for t in args]
+    want = ref.ssm(*short, c["D"], None, False, c["state"], tensor_cores=dtype == BF16)["y"]
+    hla.hla_sync_status()
+    y = y[:, :, :12]
+    ref.close(y, want[0], want[1] + ref.half_step(dtype) * (want[0].abs() + want[1]) + 2 * ref.U * want[0].abs(), "y")
