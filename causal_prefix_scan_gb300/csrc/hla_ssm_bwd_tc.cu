@@ -226,10 +226,7 @@ HLA_DEVICE void stream(const Waits &ws, int K, int full, int empty, int rawb, ui
         __syncwarp();
         if (clear) ok = clear_landed(ws, rawb, raw, full + s, t, BLOCKS, len - t0);
     }
-    // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
-    if (ok)
-        for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(ws.bar(full + i % SLOTS), ring_phase<SLOTS>(i), ws.err);
-    __syncwarp();
+    wait_landed<SLOTS>(ws, full, k);
 }
 
 template <int NB>
@@ -275,7 +272,7 @@ __device__ __forceinline__ void states_load(const StatesParams &sp, const Waits 
             }
             __syncwarp();
         }
-        if (ok && k > 0) mbar_wait(ws.bar(L::B_Y), (uint32_t)(k - 1) & 1u, ws.err);
+        wait_landed<1>(ws, L::B_Y, k);
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     } else {  // the two tiles of a chunk in turn
@@ -294,11 +291,8 @@ __device__ __forceinline__ void states_load(const StatesParams &sp, const Waits 
             __syncwarp();
             if (clear) ok = clear_landed(ws, L::B_RAWB, raw, full, t, NB, w.len - t0);
         }
-        if (ok && visits > 0) {
-            mbar_wait(ws.bar(L::B_P), (uint32_t)(visits - 1) & 1u, ws.err);
-            mbar_wait(ws.bar(L::B_Q), (uint32_t)(visits - 1) & 1u, ws.err);
-        }
-        __syncwarp();
+        wait_landed<1>(ws, L::B_P, (r + 1) / 2);
+        wait_landed<1>(ws, L::B_Q, r / 2);
     }
 }
 
@@ -637,7 +631,7 @@ __device__ __forceinline__ void grad_load_xd(const GradParams &p, const Waits &w
     const int lane = threadIdx.x & 31;
     const bool clear = job.live < T;
     uint32_t raw = 0;
-    int i = 0;
+    int i = 0, weights = 0;  // copies issued
     bool ok = true;
 #pragma unroll 1
     for (; i < 2 * job.U && ok; ++i) {
@@ -649,6 +643,7 @@ __device__ __forceinline__ void grad_load_xd(const GradParams &p, const Waits &w
                 mbar_expect_tx(ws.bar(L::B_DEC + (u & 1)), sizeof(Dec));
                 bulk_load(base + L::OFF_DEC + (u & 1) * sizeof(Dec), dec_of(p.a, p.dec, job.b, h, job.c), sizeof(Dec), ws.bar(L::B_DEC + (u & 1)));
             }
+            ++weights;
         }
         if (i >= L::NS && !(ok = ws.wait(L::B_XDE + s, ring_phase<L::NS>(i) ^ 1u))) break;
         uint8_t *t = base + L::OFF_XD + s * kHalf;
@@ -663,12 +658,8 @@ __device__ __forceinline__ void grad_load_xd(const GradParams &p, const Waits &w
         __syncwarp();
         if (clear) ok = clear_landed(ws, L::B_RAW, raw, L::B_XD + s, t, 1, job.live);
     }
-    // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
-    if (ok) {
-        for (int k = max(0, i - L::NS); k < i; ++k) mbar_wait(ws.bar(L::B_XD + k % L::NS), ring_phase<L::NS>(k), ws.err);
-        for (int k = max(0, job.U - 2); k < job.U; ++k) mbar_wait(ws.bar(L::B_DEC + (k & 1)), ring_phase<2>(k), ws.err);
-    }
-    __syncwarp();
+    wait_landed<L::NS>(ws, L::B_XD, i);
+    wait_landed<2>(ws, L::B_DEC, weights);
 }
 
 template <int NB>
@@ -702,12 +693,9 @@ __device__ __forceinline__ void grad_load_state(const GradParams &p, const Waits
         }
         __syncwarp();
     }
-    if (ok) {
-        mbar_wait(ws.bar(L::B_BC), 0u, ws.err);
-        mbar_wait(ws.bar(L::B_H), (uint32_t)(job.U - 1) & 1u, ws.err);
-        mbar_wait(ws.bar(L::B_G), (uint32_t)(job.U - 1) & 1u, ws.err);
-    }
-    __syncwarp();
+    wait_landed<1>(ws, L::B_BC, 1);
+    wait_landed<1>(ws, L::B_H, u);
+    wait_landed<1>(ws, L::B_G, u);
 }
 
 // dX of each head's columns to memory; after a head's last columns the sums of E, four adjacent

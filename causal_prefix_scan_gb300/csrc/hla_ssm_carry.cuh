@@ -74,13 +74,22 @@ HLA_DEVICE void mma_state(uint32_t d, uint64_t b, uint64_t w, bool acc) {
 // Phase of use i of a ring of NS slots.
 template <int NS>
 HLA_DEVICE uint32_t ring_phase(int i) { return (uint32_t)(i / NS) & 1u; }
-// A tile that ends behind the sequence comes by way of barrier `raw` and is cleared there.
+// A tile that ends behind the sequence comes by way of barrier `raw` and is cleared there; in an aborted
+// CTA too, so that `bar` is all that its last wait for copies in flight has to ask.
 HLA_DEVICE bool clear_landed(const Waits &ws, int raw, uint32_t &phase, int bar, uint8_t *tile, int blocks, int rows) {
-    if (!ws.wait(raw, phase)) return false;
+    const bool ok = ws.wait(raw, phase);
+    if (!ok) mbar_wait(ws.bar(raw), phase, ws.err);
     phase ^= 1u;
     clear_rows(tile, blocks, rows);
     if ((threadIdx.x & 31) == 0) mbar_arrive(ws.bar(bar));
-    return true;
+    return ok;
+}
+// The end of a warp that has issued `uses` copies into a ring of NS slots: nothing may land after the
+// CTA has ended (only an aborted CTA still has copies in flight).
+template <int NS>
+HLA_DEVICE void wait_landed(const Waits &ws, int full, int uses) {
+    for (int i = max(0, uses - NS); i < uses; ++i) mbar_wait(ws.bar(full + i % NS), ring_phase<NS>(i), ws.err);
+    __syncwarp();
 }
 
 // ------------------------------------------------------------ sums of pieces
@@ -141,10 +150,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) ssm_sum_kernel(const __grid_co
             __syncwarp();
             if (clear) ok = clear_landed(ws, is_x ? L::B_RAWX : L::B_RAW, raw, full + s, t, is_x ? 1 : NB, w.len - t0);
         }
-        // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
-        if (ok)
-            for (int e = max(0, i - NS); e < i; ++e) mbar_wait(ws.bar(full + e % NS), (uint32_t)(e / NS) & 1u, a.err);
-        __syncwarp();
+        is_x ? wait_landed<L::NX>(ws, full, i) : wait_landed<L::NR>(ws, full, i);
     } else if (warp == kWarpMma) {
         const uint32_t tb = uniform(cta.tb);
         bool ok = true;
@@ -443,10 +449,7 @@ __device__ __forceinline__ void carry_load(const Params &p, const Waits &ws, uin
         __syncwarp();
         if (clear) ok = clear_landed(ws, L::B_RAW, raw, L::B_R + s, t, NB, w.len - t0);
     }
-    // nothing may land after the CTA has ended (only an aborted CTA still has copies in flight)
-    if (ok)
-        for (int i = max(0, r - L::NR); i < r; ++i) mbar_wait(ws.bar(L::B_R + i % L::NR), ring_phase<L::NR>(i), a.err);
-    __syncwarp();
+    wait_landed<L::NR>(ws, L::B_R, r);
 }
 
 template <int NB>
@@ -472,9 +475,7 @@ __device__ __forceinline__ void carry_load_x(const Params &p, const Waits &ws, u
         __syncwarp();
         if (clear) ok = clear_landed(ws, L::B_RAWX, raw, L::B_X + s, x, 1, w.len - t0);
     }
-    if (ok)
-        for (int i = max(0, k - L::NX); i < k; ++i) mbar_wait(ws.bar(L::B_X + i % L::NX), ring_phase<L::NX>(i), a.err);
-    __syncwarp();
+    wait_landed<L::NX>(ws, L::B_X, k);
 }
 
 // 128 rows of 64 columns of a head, from a tile in shared memory, by one warp: whole chunks by TMA;
