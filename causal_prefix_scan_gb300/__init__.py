@@ -1158,8 +1158,9 @@ def _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, device):
 
 
 def ssm_workspace(x, B, backward: bool = False, stream=None):
-    """A workspace for ssm_forward (or ssm_backward) of x [B,H,n,P] and B [B,G,n,N]: the states
-    between chunks of tokens; no initial contents.  Calls that may overlap in time need one each."""
+    """A workspace for ssm_forward (or ssm_backward) of x [B,H,n,P] and B [B,G,n,N], whatever their
+    strides: the states between chunks of tokens (forward: less than x's own bytes where prompts are
+    long); no initial contents.  Calls that may overlap in time need one each."""
     import torch
     p = hla_ssm_params(x.shape[0], x.shape[1], B.shape[1], x.shape[2], x.shape[3], B.shape[3], _dtype_code(x), 0, None,
                        None, None, None)

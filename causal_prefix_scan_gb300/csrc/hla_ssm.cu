@@ -119,7 +119,7 @@ hla_status check_rates(const hla_ssm_params *p) {
 Args make(const hla_ssm_params *p) {
     Args a{};
     a.B = p->B; a.H = p->H; a.G = p->G; a.R = p->H / p->G;
-    a.n = p->n; a.P = p->P; a.N = p->N;
+    a.n = a.rows = p->n; a.P = p->P; a.N = p->N;
     a.softplus = p->dt_softplus != 0;
     a.A = p->A; a.D = p->D; a.dt_bias = p->dt_bias;
     a.lengths = p->lengths;
@@ -131,30 +131,6 @@ struct Sizes {
     explicit Sizes(const hla_ssm_params *p, int n)
         : x{p->B, p->H, n, p->P}, dt{p->B, p->H, n, 1}, b{p->B, p->G, n, p->N} {}
 };
-
-// Workspace of the CUDA-core path; sets the pointers when `base` is given.
-size_t simt_space(Args &a, bool backward, uint8_t *base) {
-    const int Q = simt_chunk(a.P, a.N);
-    a.nc = (int)(((long long)a.n + Q - 1) / Q);
-    size_t at = 0;
-    auto take = [&](size_t floats) {
-        float *p = base ? reinterpret_cast<float *>(base + at) : nullptr;
-        at += align256(floats * 4);
-        return p;
-    };
-    const size_t units = (size_t)a.B * a.H * a.nc;
-    a.h = take(units * a.N * a.P);
-    a.factor = take(units);
-    if (backward) {
-        // a group's heads are shared by as many CTAs as fill the device about twice
-        const long long ctas = (long long)a.B * a.G * a.nc, want = (304 + ctas - 1) / ctas;
-        a.splits = (int)(want < a.R ? want : a.R);
-        a.g = take(units * a.N * a.P);
-        a.dbc = take((size_t)a.splits * 2 * a.B * a.G * a.n * a.N);
-        a.sums = take((size_t)a.B * a.nc * 3 * a.H);
-    }
-    return at;
-}
 
 hla_status take_workspace(Args &a, bool backward, void *ws, size_t bytes, size_t need) {
     if (!ws || bytes < need) return report(HLA_ERR_ARG, "workspace too small (hla_ssm_workspace_size)");

@@ -36,11 +36,17 @@ struct Args {
     const float *state_in, *d_state_out;
     float *state_out, *d_state_in, *dA, *dD, *dbias;
     // workspace
-    int nc;               // chunks of a sequence
+    int nc;               // chunks of a sequence (CUDA cores: of the span under way)
     int splits;           // backward: CTAs that share a group's heads
-    float *h, *g;         // [B][H][nc][N][P]: states and their gradients
-    float *factor;        // [B][H][nc]: 2^s_end
-    float *dbc;           // [splits][2][B][G][n][N]
+    int t0, rows;         // CUDA cores: first token of the span, its tokens
+    int hc, h0;           // CUDA cores: chunks that `h` holds, the span's first among them
+    int sum0, sumc;       // CUDA cores: the span's first chunk and all chunks, in `sums`
+    const float *from[2]; // CUDA cores: states before the span, gradients behind it
+    float *to[2];         // ... states behind it, gradients before it
+    float *carry;         // [B][H][N][P]: either, between spans
+    float *h, *g;         // [B][H][nc][N][P]: states (`hc` chunks of them) and their gradients
+    float *factor;        // [B][H][hc]: 2^s_end
+    float *dbc;           // [splits][2][B][G][rows][N]
     void *dec;            // [B][H][nc]: the chunks' weights (tensor cores)
     unsigned char *image[2];  // tensor cores, backward: the chunks' states and their gradients, and fp32 sums of tokens and borders
     float *inter, *aside, *dots, *own, *dd;
@@ -148,12 +154,15 @@ HLA_DEVICE void chunk_decays(const Args &a, int b, int h, int t0, int len, float
     }
 }
 
-// CUDA cores (any strides, widths and types): chunks of 64 tokens, 32 where both widths pass 64.
+// CUDA cores (any strides, widths and types): chunks of 64 tokens, 32 where both widths pass 64, taken in
+// spans whose states fit a workspace of bounded size.
 inline int simt_chunk(int P, int N) { return P > 64 && N > 64 ? 32 : 64; }
+size_t simt_space(Args &a, bool backward, uint8_t *base);  // bytes; sets the pointers when `base` is given
 cudaError_t simt_forward(const Args &a, hla_dtype dt, cudaStream_t st);
 cudaError_t simt_backward(const Args &a, hla_dtype dt, cudaStream_t st);
-// What both backward paths end with: dB, dC from their parts if there are any, dA, dD and dt_bias' gradient.
-cudaError_t join(const Args &a, hla_dtype dt, bool parts, int rows, cudaStream_t st);
+// What both backward paths end with: dB, dC from their parts; dA, dD and dt_bias' gradient from `rows` sums.
+cudaError_t join_parts(const Args &a, hla_dtype dt, cudaStream_t st);
+cudaError_t join_sums(const Args &a, int rows, cudaStream_t st);
 
 // Tensor cores: bf16 whose rows start on 16-byte boundaries (tc_takes); the workspace's bytes, its
 // pointers set when `base` is given; cudaErrorNotSupported, with nothing launched, when the driver

@@ -950,7 +950,8 @@ cudaError_t tc_backward(const Args &a, cudaStream_t st) {
         return cudaErrorNotSupported;
     g.mx = p.mx[0]; g.mdy = p.mx[1]; g.mb = p.mb[0]; g.mc = p.mb[1];
     e = a.N <= 64 ? launch<1>(sp, g, st) : launch<2>(sp, g, st);
-    return e == cudaSuccess ? join(a, HLA_BF16, a.splits > 1, a.B * p.plan.pieces, st) : e;
+    if (e == cudaSuccess && a.splits > 1) e = join_parts(a, HLA_BF16, st);
+    return e == cudaSuccess ? join_sums(a, a.B * p.plan.pieces, st) : e;
 }
 
 }  // namespace ssm

@@ -653,7 +653,14 @@ typedef struct {
 } hla_ssm_params;
 
 /* Bytes of workspace of hla_ssm_forward (backward 0) or hla_ssm_backward (1); 256-byte aligned,
- * no initial contents needed; calls that may overlap in time need one each. */
+ * no initial contents needed; calls that may overlap in time need one each.  One size for both paths
+ * (the tensors' alignment chooses), the larger of what they take:
+ *   forward, CUDA cores: the states (4 N P bytes) of all chunks of 64 tokens (32 where both widths pass 64),
+ *     of at most 64 MB or 2,048 of them where there are more, and one for each head; tensor cores: 32 bytes
+ *     a token and head, and up to 512 states for each head where heads are few;
+ *   backward, CUDA cores: the states of all chunks, of their gradients what a forward holds, and the parts of db
+ *     and dc over as many tokens; tensor cores: 32 KB and two bf16 images of a state (N rounded up to 64 or 128) for
+ *     each chunk of 128 tokens and 64 columns of a head, and about 80 bytes a token and head. */
 HLA_API size_t hla_ssm_workspace_size(const hla_ssm_params *p, int backward);
 
 /* The scan over n tokens.  state_in [B][H][N][P] fp32 or NULL (zeros); state_out after each
