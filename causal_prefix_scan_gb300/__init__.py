@@ -753,6 +753,13 @@ def _int32(x, name):
     return x
 
 
+def _fits(*tensors):
+    """The same of sizes (strides are 64 bits wide)."""
+    for t in tensors:
+        if max(t.shape) >= 2 ** 31:
+            raise ValueError(f"a size of {max(t.shape)} does not fit 32 bits")
+
+
 def _gated_params(x, g, gate, rate, lengths, device):
     if gate not in _GATES:
         raise ValueError(f"gate must be one of {sorted(_GATES)}")
@@ -1025,6 +1032,7 @@ def _conv_params(x, weight, bias, activation, lengths, device):
     _expect(x, "x", x.shape, x.dtype, device)
     if weight.dim() != 2:
         raise ValueError("weight must be [d, width]")
+    _fits(x, weight)
     _expect(weight, "weight", (d, weight.shape[1]), torch.float32, device, True)
     _optional(bias, "bias", (d,), torch.float32, device)
     _optional(lengths, "lengths", (B,), torch.int32, device)
@@ -1144,6 +1152,7 @@ def _ssm_params(x, dt, A, B, C, D, dt_bias, dt_softplus, lengths, device):
     batch, H, P = x.shape[0], x.shape[1], x.shape[-1]
     if B.dim() != x.dim():
         raise ValueError("B and C must be [B, G, n, N] (a step's [B, G, N])")
+    _fits(x, B)
     G, N = B.shape[1], B.shape[-1]
     _expect(x, "x", x.shape, x.dtype, device)
     _expect_steps(dt, "dt", (batch, H) + tail, x.dtype, device)
@@ -1162,6 +1171,7 @@ def ssm_workspace(x, B, backward: bool = False, stream=None):
     strides: the states between chunks of tokens (forward: less than x's own bytes where prompts are
     long); no initial contents.  Calls that may overlap in time need one each."""
     import torch
+    _fits(x, B)
     p = hla_ssm_params(x.shape[0], x.shape[1], B.shape[1], x.shape[2], x.shape[3], B.shape[3], _dtype_code(x), 0, None,
                        None, None, None)
     with _on(stream, x.device):
@@ -1251,6 +1261,7 @@ def _norm_params(x, weight, bias, groups, eps, center, gate, gate_first, activat
     code = _dtype_code(x)
     if x.dim() != 3:
         raise ValueError("x must be [B, n, d]")
+    _fits(x)
     B, n, d = x.shape
     _expect(x, "x", x.shape, x.dtype, device)
     if gate is not None:
@@ -1286,6 +1297,7 @@ def norm_workspace(x, stream=None):
     """A workspace for norm_backward of x [B,n,d], whatever its groups: partial sums for the scale's
     and the shift's gradients.  Calls that may overlap in time need one each."""
     import torch
+    _fits(x)
     p = hla_norm_params(*x.shape, 1, _dtype_code(x), 0, 0, 0, 0.0, None, None, None)
     with _on(stream, x.device):
         return torch.empty(max(hla_norm_backward_workspace_size(p), 1), dtype=torch.uint8, device=x.device)
