@@ -207,7 +207,7 @@ HLA_DEVICE const Dec *dec_of(const Args &a, const Dec *dec, int b, int h, int c)
 // One CTA for 8 heads of a chunk: their steps through shared memory, whichever of heads and tokens
 // lie side by side; then a warp for each head, four adjacent tokens a lane.
 constexpr int kWeightHeads = 8;
-static __global__ void __launch_bounds__(kWeightHeads * 32) ssm_weights_kernel(const Args a, Dec *dec) {
+static __global__ void __launch_bounds__(kWeightHeads * 32, 8) ssm_weights_kernel(const Args a, Dec *dec) {
     constexpr int W = kWeightHeads;
     __shared__ float raw[T][W + 1];
     const int groups = (a.H + W - 1) / W, h0 = blockIdx.x % groups * W, c = blockIdx.x / groups % a.nc, b = blockIdx.x / groups / a.nc;
