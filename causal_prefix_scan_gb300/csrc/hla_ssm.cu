@@ -8,9 +8,10 @@ namespace {
 // ------------------------------------------------------------ one token
 // h = 2^a h + dt b x^T, y = c h + D x over the fp32 state [N][P] of one (sequence, head): read and
 // written once, which bounds it.  LP lanes take VEC adjacent columns each and step down the rows;
-// the rows' sums for y meet in shared memory.  kStepAhead rows are in flight (b128 h64 p64 s128 69 us,
-// 6.2 TB/s; one at a time 89).  A CTA takes all columns of a head, or a few of them
-// where the heads alone would leave SMs idle: columns need no sums between CTAs.
+// the rows' sums for y meet in shared memory.  kStepAhead rows are in flight, the first of them ahead
+// of the decay, which waits for dt and A (b128 h64 p64 s128 67 us, 6.4 TB/s; behind it 73, one row at a
+// time 89).  A CTA takes all columns of a head, or a few of them where the heads alone would leave SMs
+// idle: columns need no sums between CTAs.
 constexpr int kStepThreads = 256, kStepAhead = 4;
 
 template <typename T, int VEC, int LP>
@@ -25,6 +26,20 @@ __global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(const Args a,
     const T *ct = static_cast<const T *>(a.c.p) + (size_t)b * a.c.sb + (size_t)(h / a.R) * a.c.sh;
     const T *xt = static_cast<const T *>(a.x.p) + (size_t)b * a.x.sb + (size_t)h * a.x.sh;
     float *st = state + ((size_t)b * a.H + h) * a.N * a.P + p;
+    raw_t<float, VEC> raw[kStepAhead];
+    float bn[kStepAhead][1], cn[kStepAhead][1];
+    auto fetch = [&](int n0) {
+#pragma unroll
+        for (int i = 0; i < kStepAhead; ++i) {
+            const int n = n0 + i * ROWS;
+            if (n < a.N && ok) raw[i] = load_raw<float, VEC>(st + (size_t)n * a.P);
+            if (n < a.N) {
+                widen<T, 1>(load_raw<T, 1>(bt + n), bn[i]);
+                widen<T, 1>(load_raw<T, 1>(ct + n), cn[i]);
+            }
+        }
+    };
+    fetch(tid / LP);  // ahead of the decay, which waits for dt and A
     float slope, x[VEC], y[VEC];
     const float dt = step_of<T>(a, b, h, 0, a.softplus && a.dt_bias ? a.dt_bias[h] : 0.f, slope);
     const float decay = ex2_approx(log_decay(dt, a.A[h] * kLog2e));
@@ -35,18 +50,7 @@ __global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(const Args a,
         x[v] = f[0];
         y[v] = 0.f;
     }
-    for (int n0 = tid / LP; n0 < a.N; n0 += ROWS * kStepAhead) {
-        raw_t<float, VEC> raw[kStepAhead];
-        float bn[kStepAhead][1], cn[kStepAhead][1];
-#pragma unroll
-        for (int i = 0; i < kStepAhead; ++i) {
-            const int n = n0 + i * ROWS;
-            if (n < a.N && ok) raw[i] = load_raw<float, VEC>(st + (size_t)n * a.P);
-            if (n < a.N) {
-                widen<T, 1>(load_raw<T, 1>(bt + n), bn[i]);
-                widen<T, 1>(load_raw<T, 1>(ct + n), cn[i]);
-            }
-        }
+    for (int n0 = tid / LP;;) {
 #pragma unroll
         for (int i = 0; i < kStepAhead; ++i) {
             const int n = n0 + i * ROWS;
@@ -61,6 +65,8 @@ __global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(const Args a,
             }
             store_raw<float, VEC>(st + (size_t)n * a.P, narrow<float, VEC>(s));
         }
+        if ((n0 += ROWS * kStepAhead) >= a.N) break;
+        fetch(n0);
     }
 #pragma unroll
     for (int o = 16; o >= LP; o >>= 1)
