@@ -756,7 +756,7 @@ def _int32(x, name):
 def _fits(*tensors):
     """The same of sizes (strides are 64 bits wide)."""
     for t in tensors:
-        if max(t.shape) >= 2 ** 31:
+        if not 0 < t.numel() < 2 ** 31 and max(t.shape) >= 2 ** 31:  # (the largest of a shape takes longer to find)
             raise ValueError(f"a size of {max(t.shape)} does not fit 32 bits")
 
 
