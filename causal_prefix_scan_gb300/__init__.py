@@ -1186,7 +1186,9 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False,
     (or None) fp32 and dt as given, or softplus(dt + dt_bias) with dt_softplus (dt_bias [H] fp32 or
     None).  state_in [B,H,N,P] fp32 or None (zeros); lengths [B] int32: tokens of each sequence
     (rows behind them: zero in a new y, left as they were in ``out``).  A new y lies in memory as
-    x does (tokens outside heads, or heads outside tokens).  Returns y (and the final state)."""
+    x does (tokens outside heads, or heads outside tokens).  Rows below the lengths must be finite.  bf16 on
+    16-byte rows takes weights and states rounded to bf16 on the way to y (never in the state).
+    Returns y (and the final state)."""
     import torch
     dev = _current(x)
     if x.dim() != 4:

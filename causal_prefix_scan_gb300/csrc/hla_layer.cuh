@@ -6,8 +6,9 @@
 namespace hla {
 namespace layer {
 
-// sigma(z) from one exponential and one reciprocal, each a few units in the last place off; the
-// exponential overflows to infinity below -88, where sigma is 0 to the last bit that counts.
+// sigma(z) from one exponential and one reciprocal: (16 + 2 |z|) 2^-24 of it off at most, the second part by
+// the exponential's argument, which is rounded twice.  The exponential overflows to infinity below -88, where
+// sigma is 0 to the last bit that counts.
 HLA_DEVICE float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(z * -1.4426950408889634f)); }
 HLA_DEVICE float silu(float z) { return z * sigmoid(z); }
 HLA_DEVICE float silu_slope(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }  // s = sigma(z)

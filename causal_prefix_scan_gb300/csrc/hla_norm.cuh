@@ -10,8 +10,8 @@
 // registers); while it reduces, the SM's other CTAs load.  Groups wider than a team holds go through
 // a kernel that reads them again for each pass.
 // Measured, bf16: forward n16384 d4096 in 64 groups, gate behind, 77 us, 5.2 TB/s; backward b2 n8192
-// d4096 in one group, gate in front, 171 us, 3.9 TB/s: issue slots and the three sums over 512
-// threads a token bound it.  The next token's rows come by way of shared memory and the gate's sigmoid
+// d4096 in one group, gate in front, no mean, 171 us, 3.9 TB/s: issue slots (59 % busy) and two sums over
+// 512 threads a token, one after the other (three with a mean), bound it.  The next token's rows come by way of shared memory and the gate's sigmoid
 // waits there for the end: 64 registers a thread hold neither (loaded when due and formed twice: 79 and 191).
 #pragma once
 #include "hla_layer.cuh"

@@ -13,6 +13,9 @@
 // so that dB and dC leave once per CTA.  A chunk's heads are shared by several CTAs only where
 // chunks alone are too few; their parts are then added by a kernel of its own.  finish_kernel puts
 // the sums together.
+// Roundings: M, S and the images once, since dx, dB and dC are stored in bf16 anyway and a second part of any
+// would double its products; the weighted rows that meet h and g in two parts, which GB's free columns
+// hold (dB, dC 2.6e-3 -> 2.3e-3 off).  What the gradients of dt, A and dt_bias take is never rounded.
 // Roles of grad_kernel (20 warps): 0-15 elementwise, 16 MMA, 17 loads of X, dY and weights, 18 of B, C
 // and the images, 19 stores dX and the sums.
 #include <cstring>
@@ -37,7 +40,7 @@ using namespace tcs;
 // scheduler, and latency.
 // Roles (20 warps): 0-15 elementwise, 16 MMA, 17 loads of the rows that enter, 18 of those that meet
 // the state and the images' stores, 19 loads of B and C.
-constexpr int kStatesThreads = 20 * 32, kWarpLoadBc = 19;
+constexpr int kStatesThreads = 20 * 32;
 template <int NB>
 struct LayStates {
     static constexpr int NX = 2, ND = 4;           // stages of the rows that enter, of the weights
@@ -100,7 +103,7 @@ __device__ __forceinline__ void states_elem(const StatesParams &sp, const Waits 
     auto dec = [&](int k) -> const Dec & { return *reinterpret_cast<const Dec *>(base + L::OFF_DEC + k % L::ND * kDecBytes); };
     auto aside = [&](int c) { return sp.aside + ((unit * p.plan.PT + w.pt) * a.nc + c) * 2048 + threadIdx.x; };
     // The rows that enter do not depend on the state: they are scaled a visit ahead, while the state meets
-    // Q, and their product runs while the next state is split (a visit 5500 -> 3300 clocks).
+    // Q, and their product runs while the next state is split.
     auto scale = [&](int k) {
         if (!ws.wait(L::B_X + (k & 1), ring_phase<2>(k))) return false;
         const Dec &d = dec(k);

@@ -239,8 +239,10 @@ static __global__ void __launch_bounds__(256) ssm_piece_scan_kernel(const __grid
 // ------------------------------------------------------------ walk along a piece
 // The outputs of the forward.  The elementwise warps take a chunk's steps in an order that leaves
 // the tensor cores a step's time for each product: M of chunk k; state behind k, and its bf16 rows;
-// weighted rows of k + 1; y of k, which leaves by TMA from x's own tile.  (All steps one after the
-// other took 4,500 cycles a chunk, two groups of warps at once 4,300, this order 3,300.)
+// weighted rows of k + 1; y of k, which leaves by TMA from x's own tile.
+// M and the rows of the state that meet C are rounded to bf16 once, since y is (2.0e-3 to 2.3e-3 off, its own
+// rounding 1.7e-3): a second part of the state would be another product of 64 columns and 8 NB KB a chunk
+// through shared memory, which bounds the walk.  The state itself stays in fp32.
 // n16384 h64 p64 s128: 145 us, 128 CTAs.  A chunk moves 400 KB through shared memory (operands of the
 // products 208, tiles in and out 96, weighted parts and rows 96), 3,200 of its 4,300 cycles.
 constexpr int kCarryThreads = 20 * 32;
